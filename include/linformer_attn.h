@@ -98,7 +98,8 @@ typedef enum {
                                        missing in PER_HEAD / HEADWISE mode */
     LINFORMER_ERR_ALLOC = -7,       /* workspace allocation failed */
     LINFORMER_ERR_LAUNCH = -8,      /* a CUDA call or kernel launch failed */
-    LINFORMER_ERR_DEVICE = -9       /* a device-side bounded wait ran out */
+    LINFORMER_ERR_DEVICE = -9,      /* a device-side bounded wait ran out */
+    LINFORMER_ERR_VALUE = -10       /* a parameter or a stride is out of its range */
 } linformer_status;
 
 /* Which kernels a call uses. */
@@ -117,7 +118,10 @@ typedef enum {
     LINFORMER_KERNEL_WINDOW = 4,    /* linformer_window_projection */
     LINFORMER_KERNEL_BACKWARD = 5,  /* the kernels of linformer_attn_bwd */
     LINFORMER_KERNEL_DENSE = 6,     /* the kernels of linformer_dense_attn_fwd */
-    LINFORMER_KERNEL_COUNT = 7
+    LINFORMER_KERNEL_ROTARY = 7,    /* the kernels of linformer_rotary */
+    LINFORMER_KERNEL_SOFTMAX = 8,   /* the kernels of linformer_softmax_attn_fwd */
+    LINFORMER_KERNEL_SOFTMAX_BWD = 9, /* the kernels of linformer_softmax_attn_bwd */
+    LINFORMER_KERNEL_COUNT = 10
 } linformer_kernel_id;
 
 /*
@@ -218,6 +222,115 @@ LINFORMER_API int linformer_attn_bwd(const void *Q, const void *K, const void *V
 LINFORMER_API int linformer_dense_attn_fwd(const void *Q, const void *K, const void *V,
                                            const int32_t *pad_lengths, void *O, int b, int h,
                                            int n, int d, int dtype, void *stream);
+
+/*
+ * Strided tensors.  The entry points below take, beside each tensor of shape
+ * [b][heads][n][d], its element strides {batch, head, row} as int64_t[3] (host memory, read
+ * during the call), or NULL for a dense tensor; the last dimension is contiguous.  A stride
+ * of a dimension of size one is ignored; others are positive and at most 2^38.  An output's
+ * strides are at least d (its elements must not overlap each other or an input, except
+ * where a call says that it works in place).
+ */
+
+/*
+ * Exact softmax attention without the n x n scores in memory, with what its backward pass
+ * needs: for batch entry beta, query head eta and its key/value head eta / (hq / hk),
+ *
+ *     s_ij = scale Q_i . K_j,   lse_i = log sum_j exp(s_ij),
+ *     O_i  = sum_j exp(s_ij - lse_i) V_j
+ *
+ * over the keys j < Lk that query i sees, Lq = q_lengths[beta], Lk = k_lengths[beta]
+ * (device int32[b], clamped to [0, nq] and [0, nk]; NULL: nq, nk).  With causal != 0 the
+ * valid parts end together: query i stands at position i + Lk - Lq and sees keys up to its
+ * own position, with window > 0 only the last `window` of them (itself included).  A row
+ * that sees no key, and rows i >= Lq, get O = 0 and lse = -infinity; rows of Q, K and V
+ * past the lengths may hold anything.  Rows within the lengths have to be finite, also
+ * those that a causal mask hides.
+ *
+ * Q, O: [b][hq][nq][d]; K, V: [b][hk][nk][d], hq a multiple of hk; lse: dense fp32
+ * [b][hq][nq].  dtype LINFORMER_BF16 (else LINFORMER_ERR_UNSUPPORTED), d a multiple of 8 up
+ * to 128 (else LINFORMER_ERR_UNSUPPORTED), 0 < scale < infinity, causal 0 or 1, window >= 0
+ * and 0 unless causal (else LINFORMER_ERR_VALUE); nq, nk and b hq up to 2^29.  Pointers are
+ * 16-byte aligned (lse and the lengths: 4) and strides multiples of 8.  A few query rows
+ * (single tokens over a cache) are served by splitting the keys over the GPU; the parts are
+ * joined in a stream-ordered workspace.  The result of a call does not depend on timing.
+ */
+LINFORMER_API int linformer_softmax_attn_fwd(
+    const void *Q, const int64_t *Q_strides, const void *K, const int64_t *K_strides,
+    const void *V, const int64_t *V_strides, void *O, const int64_t *O_strides, float *lse,
+    const int32_t *q_lengths, const int32_t *k_lengths, int b, int hq, int hk, int nq, int nk,
+    int d, float scale, int causal, int window, int dtype, void *stream);
+
+/*
+ * The backward of linformer_softmax_attn_fwd: from its inputs, its O and lse, and dO =
+ * dLoss/dO, writes
+ *
+ *     dV_j = sum_i p_ij dO_i,          p_ij = exp(s_ij - lse_i)  (recomputed),
+ *     dQ_i = scale sum_j g_ij K_j,     g_ij = p_ij (dO_i . V_j - dO_i . O_i),
+ *     dK_j = scale sum_i g_ij Q_i,
+ *
+ * dK and dV summed over the query heads that share the key/value head; rows past the
+ * lengths get zero.  Same argument rules; dO and dQ are shaped like O, dK and dV like K.
+ * Sums are formed in a fixed order (no atomics): repeated calls agree bit for bit.  The
+ * workspace is 8 bytes per query row, rows rounded up to 128 per head.
+ */
+LINFORMER_API int linformer_softmax_attn_bwd(
+    const void *Q, const int64_t *Q_strides, const void *K, const int64_t *K_strides,
+    const void *V, const int64_t *V_strides, const void *O, const int64_t *O_strides,
+    const void *dO, const int64_t *dO_strides, const float *lse, void *dQ,
+    const int64_t *dQ_strides, void *dK, const int64_t *dK_strides, void *dV,
+    const int64_t *dV_strides, const int32_t *q_lengths, const int32_t *k_lengths, int b, int hq,
+    int hk, int nq, int nk, int d, float scale, int causal, int window, int dtype, void *stream);
+
+/* Which elements of a head form pair i of rot / 2. */
+typedef enum {
+    LINFORMER_ROTARY_HALVES = 0,      /* i and i + rot / 2 */
+    LINFORMER_ROTARY_INTERLEAVED = 1  /* 2 i and 2 i + 1 */
+} linformer_rotary_layout;
+
+/* How a rotary frequency f_i = base^(-2 i / rot) is scaled for contexts longer than the
+ * trained one. */
+typedef enum {
+    LINFORMER_ROTARY_PLAIN = 0,
+    LINFORMER_ROTARY_LINEAR = 1,   /* f_i / factor: positions are compressed */
+    LINFORMER_ROTARY_BASE = 2,     /* base factor^(rot / (rot - 2)): the slowest pair is
+                                      slowed by factor, the fastest keeps its frequency */
+    LINFORMER_ROTARY_BY_PARTS = 3  /* by the turns r_i = original_length f_i / 2 pi that a pair
+                                      makes in the original context: f_i from beta_fast turns
+                                      up, f_i / factor from beta_slow down, linear between */
+} linformer_rotary_scaling;
+
+/*
+ * Rotary positions: pair i of the first rot elements of every head at position pos is turned
+ * by the angle pos f_i and scaled by `amplitude`,
+ *
+ *     y_a = amplitude (x_a cos - x_z sin),   y_z = amplitude (x_z cos + x_a sin);
+ *
+ * elements from rot on are copied.  inverse = 1 turns backwards: with it the call maps the
+ * gradient of Y to the gradient of X.  One call takes up to two tensors that stand at the
+ * same positions (queries and keys): X [b][hx][n][d] -> Y, and, with hx2 > 0, X2 [b][hx2][n][d]
+ * -> Y2.  Y may be X with the same strides (in place).
+ *
+ * positions: device int32 [b][n] (dense), or NULL for start + row.  phase: device, rot / 2
+ * entries, each the pair's turns per position f_i / 2 pi modulo 1 as a 64-bit binary fraction
+ * (linformer_rotary_phase fills it; it is kept and used again by the caller).  Angles are
+ * exact to fp32 at every int32 position.  dtype LINFORMER_F32 or LINFORMER_BF16 (the turn in
+ * fp32, rounded once).  2 <= rot <= d, even; a finite amplitude; start + n <= 2^31 (else
+ * LINFORMER_ERR_VALUE).  X, Y, X2, Y2 16-byte aligned, phase 8; any strides (multiples of 16
+ * bytes, d and rot / 2 multiples of 16 bytes run fastest).
+ */
+LINFORMER_API int linformer_rotary(const void *X, const int64_t *X_strides, void *Y,
+                                   const int64_t *Y_strides, int hx, const void *X2,
+                                   const int64_t *X2_strides, void *Y2, const int64_t *Y2_strides,
+                                   int hx2, const uint64_t *phase, const int32_t *positions,
+                                   int start, int b, int n, int d, int rot, int layout,
+                                   float amplitude, int inverse, int dtype, void *stream);
+
+/* Fills phase (device, rot / 2 entries) for linformer_rotary, asynchronously on `stream`.
+ * base > 0, factor > 0; BY_PARTS also needs original_length >= 1 and beta_fast > beta_slow. */
+LINFORMER_API int linformer_rotary_phase(uint64_t *phase, int rot, double base, int scaling,
+                                         double factor, int original_length, double beta_fast,
+                                         double beta_slow, void *stream);
 
 /*
  * Largest number of bytes the library's workspace pool on the current device has had

@@ -30,6 +30,11 @@ struct Problem {
     size_t out_elem() const { return dtype == LINFORMER_BF16 ? 2 : 4; }
 };
 
+// Element strides of one [b][h][n][d] tensor (the last dimension is contiguous).
+struct Strides {
+    int64_t b, h, n;
+};
+
 // Brackets one kernel launch: counts it and, while profiling is on, records CUDA
 // events around it on its stream.
 class KernelScope {

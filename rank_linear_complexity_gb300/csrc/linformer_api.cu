@@ -371,6 +371,7 @@ extern "C" const char *linformer_status_string(int status) {
         case LINFORMER_ERR_ALLOC: return "workspace allocation failed";
         case LINFORMER_ERR_LAUNCH: return "CUDA call or kernel launch failed";
         case LINFORMER_ERR_DEVICE: return "device-side bounded wait ran out";
+        case LINFORMER_ERR_VALUE: return "a parameter or stride is out of its range";
         default: return "unknown status";
     }
 }
@@ -423,6 +424,7 @@ extern "C" int linformer_profile_collect(double *ms, int64_t *launches) {
 extern "C" const char *linformer_kernel_name(int id) {
     static const char *names[LINFORMER_KERNEL_COUNT] = {
         "tc_project_kernel", "tc_attend_kernel", "simt_project_kernel", "simt_attend_kernel",
-        "window_projection_kernel", "backward_kernels", "dense_attention_kernels"};
+        "window_projection_kernel", "backward_kernels", "dense_attention_kernels",
+        "rotary_kernels", "softmax_attention_kernels", "softmax_attention_backward_kernels"};
     return (id >= 0 && id < LINFORMER_KERNEL_COUNT) ? names[id] : nullptr;
 }

@@ -1,0 +1,83 @@
+// Declarations shared by the exact softmax attention kernels (forward and backward).
+#pragma once
+
+#include <cuda.h>
+#include <cuda_bf16.h>
+#include <cuda_runtime.h>
+#include <cstdint>
+
+#include "internal.cuh"
+
+namespace linformer {
+namespace sattn {
+
+constexpr int kTile = 128;  // rows of a query tile, keys of a key block
+
+// One call's arguments, already validated.
+struct Call {
+    const void *Q, *K, *V, *O, *dO;
+    void *out, *dQ, *dK, *dV;
+    Strides sQ, sK, sV, sO, sdO, sdQ, sdK, sdV;
+    float *lse;
+    const int32_t *q_lengths, *k_lengths;
+    int b, hq, hk, nq, nk, d, causal, window;
+    float scale;
+    cudaStream_t stream;
+};
+
+// Which keys the queries of one sequence see: query i of Lq stands at position
+// i + (Lk - Lq) (the valid parts end together) and sees keys [first, end).
+struct Span {
+    int Lq, Lk, causal, window;
+    __device__ __forceinline__ int end(int i) const {
+        return causal ? min(Lk, i + Lk - Lq + 1) : Lk;
+    }
+    __device__ __forceinline__ int first(int i) const {
+        return window ? max(0, i + Lk - Lq + 1 - window) : 0;
+    }
+};
+
+__device__ __forceinline__ int clamp_length(const int32_t *lengths, int batch, int n) {
+    if (!lengths) return n;
+    const int L = __ldg(lengths + batch);
+    return L < 0 ? 0 : (L > n ? n : L);
+}
+
+__device__ __forceinline__ uint32_t pack2(float a, float b) {
+    __nv_bfloat162 v = __floats2bfloat162_rn(a, b);
+    return *reinterpret_cast<uint32_t *>(&v);
+}
+
+// Eight bf16 of a 16-byte piece as floats.
+__device__ __forceinline__ void unpack8(const uint4 &v, float (&f)[8]) {
+    const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        f[2 * i] = __uint_as_float(w[i] << 16);
+        f[2 * i + 1] = __uint_as_float(w[i] & 0xffff0000u);
+    }
+}
+
+// Zeroes rows [row0, 128) of a tile of DP / 64 column halves (each 128 rows of 128 bytes;
+// whole rows, so the swizzle does not matter), shared by `count` threads.
+template <int DP>
+__device__ __forceinline__ void zero_rows(uint8_t *tile, int row0, int idx, int count) {
+#pragma unroll
+    for (int h = 0; h < DP / 64; ++h) {
+        uint4 *p = reinterpret_cast<uint4 *>(tile + h * 16384 + row0 * 128);
+        for (int i = idx; i < (kTile - row0) * 8; i += count) p[i] = make_uint4(0u, 0u, 0u, 0u);
+    }
+}
+
+// Host helpers (softmax_attn_fwd.cu).
+// Map of a [b][heads][n][d] bf16 tensor for boxes of 64 columns x `rows` rows x `hrows`
+// heads of a group of `group`: coordinates (column, row, head in group, group, batch).
+bool encode_rows(CUtensorMap *m, const void *base, const Strides &s, int b, int heads, int group,
+                 int n, int d, int rows, int hrows);
+int device_sms();
+
+int forward(const Call &c);
+int backward(const Call &c);
+
+}  // namespace sattn
+}  // namespace linformer

@@ -1,0 +1,839 @@
+// Exact softmax attention, backward.  With P_ij = exp(scale Q_i.K_j - lse_i) recomputed
+// from the forward's lse, delta_i = dO_i.O_i and
+//
+//     dP = dO V^T,   dS_ij = P_ij (dP_ij - delta_i),
+//     dV = P^T dO,   dK = scale dS^T Q,   dQ = scale dS K,
+//
+// two kernels, each a sum that one CTA owns, so that no gradient is added up by atomics
+// and every result repeats bit for bit:
+//   dq_kernel   a 128-row query tile against its key blocks: S, dP, then dQ += dS.K.  It
+//               also forms delta and leaves (lse, delta) per row for the second kernel.
+//   dkv_kernel  a 128-key block against the query tiles of every head of its group:
+//               S^T = K.Q^T and dP^T = V.dO^T, then dV += P^T.dO and dK += dS^T.Q.  With
+//               keys as the rows, P^T and dS^T leave the registers of the thread that made
+//               them for the tensor memory of the next product: no transpose, no shared
+//               memory.
+// Seven products instead of five: S and dP are formed twice, which costs less than adding
+// partial dQ through memory in a fixed order.  P and dS are rounded to bf16 as operands
+// (relative 2^-9, in sums of many terms); sums are fp32 in tensor memory.
+//
+// Roles, both kernels: warps 0-3 and 4-7 each take 64 of the 128 columns, one thread a row;
+// warp 8 loads (lane 0) and zeroes rows past the valid length (lanes 1-31, where 0 x NaN
+// would reach a sum); one thread of warp 9 issues the products.
+#include <algorithm>
+#include <cmath>
+
+#include "softmax_attn.cuh"
+#include "sm100_ptx.cuh"
+
+namespace linformer {
+namespace sattn {
+namespace {
+
+using namespace ptx;
+
+constexpr int kThreads = 320;
+constexpr int kLoadWarp = 8, kMmaWarp = 9;
+constexpr float kLog2e = 1.4426950408889634f;
+
+struct BwdParams {
+    const int32_t *q_lengths, *k_lengths;
+    const __nv_bfloat16 *O, *dO;
+    Strides sO, sdO;
+    __nv_bfloat16 *dQ, *dK, *dV;
+    Strides sdQ, sdK, sdV;
+    const float *lse;
+    float *rows;  // [b][hq][query tiles][2][128]: lse log2(e) and delta; dead rows +inf and 0
+    int b, hq, hk, group, nq, nk, d, causal, window;
+    int qtiles, kblocks;
+    int64_t items;
+    float scale, scale_log2;
+    int *status;
+};
+
+// 16 packed words of the thread's row to tensor memory, and the row's tail in a store.
+__device__ __forceinline__ void store_row(__nv_bfloat16 *dst, const uint32_t (&o)[32], int c, int d,
+                                          float f, bool zero) {
+#pragma unroll
+    for (int e = 0; e < 32; e += 8) {
+        if (c + e >= d) break;
+        uint4 w = make_uint4(0u, 0u, 0u, 0u);
+        if (!zero) {
+            w.x = pack2(__uint_as_float(o[e]) * f, __uint_as_float(o[e + 1]) * f);
+            w.y = pack2(__uint_as_float(o[e + 2]) * f, __uint_as_float(o[e + 3]) * f);
+            w.z = pack2(__uint_as_float(o[e + 4]) * f, __uint_as_float(o[e + 5]) * f);
+            w.w = pack2(__uint_as_float(o[e + 6]) * f, __uint_as_float(o[e + 7]) * f);
+        }
+        *reinterpret_cast<uint4 *>(dst + c + e) = w;
+    }
+}
+
+template <int DP>
+__device__ __forceinline__ void mma_scores(uint32_t d, uint32_t a, uint32_t b) {
+    const uint32_t idesc = idesc_f16(128, 128, 1, 0, 0);
+    const uint64_t da = sdesc(a, 16, 1024, kSwizzle128B), db = sdesc(b, 16, 1024, kSwizzle128B);
+#pragma unroll
+    for (int x = 0; x < DP / 16; ++x) {
+        const uint64_t off = (uint64_t)((x >> 2) * 1024 + (x & 3) * 2);
+        mma_ss(d, da + off, db + off, idesc, x > 0 ? 1u : 0u);
+    }
+}
+// D (128 x DP) += A (128 x 128, packed in tensor memory: columns [0, 32) hold the first 64,
+// [64, 96) the others) . B (128 rows of DP)
+template <int DP>
+__device__ __forceinline__ void mma_sum(uint32_t d, uint32_t a, uint32_t b, uint32_t acc) {
+    const uint32_t idesc = idesc_f16(128, DP, 1, 0, 1);
+    const uint64_t db = sdesc(b, 16384, 1024, kSwizzle128B);
+#pragma unroll
+    for (int x = 0; x < 8; ++x)
+        mma_ts(d, a + (x >> 2) * 64 + (x & 3) * 8, db + (uint64_t)(128 * x), idesc,
+               (acc || x > 0) ? 1u : 0u);
+}
+
+template <int DP>
+__device__ __forceinline__ void load_rows(uint8_t *dst, const CUtensorMap *m, uint64_t *bar, int row,
+                                          int head, int group, int batch) {
+#pragma unroll
+    for (int h = 0; h < DP / 64; ++h) tma_load_5d(dst + h * 16384, m, bar, h * 64, row, head, group, batch);
+}
+
+// ---------------------------------------------------------------- dQ
+template <int DP>
+struct DqLayout {
+    static constexpr uint32_t kTileBytes = kTile * DP * 2;
+    static constexpr int kStages = DP == 64 ? 8 : 5;
+    static constexpr uint32_t kS = 0, kDp = 128, kDq = 384;
+    static constexpr uint32_t kSmem = 1024 + (2 + kStages) * kTileBytes + 512;
+};
+struct DqItem {
+    int batch, head, q0, lo, hi;
+    Span sp;
+};
+__device__ __forceinline__ DqItem dq_item(const BwdParams &p, int64_t idx) {
+    DqItem it;
+    const int units = p.b * p.hq;
+    const int u = (int)(idx % units), rank = (int)(idx / units);
+    const int tile = p.causal ? p.qtiles - 1 - rank : rank;  // longest first
+    it.batch = u / p.hq;
+    it.head = u % p.hq;
+    it.q0 = tile * kTile;
+    it.sp = Span{clamp_length(p.q_lengths, it.batch, p.nq), clamp_length(p.k_lengths, it.batch, p.nk),
+                 p.causal, p.window};
+    it.lo = it.hi = 0;
+    const int last = min(it.q0 + kTile, it.sp.Lq) - 1;
+    if (last >= it.q0) {
+        const int e = it.sp.end(last), f = it.sp.first(it.q0);
+        if (e > f) {
+            it.lo = f / kTile;
+            it.hi = (e + kTile - 1) / kTile;
+        }
+    }
+    return it;
+}
+
+struct DqBarriers {
+    uint64_t q_full, q_free, s_full, s_free, dp_full[2], ds_full[2], dq_done[2], acc_free;
+    uint64_t fix_wanted, fixed, drain;
+    uint64_t full[8], empty[8];
+    uint32_t tmem;
+    int abort;
+};
+
+template <int DP>
+__global__ void __launch_bounds__(kThreads, 1)
+softmax_attn_dq_kernel(const __grid_constant__ CUtensorMap tQ, const __grid_constant__ CUtensorMap tK,
+                       const __grid_constant__ CUtensorMap tV, const __grid_constant__ CUtensorMap tdO,
+                       const BwdParams p) {
+    using C = DqLayout<DP>;
+    extern __shared__ uint8_t raw[];
+    uint8_t *smem = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(raw) + 1023) & ~uintptr_t(1023));
+    uint8_t *sQ = smem, *sdO = smem + C::kTileBytes, *sKV = smem + 2 * C::kTileBytes;
+    DqBarriers *bar = reinterpret_cast<DqBarriers *>(sKV + C::kStages * C::kTileBytes);
+    volatile int *abort_flag = &bar->abort;
+    const int tid = threadIdx.x, warp = __shfl_sync(0xffffffffu, tid >> 5, 0), lane = tid & 31;
+
+    if (tid == 0) {
+        mbar_init(&bar->q_full, 1);
+        mbar_init(&bar->q_free, 1);
+        mbar_init(&bar->s_full, 1);
+        mbar_init(&bar->s_free, 8);
+        for (int i = 0; i < 2; ++i) {
+            mbar_init(&bar->dp_full[i], 1);
+            mbar_init(&bar->ds_full[i], 8);
+            mbar_init(&bar->dq_done[i], 1);
+        }
+        mbar_init(&bar->acc_free, 8);
+        mbar_init(&bar->fix_wanted, 1);
+        mbar_init(&bar->fixed, 31);
+        mbar_init(&bar->drain, 1);
+        for (int s = 0; s < C::kStages; ++s) {
+            mbar_init(&bar->full[s], 1);
+            mbar_init(&bar->empty[s], 1);
+        }
+        bar->abort = 0;
+        fence_mbar_init();
+    }
+    if (warp == kMmaWarp) {
+        tmem_alloc(&bar->tmem, 512);
+        tmem_relinquish();
+    }
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    const uint32_t tmem = bar->tmem;
+    // ring entry 2 j + kv of an item: K (kv = 0) and V of its j-th block
+    if (warp == kLoadWarp) {
+        if (lane == 0) {
+            int ring = 0, nq = 0;
+            bool ok = true;
+            for (int64_t idx = blockIdx.x; idx < p.items && ok; idx += gridDim.x) {
+                const DqItem it = dq_item(p, idx);
+                if (it.hi <= it.lo) continue;
+                if (nq > 0 && !mbar_wait(&bar->q_free, (nq - 1) & 1, p.status, 83, abort_flag)) break;
+                mbar_arrive_expect_tx(&bar->q_full, 2 * C::kTileBytes);
+                const int g = it.head % p.group, kvh = it.head / p.group;
+                load_rows<DP>(sQ, &tQ, &bar->q_full, it.q0, g, kvh, it.batch);
+                load_rows<DP>(sdO, &tdO, &bar->q_full, it.q0, g, kvh, it.batch);
+                ++nq;
+                for (int j = it.lo; j < it.hi && ok; ++j)
+                    for (int kv = 0; kv < 2; ++kv, ++ring) {
+                        const int s = ring % C::kStages;
+                        if (ring >= C::kStages &&
+                            !mbar_wait(&bar->empty[s], (ring / C::kStages - 1) & 1, p.status, 84, abort_flag)) {
+                            ok = false;
+                            break;
+                        }
+                        mbar_arrive_expect_tx(&bar->full[s], C::kTileBytes);
+                        load_rows<DP>(sKV + s * C::kTileBytes, kv ? &tV : &tK, &bar->full[s], j * kTile, 0,
+                                      kvh, it.batch);
+                    }
+            }
+            if (nq > 0) mbar_wait_drain(&bar->q_full, (nq - 1) & 1);
+            for (int i = max(0, ring - C::kStages); i < ring; ++i)
+                mbar_wait_drain(&bar->full[i % C::kStages], (i / C::kStages) & 1);
+        } else {  // K rows past the valid length: dS is 0 there, but 0 x NaN is not
+            int ring = 0, nfix = 0;
+            for (int64_t idx = blockIdx.x; idx < p.items; idx += gridDim.x) {
+                const DqItem it = dq_item(p, idx);
+                if (it.hi <= it.lo) continue;
+                ring += 2 * (it.hi - it.lo);
+                if (it.sp.Lk >= p.nk || it.hi * kTile <= it.sp.Lk) continue;
+                if (!mbar_wait(&bar->fix_wanted, nfix & 1, p.status, 85, abort_flag)) break;
+                ++nfix;
+                zero_rows<DP>(sKV + (ring - 2) % C::kStages * C::kTileBytes,
+                              it.sp.Lk - (it.hi - 1) * kTile, lane - 1, 31);
+                fence_proxy_async_smem();
+                mbar_arrive(&bar->fixed);
+            }
+        }
+        __syncwarp();
+    } else if (warp == kMmaWarp) {
+        if (elect_one()) {
+            int ring = 0, items = 0, n = 0, nfix = 0;
+            bool ok = true;
+            const uint32_t aQ = smem_u32(sQ), adO = smem_u32(sdO), aKV = smem_u32(sKV);
+            for (int64_t idx = blockIdx.x; idx < p.items && ok; idx += gridDim.x) {
+                const DqItem it = dq_item(p, idx);
+                const int blocks = it.hi - it.lo;
+                if (blocks <= 0) continue;
+                const bool fix = it.sp.Lk < p.nk && it.hi * kTile > it.sp.Lk;
+                // S and dP of the item's block j: n + j blocks of this CTA came before
+                auto score = [&](int j) {
+                    const int r = ring + 2 * j, s = r % C::kStages;
+                    if (!mbar_wait(&bar->full[s], (r / C::kStages) & 1, p.status, 86, abort_flag)) return false;
+                    if (fix && j == blocks - 1) {
+                        mbar_arrive(&bar->fix_wanted);
+                        if (!mbar_wait(&bar->fixed, nfix & 1, p.status, 87, abort_flag)) return false;
+                        ++nfix;
+                    }
+                    if (n + j > 0 && !mbar_wait(&bar->s_free, (n + j - 1) & 1, p.status, 88, abort_flag))
+                        return false;
+                    tc_fence_after();
+                    mma_scores<DP>(tmem + C::kS, aQ, aKV + s * C::kTileBytes);
+                    mma_commit(&bar->s_full);
+                    return true;
+                };
+                auto dprob = [&](int j) {
+                    const int r = ring + 2 * j + 1, s = r % C::kStages, k = n + j;
+                    if (!mbar_wait(&bar->full[s], (r / C::kStages) & 1, p.status, 89, abort_flag)) return false;
+                    if (k >= 2 && !mbar_wait(&bar->dq_done[k & 1], ((k >> 1) - 1) & 1, p.status, 90, abort_flag))
+                        return false;
+                    tc_fence_after();
+                    mma_scores<DP>(tmem + C::kDp + 128 * (k & 1), adO, aKV + s * C::kTileBytes);
+                    mma_commit(&bar->dp_full[k & 1]);
+                    mma_commit(&bar->empty[s]);
+                    return true;
+                };
+                ok = mbar_wait(&bar->q_full, items & 1, p.status, 91, abort_flag) && score(0) && dprob(0);
+                for (int j = 0; j < blocks && ok; ++j) {
+                    if (j + 1 < blocks && !(score(j + 1) && dprob(j + 1))) {
+                        ok = false;
+                        break;
+                    }
+                    if (j + 1 >= blocks) mma_commit(&bar->q_free);  // the item's last use of Q and dO
+                    const int k = n + j, s = (ring + 2 * j) % C::kStages;
+                    ok = mbar_wait(&bar->ds_full[k & 1], (k >> 1) & 1, p.status, 92, abort_flag) &&
+                         (j > 0 || items == 0 ||
+                          mbar_wait(&bar->acc_free, (items - 1) & 1, p.status, 93, abort_flag));
+                    if (!ok) break;
+                    tc_fence_after();
+                    mma_sum<DP>(tmem + C::kDq, tmem + C::kDp + 128 * (k & 1), aKV + s * C::kTileBytes,
+                                j > 0 ? 1u : 0u);
+                    mma_commit(&bar->dq_done[k & 1]);
+                    mma_commit(&bar->empty[s]);
+                }
+                n += blocks;
+                ring += 2 * blocks;
+                ++items;
+            }
+            mma_commit(&bar->drain);
+            mbar_wait_drain(&bar->drain, 0);
+        }
+        __syncwarp();
+    } else {
+        const int w = warp >> 2, row = tid & 127;  // column half, row
+        const uint32_t lanes = (uint32_t)((warp & 3) * 32) << 16;
+        const float sl = p.scale_log2;
+        int n = 0;
+        for (int64_t idx = blockIdx.x; idx < p.items; idx += gridDim.x) {
+            const DqItem it = dq_item(p, idx);
+            const int i = it.q0 + row;
+            const bool exists = i < p.nq, valid = i < it.sp.Lq;
+            // delta_i = dO_i.O_i, and the row's entry for the other kernel
+            float delta = 0.f, lse2 = INFINITY;
+            if (valid) {
+                const uint4 *o = reinterpret_cast<const uint4 *>(p.O + it.batch * p.sO.b + it.head * p.sO.h +
+                                                                 (int64_t)i * p.sO.n);
+                const uint4 *g = reinterpret_cast<const uint4 *>(p.dO + it.batch * p.sdO.b +
+                                                                 it.head * p.sdO.h + (int64_t)i * p.sdO.n);
+                const float x = p.lse[((int64_t)it.batch * p.hq + it.head) * p.nq + i];
+                for (int c = 0; c < p.d / 8; ++c) {
+                    float a[8], b[8];
+                    unpack8(__ldg(o + c), a);
+                    unpack8(__ldg(g + c), b);
+#pragma unroll
+                    for (int e = 0; e < 8; ++e) delta = fmaf(a[e], b[e], delta);
+                }
+                if (x != -INFINITY) lse2 = x * kLog2e;
+                else delta = 0.f;
+            }
+            if (w == 0) {
+                float *dst = p.rows + (((int64_t)it.batch * p.hq + it.head) * p.qtiles + it.q0 / kTile) * 256;
+                dst[row] = lse2;
+                dst[128 + row] = delta;
+            }
+            const int first = valid ? it.sp.first(i) : 0, end = valid ? it.sp.end(i) : 0;
+            bool ok = true;
+            for (int j = it.lo; j < it.hi; ++j, ++n) {
+                if (!warp_wait(&bar->s_full, n & 1, p.status, 94, abort_flag)) {
+                    ok = false;
+                    break;
+                }
+                tc_fence_after();
+                uint32_t v[2][32];
+                tmem_ld32_async(tmem + C::kS + 64 * w + lanes, v[0]);
+                tmem_ld32_async(tmem + C::kS + 64 * w + 32 + lanes, v[1]);
+                tmem_wait_ld(v[0]);
+                tie32(v[1]);
+                tc_fence_before();
+                __syncwarp();
+                if (lane == 0) mbar_arrive(&bar->s_free);
+                const float2 sl2 = make_float2(sl, sl), off2 = make_float2(-lse2, -lse2);
+#pragma unroll
+                for (int c = 0; c < 2; ++c)
+#pragma unroll
+                    for (int e = 0; e < 32; e += 2) {
+                        const float2 y = ffma2(make_float2(__uint_as_float(v[c][e]), __uint_as_float(v[c][e + 1])),
+                                               sl2, off2);
+                        v[c][e] = __float_as_uint(ex2_approx(y.x));
+                        v[c][e + 1] = __float_as_uint(ex2_approx(y.y));
+                    }
+                const uint32_t tD = tmem + C::kDp + 128 * (n & 1) + 64 * w + lanes;
+                if (!warp_wait(&bar->dp_full[n & 1], (n >> 1) & 1, p.status, 95, abort_flag)) {
+                    ok = false;
+                    break;
+                }
+                tc_fence_after();
+                uint32_t u[2][32];
+                tmem_ld32_async(tD, u[0]);
+                tmem_ld32_async(tD + 32, u[1]);
+                tmem_wait_ld(u[0]);
+                tie32(u[1]);
+                const int k0 = j * kTile + 64 * w;
+                const float2 nd = make_float2(-delta, -delta);
+#pragma unroll
+                for (int c = 0; c < 2; ++c)
+#pragma unroll
+                    for (int e = 0; e < 32; e += 2) {
+                        const float2 y = fadd2(make_float2(__uint_as_float(u[c][e]), __uint_as_float(u[c][e + 1])), nd);
+                        const float2 z = fmul2(make_float2(__uint_as_float(v[c][e]), __uint_as_float(v[c][e + 1])), y);
+                        v[c][e] = __float_as_uint(z.x);
+                        v[c][e + 1] = __float_as_uint(z.y);
+                    }
+                // masked keys (whatever their S and dP hold) take no part
+                if (__any_sync(0xffffffffu, first > k0 || end < k0 + 64)) {
+                    const int a = first - k0;
+                    const unsigned wd = end > first ? (unsigned)(end - first) : 0u;
+#pragma unroll
+                    for (int c = 0; c < 2; ++c)
+#pragma unroll
+                        for (int e = 0; e < 32; ++e)
+                            if ((unsigned)(32 * c + e - a) >= wd) v[c][e] = 0u;
+                }
+#pragma unroll
+                for (int c = 0; c < 2; ++c) {
+                    uint32_t o[16];
+#pragma unroll
+                    for (int e = 0; e < 16; ++e)
+                        o[e] = pack2(__uint_as_float(v[c][2 * e]), __uint_as_float(v[c][2 * e + 1]));
+                    tmem_st16_async(tD + 16 * c, o);
+                }
+                tmem_wait_st();
+                tc_fence_before();
+                __syncwarp();
+                if (lane == 0) mbar_arrive(&bar->ds_full[n & 1]);
+            }
+            if (!ok) break;
+            const bool some = it.hi > it.lo;
+            if (some) {
+                if (!warp_wait(&bar->dq_done[(n - 1) & 1], ((n - 1) >> 1) & 1, p.status, 96, abort_flag)) break;
+                tc_fence_after();
+            }
+            __nv_bfloat16 *dst = p.dQ + it.batch * p.sdQ.b + it.head * p.sdQ.h + (int64_t)i * p.sdQ.n;
+#pragma unroll
+            for (int c = 0; c < DP / 2; c += 32) {
+                uint32_t o[32];
+                const int col = w * (DP / 2) + c;
+                if (some) tmem_ld32(tmem + C::kDq + col + lanes, o);
+                if (exists) store_row(dst, o, col, p.d, p.scale, !some || !valid);
+            }
+            if (some) {
+                tc_fence_before();
+                __syncwarp();
+                if (lane == 0) mbar_arrive(&bar->acc_free);
+            }
+        }
+    }
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    if (warp == kMmaWarp) tmem_dealloc(tmem, 512);
+}
+
+// ---------------------------------------------------------------- dK, dV
+template <int DP>
+struct DkvLayout {
+    static constexpr uint32_t kTileBytes = kTile * DP * 2;
+    static constexpr int kStages = DP == 64 ? 4 : 2;
+    static constexpr uint32_t kStageBytes = 2 * kTileBytes + 1024;  // Q, dO, lse and delta
+    static constexpr uint32_t kS = 0, kDp = 128, kDv = 256, kDk = 256 + DP;
+    static constexpr uint32_t kSmem = 1024 + 2 * kTileBytes + kStages * kStageBytes + 512;
+};
+struct DkvItem {
+    int batch, kvh, k0, lo, hi;  // query tiles [lo, hi) of each head of the group
+    Span sp;
+};
+__device__ __forceinline__ DkvItem dkv_item(const BwdParams &p, int64_t idx) {
+    DkvItem it;
+    const int units = p.b * p.hk;
+    const int u = (int)(idx % units);
+    it.k0 = (int)(idx / units) * kTile;  // causal: early keys are seen by the most queries
+    it.batch = u / p.hk;
+    it.kvh = u % p.hk;
+    it.sp = Span{clamp_length(p.q_lengths, it.batch, p.nq), clamp_length(p.k_lengths, it.batch, p.nk),
+                 p.causal, p.window};
+    it.lo = it.hi = 0;
+    const int last = min(it.k0 + kTile, it.sp.Lk) - 1, off = it.sp.Lk - it.sp.Lq;
+    if (last >= it.k0) {
+        const int a = p.causal ? max(0, it.k0 - off) : 0;
+        const int z = p.window ? min((long long)it.sp.Lq, (long long)last - off + p.window) : it.sp.Lq;
+        if (z > a) {
+            it.lo = a / kTile;
+            it.hi = (z + kTile - 1) / kTile;
+        }
+    }
+    return it;
+}
+
+struct DkvBarriers {
+    uint64_t kv_full, kv_free, s_full, p_full, pv_done, dp_full, ds_full, ds_done, acc_full, acc_free;
+    uint64_t fix_wanted, fixed, drain;
+    uint64_t full[4], empty[4];
+    uint32_t tmem;
+    int abort;
+};
+
+template <int DP>
+__global__ void __launch_bounds__(kThreads, 1)
+softmax_attn_dkv_kernel(const __grid_constant__ CUtensorMap tQ, const __grid_constant__ CUtensorMap tK,
+                        const __grid_constant__ CUtensorMap tV, const __grid_constant__ CUtensorMap tdO,
+                        const BwdParams p) {
+    using C = DkvLayout<DP>;
+    extern __shared__ uint8_t raw[];
+    uint8_t *smem = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(raw) + 1023) & ~uintptr_t(1023));
+    uint8_t *sK = smem, *sV = smem + C::kTileBytes, *sT = smem + 2 * C::kTileBytes;
+    // stage s: Q and dO tiles, then (after all tiles) its 1 KB of row values
+    uint8_t *sR = sT + C::kStages * 2 * C::kTileBytes;
+    DkvBarriers *bar = reinterpret_cast<DkvBarriers *>(sR + C::kStages * 1024);
+    volatile int *abort_flag = &bar->abort;
+    const int tid = threadIdx.x, warp = __shfl_sync(0xffffffffu, tid >> 5, 0), lane = tid & 31;
+
+    if (tid == 0) {
+        mbar_init(&bar->kv_full, 1);
+        mbar_init(&bar->kv_free, 1);
+        mbar_init(&bar->s_full, 1);
+        mbar_init(&bar->p_full, 8);
+        mbar_init(&bar->pv_done, 1);
+        mbar_init(&bar->dp_full, 1);
+        mbar_init(&bar->ds_full, 8);
+        mbar_init(&bar->ds_done, 1);
+        mbar_init(&bar->acc_full, 1);
+        mbar_init(&bar->acc_free, 8);
+        mbar_init(&bar->fix_wanted, 1);
+        mbar_init(&bar->fixed, 31);
+        mbar_init(&bar->drain, 1);
+        for (int s = 0; s < C::kStages; ++s) {
+            mbar_init(&bar->full[s], 1);
+            mbar_init(&bar->empty[s], 1);
+        }
+        bar->abort = 0;
+        fence_mbar_init();
+    }
+    if (warp == kMmaWarp) {
+        tmem_alloc(&bar->tmem, 512);
+        tmem_relinquish();
+    }
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    const uint32_t tmem = bar->tmem;
+
+    if (warp == kLoadWarp) {
+        if (lane == 0) {
+            int ring = 0, items = 0;
+            bool ok = true;
+            for (int64_t idx = blockIdx.x; idx < p.items && ok; idx += gridDim.x) {
+                const DkvItem it = dkv_item(p, idx);
+                if (it.hi <= it.lo) continue;
+                if (items > 0 && !mbar_wait(&bar->kv_free, (items - 1) & 1, p.status, 100, abort_flag)) break;
+                mbar_arrive_expect_tx(&bar->kv_full, 2 * C::kTileBytes);
+                load_rows<DP>(sK, &tK, &bar->kv_full, it.k0, 0, it.kvh, it.batch);
+                load_rows<DP>(sV, &tV, &bar->kv_full, it.k0, 0, it.kvh, it.batch);
+                ++items;
+                for (int g = 0; g < p.group && ok; ++g)
+                    for (int j = it.lo; j < it.hi; ++j, ++ring) {
+                        const int s = ring % C::kStages;
+                        if (ring >= C::kStages &&
+                            !mbar_wait(&bar->empty[s], (ring / C::kStages - 1) & 1, p.status, 101, abort_flag)) {
+                            ok = false;
+                            break;
+                        }
+                        uint8_t *st = sT + s * 2 * C::kTileBytes;
+                        mbar_arrive_expect_tx(&bar->full[s], 2 * C::kTileBytes + 1024);
+                        load_rows<DP>(st, &tQ, &bar->full[s], j * kTile, g, it.kvh, it.batch);
+                        load_rows<DP>(st + C::kTileBytes, &tdO, &bar->full[s], j * kTile, g, it.kvh, it.batch);
+                        const int64_t head = (int64_t)it.batch * p.hq + it.kvh * p.group + g;
+                        bulk_load(sR + s * 1024, p.rows + (head * p.qtiles + j) * 256, 1024, &bar->full[s]);
+                    }
+            }
+            if (items > 0) mbar_wait_drain(&bar->kv_full, (items - 1) & 1);
+            for (int i = max(0, ring - C::kStages); i < ring; ++i)
+                mbar_wait_drain(&bar->full[i % C::kStages], (i / C::kStages) & 1);
+        } else {  // Q and dO rows past the valid length: P and dS are 0 there, but 0 x NaN is not
+            int ring = 0, nfix = 0;
+            bool ok = true;
+            for (int64_t idx = blockIdx.x; idx < p.items && ok; idx += gridDim.x) {
+                const DkvItem it = dkv_item(p, idx);
+                if (it.hi <= it.lo) continue;
+                if (it.sp.Lq >= p.nq || it.hi * kTile <= it.sp.Lq) {
+                    ring += p.group * (it.hi - it.lo);
+                    continue;
+                }
+                for (int g = 0; g < p.group; ++g) {
+                    ring += it.hi - it.lo;
+                    if (!mbar_wait(&bar->fix_wanted, nfix & 1, p.status, 102, abort_flag)) {
+                        ok = false;
+                        break;
+                    }
+                    ++nfix;
+                    uint8_t *st = sT + (ring - 1) % C::kStages * 2 * C::kTileBytes;
+                    zero_rows<DP>(st, it.sp.Lq - (it.hi - 1) * kTile, lane - 1, 31);
+                    zero_rows<DP>(st + C::kTileBytes, it.sp.Lq - (it.hi - 1) * kTile, lane - 1, 31);
+                    fence_proxy_async_smem();
+                    mbar_arrive(&bar->fixed);
+                }
+            }
+        }
+        __syncwarp();
+    } else if (warp == kMmaWarp) {
+        if (elect_one()) {
+            int n = 0, items = 0, nfix = 0;
+            bool ok = true;
+            const uint32_t aK = smem_u32(sK), aV = smem_u32(sV), aT = smem_u32(sT);
+            for (int64_t idx = blockIdx.x; idx < p.items && ok; idx += gridDim.x) {
+                const DkvItem it = dkv_item(p, idx);
+                const int per = it.hi - it.lo;
+                if (per <= 0) continue;
+                const int steps = per * p.group;
+                const bool fix = it.sp.Lq < p.nq && it.hi * kTile > it.sp.Lq;
+                int in_head = 0;  // tile of the next score step within its head
+                auto score = [&](int j) {
+                    const int r = n + j, s = r % C::kStages;
+                    if (!mbar_wait(&bar->full[s], (r / C::kStages) & 1, p.status, 103, abort_flag)) return false;
+                    if (++in_head == per) {
+                        in_head = 0;
+                        if (fix) {
+                            mbar_arrive(&bar->fix_wanted);
+                            if (!mbar_wait(&bar->fixed, nfix & 1, p.status, 104, abort_flag)) return false;
+                            ++nfix;
+                        }
+                    }
+                    // S holds the P of the step before until its product is done
+                    if (r > 0 && !mbar_wait(&bar->pv_done, (r - 1) & 1, p.status, 105, abort_flag)) return false;
+                    tc_fence_after();
+                    mma_scores<DP>(tmem + C::kS, aK, aT + s * 2 * C::kTileBytes);
+                    mma_commit(&bar->s_full);
+                    return true;
+                };
+                auto dprob = [&](int j) {
+                    const int r = n + j, s = r % C::kStages;
+                    if (r > 0 && !mbar_wait(&bar->ds_done, (r - 1) & 1, p.status, 106, abort_flag)) return false;
+                    tc_fence_after();
+                    mma_scores<DP>(tmem + C::kDp, aV, aT + s * 2 * C::kTileBytes + C::kTileBytes);
+                    mma_commit(&bar->dp_full);
+                    return true;
+                };
+                ok = mbar_wait(&bar->kv_full, items & 1, p.status, 107, abort_flag) && score(0) && dprob(0);
+                for (int j = 0; j < steps && ok; ++j) {
+                    const int r = n + j, s = r % C::kStages;
+                    const uint32_t aQ = aT + s * 2 * C::kTileBytes, adO = aQ + C::kTileBytes;
+                    ok = mbar_wait(&bar->p_full, r & 1, p.status, 108, abort_flag) &&
+                         (j > 0 || items == 0 ||
+                          mbar_wait(&bar->acc_free, (items - 1) & 1, p.status, 109, abort_flag));
+                    if (!ok) break;
+                    tc_fence_after();
+                    mma_sum<DP>(tmem + C::kDv, tmem + C::kS, adO, j > 0 ? 1u : 0u);
+                    mma_commit(&bar->pv_done);
+                    if (j + 1 < steps && !(ok = score(j + 1))) break;
+                    if (!(ok = mbar_wait(&bar->ds_full, r & 1, p.status, 110, abort_flag))) break;
+                    tc_fence_after();
+                    mma_sum<DP>(tmem + C::kDk, tmem + C::kDp, aQ, j > 0 ? 1u : 0u);
+                    mma_commit(&bar->ds_done);
+                    mma_commit(&bar->empty[s]);
+                    if (j + 1 < steps) ok = dprob(j + 1);
+                }
+                if (!ok) break;
+                mma_commit(&bar->kv_free);
+                mma_commit(&bar->acc_full);
+                n += steps;
+                ++items;
+            }
+            mma_commit(&bar->drain);
+            mbar_wait_drain(&bar->drain, 0);
+        }
+        __syncwarp();
+    } else {
+        const int w = warp >> 2, row = tid & 127;  // query-column half, key row
+        const uint32_t lanes = (uint32_t)((warp & 3) * 32) << 16;
+        const uint32_t tS = tmem + C::kS + 64 * w + lanes, tD = tmem + C::kDp + 64 * w + lanes;
+        const float sl = p.scale_log2;
+        const float2 sl2 = make_float2(sl, sl);
+        int n = 0, items = 0;
+        bool ok = true;
+        for (int64_t idx = blockIdx.x; idx < p.items && ok; idx += gridDim.x) {
+            const DkvItem it = dkv_item(p, idx);
+            const int key = it.k0 + row, off = it.sp.Lk - it.sp.Lq;
+            const bool exists = key < p.nk, valid = key < it.sp.Lk;
+            // queries [first, end) see this key
+            const int first = p.causal ? max(0, key - off) : 0;
+            const int end = p.window ? (int)min((long long)it.sp.Lq, (long long)key - off + p.window) : it.sp.Lq;
+            const int per = it.hi - it.lo, steps = per * p.group;
+            int j = it.lo;
+            for (int x = 0; x < steps; ++x, ++n) {
+                const int s = n % C::kStages;
+                const float4 *lse4 = reinterpret_cast<const float4 *>(sR + s * 1024 + w * 256);
+                const float4 *del4 = reinterpret_cast<const float4 *>(sR + s * 1024 + 512 + w * 256);
+                if (!warp_wait(&bar->full[s], (n / C::kStages) & 1, p.status, 111, abort_flag) ||
+                    !warp_wait(&bar->s_full, n & 1, p.status, 112, abort_flag)) {
+                    ok = false;
+                    break;
+                }
+                tc_fence_after();
+                uint32_t v[2][32];
+                tmem_ld32_async(tS, v[0]);
+                tmem_ld32_async(tS + 32, v[1]);
+                tmem_wait_ld(v[0]);
+                tie32(v[1]);
+                const int q0 = j * kTile + 64 * w;
+                const bool masked = __any_sync(0xffffffffu, first > q0 || (p.window && end < q0 + 64));
+#pragma unroll
+                for (int c = 0; c < 2; ++c)
+#pragma unroll
+                    for (int e = 0; e < 32; e += 4) {
+                        const float4 l = lse4[8 * c + e / 4];
+                        const float2 y0 = ffma2(make_float2(__uint_as_float(v[c][e]), __uint_as_float(v[c][e + 1])),
+                                                sl2, make_float2(-l.x, -l.y));
+                        const float2 y1 = ffma2(make_float2(__uint_as_float(v[c][e + 2]), __uint_as_float(v[c][e + 3])),
+                                                sl2, make_float2(-l.z, -l.w));
+                        v[c][e] = __float_as_uint(ex2_approx(y0.x));
+                        v[c][e + 1] = __float_as_uint(ex2_approx(y0.y));
+                        v[c][e + 2] = __float_as_uint(ex2_approx(y1.x));
+                        v[c][e + 3] = __float_as_uint(ex2_approx(y1.y));
+                    }
+                if (masked) {
+                    const int a = first - q0;
+                    const unsigned wd = end > first ? (unsigned)(end - first) : 0u;
+#pragma unroll
+                    for (int c = 0; c < 2; ++c)
+#pragma unroll
+                        for (int e = 0; e < 32; ++e)
+                            if ((unsigned)(32 * c + e - a) >= wd) v[c][e] = 0u;
+                }
+#pragma unroll
+                for (int c = 0; c < 2; ++c) {
+                    uint32_t o[16];
+#pragma unroll
+                    for (int e = 0; e < 16; ++e)
+                        o[e] = pack2(__uint_as_float(v[c][2 * e]), __uint_as_float(v[c][2 * e + 1]));
+                    tmem_st16_async(tS + 16 * c, o);
+                }
+                tmem_wait_st();
+                tc_fence_before();
+                __syncwarp();
+                if (lane == 0) mbar_arrive(&bar->p_full);
+                if (!warp_wait(&bar->dp_full, n & 1, p.status, 113, abort_flag)) {
+                    ok = false;
+                    break;
+                }
+                tc_fence_after();
+#pragma unroll
+                for (int c = 0; c < 2; ++c) {
+                    uint32_t u[32], o[16];
+                    tmem_ld32(tD + 32 * c, u);
+                    // the other half's columns, and this half's second 32, are read before
+                    // anything is written over them: dS of 32 columns takes 16, written at
+                    // the start of the half after both loads
+#pragma unroll
+                    for (int e = 0; e < 32; e += 4) {
+                        const float4 dl = del4[8 * c + e / 4];
+                        const float2 y0 = fadd2(make_float2(__uint_as_float(u[e]), __uint_as_float(u[e + 1])),
+                                                make_float2(-dl.x, -dl.y));
+                        const float2 y1 = fadd2(make_float2(__uint_as_float(u[e + 2]), __uint_as_float(u[e + 3])),
+                                                make_float2(-dl.z, -dl.w));
+                        const float2 z0 = fmul2(make_float2(__uint_as_float(v[c][e]), __uint_as_float(v[c][e + 1])), y0);
+                        const float2 z1 = fmul2(make_float2(__uint_as_float(v[c][e + 2]), __uint_as_float(v[c][e + 3])), y1);
+                        o[e / 2] = pack2(z0.x, z0.y);
+                        o[e / 2 + 1] = pack2(z1.x, z1.y);
+                    }
+                    tmem_st16_async(tD + 16 * c, o);
+                }
+                tmem_wait_st();
+                tc_fence_before();
+                __syncwarp();
+                if (lane == 0) mbar_arrive(&bar->ds_full);
+                if (++j == it.hi) j = it.lo;
+            }
+            if (!ok) break;
+            const bool some = steps > 0;
+            if (some) {
+                if (!warp_wait(&bar->acc_full, items & 1, p.status, 114, abort_flag)) break;
+                tc_fence_after();
+                ++items;
+            }
+            __nv_bfloat16 *dk = p.dK + it.batch * p.sdK.b + it.kvh * p.sdK.h + (int64_t)key * p.sdK.n;
+            __nv_bfloat16 *dv = p.dV + it.batch * p.sdV.b + it.kvh * p.sdV.h + (int64_t)key * p.sdV.n;
+            // warps 0-3 write dV, warps 4-7 dK
+#pragma unroll
+            for (int c = 0; c < DP; c += 32) {
+                uint32_t o[32];
+                if (some) tmem_ld32(tmem + (w ? C::kDk : C::kDv) + c + lanes, o);
+                if (exists) store_row(w ? dk : dv, o, c, p.d, w ? p.scale : 1.f, !some || !valid);
+            }
+            if (some) {
+                tc_fence_before();
+                __syncwarp();
+                if (lane == 0) mbar_arrive(&bar->acc_free);
+            }
+        }
+    }
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    if (warp == kMmaWarp) tmem_dealloc(tmem, 512);
+}
+
+template <int DP>
+int launch(const Call &c, BwdParams &p) {
+    using Cq = DqLayout<DP>;
+    using Ck = DkvLayout<DP>;
+    CUtensorMap tQ, tK, tV, tdO;
+    if (!encode_rows(&tQ, c.Q, c.sQ, c.b, c.hq, p.group, c.nq, c.d, kTile, 1) ||
+        !encode_rows(&tdO, c.dO, c.sdO, c.b, c.hq, p.group, c.nq, c.d, kTile, 1) ||
+        !encode_rows(&tK, c.K, c.sK, c.b, c.hk, 1, c.nk, c.d, kTile, 1) ||
+        !encode_rows(&tV, c.V, c.sV, c.b, c.hk, 1, c.nk, c.d, kTile, 1))
+        return LINFORMER_ERR_LAUNCH;
+    if (cudaFuncSetAttribute(softmax_attn_dq_kernel<DP>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                             Cq::kSmem) != cudaSuccess ||
+        cudaFuncSetAttribute(softmax_attn_dkv_kernel<DP>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                             Ck::kSmem) != cudaSuccess)
+        return LINFORMER_ERR_LAUNCH;
+    void *ws = nullptr;
+    const int64_t qitems = (int64_t)c.b * c.hq * p.qtiles, kitems = (int64_t)c.b * c.hk * p.kblocks;
+    if (workspace_alloc(&ws, (size_t)qitems * 1024, c.stream) != LINFORMER_OK) return LINFORMER_ERR_ALLOC;
+    p.rows = static_cast<float *>(ws);
+    int st = LINFORMER_OK;
+    const int sms = device_sms();
+    {
+        KernelScope scope(LINFORMER_KERNEL_SOFTMAX_BWD, c.stream);
+        p.items = qitems;
+        softmax_attn_dq_kernel<DP><<<(int)std::min<int64_t>(qitems, sms), kThreads, Cq::kSmem, c.stream>>>(
+            tQ, tK, tV, tdO, p);
+        if (cudaGetLastError() != cudaSuccess) st = LINFORMER_ERR_LAUNCH;
+    }
+    if (!st) {
+        KernelScope scope(LINFORMER_KERNEL_SOFTMAX_BWD, c.stream);
+        p.items = kitems;
+        softmax_attn_dkv_kernel<DP><<<(int)std::min<int64_t>(kitems, sms), kThreads, Ck::kSmem, c.stream>>>(
+            tQ, tK, tV, tdO, p);
+        if (cudaGetLastError() != cudaSuccess) st = LINFORMER_ERR_LAUNCH;
+    }
+    workspace_free(ws, c.stream);
+    return st;
+}
+
+}  // namespace
+
+int backward(const Call &c) {
+    BwdParams p{};
+    p.q_lengths = c.q_lengths;
+    p.k_lengths = c.k_lengths;
+    p.O = static_cast<const __nv_bfloat16 *>(c.O);
+    p.dO = static_cast<const __nv_bfloat16 *>(c.dO);
+    p.sO = c.sO;
+    p.sdO = c.sdO;
+    p.dQ = static_cast<__nv_bfloat16 *>(c.dQ);
+    p.dK = static_cast<__nv_bfloat16 *>(c.dK);
+    p.dV = static_cast<__nv_bfloat16 *>(c.dV);
+    p.sdQ = c.sdQ;
+    p.sdK = c.sdK;
+    p.sdV = c.sdV;
+    p.lse = c.lse;
+    p.b = c.b;
+    p.hq = c.hq;
+    p.hk = c.hk;
+    p.group = c.hq / c.hk;
+    p.nq = c.nq;
+    p.nk = c.nk;
+    p.d = c.d;
+    p.causal = c.causal;
+    p.window = c.window;
+    p.qtiles = (c.nq + kTile - 1) / kTile;
+    p.kblocks = (c.nk + kTile - 1) / kTile;
+    p.scale = c.scale;
+    p.scale_log2 = c.scale * kLog2e;
+    p.status = device_status_ptr();
+    return c.d <= 64 ? launch<64>(c, p) : launch<128>(c, p);
+}
+
+}  // namespace sattn
+}  // namespace linformer

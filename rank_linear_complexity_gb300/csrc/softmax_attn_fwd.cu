@@ -1,0 +1,679 @@
+// Exact softmax attention, forward: for every query row i of every head
+//
+//     O_i = sum_j p_ij V_j,   p_ij = exp(scale Q_i.K_j - lse_i),
+//     lse_i = log sum_j exp(scale Q_i.K_j)
+//
+// over the keys that the row sees (valid length, causal, sliding window), in one pass
+// over the keys: a running maximum m and sum l per row, P = exp(s - m) in bf16 for the
+// second product, O and l rescaled when m has grown by more than 2^kLazy since it was
+// last taken (P then stays below 2^kLazy, which fp32 accumulation does not notice).
+// The n x n scores never leave the SM.
+//
+// Persistent CTAs take work items one after another: a pair of 128-row query tiles of
+// one key/value head, and (with few items) one part of the keys, whose partial result a
+// second kernel joins.  A tile's 128 rows are 128 positions of one query head, or, when
+// there are fewer positions, several heads of the group that shares the key/value head:
+// single-token decoding reads each key block once for the whole group.
+//   warps 0-3, 4-7  softmax of tile 0 and tile 1: one thread a row, S out of TMEM, P back
+//   warp 8          lane 0: TMA loads (Q per item; K and V blocks through a ring);
+//                   lanes 1-31: zero the rows of V past the valid length (P is 0 there,
+//                   but 0 x NaN is not)
+//   warp 9          one thread issues S = Q.K^T (both from shared memory) and O += P.V (P
+//                   from TMEM)
+// Tensor memory: head dimension up to 64: S0 S1 (128 columns each), P0 P1 (64), O0 O1
+// (64): S of the next block is computed while this block's exponentials are taken.  Up to
+// 128: S0 S1 with P over the first half of S, O0 O1 (128): the next S waits for P.V.
+#include <cudaTypedefs.h>
+
+#include <algorithm>
+#include <cmath>
+#include <mutex>
+
+#include "softmax_attn.cuh"
+#include "sm100_ptx.cuh"
+
+namespace linformer {
+namespace sattn {
+namespace {
+
+using namespace ptx;
+
+constexpr int kThreads = 320;
+constexpr int kLoadWarp = 8, kMmaWarp = 9;
+constexpr float kLazy = 8.f;  // log2 of the growth of the maximum that is left unscaled
+constexpr float kLog2e = 1.4426950408889634f, kLn2 = 0.6931471805599453f;
+
+struct FwdParams {
+    const int32_t *q_lengths, *k_lengths;
+    __nv_bfloat16 *out;
+    Strides so;
+    float *lse;
+    float *part_o, *part_lse;  // with splits: [split][b][hq][nq][DP] and [split][b][hq][nq]
+    int b, hq, hk, group, nq, nk, d, causal, window;
+    int qbox, hbox, nch, ntiles, npairs, nsplit, units;
+    int64_t items;
+    float scale, scale_log2;
+    int *status;
+};
+
+template <int DP>
+struct Layout {
+    static constexpr bool kSep = DP == 64;  // P beside S, not over it
+    static constexpr int kStages = DP == 64 ? 10 : 4;
+    static constexpr uint32_t kTileBytes = kTile * DP * 2;
+    static constexpr uint32_t kS = 0, kP = kSep ? 256 : 0, kPStep = kSep ? 64 : 128;
+    static constexpr uint32_t kO = kSep ? 384 : 256;
+    static constexpr uint32_t kSmem = 1024 + (2 + kStages) * kTileBytes + 512;
+};
+
+// One query tile of an item.
+struct Tile {
+    int q0, h0;      // first position, first query head in the group
+    int lo, hi;      // key blocks
+    bool live;       // exists (it has outputs to write)
+};
+struct Item {
+    int batch, kvh, split;
+    Span sp;
+    Tile t[2];
+    int lo, hi;  // union of the tiles' blocks
+};
+
+__device__ __forceinline__ Item load_item(const FwdParams &p, int64_t idx) {
+    Item it;
+    const int u = (int)(idx % p.units);
+    const int64_t r = idx / p.units;
+    it.split = (int)(r % p.nsplit);
+    const int rank = (int)(r / p.nsplit);
+    // causal rows further down see more keys: the longest items first
+    const int pair = p.causal ? p.npairs - 1 - rank : rank;
+    it.batch = u / p.hk;
+    it.kvh = u % p.hk;
+    it.sp = Span{clamp_length(p.q_lengths, it.batch, p.nq),
+                 clamp_length(p.k_lengths, it.batch, p.nk), p.causal, p.window};
+    it.lo = 1 << 30;
+    it.hi = 0;
+#pragma unroll
+    for (int t = 0; t < 2; ++t) {
+        const int lin = 2 * pair + t;
+        Tile &x = it.t[t];
+        x.live = lin < p.ntiles;
+        x.q0 = lin / p.nch * p.qbox;
+        x.h0 = lin % p.nch * p.hbox;
+        x.lo = x.hi = 0;
+        const int last = min(x.q0 + p.qbox, it.sp.Lq) - 1;
+        if (x.live && last >= x.q0) {
+            const int e = it.sp.end(last), f = it.sp.first(x.q0);
+            if (e > f) {
+                x.lo = f / kTile;
+                x.hi = (e + kTile - 1) / kTile;
+                it.lo = min(it.lo, x.lo);
+                it.hi = max(it.hi, x.hi);
+            }
+        }
+    }
+    if (it.hi > it.lo && p.nsplit > 1) {  // this item's share of the blocks
+        const int per = (it.hi - it.lo + p.nsplit - 1) / p.nsplit;
+        const int a = it.lo + it.split * per, z = min(it.hi, a + per);
+        it.lo = a;
+        it.hi = max(a, z);
+#pragma unroll
+        for (int t = 0; t < 2; ++t) {
+            it.t[t].lo = max(it.t[t].lo, a);
+            it.t[t].hi = min(it.t[t].hi, z);
+        }
+    }
+    return it;
+}
+
+// Whether the item's last block holds rows past the valid length that are in memory (rows
+// past the tensor's end come in as zero).
+__device__ __forceinline__ bool ragged_end(const Item &it, int nk) {
+    return it.hi > it.lo && it.sp.Lk < nk && it.hi * kTile > it.sp.Lk;
+}
+
+struct Barriers {
+    uint64_t q_full[2], q_free[2], s_full[2], s_free[2], p_full[2], pv_done[2], o_free[2];
+    uint64_t fix_wanted, fixed, drain;
+    uint64_t full[10], empty[10];
+    uint32_t tmem;
+    int abort;
+};
+
+template <int DP>
+__global__ void __launch_bounds__(kThreads, 1)
+softmax_attn_fwd_kernel(const __grid_constant__ CUtensorMap tQ, const __grid_constant__ CUtensorMap tK,
+                        const __grid_constant__ CUtensorMap tV, const FwdParams p) {
+    using C = Layout<DP>;
+    extern __shared__ uint8_t raw[];
+    uint8_t *smem = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(raw) + 1023) & ~uintptr_t(1023));
+    uint8_t *sQ = smem, *sKV = smem + 2 * C::kTileBytes;
+    Barriers *bar = reinterpret_cast<Barriers *>(sKV + C::kStages * C::kTileBytes);
+    volatile int *abort_flag = &bar->abort;
+    const int tid = threadIdx.x, warp = __shfl_sync(0xffffffffu, tid >> 5, 0), lane = tid & 31;
+
+    if (tid == 0) {
+        for (int t = 0; t < 2; ++t) {
+            mbar_init(&bar->q_full[t], 1);
+            mbar_init(&bar->q_free[t], 1);
+            mbar_init(&bar->s_full[t], 1);
+            mbar_init(&bar->s_free[t], 4);
+            mbar_init(&bar->p_full[t], 4);
+            mbar_init(&bar->pv_done[t], 1);
+            mbar_init(&bar->o_free[t], 4);
+        }
+        mbar_init(&bar->fix_wanted, 1);
+        mbar_init(&bar->fixed, 31);
+        mbar_init(&bar->drain, 1);
+        for (int s = 0; s < C::kStages; ++s) {
+            mbar_init(&bar->full[s], 1);
+            mbar_init(&bar->empty[s], 1);
+        }
+        bar->abort = 0;
+        fence_mbar_init();
+        prefetch_tmap(&tQ);
+        prefetch_tmap(&tK);
+        prefetch_tmap(&tV);
+    }
+    if (warp == kMmaWarp) {
+        tmem_alloc(&bar->tmem, 512);
+        tmem_relinquish();
+    }
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    const uint32_t tmem = bar->tmem;
+
+    if (warp == kLoadWarp) {
+        if (lane == 0) {  // ---------------- loads
+            int ring = 0, nq[2] = {0, 0};
+            bool ok = true;
+            for (int64_t idx = blockIdx.x; idx < p.items && ok; idx += gridDim.x) {
+                const Item it = load_item(p, idx);
+                for (int t = 0; t < 2 && ok; ++t) {
+                    if (it.t[t].hi <= it.t[t].lo) continue;
+                    if (nq[t] > 0 && !mbar_wait(&bar->q_free[t], (nq[t] - 1) & 1, p.status, 70, abort_flag)) {
+                        ok = false;
+                        break;
+                    }
+                    mbar_arrive_expect_tx(&bar->q_full[t], (uint32_t)(p.qbox * p.hbox * DP * 2));
+                    for (int h = 0; h < DP / 64; ++h)
+                        tma_load_5d(sQ + t * C::kTileBytes + h * 16384, &tQ, &bar->q_full[t], h * 64,
+                                    it.t[t].q0, it.t[t].h0, it.kvh, it.batch);
+                    ++nq[t];
+                }
+                for (int j = it.lo; j < it.hi && ok; ++j)
+                    for (int kv = 0; kv < 2; ++kv, ++ring) {
+                        const int s = ring % C::kStages;
+                        if (ring >= C::kStages &&
+                            !mbar_wait(&bar->empty[s], (ring / C::kStages - 1) & 1, p.status, 71, abort_flag)) {
+                            ok = false;
+                            break;
+                        }
+                        mbar_arrive_expect_tx(&bar->full[s], C::kTileBytes);
+                        for (int h = 0; h < DP / 64; ++h)
+                            tma_load_5d(sKV + s * C::kTileBytes + h * 16384, kv ? &tV : &tK, &bar->full[s],
+                                        h * 64, j * kTile, 0, it.kvh, it.batch);
+                    }
+            }
+            // no copy outlives the CTA
+            for (int t = 0; t < 2; ++t)
+                if (nq[t] > 0) mbar_wait_drain(&bar->q_full[t], (nq[t] - 1) & 1);
+            for (int i = max(0, ring - C::kStages); i < ring; ++i)
+                mbar_wait_drain(&bar->full[i % C::kStages], (i / C::kStages) & 1);
+        } else {  // ---------------- V rows past the valid length
+            int ring = 0, nfix = 0;
+            for (int64_t idx = blockIdx.x; idx < p.items; idx += gridDim.x) {
+                const Item it = load_item(p, idx);
+                const int blocks = max(0, it.hi - it.lo);
+                ring += 2 * blocks;
+                if (!ragged_end(it, p.nk)) continue;
+                // the issuing thread has seen the block land
+                if (!mbar_wait(&bar->fix_wanted, nfix & 1, p.status, 72, abort_flag)) break;
+                ++nfix;
+                zero_rows<DP>(sKV + (ring - 1) % C::kStages * C::kTileBytes,
+                              it.sp.Lk - (it.hi - 1) * kTile, lane - 1, 31);
+                fence_proxy_async_smem();
+                mbar_arrive(&bar->fixed);
+            }
+        }
+        __syncwarp();
+    } else if (warp == kMmaWarp) {
+        if (elect_one()) {  // ---------------- products
+            const uint32_t idesc_s = idesc_f16(128, 128, 1, 0, 0), idesc_o = idesc_f16(128, DP, 1, 0, 1);
+            int ring = 0, nfix = 0;
+            int n0 = 0, n1 = 0, i0 = 0, i1 = 0;  // per tile: blocks and items so far
+            bool ok = true;
+            // S of tile t from ring slot s
+            auto score = [&](int t, int s) {
+                const uint64_t a = sdesc(smem_u32(sQ + t * C::kTileBytes), 16, 1024, kSwizzle128B);
+                const uint64_t k = sdesc(smem_u32(sKV + s * C::kTileBytes), 16, 1024, kSwizzle128B);
+                const uint32_t d = tmem + C::kS + 128 * t;
+#pragma unroll
+                for (int x = 0; x < DP / 16; ++x) {
+                    const uint64_t off = (uint64_t)((x >> 2) * 1024 + (x & 3) * 2);
+                    mma_ss(d, a + off, k + off, idesc_s, x > 0 ? 1u : 0u);
+                }
+                mma_commit(&bar->s_full[t]);
+            };
+            auto values = [&](int t, int s, uint32_t acc) {
+                const uint64_t v = sdesc(smem_u32(sKV + s * C::kTileBytes), 16384, 1024, kSwizzle128B);
+                const uint32_t d = tmem + C::kO + DP * t, a = tmem + C::kP + C::kPStep * t;
+#pragma unroll
+                for (int x = 0; x < 8; ++x)
+                    mma_ts(d, a + 8 * x, v + (uint64_t)(128 * x), idesc_o, (acc || x > 0) ? 1u : 0u);
+                mma_commit(&bar->pv_done[t]);
+            };
+            for (int64_t idx = blockIdx.x; idx < p.items && ok; idx += gridDim.x) {
+                const Item it = load_item(p, idx);
+                const bool fix = ragged_end(it, p.nk);
+                // scores of block j for both tiles; false if a wait ran out
+                auto scores = [&](int j) {
+                    const int r = ring + 2 * (j - it.lo), s = r % C::kStages;
+                    if (!mbar_wait(&bar->full[s], (r / C::kStages) & 1, p.status, 73, abort_flag)) return false;
+#pragma unroll
+                    for (int t = 0; t < 2; ++t) {
+                        const Tile &x = it.t[t];
+                        if (j < x.lo || j >= x.hi) continue;
+                        const int nt = (t ? n1 : n0) + (j - x.lo);  // blocks of this tile before
+                        const int ni = t ? i1 : i0;
+                        if (j == x.lo && !mbar_wait(&bar->q_full[t], ni & 1, p.status, 74, abort_flag)) return false;
+                        if (nt > 0 && !mbar_wait(C::kSep ? &bar->s_free[t] : &bar->pv_done[t], (nt - 1) & 1,
+                                                 p.status, 75, abort_flag))
+                            return false;
+                        tc_fence_after();
+                        score(t, s);
+                        if (j == x.hi - 1) mma_commit(&bar->q_free[t]);
+                    }
+                    mma_commit(&bar->empty[s]);
+                    return true;
+                };
+                auto outputs = [&](int j) {
+                    const int r = ring + 2 * (j - it.lo) + 1, s = r % C::kStages;
+                    if (!mbar_wait(&bar->full[s], (r / C::kStages) & 1, p.status, 76, abort_flag)) return false;
+                    if (fix && j == it.hi - 1) {
+                        mbar_arrive(&bar->fix_wanted);
+                        if (!mbar_wait(&bar->fixed, nfix & 1, p.status, 77, abort_flag)) return false;
+                        ++nfix;
+                    }
+#pragma unroll
+                    for (int t = 0; t < 2; ++t) {
+                        const Tile &x = it.t[t];
+                        if (j < x.lo || j >= x.hi) continue;
+                        const int nt = (t ? n1 : n0) + (j - x.lo), ni = t ? i1 : i0;
+                        if (!mbar_wait(&bar->p_full[t], nt & 1, p.status, 78, abort_flag)) return false;
+                        if (j == x.lo && ni > 0 &&
+                            !mbar_wait(&bar->o_free[t], (ni - 1) & 1, p.status, 79, abort_flag))
+                            return false;
+                        tc_fence_after();
+                        values(t, s, j > x.lo ? 1u : 0u);
+                    }
+                    mma_commit(&bar->empty[s]);
+                    return true;
+                };
+                if (it.hi > it.lo) {
+                    ok = scores(it.lo);
+                    for (int j = it.lo; j < it.hi && ok; ++j) {
+                        if (C::kSep) {
+                            if (j + 1 < it.hi) ok = scores(j + 1);
+                            if (ok) ok = outputs(j);
+                        } else {
+                            ok = outputs(j);
+                            if (ok && j + 1 < it.hi) ok = scores(j + 1);
+                        }
+                    }
+                    ring += 2 * (it.hi - it.lo);
+                }
+                const int b0 = it.t[0].hi - it.t[0].lo, b1 = it.t[1].hi - it.t[1].lo;
+                if (b0 > 0) {
+                    n0 += b0;
+                    ++i0;
+                }
+                if (b1 > 0) {
+                    n1 += b1;
+                    ++i1;
+                }
+            }
+            mma_commit(&bar->drain);
+            mbar_wait_drain(&bar->drain, 0);
+        }
+        __syncwarp();
+    } else {  // ---------------- softmax of one tile, one thread a row
+        const int t = warp >> 2, row = tid & 127;
+        const uint32_t lanes = (uint32_t)((warp & 3) * 32) << 16;
+        const uint32_t tS = tmem + C::kS + 128 * t + lanes, tP = tmem + C::kP + C::kPStep * t + lanes,
+                       tO = tmem + C::kO + DP * t + lanes;
+        const float sl = p.scale_log2;
+        const int qi = row % p.qbox, hi_ = row / p.qbox;  // position and head within the tile
+        int n = 0;
+        bool ok = true;
+        for (int64_t idx = blockIdx.x; idx < p.items && ok; idx += gridDim.x) {
+            const Item it = load_item(p, idx);
+            const Tile x = t ? it.t[1] : it.t[0];
+            if (!x.live) continue;
+            const int i = x.q0 + qi, hg = x.h0 + hi_;
+            const bool exists = hi_ < p.hbox && hg < p.group && i < p.nq;
+            const bool valid = exists && i < it.sp.Lq;
+            const bool warp_valid = __any_sync(0xffffffffu, valid);
+            const int first = valid ? it.sp.first(i) : 0;
+            const int end = valid ? it.sp.end(i) : (1 << 30);
+            float m = -INFINITY, l = 0.f;  // maximum (of the raw scores), sum of 2^((s - m) sl)
+            for (int j = x.lo; j < x.hi; ++j, ++n) {
+                if (!warp_wait(&bar->s_full[t], n & 1, p.status, 80, abort_flag)) {
+                    ok = false;
+                    break;
+                }
+                tc_fence_after();
+                if (warp_valid) {
+                    uint32_t v[4][32];
+#pragma unroll
+                    for (int c = 0; c < 4; ++c) tmem_ld32_async(tS + 32 * c, v[c]);
+                    tmem_wait_ld(v[0]);
+                    tie32(v[1]);
+                    tie32(v[2]);
+                    tie32(v[3]);
+                    if (C::kSep) {
+                        tc_fence_before();
+                        __syncwarp();
+                        if (lane == 0) mbar_arrive(&bar->s_free[t]);
+                    }
+                    const int k0 = j * kTile;
+                    if (__any_sync(0xffffffffu, first > k0 || end < k0 + kTile)) {
+                        const int a = first - k0;
+                        const unsigned w = end > first ? (unsigned)(end - first) : 0u;
+#pragma unroll
+                        for (int c = 0; c < 4; ++c)
+#pragma unroll
+                            for (int e = 0; e < 32; ++e)
+                                if ((unsigned)(32 * c + e - a) >= w) v[c][e] = 0xff800000u;  // -inf
+                    }
+                    float m0 = -INFINITY, m1 = m0, m2 = m0, m3 = m0;
+#pragma unroll
+                    for (int c = 0; c < 4; ++c)
+#pragma unroll
+                        for (int e = 0; e < 32; e += 8) {
+                            m0 = max3(m0, __uint_as_float(v[c][e]), __uint_as_float(v[c][e + 1]));
+                            m1 = max3(m1, __uint_as_float(v[c][e + 2]), __uint_as_float(v[c][e + 3]));
+                            m2 = max3(m2, __uint_as_float(v[c][e + 4]), __uint_as_float(v[c][e + 5]));
+                            m3 = max3(m3, __uint_as_float(v[c][e + 6]), __uint_as_float(v[c][e + 7]));
+                        }
+                    const float mx = fmaxf(fmaxf(m0, m1), fmaxf(m2, m3));
+                    // the last product of this tile: before O is rescaled, and before P is
+                    // written where it was read from
+                    const bool grow = __any_sync(0xffffffffu, (mx - m) * sl > kLazy);
+                    if (j > x.lo && (grow || C::kSep)) {
+                        if (!warp_wait(&bar->pv_done[t], (n - 1) & 1, p.status, 81, abort_flag)) {
+                            ok = false;
+                            break;
+                        }
+                        tc_fence_after();
+                    }
+                    if (grow) {
+                        const float mn = fmaxf(m, mx);
+                        const float f = mn == -INFINITY ? 1.f : ex2_approx((m - mn) * sl);
+                        l *= f;
+                        m = mn;
+                        if (j > x.lo) {
+#pragma unroll
+                            for (int c = 0; c < DP; c += 32) {
+                                uint32_t o[32];
+                                tmem_ld32(tO + c, o);
+#pragma unroll
+                                for (int e = 0; e < 32; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * f);
+                                tmem_st32(tO + c, o);
+                            }
+                        }
+                    }
+                    const float off = m == -INFINITY ? 0.f : -m * sl;
+                    const float2 sl2 = make_float2(sl, sl), off2 = make_float2(off, off);
+                    float2 sum0 = make_float2(0.f, 0.f), sum1 = sum0;
+#pragma unroll
+                    for (int c = 0; c < 4; ++c) {
+                        uint32_t o[16];
+#pragma unroll
+                        for (int e = 0; e < 32; e += 2) {
+                            float2 y = ffma2(make_float2(__uint_as_float(v[c][e]), __uint_as_float(v[c][e + 1])),
+                                             sl2, off2);
+                            y.x = ex2_approx(y.x);
+                            y.y = ex2_approx(y.y);
+                            if (e & 2) sum1 = fadd2(sum1, y);
+                            else sum0 = fadd2(sum0, y);
+                            o[e / 2] = pack2(y.x, y.y);
+                        }
+                        tmem_st16_async(tP + 16 * c, o);
+                    }
+                    tmem_wait_st();
+                    l += (sum0.x + sum0.y) + (sum1.x + sum1.y);
+                } else if (C::kSep) {
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive(&bar->s_free[t]);
+                    // no second arrival on p_full before the other warps' first
+                    if (j > x.lo && !warp_wait(&bar->pv_done[t], (n - 1) & 1, p.status, 81, abort_flag)) {
+                        ok = false;
+                        break;
+                    }
+                }
+                tc_fence_before();
+                __syncwarp();
+                if (lane == 0) mbar_arrive(&bar->p_full[t]);
+            }
+            if (!ok) break;
+            // O / l out of TMEM; rows without keys give O = 0 and lse = -inf
+            const bool some = x.hi > x.lo;
+            if (some) {
+                if (!warp_wait(&bar->pv_done[t], (n - 1) & 1, p.status, 82, abort_flag)) break;
+                tc_fence_after();
+            }
+            const bool dead = !valid || l == 0.f;
+            const float inv = dead ? 0.f : 1.f / l;
+            const float lse = dead ? -INFINITY : m * p.scale + logf(l);
+            const int64_t head = (int64_t)it.kvh * p.group + hg;
+            const int64_t r = ((int64_t)it.batch * p.hq + head) * p.nq + i;
+            if (p.nsplit > 1) {
+                const int64_t pr = (int64_t)it.split * p.b * p.hq * p.nq + r;
+                if (some && warp_valid) {
+                    float *dst = p.part_o + pr * DP;
+#pragma unroll
+                    for (int c = 0; c < DP; c += 32) {
+                        uint32_t o[32];
+                        tmem_ld32(tO + c, o);
+                        if (!dead)
+#pragma unroll
+                            for (int e = 0; e < 32; e += 4)
+                                *reinterpret_cast<float4 *>(dst + c + e) =
+                                    make_float4(__uint_as_float(o[e]) * inv, __uint_as_float(o[e + 1]) * inv,
+                                                __uint_as_float(o[e + 2]) * inv, __uint_as_float(o[e + 3]) * inv);
+                    }
+                }
+                if (exists) p.part_lse[pr] = lse;
+            } else {
+                __nv_bfloat16 *dst = p.out + it.batch * p.so.b + head * p.so.h + (int64_t)i * p.so.n;
+#pragma unroll
+                for (int c = 0; c < DP; c += 32) {
+                    uint32_t o[32];
+                    if (some && warp_valid) tmem_ld32(tO + c, o);
+                    if (exists)
+#pragma unroll
+                        for (int e = 0; e < 32; e += 8) {
+                            if (c + e >= p.d) break;
+                            uint4 w = make_uint4(0u, 0u, 0u, 0u);
+                            if (!dead) {
+                                w.x = pack2(__uint_as_float(o[e]) * inv, __uint_as_float(o[e + 1]) * inv);
+                                w.y = pack2(__uint_as_float(o[e + 2]) * inv, __uint_as_float(o[e + 3]) * inv);
+                                w.z = pack2(__uint_as_float(o[e + 4]) * inv, __uint_as_float(o[e + 5]) * inv);
+                                w.w = pack2(__uint_as_float(o[e + 6]) * inv, __uint_as_float(o[e + 7]) * inv);
+                            }
+                            *reinterpret_cast<uint4 *>(dst + c + e) = w;
+                        }
+                }
+                if (exists) p.lse[r] = lse;
+            }
+            if (some) {
+                tc_fence_before();
+                __syncwarp();
+                if (lane == 0) mbar_arrive(&bar->o_free[t]);
+            }
+        }
+    }
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    if (warp == kMmaWarp) tmem_dealloc(tmem, 512);
+}
+
+// Joins the parts of a row: lse = log sum_s exp(lse_s), O = sum_s exp(lse_s - lse) O_s.
+// One warp a row.
+template <int DP>
+__global__ void __launch_bounds__(128) join_kernel(const FwdParams p) {
+    const int64_t rows = (int64_t)p.b * p.hq * p.nq;
+    const int64_t r = (int64_t)blockIdx.x * 4 + (threadIdx.x >> 5);
+    const int lane = threadIdx.x & 31;
+    if (r >= rows) return;
+    float m = -INFINITY;
+    for (int s = lane; s < p.nsplit; s += 32) m = fmaxf(m, p.part_lse[s * rows + r]);
+    for (int o = 16; o; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
+    const int i = (int)(r % p.nq), h = (int)(r / p.nq % p.hq), b = (int)(r / ((int64_t)p.nq * p.hq));
+    __nv_bfloat16 *dst = p.out + b * p.so.b + h * p.so.h + (int64_t)i * p.so.n;
+    constexpr int E = DP / 32;
+    float acc[E] = {}, sum = 0.f;
+    if (m != -INFINITY) {
+        for (int s = 0; s < p.nsplit; ++s) {
+            const float w = __expf(p.part_lse[s * rows + r] - m);
+            if (w == 0.f) continue;  // a part without keys wrote no O
+            sum += w;
+            const float *src = p.part_o + (s * rows + r) * DP + lane * E;
+#pragma unroll
+            for (int e = 0; e < E; ++e) acc[e] += w * src[e];
+        }
+    }
+    const float inv = sum > 0.f ? 1.f / sum : 0.f;
+    if (lane * E < p.d) {
+#pragma unroll
+        for (int e = 0; e < E; e += 2)
+            *reinterpret_cast<uint32_t *>(dst + lane * E + e) = pack2(acc[e] * inv, acc[e + 1] * inv);
+    }
+    if (lane == 0) p.lse[r] = m == -INFINITY ? -INFINITY : m + logf(sum);
+}
+
+PFN_cuTensorMapEncodeTiled_v12000 g_encode = nullptr;
+std::once_flag g_encode_once;
+
+constexpr int kMaxDev = 64;
+int g_sms[kMaxDev] = {};
+
+template <int DP>
+int launch(const Call &c, FwdParams &p) {
+    using C = Layout<DP>;
+    CUtensorMap tQ, tK, tV;
+    if (!encode_rows(&tQ, c.Q, c.sQ, c.b, c.hq, p.group, c.nq, c.d, p.qbox, p.hbox) ||
+        !encode_rows(&tK, c.K, c.sK, c.b, c.hk, 1, c.nk, c.d, kTile, 1) ||
+        !encode_rows(&tV, c.V, c.sV, c.b, c.hk, 1, c.nk, c.d, kTile, 1))
+        return LINFORMER_ERR_LAUNCH;
+    char *ws = nullptr;
+    if (p.nsplit > 1) {
+        const size_t rows = (size_t)c.b * c.hq * c.nq * p.nsplit;
+        if (workspace_alloc(reinterpret_cast<void **>(&ws), rows * (DP + 1) * sizeof(float), c.stream) !=
+            LINFORMER_OK)
+            return LINFORMER_ERR_ALLOC;
+        p.part_o = reinterpret_cast<float *>(ws);
+        p.part_lse = p.part_o + rows * DP;
+    }
+    int st = LINFORMER_OK;
+    if (cudaFuncSetAttribute(softmax_attn_fwd_kernel<DP>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                             C::kSmem) != cudaSuccess)
+        st = LINFORMER_ERR_LAUNCH;
+    if (!st) {
+        KernelScope scope(LINFORMER_KERNEL_SOFTMAX, c.stream);
+        const int grid = (int)std::min<int64_t>(p.items, device_sms());
+        softmax_attn_fwd_kernel<DP><<<grid, kThreads, C::kSmem, c.stream>>>(tQ, tK, tV, p);
+        if (cudaGetLastError() != cudaSuccess) st = LINFORMER_ERR_LAUNCH;
+    }
+    if (!st && p.nsplit > 1) {
+        KernelScope scope(LINFORMER_KERNEL_SOFTMAX, c.stream);
+        const int64_t rows = (int64_t)c.b * c.hq * c.nq;
+        join_kernel<DP><<<(unsigned)((rows + 3) / 4), 128, 0, c.stream>>>(p);
+        if (cudaGetLastError() != cudaSuccess) st = LINFORMER_ERR_LAUNCH;
+    }
+    if (ws) workspace_free(ws, c.stream);
+    return st;
+}
+
+}  // namespace
+
+bool encode_rows(CUtensorMap *m, const void *base, const Strides &s, int b, int heads, int group,
+                 int n, int d, int rows, int hrows) {
+    std::call_once(g_encode_once, [] {
+        void *fn = nullptr;
+        cudaDriverEntryPointQueryResult q{};
+        if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &fn, 12000, cudaEnableDefault,
+                                             &q) == cudaSuccess &&
+            q == cudaDriverEntryPointSuccess)
+            g_encode = reinterpret_cast<PFN_cuTensorMapEncodeTiled_v12000>(fn);
+    });
+    if (!g_encode) return false;
+    // the stride of a dimension of size one is never used, but has to be a legal one
+    auto bytes = [](int64_t stride, int64_t count) { return (cuuint64_t)(count > 1 ? stride * 2 : 16); };
+    cuuint64_t dims[5] = {(cuuint64_t)d, (cuuint64_t)n, (cuuint64_t)group, (cuuint64_t)(heads / group),
+                          (cuuint64_t)b};
+    cuuint64_t strides[4] = {bytes(s.n, n), bytes(s.h, group), bytes(s.h * group, heads / group),
+                             bytes(s.b, b)};
+    cuuint32_t box[5] = {64, (cuuint32_t)rows, (cuuint32_t)hrows, 1, 1};
+    cuuint32_t one[5] = {1, 1, 1, 1, 1};
+    return g_encode(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 5, const_cast<void *>(base), dims, strides, box,
+                    one, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+                    CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+int device_sms() {
+    int dev = 0;
+    cudaGetDevice(&dev);
+    if (dev < 0 || dev >= kMaxDev) return 148;
+    if (!g_sms[dev]) {
+        int v = 0;
+        cudaDeviceGetAttribute(&v, cudaDevAttrMultiProcessorCount, dev);
+        g_sms[dev] = v > 0 ? v : 148;
+    }
+    return g_sms[dev];
+}
+
+int forward(const Call &c) {
+    FwdParams p{};
+    p.q_lengths = c.q_lengths;
+    p.k_lengths = c.k_lengths;
+    p.out = static_cast<__nv_bfloat16 *>(c.out);
+    p.so = c.sO;
+    p.lse = c.lse;
+    p.b = c.b;
+    p.hq = c.hq;
+    p.hk = c.hk;
+    p.group = c.hq / c.hk;
+    p.nq = c.nq;
+    p.nk = c.nk;
+    p.d = c.d;
+    p.causal = c.causal;
+    p.window = c.window;
+    p.scale = c.scale;
+    p.scale_log2 = c.scale * kLog2e;
+    p.status = device_status_ptr();
+    // Rows of a tile: 128 positions of one head, or the smallest power of two that holds
+    // all positions times as many heads of the group as fit.
+    p.qbox = kTile;
+    while (p.qbox > 1 && p.qbox / 2 >= c.nq) p.qbox /= 2;
+    p.hbox = std::min(kTile / p.qbox, p.group);
+    p.nch = (p.group + p.hbox - 1) / p.hbox;
+    p.ntiles = (c.nq + p.qbox - 1) / p.qbox * p.nch;
+    p.npairs = (p.ntiles + 1) / 2;
+    p.units = c.b * c.hk;
+    const int64_t whole = (int64_t)p.units * p.npairs;
+    const int sms = device_sms();
+    // With fewer items than SMs the keys are split, at least kMinBlocks blocks a part.
+    constexpr int kMinBlocks = 4;
+    const int reach = c.window ? std::min(c.nk, c.window + kTile) : c.nk;
+    const int blocks = (reach + kTile - 1) / kTile;
+    p.nsplit = (int)std::max<int64_t>(1, std::min<int64_t>(sms / whole, blocks / kMinBlocks));
+    p.items = whole * p.nsplit;
+    return c.d <= 64 ? launch<64>(c, p) : launch<128>(c, p);
+}
+
+}  // namespace sattn
+}  // namespace linformer

@@ -17,13 +17,17 @@ from . import build as _build
 PER_HEAD, KV, HEADWISE, LAYERWISE = 0, 1, 2, 3
 F32, BF16, BF16_F32OUT = 0, 1, 2
 PATH_SIMT, PATH_TENSOR = 0, 1
-KERNEL_COUNT = 7
+KERNEL_COUNT = 10
+ROTARY_HALVES, ROTARY_INTERLEAVED = 0, 1
+ROTARY_PLAIN, ROTARY_LINEAR, ROTARY_BASE, ROTARY_BY_PARTS = 0, 1, 2, 3
 
 _lock = threading.Lock()
 _lib = None
 
 _vp = ctypes.c_void_p
 _i = ctypes.c_int
+_f = ctypes.c_float
+_d = ctypes.c_double
 
 SYMBOLS = [
     "linformer_attn_fwd", "linformer_project_fwd", "linformer_attn_fwd_host",
@@ -31,7 +35,8 @@ SYMBOLS = [
     "linformer_set_pv_terms", "linformer_launch_count", "linformer_profile_enable",
     "linformer_profile_collect", "linformer_kernel_name", "linformer_attn_fwd_noalloc",
     "linformer_window_projection", "linformer_attn_bwd", "linformer_dense_attn_fwd",
-    "linformer_pool_peak_bytes", "linformer_debug_wait_probe",
+    "linformer_pool_peak_bytes", "linformer_debug_wait_probe", "linformer_softmax_attn_fwd",
+    "linformer_softmax_attn_bwd", "linformer_rotary", "linformer_rotary_phase",
 ]
 
 
@@ -90,6 +95,17 @@ def lib() -> ctypes.CDLL:
             L.linformer_attn_bwd.restype = _i
             L.linformer_window_projection.argtypes = [_vp, _vp, _i, _i, _i, _vp]
             L.linformer_window_projection.restype = _i
+            L.linformer_softmax_attn_fwd.argtypes = ([_vp] * 11 + [_i] * 6 + [_f] + [_i] * 3
+                                                     + [_vp])
+            L.linformer_softmax_attn_fwd.restype = _i
+            L.linformer_softmax_attn_bwd.argtypes = ([_vp] * 19 + [_i] * 6 + [_f] + [_i] * 3
+                                                     + [_vp])
+            L.linformer_softmax_attn_bwd.restype = _i
+            L.linformer_rotary.argtypes = ([_vp] * 4 + [_i] + [_vp] * 4 + [_i] + [_vp] * 2
+                                           + [_i] * 6 + [_f] + [_i] * 2 + [_vp])
+            L.linformer_rotary.restype = _i
+            L.linformer_rotary_phase.argtypes = [_vp, _i, _d, _i, _d, _i, _d, _d, _vp]
+            L.linformer_rotary_phase.restype = _i
             L.linformer_kernel_name.argtypes = [_i]
             L.linformer_kernel_name.restype = ctypes.c_char_p
             _lib = L
@@ -295,3 +311,160 @@ def dense_attention(Q, K, V, lengths=None, out=None, stream=None):
     if st != 0:
         raise LinformerError(st, "linformer_dense_attn_fwd")
     return out
+
+
+# --- exact softmax attention and rotary positions (strided [b][h][n][d] tensors) ------------
+
+def _strides(x):
+    """The int64[3] of batch, head and row strides of a tensor [b][h][n][d]."""
+    b, h, n, one = x.stride()
+    if one != 1 and x.shape[3] != 1:
+        raise ValueError("the last dimension has to be contiguous")
+    return (ctypes.c_int64 * 3)(b, h, n)
+
+
+def _same_device(*tensors):
+    """The device of the tensors (None entries are passed over); they have to share it."""
+    dev = None
+    for t in tensors:
+        if t is None:
+            continue
+        if dev is None:
+            dev = t.device
+        elif t.device != dev:
+            raise ValueError(f"tensors on {dev} and {t.device}")
+    if dev.type != "cuda":
+        raise ValueError(f"CUDA tensors are needed, got {dev}")
+    return dev
+
+
+def _on(device, call):
+    """call() with `device` current: the library works on the current device."""
+    import torch
+    if torch.cuda.current_device() == device.index:
+        return call()
+    with torch.cuda.device(device):
+        return call()
+
+
+def _check_words(name, x, dtype, shape):
+    if x is not None and (x.dtype != dtype or tuple(x.shape) != shape or not x.is_contiguous()):
+        raise ValueError(f"{name}: a contiguous {dtype} tensor of shape {shape} is needed")
+
+
+def _check_shape(name, x, shape, dtype):
+    if tuple(x.shape) != shape or x.dtype != dtype:
+        raise ValueError(f"{name}: {dtype} of shape {shape} is needed, got {x.dtype} of "
+                         f"{tuple(x.shape)}")
+
+
+def softmax_attention(Q, K, V, q_lengths=None, k_lengths=None, causal: bool = False,
+                      window: int = 0, scale=None, out=None, lse=None, stream=None):
+    """(O, lse) of the exact attention of Q [b][hq][n][d] over K, V [b][hk][m][d] (bf16, any
+    strides): O shaped like Q, lse fp32 [b][hq][n] as softmax_attention_backward takes it.
+
+    causal: the valid parts end together (the last query sees every key), with window > 0
+    only the last `window` keys up to its own.  scale defaults to 1 / sqrt(d)."""
+    import torch
+    b, hq, n, d = Q.shape
+    hk, m = K.shape[1], K.shape[2]
+    _check_shape("K", K, (b, hk, m, d), Q.dtype)
+    _check_shape("V", V, (b, hk, m, d), Q.dtype)
+    device = _same_device(Q, K, V, q_lengths, k_lengths, out, lse)
+    if out is None:
+        out = torch.empty((b, hq, n, d), dtype=Q.dtype, device=device)
+    else:
+        _check_shape("out", out, (b, hq, n, d), Q.dtype)
+    if lse is None:
+        lse = torch.empty((b, hq, n), dtype=torch.float32, device=device)
+    _check_words("lse", lse, torch.float32, (b, hq, n))
+    _check_words("q_lengths", q_lengths, torch.int32, (b,))
+    _check_words("k_lengths", k_lengths, torch.int32, (b,))
+    code = dtype_code(Q)
+    st = _on(device, lambda: lib().linformer_softmax_attn_fwd(
+        Q.data_ptr(), _strides(Q), K.data_ptr(), _strides(K), V.data_ptr(), _strides(V),
+        out.data_ptr(), _strides(out), lse.data_ptr(), _ptr(q_lengths), _ptr(k_lengths), b, hq,
+        hk, n, m, d, d ** -0.5 if scale is None else scale, int(causal), window, code,
+        _stream_handle(stream)))
+    if st != 0:
+        raise LinformerError(st, "linformer_softmax_attn_fwd")
+    return out, lse
+
+
+def softmax_attention_backward(Q, K, V, O, dO, lse, q_lengths=None, k_lengths=None,
+                               causal: bool = False, window: int = 0, scale=None, dQ=None,
+                               dK=None, dV=None, stream=None):
+    """(dQ, dK, dV) from the inputs and results of softmax_attention and dO = dLoss/dO."""
+    import torch
+    b, hq, n, d = Q.shape
+    hk, m = K.shape[1], K.shape[2]
+    device = _same_device(Q, K, V, O, dO, lse, q_lengths, k_lengths, dQ, dK, dV)
+    if dQ is None:
+        dQ = torch.empty((b, hq, n, d), dtype=Q.dtype, device=device)
+    if dK is None:
+        dK = torch.empty((b, hk, m, d), dtype=Q.dtype, device=device)
+    if dV is None:
+        dV = torch.empty((b, hk, m, d), dtype=Q.dtype, device=device)
+    for name, x in (("O", O), ("dO", dO), ("dQ", dQ)):
+        _check_shape(name, x, (b, hq, n, d), Q.dtype)
+    for name, x in (("K", K), ("V", V), ("dK", dK), ("dV", dV)):
+        _check_shape(name, x, (b, hk, m, d), Q.dtype)
+    _check_words("lse", lse, torch.float32, (b, hq, n))
+    _check_words("q_lengths", q_lengths, torch.int32, (b,))
+    _check_words("k_lengths", k_lengths, torch.int32, (b,))
+    code = dtype_code(Q)
+    st = _on(device, lambda: lib().linformer_softmax_attn_bwd(
+        Q.data_ptr(), _strides(Q), K.data_ptr(), _strides(K), V.data_ptr(), _strides(V),
+        O.data_ptr(), _strides(O), dO.data_ptr(), _strides(dO), lse.data_ptr(), dQ.data_ptr(),
+        _strides(dQ), dK.data_ptr(), _strides(dK), dV.data_ptr(), _strides(dV), _ptr(q_lengths),
+        _ptr(k_lengths), b, hq, hk, n, m, d, d ** -0.5 if scale is None else scale, int(causal),
+        window, code, _stream_handle(stream)))
+    if st != 0:
+        raise LinformerError(st, "linformer_softmax_attn_bwd")
+    return dQ, dK, dV
+
+
+def rotary_phase(rot: int, base: float = 10000.0, scaling: int = ROTARY_PLAIN,
+                 factor: float = 1.0, original_length: int = 0, beta_fast: float = 32.0,
+                 beta_slow: float = 1.0, device="cuda", stream=None):
+    """The table of `rot / 2` frequencies that rotary() takes (int64, made once and kept)."""
+    import torch
+    phase = torch.empty(rot // 2, dtype=torch.int64, device=device)
+    st = _on(phase.device, lambda: lib().linformer_rotary_phase(
+        phase.data_ptr(), rot, base, scaling, factor, original_length, beta_fast, beta_slow,
+        _stream_handle(stream)))
+    if st != 0:
+        raise LinformerError(st, "linformer_rotary_phase")
+    return phase
+
+
+def rotary(x, x2=None, phase=None, positions=None, start: int = 0, rot=None,
+           layout: int = ROTARY_HALVES, amplitude: float = 1.0, inverse: bool = False, out=None,
+           out2=None, stream=None):
+    """x [b][h][n][d] (and x2 [b][h2][n][d], or None) turned to their positions; (y, y2) or y.
+
+    positions int32 [b][n], or None for start + row; rot defaults to d.  inverse=True maps
+    gradients of the results to gradients of the inputs.  out may be x (in place)."""
+    import torch
+    b, h, n, d = x.shape
+    rot = d if rot is None else rot
+    device = _same_device(x, x2, phase, positions, out, out2)
+    out = torch.empty_like(x) if out is None else out
+    _check_shape("out", out, (b, h, n, d), x.dtype)
+    _check_words("phase", phase, torch.int64, (rot // 2,))
+    _check_words("positions", positions, torch.int32, (b, n))
+    h2, second = 0, (None, None, None, None)
+    if x2 is not None:
+        h2 = x2.shape[1]
+        _check_shape("x2", x2, (b, h2, n, d), x.dtype)
+        out2 = torch.empty_like(x2) if out2 is None else out2
+        _check_shape("out2", out2, (b, h2, n, d), x.dtype)
+        second = (x2.data_ptr(), _strides(x2), out2.data_ptr(), _strides(out2))
+    code = dtype_code(x)
+    st = _on(device, lambda: lib().linformer_rotary(
+        x.data_ptr(), _strides(x), out.data_ptr(), _strides(out), h, *second, h2, _ptr(phase),
+        _ptr(positions), start, b, n, d, rot, layout, amplitude, int(inverse), code,
+        _stream_handle(stream)))
+    if st != 0:
+        raise LinformerError(st, "linformer_rotary")
+    return out if x2 is None else (out, out2)
