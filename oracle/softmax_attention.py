@@ -88,12 +88,14 @@ def forward(Q, K, V, q_lengths=None, k_lengths=None, causal=False, window=0, sca
 
 
 def backward(Q, K, V, dO, q_lengths=None, k_lengths=None, causal=False, window=0, scale=None):
-    """((dQ, dK, dV), their bounds); delta = dO.O is taken with O rounded to bf16."""
+    """((dQ, dK, dV), their bounds, the part of the bounds that comes from delta = dO.O with O
+    rounded to bf16: one error for a whole row, which sums over keys do not average out)."""
     Q, K, V, dO = host64(Q), host64(K), host64(V), host64(dO)
     d = Q.shape[3]
     scale = d ** -0.5 if scale is None else scale
     out = [np.zeros(Q.shape), np.zeros(K.shape), np.zeros(K.shape)]
     bound = [np.zeros(Q.shape), np.zeros(K.shape), np.zeros(K.shape)]
+    rows = [np.zeros(Q.shape), np.zeros(K.shape), np.zeros(K.shape)]
     for bi, h, kv, lq, lk, m in _units(Q, K, q_lengths, k_lengths, causal, window):
         q, g = _valid_rows(Q[bi, h], lq), _valid_rows(dO[bi, h], lq)
         k, v = _valid_rows(K[bi, kv], lk), _valid_rows(V[bi, kv], lk)
@@ -112,7 +114,9 @@ def backward(Q, K, V, dO, q_lengths=None, k_lengths=None, causal=False, window=0
         e_ds = (U + eps + sums) * np.abs(ds) + p * (e_delta + e_dp) * (1 + U) + eps * p * np.abs(delta)
         bound[0][bi, h] += scale * (e_ds @ np.abs(k))
         bound[1][bi, kv] += scale * (e_ds.T @ np.abs(q))
+        rows[0][bi, h] += scale * ((p * e_delta) @ np.abs(k))
+        rows[1][bi, kv] += scale * ((p * e_delta).T @ np.abs(q))
         bound[2][bi, kv] += (U + eps + sums) * (p.T @ np.abs(g))
     for x, y in zip(bound, out):
         x += U * np.abs(y) * (1 + U)
-    return tuple(out), tuple(bound)
+    return tuple(out), tuple(bound), tuple(rows)

@@ -32,7 +32,11 @@ namespace {
 
 using namespace ptx;
 
-constexpr int kThreads = 320;
+// Twelve warps (two idle), 168 registers each at launch; the two warpgroups that do the
+// arithmetic take registers from the third: 2 x 200 + 104 = 3 x 168.
+constexpr int kThreads = 384;
+constexpr uint32_t kMathRegs = 200, kIssueRegs = 104;
+static_assert(2 * kMathRegs + kIssueRegs == 3 * 168, "register split");
 constexpr int kLoadWarp = 8, kMmaWarp = 9;
 constexpr float kLog2e = 1.4426950408889634f;
 
@@ -182,6 +186,8 @@ softmax_attn_dq_kernel(const __grid_constant__ CUtensorMap tQ, const __grid_cons
     tc_fence_after();
     const uint32_t tmem = bar->tmem;
     // ring entry 2 j + kv of an item: K (kv = 0) and V of its j-th block
+    if (warp >= kLoadWarp) {
+    setmaxnreg_dec<kIssueRegs>();
     if (warp == kLoadWarp) {
         if (lane == 0) {
             int ring = 0, nq = 0;
@@ -290,7 +296,9 @@ softmax_attn_dq_kernel(const __grid_constant__ CUtensorMap tQ, const __grid_cons
             mbar_wait_drain(&bar->drain, 0);
         }
         __syncwarp();
+    }
     } else {
+    setmaxnreg_inc<kMathRegs>();
         const int w = warp >> 2, row = tid & 127;  // column half, row
         const uint32_t lanes = (uint32_t)((warp & 3) * 32) << 16;
         const float sl = p.scale_log2;
@@ -508,6 +516,8 @@ softmax_attn_dkv_kernel(const __grid_constant__ CUtensorMap tQ, const __grid_con
     tc_fence_after();
     const uint32_t tmem = bar->tmem;
 
+    if (warp >= kLoadWarp) {
+    setmaxnreg_dec<kIssueRegs>();
     if (warp == kLoadWarp) {
         if (lane == 0) {
             int ring = 0, items = 0;
@@ -632,7 +642,9 @@ softmax_attn_dkv_kernel(const __grid_constant__ CUtensorMap tQ, const __grid_con
             mbar_wait_drain(&bar->drain, 0);
         }
         __syncwarp();
+    }
     } else {
+    setmaxnreg_inc<kMathRegs>();
         const int w = warp >> 2, row = tid & 127;  // query-column half, key row
         const uint32_t lanes = (uint32_t)((warp & 3) * 32) << 16;
         const uint32_t tS = tmem + C::kS + 64 * w + lanes, tD = tmem + C::kDp + 64 * w + lanes;

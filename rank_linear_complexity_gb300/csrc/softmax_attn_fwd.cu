@@ -38,7 +38,11 @@ namespace {
 
 using namespace ptx;
 
-constexpr int kThreads = 320;
+// Twelve warps (two idle), 168 registers each at launch; the two warpgroups that do the
+// arithmetic take registers from the third: 2 x 208 + 88 = 3 x 168.
+constexpr int kThreads = 384;
+constexpr uint32_t kMathRegs = 208, kIssueRegs = 88;
+static_assert(2 * kMathRegs + kIssueRegs == 3 * 168, "register split");
 constexpr int kLoadWarp = 8, kMmaWarp = 9;
 constexpr float kLazy = 8.f;  // log2 of the growth of the maximum that is left unscaled
 constexpr float kLog2e = 1.4426950408889634f, kLn2 = 0.6931471805599453f;
@@ -184,6 +188,8 @@ softmax_attn_fwd_kernel(const __grid_constant__ CUtensorMap tQ, const __grid_con
     tc_fence_after();
     const uint32_t tmem = bar->tmem;
 
+    if (warp >= kLoadWarp) {
+    setmaxnreg_dec<kIssueRegs>();
     if (warp == kLoadWarp) {
         if (lane == 0) {  // ---------------- loads
             int ring = 0, nq[2] = {0, 0};
@@ -338,7 +344,9 @@ softmax_attn_fwd_kernel(const __grid_constant__ CUtensorMap tQ, const __grid_con
             mbar_wait_drain(&bar->drain, 0);
         }
         __syncwarp();
-    } else {  // ---------------- softmax of one tile, one thread a row
+    }
+    } else {
+    setmaxnreg_inc<kMathRegs>();  // ---------------- softmax of one tile, one thread a row
         const int t = warp >> 2, row = tid & 127;
         const uint32_t lanes = (uint32_t)((warp & 3) * 32) << 16;
         const uint32_t tS = tmem + C::kS + 128 * t + lanes, tP = tmem + C::kP + C::kPStep * t + lanes,
@@ -414,14 +422,15 @@ softmax_attn_fwd_kernel(const __grid_constant__ CUtensorMap tQ, const __grid_con
                         l *= f;
                         m = mn;
                         if (j > x.lo) {
+#pragma unroll 1
+                            for (int c = 0; c < DP; c += 8) {  // rare, and S is in registers
+                                uint32_t o[8];
+                                tmem_ld8(tO + c, o);
 #pragma unroll
-                            for (int c = 0; c < DP; c += 32) {
-                                uint32_t o[32];
-                                tmem_ld32(tO + c, o);
-#pragma unroll
-                                for (int e = 0; e < 32; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * f);
-                                tmem_st32(tO + c, o);
+                                for (int e = 0; e < 8; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * f);
+                                tmem_st8_async(tO + c, o);
                             }
+                            tmem_wait_st();
                         }
                     }
                     const float off = m == -INFINITY ? 0.f : -m * sl;

@@ -1,7 +1,9 @@
 """GPU tests of the exact softmax attention (linformer_softmax_attn_fwd / _bwd through the
 Python binding) against the fp64 oracle, elementwise within the oracle's derived bounds, and
 within 5e-3 in the 2-norm: three independent roundings of relative size at most 2^-8, rms
-2^-8 / sqrt(3), give sqrt(3) x 2^-8 / sqrt(3) = 3.9e-3, and the fp32 part is below 1e-3."""
+2^-8 / sqrt(3), give sqrt(3) x 2^-8 / sqrt(3) = 3.9e-3, and the fp32 part is below 1e-3.
+The rounding of O that delta = dO.O takes over is one error for a whole row of dS, which sums
+over the keys do not average out: its bound is allowed on top."""
 import numpy as np
 import pytest
 import torch
@@ -45,7 +47,7 @@ def status():
     assert lf.linformer_debug_read_device_status() == 0
 
 
-def within(got, ref, bound, name):
+def within(got, ref, bound, name, rows=None):
     got, bad = orc.host64(got), np.isinf(ref)
     assert np.array_equal(got[bad], ref[bad]), name
     err = np.abs(np.where(bad, 0, got) - np.where(bad, 0, ref))
@@ -55,7 +57,8 @@ def within(got, ref, bound, name):
                            f"{np.unravel_index((err - bound).argmax(), err.shape)}"
     if ref.size >= 4096 and np.linalg.norm(ref[~bad]) > 0:
         rel = np.linalg.norm(err[~bad]) / np.linalg.norm(ref[~bad])
-        assert rel <= 5e-3, f"{name}: 2-norm {rel}"
+        extra = 0 if rows is None else np.linalg.norm(rows) / np.linalg.norm(ref)
+        assert rel <= 5e-3 + extra, f"{name}: 2-norm {rel}"
 
 
 CASES = {
@@ -123,6 +126,6 @@ def test_backward(name):
             O[bi, :, q[bi]:] = float("nan")
     got = lf.softmax_attention_backward(Q, K, V, O, dO, lse, lengths(q), lengths(k), **kw)
     status()
-    refs, bounds = orc.backward(Q, K, V, dO, q, k, **kw)
-    for n, g, r, e in zip(("dQ", "dK", "dV"), got, refs, bounds):
-        within(g, r, e, n)
+    refs, bounds, rows = orc.backward(Q, K, V, dO, q, k, **kw)
+    for n, g, r, e, w in zip(("dQ", "dK", "dV"), got, refs, bounds, rows):
+        within(g, r, e, n, w)
