@@ -4,9 +4,10 @@
 //     lse_i = log sum_j exp(scale Q_i.K_j)
 //
 // over the keys that the row sees (valid length, causal, sliding window), in one pass
-// over the keys: a running maximum m and sum l per row, P = exp(s - m) in bf16 for the
-// second product, O and l rescaled when m has grown by more than 2^kLazy since it was
-// last taken (P then stays below 2^kLazy, which fp32 accumulation does not notice).
+// over the keys: a running reference m and sum l per row, P = exp(s - m) in bf16 for the
+// second product.  Any m near the maximum serves (bf16 and fp32 keep their relative
+// precision up to 2^127), so m is the maximum of the row's first block and taken anew, with
+// O and l rescaled, only when a later block's maximum outgrows it by 2^kOutgrown.
 // The n x n scores never leave the SM.
 //
 // Persistent CTAs take work items one after another: a pair of 128-row query tiles of
@@ -44,7 +45,7 @@ constexpr int kThreads = 384;
 constexpr uint32_t kMathRegs = 208, kIssueRegs = 88;
 static_assert(2 * kMathRegs + kIssueRegs == 3 * 168, "register split");
 constexpr int kLoadWarp = 8, kMmaWarp = 9;
-constexpr float kLazy = 8.f;  // log2 of the growth of the maximum that is left unscaled
+constexpr float kOutgrown = 40.f;  // log2 of the growth of the maximum that is left unscaled
 constexpr float kLog2e = 1.4426950408889634f, kLn2 = 0.6931471805599453f;
 
 struct FwdParams {
@@ -143,6 +144,36 @@ struct Barriers {
     uint32_t tmem;
     int abort;
 };
+
+// 2^(s sl + off) of 32 scores, summed and packed.
+__device__ __forceinline__ void exp_chunk(const uint32_t (&v)[32], uint32_t (&o)[16], float sl, float off,
+                                          float2 &sum0, float2 &sum1) {
+    const float2 sl2 = make_float2(sl, sl), off2 = make_float2(off, off);
+#pragma unroll
+    for (int e = 0; e < 32; e += 2) {
+        float2 y = ffma2(make_float2(__uint_as_float(v[e]), __uint_as_float(v[e + 1])), sl2, off2);
+        y.x = ex2_approx(y.x);
+        y.y = ex2_approx(y.y);
+        if (e & 2) sum1 = fadd2(sum1, y);
+        else sum0 = fadd2(sum0, y);
+        o[e / 2] = pack2(y.x, y.y);
+    }
+}
+// Columns outside [a, a + w) become -inf.
+__device__ __forceinline__ void mask_chunk(uint32_t (&v)[32], int a, int w) {
+#pragma unroll
+    for (int e = 0; e < 32; ++e)
+        if ((unsigned)(e - a) >= (unsigned)w) v[e] = 0xff800000u;
+}
+__device__ __forceinline__ float max_chunk(const uint32_t (&v)[32]) {
+    float m0 = __uint_as_float(v[0]), m1 = __uint_as_float(v[1]);
+#pragma unroll
+    for (int e = 2; e < 30; e += 4) {
+        m0 = max3(m0, __uint_as_float(v[e]), __uint_as_float(v[e + 1]));
+        m1 = max3(m1, __uint_as_float(v[e + 2]), __uint_as_float(v[e + 3]));
+    }
+    return fmaxf(max3(m0, __uint_as_float(v[30]), __uint_as_float(v[31])), m1);
+}
 
 template <int DP>
 __global__ void __launch_bounds__(kThreads, 1)
@@ -251,7 +282,7 @@ softmax_attn_fwd_kernel(const __grid_constant__ CUtensorMap tQ, const __grid_con
             int n0 = 0, n1 = 0, i0 = 0, i1 = 0;  // per tile: blocks and items so far
             bool ok = true;
             // S of tile t from ring slot s
-            auto score = [&](int t, int s) {
+            auto issue_scores = [&](int t, int s) {
                 const uint64_t a = sdesc(smem_u32(sQ + t * C::kTileBytes), 16, 1024, kSwizzle128B);
                 const uint64_t k = sdesc(smem_u32(sKV + s * C::kTileBytes), 16, 1024, kSwizzle128B);
                 const uint32_t d = tmem + C::kS + 128 * t;
@@ -262,7 +293,7 @@ softmax_attn_fwd_kernel(const __grid_constant__ CUtensorMap tQ, const __grid_con
                 }
                 mma_commit(&bar->s_full[t]);
             };
-            auto values = [&](int t, int s, uint32_t acc) {
+            auto issue_output = [&](int t, int s, uint32_t acc) {
                 const uint64_t v = sdesc(smem_u32(sKV + s * C::kTileBytes), 16384, 1024, kSwizzle128B);
                 const uint32_t d = tmem + C::kO + DP * t, a = tmem + C::kP + C::kPStep * t;
 #pragma unroll
@@ -273,62 +304,72 @@ softmax_attn_fwd_kernel(const __grid_constant__ CUtensorMap tQ, const __grid_con
             for (int64_t idx = blockIdx.x; idx < p.items && ok; idx += gridDim.x) {
                 const Item it = load_item(p, idx);
                 const bool fix = ragged_end(it, p.nk);
-                // scores of block j for both tiles; false if a wait ran out
-                auto scores = [&](int j) {
-                    const int r = ring + 2 * (j - it.lo), s = r % C::kStages;
-                    if (!mbar_wait(&bar->full[s], (r / C::kStages) & 1, p.status, 73, abort_flag)) return false;
-#pragma unroll
-                    for (int t = 0; t < 2; ++t) {
-                        const Tile &x = it.t[t];
-                        if (j < x.lo || j >= x.hi) continue;
-                        const int nt = (t ? n1 : n0) + (j - x.lo);  // blocks of this tile before
-                        const int ni = t ? i1 : i0;
-                        if (j == x.lo && !mbar_wait(&bar->q_full[t], ni & 1, p.status, 74, abort_flag)) return false;
-                        if (nt > 0 && !mbar_wait(C::kSep ? &bar->s_free[t] : &bar->pv_done[t], (nt - 1) & 1,
-                                                 p.status, 75, abort_flag))
-                            return false;
-                        tc_fence_after();
-                        score(t, s);
-                        if (j == x.hi - 1) mma_commit(&bar->q_free[t]);
-                    }
-                    mma_commit(&bar->empty[s]);
+                auto landed = [&](int r, int code) {
+                    return mbar_wait(&bar->full[r % C::kStages], (r / C::kStages) & 1, p.status, code, abort_flag);
+                };
+                // S of tile t and block j, K in ring entry r
+                auto score = [&](int t, int j, int r) {
+                    const Tile &x = it.t[t];
+                    if (j < x.lo || j >= x.hi) return true;
+                    const int nt = (t ? n1 : n0) + (j - x.lo);
+                    if (j == x.lo && !mbar_wait(&bar->q_full[t], (t ? i1 : i0) & 1, p.status, 74, abort_flag))
+                        return false;
+                    // the last S has been read; P over S: not before the product that reads P is done
+                    if (nt > 0 && !mbar_wait(C::kSep ? &bar->s_free[t] : &bar->pv_done[t], (nt - 1) & 1,
+                                             p.status, 75, abort_flag))
+                        return false;
+                    tc_fence_after();
+                    issue_scores(t, r % C::kStages);
+                    if (j == x.hi - 1) mma_commit(&bar->q_free[t]);
                     return true;
                 };
-                auto outputs = [&](int j) {
-                    const int r = ring + 2 * (j - it.lo) + 1, s = r % C::kStages;
-                    if (!mbar_wait(&bar->full[s], (r / C::kStages) & 1, p.status, 76, abort_flag)) return false;
-                    if (fix && j == it.hi - 1) {
-                        mbar_arrive(&bar->fix_wanted);
-                        if (!mbar_wait(&bar->fixed, nfix & 1, p.status, 77, abort_flag)) return false;
-                        ++nfix;
-                    }
-#pragma unroll
-                    for (int t = 0; t < 2; ++t) {
-                        const Tile &x = it.t[t];
-                        if (j < x.lo || j >= x.hi) continue;
-                        const int nt = (t ? n1 : n0) + (j - x.lo), ni = t ? i1 : i0;
-                        if (!mbar_wait(&bar->p_full[t], nt & 1, p.status, 78, abort_flag)) return false;
-                        if (j == x.lo && ni > 0 &&
-                            !mbar_wait(&bar->o_free[t], (ni - 1) & 1, p.status, 79, abort_flag))
-                            return false;
-                        tc_fence_after();
-                        values(t, s, j > x.lo ? 1u : 0u);
-                    }
-                    mma_commit(&bar->empty[s]);
+                auto output = [&](int t, int j, int r) {
+                    const Tile &x = it.t[t];
+                    if (j < x.lo || j >= x.hi) return true;
+                    const int nt = (t ? n1 : n0) + (j - x.lo), ni = t ? i1 : i0;
+                    if (!mbar_wait(&bar->p_full[t], nt & 1, p.status, 78, abort_flag)) return false;
+                    if (j == x.lo && ni > 0 && !mbar_wait(&bar->o_free[t], (ni - 1) & 1, p.status, 79, abort_flag))
+                        return false;
+                    tc_fence_after();
+                    issue_output(t, r % C::kStages, j > x.lo ? 1u : 0u);
                     return true;
                 };
+                // The tiles work half a block apart, so that one's products run while the other
+                // is in its softmax: P beside S: S0(j+1), O1(j-1), S1(j+1), O0(j); P over S:
+                // O0(j), S0(j+1), O1(j), S1(j+1).
                 if (it.hi > it.lo) {
-                    ok = scores(it.lo);
-                    for (int j = it.lo; j < it.hi && ok; ++j) {
+                    auto fixed_end = [&]() {
+                        if (!fix) return true;
+                        mbar_arrive(&bar->fix_wanted);
+                        return mbar_wait(&bar->fixed, nfix++ & 1, p.status, 77, abort_flag);
+                    };
+                    ok = landed(ring, 73) && score(0, it.lo, ring) && score(1, it.lo, ring);
+                    mma_commit(&bar->empty[ring % C::kStages]);
+                    for (int j = it.lo; j < it.hi && ok; ++j, ring += 2) {
+                        const int v = ring + 1, k = ring + 2;
+                        const bool more = j + 1 < it.hi;
+                        ok = !more || landed(k, 73);
                         if (C::kSep) {
-                            if (j + 1 < it.hi) ok = scores(j + 1);
-                            if (ok) ok = outputs(j);
+                            ok = ok && (!more || score(0, j + 1, k));
+                            if (j > it.lo) {
+                                ok = ok && output(1, j - 1, v - 2);
+                                mma_commit(&bar->empty[(v - 2) % C::kStages]);
+                            }
+                            ok = ok && (!more || score(1, j + 1, k));
+                            if (more) mma_commit(&bar->empty[k % C::kStages]);
+                            ok = ok && landed(v, 76) && (more || fixed_end()) && output(0, j, v);
+                            if (!more) {
+                                ok = ok && output(1, j, v);
+                                mma_commit(&bar->empty[v % C::kStages]);
+                            }
                         } else {
-                            ok = outputs(j);
-                            if (ok && j + 1 < it.hi) ok = scores(j + 1);
+                            ok = ok && landed(v, 76) && (more || fixed_end());
+                            for (int t = 0; t < 2 && ok; ++t)
+                                ok = output(t, j, v) && (!more || score(t, j + 1, k));
+                            mma_commit(&bar->empty[v % C::kStages]);
+                            if (more) mma_commit(&bar->empty[k % C::kStages]);
                         }
                     }
-                    ring += 2 * (it.hi - it.lo);
                 }
                 const int b0 = it.t[0].hi - it.t[0].lo, b1 = it.t[1].hi - it.t[1].lo;
                 if (b0 > 0) {
@@ -355,120 +396,116 @@ softmax_attn_fwd_kernel(const __grid_constant__ CUtensorMap tQ, const __grid_con
         const int qi = row % p.qbox, hi_ = row / p.qbox;  // position and head within the tile
         int n = 0;
         bool ok = true;
+        // P.V of the tile's block before this one is done: P may be written over, O rescaled
+        auto last_product = [&](bool any) {
+            if (any) {
+                ok = warp_wait(&bar->pv_done[t], (n - 1) & 1, p.status, 81, abort_flag);
+                tc_fence_after();
+            }
+            return ok;
+        };
         for (int64_t idx = blockIdx.x; idx < p.items && ok; idx += gridDim.x) {
-            const Item it = load_item(p, idx);
-            const Tile x = t ? it.t[1] : it.t[0];
-            if (!x.live) continue;
-            const int i = x.q0 + qi, hg = x.h0 + hi_;
-            const bool exists = hi_ < p.hbox && hg < p.group && i < p.nq;
-            const bool valid = exists && i < it.sp.Lq;
-            const bool warp_valid = __any_sync(0xffffffffu, valid);
-            const int first = valid ? it.sp.first(i) : 0;
-            const int end = valid ? it.sp.end(i) : (1 << 30);
+            int lo, hi, first, end;
+            bool valid, warp_valid;
+            {
+                const Item it = load_item(p, idx);
+                const Tile x = t ? it.t[1] : it.t[0];
+                if (!x.live) continue;
+                const int i = x.q0 + qi;
+                lo = x.lo;
+                hi = x.hi;
+                valid = hi_ < p.hbox && x.h0 + hi_ < p.group && i < it.sp.Lq;
+                first = valid ? it.sp.first(i) : 0;
+                end = valid ? it.sp.end(i) : (1 << 30);
+                warp_valid = __any_sync(0xffffffffu, valid);
+            }
             float m = -INFINITY, l = 0.f;  // maximum (of the raw scores), sum of 2^((s - m) sl)
-            for (int j = x.lo; j < x.hi; ++j, ++n) {
+            for (int j = lo; j < hi; ++j, ++n) {
                 if (!warp_wait(&bar->s_full[t], n & 1, p.status, 80, abort_flag)) {
                     ok = false;
                     break;
                 }
                 tc_fence_after();
-                if (warp_valid) {
-                    uint32_t v[4][32];
+                if (!warp_valid) {  // only takes part in the barriers
+                    __syncwarp();
+                    if (C::kSep && lane == 0) mbar_arrive(&bar->s_free[t]);
+                    // no second arrival on p_full before the other warps' first
+                    if (C::kSep && !last_product(j > lo)) break;
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive(&bar->p_full[t]);
+                    continue;
+                }
+                uint32_t v[4][32];
 #pragma unroll
-                    for (int c = 0; c < 4; ++c) tmem_ld32_async(tS + 32 * c, v[c]);
-                    tmem_wait_ld(v[0]);
-                    tie32(v[1]);
-                    tie32(v[2]);
-                    tie32(v[3]);
-                    if (C::kSep) {
-                        tc_fence_before();
-                        __syncwarp();
-                        if (lane == 0) mbar_arrive(&bar->s_free[t]);
-                    }
-                    const int k0 = j * kTile;
-                    if (__any_sync(0xffffffffu, first > k0 || end < k0 + kTile)) {
-                        const int a = first - k0;
-                        const unsigned w = end > first ? (unsigned)(end - first) : 0u;
-#pragma unroll
-                        for (int c = 0; c < 4; ++c)
-#pragma unroll
-                            for (int e = 0; e < 32; ++e)
-                                if ((unsigned)(32 * c + e - a) >= w) v[c][e] = 0xff800000u;  // -inf
-                    }
-                    float m0 = -INFINITY, m1 = m0, m2 = m0, m3 = m0;
+                for (int c = 0; c < 4; ++c) tmem_ld32_async(tS + 32 * c, v[c]);
+                tmem_wait_ld(v[0]);
+                tie32(v[1]);
+                tie32(v[2]);
+                tie32(v[3]);
+                if (C::kSep) {
+                    tc_fence_before();
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive(&bar->s_free[t]);
+                }
+                const int k0 = j * kTile;
+                if (__any_sync(0xffffffffu, first > k0 || end < k0 + kTile)) {
 #pragma unroll
                     for (int c = 0; c < 4; ++c)
-#pragma unroll
-                        for (int e = 0; e < 32; e += 8) {
-                            m0 = max3(m0, __uint_as_float(v[c][e]), __uint_as_float(v[c][e + 1]));
-                            m1 = max3(m1, __uint_as_float(v[c][e + 2]), __uint_as_float(v[c][e + 3]));
-                            m2 = max3(m2, __uint_as_float(v[c][e + 4]), __uint_as_float(v[c][e + 5]));
-                            m3 = max3(m3, __uint_as_float(v[c][e + 6]), __uint_as_float(v[c][e + 7]));
-                        }
-                    const float mx = fmaxf(fmaxf(m0, m1), fmaxf(m2, m3));
-                    // the last product of this tile: before O is rescaled, and before P is
-                    // written where it was read from
-                    const bool grow = __any_sync(0xffffffffu, (mx - m) * sl > kLazy);
-                    if (j > x.lo && (grow || C::kSep)) {
-                        if (!warp_wait(&bar->pv_done[t], (n - 1) & 1, p.status, 81, abort_flag)) {
-                            ok = false;
-                            break;
-                        }
-                        tc_fence_after();
-                    }
-                    if (grow) {
-                        const float mn = fmaxf(m, mx);
-                        const float f = mn == -INFINITY ? 1.f : ex2_approx((m - mn) * sl);
-                        l *= f;
-                        m = mn;
-                        if (j > x.lo) {
+                        mask_chunk(v[c], first - k0 - 32 * c, first < end ? end - first : 0);
+                }
+                const float mx = fmaxf(fmaxf(max_chunk(v[0]), max_chunk(v[1])),
+                                       fmaxf(max_chunk(v[2]), max_chunk(v[3])));
+                if (__any_sync(0xffffffffu, valid && (mx - m) * sl > kOutgrown)) {
+                    if (!last_product(j > lo)) break;
+                    const float mn = fmaxf(m, mx);
+                    const float f = mn == -INFINITY ? 1.f : ex2_approx((m - mn) * sl);
+                    l *= f;
+                    m = mn;
+                    if (j > lo) {
 #pragma unroll 1
-                            for (int c = 0; c < DP; c += 8) {  // rare, and S is in registers
-                                uint32_t o[8];
-                                tmem_ld8(tO + c, o);
+                        for (int c = 0; c < DP; c += 8) {  // rare, and S is in registers
+                            uint32_t q[8];
+                            tmem_ld8(tO + c, q);
 #pragma unroll
-                                for (int e = 0; e < 8; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * f);
-                                tmem_st8_async(tO + c, o);
-                            }
-                            tmem_wait_st();
+                            for (int e = 0; e < 8; ++e) q[e] = __float_as_uint(__uint_as_float(q[e]) * f);
+                            tmem_st8_async(tO + c, q);
                         }
                     }
-                    const float off = m == -INFINITY ? 0.f : -m * sl;
-                    const float2 sl2 = make_float2(sl, sl), off2 = make_float2(off, off);
-                    float2 sum0 = make_float2(0.f, 0.f), sum1 = sum0;
+                }
+                const float off = m == -INFINITY ? 0.f : -m * sl;
+                float2 sum0 = make_float2(0.f, 0.f), sum1 = sum0;
+                if (C::kSep) {
+                    // P beside S is written at the end: until then the last block's is in use
+                    uint32_t o[4][16];
+#pragma unroll
+                    for (int c = 0; c < 4; ++c) exp_chunk(v[c], o[c], sl, off, sum0, sum1);
+                    if (!last_product(j > lo)) break;
+#pragma unroll
+                    for (int c = 0; c < 4; ++c) tmem_st16_async(tP + 16 * c, o[c]);
+                } else {
 #pragma unroll
                     for (int c = 0; c < 4; ++c) {
                         uint32_t o[16];
-#pragma unroll
-                        for (int e = 0; e < 32; e += 2) {
-                            float2 y = ffma2(make_float2(__uint_as_float(v[c][e]), __uint_as_float(v[c][e + 1])),
-                                             sl2, off2);
-                            y.x = ex2_approx(y.x);
-                            y.y = ex2_approx(y.y);
-                            if (e & 2) sum1 = fadd2(sum1, y);
-                            else sum0 = fadd2(sum0, y);
-                            o[e / 2] = pack2(y.x, y.y);
-                        }
+                        exp_chunk(v[c], o, sl, off, sum0, sum1);
                         tmem_st16_async(tP + 16 * c, o);
                     }
-                    tmem_wait_st();
-                    l += (sum0.x + sum0.y) + (sum1.x + sum1.y);
-                } else if (C::kSep) {
-                    __syncwarp();
-                    if (lane == 0) mbar_arrive(&bar->s_free[t]);
-                    // no second arrival on p_full before the other warps' first
-                    if (j > x.lo && !warp_wait(&bar->pv_done[t], (n - 1) & 1, p.status, 81, abort_flag)) {
-                        ok = false;
-                        break;
-                    }
                 }
+                tmem_wait_st();
                 tc_fence_before();
                 __syncwarp();
                 if (lane == 0) mbar_arrive(&bar->p_full[t]);
+                l += (sum0.x + sum0.y) + (sum1.x + sum1.y);
             }
             if (!ok) break;
             // O / l out of TMEM; rows without keys give O = 0 and lse = -inf
-            const bool some = x.hi > x.lo;
+            const bool some = hi > lo;
+            // (derived again: kept through the loop, it would cost registers there)
+            int64_t again = idx;
+            asm volatile("" : "+l"(again));
+            const Item it = load_item(p, again);
+            const Tile x = t ? it.t[1] : it.t[0];
+            const int i = x.q0 + qi, hg = x.h0 + hi_;
+            const bool exists = hi_ < p.hbox && hg < p.group && i < p.nq;
             if (some) {
                 if (!warp_wait(&bar->pv_done[t], (n - 1) & 1, p.status, 82, abort_flag)) break;
                 tc_fence_after();
