@@ -97,6 +97,40 @@ __device__ __forceinline__ bool warp_wait(uint64_t *bar, uint32_t parity, int *s
     return ok != 0;
 }
 
+// The same two waits for short hops.  The polling thread (or all lanes of a warp together)
+// repeats try_wait without the sleep hint and looks at the abort flag and the clock only
+// every 64th time: a hop from an arrival to the waiting warp takes 88 cycles, against 600
+// where one lane polls with the hint and hands the result to the others.
+constexpr uint32_t kSpinsPerCheck = 64;
+__device__ __forceinline__ bool spin_gives_up(uint32_t &spins, uint64_t &t0, int *status, int code,
+                                              volatile int *abort) {
+    if (++spins % kSpinsPerCheck) return false;
+    if (*abort) return true;
+    const uint64_t now = globaltimer();
+    if (spins == kSpinsPerCheck) t0 = now;
+    if (now - t0 <= kWaitLimitNs) return false;
+    *abort = 1;
+    if (status) atomicExch(status, code);
+    return true;
+}
+__device__ __forceinline__ bool thread_spin(uint64_t *bar, uint32_t parity, int *status, int code,
+                                            volatile int *abort) {
+    uint32_t spins = 0;
+    uint64_t t0 = 0;
+    while (!mbar_try_wait(bar, parity))
+        if (spin_gives_up(spins, t0, status, code, abort)) return false;
+    return true;
+}
+// Every lane of a converged warp; the vote gives all of them the same answer.
+__device__ __forceinline__ bool warp_spin(uint64_t *bar, uint32_t parity, int *status, int code,
+                                          volatile int *abort) {
+    uint32_t spins = 0;
+    uint64_t t0 = 0;
+    while (!__any_sync(0xffffffffu, mbar_try_wait(bar, parity)))
+        if (__any_sync(0xffffffffu, spin_gives_up(spins, t0, status, code, abort))) return false;
+    return true;
+}
+
 // Non-blocking probe of phase `parity` of `bar`.
 __device__ __forceinline__ bool mbar_test(uint64_t *bar, uint32_t parity) {
     uint32_t ok;

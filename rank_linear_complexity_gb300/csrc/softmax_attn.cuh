@@ -75,6 +75,7 @@ __device__ __forceinline__ void zero_rows(uint8_t *tile, int row0, int idx, int 
 bool encode_rows(CUtensorMap *m, const void *base, const Strides &s, int b, int heads, int group,
                  int n, int d, int rows, int hrows);
 int device_sms();
+int allow_smem(const void *kernel, uint32_t bytes, int slot);
 
 int forward(const Call &c);
 int backward(const Call &c);

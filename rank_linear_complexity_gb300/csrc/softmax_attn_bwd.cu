@@ -195,7 +195,7 @@ softmax_attn_dq_kernel(const __grid_constant__ CUtensorMap tQ, const __grid_cons
             for (int64_t idx = blockIdx.x; idx < p.items && ok; idx += gridDim.x) {
                 const DqItem it = dq_item(p, idx);
                 if (it.hi <= it.lo) continue;
-                if (nq > 0 && !mbar_wait(&bar->q_free, (nq - 1) & 1, p.status, 83, abort_flag)) break;
+                if (nq > 0 && !thread_spin(&bar->q_free, (nq - 1) & 1, p.status, 83, abort_flag)) break;
                 mbar_arrive_expect_tx(&bar->q_full, 2 * C::kTileBytes);
                 const int g = it.head % p.group, kvh = it.head / p.group;
                 load_rows<DP>(sQ, &tQ, &bar->q_full, it.q0, g, kvh, it.batch);
@@ -205,7 +205,7 @@ softmax_attn_dq_kernel(const __grid_constant__ CUtensorMap tQ, const __grid_cons
                     for (int kv = 0; kv < 2; ++kv, ++ring) {
                         const int s = ring % C::kStages;
                         if (ring >= C::kStages &&
-                            !mbar_wait(&bar->empty[s], (ring / C::kStages - 1) & 1, p.status, 84, abort_flag)) {
+                            !thread_spin(&bar->empty[s], (ring / C::kStages - 1) & 1, p.status, 84, abort_flag)) {
                             ok = false;
                             break;
                         }
@@ -224,7 +224,7 @@ softmax_attn_dq_kernel(const __grid_constant__ CUtensorMap tQ, const __grid_cons
                 if (it.hi <= it.lo) continue;
                 ring += 2 * (it.hi - it.lo);
                 if (it.sp.Lk >= p.nk || it.hi * kTile <= it.sp.Lk) continue;
-                if (!mbar_wait(&bar->fix_wanted, nfix & 1, p.status, 85, abort_flag)) break;
+                if (!thread_spin(&bar->fix_wanted, nfix & 1, p.status, 85, abort_flag)) break;
                 ++nfix;
                 zero_rows<DP>(sKV + (ring - 2) % C::kStages * C::kTileBytes,
                               it.sp.Lk - (it.hi - 1) * kTile, lane - 1, 31);
@@ -246,13 +246,13 @@ softmax_attn_dq_kernel(const __grid_constant__ CUtensorMap tQ, const __grid_cons
                 // S and dP of the item's block j: n + j blocks of this CTA came before
                 auto score = [&](int j) {
                     const int r = ring + 2 * j, s = r % C::kStages;
-                    if (!mbar_wait(&bar->full[s], (r / C::kStages) & 1, p.status, 86, abort_flag)) return false;
+                    if (!thread_spin(&bar->full[s], (r / C::kStages) & 1, p.status, 86, abort_flag)) return false;
                     if (fix && j == blocks - 1) {
                         mbar_arrive(&bar->fix_wanted);
-                        if (!mbar_wait(&bar->fixed, nfix & 1, p.status, 87, abort_flag)) return false;
+                        if (!thread_spin(&bar->fixed, nfix & 1, p.status, 87, abort_flag)) return false;
                         ++nfix;
                     }
-                    if (n + j > 0 && !mbar_wait(&bar->s_free, (n + j - 1) & 1, p.status, 88, abort_flag))
+                    if (n + j > 0 && !thread_spin(&bar->s_free, (n + j - 1) & 1, p.status, 88, abort_flag))
                         return false;
                     tc_fence_after();
                     mma_scores<DP>(tmem + C::kS, aQ, aKV + s * C::kTileBytes);
@@ -261,8 +261,8 @@ softmax_attn_dq_kernel(const __grid_constant__ CUtensorMap tQ, const __grid_cons
                 };
                 auto dprob = [&](int j) {
                     const int r = ring + 2 * j + 1, s = r % C::kStages, k = n + j;
-                    if (!mbar_wait(&bar->full[s], (r / C::kStages) & 1, p.status, 89, abort_flag)) return false;
-                    if (k >= 2 && !mbar_wait(&bar->dq_done[k & 1], ((k >> 1) - 1) & 1, p.status, 90, abort_flag))
+                    if (!thread_spin(&bar->full[s], (r / C::kStages) & 1, p.status, 89, abort_flag)) return false;
+                    if (k >= 2 && !thread_spin(&bar->dq_done[k & 1], ((k >> 1) - 1) & 1, p.status, 90, abort_flag))
                         return false;
                     tc_fence_after();
                     mma_scores<DP>(tmem + C::kDp + 128 * (k & 1), adO, aKV + s * C::kTileBytes);
@@ -270,7 +270,7 @@ softmax_attn_dq_kernel(const __grid_constant__ CUtensorMap tQ, const __grid_cons
                     mma_commit(&bar->empty[s]);
                     return true;
                 };
-                ok = mbar_wait(&bar->q_full, items & 1, p.status, 91, abort_flag) && score(0) && dprob(0);
+                ok = thread_spin(&bar->q_full, items & 1, p.status, 91, abort_flag) && score(0) && dprob(0);
                 for (int j = 0; j < blocks && ok; ++j) {
                     if (j + 1 < blocks && !(score(j + 1) && dprob(j + 1))) {
                         ok = false;
@@ -278,9 +278,9 @@ softmax_attn_dq_kernel(const __grid_constant__ CUtensorMap tQ, const __grid_cons
                     }
                     if (j + 1 >= blocks) mma_commit(&bar->q_free);  // the item's last use of Q and dO
                     const int k = n + j, s = (ring + 2 * j) % C::kStages;
-                    ok = mbar_wait(&bar->ds_full[k & 1], (k >> 1) & 1, p.status, 92, abort_flag) &&
+                    ok = thread_spin(&bar->ds_full[k & 1], (k >> 1) & 1, p.status, 92, abort_flag) &&
                          (j > 0 || items == 0 ||
-                          mbar_wait(&bar->acc_free, (items - 1) & 1, p.status, 93, abort_flag));
+                          thread_spin(&bar->acc_free, (items - 1) & 1, p.status, 93, abort_flag));
                     if (!ok) break;
                     tc_fence_after();
                     mma_sum<DP>(tmem + C::kDq, tmem + C::kDp + 128 * (k & 1), aKV + s * C::kTileBytes,
@@ -333,7 +333,7 @@ softmax_attn_dq_kernel(const __grid_constant__ CUtensorMap tQ, const __grid_cons
             const int first = valid ? it.sp.first(i) : 0, end = valid ? it.sp.end(i) : 0;
             bool ok = true;
             for (int j = it.lo; j < it.hi; ++j, ++n) {
-                if (!warp_wait(&bar->s_full, n & 1, p.status, 94, abort_flag)) {
+                if (!warp_spin(&bar->s_full, n & 1, p.status, 94, abort_flag)) {
                     ok = false;
                     break;
                 }
@@ -357,7 +357,7 @@ softmax_attn_dq_kernel(const __grid_constant__ CUtensorMap tQ, const __grid_cons
                         v[c][e + 1] = __float_as_uint(ex2_approx(y.y));
                     }
                 const uint32_t tD = tmem + C::kDp + 128 * (n & 1) + 64 * w + lanes;
-                if (!warp_wait(&bar->dp_full[n & 1], (n >> 1) & 1, p.status, 95, abort_flag)) {
+                if (!warp_spin(&bar->dp_full[n & 1], (n >> 1) & 1, p.status, 95, abort_flag)) {
                     ok = false;
                     break;
                 }
@@ -404,7 +404,7 @@ softmax_attn_dq_kernel(const __grid_constant__ CUtensorMap tQ, const __grid_cons
             if (!ok) break;
             const bool some = it.hi > it.lo;
             if (some) {
-                if (!warp_wait(&bar->dq_done[(n - 1) & 1], ((n - 1) >> 1) & 1, p.status, 96, abort_flag)) break;
+                if (!warp_spin(&bar->dq_done[(n - 1) & 1], ((n - 1) >> 1) & 1, p.status, 96, abort_flag)) break;
                 tc_fence_after();
             }
             __nv_bfloat16 *dst = p.dQ + it.batch * p.sdQ.b + it.head * p.sdQ.h + (int64_t)i * p.sdQ.n;
@@ -525,7 +525,7 @@ softmax_attn_dkv_kernel(const __grid_constant__ CUtensorMap tQ, const __grid_con
             for (int64_t idx = blockIdx.x; idx < p.items && ok; idx += gridDim.x) {
                 const DkvItem it = dkv_item(p, idx);
                 if (it.hi <= it.lo) continue;
-                if (items > 0 && !mbar_wait(&bar->kv_free, (items - 1) & 1, p.status, 100, abort_flag)) break;
+                if (items > 0 && !thread_spin(&bar->kv_free, (items - 1) & 1, p.status, 100, abort_flag)) break;
                 mbar_arrive_expect_tx(&bar->kv_full, 2 * C::kTileBytes);
                 load_rows<DP>(sK, &tK, &bar->kv_full, it.k0, 0, it.kvh, it.batch);
                 load_rows<DP>(sV, &tV, &bar->kv_full, it.k0, 0, it.kvh, it.batch);
@@ -534,7 +534,7 @@ softmax_attn_dkv_kernel(const __grid_constant__ CUtensorMap tQ, const __grid_con
                     for (int j = it.lo; j < it.hi; ++j, ++ring) {
                         const int s = ring % C::kStages;
                         if (ring >= C::kStages &&
-                            !mbar_wait(&bar->empty[s], (ring / C::kStages - 1) & 1, p.status, 101, abort_flag)) {
+                            !thread_spin(&bar->empty[s], (ring / C::kStages - 1) & 1, p.status, 101, abort_flag)) {
                             ok = false;
                             break;
                         }
@@ -561,7 +561,7 @@ softmax_attn_dkv_kernel(const __grid_constant__ CUtensorMap tQ, const __grid_con
                 }
                 for (int g = 0; g < p.group; ++g) {
                     ring += it.hi - it.lo;
-                    if (!mbar_wait(&bar->fix_wanted, nfix & 1, p.status, 102, abort_flag)) {
+                    if (!thread_spin(&bar->fix_wanted, nfix & 1, p.status, 102, abort_flag)) {
                         ok = false;
                         break;
                     }
@@ -589,17 +589,17 @@ softmax_attn_dkv_kernel(const __grid_constant__ CUtensorMap tQ, const __grid_con
                 int in_head = 0;  // tile of the next score step within its head
                 auto score = [&](int j) {
                     const int r = n + j, s = r % C::kStages;
-                    if (!mbar_wait(&bar->full[s], (r / C::kStages) & 1, p.status, 103, abort_flag)) return false;
+                    if (!thread_spin(&bar->full[s], (r / C::kStages) & 1, p.status, 103, abort_flag)) return false;
                     if (++in_head == per) {
                         in_head = 0;
                         if (fix) {
                             mbar_arrive(&bar->fix_wanted);
-                            if (!mbar_wait(&bar->fixed, nfix & 1, p.status, 104, abort_flag)) return false;
+                            if (!thread_spin(&bar->fixed, nfix & 1, p.status, 104, abort_flag)) return false;
                             ++nfix;
                         }
                     }
                     // S holds the P of the step before until its product is done
-                    if (r > 0 && !mbar_wait(&bar->pv_done, (r - 1) & 1, p.status, 105, abort_flag)) return false;
+                    if (r > 0 && !thread_spin(&bar->pv_done, (r - 1) & 1, p.status, 105, abort_flag)) return false;
                     tc_fence_after();
                     mma_scores<DP>(tmem + C::kS, aK, aT + s * 2 * C::kTileBytes);
                     mma_commit(&bar->s_full);
@@ -607,25 +607,25 @@ softmax_attn_dkv_kernel(const __grid_constant__ CUtensorMap tQ, const __grid_con
                 };
                 auto dprob = [&](int j) {
                     const int r = n + j, s = r % C::kStages;
-                    if (r > 0 && !mbar_wait(&bar->ds_done, (r - 1) & 1, p.status, 106, abort_flag)) return false;
+                    if (r > 0 && !thread_spin(&bar->ds_done, (r - 1) & 1, p.status, 106, abort_flag)) return false;
                     tc_fence_after();
                     mma_scores<DP>(tmem + C::kDp, aV, aT + s * 2 * C::kTileBytes + C::kTileBytes);
                     mma_commit(&bar->dp_full);
                     return true;
                 };
-                ok = mbar_wait(&bar->kv_full, items & 1, p.status, 107, abort_flag) && score(0) && dprob(0);
+                ok = thread_spin(&bar->kv_full, items & 1, p.status, 107, abort_flag) && score(0) && dprob(0);
                 for (int j = 0; j < steps && ok; ++j) {
                     const int r = n + j, s = r % C::kStages;
                     const uint32_t aQ = aT + s * 2 * C::kTileBytes, adO = aQ + C::kTileBytes;
-                    ok = mbar_wait(&bar->p_full, r & 1, p.status, 108, abort_flag) &&
+                    ok = thread_spin(&bar->p_full, r & 1, p.status, 108, abort_flag) &&
                          (j > 0 || items == 0 ||
-                          mbar_wait(&bar->acc_free, (items - 1) & 1, p.status, 109, abort_flag));
+                          thread_spin(&bar->acc_free, (items - 1) & 1, p.status, 109, abort_flag));
                     if (!ok) break;
                     tc_fence_after();
                     mma_sum<DP>(tmem + C::kDv, tmem + C::kS, adO, j > 0 ? 1u : 0u);
                     mma_commit(&bar->pv_done);
                     if (j + 1 < steps && !(ok = score(j + 1))) break;
-                    if (!(ok = mbar_wait(&bar->ds_full, r & 1, p.status, 110, abort_flag))) break;
+                    if (!(ok = thread_spin(&bar->ds_full, r & 1, p.status, 110, abort_flag))) break;
                     tc_fence_after();
                     mma_sum<DP>(tmem + C::kDk, tmem + C::kDp, aQ, j > 0 ? 1u : 0u);
                     mma_commit(&bar->ds_done);
@@ -665,8 +665,8 @@ softmax_attn_dkv_kernel(const __grid_constant__ CUtensorMap tQ, const __grid_con
                 const int s = n % C::kStages;
                 const float4 *lse4 = reinterpret_cast<const float4 *>(sR + s * 1024 + w * 256);
                 const float4 *del4 = reinterpret_cast<const float4 *>(sR + s * 1024 + 512 + w * 256);
-                if (!warp_wait(&bar->full[s], (n / C::kStages) & 1, p.status, 111, abort_flag) ||
-                    !warp_wait(&bar->s_full, n & 1, p.status, 112, abort_flag)) {
+                if (!warp_spin(&bar->full[s], (n / C::kStages) & 1, p.status, 111, abort_flag) ||
+                    !warp_spin(&bar->s_full, n & 1, p.status, 112, abort_flag)) {
                     ok = false;
                     break;
                 }
@@ -713,7 +713,7 @@ softmax_attn_dkv_kernel(const __grid_constant__ CUtensorMap tQ, const __grid_con
                 tc_fence_before();
                 __syncwarp();
                 if (lane == 0) mbar_arrive(&bar->p_full);
-                if (!warp_wait(&bar->dp_full, n & 1, p.status, 113, abort_flag)) {
+                if (!warp_spin(&bar->dp_full, n & 1, p.status, 113, abort_flag)) {
                     ok = false;
                     break;
                 }
@@ -748,7 +748,7 @@ softmax_attn_dkv_kernel(const __grid_constant__ CUtensorMap tQ, const __grid_con
             if (!ok) break;
             const bool some = steps > 0;
             if (some) {
-                if (!warp_wait(&bar->acc_full, items & 1, p.status, 114, abort_flag)) break;
+                if (!warp_spin(&bar->acc_full, items & 1, p.status, 114, abort_flag)) break;
                 tc_fence_after();
                 ++items;
             }
@@ -784,16 +784,13 @@ int launch(const Call &c, BwdParams &p) {
         !encode_rows(&tK, c.K, c.sK, c.b, c.hk, 1, c.nk, c.d, kTile, 1) ||
         !encode_rows(&tV, c.V, c.sV, c.b, c.hk, 1, c.nk, c.d, kTile, 1))
         return LINFORMER_ERR_LAUNCH;
-    if (cudaFuncSetAttribute(softmax_attn_dq_kernel<DP>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                             Cq::kSmem) != cudaSuccess ||
-        cudaFuncSetAttribute(softmax_attn_dkv_kernel<DP>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                             Ck::kSmem) != cudaSuccess)
-        return LINFORMER_ERR_LAUNCH;
+    int st = allow_smem(reinterpret_cast<const void *>(softmax_attn_dq_kernel<DP>), Cq::kSmem, DP == 64 ? 2 : 3);
+    if (!st) st = allow_smem(reinterpret_cast<const void *>(softmax_attn_dkv_kernel<DP>), Ck::kSmem, DP == 64 ? 4 : 5);
+    if (st) return st;
     void *ws = nullptr;
     const int64_t qitems = (int64_t)c.b * c.hq * p.qtiles, kitems = (int64_t)c.b * c.hk * p.kblocks;
     if (workspace_alloc(&ws, (size_t)qitems * 1024, c.stream) != LINFORMER_OK) return LINFORMER_ERR_ALLOC;
     p.rows = static_cast<float *>(ws);
-    int st = LINFORMER_OK;
     const int sms = device_sms();
     {
         KernelScope scope(LINFORMER_KERNEL_SOFTMAX_BWD, c.stream);

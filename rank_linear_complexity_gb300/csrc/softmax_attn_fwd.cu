@@ -19,14 +19,17 @@
 //   warp 8          lane 0: TMA loads (Q per item; K and V blocks through a ring);
 //                   lanes 1-31: zero the rows of V past the valid length (P is 0 there,
 //                   but 0 x NaN is not)
-//   warp 9          one thread issues S = Q.K^T (both from shared memory) and O += P.V (P
-//                   from TMEM)
+//   warps 9, 10     one thread each issues a tile's S = Q.K^T (both from shared memory) and
+//                   O += P.V (P from TMEM); a thread of its own per tile, since a product
+//                   takes about 350 cycles more from issue to notice than it computes, and
+//                   one thread would spend them waiting while the other tile is ready
 // Tensor memory: head dimension up to 64: S0 S1 (128 columns each), P0 P1 (64), O0 O1
 // (64): S of the next block is computed while this block's exponentials are taken.  Up to
 // 128: S0 S1 with P over the first half of S, O0 O1 (128): the next S waits for P.V.
 #include <cudaTypedefs.h>
 
 #include <algorithm>
+#include <atomic>
 #include <cmath>
 #include <mutex>
 
@@ -39,14 +42,14 @@ namespace {
 
 using namespace ptx;
 
-// Twelve warps (two idle), 168 registers each at launch; the two warpgroups that do the
+// Twelve warps (one idle), 168 registers each at launch; the two warpgroups that do the
 // arithmetic take registers from the third: 2 x 208 + 88 = 3 x 168.
 constexpr int kThreads = 384;
 constexpr uint32_t kMathRegs = 208, kIssueRegs = 88;
 static_assert(2 * kMathRegs + kIssueRegs == 3 * 168, "register split");
 constexpr int kLoadWarp = 8, kMmaWarp = 9;
 constexpr float kOutgrown = 40.f;  // log2 of the growth of the maximum that is left unscaled
-constexpr float kLog2e = 1.4426950408889634f, kLn2 = 0.6931471805599453f;
+constexpr float kLog2e = 1.4426950408889634f;
 
 struct FwdParams {
     const int32_t *q_lengths, *k_lengths;
@@ -139,7 +142,7 @@ __device__ __forceinline__ bool ragged_end(const Item &it, int nk) {
 
 struct Barriers {
     uint64_t q_full[2], q_free[2], s_full[2], s_free[2], p_full[2], pv_done[2], o_free[2];
-    uint64_t fix_wanted, fixed, drain;
+    uint64_t fix_wanted, fixed, drain[2];
     uint64_t full[10], empty[10];
     uint32_t tmem;
     int abort;
@@ -199,10 +202,11 @@ softmax_attn_fwd_kernel(const __grid_constant__ CUtensorMap tQ, const __grid_con
         }
         mbar_init(&bar->fix_wanted, 1);
         mbar_init(&bar->fixed, 31);
-        mbar_init(&bar->drain, 1);
+        mbar_init(&bar->drain[0], 1);
+        mbar_init(&bar->drain[1], 1);
         for (int s = 0; s < C::kStages; ++s) {
             mbar_init(&bar->full[s], 1);
-            mbar_init(&bar->empty[s], 1);
+            mbar_init(&bar->empty[s], 2);  // one arrival from each tile's products
         }
         bar->abort = 0;
         fence_mbar_init();
@@ -229,7 +233,7 @@ softmax_attn_fwd_kernel(const __grid_constant__ CUtensorMap tQ, const __grid_con
                 const Item it = load_item(p, idx);
                 for (int t = 0; t < 2 && ok; ++t) {
                     if (it.t[t].hi <= it.t[t].lo) continue;
-                    if (nq[t] > 0 && !mbar_wait(&bar->q_free[t], (nq[t] - 1) & 1, p.status, 70, abort_flag)) {
+                    if (nq[t] > 0 && !thread_spin(&bar->q_free[t], (nq[t] - 1) & 1, p.status, 70, abort_flag)) {
                         ok = false;
                         break;
                     }
@@ -243,7 +247,7 @@ softmax_attn_fwd_kernel(const __grid_constant__ CUtensorMap tQ, const __grid_con
                     for (int kv = 0; kv < 2; ++kv, ++ring) {
                         const int s = ring % C::kStages;
                         if (ring >= C::kStages &&
-                            !mbar_wait(&bar->empty[s], (ring / C::kStages - 1) & 1, p.status, 71, abort_flag)) {
+                            !thread_spin(&bar->empty[s], (ring / C::kStages - 1) & 1, p.status, 71, abort_flag)) {
                             ok = false;
                             break;
                         }
@@ -266,7 +270,7 @@ softmax_attn_fwd_kernel(const __grid_constant__ CUtensorMap tQ, const __grid_con
                 ring += 2 * blocks;
                 if (!ragged_end(it, p.nk)) continue;
                 // the issuing thread has seen the block land
-                if (!mbar_wait(&bar->fix_wanted, nfix & 1, p.status, 72, abort_flag)) break;
+                if (!thread_spin(&bar->fix_wanted, nfix & 1, p.status, 72, abort_flag)) break;
                 ++nfix;
                 zero_rows<DP>(sKV + (ring - 1) % C::kStages * C::kTileBytes,
                               it.sp.Lk - (it.hi - 1) * kTile, lane - 1, 31);
@@ -275,114 +279,84 @@ softmax_attn_fwd_kernel(const __grid_constant__ CUtensorMap tQ, const __grid_con
             }
         }
         __syncwarp();
-    } else if (warp == kMmaWarp) {
-        if (elect_one()) {  // ---------------- products
+    } else if (warp == kMmaWarp || warp == kMmaWarp + 1) {
+        const int t = warp - kMmaWarp;
+        if (elect_one()) {  // ---------------- products of tile t
             const uint32_t idesc_s = idesc_f16(128, 128, 1, 0, 0), idesc_o = idesc_f16(128, DP, 1, 0, 1);
-            int ring = 0, nfix = 0;
-            int n0 = 0, n1 = 0, i0 = 0, i1 = 0;  // per tile: blocks and items so far
+            const uint64_t dq = sdesc(smem_u32(sQ + t * C::kTileBytes), 16, 1024, kSwizzle128B);
+            const uint32_t tS = tmem + C::kS + 128 * t, tP = tmem + C::kP + C::kPStep * t,
+                           tO = tmem + C::kO + DP * t;
+            int ring = 0, nfix = 0, n = 0, items = 0;  // ring entries, fixed blocks, tile's blocks and items
             bool ok = true;
-            // S of tile t from ring slot s
-            auto issue_scores = [&](int t, int s) {
-                const uint64_t a = sdesc(smem_u32(sQ + t * C::kTileBytes), 16, 1024, kSwizzle128B);
-                const uint64_t k = sdesc(smem_u32(sKV + s * C::kTileBytes), 16, 1024, kSwizzle128B);
-                const uint32_t d = tmem + C::kS + 128 * t;
-#pragma unroll
-                for (int x = 0; x < DP / 16; ++x) {
-                    const uint64_t off = (uint64_t)((x >> 2) * 1024 + (x & 3) * 2);
-                    mma_ss(d, a + off, k + off, idesc_s, x > 0 ? 1u : 0u);
-                }
-                mma_commit(&bar->s_full[t]);
-            };
-            auto issue_output = [&](int t, int s, uint32_t acc) {
-                const uint64_t v = sdesc(smem_u32(sKV + s * C::kTileBytes), 16384, 1024, kSwizzle128B);
-                const uint32_t d = tmem + C::kO + DP * t, a = tmem + C::kP + C::kPStep * t;
-#pragma unroll
-                for (int x = 0; x < 8; ++x)
-                    mma_ts(d, a + 8 * x, v + (uint64_t)(128 * x), idesc_o, (acc || x > 0) ? 1u : 0u);
-                mma_commit(&bar->pv_done[t]);
+            auto landed = [&](int r) {
+                return thread_spin(&bar->full[r % C::kStages], (r / C::kStages) & 1, p.status, 73, abort_flag);
             };
             for (int64_t idx = blockIdx.x; idx < p.items && ok; idx += gridDim.x) {
                 const Item it = load_item(p, idx);
+                const int lo = t ? it.t[1].lo : it.t[0].lo, hi = t ? it.t[1].hi : it.t[0].hi;
                 const bool fix = ragged_end(it, p.nk);
-                auto landed = [&](int r, int code) {
-                    return mbar_wait(&bar->full[r % C::kStages], (r / C::kStages) & 1, p.status, code, abort_flag);
-                };
-                // S of tile t and block j, K in ring entry r
-                auto score = [&](int t, int j, int r) {
-                    const Tile &x = it.t[t];
-                    if (j < x.lo || j >= x.hi) return true;
-                    const int nt = (t ? n1 : n0) + (j - x.lo);
-                    if (j == x.lo && !mbar_wait(&bar->q_full[t], (t ? i1 : i0) & 1, p.status, 74, abort_flag))
-                        return false;
-                    // the last S has been read; P over S: not before the product that reads P is done
-                    if (nt > 0 && !mbar_wait(C::kSep ? &bar->s_free[t] : &bar->pv_done[t], (nt - 1) & 1,
+                // S of block j (K in ring entry r): once the last S has been read and, with P
+                // over S, its product is done
+                auto score = [&](int j, int r) {
+                    if (!landed(r)) return false;
+                    if (j < lo || j >= hi) {
+                        mbar_arrive(&bar->empty[r % C::kStages]);
+                        return true;
+                    }
+                    const int nt = n + (j - lo);
+                    if (j == lo && !thread_spin(&bar->q_full[t], items & 1, p.status, 74, abort_flag)) return false;
+                    if (nt > 0 && !thread_spin(C::kSep ? &bar->s_free[t] : &bar->pv_done[t], (nt - 1) & 1,
                                              p.status, 75, abort_flag))
                         return false;
                     tc_fence_after();
-                    issue_scores(t, r % C::kStages);
-                    if (j == x.hi - 1) mma_commit(&bar->q_free[t]);
+                    const uint64_t k = sdesc(smem_u32(sKV + r % C::kStages * C::kTileBytes), 16, 1024, kSwizzle128B);
+#pragma unroll
+                    for (int x = 0; x < DP / 16; ++x) {
+                        const uint64_t off = (uint64_t)((x >> 2) * 1024 + (x & 3) * 2);
+                        mma_ss(tS, dq + off, k + off, idesc_s, x > 0 ? 1u : 0u);
+                    }
+                    mma_commit(&bar->s_full[t]);
+                    mma_commit(&bar->empty[r % C::kStages]);
+                    if (j == hi - 1) mma_commit(&bar->q_free[t]);
                     return true;
                 };
-                auto output = [&](int t, int j, int r) {
-                    const Tile &x = it.t[t];
-                    if (j < x.lo || j >= x.hi) return true;
-                    const int nt = (t ? n1 : n0) + (j - x.lo), ni = t ? i1 : i0;
-                    if (!mbar_wait(&bar->p_full[t], nt & 1, p.status, 78, abort_flag)) return false;
-                    if (j == x.lo && ni > 0 && !mbar_wait(&bar->o_free[t], (ni - 1) & 1, p.status, 79, abort_flag))
+                // O += P.V of block j (V in ring entry r)
+                auto output = [&](int j, int r) {
+                    if (!landed(r)) return false;
+                    if (fix && j == it.hi - 1) {
+                        if (t == 0) mbar_arrive(&bar->fix_wanted);
+                        if (!thread_spin(&bar->fixed, nfix++ & 1, p.status, 77, abort_flag)) return false;
+                    }
+                    if (j < lo || j >= hi) {
+                        mbar_arrive(&bar->empty[r % C::kStages]);
+                        return true;
+                    }
+                    if (!thread_spin(&bar->p_full[t], (n + (j - lo)) & 1, p.status, 78, abort_flag)) return false;
+                    if (j == lo && items > 0 &&
+                        !thread_spin(&bar->o_free[t], (items - 1) & 1, p.status, 79, abort_flag))
                         return false;
                     tc_fence_after();
-                    issue_output(t, r % C::kStages, j > x.lo ? 1u : 0u);
+                    const uint64_t v = sdesc(smem_u32(sKV + r % C::kStages * C::kTileBytes), 16384, 1024, kSwizzle128B);
+#pragma unroll
+                    for (int x = 0; x < 8; ++x)
+                        mma_ts(tO, tP + 8 * x, v + (uint64_t)(128 * x), idesc_o, (j > lo || x > 0) ? 1u : 0u);
+                    mma_commit(&bar->pv_done[t]);
+                    mma_commit(&bar->empty[r % C::kStages]);
                     return true;
                 };
-                // The tiles work half a block apart, so that one's products run while the other
-                // is in its softmax: P beside S: S0(j+1), O1(j-1), S1(j+1), O0(j); P over S:
-                // O0(j), S0(j+1), O1(j), S1(j+1).
-                if (it.hi > it.lo) {
-                    auto fixed_end = [&]() {
-                        if (!fix) return true;
-                        mbar_arrive(&bar->fix_wanted);
-                        return mbar_wait(&bar->fixed, nfix++ & 1, p.status, 77, abort_flag);
-                    };
-                    ok = landed(ring, 73) && score(0, it.lo, ring) && score(1, it.lo, ring);
-                    mma_commit(&bar->empty[ring % C::kStages]);
-                    for (int j = it.lo; j < it.hi && ok; ++j, ring += 2) {
-                        const int v = ring + 1, k = ring + 2;
-                        const bool more = j + 1 < it.hi;
-                        ok = !more || landed(k, 73);
-                        if (C::kSep) {
-                            ok = ok && (!more || score(0, j + 1, k));
-                            if (j > it.lo) {
-                                ok = ok && output(1, j - 1, v - 2);
-                                mma_commit(&bar->empty[(v - 2) % C::kStages]);
-                            }
-                            ok = ok && (!more || score(1, j + 1, k));
-                            if (more) mma_commit(&bar->empty[k % C::kStages]);
-                            ok = ok && landed(v, 76) && (more || fixed_end()) && output(0, j, v);
-                            if (!more) {
-                                ok = ok && output(1, j, v);
-                                mma_commit(&bar->empty[v % C::kStages]);
-                            }
-                        } else {
-                            ok = ok && landed(v, 76) && (more || fixed_end());
-                            for (int t = 0; t < 2 && ok; ++t)
-                                ok = output(t, j, v) && (!more || score(t, j + 1, k));
-                            mma_commit(&bar->empty[v % C::kStages]);
-                            if (more) mma_commit(&bar->empty[k % C::kStages]);
-                        }
-                    }
+                if (it.hi > it.lo) ok = score(it.lo, ring);
+                for (int j = it.lo; j < it.hi && ok; ++j, ring += 2) {
+                    const bool more = j + 1 < it.hi;
+                    if (C::kSep) ok = (!more || score(j + 1, ring + 2)) && output(j, ring + 1);
+                    else ok = output(j, ring + 1) && (!more || score(j + 1, ring + 2));
                 }
-                const int b0 = it.t[0].hi - it.t[0].lo, b1 = it.t[1].hi - it.t[1].lo;
-                if (b0 > 0) {
-                    n0 += b0;
-                    ++i0;
-                }
-                if (b1 > 0) {
-                    n1 += b1;
-                    ++i1;
+                if (hi > lo) {
+                    n += hi - lo;
+                    ++items;
                 }
             }
-            mma_commit(&bar->drain);
-            mbar_wait_drain(&bar->drain, 0);
+            mma_commit(&bar->drain[t]);
+            mbar_wait_drain(&bar->drain[t], 0);
         }
         __syncwarp();
     }
@@ -399,7 +373,7 @@ softmax_attn_fwd_kernel(const __grid_constant__ CUtensorMap tQ, const __grid_con
         // P.V of the tile's block before this one is done: P may be written over, O rescaled
         auto last_product = [&](bool any) {
             if (any) {
-                ok = warp_wait(&bar->pv_done[t], (n - 1) & 1, p.status, 81, abort_flag);
+                ok = warp_spin(&bar->pv_done[t], (n - 1) & 1, p.status, 81, abort_flag);
                 tc_fence_after();
             }
             return ok;
@@ -421,7 +395,7 @@ softmax_attn_fwd_kernel(const __grid_constant__ CUtensorMap tQ, const __grid_con
             }
             float m = -INFINITY, l = 0.f;  // maximum (of the raw scores), sum of 2^((s - m) sl)
             for (int j = lo; j < hi; ++j, ++n) {
-                if (!warp_wait(&bar->s_full[t], n & 1, p.status, 80, abort_flag)) {
+                if (!warp_spin(&bar->s_full[t], n & 1, p.status, 80, abort_flag)) {
                     ok = false;
                     break;
                 }
@@ -507,7 +481,7 @@ softmax_attn_fwd_kernel(const __grid_constant__ CUtensorMap tQ, const __grid_con
             const int i = x.q0 + qi, hg = x.h0 + hi_;
             const bool exists = hi_ < p.hbox && hg < p.group && i < p.nq;
             if (some) {
-                if (!warp_wait(&bar->pv_done[t], (n - 1) & 1, p.status, 82, abort_flag)) break;
+                if (!warp_spin(&bar->pv_done[t], (n - 1) & 1, p.status, 82, abort_flag)) break;
                 tc_fence_after();
             }
             const bool dead = !valid || l == 0.f;
@@ -624,10 +598,7 @@ int launch(const Call &c, FwdParams &p) {
         p.part_o = reinterpret_cast<float *>(ws);
         p.part_lse = p.part_o + rows * DP;
     }
-    int st = LINFORMER_OK;
-    if (cudaFuncSetAttribute(softmax_attn_fwd_kernel<DP>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                             C::kSmem) != cudaSuccess)
-        st = LINFORMER_ERR_LAUNCH;
+    int st = allow_smem(reinterpret_cast<const void *>(softmax_attn_fwd_kernel<DP>), C::kSmem, DP == 64 ? 0 : 1);
     if (!st) {
         KernelScope scope(LINFORMER_KERNEL_SOFTMAX, c.stream);
         const int grid = (int)std::min<int64_t>(p.items, device_sms());
@@ -680,6 +651,20 @@ int device_sms() {
         g_sms[dev] = v > 0 ? v : 148;
     }
     return g_sms[dev];
+}
+
+// The kernel's shared memory, allowed once per device (slot: one per kernel).
+int allow_smem(const void *kernel, uint32_t bytes, int slot) {
+    static std::atomic<uint8_t> done[kMaxDev][6];
+    int dev = 0;
+    cudaGetDevice(&dev);
+    if (dev >= 0 && dev < kMaxDev && done[dev][slot].load(std::memory_order_acquire)) return LINFORMER_OK;
+    if (cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes) != cudaSuccess) {
+        cudaGetLastError();
+        return LINFORMER_ERR_LAUNCH;
+    }
+    if (dev >= 0 && dev < kMaxDev) done[dev][slot].store(1, std::memory_order_release);
+    return LINFORMER_OK;
 }
 
 int forward(const Call &c) {

@@ -53,6 +53,8 @@ def library_path() -> str:
 def lib() -> ctypes.CDLL:
     """The loaded CUDA library (raises if it was never built)."""
     global _lib
+    if _lib is not None:
+        return _lib
     with _lock:
         if _lib is None:
             path = _build.LIB
@@ -314,48 +316,63 @@ def dense_attention(Q, K, V, lengths=None, out=None, stream=None):
 
 
 # --- exact softmax attention and rotary positions (strided [b][h][n][d] tensors) ------------
+#
+# Calls of a few microseconds: one ctypes array holds all strides of a call, and the current
+# stream comes from the binding that torch.cuda.current_stream() wraps (1 us instead of 6).
 
-def _strides(x):
-    """The int64[3] of batch, head and row strides of a tensor [b][h][n][d]."""
-    b, h, n, one = x.stride()
-    if one != 1 and x.shape[3] != 1:
-        raise ValueError("the last dimension has to be contiguous")
-    return (ctypes.c_int64 * 3)(b, h, n)
-
-
-def _same_device(*tensors):
-    """The device of the tensors (None entries are passed over); they have to share it."""
-    dev = None
-    for t in tensors:
-        if t is None:
-            continue
-        if dev is None:
-            dev = t.device
-        elif t.device != dev:
-            raise ValueError(f"tensors on {dev} and {t.device}")
-    if dev.type != "cuda":
-        raise ValueError(f"CUDA tensors are needed, got {dev}")
-    return dev
+def _strides(*tensors):
+    """(int64 array of batch, head and row strides, the address of each tensor's three)."""
+    flat = []
+    for x in tensors:
+        b, h, n, one = x.stride()
+        if one != 1 and x.shape[3] != 1:
+            raise ValueError("the last dimension has to be contiguous")
+        flat += (b, h, n)
+    arr = (ctypes.c_int64 * len(flat))(*flat)
+    at = ctypes.addressof(arr)
+    return arr, range(at, at + 24 * len(tensors), 24)
 
 
-def _on(device, call):
-    """call() with `device` current: the library works on the current device."""
+def _device_of(first, *others):
+    """The CUDA device that all tensors (None: not given) are on."""
+    device = first.device
+    if device.type != "cuda":
+        raise ValueError(f"CUDA tensors are needed, got {device}")
+    for t in others:
+        if t is not None and t.device != device:
+            raise ValueError(f"tensors on {device} and {t.device}")
+    return device
+
+
+def _launch(device, stream, name, call):
+    """call(stream handle) with `device` current (the library works on the current device)."""
     import torch
-    if torch.cuda.current_device() == device.index:
-        return call()
-    with torch.cuda.device(device):
-        return call()
+    if stream is None:
+        handle = torch._C._cuda_getCurrentRawStream(device.index)
+    else:
+        handle = _stream_handle(stream)
+    if torch._C._cuda_getDevice() == device.index:
+        st = call(handle)
+    else:
+        with torch.cuda.device(device):
+            st = call(handle)
+    if st != 0:
+        raise LinformerError(st, name)
 
 
-def _check_words(name, x, dtype, shape):
-    if x is not None and (x.dtype != dtype or tuple(x.shape) != shape or not x.is_contiguous()):
-        raise ValueError(f"{name}: a contiguous {dtype} tensor of shape {shape} is needed")
+def _check(name, x, shape, dtype, contiguous=False):
+    if x.shape != shape or x.dtype != dtype or (contiguous and not x.is_contiguous()):
+        raise ValueError(f"{name}: a{' contiguous' if contiguous else ''} {dtype} tensor of shape "
+                         f"{tuple(shape)} is needed, got {x.dtype} of {tuple(x.shape)}")
 
 
-def _check_shape(name, x, shape, dtype):
-    if tuple(x.shape) != shape or x.dtype != dtype:
-        raise ValueError(f"{name}: {dtype} of shape {shape} is needed, got {x.dtype} of "
-                         f"{tuple(x.shape)}")
+def _check_words(q_lengths, k_lengths, lse, b, hq, n):
+    import torch
+    if q_lengths is not None:
+        _check("q_lengths", q_lengths, (b,), torch.int32, True)
+    if k_lengths is not None:
+        _check("k_lengths", k_lengths, (b,), torch.int32, True)
+    _check("lse", lse, (b, hq, n), torch.float32, True)
 
 
 def softmax_attention(Q, K, V, q_lengths=None, k_lengths=None, causal: bool = False,
@@ -366,28 +383,25 @@ def softmax_attention(Q, K, V, q_lengths=None, k_lengths=None, causal: bool = Fa
     causal: the valid parts end together (the last query sees every key), with window > 0
     only the last `window` keys up to its own.  scale defaults to 1 / sqrt(d)."""
     import torch
-    b, hq, n, d = Q.shape
+    b, hq, n, d = shape = Q.shape
     hk, m = K.shape[1], K.shape[2]
-    _check_shape("K", K, (b, hk, m, d), Q.dtype)
-    _check_shape("V", V, (b, hk, m, d), Q.dtype)
-    device = _same_device(Q, K, V, q_lengths, k_lengths, out, lse)
+    dtype = Q.dtype
+    device = _device_of(Q, K, V, q_lengths, k_lengths, out, lse)
+    _check("K", K, (b, hk, m, d), dtype)
+    _check("V", V, (b, hk, m, d), dtype)
     if out is None:
-        out = torch.empty((b, hq, n, d), dtype=Q.dtype, device=device)
+        out = torch.empty(shape, dtype=dtype, device=device)
     else:
-        _check_shape("out", out, (b, hq, n, d), Q.dtype)
+        _check("out", out, shape, dtype)
     if lse is None:
         lse = torch.empty((b, hq, n), dtype=torch.float32, device=device)
-    _check_words("lse", lse, torch.float32, (b, hq, n))
-    _check_words("q_lengths", q_lengths, torch.int32, (b,))
-    _check_words("k_lengths", k_lengths, torch.int32, (b,))
+    _check_words(q_lengths, k_lengths, lse, b, hq, n)
     code = dtype_code(Q)
-    st = _on(device, lambda: lib().linformer_softmax_attn_fwd(
-        Q.data_ptr(), _strides(Q), K.data_ptr(), _strides(K), V.data_ptr(), _strides(V),
-        out.data_ptr(), _strides(out), lse.data_ptr(), _ptr(q_lengths), _ptr(k_lengths), b, hq,
-        hk, n, m, d, d ** -0.5 if scale is None else scale, int(causal), window, code,
-        _stream_handle(stream)))
-    if st != 0:
-        raise LinformerError(st, "linformer_softmax_attn_fwd")
+    keep, (sQ, sK, sV, sO) = _strides(Q, K, V, out)
+    _launch(device, stream, "linformer_softmax_attn_fwd", lambda s: lib().linformer_softmax_attn_fwd(
+        Q.data_ptr(), sQ, K.data_ptr(), sK, V.data_ptr(), sV, out.data_ptr(), sO, lse.data_ptr(),
+        _ptr(q_lengths), _ptr(k_lengths), b, hq, hk, n, m, d, d ** -0.5 if scale is None else scale,
+        1 if causal else 0, window, code, s))
     return out, lse
 
 
@@ -396,31 +410,28 @@ def softmax_attention_backward(Q, K, V, O, dO, lse, q_lengths=None, k_lengths=No
                                dK=None, dV=None, stream=None):
     """(dQ, dK, dV) from the inputs and results of softmax_attention and dO = dLoss/dO."""
     import torch
-    b, hq, n, d = Q.shape
+    b, hq, n, d = shape = Q.shape
     hk, m = K.shape[1], K.shape[2]
-    device = _same_device(Q, K, V, O, dO, lse, q_lengths, k_lengths, dQ, dK, dV)
+    kv, dtype = (b, hk, m, d), Q.dtype
+    device = _device_of(Q, K, V, O, dO, lse, q_lengths, k_lengths, dQ, dK, dV)
     if dQ is None:
-        dQ = torch.empty((b, hq, n, d), dtype=Q.dtype, device=device)
+        dQ = torch.empty(shape, dtype=dtype, device=device)
     if dK is None:
-        dK = torch.empty((b, hk, m, d), dtype=Q.dtype, device=device)
+        dK = torch.empty(kv, dtype=dtype, device=device)
     if dV is None:
-        dV = torch.empty((b, hk, m, d), dtype=Q.dtype, device=device)
+        dV = torch.empty(kv, dtype=dtype, device=device)
     for name, x in (("O", O), ("dO", dO), ("dQ", dQ)):
-        _check_shape(name, x, (b, hq, n, d), Q.dtype)
+        _check(name, x, shape, dtype)
     for name, x in (("K", K), ("V", V), ("dK", dK), ("dV", dV)):
-        _check_shape(name, x, (b, hk, m, d), Q.dtype)
-    _check_words("lse", lse, torch.float32, (b, hq, n))
-    _check_words("q_lengths", q_lengths, torch.int32, (b,))
-    _check_words("k_lengths", k_lengths, torch.int32, (b,))
+        _check(name, x, kv, dtype)
+    _check_words(q_lengths, k_lengths, lse, b, hq, n)
     code = dtype_code(Q)
-    st = _on(device, lambda: lib().linformer_softmax_attn_bwd(
-        Q.data_ptr(), _strides(Q), K.data_ptr(), _strides(K), V.data_ptr(), _strides(V),
-        O.data_ptr(), _strides(O), dO.data_ptr(), _strides(dO), lse.data_ptr(), dQ.data_ptr(),
-        _strides(dQ), dK.data_ptr(), _strides(dK), dV.data_ptr(), _strides(dV), _ptr(q_lengths),
-        _ptr(k_lengths), b, hq, hk, n, m, d, d ** -0.5 if scale is None else scale, int(causal),
-        window, code, _stream_handle(stream)))
-    if st != 0:
-        raise LinformerError(st, "linformer_softmax_attn_bwd")
+    keep, (sQ, sK, sV, sO, sdO, sdQ, sdK, sdV) = _strides(Q, K, V, O, dO, dQ, dK, dV)
+    _launch(device, stream, "linformer_softmax_attn_bwd", lambda s: lib().linformer_softmax_attn_bwd(
+        Q.data_ptr(), sQ, K.data_ptr(), sK, V.data_ptr(), sV, O.data_ptr(), sO, dO.data_ptr(), sdO,
+        lse.data_ptr(), dQ.data_ptr(), sdQ, dK.data_ptr(), sdK, dV.data_ptr(), sdV,
+        _ptr(q_lengths), _ptr(k_lengths), b, hq, hk, n, m, d, d ** -0.5 if scale is None else scale,
+        1 if causal else 0, window, code, s))
     return dQ, dK, dV
 
 
@@ -429,12 +440,9 @@ def rotary_phase(rot: int, base: float = 10000.0, scaling: int = ROTARY_PLAIN,
                  beta_slow: float = 1.0, device="cuda", stream=None):
     """The table of `rot / 2` frequencies that rotary() takes (int64, made once and kept)."""
     import torch
-    phase = torch.empty(rot // 2, dtype=torch.int64, device=device)
-    st = _on(phase.device, lambda: lib().linformer_rotary_phase(
-        phase.data_ptr(), rot, base, scaling, factor, original_length, beta_fast, beta_slow,
-        _stream_handle(stream)))
-    if st != 0:
-        raise LinformerError(st, "linformer_rotary_phase")
+    phase = torch.empty(max(rot // 2, 1), dtype=torch.int64, device=device)
+    _launch(phase.device, stream, "linformer_rotary_phase", lambda s: lib().linformer_rotary_phase(
+        phase.data_ptr(), rot, base, scaling, factor, original_length, beta_fast, beta_slow, s))
     return phase
 
 
@@ -448,23 +456,30 @@ def rotary(x, x2=None, phase=None, positions=None, start: int = 0, rot=None,
     import torch
     b, h, n, d = x.shape
     rot = d if rot is None else rot
-    device = _same_device(x, x2, phase, positions, out, out2)
-    out = torch.empty_like(x) if out is None else out
-    _check_shape("out", out, (b, h, n, d), x.dtype)
-    _check_words("phase", phase, torch.int64, (rot // 2,))
-    _check_words("positions", positions, torch.int32, (b, n))
-    h2, second = 0, (None, None, None, None)
-    if x2 is not None:
+    device = _device_of(x, x2, phase, positions, out, out2)
+    if phase is None:
+        raise ValueError("phase: the table of rotary_phase() is needed")
+    _check("phase", phase, (rot // 2,), torch.int64, True)
+    if positions is not None:
+        _check("positions", positions, (b, n), torch.int32, True)
+    if out is None:
+        out = torch.empty_like(x)
+    else:
+        _check("out", out, x.shape, x.dtype)
+    if x2 is None:
+        keep, (sX, sY) = _strides(x, out)
+        second, h2 = (None, None, None, None), 0
+    else:
         h2 = x2.shape[1]
-        _check_shape("x2", x2, (b, h2, n, d), x.dtype)
-        out2 = torch.empty_like(x2) if out2 is None else out2
-        _check_shape("out2", out2, (b, h2, n, d), x.dtype)
-        second = (x2.data_ptr(), _strides(x2), out2.data_ptr(), _strides(out2))
+        _check("x2", x2, (b, h2, n, d), x.dtype)
+        if out2 is None:
+            out2 = torch.empty_like(x2)
+        else:
+            _check("out2", out2, x2.shape, x2.dtype)
+        keep, (sX, sY, sX2, sY2) = _strides(x, out, x2, out2)
+        second = (x2.data_ptr(), sX2, out2.data_ptr(), sY2)
     code = dtype_code(x)
-    st = _on(device, lambda: lib().linformer_rotary(
-        x.data_ptr(), _strides(x), out.data_ptr(), _strides(out), h, *second, h2, _ptr(phase),
-        _ptr(positions), start, b, n, d, rot, layout, amplitude, int(inverse), code,
-        _stream_handle(stream)))
-    if st != 0:
-        raise LinformerError(st, "linformer_rotary")
+    _launch(device, stream, "linformer_rotary", lambda s: lib().linformer_rotary(
+        x.data_ptr(), sX, out.data_ptr(), sY, h, *second, h2, phase.data_ptr(), _ptr(positions),
+        start, b, n, d, rot, layout, amplitude, 1 if inverse else 0, code, s))
     return out if x2 is None else (out, out2)
