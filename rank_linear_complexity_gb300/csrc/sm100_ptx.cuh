@@ -102,33 +102,44 @@ __device__ __forceinline__ bool warp_wait(uint64_t *bar, uint32_t parity, int *s
 // every 64th time: a hop from an arrival to the waiting warp takes 88 cycles, against 600
 // where one lane polls with the hint and hands the result to the others.
 constexpr uint32_t kSpinsPerCheck = 64;
-__device__ __forceinline__ bool spin_gives_up(uint32_t &spins, uint64_t &t0, int *status, int code,
-                                              volatile int *abort) {
-    if (++spins % kSpinsPerCheck) return false;
-    if (*abort) return true;
-    const uint64_t now = globaltimer();
-    if (spins == kSpinsPerCheck) t0 = now;
-    if (now - t0 <= kWaitLimitNs) return false;
-    *abort = 1;
-    if (status) atomicExch(status, code);
-    return true;
+// (Out of line: the code of a wait is at most a few instructions wherever one stands.)
+static __device__ __noinline__ bool thread_spin_on(uint64_t *bar, uint32_t parity, int *status, int code,
+                                            volatile int *abort) {
+    const uint64_t t0 = globaltimer();
+    for (uint32_t spins = 1;; ++spins) {
+        if (mbar_try_wait(bar, parity)) return true;
+        if (spins % kSpinsPerCheck) continue;
+        if (*abort) return false;
+        if (globaltimer() - t0 > kWaitLimitNs) {
+            *abort = 1;
+            if (status) atomicExch(status, code);
+            return false;
+        }
+    }
+}
+static __device__ __noinline__ bool warp_spin_on(uint64_t *bar, uint32_t parity, int *status, int code,
+                                          volatile int *abort) {
+    const uint64_t t0 = globaltimer();
+    for (uint32_t spins = 1;; ++spins) {
+        if (__any_sync(0xffffffffu, mbar_try_wait(bar, parity))) return true;
+        if (spins % kSpinsPerCheck) continue;
+        if (__any_sync(0xffffffffu, *abort != 0)) return false;
+        if (__any_sync(0xffffffffu, globaltimer() - t0 > kWaitLimitNs)) {
+            *abort = 1;
+            if (status) atomicExch(status, code);
+            return false;
+        }
+    }
 }
 __device__ __forceinline__ bool thread_spin(uint64_t *bar, uint32_t parity, int *status, int code,
                                             volatile int *abort) {
-    uint32_t spins = 0;
-    uint64_t t0 = 0;
-    while (!mbar_try_wait(bar, parity))
-        if (spin_gives_up(spins, t0, status, code, abort)) return false;
-    return true;
+    return mbar_try_wait(bar, parity) || thread_spin_on(bar, parity, status, code, abort);
 }
 // Every lane of a converged warp; the vote gives all of them the same answer.
 __device__ __forceinline__ bool warp_spin(uint64_t *bar, uint32_t parity, int *status, int code,
                                           volatile int *abort) {
-    uint32_t spins = 0;
-    uint64_t t0 = 0;
-    while (!__any_sync(0xffffffffu, mbar_try_wait(bar, parity)))
-        if (__any_sync(0xffffffffu, spin_gives_up(spins, t0, status, code, abort))) return false;
-    return true;
+    return __any_sync(0xffffffffu, mbar_try_wait(bar, parity)) ||
+           warp_spin_on(bar, parity, status, code, abort);
 }
 
 // Non-blocking probe of phase `parity` of `bar`.

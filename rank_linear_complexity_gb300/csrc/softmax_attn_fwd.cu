@@ -286,74 +286,90 @@ softmax_attn_fwd_kernel(const __grid_constant__ CUtensorMap tQ, const __grid_con
             const uint64_t dq = sdesc(smem_u32(sQ + t * C::kTileBytes), 16, 1024, kSwizzle128B);
             const uint32_t tS = tmem + C::kS + 128 * t, tP = tmem + C::kP + C::kPStep * t,
                            tO = tmem + C::kO + DP * t;
-            int ring = 0, nfix = 0, n = 0, items = 0;  // ring entries, fixed blocks, tile's blocks and items
+            // The ring's entries in pairs, K and V of a block: where the next K and the next V
+            // stand (counted up, not divided out: this thread's own instructions are on the
+            // path from one product to the next).
+            constexpr int kPairs = C::kStages / 2;
+            struct At {
+                int s = 0;
+                uint32_t parity = 0;
+                __device__ __forceinline__ void next() {
+                    if (++s == kPairs) {
+                        s = 0;
+                        parity ^= 1u;
+                    }
+                }
+            } ak, av;
+            const uint64_t dk0 = sdesc(smem_u32(sKV), 16, 1024, kSwizzle128B),
+                           dv0 = sdesc(smem_u32(sKV) + C::kTileBytes, 16384, 1024, kSwizzle128B);
+            int nfix = 0, n = 0, items = 0;  // fixed blocks, the tile's blocks and items
             bool ok = true;
-            auto landed = [&](int r) {
-                return thread_spin(&bar->full[r % C::kStages], (r / C::kStages) & 1, p.status, 73, abort_flag);
-            };
             for (int64_t idx = blockIdx.x; idx < p.items && ok; idx += gridDim.x) {
                 const Item it = load_item(p, idx);
                 const int lo = t ? it.t[1].lo : it.t[0].lo, hi = t ? it.t[1].hi : it.t[0].hi;
                 const bool fix = ragged_end(it, p.nk);
-                // S of block j (K in ring entry r): once the last S has been read and, with P
-                // over S, its product is done
-                auto score = [&](int j, int r) {
-                    if (!landed(r)) return false;
+                int ns = n;  // blocks of the tile whose S has been issued
+                // S of block j: once the last S has been read and, with P over S, its product
+                // is done
+                auto score = [&](int j) {
+                    uint64_t *full = &bar->full[2 * ak.s], *empty = &bar->empty[2 * ak.s];
+                    if (!thread_spin(full, ak.parity, p.status, 73, abort_flag)) return false;
+                    const uint64_t k = dk0 + (uint64_t)(ak.s * (int)(2 * C::kTileBytes >> 4));
+                    ak.next();
                     if (j < lo || j >= hi) {
-                        mbar_arrive(&bar->empty[r % C::kStages]);
+                        mbar_arrive(empty);
                         return true;
                     }
-                    const int nt = n + (j - lo);
                     if (j == lo && !thread_spin(&bar->q_full[t], items & 1, p.status, 74, abort_flag)) return false;
-                    if (nt > 0 && !thread_spin(C::kSep ? &bar->s_free[t] : &bar->pv_done[t], (nt - 1) & 1,
-                                             p.status, 75, abort_flag))
+                    if (ns > 0 && !thread_spin(C::kSep ? &bar->s_free[t] : &bar->pv_done[t], (ns - 1) & 1,
+                                               p.status, 75, abort_flag))
                         return false;
+                    ++ns;
                     tc_fence_after();
-                    const uint64_t k = sdesc(smem_u32(sKV + r % C::kStages * C::kTileBytes), 16, 1024, kSwizzle128B);
 #pragma unroll
                     for (int x = 0; x < DP / 16; ++x) {
                         const uint64_t off = (uint64_t)((x >> 2) * 1024 + (x & 3) * 2);
                         mma_ss(tS, dq + off, k + off, idesc_s, x > 0 ? 1u : 0u);
                     }
                     mma_commit(&bar->s_full[t]);
-                    mma_commit(&bar->empty[r % C::kStages]);
+                    mma_commit(empty);
                     if (j == hi - 1) mma_commit(&bar->q_free[t]);
                     return true;
                 };
-                // O += P.V of block j (V in ring entry r)
-                auto output = [&](int j, int r) {
-                    if (!landed(r)) return false;
+                // O += P.V of block j
+                auto output = [&](int j) {
+                    uint64_t *full = &bar->full[2 * av.s + 1], *empty = &bar->empty[2 * av.s + 1];
+                    if (!thread_spin(full, av.parity, p.status, 76, abort_flag)) return false;
+                    const uint64_t v = dv0 + (uint64_t)(av.s * (int)(2 * C::kTileBytes >> 4));
+                    av.next();
                     if (fix && j == it.hi - 1) {
                         if (t == 0) mbar_arrive(&bar->fix_wanted);
                         if (!thread_spin(&bar->fixed, nfix++ & 1, p.status, 77, abort_flag)) return false;
                     }
                     if (j < lo || j >= hi) {
-                        mbar_arrive(&bar->empty[r % C::kStages]);
+                        mbar_arrive(empty);
                         return true;
                     }
-                    if (!thread_spin(&bar->p_full[t], (n + (j - lo)) & 1, p.status, 78, abort_flag)) return false;
+                    if (!thread_spin(&bar->p_full[t], n & 1, p.status, 78, abort_flag)) return false;
+                    ++n;
                     if (j == lo && items > 0 &&
                         !thread_spin(&bar->o_free[t], (items - 1) & 1, p.status, 79, abort_flag))
                         return false;
                     tc_fence_after();
-                    const uint64_t v = sdesc(smem_u32(sKV + r % C::kStages * C::kTileBytes), 16384, 1024, kSwizzle128B);
 #pragma unroll
                     for (int x = 0; x < 8; ++x)
                         mma_ts(tO, tP + 8 * x, v + (uint64_t)(128 * x), idesc_o, (j > lo || x > 0) ? 1u : 0u);
                     mma_commit(&bar->pv_done[t]);
-                    mma_commit(&bar->empty[r % C::kStages]);
+                    mma_commit(empty);
                     return true;
                 };
-                if (it.hi > it.lo) ok = score(it.lo, ring);
-                for (int j = it.lo; j < it.hi && ok; ++j, ring += 2) {
-                    const bool more = j + 1 < it.hi;
-                    if (C::kSep) ok = (!more || score(j + 1, ring + 2)) && output(j, ring + 1);
-                    else ok = output(j, ring + 1) && (!more || score(j + 1, ring + 2));
+                // P beside S: S(j + 1) before O(j); P over S: after it
+                if (C::kSep && it.hi > it.lo) ok = score(it.lo);
+                for (int j = it.lo; j < it.hi && ok; ++j) {
+                    if (C::kSep) ok = (j + 1 >= it.hi || score(j + 1)) && output(j);
+                    else ok = score(j) && output(j);
                 }
-                if (hi > lo) {
-                    n += hi - lo;
-                    ++items;
-                }
+                if (hi > lo) ++items;
             }
             mma_commit(&bar->drain[t]);
             mbar_wait_drain(&bar->drain[t], 0);
@@ -409,6 +425,18 @@ softmax_attn_fwd_kernel(const __grid_constant__ CUtensorMap tQ, const __grid_con
                     if (lane == 0) mbar_arrive(&bar->p_full[t]);
                     continue;
                 }
+                // Masked keys (whatever they hold) become -inf in place, in a rolled loop: the
+                // few blocks at a mask's edge must not widen the code of the others.
+                const int k0 = j * kTile;
+                if (__any_sync(0xffffffffu, first > k0 || end < k0 + kTile)) {
+#pragma unroll 1
+                    for (int c = 0; c < kTile; c += 32) {
+                        uint32_t w[32];
+                        tmem_ld32(tS + c, w);
+                        mask_chunk(w, first - k0 - c, first < end ? end - first : 0);
+                        tmem_st32(tS + c, w);
+                    }
+                }
                 uint32_t v[4][32];
 #pragma unroll
                 for (int c = 0; c < 4; ++c) tmem_ld32_async(tS + 32 * c, v[c]);
@@ -420,12 +448,6 @@ softmax_attn_fwd_kernel(const __grid_constant__ CUtensorMap tQ, const __grid_con
                     tc_fence_before();
                     __syncwarp();
                     if (lane == 0) mbar_arrive(&bar->s_free[t]);
-                }
-                const int k0 = j * kTile;
-                if (__any_sync(0xffffffffu, first > k0 || end < k0 + kTile)) {
-#pragma unroll
-                    for (int c = 0; c < 4; ++c)
-                        mask_chunk(v[c], first - k0 - 32 * c, first < end ? end - first : 0);
                 }
                 const float mx = fmaxf(fmaxf(max_chunk(v[0]), max_chunk(v[1])),
                                        fmaxf(max_chunk(v[2]), max_chunk(v[3])));
