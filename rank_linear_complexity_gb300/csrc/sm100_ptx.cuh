@@ -104,11 +104,9 @@ __device__ __forceinline__ bool warp_wait(uint64_t *bar, uint32_t parity, int *s
 constexpr uint32_t kSpinsPerCheck = 64;
 // (Out of line: the code of a wait is at most a few instructions wherever one stands.)
 static __device__ __noinline__ bool thread_spin_on(uint64_t *bar, uint32_t parity, int *status, int code,
-                                            volatile int *abort) {
+                                                   volatile int *abort) {
     const uint64_t t0 = globaltimer();
-    for (uint32_t spins = 1;; ++spins) {
-        if (mbar_try_wait(bar, parity)) return true;
-        if (spins % kSpinsPerCheck) continue;
+    while (!mbar_try_wait_sleep(bar, parity)) {
         if (*abort) return false;
         if (globaltimer() - t0 > kWaitLimitNs) {
             *abort = 1;
@@ -116,13 +114,12 @@ static __device__ __noinline__ bool thread_spin_on(uint64_t *bar, uint32_t parit
             return false;
         }
     }
+    return true;
 }
 static __device__ __noinline__ bool warp_spin_on(uint64_t *bar, uint32_t parity, int *status, int code,
-                                          volatile int *abort) {
+                                                 volatile int *abort) {
     const uint64_t t0 = globaltimer();
-    for (uint32_t spins = 1;; ++spins) {
-        if (__any_sync(0xffffffffu, mbar_try_wait(bar, parity))) return true;
-        if (spins % kSpinsPerCheck) continue;
+    while (!__any_sync(0xffffffffu, mbar_try_wait_sleep(bar, parity))) {
         if (__any_sync(0xffffffffu, *abort != 0)) return false;
         if (__any_sync(0xffffffffu, globaltimer() - t0 > kWaitLimitNs)) {
             *abort = 1;
@@ -130,6 +127,7 @@ static __device__ __noinline__ bool warp_spin_on(uint64_t *bar, uint32_t parity,
             return false;
         }
     }
+    return true;
 }
 __device__ __forceinline__ bool thread_spin(uint64_t *bar, uint32_t parity, int *status, int code,
                                             volatile int *abort) {
@@ -417,6 +415,18 @@ __device__ __forceinline__ void tmem_ld8(uint32_t taddr, uint32_t (&v)[8]) {
         "tcgen05.wait::ld.sync.aligned;"
         : "=r"(v[0]), "=r"(v[1]), "=r"(v[2]), "=r"(v[3]), "=r"(v[4]), "=r"(v[5]), "=r"(v[6]),
           "=r"(v[7])
+        : "r"(taddr)
+        : "memory");
+}
+// 16 consecutive fp32 columns of this warp's 32 TMEM lanes -> v[0..15] (load + wait).
+__device__ __forceinline__ void tmem_ld16(uint32_t taddr, uint32_t (&v)[16]) {
+    asm volatile(
+        "tcgen05.ld.sync.aligned.32x32b.x16.b32 "
+        "{%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15}, [%16];\n\t"
+        "tcgen05.wait::ld.sync.aligned;"
+        : "=r"(v[0]), "=r"(v[1]), "=r"(v[2]), "=r"(v[3]), "=r"(v[4]), "=r"(v[5]), "=r"(v[6]),
+          "=r"(v[7]), "=r"(v[8]), "=r"(v[9]), "=r"(v[10]), "=r"(v[11]), "=r"(v[12]),
+          "=r"(v[13]), "=r"(v[14]), "=r"(v[15])
         : "r"(taddr)
         : "memory");
 }

@@ -17,9 +17,11 @@
 // partial dQ through memory in a fixed order.  P and dS are rounded to bf16 as operands
 // (relative 2^-9, in sums of many terms); sums are fp32 in tensor memory.
 //
-// Roles, both kernels: warps 0-3 and 4-7 each take 64 of the 128 columns, one thread a row;
-// warp 8 loads (lane 0) and zeroes rows past the valid length (lanes 1-31, where 0 x NaN
-// would reach a sum); one thread of warp 9 issues the products.
+// Roles, both kernels: warps 0-15 do the arithmetic, four warps for each 32 of a tile's 128
+// columns, one thread a row (four such warps a scheduler hide one another's latencies);
+// warp 16 loads (lane 0) and zeroes rows past the valid length (lanes 1-31, where 0 x NaN
+// would reach a sum); one thread each of warps 17 and 18 issues products, so that a chain of
+// products that waits for arithmetic does not hold up the other one.
 #include <algorithm>
 #include <cmath>
 
@@ -32,12 +34,8 @@ namespace {
 
 using namespace ptx;
 
-// Twelve warps (two idle), 168 registers each at launch; the two warpgroups that do the
-// arithmetic take registers from the third: 2 x 200 + 104 = 3 x 168.
-constexpr int kThreads = 384;
-constexpr uint32_t kMathRegs = 200, kIssueRegs = 104;
-static_assert(2 * kMathRegs + kIssueRegs == 3 * 168, "register split");
-constexpr int kLoadWarp = 8, kMmaWarp = 9;
+constexpr int kThreads = 640;  // 96 registers each; the last warp is idle
+constexpr int kMathWarps = 16, kLoadWarp = 16, kMmaWarp = 17;
 constexpr float kLog2e = 1.4426950408889634f;
 
 struct BwdParams {
@@ -47,7 +45,9 @@ struct BwdParams {
     __nv_bfloat16 *dQ, *dK, *dV;
     Strides sdQ, sdK, sdV;
     const float *lse;
-    float *rows;  // [b][hq][query tiles][2][128]: lse log2(e) and delta; dead rows +inf and 0
+    // [b][hq][query tiles][2][128]: -lse log2(e) and -delta, as they are added; -inf and 0 for
+    // rows that are past the length or see no key
+    float *rows;
     int b, hq, hk, group, nq, nk, d, causal, window;
     int qtiles, kblocks;
     int64_t items;
@@ -55,11 +55,16 @@ struct BwdParams {
     int *status;
 };
 
-// 16 packed words of the thread's row to tensor memory, and the row's tail in a store.
-__device__ __forceinline__ void store_row(__nv_bfloat16 *dst, const uint32_t (&o)[32], int c, int d,
+// Products of two pairs of bf16, added in fp32.
+__device__ __forceinline__ float dot2(uint32_t a, uint32_t b) {
+    return __uint_as_float(a << 16) * __uint_as_float(b << 16) +
+           __uint_as_float(a & 0xffff0000u) * __uint_as_float(b & 0xffff0000u);
+}
+// 16 columns of a row, scaled and rounded (columns from d on do not exist).
+__device__ __forceinline__ void store_row(__nv_bfloat16 *dst, const uint32_t (&o)[16], int c, int d,
                                           float f, bool zero) {
 #pragma unroll
-    for (int e = 0; e < 32; e += 8) {
+    for (int e = 0; e < 16; e += 8) {
         if (c + e >= d) break;
         uint4 w = make_uint4(0u, 0u, 0u, 0u);
         if (!zero) {
@@ -82,15 +87,15 @@ __device__ __forceinline__ void mma_scores(uint32_t d, uint32_t a, uint32_t b) {
         mma_ss(d, da + off, db + off, idesc, x > 0 ? 1u : 0u);
     }
 }
-// D (128 x DP) += A (128 x 128, packed in tensor memory: columns [0, 32) hold the first 64,
-// [64, 96) the others) . B (128 rows of DP)
+// D (128 x DP) += A (128 x 128, packed in tensor memory: 32 elements in 16 columns at the
+// start of each 32) . B (128 rows of DP)
 template <int DP>
 __device__ __forceinline__ void mma_sum(uint32_t d, uint32_t a, uint32_t b, uint32_t acc) {
     const uint32_t idesc = idesc_f16(128, DP, 1, 0, 1);
     const uint64_t db = sdesc(b, 16384, 1024, kSwizzle128B);
 #pragma unroll
     for (int x = 0; x < 8; ++x)
-        mma_ts(d, a + (x >> 2) * 64 + (x & 3) * 8, db + (uint64_t)(128 * x), idesc,
+        mma_ts(d, a + (x >> 1) * 32 + (x & 1) * 8, db + (uint64_t)(128 * x), idesc,
                (acc || x > 0) ? 1u : 0u);
 }
 
@@ -107,7 +112,7 @@ struct DqLayout {
     static constexpr uint32_t kTileBytes = kTile * DP * 2;
     static constexpr int kStages = DP == 64 ? 8 : 5;
     static constexpr uint32_t kS = 0, kDp = 128, kDq = 384;
-    static constexpr uint32_t kSmem = 1024 + (2 + kStages) * kTileBytes + 512;
+    static constexpr uint32_t kSmem = 1024 + (2 + kStages) * kTileBytes + 512 + 1024;
 };
 struct DqItem {
     int batch, head, q0, lo, hi;
@@ -137,11 +142,16 @@ __device__ __forceinline__ DqItem dq_item(const BwdParams &p, int64_t idx) {
 
 struct DqBarriers {
     uint64_t q_full, q_free, s_full, s_free, dp_full[2], ds_full[2], dq_done[2], acc_free;
-    uint64_t fix_wanted, fixed, drain;
-    uint64_t full[8], empty[8];
+    uint64_t fix_wanted, fixed, drain[2];
+    uint64_t full[8], empty[8], rows_ready;
     uint32_t tmem;
     int abort;
+    // -lse and -delta of the item's rows (a warp that writes the next item's has seen all warps
+    // past this item's last block, so past their reading)
+    float rows[2 * kTile];
 };
+
+static_assert(sizeof(DqBarriers) <= 512 + 1024, "room for the barriers");
 
 template <int DP>
 __global__ void __launch_bounds__(kThreads, 1)
@@ -160,16 +170,18 @@ softmax_attn_dq_kernel(const __grid_constant__ CUtensorMap tQ, const __grid_cons
         mbar_init(&bar->q_full, 1);
         mbar_init(&bar->q_free, 1);
         mbar_init(&bar->s_full, 1);
-        mbar_init(&bar->s_free, 8);
+        mbar_init(&bar->s_free, kMathWarps);
         for (int i = 0; i < 2; ++i) {
             mbar_init(&bar->dp_full[i], 1);
-            mbar_init(&bar->ds_full[i], 8);
+            mbar_init(&bar->ds_full[i], kMathWarps);
             mbar_init(&bar->dq_done[i], 1);
         }
-        mbar_init(&bar->acc_free, 8);
+        mbar_init(&bar->rows_ready, kMathWarps);
+        mbar_init(&bar->acc_free, kMathWarps);
         mbar_init(&bar->fix_wanted, 1);
         mbar_init(&bar->fixed, 31);
-        mbar_init(&bar->drain, 1);
+        mbar_init(&bar->drain[0], 1);
+        mbar_init(&bar->drain[1], 1);
         for (int s = 0; s < C::kStages; ++s) {
             mbar_init(&bar->full[s], 1);
             mbar_init(&bar->empty[s], 1);
@@ -187,7 +199,6 @@ softmax_attn_dq_kernel(const __grid_constant__ CUtensorMap tQ, const __grid_cons
     const uint32_t tmem = bar->tmem;
     // ring entry 2 j + kv of an item: K (kv = 0) and V of its j-th block
     if (warp >= kLoadWarp) {
-    setmaxnreg_dec<kIssueRegs>();
     if (warp == kLoadWarp) {
         if (lane == 0) {
             int ring = 0, nq = 0;
@@ -234,7 +245,7 @@ softmax_attn_dq_kernel(const __grid_constant__ CUtensorMap tQ, const __grid_cons
         }
         __syncwarp();
     } else if (warp == kMmaWarp) {
-        if (elect_one()) {
+        if (elect_one()) {  // S and dP
             int ring = 0, items = 0, n = 0, nfix = 0;
             bool ok = true;
             const uint32_t aQ = smem_u32(sQ), adO = smem_u32(sdO), aKV = smem_u32(sKV);
@@ -243,158 +254,161 @@ softmax_attn_dq_kernel(const __grid_constant__ CUtensorMap tQ, const __grid_cons
                 const int blocks = it.hi - it.lo;
                 if (blocks <= 0) continue;
                 const bool fix = it.sp.Lk < p.nk && it.hi * kTile > it.sp.Lk;
-                // S and dP of the item's block j: n + j blocks of this CTA came before
-                auto score = [&](int j) {
-                    const int r = ring + 2 * j, s = r % C::kStages;
-                    if (!thread_spin(&bar->full[s], (r / C::kStages) & 1, p.status, 86, abort_flag)) return false;
-                    if (fix && j == blocks - 1) {
+                ok = thread_spin(&bar->q_full, items & 1, p.status, 91, abort_flag);
+                for (int j = 0; j < blocks && ok; ++j, ++n, ring += 2) {
+                    int s = ring % C::kStages;
+                    ok = thread_spin(&bar->full[s], (ring / C::kStages) & 1, p.status, 86, abort_flag);
+                    if (ok && fix && j == blocks - 1) {
                         mbar_arrive(&bar->fix_wanted);
-                        if (!thread_spin(&bar->fixed, nfix & 1, p.status, 87, abort_flag)) return false;
-                        ++nfix;
+                        ok = thread_spin(&bar->fixed, nfix++ & 1, p.status, 87, abort_flag);
                     }
-                    if (n + j > 0 && !thread_spin(&bar->s_free, (n + j - 1) & 1, p.status, 88, abort_flag))
-                        return false;
+                    ok = ok && (n == 0 || thread_spin(&bar->s_free, (n - 1) & 1, p.status, 88, abort_flag));
+                    if (!ok) break;
                     tc_fence_after();
                     mma_scores<DP>(tmem + C::kS, aQ, aKV + s * C::kTileBytes);
                     mma_commit(&bar->s_full);
-                    return true;
-                };
-                auto dprob = [&](int j) {
-                    const int r = ring + 2 * j + 1, s = r % C::kStages, k = n + j;
-                    if (!thread_spin(&bar->full[s], (r / C::kStages) & 1, p.status, 89, abort_flag)) return false;
-                    if (k >= 2 && !thread_spin(&bar->dq_done[k & 1], ((k >> 1) - 1) & 1, p.status, 90, abort_flag))
-                        return false;
+                    s = (ring + 1) % C::kStages;
+                    ok = thread_spin(&bar->full[s], ((ring + 1) / C::kStages) & 1, p.status, 89, abort_flag) &&
+                         (n < 2 || thread_spin(&bar->dq_done[n & 1], ((n >> 1) - 1) & 1, p.status, 90, abort_flag));
+                    if (!ok) break;
                     tc_fence_after();
-                    mma_scores<DP>(tmem + C::kDp + 128 * (k & 1), adO, aKV + s * C::kTileBytes);
-                    mma_commit(&bar->dp_full[k & 1]);
+                    mma_scores<DP>(tmem + C::kDp + 128 * (n & 1), adO, aKV + s * C::kTileBytes);
+                    mma_commit(&bar->dp_full[n & 1]);
                     mma_commit(&bar->empty[s]);
-                    return true;
-                };
-                ok = thread_spin(&bar->q_full, items & 1, p.status, 91, abort_flag) && score(0) && dprob(0);
-                for (int j = 0; j < blocks && ok; ++j) {
-                    if (j + 1 < blocks && !(score(j + 1) && dprob(j + 1))) {
-                        ok = false;
-                        break;
-                    }
-                    if (j + 1 >= blocks) mma_commit(&bar->q_free);  // the item's last use of Q and dO
-                    const int k = n + j, s = (ring + 2 * j) % C::kStages;
-                    ok = thread_spin(&bar->ds_full[k & 1], (k >> 1) & 1, p.status, 92, abort_flag) &&
+                }
+                mma_commit(&bar->q_free);
+                ++items;
+            }
+            mma_commit(&bar->drain[0]);
+            mbar_wait_drain(&bar->drain[0], 0);
+        }
+        __syncwarp();
+    } else if (warp == kMmaWarp + 1) {
+        if (elect_one()) {  // dQ
+            int ring = 0, items = 0, n = 0;
+            bool ok = true;
+            const uint32_t aKV = smem_u32(sKV);
+            for (int64_t idx = blockIdx.x; idx < p.items && ok; idx += gridDim.x) {
+                const DqItem it = dq_item(p, idx);
+                const int blocks = it.hi - it.lo;
+                if (blocks <= 0) continue;
+                for (int j = 0; j < blocks && ok; ++j, ++n, ring += 2) {
+                    // (dS says that S has been formed, so the block of K has landed)
+                    ok = thread_spin(&bar->ds_full[n & 1], (n >> 1) & 1, p.status, 92, abort_flag) &&
                          (j > 0 || items == 0 ||
                           thread_spin(&bar->acc_free, (items - 1) & 1, p.status, 93, abort_flag));
                     if (!ok) break;
                     tc_fence_after();
-                    mma_sum<DP>(tmem + C::kDq, tmem + C::kDp + 128 * (k & 1), aKV + s * C::kTileBytes,
+                    const int s = ring % C::kStages;
+                    mma_sum<DP>(tmem + C::kDq, tmem + C::kDp + 128 * (n & 1), aKV + s * C::kTileBytes,
                                 j > 0 ? 1u : 0u);
-                    mma_commit(&bar->dq_done[k & 1]);
+                    mma_commit(&bar->dq_done[n & 1]);
                     mma_commit(&bar->empty[s]);
                 }
-                n += blocks;
-                ring += 2 * blocks;
                 ++items;
             }
-            mma_commit(&bar->drain);
-            mbar_wait_drain(&bar->drain, 0);
+            mma_commit(&bar->drain[1]);
+            mbar_wait_drain(&bar->drain[1], 0);
         }
         __syncwarp();
     }
     } else {
-    setmaxnreg_inc<kMathRegs>();
-        const int w = warp >> 2, row = tid & 127;  // column half, row
+        const int w = warp >> 2, row = tid & 127;  // 32 columns, row
         const uint32_t lanes = (uint32_t)((warp & 3) * 32) << 16;
         const float sl = p.scale_log2;
-        int n = 0;
+        int n = 0, items = 0;
         for (int64_t idx = blockIdx.x; idx < p.items; idx += gridDim.x) {
             const DqItem it = dq_item(p, idx);
-            const int i = it.q0 + row;
-            const bool exists = i < p.nq, valid = i < it.sp.Lq;
-            // delta_i = dO_i.O_i, and the row's entry for the other kernel
-            float delta = 0.f, lse2 = INFINITY;
-            if (valid) {
-                const uint4 *o = reinterpret_cast<const uint4 *>(p.O + it.batch * p.sO.b + it.head * p.sO.h +
-                                                                 (int64_t)i * p.sO.n);
-                const uint4 *g = reinterpret_cast<const uint4 *>(p.dO + it.batch * p.sdO.b +
-                                                                 it.head * p.sdO.h + (int64_t)i * p.sdO.n);
-                const float x = p.lse[((int64_t)it.batch * p.hq + it.head) * p.nq + i];
-                for (int c = 0; c < p.d / 8; ++c) {
-                    float a[8], b[8];
-                    unpack8(__ldg(o + c), a);
-                    unpack8(__ldg(g + c), b);
+            const int lo = it.lo, hi = it.hi;
+            // -lse and -delta of eight rows a warp (rows read by whole warps, 8 bytes a lane),
+            // for this kernel through shared memory and for the other one.
+            float *sm = bar->rows;
+            {
+                const __nv_bfloat16 *o = p.O + it.batch * p.sO.b + it.head * p.sO.h + 4 * lane;
+                const __nv_bfloat16 *g = p.dO + it.batch * p.sdO.b + it.head * p.sdO.h + 4 * lane;
+                const int r0 = it.q0 + 8 * warp;
+                uint2 a[8], b[8];
 #pragma unroll
-                    for (int e = 0; e < 8; ++e) delta = fmaf(a[e], b[e], delta);
+                for (int r = 0; r < 8; ++r) {
+                    a[r] = b[r] = make_uint2(0u, 0u);
+                    if (r0 + r < it.sp.Lq && 4 * lane < p.d) {
+                        a[r] = __ldg(reinterpret_cast<const uint2 *>(o + (int64_t)(r0 + r) * p.sO.n));
+                        b[r] = __ldg(reinterpret_cast<const uint2 *>(g + (int64_t)(r0 + r) * p.sdO.n));
+                    }
                 }
-                if (x != -INFINITY) lse2 = x * kLog2e;
-                else delta = 0.f;
+                float x = -INFINITY, del = 0.f;
+                if (lane < 8 && r0 + lane < it.sp.Lq)
+                    x = __ldg(p.lse + ((int64_t)it.batch * p.hq + it.head) * p.nq + r0 + lane);
+#pragma unroll
+                for (int r = 0; r < 8; ++r) {
+                    float y = dot2(a[r].x, b[r].x) + dot2(a[r].y, b[r].y);
+#pragma unroll
+                    for (int k = 16; k; k >>= 1) y += __shfl_xor_sync(0xffffffffu, y, k);
+                    if (lane == r) del = y;
+                }
+                if (lane < 8) {
+                    const float nl = x == -INFINITY ? -INFINITY : -x * kLog2e, nd = x == -INFINITY ? 0.f : -del;
+                    float *dst = p.rows + (((int64_t)it.batch * p.hq + it.head) * p.qtiles + it.q0 / kTile) * 256;
+                    dst[8 * warp + lane] = sm[8 * warp + lane] = nl;
+                    dst[128 + 8 * warp + lane] = sm[128 + 8 * warp + lane] = nd;
+                }
             }
-            if (w == 0) {
-                float *dst = p.rows + (((int64_t)it.batch * p.hq + it.head) * p.qtiles + it.q0 / kTile) * 256;
-                dst[row] = lse2;
-                dst[128 + row] = delta;
+            float nl = -INFINITY, nd = 0.f;
+            if (it.hi > it.lo) {
+                __syncwarp();
+                if (lane == 0) mbar_arrive(&bar->rows_ready);
+                if (!warp_spin(&bar->rows_ready, items & 1, p.status, 97, abort_flag)) break;
+                nl = sm[row];
+                nd = sm[128 + row];
+                ++items;
             }
-            const int first = valid ? it.sp.first(i) : 0, end = valid ? it.sp.end(i) : 0;
+            const bool seen = it.q0 + row < it.sp.Lq;
+            const int first = seen ? it.sp.first(it.q0 + row) : 0, end = seen ? it.sp.end(it.q0 + row) : 0;
+            const unsigned width = end > first ? (unsigned)(end - first) : 0u;
             bool ok = true;
-            for (int j = it.lo; j < it.hi; ++j, ++n) {
+            for (int j = lo; j < hi; ++j, ++n) {
                 if (!warp_spin(&bar->s_full, n & 1, p.status, 94, abort_flag)) {
                     ok = false;
                     break;
                 }
                 tc_fence_after();
-                uint32_t v[2][32];
-                tmem_ld32_async(tmem + C::kS + 64 * w + lanes, v[0]);
-                tmem_ld32_async(tmem + C::kS + 64 * w + 32 + lanes, v[1]);
-                tmem_wait_ld(v[0]);
-                tie32(v[1]);
+                uint32_t v[32];
+                tmem_ld32(tmem + C::kS + 32 * w + lanes, v);
                 tc_fence_before();
                 __syncwarp();
                 if (lane == 0) mbar_arrive(&bar->s_free);
-                const float2 sl2 = make_float2(sl, sl), off2 = make_float2(-lse2, -lse2);
+                const float2 sl2 = make_float2(sl, sl), off2 = make_float2(nl, nl);
 #pragma unroll
-                for (int c = 0; c < 2; ++c)
-#pragma unroll
-                    for (int e = 0; e < 32; e += 2) {
-                        const float2 y = ffma2(make_float2(__uint_as_float(v[c][e]), __uint_as_float(v[c][e + 1])),
-                                               sl2, off2);
-                        v[c][e] = __float_as_uint(ex2_approx(y.x));
-                        v[c][e + 1] = __float_as_uint(ex2_approx(y.y));
-                    }
-                const uint32_t tD = tmem + C::kDp + 128 * (n & 1) + 64 * w + lanes;
+                for (int e = 0; e < 32; e += 2) {
+                    const float2 y = ffma2(make_float2(__uint_as_float(v[e]), __uint_as_float(v[e + 1])), sl2, off2);
+                    v[e] = __float_as_uint(ex2_approx(y.x));
+                    v[e + 1] = __float_as_uint(ex2_approx(y.y));
+                }
+                const uint32_t tD = tmem + C::kDp + 128 * (n & 1) + 32 * w + lanes;
                 if (!warp_spin(&bar->dp_full[n & 1], (n >> 1) & 1, p.status, 95, abort_flag)) {
                     ok = false;
                     break;
                 }
                 tc_fence_after();
-                uint32_t u[2][32];
-                tmem_ld32_async(tD, u[0]);
-                tmem_ld32_async(tD + 32, u[1]);
-                tmem_wait_ld(u[0]);
-                tie32(u[1]);
-                const int k0 = j * kTile + 64 * w;
-                const float2 nd = make_float2(-delta, -delta);
+                const int k0 = j * kTile + 32 * w;
+                const float2 nd2 = make_float2(nd, nd);
+                const bool masked = __any_sync(0xffffffffu, first > k0 || end < k0 + 32);
+                // 16 columns at a time (registers); dS takes the columns that have been read
 #pragma unroll
-                for (int c = 0; c < 2; ++c)
+                for (int c = 0; c < 32; c += 16) {
+                    uint32_t u[16], o[8];
+                    tmem_ld16(tD + c, u);
 #pragma unroll
-                    for (int e = 0; e < 32; e += 2) {
-                        const float2 y = fadd2(make_float2(__uint_as_float(u[c][e]), __uint_as_float(u[c][e + 1])), nd);
-                        const float2 z = fmul2(make_float2(__uint_as_float(v[c][e]), __uint_as_float(v[c][e + 1])), y);
-                        v[c][e] = __float_as_uint(z.x);
-                        v[c][e + 1] = __float_as_uint(z.y);
+                    for (int e = 0; e < 16; e += 2) {
+                        const float2 y = fadd2(make_float2(__uint_as_float(u[e]), __uint_as_float(u[e + 1])), nd2);
+                        float2 z = fmul2(make_float2(__uint_as_float(v[c + e]), __uint_as_float(v[c + e + 1])), y);
+                        if (masked) {  // keys that take no part, whatever their S and dP hold
+                            if ((unsigned)(c + e - (first - k0)) >= width) z.x = 0.f;
+                            if ((unsigned)(c + e + 1 - (first - k0)) >= width) z.y = 0.f;
+                        }
+                        o[e / 2] = pack2(z.x, z.y);
                     }
-                // masked keys (whatever their S and dP hold) take no part
-                if (__any_sync(0xffffffffu, first > k0 || end < k0 + 64)) {
-                    const int a = first - k0;
-                    const unsigned wd = end > first ? (unsigned)(end - first) : 0u;
-#pragma unroll
-                    for (int c = 0; c < 2; ++c)
-#pragma unroll
-                        for (int e = 0; e < 32; ++e)
-                            if ((unsigned)(32 * c + e - a) >= wd) v[c][e] = 0u;
-                }
-#pragma unroll
-                for (int c = 0; c < 2; ++c) {
-                    uint32_t o[16];
-#pragma unroll
-                    for (int e = 0; e < 16; ++e)
-                        o[e] = pack2(__uint_as_float(v[c][2 * e]), __uint_as_float(v[c][2 * e + 1]));
-                    tmem_st16_async(tD + 16 * c, o);
+                    tmem_st8_async(tD + c / 2, o);
                 }
                 tmem_wait_st();
                 tc_fence_before();
@@ -402,17 +416,23 @@ softmax_attn_dq_kernel(const __grid_constant__ CUtensorMap tQ, const __grid_cons
                 if (lane == 0) mbar_arrive(&bar->ds_full[n & 1]);
             }
             if (!ok) break;
-            const bool some = it.hi > it.lo;
+            const bool some = hi > lo;
             if (some) {
                 if (!warp_spin(&bar->dq_done[(n - 1) & 1], ((n - 1) >> 1) & 1, p.status, 96, abort_flag)) break;
                 tc_fence_after();
             }
-            __nv_bfloat16 *dst = p.dQ + it.batch * p.sdQ.b + it.head * p.sdQ.h + (int64_t)i * p.sdQ.n;
+            // (derived again: kept through the loop, it would cost registers there)
+            int64_t again = idx;
+            asm volatile("" : "+l"(again));
+            const DqItem at = dq_item(p, again);
+            const int i = at.q0 + row;
+            const bool exists = i < p.nq, valid = i < at.sp.Lq;
+            __nv_bfloat16 *dst = p.dQ + at.batch * p.sdQ.b + at.head * p.sdQ.h + (int64_t)i * p.sdQ.n;
 #pragma unroll
-            for (int c = 0; c < DP / 2; c += 32) {
-                uint32_t o[32];
-                const int col = w * (DP / 2) + c;
-                if (some) tmem_ld32(tmem + C::kDq + col + lanes, o);
+            for (int c = 0; c < DP / 4; c += 16) {
+                uint32_t o[16];
+                const int col = w * (DP / 4) + c;
+                if (some) tmem_ld16(tmem + C::kDq + col + lanes, o);
                 if (exists) store_row(dst, o, col, p.d, p.scale, !some || !valid);
             }
             if (some) {
@@ -434,8 +454,13 @@ struct DkvLayout {
     static constexpr uint32_t kTileBytes = kTile * DP * 2;
     static constexpr int kStages = DP == 64 ? 4 : 2;
     static constexpr uint32_t kStageBytes = 2 * kTileBytes + 1024;  // Q, dO, lse and delta
-    static constexpr uint32_t kS = 0, kDp = 128, kDv = 256, kDk = 256 + DP;
-    static constexpr uint32_t kSmem = 1024 + 2 * kTileBytes + kStages * kStageBytes + 512;
+    static constexpr int kKv = DP == 64 ? 2 : 1;  // items whose K and V are held
+    // S and dP of the steps in turn take kBufs buffers of 128 columns: S of step g buffer
+    // 2 g, dP buffer 2 g + 1, modulo kBufs.  Each lives from its product over the arithmetic
+    // to the product that takes its P or dS.
+    static constexpr int kBufs = DP == 64 ? 3 : 2;
+    static constexpr uint32_t kDv = 128 * kBufs, kDk = kDv + DP;
+    static constexpr uint32_t kSmem = 1024 + kKv * 2 * kTileBytes + kStages * kStageBytes + 512;
 };
 struct DkvItem {
     int batch, kvh, k0, lo, hi;  // query tiles [lo, hi) of each head of the group
@@ -463,9 +488,11 @@ __device__ __forceinline__ DkvItem dkv_item(const BwdParams &p, int64_t idx) {
     return it;
 }
 
+// Barriers of steps come in pairs, for even and odd steps: a waiter that falls behind by one
+// step still finds its own phase.
 struct DkvBarriers {
-    uint64_t kv_full, kv_free, s_full, p_full, pv_done, dp_full, ds_full, ds_done, acc_full, acc_free;
-    uint64_t fix_wanted, fixed, drain;
+    uint64_t kv_full[2], kv_free[2], s_full[2], p_full[2], pv_done[2], dp_full[2], ds_full[2], ds_done[2];
+    uint64_t acc_full, acc_free, fix_wanted, fixed[2], drain[2];
     uint64_t full[4], empty[4];
     uint32_t tmem;
     int abort;
@@ -479,7 +506,8 @@ softmax_attn_dkv_kernel(const __grid_constant__ CUtensorMap tQ, const __grid_con
     using C = DkvLayout<DP>;
     extern __shared__ uint8_t raw[];
     uint8_t *smem = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(raw) + 1023) & ~uintptr_t(1023));
-    uint8_t *sK = smem, *sV = smem + C::kTileBytes, *sT = smem + 2 * C::kTileBytes;
+    // K and V of an item at sK + (item % kKv) 2 tiles
+    uint8_t *sK = smem, *sT = smem + C::kKv * 2 * C::kTileBytes;
     // stage s: Q and dO tiles, then (after all tiles) its 1 KB of row values
     uint8_t *sR = sT + C::kStages * 2 * C::kTileBytes;
     DkvBarriers *bar = reinterpret_cast<DkvBarriers *>(sR + C::kStages * 1024);
@@ -487,22 +515,24 @@ softmax_attn_dkv_kernel(const __grid_constant__ CUtensorMap tQ, const __grid_con
     const int tid = threadIdx.x, warp = __shfl_sync(0xffffffffu, tid >> 5, 0), lane = tid & 31;
 
     if (tid == 0) {
-        mbar_init(&bar->kv_full, 1);
-        mbar_init(&bar->kv_free, 1);
-        mbar_init(&bar->s_full, 1);
-        mbar_init(&bar->p_full, 8);
-        mbar_init(&bar->pv_done, 1);
-        mbar_init(&bar->dp_full, 1);
-        mbar_init(&bar->ds_full, 8);
-        mbar_init(&bar->ds_done, 1);
-        mbar_init(&bar->acc_full, 1);
-        mbar_init(&bar->acc_free, 8);
+        for (int i = 0; i < 2; ++i) {
+            mbar_init(&bar->kv_full[i], 1);
+            mbar_init(&bar->kv_free[i], 2);
+            mbar_init(&bar->s_full[i], 1);
+            mbar_init(&bar->p_full[i], kMathWarps);
+            mbar_init(&bar->pv_done[i], 1);
+            mbar_init(&bar->dp_full[i], 1);
+            mbar_init(&bar->ds_full[i], kMathWarps);
+            mbar_init(&bar->ds_done[i], 1);
+            mbar_init(&bar->drain[i], 1);
+            mbar_init(&bar->fixed[i], 31);
+        }
+        mbar_init(&bar->acc_full, 2);
+        mbar_init(&bar->acc_free, kMathWarps);
         mbar_init(&bar->fix_wanted, 1);
-        mbar_init(&bar->fixed, 31);
-        mbar_init(&bar->drain, 1);
         for (int s = 0; s < C::kStages; ++s) {
             mbar_init(&bar->full[s], 1);
-            mbar_init(&bar->empty[s], 1);
+            mbar_init(&bar->empty[s], 2);  // both issuing threads
         }
         bar->abort = 0;
         fence_mbar_init();
@@ -517,7 +547,6 @@ softmax_attn_dkv_kernel(const __grid_constant__ CUtensorMap tQ, const __grid_con
     const uint32_t tmem = bar->tmem;
 
     if (warp >= kLoadWarp) {
-    setmaxnreg_dec<kIssueRegs>();
     if (warp == kLoadWarp) {
         if (lane == 0) {
             int ring = 0, items = 0;
@@ -525,10 +554,14 @@ softmax_attn_dkv_kernel(const __grid_constant__ CUtensorMap tQ, const __grid_con
             for (int64_t idx = blockIdx.x; idx < p.items && ok; idx += gridDim.x) {
                 const DkvItem it = dkv_item(p, idx);
                 if (it.hi <= it.lo) continue;
-                if (items > 0 && !thread_spin(&bar->kv_free, (items - 1) & 1, p.status, 100, abort_flag)) break;
-                mbar_arrive_expect_tx(&bar->kv_full, 2 * C::kTileBytes);
-                load_rows<DP>(sK, &tK, &bar->kv_full, it.k0, 0, it.kvh, it.batch);
-                load_rows<DP>(sV, &tV, &bar->kv_full, it.k0, 0, it.kvh, it.batch);
+                const int kb = items % C::kKv;
+                if (items >= C::kKv &&
+                    !thread_spin(&bar->kv_free[kb], (items / C::kKv - 1) & 1, p.status, 100, abort_flag))
+                    break;
+                uint8_t *kv = sK + kb * 2 * C::kTileBytes;
+                mbar_arrive_expect_tx(&bar->kv_full[kb], 2 * C::kTileBytes);
+                load_rows<DP>(kv, &tK, &bar->kv_full[kb], it.k0, 0, it.kvh, it.batch);
+                load_rows<DP>(kv + C::kTileBytes, &tV, &bar->kv_full[kb], it.k0, 0, it.kvh, it.batch);
                 ++items;
                 for (int g = 0; g < p.group && ok; ++g)
                     for (int j = it.lo; j < it.hi; ++j, ++ring) {
@@ -546,7 +579,8 @@ softmax_attn_dkv_kernel(const __grid_constant__ CUtensorMap tQ, const __grid_con
                         bulk_load(sR + s * 1024, p.rows + (head * p.qtiles + j) * 256, 1024, &bar->full[s]);
                     }
             }
-            if (items > 0) mbar_wait_drain(&bar->kv_full, (items - 1) & 1);
+            for (int i = max(0, items - C::kKv); i < items; ++i)
+                mbar_wait_drain(&bar->kv_full[i % C::kKv], (i / C::kKv) & 1);
             for (int i = max(0, ring - C::kStages); i < ring; ++i)
                 mbar_wait_drain(&bar->full[i % C::kStages], (i / C::kStages) & 1);
         } else {  // Q and dO rows past the valid length: P and dS are 0 there, but 0 x NaN is not
@@ -570,180 +604,191 @@ softmax_attn_dkv_kernel(const __grid_constant__ CUtensorMap tQ, const __grid_con
                     zero_rows<DP>(st, it.sp.Lq - (it.hi - 1) * kTile, lane - 1, 31);
                     zero_rows<DP>(st + C::kTileBytes, it.sp.Lq - (it.hi - 1) * kTile, lane - 1, 31);
                     fence_proxy_async_smem();
-                    mbar_arrive(&bar->fixed);
+                    mbar_arrive(&bar->fixed[(nfix - 1) & 1]);
                 }
             }
         }
         __syncwarp();
-    } else if (warp == kMmaWarp) {
+    } else if (warp == kMmaWarp || warp == kMmaWarp + 1) {
+        const bool first = warp == kMmaWarp;  // S and dV; the other thread: dP and dK
         if (elect_one()) {
             int n = 0, items = 0, nfix = 0;
             bool ok = true;
-            const uint32_t aK = smem_u32(sK), aV = smem_u32(sV), aT = smem_u32(sT);
+            const uint32_t aKV0 = smem_u32(sK) + (first ? 0 : C::kTileBytes), aT = smem_u32(sT);
+            uint64_t *done = first ? bar->pv_done : bar->ds_done, *full = first ? bar->s_full : bar->dp_full,
+                     *ready = first ? bar->p_full : bar->ds_full;
+            auto phase = [](int g) { return (uint32_t)(g >> 1) & 1u; };
+            auto buffer = [&](int g) { return tmem + 128 * ((2 * g + (first ? 0 : 1)) % C::kBufs); };
             for (int64_t idx = blockIdx.x; idx < p.items && ok; idx += gridDim.x) {
                 const DkvItem it = dkv_item(p, idx);
                 const int per = it.hi - it.lo;
                 if (per <= 0) continue;
-                const int steps = per * p.group;
+                const int steps = per * p.group, end = n + steps;
                 const bool fix = it.sp.Lq < p.nq && it.hi * kTile > it.sp.Lq;
+                const int kb = items % C::kKv;
+                const uint32_t aKV = aKV0 + kb * 2 * C::kTileBytes;
                 int in_head = 0;  // tile of the next score step within its head
-                auto score = [&](int j) {
-                    const int r = n + j, s = r % C::kStages;
-                    if (!thread_spin(&bar->full[s], (r / C::kStages) & 1, p.status, 103, abort_flag)) return false;
+                // S = K Q^T (or dP = V dO^T) of step g, into the buffer that step g - 1 or g - 2
+                // has left
+                auto score = [&](int g) {
+                    const int s = g % C::kStages;
+                    if (!thread_spin(&bar->full[s], (g / C::kStages) & 1, p.status, 103, abort_flag)) return false;
                     if (++in_head == per) {
                         in_head = 0;
                         if (fix) {
-                            mbar_arrive(&bar->fix_wanted);
-                            if (!thread_spin(&bar->fixed, nfix & 1, p.status, 104, abort_flag)) return false;
+                            if (first) mbar_arrive(&bar->fix_wanted);
+                            if (!thread_spin(&bar->fixed[nfix & 1], phase(nfix), p.status, 104, abort_flag)) return false;
                             ++nfix;
                         }
                     }
-                    // S holds the P of the step before until its product is done
-                    if (r > 0 && !thread_spin(&bar->pv_done, (r - 1) & 1, p.status, 105, abort_flag)) return false;
+                    if (C::kBufs == 2) {  // its own kind of the step before
+                        if (g >= 1 && !thread_spin(&done[(g - 1) & 1], phase(g - 1), p.status, 105, abort_flag))
+                            return false;
+                    } else if (first) {  // S follows dP of step g - 2
+                        if (g >= 2 && !thread_spin(&bar->ds_done[g & 1], phase(g - 2), p.status, 105, abort_flag))
+                            return false;
+                    } else {  // dP follows S of step g - 1
+                        if (g >= 1 && !thread_spin(&bar->pv_done[(g - 1) & 1], phase(g - 1), p.status, 106, abort_flag))
+                            return false;
+                    }
                     tc_fence_after();
-                    mma_scores<DP>(tmem + C::kS, aK, aT + s * 2 * C::kTileBytes);
-                    mma_commit(&bar->s_full);
+                    mma_scores<DP>(buffer(g), aKV, aT + s * 2 * C::kTileBytes + (first ? 0 : C::kTileBytes));
+                    mma_commit(&full[g & 1]);
                     return true;
                 };
-                auto dprob = [&](int j) {
-                    const int r = n + j, s = r % C::kStages;
-                    if (r > 0 && !thread_spin(&bar->ds_done, (r - 1) & 1, p.status, 106, abort_flag)) return false;
+                // dV += P^T dO (or dK += dS^T Q) of step g
+                auto sum = [&](int g) {
+                    const int s = g % C::kStages;
+                    if (!thread_spin(&ready[g & 1], phase(g), p.status, 108, abort_flag)) return false;
+                    if (g == n && items > 0 &&
+                        !thread_spin(&bar->acc_free, (items - 1) & 1, p.status, 109, abort_flag))
+                        return false;
                     tc_fence_after();
-                    mma_scores<DP>(tmem + C::kDp, aV, aT + s * 2 * C::kTileBytes + C::kTileBytes);
-                    mma_commit(&bar->dp_full);
-                    return true;
-                };
-                ok = thread_spin(&bar->kv_full, items & 1, p.status, 107, abort_flag) && score(0) && dprob(0);
-                for (int j = 0; j < steps && ok; ++j) {
-                    const int r = n + j, s = r % C::kStages;
-                    const uint32_t aQ = aT + s * 2 * C::kTileBytes, adO = aQ + C::kTileBytes;
-                    ok = thread_spin(&bar->p_full, r & 1, p.status, 108, abort_flag) &&
-                         (j > 0 || items == 0 ||
-                          thread_spin(&bar->acc_free, (items - 1) & 1, p.status, 109, abort_flag));
-                    if (!ok) break;
-                    tc_fence_after();
-                    mma_sum<DP>(tmem + C::kDv, tmem + C::kS, adO, j > 0 ? 1u : 0u);
-                    mma_commit(&bar->pv_done);
-                    if (j + 1 < steps && !(ok = score(j + 1))) break;
-                    if (!(ok = thread_spin(&bar->ds_full, r & 1, p.status, 110, abort_flag))) break;
-                    tc_fence_after();
-                    mma_sum<DP>(tmem + C::kDk, tmem + C::kDp, aQ, j > 0 ? 1u : 0u);
-                    mma_commit(&bar->ds_done);
+                    mma_sum<DP>(tmem + (first ? C::kDv : C::kDk), buffer(g),
+                                aT + s * 2 * C::kTileBytes + (first ? C::kTileBytes : 0), g > n ? 1u : 0u);
+                    mma_commit(&done[g & 1]);
                     mma_commit(&bar->empty[s]);
-                    if (j + 1 < steps) ok = dprob(j + 1);
+                    return true;
+                };
+                ok = thread_spin(&bar->kv_full[kb], (items / C::kKv) & 1, p.status, 107, abort_flag) && score(n);
+                if (C::kBufs == 3 && first && steps > 1) ok = ok && score(n + 1);
+                for (int g = n; g < end && ok; ++g) {
+                    if (C::kBufs == 2) ok = sum(g) && (g + 1 >= end || score(g + 1));
+                    else if (first) ok = sum(g) && (g + 2 >= end || score(g + 2));
+                    else ok = (g + 1 >= end || score(g + 1)) && sum(g);
                 }
                 if (!ok) break;
-                mma_commit(&bar->kv_free);
+                mma_commit(&bar->kv_free[kb]);
                 mma_commit(&bar->acc_full);
-                n += steps;
+                n = end;
                 ++items;
             }
-            mma_commit(&bar->drain);
-            mbar_wait_drain(&bar->drain, 0);
+            mma_commit(&bar->drain[first ? 0 : 1]);
+            mbar_wait_drain(&bar->drain[first ? 0 : 1], 0);
         }
         __syncwarp();
     }
     } else {
-    setmaxnreg_inc<kMathRegs>();
-        const int w = warp >> 2, row = tid & 127;  // query-column half, key row
+        const int w = warp >> 2, row = tid & 127;  // 32 query columns, key row
         const uint32_t lanes = (uint32_t)((warp & 3) * 32) << 16;
-        const uint32_t tS = tmem + C::kS + 64 * w + lanes, tD = tmem + C::kDp + 64 * w + lanes;
         const float sl = p.scale_log2;
         const float2 sl2 = make_float2(sl, sl);
         int n = 0, items = 0;
         bool ok = true;
         for (int64_t idx = blockIdx.x; idx < p.items && ok; idx += gridDim.x) {
-            const DkvItem it = dkv_item(p, idx);
-            const int key = it.k0 + row, off = it.sp.Lk - it.sp.Lq;
-            const bool exists = key < p.nk, valid = key < it.sp.Lk;
-            // queries [first, end) see this key
-            const int first = p.causal ? max(0, key - off) : 0;
-            const int end = p.window ? (int)min((long long)it.sp.Lq, (long long)key - off + p.window) : it.sp.Lq;
-            const int per = it.hi - it.lo, steps = per * p.group;
-            int j = it.lo;
+            int lo, hi, steps, first, end;
+            {
+                const DkvItem it = dkv_item(p, idx);
+                const int key = it.k0 + row, off = it.sp.Lk - it.sp.Lq;
+                lo = it.lo;
+                hi = it.hi;
+                steps = (hi - lo) * p.group;
+                // queries [first, end) see this key (the rows past the length need no mask:
+                // their -lse is -inf)
+                first = p.causal ? max(0, key - off) : 0;
+                end = p.window ? (int)min((long long)it.sp.Lq, (long long)key - off + p.window) : 1 << 30;
+            }
+            const unsigned width = end > first ? (unsigned)(end - first) : 0u;
+            int j = lo;
             for (int x = 0; x < steps; ++x, ++n) {
                 const int s = n % C::kStages;
-                const float4 *lse4 = reinterpret_cast<const float4 *>(sR + s * 1024 + w * 256);
-                const float4 *del4 = reinterpret_cast<const float4 *>(sR + s * 1024 + 512 + w * 256);
+                const uint32_t tS = tmem + 128 * (2 * n % C::kBufs) + 32 * w + lanes,
+                               tD = tmem + 128 * ((2 * n + 1) % C::kBufs) + 32 * w + lanes;
+                const float4 *lse4 = reinterpret_cast<const float4 *>(sR + s * 1024 + w * 128);
+                const float4 *del4 = reinterpret_cast<const float4 *>(sR + s * 1024 + 512 + w * 128);
+                const uint32_t parity = (uint32_t)(n >> 1) & 1u;
                 if (!warp_spin(&bar->full[s], (n / C::kStages) & 1, p.status, 111, abort_flag) ||
-                    !warp_spin(&bar->s_full, n & 1, p.status, 112, abort_flag)) {
+                    !warp_spin(&bar->s_full[n & 1], parity, p.status, 112, abort_flag)) {
                     ok = false;
                     break;
                 }
                 tc_fence_after();
-                uint32_t v[2][32];
-                tmem_ld32_async(tS, v[0]);
-                tmem_ld32_async(tS + 32, v[1]);
-                tmem_wait_ld(v[0]);
-                tie32(v[1]);
-                const int q0 = j * kTile + 64 * w;
-                const bool masked = __any_sync(0xffffffffu, first > q0 || (p.window && end < q0 + 64));
+                uint32_t v[32];
+                tmem_ld32(tS, v);
+                const int q0 = j * kTile + 32 * w;
+                const bool masked = __any_sync(0xffffffffu, first > q0 || end < q0 + 32);
 #pragma unroll
-                for (int c = 0; c < 2; ++c)
+                for (int c = 0; c < 32; c += 16) {
+                    uint32_t o[8];
 #pragma unroll
-                    for (int e = 0; e < 32; e += 4) {
-                        const float4 l = lse4[8 * c + e / 4];
-                        const float2 y0 = ffma2(make_float2(__uint_as_float(v[c][e]), __uint_as_float(v[c][e + 1])),
-                                                sl2, make_float2(-l.x, -l.y));
-                        const float2 y1 = ffma2(make_float2(__uint_as_float(v[c][e + 2]), __uint_as_float(v[c][e + 3])),
-                                                sl2, make_float2(-l.z, -l.w));
-                        v[c][e] = __float_as_uint(ex2_approx(y0.x));
-                        v[c][e + 1] = __float_as_uint(ex2_approx(y0.y));
-                        v[c][e + 2] = __float_as_uint(ex2_approx(y1.x));
-                        v[c][e + 3] = __float_as_uint(ex2_approx(y1.y));
+                    for (int e = c; e < c + 16; e += 4) {
+                        const float4 l = lse4[e / 4];
+                        float2 y0 = ffma2(make_float2(__uint_as_float(v[e]), __uint_as_float(v[e + 1])), sl2,
+                                          make_float2(l.x, l.y));
+                        float2 y1 = ffma2(make_float2(__uint_as_float(v[e + 2]), __uint_as_float(v[e + 3])), sl2,
+                                          make_float2(l.z, l.w));
+                        y0.x = ex2_approx(y0.x);
+                        y0.y = ex2_approx(y0.y);
+                        y1.x = ex2_approx(y1.x);
+                        y1.y = ex2_approx(y1.y);
+                        if (masked) {
+                            if ((unsigned)(e - (first - q0)) >= width) y0.x = 0.f;
+                            if ((unsigned)(e + 1 - (first - q0)) >= width) y0.y = 0.f;
+                            if ((unsigned)(e + 2 - (first - q0)) >= width) y1.x = 0.f;
+                            if ((unsigned)(e + 3 - (first - q0)) >= width) y1.y = 0.f;
+                        }
+                        v[e] = __float_as_uint(y0.x);
+                        v[e + 1] = __float_as_uint(y0.y);
+                        v[e + 2] = __float_as_uint(y1.x);
+                        v[e + 3] = __float_as_uint(y1.y);
+                        o[(e - c) / 2] = pack2(y0.x, y0.y);
+                        o[(e - c) / 2 + 1] = pack2(y1.x, y1.y);
                     }
-                if (masked) {
-                    const int a = first - q0;
-                    const unsigned wd = end > first ? (unsigned)(end - first) : 0u;
-#pragma unroll
-                    for (int c = 0; c < 2; ++c)
-#pragma unroll
-                        for (int e = 0; e < 32; ++e)
-                            if ((unsigned)(32 * c + e - a) >= wd) v[c][e] = 0u;
-                }
-#pragma unroll
-                for (int c = 0; c < 2; ++c) {
-                    uint32_t o[16];
-#pragma unroll
-                    for (int e = 0; e < 16; ++e)
-                        o[e] = pack2(__uint_as_float(v[c][2 * e]), __uint_as_float(v[c][2 * e + 1]));
-                    tmem_st16_async(tS + 16 * c, o);
+                    tmem_st8_async(tS + c / 2, o);
                 }
                 tmem_wait_st();
                 tc_fence_before();
                 __syncwarp();
-                if (lane == 0) mbar_arrive(&bar->p_full);
-                if (!warp_spin(&bar->dp_full, n & 1, p.status, 113, abort_flag)) {
+                if (lane == 0) mbar_arrive(&bar->p_full[n & 1]);
+                if (!warp_spin(&bar->dp_full[n & 1], parity, p.status, 113, abort_flag)) {
                     ok = false;
                     break;
                 }
                 tc_fence_after();
+                // 16 columns at a time (registers); dS takes the columns that have been read
 #pragma unroll
-                for (int c = 0; c < 2; ++c) {
-                    uint32_t u[32], o[16];
-                    tmem_ld32(tD + 32 * c, u);
-                    // the other half's columns, and this half's second 32, are read before
-                    // anything is written over them: dS of 32 columns takes 16, written at
-                    // the start of the half after both loads
+                for (int c = 0; c < 32; c += 16) {
+                    uint32_t u[16], o[8];
+                    tmem_ld16(tD + c, u);
 #pragma unroll
-                    for (int e = 0; e < 32; e += 4) {
-                        const float4 dl = del4[8 * c + e / 4];
+                    for (int e = 0; e < 16; e += 4) {
+                        const float4 dl = del4[(c + e) / 4];
                         const float2 y0 = fadd2(make_float2(__uint_as_float(u[e]), __uint_as_float(u[e + 1])),
-                                                make_float2(-dl.x, -dl.y));
+                                                make_float2(dl.x, dl.y));
                         const float2 y1 = fadd2(make_float2(__uint_as_float(u[e + 2]), __uint_as_float(u[e + 3])),
-                                                make_float2(-dl.z, -dl.w));
-                        const float2 z0 = fmul2(make_float2(__uint_as_float(v[c][e]), __uint_as_float(v[c][e + 1])), y0);
-                        const float2 z1 = fmul2(make_float2(__uint_as_float(v[c][e + 2]), __uint_as_float(v[c][e + 3])), y1);
+                                                make_float2(dl.z, dl.w));
+                        const float2 z0 = fmul2(make_float2(__uint_as_float(v[c + e]), __uint_as_float(v[c + e + 1])), y0);
+                        const float2 z1 = fmul2(make_float2(__uint_as_float(v[c + e + 2]), __uint_as_float(v[c + e + 3])), y1);
                         o[e / 2] = pack2(z0.x, z0.y);
                         o[e / 2 + 1] = pack2(z1.x, z1.y);
                     }
-                    tmem_st16_async(tD + 16 * c, o);
+                    tmem_st8_async(tD + c / 2, o);
                 }
                 tmem_wait_st();
                 tc_fence_before();
                 __syncwarp();
-                if (lane == 0) mbar_arrive(&bar->ds_full);
-                if (++j == it.hi) j = it.lo;
+                if (lane == 0) mbar_arrive(&bar->ds_full[n & 1]);
+                if (++j == hi) j = lo;
             }
             if (!ok) break;
             const bool some = steps > 0;
@@ -752,14 +797,21 @@ softmax_attn_dkv_kernel(const __grid_constant__ CUtensorMap tQ, const __grid_con
                 tc_fence_after();
                 ++items;
             }
+            // (derived again: kept through the loop, it would cost registers there)
+            int64_t again = idx;
+            asm volatile("" : "+l"(again));
+            const DkvItem it = dkv_item(p, again);
+            const int key = it.k0 + row;
+            const bool exists = key < p.nk, valid = key < it.sp.Lk;
             __nv_bfloat16 *dk = p.dK + it.batch * p.sdK.b + it.kvh * p.sdK.h + (int64_t)key * p.sdK.n;
             __nv_bfloat16 *dv = p.dV + it.batch * p.sdV.b + it.kvh * p.sdV.h + (int64_t)key * p.sdV.n;
-            // warps 0-3 write dV, warps 4-7 dK
+            // warps 0-7 write dV, warps 8-15 dK, half the columns each
 #pragma unroll
-            for (int c = 0; c < DP; c += 32) {
-                uint32_t o[32];
-                if (some) tmem_ld32(tmem + (w ? C::kDk : C::kDv) + c + lanes, o);
-                if (exists) store_row(w ? dk : dv, o, c, p.d, w ? p.scale : 1.f, !some || !valid);
+            for (int c = 0; c < DP / 2; c += 16) {
+                uint32_t o[16];
+                const int col = (w & 1) * (DP / 2) + c;
+                if (some) tmem_ld16(tmem + (w >> 1 ? C::kDk : C::kDv) + col + lanes, o);
+                if (exists) store_row(w >> 1 ? dk : dv, o, col, p.d, w >> 1 ? p.scale : 1.f, !some || !valid);
             }
             if (some) {
                 tc_fence_before();
