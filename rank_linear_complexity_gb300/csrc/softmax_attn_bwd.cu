@@ -17,10 +17,11 @@
 // partial dQ through memory in a fixed order.  P and dS are rounded to bf16 as operands
 // (relative 2^-9, in sums of many terms); sums are fp32 in tensor memory.
 //
-// Roles, both kernels: warps 0-15 do the arithmetic, four warps for each 32 of a tile's 128
-// columns, one thread a row (four such warps a scheduler hide one another's latencies);
-// warp 16 loads (lane 0) and zeroes rows past the valid length (lanes 1-31, where 0 x NaN
-// would reach a sum); one thread each of warps 17 and 18 issues products, so that a chain of
+// Roles, both kernels: warps 0-3 and 4-7 do the arithmetic of even and of odd steps, one
+// thread a row of 128 columns.  The groups are half a step apart, so that one's exponentials
+// (special function unit) run beside the other's dS (multiplications) and its waits;
+// warp 8 loads (lane 0) and zeroes rows past the valid length (lanes 1-31, where 0 x NaN
+// would reach a sum); one thread each of warps 9 and 10 issues products, so that a chain of
 // products that waits for arithmetic does not hold up the other one.
 #include <algorithm>
 #include <cmath>
@@ -34,8 +35,12 @@ namespace {
 
 using namespace ptx;
 
-constexpr int kThreads = 640;  // 96 registers each; the last warp is idle
-constexpr int kMathWarps = 16, kLoadWarp = 16, kMmaWarp = 17;
+// Twelve warps (one idle), 168 registers each at launch; the two warpgroups that do the
+// arithmetic take registers from the third: 2 x 208 + 88 = 3 x 168.
+constexpr int kThreads = 384;
+constexpr uint32_t kMathRegs = 208, kIssueRegs = 88;
+static_assert(2 * kMathRegs + kIssueRegs == 3 * 168, "register split");
+constexpr int kMathWarps = 8, kGroupWarps = 4, kLoadWarp = 8, kMmaWarp = 9;
 constexpr float kLog2e = 1.4426950408889634f;
 
 struct BwdParams {
@@ -55,6 +60,30 @@ struct BwdParams {
     int *status;
 };
 
+// Columns outside [a, a + w) become 0.
+__device__ __forceinline__ void mask_zero(uint32_t (&v)[32], int a, unsigned w) {
+#pragma unroll
+    for (int e = 0; e < 32; ++e)
+        if ((unsigned)(e - a) >= w) v[e] = 0u;
+}
+// The same for 128 columns in tensor memory (rolled: only blocks at a mask's edge).
+__device__ __forceinline__ void zero_outside(uint32_t t, int a, unsigned w) {
+#pragma unroll 1
+    for (int c = 0; c < kTile; c += 32) {
+        uint32_t u[32];
+        tmem_ld32(t + c, u);
+        mask_zero(u, a - c, w);
+        tmem_st32(t + c, u);
+    }
+}
+__device__ __forceinline__ float4 lds4(uint32_t addr) {
+    float4 v;
+    asm volatile("ld.shared.v4.f32 {%0, %1, %2, %3}, [%4];"
+                 : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w)
+                 : "r"(addr)
+                 : "memory");
+    return v;
+}
 // Products of two pairs of bf16, added in fp32.
 __device__ __forceinline__ float dot2(uint32_t a, uint32_t b) {
     return __uint_as_float(a << 16) * __uint_as_float(b << 16) +
@@ -87,15 +116,14 @@ __device__ __forceinline__ void mma_scores(uint32_t d, uint32_t a, uint32_t b) {
         mma_ss(d, da + off, db + off, idesc, x > 0 ? 1u : 0u);
     }
 }
-// D (128 x DP) += A (128 x 128, packed in tensor memory: 32 elements in 16 columns at the
-// start of each 32) . B (128 rows of DP)
+// D (128 x DP) += A (128 x 128, packed in 64 columns of tensor memory) . B (128 rows of DP)
 template <int DP>
 __device__ __forceinline__ void mma_sum(uint32_t d, uint32_t a, uint32_t b, uint32_t acc) {
     const uint32_t idesc = idesc_f16(128, DP, 1, 0, 1);
     const uint64_t db = sdesc(b, 16384, 1024, kSwizzle128B);
 #pragma unroll
     for (int x = 0; x < 8; ++x)
-        mma_ts(d, a + (x >> 1) * 32 + (x & 1) * 8, db + (uint64_t)(128 * x), idesc,
+        mma_ts(d, a + 8 * x, db + (uint64_t)(128 * x), idesc,
                (acc || x > 0) ? 1u : 0u);
 }
 
@@ -141,13 +169,13 @@ __device__ __forceinline__ DqItem dq_item(const BwdParams &p, int64_t idx) {
 }
 
 struct DqBarriers {
-    uint64_t q_full, q_free, s_full, s_free, dp_full[2], ds_full[2], dq_done[2], acc_free;
+    // (pairs: even and odd blocks, each with a group of warps of its own)
+    uint64_t q_full, q_free, s_full[2], s_free, dp_full[2], ds_full[2], dq_done[2], acc_full, acc_free;
     uint64_t fix_wanted, fixed, drain[2];
     uint64_t full[8], empty[8], rows_ready;
     uint32_t tmem;
     int abort;
-    // -lse and -delta of the item's rows (a warp that writes the next item's has seen all warps
-    // past this item's last block, so past their reading)
+    // -lse and -delta of the item's rows (written once all warps have left the item before)
     float rows[2 * kTile];
 };
 
@@ -169,14 +197,15 @@ softmax_attn_dq_kernel(const __grid_constant__ CUtensorMap tQ, const __grid_cons
     if (tid == 0) {
         mbar_init(&bar->q_full, 1);
         mbar_init(&bar->q_free, 1);
-        mbar_init(&bar->s_full, 1);
-        mbar_init(&bar->s_free, kMathWarps);
+        mbar_init(&bar->s_free, kGroupWarps);
         for (int i = 0; i < 2; ++i) {
+            mbar_init(&bar->s_full[i], 1);
             mbar_init(&bar->dp_full[i], 1);
-            mbar_init(&bar->ds_full[i], kMathWarps);
+            mbar_init(&bar->ds_full[i], kGroupWarps);
             mbar_init(&bar->dq_done[i], 1);
         }
         mbar_init(&bar->rows_ready, kMathWarps);
+        mbar_init(&bar->acc_full, 1);
         mbar_init(&bar->acc_free, kMathWarps);
         mbar_init(&bar->fix_wanted, 1);
         mbar_init(&bar->fixed, 31);
@@ -199,6 +228,7 @@ softmax_attn_dq_kernel(const __grid_constant__ CUtensorMap tQ, const __grid_cons
     const uint32_t tmem = bar->tmem;
     // ring entry 2 j + kv of an item: K (kv = 0) and V of its j-th block
     if (warp >= kLoadWarp) {
+    setmaxnreg_dec<kIssueRegs>();
     if (warp == kLoadWarp) {
         if (lane == 0) {
             int ring = 0, nq = 0;
@@ -266,7 +296,7 @@ softmax_attn_dq_kernel(const __grid_constant__ CUtensorMap tQ, const __grid_cons
                     if (!ok) break;
                     tc_fence_after();
                     mma_scores<DP>(tmem + C::kS, aQ, aKV + s * C::kTileBytes);
-                    mma_commit(&bar->s_full);
+                    mma_commit(&bar->s_full[n & 1]);
                     s = (ring + 1) % C::kStages;
                     ok = thread_spin(&bar->full[s], ((ring + 1) / C::kStages) & 1, p.status, 89, abort_flag) &&
                          (n < 2 || thread_spin(&bar->dq_done[n & 1], ((n >> 1) - 1) & 1, p.status, 90, abort_flag));
@@ -305,6 +335,7 @@ softmax_attn_dq_kernel(const __grid_constant__ CUtensorMap tQ, const __grid_cons
                     mma_commit(&bar->dq_done[n & 1]);
                     mma_commit(&bar->empty[s]);
                 }
+                mma_commit(&bar->acc_full);
                 ++items;
             }
             mma_commit(&bar->drain[1]);
@@ -313,23 +344,24 @@ softmax_attn_dq_kernel(const __grid_constant__ CUtensorMap tQ, const __grid_cons
         __syncwarp();
     }
     } else {
-        const int w = warp >> 2, row = tid & 127;  // 32 columns, row
+        setmaxnreg_inc<kMathRegs>();
+        const int group = warp >> 2, row = tid & 127;
         const uint32_t lanes = (uint32_t)((warp & 3) * 32) << 16;
         const float sl = p.scale_log2;
         int n = 0, items = 0;
         for (int64_t idx = blockIdx.x; idx < p.items; idx += gridDim.x) {
             const DqItem it = dq_item(p, idx);
             const int lo = it.lo, hi = it.hi;
-            // -lse and -delta of eight rows a warp (rows read by whole warps, 8 bytes a lane),
+            // -lse and -delta of sixteen rows a warp (rows read by whole warps, 8 bytes a lane),
             // for this kernel through shared memory and for the other one.
             float *sm = bar->rows;
             {
                 const __nv_bfloat16 *o = p.O + it.batch * p.sO.b + it.head * p.sO.h + 4 * lane;
                 const __nv_bfloat16 *g = p.dO + it.batch * p.sdO.b + it.head * p.sdO.h + 4 * lane;
-                const int r0 = it.q0 + 8 * warp;
-                uint2 a[8], b[8];
+                const int r0 = it.q0 + 16 * warp;
+                uint2 a[16], b[16];
 #pragma unroll
-                for (int r = 0; r < 8; ++r) {
+                for (int r = 0; r < 16; ++r) {
                     a[r] = b[r] = make_uint2(0u, 0u);
                     if (r0 + r < it.sp.Lq && 4 * lane < p.d) {
                         a[r] = __ldg(reinterpret_cast<const uint2 *>(o + (int64_t)(r0 + r) * p.sO.n));
@@ -337,20 +369,27 @@ softmax_attn_dq_kernel(const __grid_constant__ CUtensorMap tQ, const __grid_cons
                     }
                 }
                 float x = -INFINITY, del = 0.f;
-                if (lane < 8 && r0 + lane < it.sp.Lq)
+                if (lane < 16 && r0 + lane < it.sp.Lq)
                     x = __ldg(p.lse + ((int64_t)it.batch * p.hq + it.head) * p.nq + r0 + lane);
 #pragma unroll
-                for (int r = 0; r < 8; ++r) {
+                for (int r = 0; r < 16; ++r) {
                     float y = dot2(a[r].x, b[r].x) + dot2(a[r].y, b[r].y);
 #pragma unroll
                     for (int k = 16; k; k >>= 1) y += __shfl_xor_sync(0xffffffffu, y, k);
                     if (lane == r) del = y;
                 }
-                if (lane < 8) {
+                if (it.hi > it.lo && items > 0 &&
+                    !warp_spin(&bar->acc_free, (items - 1) & 1, p.status, 99, abort_flag))
+                    break;
+                if (lane < 16) {
                     const float nl = x == -INFINITY ? -INFINITY : -x * kLog2e, nd = x == -INFINITY ? 0.f : -del;
                     float *dst = p.rows + (((int64_t)it.batch * p.hq + it.head) * p.qtiles + it.q0 / kTile) * 256;
-                    dst[8 * warp + lane] = sm[8 * warp + lane] = nl;
-                    dst[128 + 8 * warp + lane] = sm[128 + 8 * warp + lane] = nd;
+                    dst[16 * warp + lane] = nl;
+                    dst[128 + 16 * warp + lane] = nd;
+                    if (it.hi > it.lo) {
+                        sm[16 * warp + lane] = nl;
+                        sm[128 + 16 * warp + lane] = nd;
+                    }
                 }
             }
             float nl = -INFINITY, nd = 0.f;
@@ -366,59 +405,69 @@ softmax_attn_dq_kernel(const __grid_constant__ CUtensorMap tQ, const __grid_cons
             const int first = seen ? it.sp.first(it.q0 + row) : 0, end = seen ? it.sp.end(it.q0 + row) : 0;
             const unsigned width = end > first ? (unsigned)(end - first) : 0u;
             bool ok = true;
-            for (int j = lo; j < hi; ++j, ++n) {
-                if (!warp_spin(&bar->s_full, n & 1, p.status, 94, abort_flag)) {
+            const int n0 = n;
+            n += max(0, hi - lo);
+            for (int j = lo + ((n0 ^ group) & 1), g = n0 + ((n0 ^ group) & 1); j < hi; j += 2, g += 2) {
+                if (!warp_spin(&bar->s_full[g & 1], (g >> 1) & 1, p.status, 94, abort_flag)) {
                     ok = false;
                     break;
                 }
                 tc_fence_after();
-                uint32_t v[32];
-                tmem_ld32(tmem + C::kS + 32 * w + lanes, v);
+                uint32_t v[4][32];
+#pragma unroll
+                for (int c = 0; c < 4; ++c) tmem_ld32_async(tmem + C::kS + 32 * c + lanes, v[c]);
+                tmem_wait_ld(v[0]);
+                tie32(v[1]);
+                tie32(v[2]);
+                tie32(v[3]);
                 tc_fence_before();
                 __syncwarp();
                 if (lane == 0) mbar_arrive(&bar->s_free);
                 const float2 sl2 = make_float2(sl, sl), off2 = make_float2(nl, nl);
 #pragma unroll
-                for (int e = 0; e < 32; e += 2) {
-                    const float2 y = ffma2(make_float2(__uint_as_float(v[e]), __uint_as_float(v[e + 1])), sl2, off2);
-                    v[e] = __float_as_uint(ex2_approx(y.x));
-                    v[e + 1] = __float_as_uint(ex2_approx(y.y));
-                }
-                const uint32_t tD = tmem + C::kDp + 128 * (n & 1) + 32 * w + lanes;
-                if (!warp_spin(&bar->dp_full[n & 1], (n >> 1) & 1, p.status, 95, abort_flag)) {
+                for (int c = 0; c < 4; ++c)
+#pragma unroll
+                    for (int e = 0; e < 32; e += 2) {
+                        const float2 y = ffma2(make_float2(__uint_as_float(v[c][e]), __uint_as_float(v[c][e + 1])),
+                                               sl2, off2);
+                        v[c][e] = __float_as_uint(ex2_approx(y.x));
+                        v[c][e + 1] = __float_as_uint(ex2_approx(y.y));
+                    }
+                // keys that take no part: P = 0 whatever S holds, and dP = delta below whatever
+                // it holds
+                const int k0 = j * kTile;
+                const bool masked = __any_sync(0xffffffffu, first > k0 || end < k0 + kTile);
+                const uint32_t tD = tmem + C::kDp + 128 * (g & 1) + lanes;
+                if (!warp_spin(&bar->dp_full[g & 1], (g >> 1) & 1, p.status, 95, abort_flag)) {
                     ok = false;
                     break;
                 }
                 tc_fence_after();
-                const int k0 = j * kTile + 32 * w;
+                if (masked) zero_outside(tD, first - k0, width);
                 const float2 nd2 = make_float2(nd, nd);
-                const bool masked = __any_sync(0xffffffffu, first > k0 || end < k0 + 32);
-                // 16 columns at a time (registers); dS takes the columns that have been read
+                // 32 columns at a time; dS takes the columns that have been read
 #pragma unroll
-                for (int c = 0; c < 32; c += 16) {
-                    uint32_t u[16], o[8];
-                    tmem_ld16(tD + c, u);
+                for (int c = 0; c < 4; ++c) {
+                    uint32_t u[32], o[16];
+                    tmem_ld32(tD + 32 * c, u);
+                    if (masked) mask_zero(v[c], first - k0 - 32 * c, width);
 #pragma unroll
-                    for (int e = 0; e < 16; e += 2) {
+                    for (int e = 0; e < 32; e += 2) {
                         const float2 y = fadd2(make_float2(__uint_as_float(u[e]), __uint_as_float(u[e + 1])), nd2);
-                        float2 z = fmul2(make_float2(__uint_as_float(v[c + e]), __uint_as_float(v[c + e + 1])), y);
-                        if (masked) {  // keys that take no part, whatever their S and dP hold
-                            if ((unsigned)(c + e - (first - k0)) >= width) z.x = 0.f;
-                            if ((unsigned)(c + e + 1 - (first - k0)) >= width) z.y = 0.f;
-                        }
+                        const float2 z = fmul2(make_float2(__uint_as_float(v[c][e]), __uint_as_float(v[c][e + 1])), y);
                         o[e / 2] = pack2(z.x, z.y);
                     }
-                    tmem_st8_async(tD + c / 2, o);
+                    tmem_st16_async(tD + 16 * c, o);
                 }
                 tmem_wait_st();
                 tc_fence_before();
                 __syncwarp();
-                if (lane == 0) mbar_arrive(&bar->ds_full[n & 1]);
+                if (lane == 0) mbar_arrive(&bar->ds_full[g & 1]);
             }
             if (!ok) break;
             const bool some = hi > lo;
             if (some) {
-                if (!warp_spin(&bar->dq_done[(n - 1) & 1], ((n - 1) >> 1) & 1, p.status, 96, abort_flag)) break;
+                if (!warp_spin(&bar->acc_full, (items - 1) & 1, p.status, 96, abort_flag)) break;
                 tc_fence_after();
             }
             // (derived again: kept through the loop, it would cost registers there)
@@ -429,9 +478,9 @@ softmax_attn_dq_kernel(const __grid_constant__ CUtensorMap tQ, const __grid_cons
             const bool exists = i < p.nq, valid = i < at.sp.Lq;
             __nv_bfloat16 *dst = p.dQ + at.batch * p.sdQ.b + at.head * p.sdQ.h + (int64_t)i * p.sdQ.n;
 #pragma unroll
-            for (int c = 0; c < DP / 4; c += 16) {
+            for (int c = 0; c < DP / 2; c += 16) {
                 uint32_t o[16];
-                const int col = w * (DP / 4) + c;
+                const int col = group * (DP / 2) + c;
                 if (some) tmem_ld16(tmem + C::kDq + col + lanes, o);
                 if (exists) store_row(dst, o, col, p.d, p.scale, !some || !valid);
             }
@@ -519,10 +568,10 @@ softmax_attn_dkv_kernel(const __grid_constant__ CUtensorMap tQ, const __grid_con
             mbar_init(&bar->kv_full[i], 1);
             mbar_init(&bar->kv_free[i], 2);
             mbar_init(&bar->s_full[i], 1);
-            mbar_init(&bar->p_full[i], kMathWarps);
+            mbar_init(&bar->p_full[i], kGroupWarps);
             mbar_init(&bar->pv_done[i], 1);
             mbar_init(&bar->dp_full[i], 1);
-            mbar_init(&bar->ds_full[i], kMathWarps);
+            mbar_init(&bar->ds_full[i], kGroupWarps);
             mbar_init(&bar->ds_done[i], 1);
             mbar_init(&bar->drain[i], 1);
             mbar_init(&bar->fixed[i], 31);
@@ -547,6 +596,7 @@ softmax_attn_dkv_kernel(const __grid_constant__ CUtensorMap tQ, const __grid_con
     const uint32_t tmem = bar->tmem;
 
     if (warp >= kLoadWarp) {
+    setmaxnreg_dec<kIssueRegs>();
     if (warp == kLoadWarp) {
         if (lane == 0) {
             int ring = 0, items = 0;
@@ -689,7 +739,8 @@ softmax_attn_dkv_kernel(const __grid_constant__ CUtensorMap tQ, const __grid_con
         __syncwarp();
     }
     } else {
-        const int w = warp >> 2, row = tid & 127;  // 32 query columns, key row
+        setmaxnreg_inc<kMathRegs>();
+        const int group = warp >> 2, row = tid & 127;
         const uint32_t lanes = (uint32_t)((warp & 3) * 32) << 16;
         const float sl = p.scale_log2;
         const float2 sl2 = make_float2(sl, sl);
@@ -709,87 +760,85 @@ softmax_attn_dkv_kernel(const __grid_constant__ CUtensorMap tQ, const __grid_con
                 end = p.window ? (int)min((long long)it.sp.Lq, (long long)key - off + p.window) : 1 << 30;
             }
             const unsigned width = end > first ? (unsigned)(end - first) : 0u;
-            int j = lo;
-            for (int x = 0; x < steps; ++x, ++n) {
-                const int s = n % C::kStages;
-                const uint32_t tS = tmem + 128 * (2 * n % C::kBufs) + 32 * w + lanes,
-                               tD = tmem + 128 * ((2 * n + 1) % C::kBufs) + 32 * w + lanes;
-                const float4 *lse4 = reinterpret_cast<const float4 *>(sR + s * 1024 + w * 128);
-                const float4 *del4 = reinterpret_cast<const float4 *>(sR + s * 1024 + 512 + w * 128);
-                const uint32_t parity = (uint32_t)(n >> 1) & 1u;
-                if (!warp_spin(&bar->full[s], (n / C::kStages) & 1, p.status, 111, abort_flag) ||
-                    !warp_spin(&bar->s_full[n & 1], parity, p.status, 112, abort_flag)) {
+            const int skip = (n ^ group) & 1, per = hi - lo;
+            int j = skip && per > 0 ? skip % per : 0;  // tile of the step within its head
+            for (int g = n + skip; g < n + steps; g += 2) {
+                const int s = g % C::kStages;
+                const uint32_t tS = tmem + 128 * (2 * g % C::kBufs) + lanes,
+                               tD = tmem + 128 * ((2 * g + 1) % C::kBufs) + lanes;
+                const uint32_t aR = smem_u32(sR) + s * 1024;  // the rows' -lse and, 512 on, -delta
+                const uint32_t parity = (uint32_t)(g >> 1) & 1u;
+                if (!warp_spin(&bar->full[s], (g / C::kStages) & 1, p.status, 111, abort_flag) ||
+                    !warp_spin(&bar->s_full[g & 1], parity, p.status, 112, abort_flag)) {
                     ok = false;
                     break;
                 }
                 tc_fence_after();
-                uint32_t v[32];
-                tmem_ld32(tS, v);
-                const int q0 = j * kTile + 32 * w;
-                const bool masked = __any_sync(0xffffffffu, first > q0 || end < q0 + 32);
+                uint32_t v[4][32];
 #pragma unroll
-                for (int c = 0; c < 32; c += 16) {
-                    uint32_t o[8];
+                for (int c = 0; c < 4; ++c) tmem_ld32_async(tS + 32 * c, v[c]);
+                tmem_wait_ld(v[0]);
+                tie32(v[1]);
+                tie32(v[2]);
+                tie32(v[3]);
+                const int q0 = (lo + j) * kTile;
+                const bool masked = __any_sync(0xffffffffu, first > q0 || end < q0 + kTile);
 #pragma unroll
-                    for (int e = c; e < c + 16; e += 4) {
-                        const float4 l = lse4[e / 4];
-                        float2 y0 = ffma2(make_float2(__uint_as_float(v[e]), __uint_as_float(v[e + 1])), sl2,
-                                          make_float2(l.x, l.y));
-                        float2 y1 = ffma2(make_float2(__uint_as_float(v[e + 2]), __uint_as_float(v[e + 3])), sl2,
-                                          make_float2(l.z, l.w));
-                        y0.x = ex2_approx(y0.x);
-                        y0.y = ex2_approx(y0.y);
-                        y1.x = ex2_approx(y1.x);
-                        y1.y = ex2_approx(y1.y);
-                        if (masked) {
-                            if ((unsigned)(e - (first - q0)) >= width) y0.x = 0.f;
-                            if ((unsigned)(e + 1 - (first - q0)) >= width) y0.y = 0.f;
-                            if ((unsigned)(e + 2 - (first - q0)) >= width) y1.x = 0.f;
-                            if ((unsigned)(e + 3 - (first - q0)) >= width) y1.y = 0.f;
-                        }
-                        v[e] = __float_as_uint(y0.x);
-                        v[e + 1] = __float_as_uint(y0.y);
-                        v[e + 2] = __float_as_uint(y1.x);
-                        v[e + 3] = __float_as_uint(y1.y);
-                        o[(e - c) / 2] = pack2(y0.x, y0.y);
-                        o[(e - c) / 2 + 1] = pack2(y1.x, y1.y);
+                for (int c = 0; c < 4; ++c) {
+#pragma unroll
+                    for (int e = 0; e < 32; e += 4) {
+                        const float4 l = lds4(aR + 4 * (32 * c + e));
+                        const float2 y0 = ffma2(make_float2(__uint_as_float(v[c][e]), __uint_as_float(v[c][e + 1])),
+                                                sl2, make_float2(l.x, l.y));
+                        const float2 y1 = ffma2(make_float2(__uint_as_float(v[c][e + 2]), __uint_as_float(v[c][e + 3])),
+                                                sl2, make_float2(l.z, l.w));
+                        v[c][e] = __float_as_uint(ex2_approx(y0.x));
+                        v[c][e + 1] = __float_as_uint(ex2_approx(y0.y));
+                        v[c][e + 2] = __float_as_uint(ex2_approx(y1.x));
+                        v[c][e + 3] = __float_as_uint(ex2_approx(y1.y));
                     }
-                    tmem_st8_async(tS + c / 2, o);
+                    if (masked) mask_zero(v[c], first - q0 - 32 * c, width);
+                    uint32_t o[16];
+#pragma unroll
+                    for (int e = 0; e < 16; ++e)
+                        o[e] = pack2(__uint_as_float(v[c][2 * e]), __uint_as_float(v[c][2 * e + 1]));
+                    tmem_st16_async(tS + 16 * c, o);
                 }
                 tmem_wait_st();
                 tc_fence_before();
                 __syncwarp();
-                if (lane == 0) mbar_arrive(&bar->p_full[n & 1]);
-                if (!warp_spin(&bar->dp_full[n & 1], parity, p.status, 113, abort_flag)) {
+                if (lane == 0) mbar_arrive(&bar->p_full[g & 1]);
+                if (!warp_spin(&bar->dp_full[g & 1], parity, p.status, 113, abort_flag)) {
                     ok = false;
                     break;
                 }
                 tc_fence_after();
-                // 16 columns at a time (registers); dS takes the columns that have been read
+                // 32 columns at a time; dS takes the columns that have been read
 #pragma unroll
-                for (int c = 0; c < 32; c += 16) {
-                    uint32_t u[16], o[8];
-                    tmem_ld16(tD + c, u);
+                for (int c = 0; c < 4; ++c) {
+                    uint32_t u[32], o[16];
+                    tmem_ld32(tD + 32 * c, u);
 #pragma unroll
-                    for (int e = 0; e < 16; e += 4) {
-                        const float4 dl = del4[(c + e) / 4];
+                    for (int e = 0; e < 32; e += 4) {
+                        const float4 dl = lds4(aR + 512 + 4 * (32 * c + e));
                         const float2 y0 = fadd2(make_float2(__uint_as_float(u[e]), __uint_as_float(u[e + 1])),
                                                 make_float2(dl.x, dl.y));
                         const float2 y1 = fadd2(make_float2(__uint_as_float(u[e + 2]), __uint_as_float(u[e + 3])),
                                                 make_float2(dl.z, dl.w));
-                        const float2 z0 = fmul2(make_float2(__uint_as_float(v[c + e]), __uint_as_float(v[c + e + 1])), y0);
-                        const float2 z1 = fmul2(make_float2(__uint_as_float(v[c + e + 2]), __uint_as_float(v[c + e + 3])), y1);
+                        const float2 z0 = fmul2(make_float2(__uint_as_float(v[c][e]), __uint_as_float(v[c][e + 1])), y0);
+                        const float2 z1 = fmul2(make_float2(__uint_as_float(v[c][e + 2]), __uint_as_float(v[c][e + 3])), y1);
                         o[e / 2] = pack2(z0.x, z0.y);
                         o[e / 2 + 1] = pack2(z1.x, z1.y);
                     }
-                    tmem_st8_async(tD + c / 2, o);
+                    tmem_st16_async(tD + 16 * c, o);
                 }
                 tmem_wait_st();
                 tc_fence_before();
                 __syncwarp();
-                if (lane == 0) mbar_arrive(&bar->ds_full[n & 1]);
-                if (++j == hi) j = lo;
+                if (lane == 0) mbar_arrive(&bar->ds_full[g & 1]);
+                j = (j + 2) % per;
             }
+            n += max(0, steps);
             if (!ok) break;
             const bool some = steps > 0;
             if (some) {
@@ -805,13 +854,12 @@ softmax_attn_dkv_kernel(const __grid_constant__ CUtensorMap tQ, const __grid_con
             const bool exists = key < p.nk, valid = key < it.sp.Lk;
             __nv_bfloat16 *dk = p.dK + it.batch * p.sdK.b + it.kvh * p.sdK.h + (int64_t)key * p.sdK.n;
             __nv_bfloat16 *dv = p.dV + it.batch * p.sdV.b + it.kvh * p.sdV.h + (int64_t)key * p.sdV.n;
-            // warps 0-7 write dV, warps 8-15 dK, half the columns each
+            // warps 0-3 write dV, warps 4-7 dK
 #pragma unroll
-            for (int c = 0; c < DP / 2; c += 16) {
+            for (int c = 0; c < DP; c += 16) {
                 uint32_t o[16];
-                const int col = (w & 1) * (DP / 2) + c;
-                if (some) tmem_ld16(tmem + (w >> 1 ? C::kDk : C::kDv) + col + lanes, o);
-                if (exists) store_row(w >> 1 ? dk : dv, o, col, p.d, w >> 1 ? p.scale : 1.f, !some || !valid);
+                if (some) tmem_ld16(tmem + (group ? C::kDk : C::kDv) + c + lanes, o);
+                if (exists) store_row(group ? dk : dv, o, c, p.d, group ? p.scale : 1.f, !some || !valid);
             }
             if (some) {
                 tc_fence_before();
