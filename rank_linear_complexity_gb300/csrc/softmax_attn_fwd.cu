@@ -168,6 +168,29 @@ __device__ __forceinline__ void mask_chunk(uint32_t (&v)[32], int a, int w) {
     for (int e = 0; e < 32; ++e)
         if ((unsigned)(e - a) >= (unsigned)w) v[e] = 0xff800000u;
 }
+// Both out of line, away from the code of the common block.
+// The masked scores of a block of 128 become -inf in tensor memory.
+__device__ __noinline__ void mask_block(uint32_t t, int a, int w) {
+#pragma unroll 1
+    for (int c = 0; c < kTile; c += 32) {
+        uint32_t v[32];
+        tmem_ld32(t + c, v);
+        mask_chunk(v, a - c, w);
+        tmem_st32(t + c, v);
+    }
+}
+// O times f, eight columns at a time (the caller's scores are in registers).
+__device__ __noinline__ void rescale_output(uint32_t t, int columns, float f) {
+#pragma unroll 1
+    for (int c = 0; c < columns; c += 8) {
+        uint32_t q[8];
+        tmem_ld8(t + c, q);
+#pragma unroll
+        for (int e = 0; e < 8; ++e) q[e] = __float_as_uint(__uint_as_float(q[e]) * f);
+        tmem_st8_async(t + c, q);
+    }
+    tmem_wait_st();
+}
 __device__ __forceinline__ float max_chunk(const uint32_t (&v)[32]) {
     float m0 = __uint_as_float(v[0]), m1 = __uint_as_float(v[1]);
 #pragma unroll
@@ -429,13 +452,7 @@ softmax_attn_fwd_kernel(const __grid_constant__ CUtensorMap tQ, const __grid_con
                 // few blocks at a mask's edge must not widen the code of the others.
                 const int k0 = j * kTile;
                 if (__any_sync(0xffffffffu, first > k0 || end < k0 + kTile)) {
-#pragma unroll 1
-                    for (int c = 0; c < kTile; c += 32) {
-                        uint32_t w[32];
-                        tmem_ld32(tS + c, w);
-                        mask_chunk(w, first - k0 - c, first < end ? end - first : 0);
-                        tmem_st32(tS + c, w);
-                    }
+mask_block(tS, first - k0, first < end ? end - first : 0);
                 }
                 uint32_t v[4][32];
 #pragma unroll
@@ -458,14 +475,7 @@ softmax_attn_fwd_kernel(const __grid_constant__ CUtensorMap tQ, const __grid_con
                     l *= f;
                     m = mn;
                     if (j > lo) {
-#pragma unroll 1
-                        for (int c = 0; c < DP; c += 8) {  // rare, and S is in registers
-                            uint32_t q[8];
-                            tmem_ld8(tO + c, q);
-#pragma unroll
-                            for (int e = 0; e < 8; ++e) q[e] = __float_as_uint(__uint_as_float(q[e]) * f);
-                            tmem_st8_async(tO + c, q);
-                        }
+rescale_output(tO, DP, f);
                     }
                 }
                 const float off = m == -INFINITY ? 0.f : -m * sl;
