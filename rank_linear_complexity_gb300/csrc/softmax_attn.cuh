@@ -12,6 +12,7 @@ namespace linformer {
 namespace sattn {
 
 constexpr int kTile = 128;  // rows of a query tile, keys of a key block
+constexpr int64_t kMaxItems = 1 << 30;  // work items of a launch (counted in 32 bits)
 
 // One call's arguments, already validated.
 struct Call {

@@ -55,7 +55,7 @@ struct BwdParams {
     float *rows;
     int b, hq, hk, group, nq, nk, d, causal, window;
     int qtiles, kblocks;
-    int64_t items;
+    int items;
     float scale, scale_log2;
     int *status;
 };
@@ -146,13 +146,13 @@ struct DqItem {
     int batch, head, q0, lo, hi;
     Span sp;
 };
-__device__ __forceinline__ DqItem dq_item(const BwdParams &p, int64_t idx) {
+__device__ __forceinline__ DqItem dq_item(const BwdParams &p, int idx) {
     DqItem it;
     const int units = p.b * p.hq;
-    const int u = (int)(idx % units), rank = (int)(idx / units);
+    const int rank = idx / units, u = idx - rank * units;
     const int tile = p.causal ? p.qtiles - 1 - rank : rank;  // longest first
     it.batch = u / p.hq;
-    it.head = u % p.hq;
+    it.head = u - it.batch * p.hq;
     it.q0 = tile * kTile;
     it.sp = Span{clamp_length(p.q_lengths, it.batch, p.nq), clamp_length(p.k_lengths, it.batch, p.nk),
                  p.causal, p.window};
@@ -233,7 +233,7 @@ softmax_attn_dq_kernel(const __grid_constant__ CUtensorMap tQ, const __grid_cons
         if (lane == 0) {
             int ring = 0, nq = 0;
             bool ok = true;
-            for (int64_t idx = blockIdx.x; idx < p.items && ok; idx += gridDim.x) {
+            for (int idx = blockIdx.x; idx < p.items && ok; idx += gridDim.x) {
                 const DqItem it = dq_item(p, idx);
                 if (it.hi <= it.lo) continue;
                 if (nq > 0 && !thread_spin(&bar->q_free, (nq - 1) & 1, p.status, 83, abort_flag)) break;
@@ -260,7 +260,7 @@ softmax_attn_dq_kernel(const __grid_constant__ CUtensorMap tQ, const __grid_cons
                 mbar_wait_drain(&bar->full[i % C::kStages], (i / C::kStages) & 1);
         } else {  // K rows past the valid length: dS is 0 there, but 0 x NaN is not
             int ring = 0, nfix = 0;
-            for (int64_t idx = blockIdx.x; idx < p.items; idx += gridDim.x) {
+            for (int idx = blockIdx.x; idx < p.items; idx += gridDim.x) {
                 const DqItem it = dq_item(p, idx);
                 if (it.hi <= it.lo) continue;
                 ring += 2 * (it.hi - it.lo);
@@ -279,7 +279,7 @@ softmax_attn_dq_kernel(const __grid_constant__ CUtensorMap tQ, const __grid_cons
             int ring = 0, items = 0, n = 0, nfix = 0;
             bool ok = true;
             const uint32_t aQ = smem_u32(sQ), adO = smem_u32(sdO), aKV = smem_u32(sKV);
-            for (int64_t idx = blockIdx.x; idx < p.items && ok; idx += gridDim.x) {
+            for (int idx = blockIdx.x; idx < p.items && ok; idx += gridDim.x) {
                 const DqItem it = dq_item(p, idx);
                 const int blocks = it.hi - it.lo;
                 if (blocks <= 0) continue;
@@ -318,7 +318,7 @@ softmax_attn_dq_kernel(const __grid_constant__ CUtensorMap tQ, const __grid_cons
             int ring = 0, items = 0, n = 0;
             bool ok = true;
             const uint32_t aKV = smem_u32(sKV);
-            for (int64_t idx = blockIdx.x; idx < p.items && ok; idx += gridDim.x) {
+            for (int idx = blockIdx.x; idx < p.items && ok; idx += gridDim.x) {
                 const DqItem it = dq_item(p, idx);
                 const int blocks = it.hi - it.lo;
                 if (blocks <= 0) continue;
@@ -349,7 +349,7 @@ softmax_attn_dq_kernel(const __grid_constant__ CUtensorMap tQ, const __grid_cons
         const uint32_t lanes = (uint32_t)((warp & 3) * 32) << 16;
         const float sl = p.scale_log2;
         int n = 0, items = 0;
-        for (int64_t idx = blockIdx.x; idx < p.items; idx += gridDim.x) {
+        for (int idx = blockIdx.x; idx < p.items; idx += gridDim.x) {
             const DqItem it = dq_item(p, idx);
             const int lo = it.lo, hi = it.hi;
             // -lse and -delta of sixteen rows a warp (rows read by whole warps, 8 bytes a lane),
@@ -471,8 +471,8 @@ softmax_attn_dq_kernel(const __grid_constant__ CUtensorMap tQ, const __grid_cons
                 tc_fence_after();
             }
             // (derived again: kept through the loop, it would cost registers there)
-            int64_t again = idx;
-            asm volatile("" : "+l"(again));
+            int again = idx;
+            asm volatile("" : "+r"(again));
             const DqItem at = dq_item(p, again);
             const int i = at.q0 + row;
             const bool exists = i < p.nq, valid = i < at.sp.Lq;
@@ -515,13 +515,13 @@ struct DkvItem {
     int batch, kvh, k0, lo, hi;  // query tiles [lo, hi) of each head of the group
     Span sp;
 };
-__device__ __forceinline__ DkvItem dkv_item(const BwdParams &p, int64_t idx) {
+__device__ __forceinline__ DkvItem dkv_item(const BwdParams &p, int idx) {
     DkvItem it;
     const int units = p.b * p.hk;
-    const int u = (int)(idx % units);
-    it.k0 = (int)(idx / units) * kTile;  // causal: early keys are seen by the most queries
+    const int block = idx / units, u = idx - block * units;
+    it.k0 = block * kTile;  // causal: early keys are seen by the most queries
     it.batch = u / p.hk;
-    it.kvh = u % p.hk;
+    it.kvh = u - it.batch * p.hk;
     it.sp = Span{clamp_length(p.q_lengths, it.batch, p.nq), clamp_length(p.k_lengths, it.batch, p.nk),
                  p.causal, p.window};
     it.lo = it.hi = 0;
@@ -601,7 +601,7 @@ softmax_attn_dkv_kernel(const __grid_constant__ CUtensorMap tQ, const __grid_con
         if (lane == 0) {
             int ring = 0, items = 0;
             bool ok = true;
-            for (int64_t idx = blockIdx.x; idx < p.items && ok; idx += gridDim.x) {
+            for (int idx = blockIdx.x; idx < p.items && ok; idx += gridDim.x) {
                 const DkvItem it = dkv_item(p, idx);
                 if (it.hi <= it.lo) continue;
                 const int kb = items % C::kKv;
@@ -636,7 +636,7 @@ softmax_attn_dkv_kernel(const __grid_constant__ CUtensorMap tQ, const __grid_con
         } else {  // Q and dO rows past the valid length: P and dS are 0 there, but 0 x NaN is not
             int ring = 0, nfix = 0;
             bool ok = true;
-            for (int64_t idx = blockIdx.x; idx < p.items && ok; idx += gridDim.x) {
+            for (int idx = blockIdx.x; idx < p.items && ok; idx += gridDim.x) {
                 const DkvItem it = dkv_item(p, idx);
                 if (it.hi <= it.lo) continue;
                 if (it.sp.Lq >= p.nq || it.hi * kTile <= it.sp.Lq) {
@@ -669,7 +669,7 @@ softmax_attn_dkv_kernel(const __grid_constant__ CUtensorMap tQ, const __grid_con
                      *ready = first ? bar->p_full : bar->ds_full;
             auto phase = [](int g) { return (uint32_t)(g >> 1) & 1u; };
             auto buffer = [&](int g) { return tmem + 128 * ((2 * g + (first ? 0 : 1)) % C::kBufs); };
-            for (int64_t idx = blockIdx.x; idx < p.items && ok; idx += gridDim.x) {
+            for (int idx = blockIdx.x; idx < p.items && ok; idx += gridDim.x) {
                 const DkvItem it = dkv_item(p, idx);
                 const int per = it.hi - it.lo;
                 if (per <= 0) continue;
@@ -746,7 +746,7 @@ softmax_attn_dkv_kernel(const __grid_constant__ CUtensorMap tQ, const __grid_con
         const float2 sl2 = make_float2(sl, sl);
         int n = 0, items = 0;
         bool ok = true;
-        for (int64_t idx = blockIdx.x; idx < p.items && ok; idx += gridDim.x) {
+        for (int idx = blockIdx.x; idx < p.items && ok; idx += gridDim.x) {
             int lo, hi, steps, first, end;
             {
                 const DkvItem it = dkv_item(p, idx);
@@ -847,8 +847,8 @@ softmax_attn_dkv_kernel(const __grid_constant__ CUtensorMap tQ, const __grid_con
                 ++items;
             }
             // (derived again: kept through the loop, it would cost registers there)
-            int64_t again = idx;
-            asm volatile("" : "+l"(again));
+            int again = idx;
+            asm volatile("" : "+r"(again));
             const DkvItem it = dkv_item(p, again);
             const int key = it.k0 + row;
             const bool exists = key < p.nk, valid = key < it.sp.Lk;
@@ -889,19 +889,20 @@ int launch(const Call &c, BwdParams &p) {
     if (st) return st;
     void *ws = nullptr;
     const int64_t qitems = (int64_t)c.b * c.hq * p.qtiles, kitems = (int64_t)c.b * c.hk * p.kblocks;
+    if (qitems > kMaxItems || kitems > kMaxItems) return LINFORMER_ERR_SIZE;
     if (workspace_alloc(&ws, (size_t)qitems * 1024, c.stream) != LINFORMER_OK) return LINFORMER_ERR_ALLOC;
     p.rows = static_cast<float *>(ws);
     const int sms = device_sms();
     {
         KernelScope scope(LINFORMER_KERNEL_SOFTMAX_BWD, c.stream);
-        p.items = qitems;
+        p.items = (int)qitems;
         softmax_attn_dq_kernel<DP><<<(int)std::min<int64_t>(qitems, sms), kThreads, Cq::kSmem, c.stream>>>(
             tQ, tK, tV, tdO, p);
         if (cudaGetLastError() != cudaSuccess) st = LINFORMER_ERR_LAUNCH;
     }
     if (!st) {
         KernelScope scope(LINFORMER_KERNEL_SOFTMAX_BWD, c.stream);
-        p.items = kitems;
+        p.items = (int)kitems;
         softmax_attn_dkv_kernel<DP><<<(int)std::min<int64_t>(kitems, sms), kThreads, Ck::kSmem, c.stream>>>(
             tQ, tK, tV, tdO, p);
         if (cudaGetLastError() != cudaSuccess) st = LINFORMER_ERR_LAUNCH;

@@ -59,7 +59,7 @@ struct FwdParams {
     float *part_o, *part_lse;  // with splits: [split][b][hq][nq][DP] and [split][b][hq][nq]
     int b, hq, hk, group, nq, nk, d, causal, window;
     int qbox, hbox, nch, ntiles, npairs, nsplit, units;
-    int64_t items;
+    int items;
     float scale, scale_log2;
     int *status;
 };
@@ -87,16 +87,22 @@ struct Item {
     int lo, hi;  // union of the tiles' blocks
 };
 
-__device__ __forceinline__ Item load_item(const FwdParams &p, int64_t idx) {
+__device__ __forceinline__ Item load_item(const FwdParams &p, int idx) {
     Item it;
-    const int u = (int)(idx % p.units);
-    const int64_t r = idx / p.units;
-    it.split = (int)(r % p.nsplit);
-    const int rank = (int)(r / p.nsplit);
+    // (32-bit divisions, and none where the divisor is often one: every role does this for
+    // every item)
+    int rank = idx / p.units;
+    const int u = idx - rank * p.units;
+    it.split = 0;
+    if (p.nsplit > 1) {
+        const int r = rank;
+        rank = r / p.nsplit;
+        it.split = r - rank * p.nsplit;
+    }
     // causal rows further down see more keys: the longest items first
     const int pair = p.causal ? p.npairs - 1 - rank : rank;
     it.batch = u / p.hk;
-    it.kvh = u % p.hk;
+    it.kvh = u - it.batch * p.hk;
     it.sp = Span{clamp_length(p.q_lengths, it.batch, p.nq),
                  clamp_length(p.k_lengths, it.batch, p.nk), p.causal, p.window};
     it.lo = 1 << 30;
@@ -106,8 +112,9 @@ __device__ __forceinline__ Item load_item(const FwdParams &p, int64_t idx) {
         const int lin = 2 * pair + t;
         Tile &x = it.t[t];
         x.live = lin < p.ntiles;
-        x.q0 = lin / p.nch * p.qbox;
-        x.h0 = lin % p.nch * p.hbox;
+        const int qt = p.nch > 1 ? lin / p.nch : lin;
+        x.q0 = qt * p.qbox;
+        x.h0 = (lin - qt * p.nch) * p.hbox;
         x.lo = x.hi = 0;
         const int last = min(x.q0 + p.qbox, it.sp.Lq) - 1;
         if (x.live && last >= x.q0) {
@@ -252,7 +259,7 @@ softmax_attn_fwd_kernel(const __grid_constant__ CUtensorMap tQ, const __grid_con
         if (lane == 0) {  // ---------------- loads
             int ring = 0, nq[2] = {0, 0};
             bool ok = true;
-            for (int64_t idx = blockIdx.x; idx < p.items && ok; idx += gridDim.x) {
+            for (int idx = blockIdx.x; idx < p.items && ok; idx += gridDim.x) {
                 const Item it = load_item(p, idx);
                 for (int t = 0; t < 2 && ok; ++t) {
                     if (it.t[t].hi <= it.t[t].lo) continue;
@@ -287,7 +294,7 @@ softmax_attn_fwd_kernel(const __grid_constant__ CUtensorMap tQ, const __grid_con
                 mbar_wait_drain(&bar->full[i % C::kStages], (i / C::kStages) & 1);
         } else {  // ---------------- V rows past the valid length
             int ring = 0, nfix = 0;
-            for (int64_t idx = blockIdx.x; idx < p.items; idx += gridDim.x) {
+            for (int idx = blockIdx.x; idx < p.items; idx += gridDim.x) {
                 const Item it = load_item(p, idx);
                 const int blocks = max(0, it.hi - it.lo);
                 ring += 2 * blocks;
@@ -327,7 +334,7 @@ softmax_attn_fwd_kernel(const __grid_constant__ CUtensorMap tQ, const __grid_con
                            dv0 = sdesc(smem_u32(sKV) + C::kTileBytes, 16384, 1024, kSwizzle128B);
             int nfix = 0, n = 0, items = 0;  // fixed blocks, the tile's blocks and items
             bool ok = true;
-            for (int64_t idx = blockIdx.x; idx < p.items && ok; idx += gridDim.x) {
+            for (int idx = blockIdx.x; idx < p.items && ok; idx += gridDim.x) {
                 const Item it = load_item(p, idx);
                 const int lo = t ? it.t[1].lo : it.t[0].lo, hi = t ? it.t[1].hi : it.t[0].hi;
                 const bool fix = ragged_end(it, p.nk);
@@ -417,7 +424,7 @@ softmax_attn_fwd_kernel(const __grid_constant__ CUtensorMap tQ, const __grid_con
             }
             return ok;
         };
-        for (int64_t idx = blockIdx.x; idx < p.items && ok; idx += gridDim.x) {
+        for (int idx = blockIdx.x; idx < p.items && ok; idx += gridDim.x) {
             int lo, hi, first, end;
             bool valid, warp_valid;
             {
@@ -506,8 +513,8 @@ rescale_output(tO, DP, f);
             // O / l out of TMEM; rows without keys give O = 0 and lse = -inf
             const bool some = hi > lo;
             // (derived again: kept through the loop, it would cost registers there)
-            int64_t again = idx;
-            asm volatile("" : "+l"(again));
+            int again = idx;
+            asm volatile("" : "+r"(again));
             const Item it = load_item(p, again);
             const Tile x = t ? it.t[1] : it.t[0];
             const int i = x.q0 + qi, hg = x.h0 + hi_;
@@ -633,7 +640,7 @@ int launch(const Call &c, FwdParams &p) {
     int st = allow_smem(reinterpret_cast<const void *>(softmax_attn_fwd_kernel<DP>), C::kSmem, DP == 64 ? 0 : 1);
     if (!st) {
         KernelScope scope(LINFORMER_KERNEL_SOFTMAX, c.stream);
-        const int grid = (int)std::min<int64_t>(p.items, device_sms());
+        const int grid = (int)std::min(p.items, device_sms());
         softmax_attn_fwd_kernel<DP><<<grid, kThreads, C::kSmem, c.stream>>>(tQ, tK, tV, p);
         if (cudaGetLastError() != cudaSuccess) st = LINFORMER_ERR_LAUNCH;
     }
@@ -728,13 +735,14 @@ int forward(const Call &c) {
     p.npairs = (p.ntiles + 1) / 2;
     p.units = c.b * c.hk;
     const int64_t whole = (int64_t)p.units * p.npairs;
+    if (whole > kMaxItems) return LINFORMER_ERR_SIZE;
     const int sms = device_sms();
     // With fewer items than SMs the keys are split, at least kMinBlocks blocks a part.
     constexpr int kMinBlocks = 4;
     const int reach = c.window ? std::min(c.nk, c.window + kTile) : c.nk;
     const int blocks = (reach + kTile - 1) / kTile;
     p.nsplit = (int)std::max<int64_t>(1, std::min<int64_t>(sms / whole, blocks / kMinBlocks));
-    p.items = whole * p.nsplit;
+    p.items = (int)whole * p.nsplit;
     return c.d <= 64 ? launch<64>(c, p) : launch<128>(c, p);
 }
 
