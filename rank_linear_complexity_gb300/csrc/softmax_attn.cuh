@@ -49,6 +49,20 @@ __device__ __forceinline__ uint32_t pack2(float a, float b) {
     return *reinterpret_cast<uint32_t *>(&v);
 }
 
+// Whether every 16 columns of a tensor are 32 aligned bytes (strides of dimensions of size one
+// do not count, but are harmless when they say no).
+inline int wide_stores(const void *p, const Strides &s, int d) {
+    return (reinterpret_cast<uintptr_t>(p) % 32 == 0 && d % 16 == 0 && s.b % 16 == 0 && s.h % 16 == 0 &&
+            s.n % 16 == 0)
+               ? 1
+               : 0;
+}
+__device__ __forceinline__ void store32(void *p, const uint32_t (&w)[8]) {
+    asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(p), "r"(w[0]),
+                 "r"(w[1]), "r"(w[2]), "r"(w[3]), "r"(w[4]), "r"(w[5]), "r"(w[6]), "r"(w[7])
+                 : "memory");
+}
+
 // Eight bf16 of a 16-byte piece as floats.
 __device__ __forceinline__ void unpack8(const uint4 &v, float (&f)[8]) {
     const uint32_t w[4] = {v.x, v.y, v.z, v.w};

@@ -4,10 +4,10 @@
 //     dP = dO V^T,   dS_ij = P_ij (dP_ij - delta_i),
 //     dV = P^T dO,   dK = scale dS^T Q,   dQ = scale dS K,
 //
-// two kernels, each a sum that one CTA owns, so that no gradient is added up by atomics
+// two kernels after a small one, each a sum that one CTA owns, so that no gradient is added up by atomics
 // and every result repeats bit for bit:
-//   dq_kernel   a 128-row query tile against its key blocks: S, dP, then dQ += dS.K.  It
-//               also forms delta and leaves (lse, delta) per row for the second kernel.
+//   rows_kernel  -lse log2(e) and -delta of every query row, for the other two.
+//   dq_kernel   a 128-row query tile against its key blocks: S, dP, then dQ += dS.K.
 //   dkv_kernel  a 128-key block against the query tiles of every head of its group:
 //               S^T = K.Q^T and dP^T = V.dO^T, then dV += P^T.dO and dK += dS^T.Q.  With
 //               keys as the rows, P^T and dS^T leave the registers of the thread that made
@@ -55,6 +55,7 @@ struct BwdParams {
     float *rows;
     int b, hq, hk, group, nq, nk, d, causal, window;
     int qtiles, kblocks;
+    int wide;  // bits: dQ, dK, dV take 32-byte stores
     int items;
     float scale, scale_log2;
     int *status;
@@ -89,20 +90,20 @@ __device__ __forceinline__ float dot2(uint32_t a, uint32_t b) {
     return __uint_as_float(a << 16) * __uint_as_float(b << 16) +
            __uint_as_float(a & 0xffff0000u) * __uint_as_float(b & 0xffff0000u);
 }
-// 16 columns of a row, scaled and rounded (columns from d on do not exist).
+// 16 columns of a row, scaled and rounded (columns from d on do not exist): one 32-byte store
+// where the tensor allows it (a warp's store touches 32 rows, and each row's line costs a
+// cycle of the load/store unit), else two of 16 bytes.
 __device__ __forceinline__ void store_row(__nv_bfloat16 *dst, const uint32_t (&o)[16], int c, int d,
-                                          float f, bool zero) {
+                                          float f, bool zero, bool wide) {
+    uint32_t w[8];
 #pragma unroll
-    for (int e = 0; e < 16; e += 8) {
-        if (c + e >= d) break;
-        uint4 w = make_uint4(0u, 0u, 0u, 0u);
-        if (!zero) {
-            w.x = pack2(__uint_as_float(o[e]) * f, __uint_as_float(o[e + 1]) * f);
-            w.y = pack2(__uint_as_float(o[e + 2]) * f, __uint_as_float(o[e + 3]) * f);
-            w.z = pack2(__uint_as_float(o[e + 4]) * f, __uint_as_float(o[e + 5]) * f);
-            w.w = pack2(__uint_as_float(o[e + 6]) * f, __uint_as_float(o[e + 7]) * f);
-        }
-        *reinterpret_cast<uint4 *>(dst + c + e) = w;
+    for (int e = 0; e < 8; ++e)
+        w[e] = zero ? 0u : pack2(__uint_as_float(o[2 * e]) * f, __uint_as_float(o[2 * e + 1]) * f);
+    if (wide) {
+        if (c < d) store32(dst + c, w);
+    } else {
+        if (c < d) *reinterpret_cast<uint4 *>(dst + c) = make_uint4(w[0], w[1], w[2], w[3]);
+        if (c + 8 < d) *reinterpret_cast<uint4 *>(dst + c + 8) = make_uint4(w[4], w[5], w[6], w[7]);
     }
 }
 
@@ -132,6 +133,43 @@ __device__ __forceinline__ void load_rows(uint8_t *dst, const CUtensorMap *m, ui
                                           int head, int group, int batch) {
 #pragma unroll
     for (int h = 0; h < DP / 64; ++h) tma_load_5d(dst + h * 16384, m, bar, h * 64, row, head, group, batch);
+}
+
+// ---------------------------------------------------------------- row values
+// -lse log2(e) and -delta = -dO.O of a query tile's 128 rows, eight warps of sixteen rows, read
+// by whole warps (8 bytes a lane).  Bound by memory: O and dO once.
+constexpr int kRowsThreads = 256;
+__global__ void __launch_bounds__(kRowsThreads) rows_kernel(const BwdParams p) {
+    launch_dependents();
+    const int unit = blockIdx.x / p.qtiles, tile = blockIdx.x - unit * p.qtiles;
+    const int batch = unit / p.hq, head = unit - batch * p.hq;
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, r0 = tile * kTile + 16 * warp;
+    const int Lq = clamp_length(p.q_lengths, batch, p.nq);
+    const __nv_bfloat16 *o = p.O + batch * p.sO.b + head * p.sO.h + 4 * lane;
+    const __nv_bfloat16 *g = p.dO + batch * p.sdO.b + head * p.sdO.h + 4 * lane;
+    uint2 a[16], b[16];
+#pragma unroll
+    for (int r = 0; r < 16; ++r) {
+        a[r] = b[r] = make_uint2(0u, 0u);
+        if (r0 + r < Lq && 4 * lane < p.d) {
+            a[r] = __ldg(reinterpret_cast<const uint2 *>(o + (int64_t)(r0 + r) * p.sO.n));
+            b[r] = __ldg(reinterpret_cast<const uint2 *>(g + (int64_t)(r0 + r) * p.sdO.n));
+        }
+    }
+    float x = -INFINITY, delta = 0.f;
+    if (lane < 16 && r0 + lane < Lq) x = __ldg(p.lse + (int64_t)unit * p.nq + r0 + lane);
+#pragma unroll
+    for (int r = 0; r < 16; ++r) {
+        float y = dot2(a[r].x, b[r].x) + dot2(a[r].y, b[r].y);
+#pragma unroll
+        for (int k = 16; k; k >>= 1) y += __shfl_xor_sync(0xffffffffu, y, k);
+        if (lane == r) delta = y;
+    }
+    if (lane < 16) {
+        float *dst = p.rows + (int64_t)blockIdx.x * 256 + 16 * warp + lane;
+        dst[0] = x == -INFINITY ? -INFINITY : -x * kLog2e;
+        dst[128] = x == -INFINITY ? 0.f : -delta;
+    }
 }
 
 // ---------------------------------------------------------------- dQ
@@ -172,11 +210,10 @@ struct DqBarriers {
     // (pairs: even and odd blocks, each with a group of warps of its own)
     uint64_t q_full, q_free, s_full[2], s_free, dp_full[2], ds_full[2], dq_done[2], acc_full, acc_free;
     uint64_t fix_wanted, fixed, drain[2];
-    uint64_t full[8], empty[8], rows_ready;
+    uint64_t full[8], empty[8];
     uint32_t tmem;
     int abort;
-    // -lse and -delta of the item's rows (written once all warps have left the item before)
-    float rows[2 * kTile];
+    alignas(16) float rows[2 * kTile];  // the item's rows, loaded with Q and dO
 };
 
 static_assert(sizeof(DqBarriers) <= 512 + 1024, "room for the barriers");
@@ -196,7 +233,7 @@ softmax_attn_dq_kernel(const __grid_constant__ CUtensorMap tQ, const __grid_cons
 
     if (tid == 0) {
         mbar_init(&bar->q_full, 1);
-        mbar_init(&bar->q_free, 1);
+        mbar_init(&bar->q_free, 1 + kMathWarps);  // the products, and the rows read
         mbar_init(&bar->s_free, kGroupWarps);
         for (int i = 0; i < 2; ++i) {
             mbar_init(&bar->s_full[i], 1);
@@ -204,7 +241,6 @@ softmax_attn_dq_kernel(const __grid_constant__ CUtensorMap tQ, const __grid_cons
             mbar_init(&bar->ds_full[i], kGroupWarps);
             mbar_init(&bar->dq_done[i], 1);
         }
-        mbar_init(&bar->rows_ready, kMathWarps);
         mbar_init(&bar->acc_full, 1);
         mbar_init(&bar->acc_free, kMathWarps);
         mbar_init(&bar->fix_wanted, 1);
@@ -231,14 +267,18 @@ softmax_attn_dq_kernel(const __grid_constant__ CUtensorMap tQ, const __grid_cons
     setmaxnreg_dec<kIssueRegs>();
     if (warp == kLoadWarp) {
         if (lane == 0) {
+            wait_prerequisites();  // the row values; and only then may the third kernel start
+            launch_dependents();
             int ring = 0, nq = 0;
             bool ok = true;
             for (int idx = blockIdx.x; idx < p.items && ok; idx += gridDim.x) {
                 const DqItem it = dq_item(p, idx);
                 if (it.hi <= it.lo) continue;
                 if (nq > 0 && !thread_spin(&bar->q_free, (nq - 1) & 1, p.status, 83, abort_flag)) break;
-                mbar_arrive_expect_tx(&bar->q_full, 2 * C::kTileBytes);
+                mbar_arrive_expect_tx(&bar->q_full, 2 * C::kTileBytes + 1024);
                 const int g = it.head % p.group, kvh = it.head / p.group;
+                bulk_load(bar->rows, p.rows + (((int64_t)it.batch * p.hq + it.head) * p.qtiles + it.q0 / kTile) * 256,
+                          1024, &bar->q_full);
                 load_rows<DP>(sQ, &tQ, &bar->q_full, it.q0, g, kvh, it.batch);
                 load_rows<DP>(sdO, &tdO, &bar->q_full, it.q0, g, kvh, it.batch);
                 ++nq;
@@ -352,53 +392,13 @@ softmax_attn_dq_kernel(const __grid_constant__ CUtensorMap tQ, const __grid_cons
         for (int idx = blockIdx.x; idx < p.items; idx += gridDim.x) {
             const DqItem it = dq_item(p, idx);
             const int lo = it.lo, hi = it.hi;
-            // -lse and -delta of sixteen rows a warp (rows read by whole warps, 8 bytes a lane),
-            // for this kernel through shared memory and for the other one.
-            float *sm = bar->rows;
-            {
-                const __nv_bfloat16 *o = p.O + it.batch * p.sO.b + it.head * p.sO.h + 4 * lane;
-                const __nv_bfloat16 *g = p.dO + it.batch * p.sdO.b + it.head * p.sdO.h + 4 * lane;
-                const int r0 = it.q0 + 16 * warp;
-                uint2 a[16], b[16];
-#pragma unroll
-                for (int r = 0; r < 16; ++r) {
-                    a[r] = b[r] = make_uint2(0u, 0u);
-                    if (r0 + r < it.sp.Lq && 4 * lane < p.d) {
-                        a[r] = __ldg(reinterpret_cast<const uint2 *>(o + (int64_t)(r0 + r) * p.sO.n));
-                        b[r] = __ldg(reinterpret_cast<const uint2 *>(g + (int64_t)(r0 + r) * p.sdO.n));
-                    }
-                }
-                float x = -INFINITY, del = 0.f;
-                if (lane < 16 && r0 + lane < it.sp.Lq)
-                    x = __ldg(p.lse + ((int64_t)it.batch * p.hq + it.head) * p.nq + r0 + lane);
-#pragma unroll
-                for (int r = 0; r < 16; ++r) {
-                    float y = dot2(a[r].x, b[r].x) + dot2(a[r].y, b[r].y);
-#pragma unroll
-                    for (int k = 16; k; k >>= 1) y += __shfl_xor_sync(0xffffffffu, y, k);
-                    if (lane == r) del = y;
-                }
-                if (it.hi > it.lo && items > 0 &&
-                    !warp_spin(&bar->acc_free, (items - 1) & 1, p.status, 99, abort_flag))
-                    break;
-                if (lane < 16) {
-                    const float nl = x == -INFINITY ? -INFINITY : -x * kLog2e, nd = x == -INFINITY ? 0.f : -del;
-                    float *dst = p.rows + (((int64_t)it.batch * p.hq + it.head) * p.qtiles + it.q0 / kTile) * 256;
-                    dst[16 * warp + lane] = nl;
-                    dst[128 + 16 * warp + lane] = nd;
-                    if (it.hi > it.lo) {
-                        sm[16 * warp + lane] = nl;
-                        sm[128 + 16 * warp + lane] = nd;
-                    }
-                }
-            }
-            float nl = -INFINITY, nd = 0.f;
-            if (it.hi > it.lo) {
+            float nl = 0.f, nd = 0.f;
+            if (hi > lo) {  // the row values come with Q and dO
+                if (!warp_spin(&bar->q_full, items & 1, p.status, 97, abort_flag)) break;
+                nl = bar->rows[row];
+                nd = bar->rows[128 + row];
                 __syncwarp();
-                if (lane == 0) mbar_arrive(&bar->rows_ready);
-                if (!warp_spin(&bar->rows_ready, items & 1, p.status, 97, abort_flag)) break;
-                nl = sm[row];
-                nd = sm[128 + row];
+                if (lane == 0) mbar_arrive(&bar->q_free);
                 ++items;
             }
             const bool seen = it.q0 + row < it.sp.Lq;
@@ -470,19 +470,15 @@ softmax_attn_dq_kernel(const __grid_constant__ CUtensorMap tQ, const __grid_cons
                 if (!warp_spin(&bar->acc_full, (items - 1) & 1, p.status, 96, abort_flag)) break;
                 tc_fence_after();
             }
-            // (derived again: kept through the loop, it would cost registers there)
-            int again = idx;
-            asm volatile("" : "+r"(again));
-            const DqItem at = dq_item(p, again);
-            const int i = at.q0 + row;
-            const bool exists = i < p.nq, valid = i < at.sp.Lq;
-            __nv_bfloat16 *dst = p.dQ + at.batch * p.sdQ.b + at.head * p.sdQ.h + (int64_t)i * p.sdQ.n;
+            const int i = it.q0 + row;
+            const bool exists = i < p.nq, valid = i < it.sp.Lq;
+            __nv_bfloat16 *dst = p.dQ + it.batch * p.sdQ.b + it.head * p.sdQ.h + (int64_t)i * p.sdQ.n;
 #pragma unroll
             for (int c = 0; c < DP / 2; c += 16) {
                 uint32_t o[16];
                 const int col = group * (DP / 2) + c;
                 if (some) tmem_ld16(tmem + C::kDq + col + lanes, o);
-                if (exists) store_row(dst, o, col, p.d, p.scale, !some || !valid);
+                if (exists) store_row(dst, o, col, p.d, p.scale, !some || !valid, p.wide & 1);
             }
             if (some) {
                 tc_fence_before();
@@ -747,18 +743,13 @@ softmax_attn_dkv_kernel(const __grid_constant__ CUtensorMap tQ, const __grid_con
         int n = 0, items = 0;
         bool ok = true;
         for (int idx = blockIdx.x; idx < p.items && ok; idx += gridDim.x) {
-            int lo, hi, steps, first, end;
-            {
-                const DkvItem it = dkv_item(p, idx);
-                const int key = it.k0 + row, off = it.sp.Lk - it.sp.Lq;
-                lo = it.lo;
-                hi = it.hi;
-                steps = (hi - lo) * p.group;
-                // queries [first, end) see this key (the rows past the length need no mask:
-                // their -lse is -inf)
-                first = p.causal ? max(0, key - off) : 0;
-                end = p.window ? (int)min((long long)it.sp.Lq, (long long)key - off + p.window) : 1 << 30;
-            }
+            const DkvItem it = dkv_item(p, idx);
+            const int key = it.k0 + row, off = it.sp.Lk - it.sp.Lq, lo = it.lo, hi = it.hi,
+                      steps = (hi - lo) * p.group;
+            // queries [first, end) see this key (the rows past the length need no mask: their
+            // -lse is -inf)
+            const int first = p.causal ? max(0, key - off) : 0;
+            const int end = p.window ? (int)min((long long)it.sp.Lq, (long long)key - off + p.window) : 1 << 30;
             const unsigned width = end > first ? (unsigned)(end - first) : 0u;
             const int skip = (n ^ group) & 1, per = hi - lo;
             int j = skip && per > 0 ? skip % per : 0;  // tile of the step within its head
@@ -846,11 +837,6 @@ softmax_attn_dkv_kernel(const __grid_constant__ CUtensorMap tQ, const __grid_con
                 tc_fence_after();
                 ++items;
             }
-            // (derived again: kept through the loop, it would cost registers there)
-            int again = idx;
-            asm volatile("" : "+r"(again));
-            const DkvItem it = dkv_item(p, again);
-            const int key = it.k0 + row;
             const bool exists = key < p.nk, valid = key < it.sp.Lk;
             __nv_bfloat16 *dk = p.dK + it.batch * p.sdK.b + it.kvh * p.sdK.h + (int64_t)key * p.sdK.n;
             __nv_bfloat16 *dv = p.dV + it.batch * p.sdV.b + it.kvh * p.sdV.h + (int64_t)key * p.sdV.n;
@@ -859,7 +845,8 @@ softmax_attn_dkv_kernel(const __grid_constant__ CUtensorMap tQ, const __grid_con
             for (int c = 0; c < DP; c += 16) {
                 uint32_t o[16];
                 if (some) tmem_ld16(tmem + (group ? C::kDk : C::kDv) + c + lanes, o);
-                if (exists) store_row(group ? dk : dv, o, c, p.d, group ? p.scale : 1.f, !some || !valid);
+                if (exists) store_row(group ? dk : dv, o, c, p.d, group ? p.scale : 1.f, !some || !valid,
+                                      p.wide >> (group ? 1 : 2) & 1);
             }
             if (some) {
                 tc_fence_before();
@@ -868,6 +855,7 @@ softmax_attn_dkv_kernel(const __grid_constant__ CUtensorMap tQ, const __grid_con
             }
         }
     }
+    if (warp == kLoadWarp) wait_prerequisites();  // no later kernel before the second one has ended
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
@@ -895,18 +883,37 @@ int launch(const Call &c, BwdParams &p) {
     const int sms = device_sms();
     {
         KernelScope scope(LINFORMER_KERNEL_SOFTMAX_BWD, c.stream);
-        p.items = (int)qitems;
-        softmax_attn_dq_kernel<DP><<<(int)std::min<int64_t>(qitems, sms), kThreads, Cq::kSmem, c.stream>>>(
-            tQ, tK, tV, tdO, p);
+        rows_kernel<<<(unsigned)qitems, kRowsThreads, 0, c.stream>>>(p);
         if (cudaGetLastError() != cudaSuccess) st = LINFORMER_ERR_LAUNCH;
+    }
+    // The other two as programmatic dependents: the second is set up while the first ends, and
+    // the third, which needs only the first one's rows, takes over SMs as the second leaves
+    // them (and ends after it).
+    cudaLaunchConfig_t cfg{};
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    cfg.blockDim = dim3(kThreads);
+    cfg.stream = c.stream;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    if (!st) {
+        KernelScope scope(LINFORMER_KERNEL_SOFTMAX_BWD, c.stream);
+        p.items = (int)qitems;
+        cfg.gridDim = dim3((unsigned)std::min<int64_t>(qitems, sms));
+        cfg.dynamicSmemBytes = Cq::kSmem;
+        if (cudaLaunchKernelEx(&cfg, softmax_attn_dq_kernel<DP>, tQ, tK, tV, tdO, p) != cudaSuccess)
+            st = LINFORMER_ERR_LAUNCH;
     }
     if (!st) {
         KernelScope scope(LINFORMER_KERNEL_SOFTMAX_BWD, c.stream);
         p.items = (int)kitems;
-        softmax_attn_dkv_kernel<DP><<<(int)std::min<int64_t>(kitems, sms), kThreads, Ck::kSmem, c.stream>>>(
-            tQ, tK, tV, tdO, p);
-        if (cudaGetLastError() != cudaSuccess) st = LINFORMER_ERR_LAUNCH;
+        cfg.gridDim = dim3((unsigned)std::min<int64_t>(kitems, sms));
+        cfg.dynamicSmemBytes = Ck::kSmem;
+        if (cudaLaunchKernelEx(&cfg, softmax_attn_dkv_kernel<DP>, tQ, tK, tV, tdO, p) != cudaSuccess)
+            st = LINFORMER_ERR_LAUNCH;
     }
+    if (st) cudaGetLastError();
     workspace_free(ws, c.stream);
     return st;
 }
@@ -941,6 +948,7 @@ int backward(const Call &c) {
     p.kblocks = (c.nk + kTile - 1) / kTile;
     p.scale = c.scale;
     p.scale_log2 = c.scale * kLog2e;
+    p.wide = wide_stores(c.dQ, c.sdQ, c.d) | wide_stores(c.dK, c.sdK, c.d) << 1 | wide_stores(c.dV, c.sdV, c.d) << 2;
     p.status = device_status_ptr();
     return c.d <= 64 ? launch<64>(c, p) : launch<128>(c, p);
 }

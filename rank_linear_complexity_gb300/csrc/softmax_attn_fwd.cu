@@ -61,6 +61,7 @@ struct FwdParams {
     int qbox, hbox, nch, ntiles, npairs, nsplit, units;
     int items;
     float scale, scale_log2;
+    int wide;  // O takes 32-byte stores
     int *status;
 };
 
@@ -548,22 +549,21 @@ rescale_output(tO, DP, f);
             } else {
                 __nv_bfloat16 *dst = p.out + it.batch * p.so.b + head * p.so.h + (int64_t)i * p.so.n;
 #pragma unroll
-                for (int c = 0; c < DP; c += 32) {
-                    uint32_t o[32];
-                    if (some && warp_valid) tmem_ld32(tO + c, o);
-                    if (exists)
+                for (int c = 0; c < DP; c += 16) {
+                    uint32_t o[16], y[8];
+                    if (some && warp_valid) tmem_ld16(tO + c, o);
+                    if (!exists || c >= p.d) continue;
 #pragma unroll
-                        for (int e = 0; e < 32; e += 8) {
-                            if (c + e >= p.d) break;
-                            uint4 w = make_uint4(0u, 0u, 0u, 0u);
-                            if (!dead) {
-                                w.x = pack2(__uint_as_float(o[e]) * inv, __uint_as_float(o[e + 1]) * inv);
-                                w.y = pack2(__uint_as_float(o[e + 2]) * inv, __uint_as_float(o[e + 3]) * inv);
-                                w.z = pack2(__uint_as_float(o[e + 4]) * inv, __uint_as_float(o[e + 5]) * inv);
-                                w.w = pack2(__uint_as_float(o[e + 6]) * inv, __uint_as_float(o[e + 7]) * inv);
-                            }
-                            *reinterpret_cast<uint4 *>(dst + c + e) = w;
-                        }
+                    for (int e = 0; e < 8; ++e)
+                        y[e] = dead ? 0u : pack2(__uint_as_float(o[2 * e]) * inv, __uint_as_float(o[2 * e + 1]) * inv);
+                    // one store of 32 bytes where the tensor allows it: a warp's store touches
+                    // 32 rows, and each row's line costs a cycle of the load/store unit
+                    if (p.wide) {
+                        store32(dst + c, y);
+                    } else {
+                        *reinterpret_cast<uint4 *>(dst + c) = make_uint4(y[0], y[1], y[2], y[3]);
+                        if (c + 8 < p.d) *reinterpret_cast<uint4 *>(dst + c + 8) = make_uint4(y[4], y[5], y[6], y[7]);
+                    }
                 }
                 if (exists) p.lse[r] = lse;
             }
@@ -724,6 +724,7 @@ int forward(const Call &c) {
     p.window = c.window;
     p.scale = c.scale;
     p.scale_log2 = c.scale * kLog2e;
+    p.wide = wide_stores(c.out, c.sO, c.d);
     p.status = device_status_ptr();
     // Rows of a tile: 128 positions of one head, or the smallest power of two that holds
     // all positions times as many heads of the group as fit.
