@@ -253,6 +253,7 @@ softmax_attn_fwd_kernel(const __grid_constant__ CUtensorMap tQ, const __grid_con
     __syncthreads();
     tc_fence_after();
     const uint32_t tmem = bar->tmem;
+    if (p.nsplit > 1 && tid == 0) launch_dependents();  // the join, which waits for this grid's end
 
     if (warp >= kLoadWarp) {
     setmaxnreg_dec<kIssueRegs>();
@@ -588,6 +589,7 @@ __global__ void __launch_bounds__(128) join_kernel(const FwdParams p) {
     const int64_t r = (int64_t)blockIdx.x * 4 + (threadIdx.x >> 5);
     const int lane = threadIdx.x & 31;
     if (r >= rows) return;
+    wait_prerequisites();
     float m = -INFINITY;
     for (int s = lane; s < p.nsplit; s += 32) m = fmaxf(m, p.part_lse[s * rows + r]);
     for (int o = 16; o; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
@@ -647,8 +649,20 @@ int launch(const Call &c, FwdParams &p) {
     if (!st && p.nsplit > 1) {
         KernelScope scope(LINFORMER_KERNEL_SOFTMAX, c.stream);
         const int64_t rows = (int64_t)c.b * c.hq * c.nq;
-        join_kernel<DP><<<(unsigned)((rows + 3) / 4), 128, 0, c.stream>>>(p);
-        if (cudaGetLastError() != cudaSuccess) st = LINFORMER_ERR_LAUNCH;
+        // set up while the parts are computed; it waits for them before it reads
+        cudaLaunchConfig_t cfg{};
+        cudaLaunchAttribute attr[1];
+        attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+        attr[0].val.programmaticStreamSerializationAllowed = 1;
+        cfg.gridDim = dim3((unsigned)((rows + 3) / 4));
+        cfg.blockDim = dim3(128);
+        cfg.stream = c.stream;
+        cfg.attrs = attr;
+        cfg.numAttrs = 1;
+        if (cudaLaunchKernelEx(&cfg, join_kernel<DP>, p) != cudaSuccess) {
+            cudaGetLastError();
+            st = LINFORMER_ERR_LAUNCH;
+        }
     }
     if (ws) workspace_free(ws, c.stream);
     return st;
@@ -738,11 +752,15 @@ int forward(const Call &c) {
     const int64_t whole = (int64_t)p.units * p.npairs;
     if (whole > kMaxItems) return LINFORMER_ERR_SIZE;
     const int sms = device_sms();
-    // With fewer items than SMs the keys are split, at least kMinBlocks blocks a part.
-    constexpr int kMinBlocks = 4;
+    // The keys are split where whole rows give fewer items than SMs; and where a tile has so
+    // few rows that a part's result is small beside the keys it reads, down to kWaves items an
+    // SM, so that sequences of differing lengths even out.  At least kMinBlocks blocks a part
+    // (from 12 blocks on: the second launch costs what a block or two takes).
+    constexpr int kMinBlocks = 4, kFirst = 12, kFewRows = 16, kWaves = 6;
     const int reach = c.window ? std::min(c.nk, c.window + kTile) : c.nk;
     const int blocks = (reach + kTile - 1) / kTile;
-    p.nsplit = (int)std::max<int64_t>(1, std::min<int64_t>(sms / whole, blocks / kMinBlocks));
+    const int64_t wanted = p.qbox * p.hbox <= kFewRows ? (kWaves * (int64_t)sms + whole - 1) / whole : sms / whole;
+    p.nsplit = blocks < kFirst ? 1 : (int)std::max<int64_t>(1, std::min<int64_t>(wanted, blocks / kMinBlocks));
     p.items = (int)whole * p.nsplit;
     return c.d <= 64 ? launch<64>(c, p) : launch<128>(c, p);
 }

@@ -317,62 +317,63 @@ def dense_attention(Q, K, V, lengths=None, out=None, stream=None):
 
 # --- exact softmax attention and rotary positions (strided [b][h][n][d] tensors) ------------
 #
-# Calls of a few microseconds: one ctypes array holds all strides of a call, and the current
-# stream comes from the binding that torch.cuda.current_stream() wraps (1 us instead of 6).
+# Calls of a few microseconds, so these marshal with care: no closures, strides by value from a
+# small table, the current stream from the binding that torch.cuda.current_stream() wraps
+# (1 us instead of 6), one comparison of shapes where one says it all.
 
-def _strides(*tensors):
-    """(int64 array of batch, head and row strides, the address of each tensor's three)."""
-    flat = []
-    for x in tensors:
-        b, h, n, one = x.stride()
-        if one != 1 and x.shape[3] != 1:
+_stride_table = {}  # (batch, head, row) strides -> int64[3]
+
+
+def _strides(x):
+    """Address of the tensor's batch, head and row strides (None: dense)."""
+    if x.is_contiguous():
+        return None
+    key = x.stride()
+    arr = _stride_table.get(key)
+    if arr is None:
+        if key[3] != 1 and x.shape[3] != 1:
             raise ValueError("the last dimension has to be contiguous")
-        flat += (b, h, n)
-    arr = (ctypes.c_int64 * len(flat))(*flat)
-    at = ctypes.addressof(arr)
-    return arr, range(at, at + 24 * len(tensors), 24)
+        if len(_stride_table) >= 4096:
+            _stride_table.clear()
+        arr = _stride_table[key] = (ctypes.c_int64 * 3)(*key[:3])
+    return arr
 
 
-def _device_of(first, *others):
-    """The CUDA device that all tensors (None: not given) are on."""
-    device = first.device
+def _stream_of(device, stream, *tensors):
+    """The stream handle, after a check that the tensors (None: not given) are on `device`."""
     if device.type != "cuda":
         raise ValueError(f"CUDA tensors are needed, got {device}")
-    for t in others:
+    for t in tensors:
         if t is not None and t.device != device:
             raise ValueError(f"tensors on {device} and {t.device}")
-    return device
-
-
-def _launch(device, stream, name, call):
-    """call(stream handle) with `device` current (the library works on the current device)."""
-    import torch
     if stream is None:
-        handle = torch._C._cuda_getCurrentRawStream(device.index)
-    else:
-        handle = _stream_handle(stream)
+        import torch
+        return torch._C._cuda_getCurrentRawStream(device.index)
+    return _stream_handle(stream)
+
+
+def _call(fn, device, args, name):
+    """fn(*args) with `device` current (the library works on the current device)."""
+    import torch
     if torch._C._cuda_getDevice() == device.index:
-        st = call(handle)
+        st = fn(*args)
     else:
         with torch.cuda.device(device):
-            st = call(handle)
+            st = fn(*args)
     if st != 0:
         raise LinformerError(st, name)
 
 
-def _check(name, x, shape, dtype, contiguous=False):
-    if x.shape != shape or x.dtype != dtype or (contiguous and not x.is_contiguous()):
-        raise ValueError(f"{name}: a{' contiguous' if contiguous else ''} {dtype} tensor of shape "
-                         f"{tuple(shape)} is needed, got {x.dtype} of {tuple(x.shape)}")
+def _check(name, x, shape, dtype):
+    if x.shape != shape or x.dtype != dtype:
+        raise ValueError(f"{name}: {dtype} of shape {tuple(shape)} is needed, got {x.dtype} of "
+                         f"{tuple(x.shape)}")
 
 
-def _check_words(q_lengths, k_lengths, lse, b, hq, n):
-    import torch
-    if q_lengths is not None:
-        _check("q_lengths", q_lengths, (b,), torch.int32, True)
-    if k_lengths is not None:
-        _check("k_lengths", k_lengths, (b,), torch.int32, True)
-    _check("lse", lse, (b, hq, n), torch.float32, True)
+def _check_dense(name, x, shape, dtype):
+    _check(name, x, shape, dtype)
+    if not x.is_contiguous():
+        raise ValueError(f"{name}: a contiguous tensor is needed")
 
 
 def softmax_attention(Q, K, V, q_lengths=None, k_lengths=None, causal: bool = False,
@@ -383,25 +384,32 @@ def softmax_attention(Q, K, V, q_lengths=None, k_lengths=None, causal: bool = Fa
     causal: the valid parts end together (the last query sees every key), with window > 0
     only the last `window` keys up to its own.  scale defaults to 1 / sqrt(d)."""
     import torch
-    b, hq, n, d = shape = Q.shape
-    hk, m = K.shape[1], K.shape[2]
-    dtype = Q.dtype
-    device = _device_of(Q, K, V, q_lengths, k_lengths, out, lse)
-    _check("K", K, (b, hk, m, d), dtype)
-    _check("V", V, (b, hk, m, d), dtype)
+    shape, kv, dtype, device = Q.shape, K.shape, Q.dtype, Q.device
+    b, hq, n, d = shape
+    _, hk, m, _ = kv
+    handle = _stream_of(device, stream, K, V, q_lengths, k_lengths, out, lse)
+    if kv[0] != b or kv[3] != d or K.dtype != dtype:
+        _check("K", K, (b, hk, m, d), dtype)
+    _check("V", V, kv, dtype)
     if out is None:
         out = torch.empty(shape, dtype=dtype, device=device)
     else:
         _check("out", out, shape, dtype)
     if lse is None:
         lse = torch.empty((b, hq, n), dtype=torch.float32, device=device)
-    _check_words(q_lengths, k_lengths, lse, b, hq, n)
-    code = dtype_code(Q)
-    keep, (sQ, sK, sV, sO) = _strides(Q, K, V, out)
-    _launch(device, stream, "linformer_softmax_attn_fwd", lambda s: lib().linformer_softmax_attn_fwd(
-        Q.data_ptr(), sQ, K.data_ptr(), sK, V.data_ptr(), sV, out.data_ptr(), sO, lse.data_ptr(),
-        _ptr(q_lengths), _ptr(k_lengths), b, hq, hk, n, m, d, d ** -0.5 if scale is None else scale,
-        1 if causal else 0, window, code, s))
+    else:
+        _check_dense("lse", lse, (b, hq, n), torch.float32)
+    if q_lengths is not None:
+        _check_dense("q_lengths", q_lengths, (b,), torch.int32)
+        q_lengths = q_lengths.data_ptr()
+    if k_lengths is not None:
+        _check_dense("k_lengths", k_lengths, (b,), torch.int32)
+        k_lengths = k_lengths.data_ptr()
+    _call(lib().linformer_softmax_attn_fwd, device,
+          (Q.data_ptr(), _strides(Q), K.data_ptr(), _strides(K), V.data_ptr(), _strides(V),
+           out.data_ptr(), _strides(out), lse.data_ptr(), q_lengths, k_lengths, b, hq, hk, n, m, d,
+           d ** -0.5 if scale is None else scale, 1 if causal else 0, window, dtype_code(Q), handle),
+          "linformer_softmax_attn_fwd")
     return out, lse
 
 
@@ -410,28 +418,41 @@ def softmax_attention_backward(Q, K, V, O, dO, lse, q_lengths=None, k_lengths=No
                                dK=None, dV=None, stream=None):
     """(dQ, dK, dV) from the inputs and results of softmax_attention and dO = dLoss/dO."""
     import torch
-    b, hq, n, d = shape = Q.shape
-    hk, m = K.shape[1], K.shape[2]
-    kv, dtype = (b, hk, m, d), Q.dtype
-    device = _device_of(Q, K, V, O, dO, lse, q_lengths, k_lengths, dQ, dK, dV)
+    shape, kv, dtype, device = Q.shape, K.shape, Q.dtype, Q.device
+    b, hq, n, d = shape
+    _, hk, m, _ = kv
+    handle = _stream_of(device, stream, K, V, O, dO, lse, q_lengths, k_lengths, dQ, dK, dV)
+    if kv[0] != b or kv[3] != d or K.dtype != dtype:
+        _check("K", K, (b, hk, m, d), dtype)
+    _check("V", V, kv, dtype)
+    _check("O", O, shape, dtype)
+    _check("dO", dO, shape, dtype)
+    _check_dense("lse", lse, (b, hq, n), torch.float32)
     if dQ is None:
         dQ = torch.empty(shape, dtype=dtype, device=device)
+    else:
+        _check("dQ", dQ, shape, dtype)
     if dK is None:
         dK = torch.empty(kv, dtype=dtype, device=device)
+    else:
+        _check("dK", dK, kv, dtype)
     if dV is None:
         dV = torch.empty(kv, dtype=dtype, device=device)
-    for name, x in (("O", O), ("dO", dO), ("dQ", dQ)):
-        _check(name, x, shape, dtype)
-    for name, x in (("K", K), ("V", V), ("dK", dK), ("dV", dV)):
-        _check(name, x, kv, dtype)
-    _check_words(q_lengths, k_lengths, lse, b, hq, n)
-    code = dtype_code(Q)
-    keep, (sQ, sK, sV, sO, sdO, sdQ, sdK, sdV) = _strides(Q, K, V, O, dO, dQ, dK, dV)
-    _launch(device, stream, "linformer_softmax_attn_bwd", lambda s: lib().linformer_softmax_attn_bwd(
-        Q.data_ptr(), sQ, K.data_ptr(), sK, V.data_ptr(), sV, O.data_ptr(), sO, dO.data_ptr(), sdO,
-        lse.data_ptr(), dQ.data_ptr(), sdQ, dK.data_ptr(), sdK, dV.data_ptr(), sdV,
-        _ptr(q_lengths), _ptr(k_lengths), b, hq, hk, n, m, d, d ** -0.5 if scale is None else scale,
-        1 if causal else 0, window, code, s))
+    else:
+        _check("dV", dV, kv, dtype)
+    if q_lengths is not None:
+        _check_dense("q_lengths", q_lengths, (b,), torch.int32)
+        q_lengths = q_lengths.data_ptr()
+    if k_lengths is not None:
+        _check_dense("k_lengths", k_lengths, (b,), torch.int32)
+        k_lengths = k_lengths.data_ptr()
+    _call(lib().linformer_softmax_attn_bwd, device,
+          (Q.data_ptr(), _strides(Q), K.data_ptr(), _strides(K), V.data_ptr(), _strides(V),
+           O.data_ptr(), _strides(O), dO.data_ptr(), _strides(dO), lse.data_ptr(), dQ.data_ptr(),
+           _strides(dQ), dK.data_ptr(), _strides(dK), dV.data_ptr(), _strides(dV), q_lengths,
+           k_lengths, b, hq, hk, n, m, d, d ** -0.5 if scale is None else scale, 1 if causal else 0,
+           window, dtype_code(Q), handle),
+          "linformer_softmax_attn_bwd")
     return dQ, dK, dV
 
 
@@ -441,8 +462,10 @@ def rotary_phase(rot: int, base: float = 10000.0, scaling: int = ROTARY_PLAIN,
     """The table of `rot / 2` frequencies that rotary() takes (int64, made once and kept)."""
     import torch
     phase = torch.empty(max(rot // 2, 1), dtype=torch.int64, device=device)
-    _launch(phase.device, stream, "linformer_rotary_phase", lambda s: lib().linformer_rotary_phase(
-        phase.data_ptr(), rot, base, scaling, factor, original_length, beta_fast, beta_slow, s))
+    handle = _stream_of(phase.device, stream)
+    _call(lib().linformer_rotary_phase, phase.device,
+          (phase.data_ptr(), rot, base, scaling, factor, original_length, beta_fast, beta_slow, handle),
+          "linformer_rotary_phase")
     return phase
 
 
@@ -454,32 +477,34 @@ def rotary(x, x2=None, phase=None, positions=None, start: int = 0, rot=None,
     positions int32 [b][n], or None for start + row; rot defaults to d.  inverse=True maps
     gradients of the results to gradients of the inputs.  out may be x (in place)."""
     import torch
-    b, h, n, d = x.shape
-    rot = d if rot is None else rot
-    device = _device_of(x, x2, phase, positions, out, out2)
+    shape, dtype, device = x.shape, x.dtype, x.device
+    b, h, n, d = shape
+    if rot is None:
+        rot = d
+    handle = _stream_of(device, stream, x2, phase, positions, out, out2)
     if phase is None:
         raise ValueError("phase: the table of rotary_phase() is needed")
-    _check("phase", phase, (rot // 2,), torch.int64, True)
+    _check_dense("phase", phase, (rot // 2,), torch.int64)
     if positions is not None:
-        _check("positions", positions, (b, n), torch.int32, True)
+        _check_dense("positions", positions, (b, n), torch.int32)
+        positions = positions.data_ptr()
     if out is None:
         out = torch.empty_like(x)
     else:
-        _check("out", out, x.shape, x.dtype)
-    if x2 is None:
-        keep, (sX, sY) = _strides(x, out)
-        second, h2 = (None, None, None, None), 0
-    else:
+        _check("out", out, shape, dtype)
+    px2 = sx2 = py2 = sy2 = None
+    h2 = 0
+    if x2 is not None:
         h2 = x2.shape[1]
-        _check("x2", x2, (b, h2, n, d), x.dtype)
+        _check("x2", x2, (b, h2, n, d), dtype)
         if out2 is None:
             out2 = torch.empty_like(x2)
         else:
-            _check("out2", out2, x2.shape, x2.dtype)
-        keep, (sX, sY, sX2, sY2) = _strides(x, out, x2, out2)
-        second = (x2.data_ptr(), sX2, out2.data_ptr(), sY2)
-    code = dtype_code(x)
-    _launch(device, stream, "linformer_rotary", lambda s: lib().linformer_rotary(
-        x.data_ptr(), sX, out.data_ptr(), sY, h, *second, h2, phase.data_ptr(), _ptr(positions),
-        start, b, n, d, rot, layout, amplitude, 1 if inverse else 0, code, s))
+            _check("out2", out2, x2.shape, dtype)
+        px2, sx2, py2, sy2 = x2.data_ptr(), _strides(x2), out2.data_ptr(), _strides(out2)
+    _call(lib().linformer_rotary, device,
+          (x.data_ptr(), _strides(x), out.data_ptr(), _strides(out), h, px2, sx2, py2, sy2, h2,
+           phase.data_ptr(), positions, start, b, n, d, rot, layout, amplitude, 1 if inverse else 0,
+           dtype_code(x), handle),
+          "linformer_rotary")
     return out if x2 is None else (out, out2)
