@@ -140,7 +140,7 @@ extern "C" int linformer_rotary(const void *X, const int64_t *X_strides, void *Y
                                 const int64_t *Y2_strides, int hx2, const uint64_t *phase,
                                 const int32_t *positions, int start, int b, int n, int d, int rot,
                                 int layout, float amplitude, int inverse, int dtype, void *stream) {
-    if (!X || !Y || !phase || (hx2 && (!X2 || !Y2))) return LINFORMER_ERR_NULL;
+    if (!X || !Y || !phase || (hx2 > 0 && (!X2 || !Y2))) return LINFORMER_ERR_NULL;
     if (b < 1 || hx < 1 || hx2 < 0 || n < 1 || d < 1) return LINFORMER_ERR_SIZE;
     if ((int64_t)b * ((int64_t)hx + hx2) > (1 << 29) || (int64_t)b * n > (1LL << 33) || d > (1 << 20) ||
         hx > (1 << 20) || hx2 > (1 << 20))

@@ -129,3 +129,204 @@ def test_backward(name):
     refs, bounds, rows = orc.backward(Q, K, V, dO, q, k, **kw)
     for n, g, r, e, w in zip(("dQ", "dK", "dV"), got, refs, bounds, rows):
         within(g, r, e, n, w)
+
+
+# --- ways of calling ----------------------------------------------------------------------
+
+def same(a, b):
+    return all(torch.equal(x.view(torch.int16), y.view(torch.int16)) if x.dtype == BF
+               else torch.equal(x.view(torch.int32), y.view(torch.int32)) for x, y in zip(a, b))
+
+
+def test_results_repeat_bit_for_bit():
+    Q, K, V, dO = tensors(2, 8, 2, 500, 700, 128, seed=3)
+    O, lse = lf.softmax_attention(Q, K, V)
+    g = lf.softmax_attention_backward(Q, K, V, O, dO, lse)
+    for _ in range(5):
+        assert same(lf.softmax_attention(Q, K, V), (O, lse))
+        assert same(lf.softmax_attention_backward(Q, K, V, O, dO, lse), g)
+    status()
+
+
+def test_outputs_only_where_they_belong():
+    """Slices of wider buffers (rows, heads, columns around them untouched), lse in a longer one."""
+    b, hq, hk, n, d = 2, 4, 2, 150, 64
+    Q, K, V, dO = tensors(b, hq, hk, n, n, d, seed=5)
+    kw = dict(causal=True, q_lengths=lengths([150, 77]), k_lengths=lengths([150, 77]))
+
+    def room(h):
+        return torch.full((b, h + 2, n + 3, d + 16), 7.0, dtype=BF, device=DEV)
+
+    def inner(x):
+        return x[:, 1:-1, 1:-2, 8:-8]
+
+    O0, lse0 = lf.softmax_attention(Q, K, V, **kw)
+    g0 = lf.softmax_attention_backward(Q, K, V, O0, dO, lse0, **kw)
+    R = [room(hq), room(hq), room(hk), room(hk)]
+    ends = torch.full((b * hq * n + 64,), 7.0, device=DEV)
+    lse = ends[32:-32].view(b, hq, n)
+    O, _ = lf.softmax_attention(Q, K, V, out=inner(R[0]), lse=lse, **kw)
+    g = lf.softmax_attention_backward(Q, K, V, O, dO, lse, dQ=inner(R[1]), dK=inner(R[2]),
+                                      dV=inner(R[3]), **kw)
+    status()
+    assert same((O, lse, *g), (O0, lse0, *g0))
+    for x in R:
+        inner(x).fill_(7.0)
+        assert (x == 7.0).all()
+    assert (ends[:32] == 7).all() and (ends[-32:] == 7).all()
+
+
+def test_large_logits_after_small_ones():
+    """A row's later blocks outgrow its first by more than fp32 holds; also the reverse."""
+    for flip in (False, True):
+        Q, K, V, dO = tensors(1, 2, 1, 200, 640, 64, seed=7, gain=1)
+        ramp = torch.linspace(0.01, 40, 640, device=DEV)
+        K.mul_((ramp.flip(0) if flip else ramp)[:, None].to(BF))
+        O, lse = lf.softmax_attention(Q, K, V, scale=1.0)
+        status()
+        ref, rl, bO, bl = orc.forward(Q, K, V, scale=1.0)
+        within(O, ref, bO, f"O {flip}")
+        within(lse, rl, bl, f"lse {flip}")
+
+
+def test_gradient_against_differences():
+    """The kernel's gradients against central differences of the oracle's loss in a random
+    direction.  With f = sum(O dO), |f' - difference| is below the gradients' own bounds times
+    the direction, plus the difference's truncation: h^2 / 6 f''' with h = 1e-4, below 1e-6 of
+    the gradient here."""
+    b, hq, hk, n, d = 1, 4, 2, 90, 64
+    Q, K, V, dO = tensors(b, hq, hk, n, n, d, seed=11, gain=1)
+    kw = dict(causal=True)
+    ref = orc.forward(Q, K, V, **kw)
+    O, lse = torch.from_numpy(ref[0]).to(DEV, BF), torch.from_numpy(ref[1]).to(DEV, torch.float32)
+    got = lf.softmax_attention_backward(Q, K, V, O, dO, lse, **kw)
+    status()
+    refs, bounds, _ = orc.backward(Q, K, V, dO, **kw)
+    rng = np.random.default_rng(1)
+    x = [orc.host64(t) for t in (Q, K, V)]
+    g64 = orc.host64(dO)
+    for i in range(3):
+        D = rng.standard_normal(x[i].shape)
+        h = 1e-4
+        f = []
+        for s in (h, -h):
+            y = list(x)
+            y[i] = x[i] + s * D
+            f.append((orc.forward(*y, **kw)[0] * g64).sum())
+        slope = (f[0] - f[1]) / (2 * h)
+        mine = (orc.host64(got[i]) * D).sum()
+        allowed = (bounds[i] * np.abs(D)).sum() + 1e-6 * np.abs(refs[i] * D).sum()
+        assert abs(mine - slope) <= allowed, (i, mine, slope, allowed)
+
+
+def test_two_streams_at_once():
+    sets = [tensors(2, 8, 2, 300 + 7 * i, 500, 64, seed=20 + i) for i in range(2)]
+    alone = []
+    for Q, K, V, dO in sets:
+        O, lse = lf.softmax_attention(Q, K, V)
+        alone.append((O, lse, *lf.softmax_attention_backward(Q, K, V, O, dO, lse)))
+    torch.cuda.synchronize()
+    streams = [torch.cuda.Stream(), torch.cuda.Stream()]
+    for _ in range(10):
+        got = []
+        for (Q, K, V, dO), s in zip(sets, streams):
+            with torch.cuda.stream(s):
+                O, lse = lf.softmax_attention(Q, K, V)
+                got.append((O, lse, *lf.softmax_attention_backward(Q, K, V, O, dO, lse)))
+        torch.cuda.synchronize()
+        assert all(same(x, y) for x, y in zip(got, alone))
+    s = streams[0]   # a stream given as an argument, from another current one
+    s.wait_stream(torch.cuda.current_stream())
+    Q, K, V, _ = sets[0]
+    got = lf.softmax_attention(Q, K, V, stream=s)
+    s.synchronize()
+    assert same(got, alone[0][:2])
+    status()
+
+
+@pytest.mark.parametrize("nq,nk", [(260, 260), (1, 5000)])
+def test_captured_and_replayed(nq, nk):
+    """Two graphs with forward and backward (and the split forward's workspace) replayed in
+    turn, and once with inputs rewritten, give what eager calls give."""
+    data = [tensors(2, 4, 2, nq, nk, 128, seed=30 + i) for i in range(2)]
+    new = tensors(2, 4, 2, nq, nk, 128, seed=40)
+
+    def step(Q, K, V, dO):
+        O, lse = lf.softmax_attention(Q, K, V, causal=True)
+        return (O, lse, *lf.softmax_attention_backward(Q, K, V, O, dO, lse, causal=True))
+
+    eager = [step(*x) for x in data]
+    eager_new = step(*new)
+    torch.cuda.synchronize()
+    graphs = []
+    for x in data:
+        g = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(g):
+            out = step(*x)
+        graphs.append((g, out))
+    for _ in range(3):
+        for g, _ in graphs:
+            g.replay()
+    torch.cuda.synchronize()
+    assert all(same(out, e) for (_, out), e in zip(graphs, eager))
+    for dst, src in zip(data[0], new):
+        dst.copy_(src)
+    graphs[0][0].replay()
+    torch.cuda.synchronize()
+    assert same(graphs[0][1], eager_new)
+    status()
+
+
+def test_workspace_stays_in_its_bounds(monkeypatch):
+    """Guard bytes behind the workspaces of a split forward and of a backward."""
+    monkeypatch.setenv("LINFORMER_WORKSPACE_GUARD", "1")
+    Q, K, V, dO = tensors(3, 4, 1, 3, 4000, 96, seed=50)
+    O, lse = lf.softmax_attention(Q, K, V)
+    lf.softmax_attention_backward(Q, K, V, O, dO, lse)
+    status()
+
+
+def test_failed_allocation_is_reported(monkeypatch):
+    Q, K, V, dO = tensors(1, 2, 1, 64, 64, 64, seed=51)
+    O, lse = lf.softmax_attention(Q, K, V)
+    monkeypatch.setenv("LINFORMER_FAIL_ALLOC", "1")
+    with pytest.raises(lf.LinformerError) as e:
+        lf.softmax_attention_backward(Q, K, V, O, dO, lse)
+    assert e.value.status == -7
+    monkeypatch.delenv("LINFORMER_FAIL_ALLOC")
+    lf.softmax_attention_backward(Q, K, V, O, dO, lse)
+    status()
+
+
+def test_long_cache_offsets():
+    """One token over a cache whose last head starts beyond 2^31 elements (the other heads are
+    a stride away, not memory that is read): 2.3 GB of K and of V, the head checked is real."""
+    n, d, heads = 70000, 128, 2
+    stride = (1 << 31) // 2 // d * d + d * 64
+    buf = torch.empty(stride + n * d, dtype=BF, device=DEV)
+    K = torch.as_strided(buf, (1, heads, n, d), (heads * stride, stride, d, 1))
+    g = torch.Generator(device=DEV).manual_seed(9)
+    for h in range(heads):
+        K[0, h] = torch.randn(n, d, generator=g, device=DEV).to(BF)
+    Q = torch.randn(1, heads, 1, d, generator=g, device=DEV).to(BF)
+    O, lse = lf.softmax_attention(Q, K, K)
+    status()
+    ref, rl, bO, bl = orc.forward(Q, K, K)
+    within(O, ref, bO, "O")
+    within(lse, rl, bl, "lse")
+
+
+def test_as_the_linformer_core():
+    """Queries over the projected keys and values (nk = k): the attention step of the Linformer
+    forward, with Kbar and Vbar from linformer_project_fwd rounded to bf16."""
+    from rank_linear_complexity_gb300.workloads import BF16, HEADWISE, make_inputs
+    b, h, n, d, k = 2, 3, 384, 64, 128
+    x = make_inputs(b, h, n, d, k, HEADWISE, BF16, seed=60)
+    g = {kk: (v.to(DEV) if v is not None else None) for kk, v in x.items()}
+    Kb, Vb = lf.projection(g["K"], g["V"], g["E"], g["F"], None, HEADWISE)
+    Kb, Vb = Kb.to(BF), Vb.to(BF)
+    O, lse = lf.softmax_attention(g["Q"], Kb, Vb)
+    status()
+    ref, rl, bO, bl = orc.forward(g["Q"], Kb, Vb)
+    within(O, ref, bO, "O")
+    within(lse, rl, bl, "lse")
