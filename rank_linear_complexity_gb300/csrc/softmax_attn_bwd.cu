@@ -117,15 +117,15 @@ __device__ __forceinline__ void mma_scores(uint32_t d, uint32_t a, uint32_t b) {
         mma_ss(d, da + off, db + off, idesc, x > 0 ? 1u : 0u);
     }
 }
-// D (128 x DP) += A (128 x 128, packed in 64 columns of tensor memory) . B (128 rows of DP)
+// D (128 x DP) += A (128 x 64, packed in 32 columns of tensor memory) . B (64 rows of DP): half
+// of a step's sum, issued as soon as that half of P or dS is there.
 template <int DP>
-__device__ __forceinline__ void mma_sum(uint32_t d, uint32_t a, uint32_t b, uint32_t acc) {
+__device__ __forceinline__ void mma_sum_half(uint32_t d, uint32_t a, uint32_t b, uint32_t acc) {
     const uint32_t idesc = idesc_f16(128, DP, 1, 0, 1);
     const uint64_t db = sdesc(b, 16384, 1024, kSwizzle128B);
 #pragma unroll
-    for (int x = 0; x < 8; ++x)
-        mma_ts(d, a + 8 * x, db + (uint64_t)(128 * x), idesc,
-               (acc || x > 0) ? 1u : 0u);
+    for (int x = 0; x < 4; ++x)
+        mma_ts(d, a + 8 * x, db + (uint64_t)(128 * x), idesc, (acc || x > 0) ? 1u : 0u);
 }
 
 template <int DP>
@@ -208,7 +208,8 @@ __device__ __forceinline__ DqItem dq_item(const BwdParams &p, int idx) {
 
 struct DqBarriers {
     // (pairs: even and odd blocks, each with a group of warps of its own)
-    uint64_t q_full, q_free, s_full[2], s_free, dp_full[2], ds_full[2], dq_done[2], acc_full, acc_free;
+    uint64_t q_full, q_free, s_full[2], s_free, dp_full[2], ds_full[2][2], dq_done[2];
+    uint64_t acc_full, acc_free;
     uint64_t fix_wanted, fixed, drain[2];
     uint64_t full[8], empty[8];
     uint32_t tmem;
@@ -238,7 +239,8 @@ softmax_attn_dq_kernel(const __grid_constant__ CUtensorMap tQ, const __grid_cons
         for (int i = 0; i < 2; ++i) {
             mbar_init(&bar->s_full[i], 1);
             mbar_init(&bar->dp_full[i], 1);
-            mbar_init(&bar->ds_full[i], kGroupWarps);
+            mbar_init(&bar->ds_full[i][0], kGroupWarps);  // halves of 64 columns
+            mbar_init(&bar->ds_full[i][1], kGroupWarps);
             mbar_init(&bar->dq_done[i], 1);
         }
         mbar_init(&bar->acc_full, 1);
@@ -364,14 +366,18 @@ softmax_attn_dq_kernel(const __grid_constant__ CUtensorMap tQ, const __grid_cons
                 if (blocks <= 0) continue;
                 for (int j = 0; j < blocks && ok; ++j, ++n, ring += 2) {
                     // (dS says that S has been formed, so the block of K has landed)
-                    ok = thread_spin(&bar->ds_full[n & 1], (n >> 1) & 1, p.status, 92, abort_flag) &&
+                    const int s = ring % C::kStages;
+                    const uint32_t ds = tmem + C::kDp + 128 * (n & 1), k = aKV + s * C::kTileBytes;
+                    ok = thread_spin(&bar->ds_full[n & 1][0], (n >> 1) & 1, p.status, 92, abort_flag) &&
                          (j > 0 || items == 0 ||
                           thread_spin(&bar->acc_free, (items - 1) & 1, p.status, 93, abort_flag));
                     if (!ok) break;
                     tc_fence_after();
-                    const int s = ring % C::kStages;
-                    mma_sum<DP>(tmem + C::kDq, tmem + C::kDp + 128 * (n & 1), aKV + s * C::kTileBytes,
-                                j > 0 ? 1u : 0u);
+                    mma_sum_half<DP>(tmem + C::kDq, ds, k, j > 0 ? 1u : 0u);
+                    ok = thread_spin(&bar->ds_full[n & 1][1], (n >> 1) & 1, p.status, 92, abort_flag);
+                    if (!ok) break;
+                    tc_fence_after();
+                    mma_sum_half<DP>(tmem + C::kDq, ds + 32, k + 8192, 1u);
                     mma_commit(&bar->dq_done[n & 1]);
                     mma_commit(&bar->empty[s]);
                 }
@@ -458,11 +464,13 @@ softmax_attn_dq_kernel(const __grid_constant__ CUtensorMap tQ, const __grid_cons
                         o[e / 2] = pack2(z.x, z.y);
                     }
                     tmem_st16_async(tD + 16 * c, o);
+                    if (c & 1) {
+                        tmem_wait_st();
+                        tc_fence_before();
+                        __syncwarp();
+                        if (lane == 0) mbar_arrive(&bar->ds_full[g & 1][c >> 1]);
+                    }
                 }
-                tmem_wait_st();
-                tc_fence_before();
-                __syncwarp();
-                if (lane == 0) mbar_arrive(&bar->ds_full[g & 1]);
             }
             if (!ok) break;
             const bool some = hi > lo;
@@ -536,7 +544,7 @@ __device__ __forceinline__ DkvItem dkv_item(const BwdParams &p, int idx) {
 // Barriers of steps come in pairs, for even and odd steps: a waiter that falls behind by one
 // step still finds its own phase.
 struct DkvBarriers {
-    uint64_t kv_full[2], kv_free[2], s_full[2], p_full[2], pv_done[2], dp_full[2], ds_full[2], ds_done[2];
+    uint64_t kv_full[2], kv_free[2], s_full[2], p_full[2][2], pv_done[2], dp_full[2], ds_full[2][2], ds_done[2];
     uint64_t acc_full, acc_free, fix_wanted, fixed[2], drain[2];
     uint64_t full[4], empty[4];
     uint32_t tmem;
@@ -564,10 +572,12 @@ softmax_attn_dkv_kernel(const __grid_constant__ CUtensorMap tQ, const __grid_con
             mbar_init(&bar->kv_full[i], 1);
             mbar_init(&bar->kv_free[i], 2);
             mbar_init(&bar->s_full[i], 1);
-            mbar_init(&bar->p_full[i], kGroupWarps);
+            for (int h = 0; h < 2; ++h) {  // halves of 64 columns
+                mbar_init(&bar->p_full[i][h], kGroupWarps);
+                mbar_init(&bar->ds_full[i][h], kGroupWarps);
+            }
             mbar_init(&bar->pv_done[i], 1);
             mbar_init(&bar->dp_full[i], 1);
-            mbar_init(&bar->ds_full[i], kGroupWarps);
             mbar_init(&bar->ds_done[i], 1);
             mbar_init(&bar->drain[i], 1);
             mbar_init(&bar->fixed[i], 31);
@@ -662,7 +672,7 @@ softmax_attn_dkv_kernel(const __grid_constant__ CUtensorMap tQ, const __grid_con
             bool ok = true;
             const uint32_t aKV0 = smem_u32(sK) + (first ? 0 : C::kTileBytes), aT = smem_u32(sT);
             uint64_t *done = first ? bar->pv_done : bar->ds_done, *full = first ? bar->s_full : bar->dp_full,
-                     *ready = first ? bar->p_full : bar->ds_full;
+                     (*ready)[2] = first ? bar->p_full : bar->ds_full;
             auto phase = [](int g) { return (uint32_t)(g >> 1) & 1u; };
             auto buffer = [&](int g) { return tmem + 128 * ((2 * g + (first ? 0 : 1)) % C::kBufs); };
             for (int idx = blockIdx.x; idx < p.items && ok; idx += gridDim.x) {
@@ -705,13 +715,17 @@ softmax_attn_dkv_kernel(const __grid_constant__ CUtensorMap tQ, const __grid_con
                 // dV += P^T dO (or dK += dS^T Q) of step g
                 auto sum = [&](int g) {
                     const int s = g % C::kStages;
-                    if (!thread_spin(&ready[g & 1], phase(g), p.status, 108, abort_flag)) return false;
+                    const uint32_t d = tmem + (first ? C::kDv : C::kDk), m = buffer(g),
+                                   t = aT + s * 2 * C::kTileBytes + (first ? C::kTileBytes : 0);
+                    if (!thread_spin(&ready[g & 1][0], phase(g), p.status, 108, abort_flag)) return false;
                     if (g == n && items > 0 &&
                         !thread_spin(&bar->acc_free, (items - 1) & 1, p.status, 109, abort_flag))
                         return false;
                     tc_fence_after();
-                    mma_sum<DP>(tmem + (first ? C::kDv : C::kDk), buffer(g),
-                                aT + s * 2 * C::kTileBytes + (first ? C::kTileBytes : 0), g > n ? 1u : 0u);
+                    mma_sum_half<DP>(d, m, t, g > n ? 1u : 0u);
+                    if (!thread_spin(&ready[g & 1][1], phase(g), p.status, 108, abort_flag)) return false;
+                    tc_fence_after();
+                    mma_sum_half<DP>(d, m + 32, t + 8192, 1u);
                     mma_commit(&done[g & 1]);
                     mma_commit(&bar->empty[s]);
                     return true;
@@ -794,11 +808,13 @@ softmax_attn_dkv_kernel(const __grid_constant__ CUtensorMap tQ, const __grid_con
                     for (int e = 0; e < 16; ++e)
                         o[e] = pack2(__uint_as_float(v[c][2 * e]), __uint_as_float(v[c][2 * e + 1]));
                     tmem_st16_async(tS + 16 * c, o);
+                    if (c & 1) {
+                        tmem_wait_st();
+                        tc_fence_before();
+                        __syncwarp();
+                        if (lane == 0) mbar_arrive(&bar->p_full[g & 1][c >> 1]);
+                    }
                 }
-                tmem_wait_st();
-                tc_fence_before();
-                __syncwarp();
-                if (lane == 0) mbar_arrive(&bar->p_full[g & 1]);
                 if (!warp_spin(&bar->dp_full[g & 1], parity, p.status, 113, abort_flag)) {
                     ok = false;
                     break;
@@ -822,11 +838,13 @@ softmax_attn_dkv_kernel(const __grid_constant__ CUtensorMap tQ, const __grid_con
                         o[e / 2 + 1] = pack2(z1.x, z1.y);
                     }
                     tmem_st16_async(tD + 16 * c, o);
+                    if (c & 1) {
+                        tmem_wait_st();
+                        tc_fence_before();
+                        __syncwarp();
+                        if (lane == 0) mbar_arrive(&bar->ds_full[g & 1][c >> 1]);
+                    }
                 }
-                tmem_wait_st();
-                tc_fence_before();
-                __syncwarp();
-                if (lane == 0) mbar_arrive(&bar->ds_full[g & 1]);
                 j = (j + 2) % per;
             }
             n += max(0, steps);

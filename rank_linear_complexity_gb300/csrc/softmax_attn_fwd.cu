@@ -149,7 +149,7 @@ __device__ __forceinline__ bool ragged_end(const Item &it, int nk) {
 }
 
 struct Barriers {
-    uint64_t q_full[2], q_free[2], s_full[2], s_free[2], p_full[2], pv_done[2], o_free[2];
+    uint64_t q_full[2], q_free[2], s_full[2], s_free[2], p_full[2], p_half[2], pv_done[2], o_free[2];
     uint64_t fix_wanted, fixed, drain[2];
     uint64_t full[10], empty[10];
     uint32_t tmem;
@@ -228,6 +228,7 @@ softmax_attn_fwd_kernel(const __grid_constant__ CUtensorMap tQ, const __grid_con
             mbar_init(&bar->s_full[t], 1);
             mbar_init(&bar->s_free[t], 4);
             mbar_init(&bar->p_full[t], 4);
+            mbar_init(&bar->p_half[t], 4);
             mbar_init(&bar->pv_done[t], 1);
             mbar_init(&bar->o_free[t], 4);
         }
@@ -382,15 +383,24 @@ softmax_attn_fwd_kernel(const __grid_constant__ CUtensorMap tQ, const __grid_con
                         mbar_arrive(empty);
                         return true;
                     }
-                    if (!thread_spin(&bar->p_full[t], n & 1, p.status, 78, abort_flag)) return false;
-                    ++n;
+                    // P over S comes in halves of 64 keys: the first half's products run while
+                    // the other is in its exponentials
+                    if (!thread_spin(C::kSep ? &bar->p_full[t] : &bar->p_half[t], n & 1, p.status, 78, abort_flag))
+                        return false;
                     if (j == lo && items > 0 &&
                         !thread_spin(&bar->o_free[t], (items - 1) & 1, p.status, 79, abort_flag))
                         return false;
                     tc_fence_after();
 #pragma unroll
-                    for (int x = 0; x < 8; ++x)
+                    for (int x = 0; x < 4; ++x)
                         mma_ts(tO, tP + 8 * x, v + (uint64_t)(128 * x), idesc_o, (j > lo || x > 0) ? 1u : 0u);
+                    if (!C::kSep) {
+                        if (!thread_spin(&bar->p_full[t], n & 1, p.status, 78, abort_flag)) return false;
+                        tc_fence_after();
+                    }
+                    ++n;
+#pragma unroll
+                    for (int x = 4; x < 8; ++x) mma_ts(tO, tP + 8 * x, v + (uint64_t)(128 * x), idesc_o, 1u);
                     mma_commit(&bar->pv_done[t]);
                     mma_commit(empty);
                     return true;
@@ -454,6 +464,7 @@ softmax_attn_fwd_kernel(const __grid_constant__ CUtensorMap tQ, const __grid_con
                     // no second arrival on p_full before the other warps' first
                     if (C::kSep && !last_product(j > lo)) break;
                     __syncwarp();
+                    if (!C::kSep && lane == 0) mbar_arrive(&bar->p_half[t]);
                     if (lane == 0) mbar_arrive(&bar->p_full[t]);
                     continue;
                 }
@@ -503,6 +514,12 @@ rescale_output(tO, DP, f);
                         uint32_t o[16];
                         exp_chunk(v[c], o, sl, off, sum0, sum1);
                         tmem_st16_async(tP + 16 * c, o);
+                        if (c == 1) {
+                            tmem_wait_st();
+                            tc_fence_before();
+                            __syncwarp();
+                            if (lane == 0) mbar_arrive(&bar->p_half[t]);
+                        }
                     }
                 }
                 tmem_wait_st();
