@@ -90,21 +90,38 @@ __device__ __forceinline__ float dot2(uint32_t a, uint32_t b) {
     return __uint_as_float(a << 16) * __uint_as_float(b << 16) +
            __uint_as_float(a & 0xffff0000u) * __uint_as_float(b & 0xffff0000u);
 }
-// 16 columns of a row, scaled and rounded (columns from d on do not exist): one 32-byte store
-// where the tensor allows it (a warp's store touches 32 rows, and each row's line costs a
-// cycle of the load/store unit), else two of 16 bytes.
-__device__ __forceinline__ void store_row(__nv_bfloat16 *dst, const uint32_t (&o)[16], int c, int d,
+// 32 columns of a row, scaled and rounded (columns from d on do not exist): 32-byte stores where
+// the tensor allows them (a warp's store touches 32 rows, and each row's line costs a cycle of
+// the load/store unit), else two of 16 bytes for each.
+__device__ __forceinline__ void store_row(__nv_bfloat16 *dst, const uint32_t (&o)[32], int c, int d,
                                           float f, bool zero, bool wide) {
-    uint32_t w[8];
 #pragma unroll
-    for (int e = 0; e < 8; ++e)
-        w[e] = zero ? 0u : pack2(__uint_as_float(o[2 * e]) * f, __uint_as_float(o[2 * e + 1]) * f);
-    if (wide) {
-        if (c < d) store32(dst + c, w);
-    } else {
-        if (c < d) *reinterpret_cast<uint4 *>(dst + c) = make_uint4(w[0], w[1], w[2], w[3]);
-        if (c + 8 < d) *reinterpret_cast<uint4 *>(dst + c + 8) = make_uint4(w[4], w[5], w[6], w[7]);
+    for (int x = 0; x < 32; x += 16) {
+        uint32_t w[8];
+#pragma unroll
+        for (int e = 0; e < 8; ++e)
+            w[e] = zero ? 0u : pack2(__uint_as_float(o[x + 2 * e]) * f, __uint_as_float(o[x + 2 * e + 1]) * f);
+        if (wide) {
+            if (c + x < d) store32(dst + c + x, w);
+        } else {
+            if (c + x < d) *reinterpret_cast<uint4 *>(dst + c + x) = make_uint4(w[0], w[1], w[2], w[3]);
+            if (c + x + 8 < d) *reinterpret_cast<uint4 *>(dst + c + x + 8) = make_uint4(w[4], w[5], w[6], w[7]);
+        }
     }
+}
+// 32 N columns of an accumulator, one wait for all.
+// The first d columns of a row as zero.
+__device__ __forceinline__ void zero_row(__nv_bfloat16 *dst, int d) {
+#pragma unroll 1
+    for (int c = 0; c < d; c += 8) *reinterpret_cast<uint4 *>(dst + c) = make_uint4(0u, 0u, 0u, 0u);
+}
+template <int N>
+__device__ __forceinline__ void load_columns(uint32_t t, uint32_t (&o)[N][32]) {
+#pragma unroll
+    for (int c = 0; c < N; ++c) tmem_ld32_async(t + 32 * c, o[c]);
+    tmem_wait_ld(o[0]);
+#pragma unroll
+    for (int c = 1; c < N; ++c) tie32(o[c]);
 }
 
 template <int DP>
@@ -395,8 +412,8 @@ softmax_attn_dq_kernel(const __grid_constant__ CUtensorMap tQ, const __grid_cons
         const uint32_t lanes = (uint32_t)((warp & 3) * 32) << 16;
         const float sl = p.scale_log2;
         int n = 0, items = 0;
+        DqItem it = dq_item(p, min((int)blockIdx.x, p.items - 1));
         for (int idx = blockIdx.x; idx < p.items; idx += gridDim.x) {
-            const DqItem it = dq_item(p, idx);
             const int lo = it.lo, hi = it.hi;
             float nl = 0.f, nd = 0.f;
             if (hi > lo) {  // the row values come with Q and dO
@@ -474,25 +491,26 @@ softmax_attn_dq_kernel(const __grid_constant__ CUtensorMap tQ, const __grid_cons
             }
             if (!ok) break;
             const bool some = hi > lo;
-            if (some) {
-                if (!warp_spin(&bar->acc_full, (items - 1) & 1, p.status, 96, abort_flag)) break;
-                tc_fence_after();
-            }
+            const DqItem next = dq_item(p, min(idx + (int)gridDim.x, p.items - 1));  // while dQ ends
             const int i = it.q0 + row;
             const bool exists = i < p.nq, valid = i < it.sp.Lq;
             __nv_bfloat16 *dst = p.dQ + it.batch * p.sdQ.b + it.head * p.sdQ.h + (int64_t)i * p.sdQ.n;
-#pragma unroll
-            for (int c = 0; c < DP / 2; c += 16) {
-                uint32_t o[16];
-                const int col = group * (DP / 2) + c;
-                if (some) tmem_ld16(tmem + C::kDq + col + lanes, o);
-                if (exists) store_row(dst, o, col, p.d, p.scale, !some || !valid, p.wide & 1);
-            }
             if (some) {
+                if (!warp_spin(&bar->acc_full, (items - 1) & 1, p.status, 96, abort_flag)) break;
+                tc_fence_after();
+                uint32_t o[DP / 64][32];  // the group's half of the columns
+                load_columns(tmem + C::kDq + group * (DP / 2) + lanes, o);
                 tc_fence_before();
                 __syncwarp();
                 if (lane == 0) mbar_arrive(&bar->acc_free);
+                if (exists)
+#pragma unroll
+                    for (int c = 0; c < DP / 64; ++c)
+                        store_row(dst, o[c], group * (DP / 2) + 32 * c, p.d, p.scale, !valid, p.wide & 1);
+            } else if (exists && group == 0) {
+                zero_row(dst, p.d);
             }
+            it = next;
         }
     }
     tc_fence_before();
@@ -756,8 +774,8 @@ softmax_attn_dkv_kernel(const __grid_constant__ CUtensorMap tQ, const __grid_con
         const float2 sl2 = make_float2(sl, sl);
         int n = 0, items = 0;
         bool ok = true;
+        DkvItem it = dkv_item(p, min((int)blockIdx.x, p.items - 1));
         for (int idx = blockIdx.x; idx < p.items && ok; idx += gridDim.x) {
-            const DkvItem it = dkv_item(p, idx);
             const int key = it.k0 + row, off = it.sp.Lk - it.sp.Lq, lo = it.lo, hi = it.hi,
                       steps = (hi - lo) * p.group;
             // queries [first, end) see this key (the rows past the length need no mask: their
@@ -850,27 +868,29 @@ softmax_attn_dkv_kernel(const __grid_constant__ CUtensorMap tQ, const __grid_con
             n += max(0, steps);
             if (!ok) break;
             const bool some = steps > 0;
+            const DkvItem next = dkv_item(p, min(idx + (int)gridDim.x, p.items - 1));  // while the sums end
+            const bool exists = key < p.nk, valid = key < it.sp.Lk;
+            // warps 0-3 write dV, warps 4-7 dK
+            __nv_bfloat16 *dst =
+                group ? p.dK + it.batch * p.sdK.b + it.kvh * p.sdK.h + (int64_t)key * p.sdK.n
+                      : p.dV + it.batch * p.sdV.b + it.kvh * p.sdV.h + (int64_t)key * p.sdV.n;
             if (some) {
                 if (!warp_spin(&bar->acc_full, items & 1, p.status, 114, abort_flag)) break;
                 tc_fence_after();
                 ++items;
-            }
-            const bool exists = key < p.nk, valid = key < it.sp.Lk;
-            __nv_bfloat16 *dk = p.dK + it.batch * p.sdK.b + it.kvh * p.sdK.h + (int64_t)key * p.sdK.n;
-            __nv_bfloat16 *dv = p.dV + it.batch * p.sdV.b + it.kvh * p.sdV.h + (int64_t)key * p.sdV.n;
-            // warps 0-3 write dV, warps 4-7 dK
-#pragma unroll
-            for (int c = 0; c < DP; c += 16) {
-                uint32_t o[16];
-                if (some) tmem_ld16(tmem + (group ? C::kDk : C::kDv) + c + lanes, o);
-                if (exists) store_row(group ? dk : dv, o, c, p.d, group ? p.scale : 1.f, !some || !valid,
-                                      p.wide >> (group ? 1 : 2) & 1);
-            }
-            if (some) {
+                uint32_t o[DP / 32][32];
+                load_columns(tmem + (group ? C::kDk : C::kDv) + lanes, o);
                 tc_fence_before();
                 __syncwarp();
                 if (lane == 0) mbar_arrive(&bar->acc_free);
+                if (exists)
+#pragma unroll
+                    for (int c = 0; c < DP / 32; ++c)
+                        store_row(dst, o[c], 32 * c, p.d, group ? p.scale : 1.f, !valid, p.wide >> (group ? 1 : 2) & 1);
+            } else if (exists) {
+                zero_row(dst, p.d);
             }
+            it = next;
         }
     }
     if (warp == kLoadWarp) wait_prerequisites();  // no later kernel before the second one has ended

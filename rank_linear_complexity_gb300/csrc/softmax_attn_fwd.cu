@@ -436,21 +436,34 @@ softmax_attn_fwd_kernel(const __grid_constant__ CUtensorMap tQ, const __grid_con
             }
             return ok;
         };
-        for (int idx = blockIdx.x; idx < p.items && ok; idx += gridDim.x) {
+        // What the thread's row does in an item, worked out while the item before it ends.
+        struct Row {
             int lo, hi, first, end;
-            bool valid, warp_valid;
-            {
-                const Item it = load_item(p, idx);
-                const Tile x = t ? it.t[1] : it.t[0];
-                if (!x.live) continue;
-                const int i = x.q0 + qi;
-                lo = x.lo;
-                hi = x.hi;
-                valid = hi_ < p.hbox && x.h0 + hi_ < p.group && i < it.sp.Lq;
-                first = valid ? it.sp.first(i) : 0;
-                end = valid ? it.sp.end(i) : (1 << 30);
-                warp_valid = __any_sync(0xffffffffu, valid);
+            bool live, valid, warp_valid;
+        };
+        auto row_of = [&](int idx) {
+            const Item it = load_item(p, min(idx, p.items - 1));
+            const Tile x = t ? it.t[1] : it.t[0];
+            const int i = x.q0 + qi;
+            Row r;
+            r.live = x.live;
+            r.lo = x.lo;
+            r.hi = x.hi;
+            r.valid = x.live && hi_ < p.hbox && x.h0 + hi_ < p.group && i < it.sp.Lq;
+            r.first = r.valid ? it.sp.first(i) : 0;
+            r.end = r.valid ? it.sp.end(i) : (1 << 30);
+            r.warp_valid = __any_sync(0xffffffffu, r.valid);
+            return r;
+        };
+        Row next = row_of(blockIdx.x);
+        for (int idx = blockIdx.x; idx < p.items && ok; idx += gridDim.x) {
+            const Row now = next;
+            if (!now.live) {
+                next = row_of(idx + gridDim.x);
+                continue;
             }
+            const int lo = now.lo, hi = now.hi, first = now.first, end = now.end;
+            const bool valid = now.valid, warp_valid = now.warp_valid;
             float m = -INFINITY, l = 0.f;  // maximum (of the raw scores), sum of 2^((s - m) sl)
             for (int j = lo; j < hi; ++j, ++n) {
                 if (!warp_spin(&bar->s_full[t], n & 1, p.status, 80, abort_flag)) {
@@ -538,58 +551,63 @@ rescale_output(tO, DP, f);
             const Tile x = t ? it.t[1] : it.t[0];
             const int i = x.q0 + qi, hg = x.h0 + hi_;
             const bool exists = hi_ < p.hbox && hg < p.group && i < p.nq;
-            if (some) {
-                if (!warp_spin(&bar->pv_done[t], (n - 1) & 1, p.status, 82, abort_flag)) break;
-                tc_fence_after();
-            }
+            next = row_of(idx + gridDim.x);
             const bool dead = !valid || l == 0.f;
             const float inv = dead ? 0.f : 1.f / l;
             const float lse = dead ? -INFINITY : m * p.scale + logf(l);
             const int64_t head = (int64_t)it.kvh * p.group + hg;
             const int64_t r = ((int64_t)it.batch * p.hq + head) * p.nq + i;
-            if (p.nsplit > 1) {
-                const int64_t pr = (int64_t)it.split * p.b * p.hq * p.nq + r;
-                if (some && warp_valid) {
-                    float *dst = p.part_o + pr * DP;
-#pragma unroll
-                    for (int c = 0; c < DP; c += 32) {
-                        uint32_t o[32];
-                        tmem_ld32(tO + c, o);
-                        if (!dead)
-#pragma unroll
-                            for (int e = 0; e < 32; e += 4)
-                                *reinterpret_cast<float4 *>(dst + c + e) =
-                                    make_float4(__uint_as_float(o[e]) * inv, __uint_as_float(o[e + 1]) * inv,
-                                                __uint_as_float(o[e + 2]) * inv, __uint_as_float(o[e + 3]) * inv);
-                    }
-                }
-                if (exists) p.part_lse[pr] = lse;
-            } else {
-                __nv_bfloat16 *dst = p.out + it.batch * p.so.b + head * p.so.h + (int64_t)i * p.so.n;
-#pragma unroll
-                for (int c = 0; c < DP; c += 16) {
-                    uint32_t o[16], y[8];
-                    if (some && warp_valid) tmem_ld16(tO + c, o);
-                    if (!exists || c >= p.d) continue;
-#pragma unroll
-                    for (int e = 0; e < 8; ++e)
-                        y[e] = dead ? 0u : pack2(__uint_as_float(o[2 * e]) * inv, __uint_as_float(o[2 * e + 1]) * inv);
-                    // one store of 32 bytes where the tensor allows it: a warp's store touches
-                    // 32 rows, and each row's line costs a cycle of the load/store unit
-                    if (p.wide) {
-                        store32(dst + c, y);
-                    } else {
-                        *reinterpret_cast<uint4 *>(dst + c) = make_uint4(y[0], y[1], y[2], y[3]);
-                        if (c + 8 < p.d) *reinterpret_cast<uint4 *>(dst + c + 8) = make_uint4(y[4], y[5], y[6], y[7]);
-                    }
-                }
-                if (exists) p.lse[r] = lse;
-            }
+            const int64_t pr = (int64_t)it.split * p.b * p.hq * p.nq + r;
+            __nv_bfloat16 *dst = p.out + it.batch * p.so.b + head * p.so.h + (int64_t)i * p.so.n;
             if (some) {
-                tc_fence_before();
-                __syncwarp();
-                if (lane == 0) mbar_arrive(&bar->o_free[t]);
+                if (!warp_spin(&bar->pv_done[t], (n - 1) & 1, p.status, 82, abort_flag)) break;
+                tc_fence_after();
+                if (warp_valid) {
+                    uint32_t o[DP / 32][32];
+#pragma unroll
+                    for (int c = 0; c < DP / 32; ++c) tmem_ld32_async(tO + 32 * c, o[c]);
+                    tmem_wait_ld(o[0]);
+#pragma unroll
+                    for (int c = 1; c < DP / 32; ++c) tie32(o[c]);
+                    tc_fence_before();
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive(&bar->o_free[t]);
+#pragma unroll
+                    for (int c = 0; c < DP; c += 16) {
+                        float y[16];
+#pragma unroll
+                        for (int e = 0; e < 16; ++e) y[e] = dead ? 0.f : __uint_as_float(o[c / 32][c % 32 + e]) * inv;
+                        if (p.nsplit > 1) {
+                            if (dead) continue;
+#pragma unroll
+                            for (int e = 0; e < 16; e += 4)
+                                *reinterpret_cast<float4 *>(p.part_o + pr * DP + c + e) =
+                                    make_float4(y[e], y[e + 1], y[e + 2], y[e + 3]);
+                        } else if (exists && c < p.d) {
+                            uint32_t w[8];
+#pragma unroll
+                            for (int e = 0; e < 8; ++e) w[e] = pack2(y[2 * e], y[2 * e + 1]);
+                            // one store of 32 bytes where the tensor allows it: a warp's store
+                            // touches 32 rows, and each row's line costs a cycle of the
+                            // load/store unit
+                            if (p.wide) {
+                                store32(dst + c, w);
+                            } else {
+                                *reinterpret_cast<uint4 *>(dst + c) = make_uint4(w[0], w[1], w[2], w[3]);
+                                if (c + 8 < p.d) *reinterpret_cast<uint4 *>(dst + c + 8) = make_uint4(w[4], w[5], w[6], w[7]);
+                            }
+                        }
+                    }
+                } else {
+                    tc_fence_before();
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive(&bar->o_free[t]);
+                }
             }
+            if (!(some && warp_valid) && exists && p.nsplit == 1)
+#pragma unroll 1
+                for (int c = 0; c < p.d; c += 8) *reinterpret_cast<uint4 *>(dst + c) = make_uint4(0u, 0u, 0u, 0u);
+            if (exists) (p.nsplit > 1 ? p.part_lse[pr] : p.lse[r]) = lse;
         }
     }
     tc_fence_before();
