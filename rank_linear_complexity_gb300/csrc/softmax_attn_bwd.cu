@@ -61,22 +61,20 @@ struct BwdParams {
     int *status;
 };
 
-// Columns outside [a, a + w) become 0.
-__device__ __forceinline__ void mask_zero(uint32_t (&v)[32], int a, unsigned w) {
-#pragma unroll
-    for (int e = 0; e < 32; ++e)
-        if ((unsigned)(e - a) >= w) v[e] = 0u;
-}
-// The same for 128 columns in tensor memory (rolled: only blocks at a mask's edge).
-__device__ __forceinline__ void zero_outside(uint32_t t, int a, unsigned w) {
+// Columns outside [a, a + w) of 128 in tensor memory become `value`: for the few blocks at a
+// mask's edge, out of line, away from the code of the others.
+__device__ __noinline__ void fill_outside(uint32_t t, int a, unsigned w, uint32_t value) {
 #pragma unroll 1
     for (int c = 0; c < kTile; c += 32) {
         uint32_t u[32];
         tmem_ld32(t + c, u);
-        mask_zero(u, a - c, w);
+#pragma unroll
+        for (int e = 0; e < 32; ++e)
+            if ((unsigned)(c + e - a) >= w) u[e] = value;
         tmem_st32(t + c, u);
     }
 }
+constexpr uint32_t kMinusInf = 0xff800000u;
 __device__ __forceinline__ float4 lds4(uint32_t addr) {
     float4 v;
     asm volatile("ld.shared.v4.f32 {%0, %1, %2, %3}, [%4];"
@@ -436,6 +434,10 @@ softmax_attn_dq_kernel(const __grid_constant__ CUtensorMap tQ, const __grid_cons
                     break;
                 }
                 tc_fence_after();
+                // keys that take no part: P = 0 whatever S holds, and dP = 0 below whatever it holds
+                const int k0 = j * kTile;
+                const bool masked = __any_sync(0xffffffffu, first > k0 || end < k0 + kTile);
+                if (masked) fill_outside(tmem + C::kS + lanes, first - k0, width, kMinusInf);
                 uint32_t v[4][32];
 #pragma unroll
                 for (int c = 0; c < 4; ++c) tmem_ld32_async(tmem + C::kS + 32 * c + lanes, v[c]);
@@ -456,24 +458,19 @@ softmax_attn_dq_kernel(const __grid_constant__ CUtensorMap tQ, const __grid_cons
                         v[c][e] = __float_as_uint(ex2_approx(y.x));
                         v[c][e + 1] = __float_as_uint(ex2_approx(y.y));
                     }
-                // keys that take no part: P = 0 whatever S holds, and dP = delta below whatever
-                // it holds
-                const int k0 = j * kTile;
-                const bool masked = __any_sync(0xffffffffu, first > k0 || end < k0 + kTile);
                 const uint32_t tD = tmem + C::kDp + 128 * (g & 1) + lanes;
                 if (!warp_spin(&bar->dp_full[g & 1], (g >> 1) & 1, p.status, 95, abort_flag)) {
                     ok = false;
                     break;
                 }
                 tc_fence_after();
-                if (masked) zero_outside(tD, first - k0, width);
+                if (masked) fill_outside(tD, first - k0, width, 0u);
                 const float2 nd2 = make_float2(nd, nd);
                 // 32 columns at a time; dS takes the columns that have been read
 #pragma unroll
                 for (int c = 0; c < 4; ++c) {
                     uint32_t u[32], o[16];
                     tmem_ld32(tD + 32 * c, u);
-                    if (masked) mask_zero(v[c], first - k0 - 32 * c, width);
 #pragma unroll
                     for (int e = 0; e < 32; e += 2) {
                         const float2 y = fadd2(make_float2(__uint_as_float(u[e]), __uint_as_float(u[e + 1])), nd2);
@@ -797,6 +794,9 @@ softmax_attn_dkv_kernel(const __grid_constant__ CUtensorMap tQ, const __grid_con
                     break;
                 }
                 tc_fence_after();
+                const int q0 = (lo + j) * kTile;
+                if (__any_sync(0xffffffffu, first > q0 || end < q0 + kTile))
+                    fill_outside(tS, first - q0, width, kMinusInf);
                 uint32_t v[4][32];
 #pragma unroll
                 for (int c = 0; c < 4; ++c) tmem_ld32_async(tS + 32 * c, v[c]);
@@ -804,8 +804,6 @@ softmax_attn_dkv_kernel(const __grid_constant__ CUtensorMap tQ, const __grid_con
                 tie32(v[1]);
                 tie32(v[2]);
                 tie32(v[3]);
-                const int q0 = (lo + j) * kTile;
-                const bool masked = __any_sync(0xffffffffu, first > q0 || end < q0 + kTile);
 #pragma unroll
                 for (int c = 0; c < 4; ++c) {
 #pragma unroll
@@ -820,7 +818,6 @@ softmax_attn_dkv_kernel(const __grid_constant__ CUtensorMap tQ, const __grid_con
                         v[c][e + 2] = __float_as_uint(ex2_approx(y1.x));
                         v[c][e + 3] = __float_as_uint(ex2_approx(y1.y));
                     }
-                    if (masked) mask_zero(v[c], first - q0 - 32 * c, width);
                     uint32_t o[16];
 #pragma unroll
                     for (int e = 0; e < 16; ++e)
