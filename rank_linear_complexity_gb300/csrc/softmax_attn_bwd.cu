@@ -17,9 +17,8 @@
 // partial dQ through memory in a fixed order.  P and dS are rounded to bf16 as operands
 // (relative 2^-9, in sums of many terms); sums are fp32 in tensor memory.
 //
-// Roles, both kernels: warps 0-3 and 4-7 do the arithmetic of even and of odd steps, one
-// thread a row of 128 columns.  The groups are half a step apart, so that one's exponentials
-// (special function unit) run beside the other's dS (multiplications) and its waits;
+// Roles, both kernels: warps 0-3 and 4-7 do the arithmetic of the two halves (64 columns) of
+// every step, one thread a row; each half's P or dS is multiplied as soon as it is there;
 // warp 8 loads (lane 0) and zeroes rows past the valid length (lanes 1-31, where 0 x NaN
 // would reach a sum); one thread each of warps 9 and 10 issues products, so that a chain of
 // products that waits for arithmetic does not hold up the other one.
@@ -40,7 +39,7 @@ using namespace ptx;
 constexpr int kThreads = 384;
 constexpr uint32_t kMathRegs = 208, kIssueRegs = 88;
 static_assert(2 * kMathRegs + kIssueRegs == 3 * 168, "register split");
-constexpr int kMathWarps = 8, kGroupWarps = 4, kLoadWarp = 8, kMmaWarp = 9;
+constexpr int kMathWarps = 8, kHalfWarps = 4, kLoadWarp = 8, kMmaWarp = 9;
 constexpr float kLog2e = 1.4426950408889634f;
 
 struct BwdParams {
@@ -61,11 +60,11 @@ struct BwdParams {
     int *status;
 };
 
-// Columns outside [a, a + w) of 128 in tensor memory become `value`: for the few blocks at a
+// Columns outside [a, a + w) of 64 in tensor memory become `value`: for the few blocks at a
 // mask's edge, out of line, away from the code of the others.
 __device__ __noinline__ void fill_outside(uint32_t t, int a, unsigned w, uint32_t value) {
 #pragma unroll 1
-    for (int c = 0; c < kTile; c += 32) {
+    for (int c = 0; c < 64; c += 32) {
         uint32_t u[32];
         tmem_ld32(t + c, u);
 #pragma unroll
@@ -151,39 +150,45 @@ __device__ __forceinline__ void load_rows(uint8_t *dst, const CUtensorMap *m, ui
 }
 
 // ---------------------------------------------------------------- row values
-// -lse log2(e) and -delta = -dO.O of a query tile's 128 rows, eight warps of sixteen rows, read
-// by whole warps (8 bytes a lane).  Bound by memory: O and dO once.
+// -lse log2(e) and -delta = -dO.O of a query tile's 128 rows, eight warps of sixteen rows; a row
+// is read by DP / 8 lanes, 16 bytes each.  Bound by memory: O and dO once.
 constexpr int kRowsThreads = 256;
+template <int DP>
 __global__ void __launch_bounds__(kRowsThreads) rows_kernel(const BwdParams p) {
     launch_dependents();
+    constexpr int kLanes = DP / 8, kAtOnce = 32 / kLanes, kTurns = 16 / kAtOnce;
     const int unit = blockIdx.x / p.qtiles, tile = blockIdx.x - unit * p.qtiles;
     const int batch = unit / p.hq, head = unit - batch * p.hq;
-    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, r0 = tile * kTile + 16 * warp;
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, col = lane % kLanes * 8;
     const int Lq = clamp_length(p.q_lengths, batch, p.nq);
-    const __nv_bfloat16 *o = p.O + batch * p.sO.b + head * p.sO.h + 4 * lane;
-    const __nv_bfloat16 *g = p.dO + batch * p.sdO.b + head * p.sdO.h + 4 * lane;
-    uint2 a[16], b[16];
+    const int r0 = tile * kTile + 16 * warp + lane / kLanes;  // the lane's row of the first turn
+    const __nv_bfloat16 *o = p.O + batch * p.sO.b + head * p.sO.h + col;
+    const __nv_bfloat16 *g = p.dO + batch * p.sdO.b + head * p.sdO.h + col;
+    uint4 a[kTurns], b[kTurns];
+    float x[kTurns];
 #pragma unroll
-    for (int r = 0; r < 16; ++r) {
-        a[r] = b[r] = make_uint2(0u, 0u);
-        if (r0 + r < Lq && 4 * lane < p.d) {
-            a[r] = __ldg(reinterpret_cast<const uint2 *>(o + (int64_t)(r0 + r) * p.sO.n));
-            b[r] = __ldg(reinterpret_cast<const uint2 *>(g + (int64_t)(r0 + r) * p.sdO.n));
+    for (int t = 0; t < kTurns; ++t) {
+        const int i = r0 + t * kAtOnce;
+        a[t] = b[t] = make_uint4(0u, 0u, 0u, 0u);
+        x[t] = -INFINITY;
+        if (i < Lq) {
+            if (col < p.d) {
+                a[t] = __ldg(reinterpret_cast<const uint4 *>(o + (int64_t)i * p.sO.n));
+                b[t] = __ldg(reinterpret_cast<const uint4 *>(g + (int64_t)i * p.sdO.n));
+            }
+            x[t] = __ldg(p.lse + (int64_t)unit * p.nq + i);
         }
     }
-    float x = -INFINITY, delta = 0.f;
-    if (lane < 16 && r0 + lane < Lq) x = __ldg(p.lse + (int64_t)unit * p.nq + r0 + lane);
+    float *dst = p.rows + (int64_t)blockIdx.x * 256 + 16 * warp + lane / kLanes;
 #pragma unroll
-    for (int r = 0; r < 16; ++r) {
-        float y = dot2(a[r].x, b[r].x) + dot2(a[r].y, b[r].y);
+    for (int t = 0; t < kTurns; ++t) {
+        float y = (dot2(a[t].x, b[t].x) + dot2(a[t].y, b[t].y)) + (dot2(a[t].z, b[t].z) + dot2(a[t].w, b[t].w));
 #pragma unroll
-        for (int k = 16; k; k >>= 1) y += __shfl_xor_sync(0xffffffffu, y, k);
-        if (lane == r) delta = y;
-    }
-    if (lane < 16) {
-        float *dst = p.rows + (int64_t)blockIdx.x * 256 + 16 * warp + lane;
-        dst[0] = x == -INFINITY ? -INFINITY : -x * kLog2e;
-        dst[128] = x == -INFINITY ? 0.f : -delta;
+        for (int k = kLanes / 2; k; k >>= 1) y += __shfl_xor_sync(0xffffffffu, y, k);
+        if (lane % kLanes == 0) {
+            dst[t * kAtOnce] = x[t] == -INFINITY ? -INFINITY : -x[t] * kLog2e;
+            dst[t * kAtOnce + 128] = x[t] == -INFINITY ? 0.f : -y;
+        }
     }
 }
 
@@ -222,7 +227,7 @@ __device__ __forceinline__ DqItem dq_item(const BwdParams &p, int idx) {
 }
 
 struct DqBarriers {
-    // (pairs: even and odd blocks, each with a group of warps of its own)
+    // (pairs: even and odd blocks)
     uint64_t q_full, q_free, s_full[2], s_free, dp_full[2], ds_full[2][2], dq_done[2];
     uint64_t acc_full, acc_free;
     uint64_t fix_wanted, fixed, drain[2];
@@ -250,12 +255,12 @@ softmax_attn_dq_kernel(const __grid_constant__ CUtensorMap tQ, const __grid_cons
     if (tid == 0) {
         mbar_init(&bar->q_full, 1);
         mbar_init(&bar->q_free, 1 + kMathWarps);  // the products, and the rows read
-        mbar_init(&bar->s_free, kGroupWarps);
+        mbar_init(&bar->s_free, kMathWarps);
         for (int i = 0; i < 2; ++i) {
             mbar_init(&bar->s_full[i], 1);
             mbar_init(&bar->dp_full[i], 1);
-            mbar_init(&bar->ds_full[i][0], kGroupWarps);  // halves of 64 columns
-            mbar_init(&bar->ds_full[i][1], kGroupWarps);
+            mbar_init(&bar->ds_full[i][0], kHalfWarps);  // halves of 64 columns
+            mbar_init(&bar->ds_full[i][1], kHalfWarps);
             mbar_init(&bar->dq_done[i], 1);
         }
         mbar_init(&bar->acc_full, 1);
@@ -392,7 +397,7 @@ softmax_attn_dq_kernel(const __grid_constant__ CUtensorMap tQ, const __grid_cons
                     ok = thread_spin(&bar->ds_full[n & 1][1], (n >> 1) & 1, p.status, 92, abort_flag);
                     if (!ok) break;
                     tc_fence_after();
-                    mma_sum_half<DP>(tmem + C::kDq, ds + 32, k + 8192, 1u);
+                    mma_sum_half<DP>(tmem + C::kDq, ds + 64, k + 8192, 1u);
                     mma_commit(&bar->dq_done[n & 1]);
                     mma_commit(&bar->empty[s]);
                 }
@@ -406,7 +411,7 @@ softmax_attn_dq_kernel(const __grid_constant__ CUtensorMap tQ, const __grid_cons
     }
     } else {
         setmaxnreg_inc<kMathRegs>();
-        const int group = warp >> 2, row = tid & 127;
+        const int half = warp >> 2, row = tid & 127;
         const uint32_t lanes = (uint32_t)((warp & 3) * 32) << 16;
         const float sl = p.scale_log2;
         int n = 0, items = 0;
@@ -426,31 +431,25 @@ softmax_attn_dq_kernel(const __grid_constant__ CUtensorMap tQ, const __grid_cons
             const int first = seen ? it.sp.first(it.q0 + row) : 0, end = seen ? it.sp.end(it.q0 + row) : 0;
             const unsigned width = end > first ? (unsigned)(end - first) : 0u;
             bool ok = true;
-            const int n0 = n;
-            n += max(0, hi - lo);
-            for (int j = lo + ((n0 ^ group) & 1), g = n0 + ((n0 ^ group) & 1); j < hi; j += 2, g += 2) {
+            for (int j = lo, g = n; j < hi; ++j, ++g) {
                 if (!warp_spin(&bar->s_full[g & 1], (g >> 1) & 1, p.status, 94, abort_flag)) {
                     ok = false;
                     break;
                 }
                 tc_fence_after();
                 // keys that take no part: P = 0 whatever S holds, and dP = 0 below whatever it holds
-                const int k0 = j * kTile;
-                const bool masked = __any_sync(0xffffffffu, first > k0 || end < k0 + kTile);
-                if (masked) fill_outside(tmem + C::kS + lanes, first - k0, width, kMinusInf);
-                uint32_t v[4][32];
-#pragma unroll
-                for (int c = 0; c < 4; ++c) tmem_ld32_async(tmem + C::kS + 32 * c + lanes, v[c]);
-                tmem_wait_ld(v[0]);
-                tie32(v[1]);
-                tie32(v[2]);
-                tie32(v[3]);
+                const int k0 = j * kTile + 64 * half;
+                const bool masked = __any_sync(0xffffffffu, first > k0 || end < k0 + 64);
+                const uint32_t tS = tmem + C::kS + 64 * half + lanes;
+                if (masked) fill_outside(tS, first - k0, width, kMinusInf);
+                uint32_t v[2][32];
+                load_columns(tS, v);
                 tc_fence_before();
                 __syncwarp();
                 if (lane == 0) mbar_arrive(&bar->s_free);
                 const float2 sl2 = make_float2(sl, sl), off2 = make_float2(nl, nl);
 #pragma unroll
-                for (int c = 0; c < 4; ++c)
+                for (int c = 0; c < 2; ++c)
 #pragma unroll
                     for (int e = 0; e < 32; e += 2) {
                         const float2 y = ffma2(make_float2(__uint_as_float(v[c][e]), __uint_as_float(v[c][e + 1])),
@@ -458,7 +457,7 @@ softmax_attn_dq_kernel(const __grid_constant__ CUtensorMap tQ, const __grid_cons
                         v[c][e] = __float_as_uint(ex2_approx(y.x));
                         v[c][e + 1] = __float_as_uint(ex2_approx(y.y));
                     }
-                const uint32_t tD = tmem + C::kDp + 128 * (g & 1) + lanes;
+                const uint32_t tD = tmem + C::kDp + 128 * (g & 1) + 64 * half + lanes;
                 if (!warp_spin(&bar->dp_full[g & 1], (g >> 1) & 1, p.status, 95, abort_flag)) {
                     ok = false;
                     break;
@@ -466,26 +465,22 @@ softmax_attn_dq_kernel(const __grid_constant__ CUtensorMap tQ, const __grid_cons
                 tc_fence_after();
                 if (masked) fill_outside(tD, first - k0, width, 0u);
                 const float2 nd2 = make_float2(nd, nd);
-                // 32 columns at a time; dS takes the columns that have been read
+                uint32_t u[2][32], o[32];
+                load_columns(tD, u);
 #pragma unroll
-                for (int c = 0; c < 4; ++c) {
-                    uint32_t u[32], o[16];
-                    tmem_ld32(tD + 32 * c, u);
+                for (int c = 0; c < 2; ++c)
 #pragma unroll
                     for (int e = 0; e < 32; e += 2) {
-                        const float2 y = fadd2(make_float2(__uint_as_float(u[e]), __uint_as_float(u[e + 1])), nd2);
+                        const float2 y = fadd2(make_float2(__uint_as_float(u[c][e]), __uint_as_float(u[c][e + 1])), nd2);
                         const float2 z = fmul2(make_float2(__uint_as_float(v[c][e]), __uint_as_float(v[c][e + 1])), y);
-                        o[e / 2] = pack2(z.x, z.y);
+                        o[16 * c + e / 2] = pack2(z.x, z.y);
                     }
-                    tmem_st16_async(tD + 16 * c, o);
-                    if (c & 1) {
-                        tmem_wait_st();
-                        tc_fence_before();
-                        __syncwarp();
-                        if (lane == 0) mbar_arrive(&bar->ds_full[g & 1][c >> 1]);
-                    }
-                }
+                tmem_st32(tD, o);
+                tc_fence_before();
+                __syncwarp();
+                if (lane == 0) mbar_arrive(&bar->ds_full[g & 1][half]);
             }
+            n += max(0, hi - lo);
             if (!ok) break;
             const bool some = hi > lo;
             const DqItem next = dq_item(p, min(idx + (int)gridDim.x, p.items - 1));  // while dQ ends
@@ -495,16 +490,16 @@ softmax_attn_dq_kernel(const __grid_constant__ CUtensorMap tQ, const __grid_cons
             if (some) {
                 if (!warp_spin(&bar->acc_full, (items - 1) & 1, p.status, 96, abort_flag)) break;
                 tc_fence_after();
-                uint32_t o[DP / 64][32];  // the group's half of the columns
-                load_columns(tmem + C::kDq + group * (DP / 2) + lanes, o);
+                uint32_t o[DP / 64][32];  // half of the columns
+                load_columns(tmem + C::kDq + half * (DP / 2) + lanes, o);
                 tc_fence_before();
                 __syncwarp();
                 if (lane == 0) mbar_arrive(&bar->acc_free);
                 if (exists)
 #pragma unroll
                     for (int c = 0; c < DP / 64; ++c)
-                        store_row(dst, o[c], group * (DP / 2) + 32 * c, p.d, p.scale, !valid, p.wide & 1);
-            } else if (exists && group == 0) {
+                        store_row(dst, o[c], half * (DP / 2) + 32 * c, p.d, p.scale, !valid, p.wide & 1);
+            } else if (exists && half == 0) {
                 zero_row(dst, p.d);
             }
             it = next;
@@ -588,8 +583,8 @@ softmax_attn_dkv_kernel(const __grid_constant__ CUtensorMap tQ, const __grid_con
             mbar_init(&bar->kv_free[i], 2);
             mbar_init(&bar->s_full[i], 1);
             for (int h = 0; h < 2; ++h) {  // halves of 64 columns
-                mbar_init(&bar->p_full[i][h], kGroupWarps);
-                mbar_init(&bar->ds_full[i][h], kGroupWarps);
+                mbar_init(&bar->p_full[i][h], kHalfWarps);
+                mbar_init(&bar->ds_full[i][h], kHalfWarps);
             }
             mbar_init(&bar->pv_done[i], 1);
             mbar_init(&bar->dp_full[i], 1);
@@ -740,7 +735,7 @@ softmax_attn_dkv_kernel(const __grid_constant__ CUtensorMap tQ, const __grid_con
                     mma_sum_half<DP>(d, m, t, g > n ? 1u : 0u);
                     if (!thread_spin(&ready[g & 1][1], phase(g), p.status, 108, abort_flag)) return false;
                     tc_fence_after();
-                    mma_sum_half<DP>(d, m + 32, t + 8192, 1u);
+                    mma_sum_half<DP>(d, m + 64, t + 8192, 1u);
                     mma_commit(&done[g & 1]);
                     mma_commit(&bar->empty[s]);
                     return true;
@@ -765,7 +760,7 @@ softmax_attn_dkv_kernel(const __grid_constant__ CUtensorMap tQ, const __grid_con
     }
     } else {
         setmaxnreg_inc<kMathRegs>();
-        const int group = warp >> 2, row = tid & 127;
+        const int half = warp >> 2, row = tid & 127;
         const uint32_t lanes = (uint32_t)((warp & 3) * 32) << 16;
         const float sl = p.scale_log2;
         const float2 sl2 = make_float2(sl, sl);
@@ -780,13 +775,12 @@ softmax_attn_dkv_kernel(const __grid_constant__ CUtensorMap tQ, const __grid_con
             const int first = p.causal ? max(0, key - off) : 0;
             const int end = p.window ? (int)min((long long)it.sp.Lq, (long long)key - off + p.window) : 1 << 30;
             const unsigned width = end > first ? (unsigned)(end - first) : 0u;
-            const int skip = (n ^ group) & 1, per = hi - lo;
-            int j = skip && per > 0 ? skip % per : 0;  // tile of the step within its head
-            for (int g = n + skip; g < n + steps; g += 2) {
+            int j = lo;
+            for (int g = n; g < n + steps; ++g) {
                 const int s = g % C::kStages;
-                const uint32_t tS = tmem + 128 * (2 * g % C::kBufs) + lanes,
-                               tD = tmem + 128 * ((2 * g + 1) % C::kBufs) + lanes;
-                const uint32_t aR = smem_u32(sR) + s * 1024;  // the rows' -lse and, 512 on, -delta
+                const uint32_t tS = tmem + 128 * (2 * g % C::kBufs) + 64 * half + lanes,
+                               tD = tmem + 128 * ((2 * g + 1) % C::kBufs) + 64 * half + lanes;
+                const uint32_t aR = smem_u32(sR) + s * 1024 + 256 * half;  // -lse and, 512 on, -delta
                 const uint32_t parity = (uint32_t)(g >> 1) & 1u;
                 if (!warp_spin(&bar->full[s], (g / C::kStages) & 1, p.status, 111, abort_flag) ||
                     !warp_spin(&bar->s_full[g & 1], parity, p.status, 112, abort_flag)) {
@@ -794,18 +788,13 @@ softmax_attn_dkv_kernel(const __grid_constant__ CUtensorMap tQ, const __grid_con
                     break;
                 }
                 tc_fence_after();
-                const int q0 = (lo + j) * kTile;
-                if (__any_sync(0xffffffffu, first > q0 || end < q0 + kTile))
+                const int q0 = j * kTile + 64 * half;
+                if (__any_sync(0xffffffffu, first > q0 || end < q0 + 64))
                     fill_outside(tS, first - q0, width, kMinusInf);
-                uint32_t v[4][32];
+                uint32_t v[2][32], o[32];
+                load_columns(tS, v);
 #pragma unroll
-                for (int c = 0; c < 4; ++c) tmem_ld32_async(tS + 32 * c, v[c]);
-                tmem_wait_ld(v[0]);
-                tie32(v[1]);
-                tie32(v[2]);
-                tie32(v[3]);
-#pragma unroll
-                for (int c = 0; c < 4; ++c) {
+                for (int c = 0; c < 2; ++c)
 #pragma unroll
                     for (int e = 0; e < 32; e += 4) {
                         const float4 l = lds4(aR + 4 * (32 * c + e));
@@ -817,50 +806,39 @@ softmax_attn_dkv_kernel(const __grid_constant__ CUtensorMap tQ, const __grid_con
                         v[c][e + 1] = __float_as_uint(ex2_approx(y0.y));
                         v[c][e + 2] = __float_as_uint(ex2_approx(y1.x));
                         v[c][e + 3] = __float_as_uint(ex2_approx(y1.y));
+                        o[16 * c + e / 2] = pack2(__uint_as_float(v[c][e]), __uint_as_float(v[c][e + 1]));
+                        o[16 * c + e / 2 + 1] = pack2(__uint_as_float(v[c][e + 2]), __uint_as_float(v[c][e + 3]));
                     }
-                    uint32_t o[16];
-#pragma unroll
-                    for (int e = 0; e < 16; ++e)
-                        o[e] = pack2(__uint_as_float(v[c][2 * e]), __uint_as_float(v[c][2 * e + 1]));
-                    tmem_st16_async(tS + 16 * c, o);
-                    if (c & 1) {
-                        tmem_wait_st();
-                        tc_fence_before();
-                        __syncwarp();
-                        if (lane == 0) mbar_arrive(&bar->p_full[g & 1][c >> 1]);
-                    }
-                }
+                tmem_st32(tS, o);
+                tc_fence_before();
+                __syncwarp();
+                if (lane == 0) mbar_arrive(&bar->p_full[g & 1][half]);
                 if (!warp_spin(&bar->dp_full[g & 1], parity, p.status, 113, abort_flag)) {
                     ok = false;
                     break;
                 }
                 tc_fence_after();
-                // 32 columns at a time; dS takes the columns that have been read
+                uint32_t u[2][32];
+                load_columns(tD, u);
 #pragma unroll
-                for (int c = 0; c < 4; ++c) {
-                    uint32_t u[32], o[16];
-                    tmem_ld32(tD + 32 * c, u);
+                for (int c = 0; c < 2; ++c)
 #pragma unroll
                     for (int e = 0; e < 32; e += 4) {
                         const float4 dl = lds4(aR + 512 + 4 * (32 * c + e));
-                        const float2 y0 = fadd2(make_float2(__uint_as_float(u[e]), __uint_as_float(u[e + 1])),
+                        const float2 y0 = fadd2(make_float2(__uint_as_float(u[c][e]), __uint_as_float(u[c][e + 1])),
                                                 make_float2(dl.x, dl.y));
-                        const float2 y1 = fadd2(make_float2(__uint_as_float(u[e + 2]), __uint_as_float(u[e + 3])),
+                        const float2 y1 = fadd2(make_float2(__uint_as_float(u[c][e + 2]), __uint_as_float(u[c][e + 3])),
                                                 make_float2(dl.z, dl.w));
                         const float2 z0 = fmul2(make_float2(__uint_as_float(v[c][e]), __uint_as_float(v[c][e + 1])), y0);
                         const float2 z1 = fmul2(make_float2(__uint_as_float(v[c][e + 2]), __uint_as_float(v[c][e + 3])), y1);
-                        o[e / 2] = pack2(z0.x, z0.y);
-                        o[e / 2 + 1] = pack2(z1.x, z1.y);
+                        o[16 * c + e / 2] = pack2(z0.x, z0.y);
+                        o[16 * c + e / 2 + 1] = pack2(z1.x, z1.y);
                     }
-                    tmem_st16_async(tD + 16 * c, o);
-                    if (c & 1) {
-                        tmem_wait_st();
-                        tc_fence_before();
-                        __syncwarp();
-                        if (lane == 0) mbar_arrive(&bar->ds_full[g & 1][c >> 1]);
-                    }
-                }
-                j = (j + 2) % per;
+                tmem_st32(tD, o);
+                tc_fence_before();
+                __syncwarp();
+                if (lane == 0) mbar_arrive(&bar->ds_full[g & 1][half]);
+                if (++j == hi) j = lo;
             }
             n += max(0, steps);
             if (!ok) break;
@@ -869,21 +847,21 @@ softmax_attn_dkv_kernel(const __grid_constant__ CUtensorMap tQ, const __grid_con
             const bool exists = key < p.nk, valid = key < it.sp.Lk;
             // warps 0-3 write dV, warps 4-7 dK
             __nv_bfloat16 *dst =
-                group ? p.dK + it.batch * p.sdK.b + it.kvh * p.sdK.h + (int64_t)key * p.sdK.n
+                half ? p.dK + it.batch * p.sdK.b + it.kvh * p.sdK.h + (int64_t)key * p.sdK.n
                       : p.dV + it.batch * p.sdV.b + it.kvh * p.sdV.h + (int64_t)key * p.sdV.n;
             if (some) {
                 if (!warp_spin(&bar->acc_full, items & 1, p.status, 114, abort_flag)) break;
                 tc_fence_after();
                 ++items;
                 uint32_t o[DP / 32][32];
-                load_columns(tmem + (group ? C::kDk : C::kDv) + lanes, o);
+                load_columns(tmem + (half ? C::kDk : C::kDv) + lanes, o);
                 tc_fence_before();
                 __syncwarp();
                 if (lane == 0) mbar_arrive(&bar->acc_free);
                 if (exists)
 #pragma unroll
                     for (int c = 0; c < DP / 32; ++c)
-                        store_row(dst, o[c], 32 * c, p.d, group ? p.scale : 1.f, !valid, p.wide >> (group ? 1 : 2) & 1);
+                        store_row(dst, o[c], 32 * c, p.d, half ? p.scale : 1.f, !valid, p.wide >> (half ? 1 : 2) & 1);
             } else if (exists) {
                 zero_row(dst, p.d);
             }
@@ -918,7 +896,7 @@ int launch(const Call &c, BwdParams &p) {
     const int sms = device_sms();
     {
         KernelScope scope(LINFORMER_KERNEL_SOFTMAX_BWD, c.stream);
-        rows_kernel<<<(unsigned)qitems, kRowsThreads, 0, c.stream>>>(p);
+        rows_kernel<DP><<<(unsigned)qitems, kRowsThreads, 0, c.stream>>>(p);
         if (cudaGetLastError() != cudaSuccess) st = LINFORMER_ERR_LAUNCH;
     }
     // The other two as programmatic dependents: the second is set up while the first ends, and
