@@ -28,7 +28,8 @@
  * t >= L of K and V count as zero before the projection, whatever they hold,
  * and query rows i >= L get O = 0.  NULL means L = n for every entry.
  *
- * Layouts: every tensor is dense and row-major.  Q, K, V, O: [b][h][n][d].
+ * Layouts: every tensor is dense and row-major, but for the calls that take strides (see
+ * there).  Q, K, V, O: [b][h][n][d].
  * E, F: as listed above ([k][n] rows of length n).
  *
  * Number types (dtype):
@@ -228,8 +229,9 @@ LINFORMER_API int linformer_dense_attn_fwd(const void *Q, const void *K, const v
  * [b][heads][n][d], its element strides {batch, head, row} as int64_t[3] (host memory, read
  * during the call), or NULL for a dense tensor; the last dimension is contiguous.  A stride
  * of a dimension of size one is ignored; others are positive and at most 2^38.  An output's
- * strides are at least d (its elements must not overlap each other or an input, except
- * where a call says that it works in place).
+ * strides are at least d, and its elements must not overlap each other or another tensor of the
+ * call, except where a call says that it works in place (an output that starts where another
+ * tensor does is refused with LINFORMER_ERR_VALUE).
  */
 
 /*
@@ -249,8 +251,9 @@ LINFORMER_API int linformer_dense_attn_fwd(const void *Q, const void *K, const v
  *
  * Q, O: [b][hq][nq][d]; K, V: [b][hk][nk][d], hq a multiple of hk; lse: dense fp32
  * [b][hq][nq].  dtype LINFORMER_BF16 (else LINFORMER_ERR_UNSUPPORTED), d a multiple of 8 up
- * to 128 (else LINFORMER_ERR_UNSUPPORTED), 0 < scale < infinity, causal 0 or 1, window >= 0
- * and 0 unless causal (else LINFORMER_ERR_VALUE); nq, nk and b hq up to 2^29.  Pointers are
+ * to 128 (else LINFORMER_ERR_UNSUPPORTED), 0 < scale < 2^127, causal 0 or 1, window >= 0
+ * and 0 unless causal (else LINFORMER_ERR_VALUE); nq, nk and b hq up to 2^29, and up to 2^30 tiles of 128 rows over
+ * all heads (else LINFORMER_ERR_SIZE).  Pointers are
  * 16-byte aligned (lse and the lengths: 4) and strides multiples of 8.  A few query rows
  * (single tokens over a cache) are served by splitting the keys over the GPU; the parts are
  * joined in a stream-ordered workspace.  The result of a call does not depend on timing.

@@ -97,12 +97,11 @@ __device__ __forceinline__ bool warp_wait(uint64_t *bar, uint32_t parity, int *s
     return ok != 0;
 }
 
-// The same two waits for short hops.  The polling thread (or all lanes of a warp together)
-// repeats try_wait without the sleep hint and looks at the abort flag and the clock only
-// every 64th time: a hop from an arrival to the waiting warp takes 88 cycles, against 600
-// where one lane polls with the hint and hands the result to the others.
-constexpr uint32_t kSpinsPerCheck = 64;
-// (Out of line: the code of a wait is at most a few instructions wherever one stands.)
+// The same two waits for short hops.  The first try_wait (all lanes of a warp together) has no
+// sleep hint: a hop from an arrival to the waiting warp takes 88 cycles, against 600 where one
+// lane polls with the hint and hands the result to the others.  Longer waits go on out of
+// line, with the hint, the abort flag and the clock, so that the code of a wait is a few
+// instructions wherever one stands.
 static __device__ __noinline__ bool thread_spin_on(uint64_t *bar, uint32_t parity, int *status, int code,
                                                    volatile int *abort) {
     const uint64_t t0 = globaltimer();
@@ -415,18 +414,6 @@ __device__ __forceinline__ void tmem_ld8(uint32_t taddr, uint32_t (&v)[8]) {
         "tcgen05.wait::ld.sync.aligned;"
         : "=r"(v[0]), "=r"(v[1]), "=r"(v[2]), "=r"(v[3]), "=r"(v[4]), "=r"(v[5]), "=r"(v[6]),
           "=r"(v[7])
-        : "r"(taddr)
-        : "memory");
-}
-// 16 consecutive fp32 columns of this warp's 32 TMEM lanes -> v[0..15] (load + wait).
-__device__ __forceinline__ void tmem_ld16(uint32_t taddr, uint32_t (&v)[16]) {
-    asm volatile(
-        "tcgen05.ld.sync.aligned.32x32b.x16.b32 "
-        "{%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15}, [%16];\n\t"
-        "tcgen05.wait::ld.sync.aligned;"
-        : "=r"(v[0]), "=r"(v[1]), "=r"(v[2]), "=r"(v[3]), "=r"(v[4]), "=r"(v[5]), "=r"(v[6]),
-          "=r"(v[7]), "=r"(v[8]), "=r"(v[9]), "=r"(v[10]), "=r"(v[11]), "=r"(v[12]),
-          "=r"(v[13]), "=r"(v[14]), "=r"(v[15])
         : "r"(taddr)
         : "memory");
 }

@@ -63,16 +63,6 @@ __device__ __forceinline__ void store32(void *p, const uint32_t (&w)[8]) {
                  : "memory");
 }
 
-// Eight bf16 of a 16-byte piece as floats.
-__device__ __forceinline__ void unpack8(const uint4 &v, float (&f)[8]) {
-    const uint32_t w[4] = {v.x, v.y, v.z, v.w};
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-        f[2 * i] = __uint_as_float(w[i] << 16);
-        f[2 * i + 1] = __uint_as_float(w[i] & 0xffff0000u);
-    }
-}
-
 // Zeroes rows [row0, 128) of a tile of DP / 64 column halves (each 128 rows of 128 bytes;
 // whole rows, so the swizzle does not matter), shared by `count` threads.
 template <int DP>

@@ -48,7 +48,8 @@ int check_attention(int b, int hq, int hk, int nq, int nk, int d, float scale, i
     if (nq > (1 << 29) || nk > (1 << 29) || (int64_t)b * hq > (1 << 29)) return LINFORMER_ERR_SIZE;
     if (dtype < LINFORMER_F32 || dtype > LINFORMER_BF16_F32OUT) return LINFORMER_ERR_ENUM;
     if (dtype != LINFORMER_BF16 || d > 128 || d % 8) return LINFORMER_ERR_UNSUPPORTED;
-    if (!std::isfinite(scale) || scale <= 0.f || window < 0 || (window && !causal) || causal < 0 ||
+    // (the scale is multiplied by log2(e) for the exponentials)
+    if (!std::isfinite(scale * 1.5f) || scale <= 0.f || window < 0 || (window && !causal) || causal < 0 ||
         causal > 1)
         return LINFORMER_ERR_VALUE;
     const void *words[] = {lse, q_lengths, k_lengths};
@@ -61,6 +62,10 @@ int check_attention(int b, int hq, int hk, int nq, int nk, int d, float scale, i
         const int st = check_strides(*v.to, b, v.heads, v.n, d, 8, v.output);
         if (st) return st;
     }
+    // an output that starts where another tensor does overlaps it
+    for (int i = 0; i < count; ++i)
+        for (int k = 0; views[i].output && k < count; ++k)
+            if (k != i && views[k].p == views[i].p) return LINFORMER_ERR_VALUE;
     return LINFORMER_OK;
 }
 
@@ -174,6 +179,7 @@ extern "C" int linformer_rotary(const void *X, const int64_t *X_strides, void *Y
                                (n > 1 && c.sx[w].n != c.sy[w].n)))
             return LINFORMER_ERR_VALUE;
     }
+    if (hx2 && (Y == Y2 || Y == X2 || Y2 == X)) return LINFORMER_ERR_VALUE;  // overlapping outputs
     c.phase = phase;
     c.positions = positions;
     c.start = start;

@@ -655,7 +655,7 @@ PFN_cuTensorMapEncodeTiled_v12000 g_encode = nullptr;
 std::once_flag g_encode_once;
 
 constexpr int kMaxDev = 64;
-int g_sms[kMaxDev] = {};
+std::atomic<int> g_sms[kMaxDev] = {};
 
 template <int DP>
 int launch(const Call &c, FwdParams &p) {
@@ -733,12 +733,12 @@ int device_sms() {
     int dev = 0;
     cudaGetDevice(&dev);
     if (dev < 0 || dev >= kMaxDev) return 148;
-    if (!g_sms[dev]) {
-        int v = 0;
+    int v = g_sms[dev].load(std::memory_order_relaxed);
+    if (!v) {
         cudaDeviceGetAttribute(&v, cudaDevAttrMultiProcessorCount, dev);
-        g_sms[dev] = v > 0 ? v : 148;
+        g_sms[dev].store(v = v > 0 ? v : 148, std::memory_order_relaxed);
     }
-    return g_sms[dev];
+    return v;
 }
 
 // The kernel's shared memory, allowed once per device (slot: one per kernel).

@@ -331,7 +331,7 @@ def _strides(x):
     key = x.stride()
     arr = _stride_table.get(key)
     if arr is None:
-        if key[3] != 1 and x.shape[3] != 1:
+        if key[3] != 1:
             raise ValueError("the last dimension has to be contiguous")
         if len(_stride_table) >= 4096:
             _stride_table.clear()
@@ -362,6 +362,13 @@ def _call(fn, device, args, name):
             st = fn(*args)
     if st != 0:
         raise LinformerError(st, name)
+
+
+def _int32(name, x):
+    """Refuses what would not survive the passage to a C int."""
+    if not -0x80000000 <= x <= 0x7fffffff:
+        raise ValueError(f"{name} = {x} is outside the 32-bit range")
+    return x
 
 
 def _check(name, x, shape, dtype):
@@ -408,7 +415,8 @@ def softmax_attention(Q, K, V, q_lengths=None, k_lengths=None, causal: bool = Fa
     _call(lib().linformer_softmax_attn_fwd, device,
           (Q.data_ptr(), _strides(Q), K.data_ptr(), _strides(K), V.data_ptr(), _strides(V),
            out.data_ptr(), _strides(out), lse.data_ptr(), q_lengths, k_lengths, b, hq, hk, n, m, d,
-           d ** -0.5 if scale is None else scale, 1 if causal else 0, window, dtype_code(Q), handle),
+           d ** -0.5 if scale is None else scale, 1 if causal else 0,
+           _int32("window", window), dtype_code(Q), handle),
           "linformer_softmax_attn_fwd")
     return out, lse
 
@@ -451,7 +459,7 @@ def softmax_attention_backward(Q, K, V, O, dO, lse, q_lengths=None, k_lengths=No
            O.data_ptr(), _strides(O), dO.data_ptr(), _strides(dO), lse.data_ptr(), dQ.data_ptr(),
            _strides(dQ), dK.data_ptr(), _strides(dK), dV.data_ptr(), _strides(dV), q_lengths,
            k_lengths, b, hq, hk, n, m, d, d ** -0.5 if scale is None else scale, 1 if causal else 0,
-           window, dtype_code(Q), handle),
+           _int32("window", window), dtype_code(Q), handle),
           "linformer_softmax_attn_bwd")
     return dQ, dK, dV
 
@@ -504,7 +512,7 @@ def rotary(x, x2=None, phase=None, positions=None, start: int = 0, rot=None,
         px2, sx2, py2, sy2 = x2.data_ptr(), _strides(x2), out2.data_ptr(), _strides(out2)
     _call(lib().linformer_rotary, device,
           (x.data_ptr(), _strides(x), out.data_ptr(), _strides(out), h, px2, sx2, py2, sy2, h2,
-           phase.data_ptr(), positions, start, b, n, d, rot, layout, amplitude, 1 if inverse else 0,
-           dtype_code(x), handle),
+           phase.data_ptr(), positions, _int32("start", start), b, n, d, rot, layout, amplitude,
+           1 if inverse else 0, dtype_code(x), handle),
           "linformer_rotary")
     return out if x2 is None else (out, out2)

@@ -115,6 +115,47 @@ def test_phase_refusals(L, kw, expected):
                                     a["original"], a["fast"], a["slow"], 0) == expected
 
 
+@pytest.mark.parametrize("kw", [dict(O=A), dict(O=A + 16), dict(O=A + 32), dict(scale=3e38)])
+def test_forward_refuses_an_output_over_an_input(L, kw):
+    a = forward_args(K=A + 16, V=A + 32, **kw)
+    if "O" not in kw:
+        a["O"] = A + 48
+    st = L.linformer_softmax_attn_fwd(*(a[k] for k in (
+        "Q", "sQ", "K", "sK", "V", "sV", "O", "sO", "lse", "ql", "kl", "b", "hq", "hk", "nq", "nk",
+        "d", "scale", "causal", "window", "dtype")), 0)
+    assert st == -10, lf.status_string(st)
+
+
+@pytest.mark.parametrize("same", [("dQ", "Q"), ("dK", "K"), ("dV", "V"), ("dQ", "dO"), ("dK", "dV"),
+                                  ("dV", "O")])
+def test_backward_refuses_an_output_over_another_tensor(L, same):
+    t = {k: A + 16 * i for i, k in enumerate(("Q", "K", "V", "O", "dO", "dQ", "dK", "dV"))}
+    t[same[0]] = t[same[1]]
+    st = L.linformer_softmax_attn_bwd(
+        t["Q"], None, t["K"], None, t["V"], None, t["O"], None, t["dO"], None, A, t["dQ"], None,
+        t["dK"], None, t["dV"], None, None, None, 2, 4, 2, 64, 64, 64, 0.125, 1, 0, 1, 0)
+    assert st == -10, lf.status_string(st)
+
+
+@pytest.mark.parametrize("y,x2,y2", [(A + 16, A + 32, A + 16), (A + 16, A + 16, A + 32),
+                                     (A + 16, A + 32, A)])
+def test_rotary_refuses_an_output_over_the_other_tensor(L, y, x2, y2):
+    st = L.linformer_rotary(A, None, y, None, 4, x2, None, y2, None, 4, A, None, 0, 2, 16, 64, 64, 0,
+                            1.0, 0, 1, 0)
+    assert st == -10, lf.status_string(st)
+
+
+def test_binding_refuses_rows_with_gaps_and_wide_integers():
+    gaps = torch.zeros(2, 2, 3, 16)[..., ::2]
+    for x in (gaps[..., :1], gaps):  # the same strides, the last dimension of size one first
+        with pytest.raises(ValueError, match="contiguous"):
+            lf._strides(x)
+    assert lf._int32("start", -2 ** 31) == -2 ** 31
+    for x in (2 ** 31, -2 ** 31 - 1, 2 ** 32):
+        with pytest.raises(ValueError, match="32-bit"):
+            lf._int32("start", x)
+
+
 def test_binding_refuses_host_tensors_and_wrong_shapes():
     q = torch.zeros(1, 2, 4, 64, dtype=torch.bfloat16)
     with pytest.raises(ValueError):
