@@ -63,14 +63,14 @@ __device__ __forceinline__ void store32(void *p, const uint32_t (&w)[8]) {
                  : "memory");
 }
 
-// Zeroes rows [row0, 128) of a tile of DP / 64 column halves (each 128 rows of 128 bytes;
+// Zeroes rows [row0, kRows) of a tile of DP / 64 column halves (each kRows rows of 128 bytes;
 // whole rows, so the swizzle does not matter), shared by `count` threads.
-template <int DP>
+template <int DP, int kRows>
 __device__ __forceinline__ void zero_rows(uint8_t *tile, int row0, int idx, int count) {
 #pragma unroll
     for (int h = 0; h < DP / 64; ++h) {
-        uint4 *p = reinterpret_cast<uint4 *>(tile + h * 16384 + row0 * 128);
-        for (int i = idx; i < (kTile - row0) * 8; i += count) p[i] = make_uint4(0u, 0u, 0u, 0u);
+        uint4 *p = reinterpret_cast<uint4 *>(tile + h * kRows * 128 + row0 * 128);
+        for (int i = idx; i < (kRows - row0) * 8; i += count) p[i] = make_uint4(0u, 0u, 0u, 0u);
     }
 }
 

@@ -34,12 +34,15 @@ namespace {
 
 using namespace ptx;
 
-// Twelve warps (one idle), 168 registers each at launch; the two warpgroups that do the
-// arithmetic take registers from the third: 2 x 208 + 88 = 3 x 168.
-constexpr int kThreads = 384;
-constexpr uint32_t kMathRegs = 208, kIssueRegs = 88;
-static_assert(2 * kMathRegs + kIssueRegs == 3 * 168, "register split");
-constexpr int kMathWarps = 8, kHalfWarps = 4, kLoadWarp = 8, kMmaWarp = 9;
+constexpr int kHalf = 64;  // columns of a step: queries (dK, dV) or keys (dQ)
+// G warpgroups do the arithmetic and a last one loads and issues; it hands registers to the
+// others, whose shares add up to the launch's.
+constexpr int threads_of(int G) { return 128 * (G + 1); }
+__host__ __device__ constexpr uint32_t math_regs(int G) { return G == 3 ? 144 : 208; }
+__host__ __device__ constexpr uint32_t issue_regs(int G) { return G == 3 ? 80 : 88; }
+constexpr uint32_t launch_regs(int G) { return 65536 / threads_of(G) / 8 * 8; }
+static_assert(3 * math_regs(3) + issue_regs(3) == 4 * launch_regs(3), "register split");
+static_assert(2 * math_regs(2) + issue_regs(2) == 3 * launch_regs(2), "register split");
 constexpr float kLog2e = 1.4426950408889634f;
 
 struct BwdParams {
@@ -49,7 +52,7 @@ struct BwdParams {
     __nv_bfloat16 *dQ, *dK, *dV;
     Strides sdQ, sdK, sdV;
     const float *lse;
-    // [b][hq][query tiles][2][128]: -lse log2(e) and -delta, as they are added; -inf and 0 for
+    // [b][hq][2 query tiles][2][64]: -lse log2(e) and -delta, as they are added; -inf and 0 for
     // rows that are past the length or see no key
     float *rows;
     int b, hq, hk, group, nq, nk, d, causal, window;
@@ -60,20 +63,20 @@ struct BwdParams {
     int *status;
 };
 
-// Columns outside [a, a + w) of 64 in tensor memory become `value`: for the few blocks at a
+// Columns outside [a, a + w) of 64 in tensor memory become -inf: for the few steps at a
 // mask's edge, out of line, away from the code of the others.
-__device__ __noinline__ void fill_outside(uint32_t t, int a, unsigned w, uint32_t value) {
+constexpr uint32_t kMinusInf = 0xff800000u;
+__device__ __noinline__ void hide_outside(uint32_t t, int a, unsigned w) {
 #pragma unroll 1
     for (int c = 0; c < 64; c += 32) {
         uint32_t u[32];
         tmem_ld32(t + c, u);
 #pragma unroll
         for (int e = 0; e < 32; ++e)
-            if ((unsigned)(c + e - a) >= w) u[e] = value;
+            if ((unsigned)(c + e - a) >= w) u[e] = kMinusInf;
         tmem_st32(t + c, u);
     }
 }
-constexpr uint32_t kMinusInf = 0xff800000u;
 __device__ __forceinline__ float4 lds4(uint32_t addr) {
     float4 v;
     asm volatile("ld.shared.v4.f32 {%0, %1, %2, %3}, [%4];"
@@ -106,12 +109,12 @@ __device__ __forceinline__ void store_row(__nv_bfloat16 *dst, const uint32_t (&o
         }
     }
 }
-// 32 N columns of an accumulator, one wait for all.
 // The first d columns of a row as zero.
 __device__ __forceinline__ void zero_row(__nv_bfloat16 *dst, int d) {
 #pragma unroll 1
     for (int c = 0; c < d; c += 8) *reinterpret_cast<uint4 *>(dst + c) = make_uint4(0u, 0u, 0u, 0u);
 }
+// 32 N columns of tensor memory, one wait for all.
 template <int N>
 __device__ __forceinline__ void load_columns(uint32_t t, uint32_t (&o)[N][32]) {
 #pragma unroll
@@ -121,33 +124,104 @@ __device__ __forceinline__ void load_columns(uint32_t t, uint32_t (&o)[N][32]) {
     for (int c = 1; c < N; ++c) tie32(o[c]);
 }
 
+// D (128 x 64) = A (128 rows of DP) . B (64 rows of DP)^T, both in shared memory.
 template <int DP>
 __device__ __forceinline__ void mma_scores(uint32_t d, uint32_t a, uint32_t b) {
-    const uint32_t idesc = idesc_f16(128, 128, 1, 0, 0);
+    const uint32_t idesc = idesc_f16(128, kHalf, 1, 0, 0);
     const uint64_t da = sdesc(a, 16, 1024, kSwizzle128B), db = sdesc(b, 16, 1024, kSwizzle128B);
 #pragma unroll
-    for (int x = 0; x < DP / 16; ++x) {
-        const uint64_t off = (uint64_t)((x >> 2) * 1024 + (x & 3) * 2);
-        mma_ss(d, da + off, db + off, idesc, x > 0 ? 1u : 0u);
-    }
+    for (int x = 0; x < DP / 16; ++x)
+        mma_ss(d, da + (uint64_t)((x >> 2) * 1024 + (x & 3) * 2), db + (uint64_t)((x >> 2) * 512 + (x & 3) * 2),
+               idesc, x > 0 ? 1u : 0u);
 }
-// D (128 x DP) += A (128 x 64, packed in 32 columns of tensor memory) . B (64 rows of DP): half
-// of a step's sum, issued as soon as that half of P or dS is there.
+// D (128 x DP) += A (128 x 64, packed in 32 columns of tensor memory) . B (64 rows of DP).
 template <int DP>
-__device__ __forceinline__ void mma_sum_half(uint32_t d, uint32_t a, uint32_t b, uint32_t acc) {
+__device__ __forceinline__ void mma_sum(uint32_t d, uint32_t a, uint32_t b, uint32_t acc) {
     const uint32_t idesc = idesc_f16(128, DP, 1, 0, 1);
-    const uint64_t db = sdesc(b, 16384, 1024, kSwizzle128B);
+    const uint64_t db = sdesc(b, 8192, 1024, kSwizzle128B);
 #pragma unroll
-    for (int x = 0; x < 4; ++x)
+    for (int x = 0; x < kHalf / 16; ++x)
         mma_ts(d, a + 8 * x, db + (uint64_t)(128 * x), idesc, (acc || x > 0) ? 1u : 0u);
 }
 
-template <int DP>
+// 64 N rows of DP columns, each 64 columns a tile of its own (maps have boxes of 64 x 64).
+template <int DP, int N>
 __device__ __forceinline__ void load_rows(uint8_t *dst, const CUtensorMap *m, uint64_t *bar, int row,
                                           int head, int group, int batch) {
 #pragma unroll
-    for (int h = 0; h < DP / 64; ++h) tma_load_5d(dst + h * 16384, m, bar, h * 64, row, head, group, batch);
+    for (int c = 0; c < DP / 64; ++c)
+#pragma unroll
+        for (int r = 0; r < N; ++r)
+            tma_load_5d(dst + (c * N + r) * 8192, m, bar, c * 64, row + 64 * r, head, group, batch);
 }
+
+// Waits by shared-memory address (the issuing threads' few instructions between a barrier and
+// a product are what the tensor cores wait for).
+__device__ __forceinline__ bool try_at(uint32_t bar, uint32_t parity) {
+    uint32_t ok;
+    asm volatile(
+        "{\n\t.reg .pred p;\n\tmbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2;\n\t"
+        "selp.u32 %0, 1, 0, p;\n\t}"
+        : "=r"(ok)
+        : "r"(bar), "r"(parity)
+        : "memory");
+    return ok != 0;
+}
+static __device__ __noinline__ bool spin_on(uint32_t bar, uint32_t parity, int *status, int code,
+                                            volatile int *abort) {
+    const uint64_t t0 = globaltimer();
+    while (!try_at(bar, parity)) {
+        if (*abort) return false;
+        if (globaltimer() - t0 > kWaitLimitNs) {
+            *abort = 1;
+            if (status) atomicExch(status, code);
+            return false;
+        }
+    }
+    return true;
+}
+__device__ __forceinline__ bool spin_at(uint32_t bar, uint32_t parity, int *status, int code,
+                                        volatile int *abort) {
+    return try_at(bar, parity) || spin_on(bar, parity, status, code, abort);
+}
+static __device__ __noinline__ bool warp_spin_on_at(uint32_t bar, uint32_t parity, int *status, int code,
+                                                    volatile int *abort) {
+    const uint64_t t0 = globaltimer();
+    while (!__any_sync(0xffffffffu, try_at(bar, parity))) {
+        if (__any_sync(0xffffffffu, *abort != 0)) return false;
+        if (__any_sync(0xffffffffu, globaltimer() - t0 > kWaitLimitNs)) {
+            *abort = 1;
+            if (status) atomicExch(status, code);
+            return false;
+        }
+    }
+    return true;
+}
+__device__ __forceinline__ bool warp_spin_at(uint32_t bar, uint32_t parity, int *status, int code,
+                                             volatile int *abort) {
+    return __any_sync(0xffffffffu, try_at(bar, parity)) || warp_spin_on_at(bar, parity, status, code, abort);
+}
+__device__ __forceinline__ void arrive_at(uint32_t bar) {
+    asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];" ::"r"(bar) : "memory");
+}
+__device__ __forceinline__ void commit_at(uint32_t bar) {
+    asm volatile("tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(bar) : "memory");
+}
+// Where a step stands in a ring of N = some times G positions: the position (its stage and its
+// barriers of every kind), the ring's phase, and the slot.
+template <int G, int N>
+struct Ring {
+    uint32_t pos = 0, phase = 0, slot = 0;
+    // the step G before: the slot's last user (its phase; the first G steps find a fresh
+    // barrier, whose phase -1 counts as over)
+    __device__ __forceinline__ uint32_t before() const { return pos >= G ? pos - G : pos + N - G; }
+    __device__ __forceinline__ uint32_t phase_before() const { return pos >= G ? phase : phase ^ 1u; }
+    __device__ __forceinline__ void next() {
+        ++pos;
+        slot = slot == G - 1 ? 0 : slot + 1;
+        if (pos == N) pos = 0, phase ^= 1u;
+    }
+};
 
 // ---------------------------------------------------------------- row values
 // -lse log2(e) and -delta = -dO.O of a query tile's 128 rows, eight warps of sixteen rows; a row
@@ -179,7 +253,7 @@ __global__ void __launch_bounds__(kRowsThreads) rows_kernel(const BwdParams p) {
             x[t] = __ldg(p.lse + (int64_t)unit * p.nq + i);
         }
     }
-    float *dst = p.rows + (int64_t)blockIdx.x * 256 + 16 * warp + lane / kLanes;
+    float *dst = p.rows + (int64_t)blockIdx.x * 256 + (warp >> 2) * 128 + 16 * (warp & 3) + lane / kLanes;
 #pragma unroll
     for (int t = 0; t < kTurns; ++t) {
         float y = (dot2(a[t].x, b[t].x) + dot2(a[t].y, b[t].y)) + (dot2(a[t].z, b[t].z) + dot2(a[t].w, b[t].w));
@@ -187,7 +261,7 @@ __global__ void __launch_bounds__(kRowsThreads) rows_kernel(const BwdParams p) {
         for (int k = kLanes / 2; k; k >>= 1) y += __shfl_xor_sync(0xffffffffu, y, k);
         if (lane % kLanes == 0) {
             dst[t * kAtOnce] = x[t] == -INFINITY ? -INFINITY : -x[t] * kLog2e;
-            dst[t * kAtOnce + 128] = x[t] == -INFINITY ? 0.f : -y;
+            dst[t * kAtOnce + 64] = x[t] == -INFINITY ? 0.f : -y;
         }
     }
 }
@@ -195,13 +269,15 @@ __global__ void __launch_bounds__(kRowsThreads) rows_kernel(const BwdParams p) {
 // ---------------------------------------------------------------- dQ
 template <int DP>
 struct DqLayout {
-    static constexpr uint32_t kTileBytes = kTile * DP * 2;
-    static constexpr int kStages = DP == 64 ? 8 : 5;
-    static constexpr uint32_t kS = 0, kDp = 128, kDq = 384;
-    static constexpr uint32_t kSmem = 1024 + (2 + kStages) * kTileBytes + 512 + 1024;
+    // slots, one of each warpgroup: S in 64 columns, dP in 64
+    static constexpr int G = DP == 64 ? 3 : 2;
+    static constexpr uint32_t kTileBytes = kTile * DP * 2, kStepBytes = kHalf * DP * 2;
+    static constexpr int kStages = DP == 64 ? 12 : 4;  // of a step's K and V
+    static constexpr uint32_t kDq = 128 * G;
+    static constexpr uint32_t kSmem = 1024 + 2 * kTileBytes + kStages * 2 * kStepBytes + 1024 + 1024;
 };
 struct DqItem {
-    int batch, head, q0, lo, hi;
+    int batch, head, q0, lo, hi;  // steps [lo, hi) of 64 keys
     Span sp;
 };
 __device__ __forceinline__ DqItem dq_item(const BwdParams &p, int idx) {
@@ -219,60 +295,56 @@ __device__ __forceinline__ DqItem dq_item(const BwdParams &p, int idx) {
     if (last >= it.q0) {
         const int e = it.sp.end(last), f = it.sp.first(it.q0);
         if (e > f) {
-            it.lo = f / kTile;
-            it.hi = (e + kTile - 1) / kTile;
+            it.lo = f / kHalf;
+            it.hi = (e + kHalf - 1) / kHalf;
         }
     }
     return it;
 }
 
+// Barriers of steps: one of each kind for every position of the ring.
 struct DqBarriers {
-    // (pairs: even and odd blocks)
-    uint64_t q_full, q_free, s_full[2], s_free, dp_full[2], ds_full[2][2], dq_done[2];
-    uint64_t acc_full, acc_free;
-    uint64_t fix_wanted, fixed, drain[2];
-    uint64_t full[8], empty[8];
+    uint64_t k_full[12], v_full[12], s_full[12], s_free[12], dp_full[12], ds_full[12], dq_done[12];
+    uint64_t q_full, q_free, acc_full, acc_free, fix_wanted, fixed_k, fixed_v, drain[3];
     uint32_t tmem;
     int abort;
     alignas(16) float rows[2 * kTile];  // the item's rows, loaded with Q and dO
 };
 
-static_assert(sizeof(DqBarriers) <= 512 + 1024, "room for the barriers");
+static_assert(sizeof(DqBarriers) <= 2048, "room for the barriers");
 
 template <int DP>
-__global__ void __launch_bounds__(kThreads, 1)
+__global__ void __launch_bounds__(threads_of(DqLayout<DP>::G), 1)
 softmax_attn_dq_kernel(const __grid_constant__ CUtensorMap tQ, const __grid_constant__ CUtensorMap tK,
                        const __grid_constant__ CUtensorMap tV, const __grid_constant__ CUtensorMap tdO,
                        const BwdParams p) {
     using C = DqLayout<DP>;
+    constexpr int G = C::G, kLoadWarp = 4 * G, kMmaWarp = 4 * G + 1;
     extern __shared__ uint8_t raw[];
     uint8_t *smem = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(raw) + 1023) & ~uintptr_t(1023));
     uint8_t *sQ = smem, *sdO = smem + C::kTileBytes, *sKV = smem + 2 * C::kTileBytes;
-    DqBarriers *bar = reinterpret_cast<DqBarriers *>(sKV + C::kStages * C::kTileBytes);
+    DqBarriers *bar = reinterpret_cast<DqBarriers *>(sKV + C::kStages * 2 * C::kStepBytes);
     volatile int *abort_flag = &bar->abort;
     const int tid = threadIdx.x, warp = __shfl_sync(0xffffffffu, tid >> 5, 0), lane = tid & 31;
 
     if (tid == 0) {
         mbar_init(&bar->q_full, 1);
-        mbar_init(&bar->q_free, 1 + kMathWarps);  // the products, and the rows read
-        mbar_init(&bar->s_free, kMathWarps);
-        for (int i = 0; i < 2; ++i) {
+        mbar_init(&bar->q_free, 2 + 4 * G);  // the products, and the rows read
+        for (int i = 0; i < C::kStages; ++i) {
+            mbar_init(&bar->k_full[i], 1);
+            mbar_init(&bar->v_full[i], 1);
             mbar_init(&bar->s_full[i], 1);
+            mbar_init(&bar->s_free[i], 4);
             mbar_init(&bar->dp_full[i], 1);
-            mbar_init(&bar->ds_full[i][0], kHalfWarps);  // halves of 64 columns
-            mbar_init(&bar->ds_full[i][1], kHalfWarps);
+            mbar_init(&bar->ds_full[i], 4);
             mbar_init(&bar->dq_done[i], 1);
         }
         mbar_init(&bar->acc_full, 1);
-        mbar_init(&bar->acc_free, kMathWarps);
-        mbar_init(&bar->fix_wanted, 1);
-        mbar_init(&bar->fixed, 31);
-        mbar_init(&bar->drain[0], 1);
-        mbar_init(&bar->drain[1], 1);
-        for (int s = 0; s < C::kStages; ++s) {
-            mbar_init(&bar->full[s], 1);
-            mbar_init(&bar->empty[s], 1);
-        }
+        mbar_init(&bar->acc_free, 8);
+        mbar_init(&bar->fix_wanted, 2);
+        mbar_init(&bar->fixed_k, 31);
+        mbar_init(&bar->fixed_v, 31);
+        for (int i = 0; i < 3; ++i) mbar_init(&bar->drain[i], 1);
         bar->abort = 0;
         fence_mbar_init();
     }
@@ -284,14 +356,14 @@ softmax_attn_dq_kernel(const __grid_constant__ CUtensorMap tQ, const __grid_cons
     __syncthreads();
     tc_fence_after();
     const uint32_t tmem = bar->tmem;
-    // ring entry 2 j + kv of an item: K (kv = 0) and V of its j-th block
     if (warp >= kLoadWarp) {
-    setmaxnreg_dec<kIssueRegs>();
+    setmaxnreg_dec<issue_regs(G)>();
     if (warp == kLoadWarp) {
         if (lane == 0) {
             wait_prerequisites();  // the row values; and only then may the third kernel start
             launch_dependents();
-            int ring = 0, nq = 0;
+            int steps = 0, nq = 0;
+            Ring<G, C::kStages> at;
             bool ok = true;
             for (int idx = blockIdx.x; idx < p.items && ok; idx += gridDim.x) {
                 const DqItem it = dq_item(p, idx);
@@ -301,128 +373,126 @@ softmax_attn_dq_kernel(const __grid_constant__ CUtensorMap tQ, const __grid_cons
                 const int g = it.head % p.group, kvh = it.head / p.group;
                 bulk_load(bar->rows, p.rows + (((int64_t)it.batch * p.hq + it.head) * p.qtiles + it.q0 / kTile) * 256,
                           1024, &bar->q_full);
-                load_rows<DP>(sQ, &tQ, &bar->q_full, it.q0, g, kvh, it.batch);
-                load_rows<DP>(sdO, &tdO, &bar->q_full, it.q0, g, kvh, it.batch);
+                load_rows<DP, 2>(sQ, &tQ, &bar->q_full, it.q0, g, kvh, it.batch);
+                load_rows<DP, 2>(sdO, &tdO, &bar->q_full, it.q0, g, kvh, it.batch);
                 ++nq;
-                for (int j = it.lo; j < it.hi && ok; ++j)
-                    for (int kv = 0; kv < 2; ++kv, ++ring) {
-                        const int s = ring % C::kStages;
-                        if (ring >= C::kStages &&
-                            !thread_spin(&bar->empty[s], (ring / C::kStages - 1) & 1, p.status, 84, abort_flag)) {
-                            ok = false;
-                            break;
-                        }
-                        mbar_arrive_expect_tx(&bar->full[s], C::kTileBytes);
-                        load_rows<DP>(sKV + s * C::kTileBytes, kv ? &tV : &tK, &bar->full[s], j * kTile, 0,
-                                      kvh, it.batch);
-                    }
+                for (int j = it.lo; j < it.hi; ++j, ++steps, at.next()) {
+                    uint8_t *st = sKV + at.pos * 2 * C::kStepBytes;
+                    // (dQ comes last: with it all products of a step have been formed)
+                    ok = thread_spin(&bar->dq_done[at.pos], at.phase ^ 1, p.status, 84, abort_flag);
+                    if (!ok) break;
+                    mbar_arrive_expect_tx(&bar->k_full[at.pos], C::kStepBytes);
+                    load_rows<DP, 1>(st, &tK, &bar->k_full[at.pos], j * kHalf, 0, kvh, it.batch);
+                    mbar_arrive_expect_tx(&bar->v_full[at.pos], C::kStepBytes);
+                    load_rows<DP, 1>(st + C::kStepBytes, &tV, &bar->v_full[at.pos], j * kHalf, 0, kvh, it.batch);
+                }
             }
             if (nq > 0) mbar_wait_drain(&bar->q_full, (nq - 1) & 1);
-            for (int i = max(0, ring - C::kStages); i < ring; ++i)
-                mbar_wait_drain(&bar->full[i % C::kStages], (i / C::kStages) & 1);
-        } else {  // K rows past the valid length: dS is 0 there, but 0 x NaN is not
+            for (int i = max(0, steps - C::kStages); i < steps; ++i) {
+                mbar_wait_drain(&bar->k_full[i % C::kStages], (i / C::kStages) & 1);
+                mbar_wait_drain(&bar->v_full[i % C::kStages], (i / C::kStages) & 1);
+            }
+        } else {  // K and V rows past the valid length: P and dS are 0 there, but 0 x NaN is not
             int ring = 0, nfix = 0;
             for (int idx = blockIdx.x; idx < p.items; idx += gridDim.x) {
                 const DqItem it = dq_item(p, idx);
                 if (it.hi <= it.lo) continue;
-                ring += 2 * (it.hi - it.lo);
-                if (it.sp.Lk >= p.nk || it.hi * kTile <= it.sp.Lk) continue;
+                ring += it.hi - it.lo;
+                if (it.sp.Lk >= p.nk || it.hi * kHalf <= it.sp.Lk) continue;
                 if (!thread_spin(&bar->fix_wanted, nfix & 1, p.status, 85, abort_flag)) break;
                 ++nfix;
-                zero_rows<DP>(sKV + (ring - 2) % C::kStages * C::kTileBytes,
-                              it.sp.Lk - (it.hi - 1) * kTile, lane - 1, 31);
+                const int row0 = it.sp.Lk - (it.hi - 1) * kHalf;
+                uint8_t *st = sKV + (ring - 1) % C::kStages * 2 * C::kStepBytes;
+                zero_rows<DP, kHalf>(st, row0, lane - 1, 31);
+                zero_rows<DP, kHalf>(st + C::kStepBytes, row0, lane - 1, 31);
                 fence_proxy_async_smem();
-                mbar_arrive(&bar->fixed);
+                mbar_arrive(&bar->fixed_k);
+                mbar_arrive(&bar->fixed_v);
             }
         }
         __syncwarp();
-    } else if (warp == kMmaWarp) {
-        if (elect_one()) {  // S and dP
-            int ring = 0, items = 0, n = 0, nfix = 0;
+    } else if (warp <= kMmaWarp + 1) {
+        const bool first = warp == kMmaWarp;  // S = Q K^T; the other thread: dP = dO V^T
+        if (elect_one()) {
+            int items = 0;
+            uint32_t nfix = 0;
+            Ring<G, C::kStages> at;
             bool ok = true;
-            const uint32_t aQ = smem_u32(sQ), adO = smem_u32(sdO), aKV = smem_u32(sKV);
+            const uint32_t a = smem_u32(first ? sQ : sdO), b = smem_u32(sKV) + (first ? 0 : C::kStepBytes),
+                           slots = tmem + (first ? 0 : 64), loaded = smem_u32(first ? bar->k_full : bar->v_full),
+                           free = smem_u32(first ? bar->s_free : bar->dq_done),
+                           out = smem_u32(first ? bar->s_full : bar->dp_full),
+                           fixed = smem_u32(first ? &bar->fixed_k : &bar->fixed_v);
             for (int idx = blockIdx.x; idx < p.items && ok; idx += gridDim.x) {
                 const DqItem it = dq_item(p, idx);
-                const int blocks = it.hi - it.lo;
-                if (blocks <= 0) continue;
-                const bool fix = it.sp.Lk < p.nk && it.hi * kTile > it.sp.Lk;
+                const int steps = it.hi - it.lo;
+                if (steps <= 0) continue;
+                const bool fix = it.sp.Lk < p.nk && it.hi * kHalf > it.sp.Lk;
                 ok = thread_spin(&bar->q_full, items & 1, p.status, 91, abort_flag);
-                for (int j = 0; j < blocks && ok; ++j, ++n, ring += 2) {
-                    int s = ring % C::kStages;
-                    ok = thread_spin(&bar->full[s], (ring / C::kStages) & 1, p.status, 86, abort_flag);
-                    if (ok && fix && j == blocks - 1) {
+                for (int j = steps; j > 0 && ok; --j, at.next()) {
+                    ok = spin_at(loaded + 8 * at.pos, at.phase, p.status, 86, abort_flag) &&
+                         spin_at(free + 8 * at.before(), at.phase_before(), p.status, 88, abort_flag);
+                    if (ok && fix && j == 1) {
                         mbar_arrive(&bar->fix_wanted);
-                        ok = thread_spin(&bar->fixed, nfix++ & 1, p.status, 87, abort_flag);
+                        ok = spin_at(fixed, nfix++ & 1, p.status, 87, abort_flag);
                     }
-                    ok = ok && (n == 0 || thread_spin(&bar->s_free, (n - 1) & 1, p.status, 88, abort_flag));
                     if (!ok) break;
                     tc_fence_after();
-                    mma_scores<DP>(tmem + C::kS, aQ, aKV + s * C::kTileBytes);
-                    mma_commit(&bar->s_full[n & 1]);
-                    s = (ring + 1) % C::kStages;
-                    ok = thread_spin(&bar->full[s], ((ring + 1) / C::kStages) & 1, p.status, 89, abort_flag) &&
-                         (n < 2 || thread_spin(&bar->dq_done[n & 1], ((n >> 1) - 1) & 1, p.status, 90, abort_flag));
-                    if (!ok) break;
-                    tc_fence_after();
-                    mma_scores<DP>(tmem + C::kDp + 128 * (n & 1), adO, aKV + s * C::kTileBytes);
-                    mma_commit(&bar->dp_full[n & 1]);
-                    mma_commit(&bar->empty[s]);
+                    mma_scores<DP>(slots + 128 * at.slot, a, b + at.pos * (2 * C::kStepBytes));
+                    commit_at(out + 8 * at.pos);
                 }
                 mma_commit(&bar->q_free);
                 ++items;
             }
-            mma_commit(&bar->drain[0]);
-            mbar_wait_drain(&bar->drain[0], 0);
+            mma_commit(&bar->drain[first ? 0 : 1]);
+            mbar_wait_drain(&bar->drain[first ? 0 : 1], 0);
         }
         __syncwarp();
-    } else if (warp == kMmaWarp + 1) {
-        if (elect_one()) {  // dQ
-            int ring = 0, items = 0, n = 0;
+    } else {
+        if (elect_one()) {  // dQ += dS K
+            int items = 0;
+            Ring<G, C::kStages> at;
             bool ok = true;
-            const uint32_t aKV = smem_u32(sKV);
+            const uint32_t b = smem_u32(sKV), ready = smem_u32(bar->ds_full), done = smem_u32(bar->dq_done);
             for (int idx = blockIdx.x; idx < p.items && ok; idx += gridDim.x) {
                 const DqItem it = dq_item(p, idx);
-                const int blocks = it.hi - it.lo;
-                if (blocks <= 0) continue;
-                for (int j = 0; j < blocks && ok; ++j, ++n, ring += 2) {
+                const int steps = it.hi - it.lo;
+                if (steps <= 0) continue;
+                if (items > 0) ok = thread_spin(&bar->acc_free, (items - 1) & 1, p.status, 93, abort_flag);
+                for (int j = 0; j < steps && ok; ++j, at.next()) {
                     // (dS says that S has been formed, so the block of K has landed)
-                    const int s = ring % C::kStages;
-                    const uint32_t ds = tmem + C::kDp + 128 * (n & 1), k = aKV + s * C::kTileBytes;
-                    ok = thread_spin(&bar->ds_full[n & 1][0], (n >> 1) & 1, p.status, 92, abort_flag) &&
-                         (j > 0 || items == 0 ||
-                          thread_spin(&bar->acc_free, (items - 1) & 1, p.status, 93, abort_flag));
+                    ok = spin_at(ready + 8 * at.pos, at.phase, p.status, 92, abort_flag);
                     if (!ok) break;
                     tc_fence_after();
-                    mma_sum_half<DP>(tmem + C::kDq, ds, k, j > 0 ? 1u : 0u);
-                    ok = thread_spin(&bar->ds_full[n & 1][1], (n >> 1) & 1, p.status, 92, abort_flag);
-                    if (!ok) break;
-                    tc_fence_after();
-                    mma_sum_half<DP>(tmem + C::kDq, ds + 64, k + 8192, 1u);
-                    mma_commit(&bar->dq_done[n & 1]);
-                    mma_commit(&bar->empty[s]);
+                    mma_sum<DP>(tmem + C::kDq, tmem + 128 * at.slot + 64, b + at.pos * (2 * C::kStepBytes), j > 0 ? 1u : 0u);
+                    commit_at(done + 8 * at.pos);
                 }
                 mma_commit(&bar->acc_full);
                 ++items;
             }
-            mma_commit(&bar->drain[1]);
-            mbar_wait_drain(&bar->drain[1], 0);
+            mma_commit(&bar->drain[2]);
+            mbar_wait_drain(&bar->drain[2], 0);
         }
         __syncwarp();
     }
     } else {
-        setmaxnreg_inc<kMathRegs>();
-        const int half = warp >> 2, row = tid & 127;
+        setmaxnreg_inc<math_regs(G)>();
+        const int w = warp >> 2, row = tid & 127;
         const uint32_t lanes = (uint32_t)((warp & 3) * 32) << 16;
-        const float sl = p.scale_log2;
+        const uint32_t tS = tmem + 128 * w + lanes, tD = tS + 64;
+        const float2 sl2 = make_float2(p.scale_log2, p.scale_log2);
+        const uint32_t s_full = smem_u32(bar->s_full), s_free = smem_u32(bar->s_free), dp_full = smem_u32(bar->dp_full),
+                       ds_full = smem_u32(bar->ds_full);
         int n = 0, items = 0;
+        uint32_t pos = w, phase = 0;  // in the ring; the warpgroup's steps are at w, w + G and so on
         DqItem it = dq_item(p, min((int)blockIdx.x, p.items - 1));
         for (int idx = blockIdx.x; idx < p.items; idx += gridDim.x) {
-            const int lo = it.lo, hi = it.hi;
+            const int steps = max(0, it.hi - it.lo);
             float nl = 0.f, nd = 0.f;
-            if (hi > lo) {  // the row values come with Q and dO
+            if (steps) {  // the row values come with Q and dO
                 if (!warp_spin(&bar->q_full, items & 1, p.status, 97, abort_flag)) break;
-                nl = bar->rows[row];
-                nd = bar->rows[128 + row];
+                nl = bar->rows[(row >> 6) * 128 + (row & 63)];
+                nd = bar->rows[(row >> 6) * 128 + 64 + (row & 63)];
                 __syncwarp();
                 if (lane == 0) mbar_arrive(&bar->q_free);
                 ++items;
@@ -431,23 +501,23 @@ softmax_attn_dq_kernel(const __grid_constant__ CUtensorMap tQ, const __grid_cons
             const int first = seen ? it.sp.first(it.q0 + row) : 0, end = seen ? it.sp.end(it.q0 + row) : 0;
             const unsigned width = end > first ? (unsigned)(end - first) : 0u;
             bool ok = true;
-            for (int j = lo, g = n; j < hi; ++j, ++g) {
-                if (!warp_spin(&bar->s_full[g & 1], (g >> 1) & 1, p.status, 94, abort_flag)) {
+            const int skip = (w + G - n % G) % G;
+            for (int j = skip; j < steps; j += G) {
+                if (!warp_spin_at(s_full + 8 * pos, phase, p.status, 94, abort_flag)) {
                     ok = false;
                     break;
                 }
                 tc_fence_after();
-                // keys that take no part: P = 0 whatever S holds, and dP = 0 below whatever it holds
-                const int k0 = j * kTile + 64 * half;
-                const bool masked = __any_sync(0xffffffffu, first > k0 || end < k0 + 64);
-                const uint32_t tS = tmem + C::kS + 64 * half + lanes;
-                if (masked) fill_outside(tS, first - k0, width, kMinusInf);
+                // keys that take no part: P = 0 whatever S holds (and rows past the length are
+                // zeros in shared memory, so dP is finite)
+                const int k0 = (it.lo + j) * kHalf;
+                if (__any_sync(0xffffffffu, first > k0 || end < k0 + kHalf)) hide_outside(tS, first - k0, width);
                 uint32_t v[2][32];
                 load_columns(tS, v);
                 tc_fence_before();
                 __syncwarp();
-                if (lane == 0) mbar_arrive(&bar->s_free);
-                const float2 sl2 = make_float2(sl, sl), off2 = make_float2(nl, nl);
+                if (lane == 0) arrive_at(s_free + 8 * pos);
+                const float2 off2 = make_float2(nl, nl);
 #pragma unroll
                 for (int c = 0; c < 2; ++c)
 #pragma unroll
@@ -457,49 +527,51 @@ softmax_attn_dq_kernel(const __grid_constant__ CUtensorMap tQ, const __grid_cons
                         v[c][e] = __float_as_uint(ex2_approx(y.x));
                         v[c][e + 1] = __float_as_uint(ex2_approx(y.y));
                     }
-                const uint32_t tD = tmem + C::kDp + 128 * (g & 1) + 64 * half + lanes;
-                if (!warp_spin(&bar->dp_full[g & 1], (g >> 1) & 1, p.status, 95, abort_flag)) {
+                if (!warp_spin_at(dp_full + 8 * pos, phase, p.status, 95, abort_flag)) {
                     ok = false;
                     break;
                 }
                 tc_fence_after();
-                if (masked) fill_outside(tD, first - k0, width, 0u);
                 const float2 nd2 = make_float2(nd, nd);
-                uint32_t u[2][32], o[32];
-                load_columns(tD, u);
+                // 32 columns at a time; dS takes the columns that have been read
 #pragma unroll
-                for (int c = 0; c < 2; ++c)
+                for (int c = 0; c < 2; ++c) {
+                    uint32_t u[32], o[16];
+                    tmem_ld32(tD + 32 * c, u);
 #pragma unroll
                     for (int e = 0; e < 32; e += 2) {
-                        const float2 y = fadd2(make_float2(__uint_as_float(u[c][e]), __uint_as_float(u[c][e + 1])), nd2);
+                        const float2 y = fadd2(make_float2(__uint_as_float(u[e]), __uint_as_float(u[e + 1])), nd2);
                         const float2 z = fmul2(make_float2(__uint_as_float(v[c][e]), __uint_as_float(v[c][e + 1])), y);
-                        o[16 * c + e / 2] = pack2(z.x, z.y);
+                        o[e / 2] = pack2(z.x, z.y);
                     }
-                tmem_st32(tD, o);
+                    tmem_st16_async(tD + 16 * c, o);
+                }
+                tmem_wait_st();
                 tc_fence_before();
                 __syncwarp();
-                if (lane == 0) mbar_arrive(&bar->ds_full[g & 1][half]);
+                if (lane == 0) arrive_at(ds_full + 8 * pos);
+                pos += G;
+                if (pos >= C::kStages) pos = w, phase ^= 1u;
             }
-            n += max(0, hi - lo);
+            n += steps;
             if (!ok) break;
-            const bool some = hi > lo;
             const DqItem next = dq_item(p, min(idx + (int)gridDim.x, p.items - 1));  // while dQ ends
             const int i = it.q0 + row;
             const bool exists = i < p.nq, valid = i < it.sp.Lq;
             __nv_bfloat16 *dst = p.dQ + it.batch * p.sdQ.b + it.head * p.sdQ.h + (int64_t)i * p.sdQ.n;
-            if (some) {
+            if (w < 2 && steps) {  // half of the columns each
                 if (!warp_spin(&bar->acc_full, (items - 1) & 1, p.status, 96, abort_flag)) break;
                 tc_fence_after();
-                uint32_t o[DP / 64][32];  // half of the columns
-                load_columns(tmem + C::kDq + half * (DP / 2) + lanes, o);
+                uint32_t o[DP / 64][32];
+                load_columns(tmem + C::kDq + w * (DP / 2) + lanes, o);
                 tc_fence_before();
                 __syncwarp();
                 if (lane == 0) mbar_arrive(&bar->acc_free);
                 if (exists)
 #pragma unroll
                     for (int c = 0; c < DP / 64; ++c)
-                        store_row(dst, o[c], half * (DP / 2) + 32 * c, p.d, p.scale, !valid, p.wide & 1);
-            } else if (exists && half == 0) {
+                        store_row(dst, o[c], w * (DP / 2) + 32 * c, p.d, p.scale, !valid, p.wide & 1);
+            } else if (w == 0 && exists) {
                 zero_row(dst, p.d);
             }
             it = next;
@@ -514,19 +586,16 @@ softmax_attn_dq_kernel(const __grid_constant__ CUtensorMap tQ, const __grid_cons
 // ---------------------------------------------------------------- dK, dV
 template <int DP>
 struct DkvLayout {
-    static constexpr uint32_t kTileBytes = kTile * DP * 2;
-    static constexpr int kStages = DP == 64 ? 4 : 2;
-    static constexpr uint32_t kStageBytes = 2 * kTileBytes + 1024;  // Q, dO, lse and delta
+    // slots, one of each warpgroup: S in 64 columns, dP in 64 (as many as fit beside dV and dK)
+    static constexpr int G = DP == 64 ? 3 : 2;
+    static constexpr uint32_t kTileBytes = kTile * DP * 2, kStepBytes = kHalf * DP * 2;
+    static constexpr int kStages = DP == 64 ? 9 : 4;  // steps: Q, dO, lse and delta
     static constexpr int kKv = DP == 64 ? 2 : 1;  // items whose K and V are held
-    // S and dP of the steps in turn take kBufs buffers of 128 columns: S of step g buffer
-    // 2 g, dP buffer 2 g + 1, modulo kBufs.  Each lives from its product over the arithmetic
-    // to the product that takes its P or dS.
-    static constexpr int kBufs = DP == 64 ? 3 : 2;
-    static constexpr uint32_t kDv = 128 * kBufs, kDk = kDv + DP;
-    static constexpr uint32_t kSmem = 1024 + kKv * 2 * kTileBytes + kStages * kStageBytes + 512;
+    static constexpr uint32_t kDv = 128 * G, kDk = kDv + DP;
+    static constexpr uint32_t kSmem = 1024 + kKv * 2 * kTileBytes + kStages * (2 * kStepBytes + 512) + 1024;
 };
 struct DkvItem {
-    int batch, kvh, k0, lo, hi;  // query tiles [lo, hi) of each head of the group
+    int batch, kvh, k0, lo, hi;  // steps [lo, hi) of 64 queries of each head of the group
     Span sp;
 };
 __device__ __forceinline__ DkvItem dkv_item(const BwdParams &p, int idx) {
@@ -544,36 +613,35 @@ __device__ __forceinline__ DkvItem dkv_item(const BwdParams &p, int idx) {
         const int a = p.causal ? max(0, it.k0 - off) : 0;
         const int z = p.window ? min((long long)it.sp.Lq, (long long)last - off + p.window) : it.sp.Lq;
         if (z > a) {
-            it.lo = a / kTile;
-            it.hi = (z + kTile - 1) / kTile;
+            it.lo = a / kHalf;
+            it.hi = (z + kHalf - 1) / kHalf;
         }
     }
     return it;
 }
 
-// Barriers of steps come in pairs, for even and odd steps: a waiter that falls behind by one
-// step still finds its own phase.
 struct DkvBarriers {
-    uint64_t kv_full[2], kv_free[2], s_full[2], p_full[2][2], pv_done[2], dp_full[2], ds_full[2][2], ds_done[2];
-    uint64_t acc_full, acc_free, fix_wanted, fixed[2], drain[2];
-    uint64_t full[4], empty[4];
+    uint64_t full[9], fixed[9], s_full[9], p_full[9], pv_done[9], dp_full[9], ds_full[9], ds_done[9];
+    uint64_t kv_full[2], kv_free[2], acc_full, acc_free, fix_wanted, drain[3];
     uint32_t tmem;
     int abort;
 };
+static_assert(sizeof(DkvBarriers) <= 1024, "room for the barriers");
 
 template <int DP>
-__global__ void __launch_bounds__(kThreads, 1)
+__global__ void __launch_bounds__(threads_of(DkvLayout<DP>::G), 1)
 softmax_attn_dkv_kernel(const __grid_constant__ CUtensorMap tQ, const __grid_constant__ CUtensorMap tK,
                         const __grid_constant__ CUtensorMap tV, const __grid_constant__ CUtensorMap tdO,
                         const BwdParams p) {
     using C = DkvLayout<DP>;
+    constexpr int G = C::G, kLoadWarp = 4 * G, kMmaWarp = 4 * G + 1;
     extern __shared__ uint8_t raw[];
     uint8_t *smem = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(raw) + 1023) & ~uintptr_t(1023));
     // K and V of an item at sK + (item % kKv) 2 tiles
     uint8_t *sK = smem, *sT = smem + C::kKv * 2 * C::kTileBytes;
-    // stage s: Q and dO tiles, then (after all tiles) its 1 KB of row values
-    uint8_t *sR = sT + C::kStages * 2 * C::kTileBytes;
-    DkvBarriers *bar = reinterpret_cast<DkvBarriers *>(sR + C::kStages * 1024);
+    // stage s: the step's Q and dO, then (after all of them) its 512 bytes of row values
+    uint8_t *sR = sT + C::kStages * 2 * C::kStepBytes;
+    DkvBarriers *bar = reinterpret_cast<DkvBarriers *>(sR + C::kStages * 512);
     volatile int *abort_flag = &bar->abort;
     const int tid = threadIdx.x, warp = __shfl_sync(0xffffffffu, tid >> 5, 0), lane = tid & 31;
 
@@ -581,24 +649,21 @@ softmax_attn_dkv_kernel(const __grid_constant__ CUtensorMap tQ, const __grid_con
         for (int i = 0; i < 2; ++i) {
             mbar_init(&bar->kv_full[i], 1);
             mbar_init(&bar->kv_free[i], 2);
+        }
+        for (int i = 0; i < 3; ++i) mbar_init(&bar->drain[i], 1);
+        for (int i = 0; i < C::kStages; ++i) {
+            mbar_init(&bar->full[i], 1);
+            mbar_init(&bar->fixed[i], 31);
             mbar_init(&bar->s_full[i], 1);
-            for (int h = 0; h < 2; ++h) {  // halves of 64 columns
-                mbar_init(&bar->p_full[i][h], kHalfWarps);
-                mbar_init(&bar->ds_full[i][h], kHalfWarps);
-            }
+            mbar_init(&bar->p_full[i], 4);
             mbar_init(&bar->pv_done[i], 1);
             mbar_init(&bar->dp_full[i], 1);
+            mbar_init(&bar->ds_full[i], 4);
             mbar_init(&bar->ds_done[i], 1);
-            mbar_init(&bar->drain[i], 1);
-            mbar_init(&bar->fixed[i], 31);
         }
-        mbar_init(&bar->acc_full, 2);
-        mbar_init(&bar->acc_free, kMathWarps);
+        mbar_init(&bar->acc_full, 1);
+        mbar_init(&bar->acc_free, 8);
         mbar_init(&bar->fix_wanted, 1);
-        for (int s = 0; s < C::kStages; ++s) {
-            mbar_init(&bar->full[s], 1);
-            mbar_init(&bar->empty[s], 2);  // both issuing threads
-        }
         bar->abort = 0;
         fence_mbar_init();
     }
@@ -612,10 +677,11 @@ softmax_attn_dkv_kernel(const __grid_constant__ CUtensorMap tQ, const __grid_con
     const uint32_t tmem = bar->tmem;
 
     if (warp >= kLoadWarp) {
-    setmaxnreg_dec<kIssueRegs>();
+    setmaxnreg_dec<issue_regs(G)>();
     if (warp == kLoadWarp) {
         if (lane == 0) {
             int ring = 0, items = 0;
+            Ring<G, C::kStages> at;
             bool ok = true;
             for (int idx = blockIdx.x; idx < p.items && ok; idx += gridDim.x) {
                 const DkvItem it = dkv_item(p, idx);
@@ -626,23 +692,23 @@ softmax_attn_dkv_kernel(const __grid_constant__ CUtensorMap tQ, const __grid_con
                     break;
                 uint8_t *kv = sK + kb * 2 * C::kTileBytes;
                 mbar_arrive_expect_tx(&bar->kv_full[kb], 2 * C::kTileBytes);
-                load_rows<DP>(kv, &tK, &bar->kv_full[kb], it.k0, 0, it.kvh, it.batch);
-                load_rows<DP>(kv + C::kTileBytes, &tV, &bar->kv_full[kb], it.k0, 0, it.kvh, it.batch);
+                load_rows<DP, 2>(kv, &tK, &bar->kv_full[kb], it.k0, 0, it.kvh, it.batch);
+                load_rows<DP, 2>(kv + C::kTileBytes, &tV, &bar->kv_full[kb], it.k0, 0, it.kvh, it.batch);
                 ++items;
                 for (int g = 0; g < p.group && ok; ++g)
-                    for (int j = it.lo; j < it.hi; ++j, ++ring) {
-                        const int s = ring % C::kStages;
-                        if (ring >= C::kStages &&
-                            !thread_spin(&bar->empty[s], (ring / C::kStages - 1) & 1, p.status, 101, abort_flag)) {
+                    for (int j = it.lo; j < it.hi; ++j, ++ring, at.next()) {
+                        const int s = at.pos;
+                        // (dK comes last: with it all products of a step have been formed)
+                        if (!thread_spin(&bar->ds_done[s], at.phase ^ 1, p.status, 101, abort_flag)) {
                             ok = false;
                             break;
                         }
-                        uint8_t *st = sT + s * 2 * C::kTileBytes;
-                        mbar_arrive_expect_tx(&bar->full[s], 2 * C::kTileBytes + 1024);
-                        load_rows<DP>(st, &tQ, &bar->full[s], j * kTile, g, it.kvh, it.batch);
-                        load_rows<DP>(st + C::kTileBytes, &tdO, &bar->full[s], j * kTile, g, it.kvh, it.batch);
+                        uint8_t *st = sT + s * 2 * C::kStepBytes;
+                        mbar_arrive_expect_tx(&bar->full[s], 2 * C::kStepBytes + 512);
+                        load_rows<DP, 1>(st, &tQ, &bar->full[s], j * kHalf, g, it.kvh, it.batch);
+                        load_rows<DP, 1>(st + C::kStepBytes, &tdO, &bar->full[s], j * kHalf, g, it.kvh, it.batch);
                         const int64_t head = (int64_t)it.batch * p.hq + it.kvh * p.group + g;
-                        bulk_load(sR + s * 1024, p.rows + (head * p.qtiles + j) * 256, 1024, &bar->full[s]);
+                        bulk_load(sR + s * 512, p.rows + (head * 2 * p.qtiles + j) * 128, 512, &bar->full[s]);
                     }
             }
             for (int i = max(0, items - C::kKv); i < items; ++i)
@@ -655,7 +721,7 @@ softmax_attn_dkv_kernel(const __grid_constant__ CUtensorMap tQ, const __grid_con
             for (int idx = blockIdx.x; idx < p.items && ok; idx += gridDim.x) {
                 const DkvItem it = dkv_item(p, idx);
                 if (it.hi <= it.lo) continue;
-                if (it.sp.Lq >= p.nq || it.hi * kTile <= it.sp.Lq) {
+                if (it.sp.Lq >= p.nq || it.hi * kHalf <= it.sp.Lq) {
                     ring += p.group * (it.hi - it.lo);
                     continue;
                 }
@@ -666,135 +732,136 @@ softmax_attn_dkv_kernel(const __grid_constant__ CUtensorMap tQ, const __grid_con
                         break;
                     }
                     ++nfix;
-                    uint8_t *st = sT + (ring - 1) % C::kStages * 2 * C::kTileBytes;
-                    zero_rows<DP>(st, it.sp.Lq - (it.hi - 1) * kTile, lane - 1, 31);
-                    zero_rows<DP>(st + C::kTileBytes, it.sp.Lq - (it.hi - 1) * kTile, lane - 1, 31);
+                    const int s = (ring - 1) % C::kStages, row0 = it.sp.Lq - (it.hi - 1) * kHalf;
+                    uint8_t *st = sT + s * 2 * C::kStepBytes;
+                    zero_rows<DP, kHalf>(st, row0, lane - 1, 31);
+                    zero_rows<DP, kHalf>(st + C::kStepBytes, row0, lane - 1, 31);
                     fence_proxy_async_smem();
-                    mbar_arrive(&bar->fixed[(nfix - 1) & 1]);
+                    mbar_arrive(&bar->fixed[s]);
                 }
             }
         }
         __syncwarp();
-    } else if (warp == kMmaWarp || warp == kMmaWarp + 1) {
-        const bool first = warp == kMmaWarp;  // S and dV; the other thread: dP and dK
+    } else if (warp <= kMmaWarp + 1) {
+        const bool first = warp == kMmaWarp;  // S = K Q^T; the other thread: dP = V dO^T
         if (elect_one()) {
-            int n = 0, items = 0, nfix = 0;
+            int items = 0;
+            uint32_t fixes = 0;  // bit s: parity of stage s's next fix
+            Ring<G, C::kStages> at;
             bool ok = true;
-            const uint32_t aKV0 = smem_u32(sK) + (first ? 0 : C::kTileBytes), aT = smem_u32(sT);
-            uint64_t *done = first ? bar->pv_done : bar->ds_done, *full = first ? bar->s_full : bar->dp_full,
-                     (*ready)[2] = first ? bar->p_full : bar->ds_full;
-            auto phase = [](int g) { return (uint32_t)(g >> 1) & 1u; };
-            auto buffer = [&](int g) { return tmem + 128 * ((2 * g + (first ? 0 : 1)) % C::kBufs); };
+            const uint32_t a0 = smem_u32(sK) + (first ? 0 : C::kTileBytes), b = smem_u32(sT) + (first ? 0 : C::kStepBytes),
+                           slots = tmem + (first ? 0 : 64), loaded = smem_u32(bar->full),
+                           done = smem_u32(first ? bar->pv_done : bar->ds_done),
+                           out = smem_u32(first ? bar->s_full : bar->dp_full), fixed = smem_u32(bar->fixed);
             for (int idx = blockIdx.x; idx < p.items && ok; idx += gridDim.x) {
                 const DkvItem it = dkv_item(p, idx);
                 const int per = it.hi - it.lo;
                 if (per <= 0) continue;
-                const int steps = per * p.group, end = n + steps;
-                const bool fix = it.sp.Lq < p.nq && it.hi * kTile > it.sp.Lq;
+                const bool fix = it.sp.Lq < p.nq && it.hi * kHalf > it.sp.Lq;
                 const int kb = items % C::kKv;
-                const uint32_t aKV = aKV0 + kb * 2 * C::kTileBytes;
-                int in_head = 0;  // tile of the next score step within its head
-                // S = K Q^T (or dP = V dO^T) of step g, into the buffer that step g - 1 or g - 2
-                // has left
-                auto score = [&](int g) {
-                    const int s = g % C::kStages;
-                    if (!thread_spin(&bar->full[s], (g / C::kStages) & 1, p.status, 103, abort_flag)) return false;
-                    if (++in_head == per) {
-                        in_head = 0;
-                        if (fix) {
-                            if (first) mbar_arrive(&bar->fix_wanted);
-                            if (!thread_spin(&bar->fixed[nfix & 1], phase(nfix), p.status, 104, abort_flag)) return false;
-                            ++nfix;
-                        }
+                const uint32_t a = a0 + kb * 2 * C::kTileBytes;
+                int in_head = per;
+                ok = thread_spin(&bar->kv_full[kb], (items / C::kKv) & 1, p.status, 107, abort_flag);
+                for (int j = per * p.group; j > 0 && ok; --j, at.next()) {
+                    ok = spin_at(loaded + 8 * at.pos, at.phase, p.status, 103, abort_flag) &&
+                         spin_at(done + 8 * at.before(), at.phase_before(), p.status, 105, abort_flag);
+                    if (ok && fix && --in_head == 0) {
+                        in_head = per;
+                        if (first) mbar_arrive(&bar->fix_wanted);
+                        ok = spin_at(fixed + 8 * at.pos, fixes >> at.pos & 1, p.status, 104, abort_flag);
+                        fixes ^= 1u << at.pos;
                     }
-                    if (C::kBufs == 2) {  // its own kind of the step before
-                        if (g >= 1 && !thread_spin(&done[(g - 1) & 1], phase(g - 1), p.status, 105, abort_flag))
-                            return false;
-                    } else if (first) {  // S follows dP of step g - 2
-                        if (g >= 2 && !thread_spin(&bar->ds_done[g & 1], phase(g - 2), p.status, 105, abort_flag))
-                            return false;
-                    } else {  // dP follows S of step g - 1
-                        if (g >= 1 && !thread_spin(&bar->pv_done[(g - 1) & 1], phase(g - 1), p.status, 106, abort_flag))
-                            return false;
-                    }
+                    if (!ok) break;
                     tc_fence_after();
-                    mma_scores<DP>(buffer(g), aKV, aT + s * 2 * C::kTileBytes + (first ? 0 : C::kTileBytes));
-                    mma_commit(&full[g & 1]);
-                    return true;
-                };
-                // dV += P^T dO (or dK += dS^T Q) of step g
-                auto sum = [&](int g) {
-                    const int s = g % C::kStages;
-                    const uint32_t d = tmem + (first ? C::kDv : C::kDk), m = buffer(g),
-                                   t = aT + s * 2 * C::kTileBytes + (first ? C::kTileBytes : 0);
-                    if (!thread_spin(&ready[g & 1][0], phase(g), p.status, 108, abort_flag)) return false;
-                    if (g == n && items > 0 &&
-                        !thread_spin(&bar->acc_free, (items - 1) & 1, p.status, 109, abort_flag))
-                        return false;
-                    tc_fence_after();
-                    mma_sum_half<DP>(d, m, t, g > n ? 1u : 0u);
-                    if (!thread_spin(&ready[g & 1][1], phase(g), p.status, 108, abort_flag)) return false;
-                    tc_fence_after();
-                    mma_sum_half<DP>(d, m + 64, t + 8192, 1u);
-                    mma_commit(&done[g & 1]);
-                    mma_commit(&bar->empty[s]);
-                    return true;
-                };
-                ok = thread_spin(&bar->kv_full[kb], (items / C::kKv) & 1, p.status, 107, abort_flag) && score(n);
-                if (C::kBufs == 3 && first && steps > 1) ok = ok && score(n + 1);
-                for (int g = n; g < end && ok; ++g) {
-                    if (C::kBufs == 2) ok = sum(g) && (g + 1 >= end || score(g + 1));
-                    else if (first) ok = sum(g) && (g + 2 >= end || score(g + 2));
-                    else ok = (g + 1 >= end || score(g + 1)) && sum(g);
+                    mma_scores<DP>(slots + 128 * at.slot, a, b + at.pos * (2 * C::kStepBytes));
+                    commit_at(out + 8 * at.pos);
                 }
-                if (!ok) break;
                 mma_commit(&bar->kv_free[kb]);
-                mma_commit(&bar->acc_full);
-                n = end;
                 ++items;
             }
             mma_commit(&bar->drain[first ? 0 : 1]);
             mbar_wait_drain(&bar->drain[first ? 0 : 1], 0);
         }
         __syncwarp();
+    } else {
+        if (elect_one()) {  // dV += P^T dO of each step, then dK += dS^T Q, with three slots of the step before
+            constexpr int kLag = G - 2;
+            int items = 0;
+            Ring<G, C::kStages> av, ak;
+            bool ok = true;
+            const uint32_t b = smem_u32(sT), p_full = smem_u32(bar->p_full), ds_full = smem_u32(bar->ds_full),
+                           pv_done = smem_u32(bar->pv_done), ds_done = smem_u32(bar->ds_done);
+            for (int idx = blockIdx.x; idx < p.items && ok; idx += gridDim.x) {
+                const DkvItem it = dkv_item(p, idx);
+                const int steps = (it.hi - it.lo) * p.group;
+                if (steps <= 0) continue;
+                if (items > 0) ok = thread_spin(&bar->acc_free, (items - 1) & 1, p.status, 109, abort_flag);
+                for (int j = 0; j < steps + kLag && ok; ++j) {
+                    if (j < steps) {
+                        ok = spin_at(p_full + 8 * av.pos, av.phase, p.status, 106, abort_flag);
+                        if (!ok) break;
+                        tc_fence_after();
+                        mma_sum<DP>(tmem + C::kDv, tmem + 128 * av.slot, b + av.pos * (2 * C::kStepBytes) + C::kStepBytes,
+                                    j > 0 ? 1u : 0u);
+                        commit_at(pv_done + 8 * av.pos);
+                        av.next();
+                    }
+                    if (j >= kLag) {
+                        ok = spin_at(ds_full + 8 * ak.pos, ak.phase, p.status, 108, abort_flag);
+                        if (!ok) break;
+                        tc_fence_after();
+                        mma_sum<DP>(tmem + C::kDk, tmem + 128 * ak.slot + 64, b + ak.pos * (2 * C::kStepBytes),
+                                    j > kLag ? 1u : 0u);
+                        commit_at(ds_done + 8 * ak.pos);
+                        ak.next();
+                    }
+                }
+                mma_commit(&bar->acc_full);
+                ++items;
+            }
+            mma_commit(&bar->drain[2]);
+            mbar_wait_drain(&bar->drain[2], 0);
+        }
+        __syncwarp();
     }
     } else {
-        setmaxnreg_inc<kMathRegs>();
-        const int half = warp >> 2, row = tid & 127;
+        setmaxnreg_inc<math_regs(G)>();
+        const int w = warp >> 2, row = tid & 127;
         const uint32_t lanes = (uint32_t)((warp & 3) * 32) << 16;
-        const float sl = p.scale_log2;
-        const float2 sl2 = make_float2(sl, sl);
+        const uint32_t tS = tmem + 128 * w + lanes, tD = tS + 64;
+        const float2 sl2 = make_float2(p.scale_log2, p.scale_log2);
+        const uint32_t s_full = smem_u32(bar->s_full), p_full = smem_u32(bar->p_full), dp_full = smem_u32(bar->dp_full),
+                       ds_full = smem_u32(bar->ds_full), loaded = smem_u32(bar->full), rows = smem_u32(sR);
         int n = 0, items = 0;
+        uint32_t pos = w, phase = 0;  // in the ring; the warpgroup's steps are at w, w + G and so on
         bool ok = true;
         DkvItem it = dkv_item(p, min((int)blockIdx.x, p.items - 1));
         for (int idx = blockIdx.x; idx < p.items && ok; idx += gridDim.x) {
-            const int key = it.k0 + row, off = it.sp.Lk - it.sp.Lq, lo = it.lo, hi = it.hi,
-                      steps = (hi - lo) * p.group;
+            const int key = it.k0 + row, off = it.sp.Lk - it.sp.Lq, hi = it.hi, per = max(0, hi - it.lo),
+                      steps = per * p.group;
             // queries [first, end) see this key (the rows past the length need no mask: their
             // -lse is -inf)
             const int first = p.causal ? max(0, key - off) : 0;
             const int end = p.window ? (int)min((long long)it.sp.Lq, (long long)key - off + p.window) : 1 << 30;
             const unsigned width = end > first ? (unsigned)(end - first) : 0u;
-            int j = lo;
-            for (int g = n; g < n + steps; ++g) {
-                const int s = g % C::kStages;
-                const uint32_t tS = tmem + 128 * (2 * g % C::kBufs) + 64 * half + lanes,
-                               tD = tmem + 128 * ((2 * g + 1) % C::kBufs) + 64 * half + lanes;
-                const uint32_t aR = smem_u32(sR) + s * 1024 + 256 * half;  // -lse and, 512 on, -delta
-                const uint32_t parity = (uint32_t)(g >> 1) & 1u;
-                if (!warp_spin(&bar->full[s], (g / C::kStages) & 1, p.status, 111, abort_flag) ||
-                    !warp_spin(&bar->s_full[g & 1], parity, p.status, 112, abort_flag)) {
+            int h = n + (w + G - n % G) % G, j = it.lo + h - n;
+            n += steps;
+            for (; h < n; h += G, j += G) {
+                while (j >= hi) j -= per;  // the next head
+                const uint32_t aR = rows + pos * 512;  // -lse and, 256 on, -delta
+                if (!warp_spin_at(s_full + 8 * pos, phase, p.status, 112, abort_flag) ||
+                    !warp_spin_at(loaded + 8 * pos, phase, p.status, 111, abort_flag)) {
                     ok = false;
                     break;
                 }
                 tc_fence_after();
-                const int q0 = j * kTile + 64 * half;
-                if (__any_sync(0xffffffffu, first > q0 || end < q0 + 64))
-                    fill_outside(tS, first - q0, width, kMinusInf);
-                uint32_t v[2][32], o[32];
+                const int q0 = j * kHalf;
+                if (__any_sync(0xffffffffu, first > q0 || end < q0 + kHalf)) hide_outside(tS, first - q0, width);
+                uint32_t v[2][32];
                 load_columns(tS, v);
 #pragma unroll
-                for (int c = 0; c < 2; ++c)
+                for (int c = 0; c < 2; ++c) {
+                    uint32_t o[16];
 #pragma unroll
                     for (int e = 0; e < 32; e += 4) {
                         const float4 l = lds4(aR + 4 * (32 * c + e));
@@ -806,63 +873,67 @@ softmax_attn_dkv_kernel(const __grid_constant__ CUtensorMap tQ, const __grid_con
                         v[c][e + 1] = __float_as_uint(ex2_approx(y0.y));
                         v[c][e + 2] = __float_as_uint(ex2_approx(y1.x));
                         v[c][e + 3] = __float_as_uint(ex2_approx(y1.y));
-                        o[16 * c + e / 2] = pack2(__uint_as_float(v[c][e]), __uint_as_float(v[c][e + 1]));
-                        o[16 * c + e / 2 + 1] = pack2(__uint_as_float(v[c][e + 2]), __uint_as_float(v[c][e + 3]));
+                        o[e / 2] = pack2(__uint_as_float(v[c][e]), __uint_as_float(v[c][e + 1]));
+                        o[e / 2 + 1] = pack2(__uint_as_float(v[c][e + 2]), __uint_as_float(v[c][e + 3]));
                     }
-                tmem_st32(tS, o);
+                    tmem_st16_async(tS + 16 * c, o);
+                }
+                tmem_wait_st();
                 tc_fence_before();
                 __syncwarp();
-                if (lane == 0) mbar_arrive(&bar->p_full[g & 1][half]);
-                if (!warp_spin(&bar->dp_full[g & 1], parity, p.status, 113, abort_flag)) {
+                if (lane == 0) arrive_at(p_full + 8 * pos);
+                if (!warp_spin_at(dp_full + 8 * pos, phase, p.status, 113, abort_flag)) {
                     ok = false;
                     break;
                 }
                 tc_fence_after();
-                uint32_t u[2][32];
-                load_columns(tD, u);
+                // 32 columns at a time; dS takes the columns that have been read
 #pragma unroll
-                for (int c = 0; c < 2; ++c)
+                for (int c = 0; c < 2; ++c) {
+                    uint32_t u[32], o[16];
+                    tmem_ld32(tD + 32 * c, u);
 #pragma unroll
                     for (int e = 0; e < 32; e += 4) {
-                        const float4 dl = lds4(aR + 512 + 4 * (32 * c + e));
-                        const float2 y0 = fadd2(make_float2(__uint_as_float(u[c][e]), __uint_as_float(u[c][e + 1])),
+                        const float4 dl = lds4(aR + 256 + 4 * (32 * c + e));
+                        const float2 y0 = fadd2(make_float2(__uint_as_float(u[e]), __uint_as_float(u[e + 1])),
                                                 make_float2(dl.x, dl.y));
-                        const float2 y1 = fadd2(make_float2(__uint_as_float(u[c][e + 2]), __uint_as_float(u[c][e + 3])),
+                        const float2 y1 = fadd2(make_float2(__uint_as_float(u[e + 2]), __uint_as_float(u[e + 3])),
                                                 make_float2(dl.z, dl.w));
                         const float2 z0 = fmul2(make_float2(__uint_as_float(v[c][e]), __uint_as_float(v[c][e + 1])), y0);
                         const float2 z1 = fmul2(make_float2(__uint_as_float(v[c][e + 2]), __uint_as_float(v[c][e + 3])), y1);
-                        o[16 * c + e / 2] = pack2(z0.x, z0.y);
-                        o[16 * c + e / 2 + 1] = pack2(z1.x, z1.y);
+                        o[e / 2] = pack2(z0.x, z0.y);
+                        o[e / 2 + 1] = pack2(z1.x, z1.y);
                     }
-                tmem_st32(tD, o);
+                    tmem_st16_async(tD + 16 * c, o);
+                }
+                tmem_wait_st();
                 tc_fence_before();
                 __syncwarp();
-                if (lane == 0) mbar_arrive(&bar->ds_full[g & 1][half]);
-                if (++j == hi) j = lo;
+                if (lane == 0) arrive_at(ds_full + 8 * pos);
+                pos += G;
+                if (pos >= C::kStages) pos = w, phase ^= 1u;
             }
-            n += max(0, steps);
             if (!ok) break;
-            const bool some = steps > 0;
             const DkvItem next = dkv_item(p, min(idx + (int)gridDim.x, p.items - 1));  // while the sums end
             const bool exists = key < p.nk, valid = key < it.sp.Lk;
-            // warps 0-3 write dV, warps 4-7 dK
+            // the first two warpgroups write dV and dK
             __nv_bfloat16 *dst =
-                half ? p.dK + it.batch * p.sdK.b + it.kvh * p.sdK.h + (int64_t)key * p.sdK.n
-                      : p.dV + it.batch * p.sdV.b + it.kvh * p.sdV.h + (int64_t)key * p.sdV.n;
-            if (some) {
+                w ? p.dK + it.batch * p.sdK.b + it.kvh * p.sdK.h + (int64_t)key * p.sdK.n
+                  : p.dV + it.batch * p.sdV.b + it.kvh * p.sdV.h + (int64_t)key * p.sdV.n;
+            if (w < 2 && steps) {
                 if (!warp_spin(&bar->acc_full, items & 1, p.status, 114, abort_flag)) break;
                 tc_fence_after();
                 ++items;
                 uint32_t o[DP / 32][32];
-                load_columns(tmem + (half ? C::kDk : C::kDv) + lanes, o);
+                load_columns(tmem + (w ? C::kDk : C::kDv) + lanes, o);
                 tc_fence_before();
                 __syncwarp();
                 if (lane == 0) mbar_arrive(&bar->acc_free);
                 if (exists)
 #pragma unroll
                     for (int c = 0; c < DP / 32; ++c)
-                        store_row(dst, o[c], 32 * c, p.d, half ? p.scale : 1.f, !valid, p.wide >> (half ? 1 : 2) & 1);
-            } else if (exists) {
+                        store_row(dst, o[c], 32 * c, p.d, w ? p.scale : 1.f, !valid, p.wide >> (w ? 1 : 2) & 1);
+            } else if (w < 2 && exists) {
                 zero_row(dst, p.d);
             }
             it = next;
@@ -880,10 +951,10 @@ int launch(const Call &c, BwdParams &p) {
     using Cq = DqLayout<DP>;
     using Ck = DkvLayout<DP>;
     CUtensorMap tQ, tK, tV, tdO;
-    if (!encode_rows(&tQ, c.Q, c.sQ, c.b, c.hq, p.group, c.nq, c.d, kTile, 1) ||
-        !encode_rows(&tdO, c.dO, c.sdO, c.b, c.hq, p.group, c.nq, c.d, kTile, 1) ||
-        !encode_rows(&tK, c.K, c.sK, c.b, c.hk, 1, c.nk, c.d, kTile, 1) ||
-        !encode_rows(&tV, c.V, c.sV, c.b, c.hk, 1, c.nk, c.d, kTile, 1))
+    if (!encode_rows(&tQ, c.Q, c.sQ, c.b, c.hq, p.group, c.nq, c.d, kHalf, 1) ||
+        !encode_rows(&tdO, c.dO, c.sdO, c.b, c.hq, p.group, c.nq, c.d, kHalf, 1) ||
+        !encode_rows(&tK, c.K, c.sK, c.b, c.hk, 1, c.nk, c.d, kHalf, 1) ||
+        !encode_rows(&tV, c.V, c.sV, c.b, c.hk, 1, c.nk, c.d, kHalf, 1))
         return LINFORMER_ERR_LAUNCH;
     int st = allow_smem(reinterpret_cast<const void *>(softmax_attn_dq_kernel<DP>), Cq::kSmem, DP == 64 ? 2 : 3);
     if (!st) st = allow_smem(reinterpret_cast<const void *>(softmax_attn_dkv_kernel<DP>), Ck::kSmem, DP == 64 ? 4 : 5);
@@ -906,7 +977,6 @@ int launch(const Call &c, BwdParams &p) {
     cudaLaunchAttribute attr[1];
     attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
     attr[0].val.programmaticStreamSerializationAllowed = 1;
-    cfg.blockDim = dim3(kThreads);
     cfg.stream = c.stream;
     cfg.attrs = attr;
     cfg.numAttrs = 1;
@@ -914,6 +984,7 @@ int launch(const Call &c, BwdParams &p) {
         KernelScope scope(LINFORMER_KERNEL_SOFTMAX_BWD, c.stream);
         p.items = (int)qitems;
         cfg.gridDim = dim3((unsigned)std::min<int64_t>(qitems, sms));
+        cfg.blockDim = dim3(threads_of(Cq::G));
         cfg.dynamicSmemBytes = Cq::kSmem;
         if (cudaLaunchKernelEx(&cfg, softmax_attn_dq_kernel<DP>, tQ, tK, tV, tdO, p) != cudaSuccess)
             st = LINFORMER_ERR_LAUNCH;
@@ -922,6 +993,7 @@ int launch(const Call &c, BwdParams &p) {
         KernelScope scope(LINFORMER_KERNEL_SOFTMAX_BWD, c.stream);
         p.items = (int)kitems;
         cfg.gridDim = dim3((unsigned)std::min<int64_t>(kitems, sms));
+        cfg.blockDim = dim3(threads_of(Ck::G));
         cfg.dynamicSmemBytes = Ck::kSmem;
         if (cudaLaunchKernelEx(&cfg, softmax_attn_dkv_kernel<DP>, tQ, tK, tV, tdO, p) != cudaSuccess)
             st = LINFORMER_ERR_LAUNCH;

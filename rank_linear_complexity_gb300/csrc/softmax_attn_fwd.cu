@@ -305,7 +305,7 @@ softmax_attn_fwd_kernel(const __grid_constant__ CUtensorMap tQ, const __grid_con
                 // the issuing thread has seen the block land
                 if (!thread_spin(&bar->fix_wanted, nfix & 1, p.status, 72, abort_flag)) break;
                 ++nfix;
-                zero_rows<DP>(sKV + (ring - 1) % C::kStages * C::kTileBytes,
+                zero_rows<DP, kTile>(sKV + (ring - 1) % C::kStages * C::kTileBytes,
                               it.sp.Lk - (it.hi - 1) * kTile, lane - 1, 31);
                 fence_proxy_async_smem();
                 mbar_arrive(&bar->fixed);
