@@ -38,35 +38,44 @@ __device__ __forceinline__ void mbar_arrive_expect_tx(uint64_t *bar, uint32_t by
                  "r"(bytes)
                  : "memory");
 }
-__device__ __forceinline__ void mbar_arrive(uint64_t *bar) {
-    asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];" ::"r"(smem_u32(bar)) : "memory");
+// (Barriers are named by pointer, or by shared-memory address where the few instructions
+// between a wait and a product count.)
+__device__ __forceinline__ void mbar_arrive(uint32_t bar) {
+    asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];" ::"r"(bar) : "memory");
 }
-__device__ __forceinline__ bool mbar_try_wait(uint64_t *bar, uint32_t parity) {
+__device__ __forceinline__ void mbar_arrive(uint64_t *bar) { mbar_arrive(smem_u32(bar)); }
+__device__ __forceinline__ bool mbar_try_wait(uint32_t bar, uint32_t parity) {
     uint32_t ok;
     asm volatile(
         "{\n\t.reg .pred p;\n\t"
         "mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2;\n\t"
         "selp.u32 %0, 1, 0, p;\n\t}"
         : "=r"(ok)
-        : "r"(smem_u32(bar)), "r"(parity)
+        : "r"(bar), "r"(parity)
         : "memory");
     return ok != 0;
+}
+__device__ __forceinline__ bool mbar_try_wait(uint64_t *bar, uint32_t parity) {
+    return mbar_try_wait(smem_u32(bar), parity);
 }
 
 // try_wait with a suspend-time hint: a waiting thread sleeps until the phase
 // completes (it is woken within about a hundred cycles) or the hint elapses,
 // instead of spinning and taking issue slots from the warps that compute.
 constexpr uint32_t kSuspendHintNs = 100000;
-__device__ __forceinline__ bool mbar_try_wait_sleep(uint64_t *bar, uint32_t parity) {
+__device__ __forceinline__ bool mbar_try_wait_sleep(uint32_t bar, uint32_t parity) {
     uint32_t ok;
     asm volatile(
         "{\n\t.reg .pred p;\n\t"
         "mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2, %3;\n\t"
         "selp.u32 %0, 1, 0, p;\n\t}"
         : "=r"(ok)
-        : "r"(smem_u32(bar)), "r"(parity), "r"(kSuspendHintNs)
+        : "r"(bar), "r"(parity), "r"(kSuspendHintNs)
         : "memory");
     return ok != 0;
+}
+__device__ __forceinline__ bool mbar_try_wait_sleep(uint64_t *bar, uint32_t parity) {
+    return mbar_try_wait_sleep(smem_u32(bar), parity);
 }
 
 // Waits for phase `parity` of `bar` to complete.  Returns false (after setting
@@ -102,7 +111,7 @@ __device__ __forceinline__ bool warp_wait(uint64_t *bar, uint32_t parity, int *s
 // lane polls with the hint and hands the result to the others.  Longer waits go on out of
 // line, with the hint, the abort flag and the clock, so that the code of a wait is a few
 // instructions wherever one stands.
-static __device__ __noinline__ bool thread_spin_on(uint64_t *bar, uint32_t parity, int *status, int code,
+static __device__ __noinline__ bool thread_spin_on(uint32_t bar, uint32_t parity, int *status, int code,
                                                    volatile int *abort) {
     const uint64_t t0 = globaltimer();
     while (!mbar_try_wait_sleep(bar, parity)) {
@@ -115,7 +124,7 @@ static __device__ __noinline__ bool thread_spin_on(uint64_t *bar, uint32_t parit
     }
     return true;
 }
-static __device__ __noinline__ bool warp_spin_on(uint64_t *bar, uint32_t parity, int *status, int code,
+static __device__ __noinline__ bool warp_spin_on(uint32_t bar, uint32_t parity, int *status, int code,
                                                  volatile int *abort) {
     const uint64_t t0 = globaltimer();
     while (!__any_sync(0xffffffffu, mbar_try_wait_sleep(bar, parity))) {
@@ -128,15 +137,23 @@ static __device__ __noinline__ bool warp_spin_on(uint64_t *bar, uint32_t parity,
     }
     return true;
 }
-__device__ __forceinline__ bool thread_spin(uint64_t *bar, uint32_t parity, int *status, int code,
+__device__ __forceinline__ bool thread_spin(uint32_t bar, uint32_t parity, int *status, int code,
                                             volatile int *abort) {
     return mbar_try_wait(bar, parity) || thread_spin_on(bar, parity, status, code, abort);
 }
+__device__ __forceinline__ bool thread_spin(uint64_t *bar, uint32_t parity, int *status, int code,
+                                            volatile int *abort) {
+    return thread_spin(smem_u32(bar), parity, status, code, abort);
+}
 // Every lane of a converged warp; the vote gives all of them the same answer.
-__device__ __forceinline__ bool warp_spin(uint64_t *bar, uint32_t parity, int *status, int code,
+__device__ __forceinline__ bool warp_spin(uint32_t bar, uint32_t parity, int *status, int code,
                                           volatile int *abort) {
     return __any_sync(0xffffffffu, mbar_try_wait(bar, parity)) ||
            warp_spin_on(bar, parity, status, code, abort);
+}
+__device__ __forceinline__ bool warp_spin(uint64_t *bar, uint32_t parity, int *status, int code,
+                                          volatile int *abort) {
+    return warp_spin(smem_u32(bar), parity, status, code, abort);
 }
 
 // Non-blocking probe of phase `parity` of `bar`.
@@ -303,12 +320,10 @@ __device__ __forceinline__ void mma_ts(uint32_t d_tmem, uint32_t a_tmem, uint64_
         : "memory");
 }
 // Arrive once on `bar` when every tcgen05.mma this thread issued so far has completed.
-__device__ __forceinline__ void mma_commit(uint64_t *bar) {
-    asm volatile(
-        "tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(
-            smem_u32(bar))
-        : "memory");
+__device__ __forceinline__ void mma_commit(uint32_t bar) {
+    asm volatile("tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(bar) : "memory");
 }
+__device__ __forceinline__ void mma_commit(uint64_t *bar) { mma_commit(smem_u32(bar)); }
 
 // 32 consecutive fp32 columns of this warp's 32 TMEM lanes -> v[0..31] (load + wait).
 __device__ __forceinline__ void tmem_ld32(uint32_t taddr, uint32_t (&v)[32]) {

@@ -4,24 +4,33 @@
 //     dP = dO V^T,   dS_ij = P_ij (dP_ij - delta_i),
 //     dV = P^T dO,   dK = scale dS^T Q,   dQ = scale dS K,
 //
-// two kernels after a small one, each a sum that one CTA owns, so that no gradient is added up by atomics
-// and every result repeats bit for bit:
+// two kernels after a small one, each a sum that one CTA owns, so that no gradient is added up
+// by atomics and every result repeats bit for bit:
 //   rows_kernel  -lse log2(e) and -delta of every query row, for the other two.
-//   dq_kernel   a 128-row query tile against its key blocks: S, dP, then dQ += dS.K.
-//   dkv_kernel  a 128-key block against the query tiles of every head of its group:
-//               S^T = K.Q^T and dP^T = V.dO^T, then dV += P^T.dO and dK += dS^T.Q.  With
-//               keys as the rows, P^T and dS^T leave the registers of the thread that made
-//               them for the tensor memory of the next product: no transpose, no shared
-//               memory.
+//   dq_kernel    a 128-row query tile against its keys: S, dP, then dQ += dS.K.
+//   dkv_kernel   a 128-key block against the queries of every head of its group:
+//                S^T = K.Q^T and dP^T = V.dO^T, then dV += P^T.dO and dK += dS^T.Q.  With
+//                keys as the rows, P^T and dS^T leave the registers of the thread that made
+//                them for the tensor memory of the next product: no transpose, no shared
+//                memory.
 // Seven products instead of five: S and dP are formed twice, which costs less than adding
 // partial dQ through memory in a fixed order.  P and dS are rounded to bf16 as operands
 // (relative 2^-9, in sums of many terms); sums are fp32 in tensor memory.
 //
-// Roles, both kernels: warps 0-3 and 4-7 do the arithmetic of the two halves (64 columns) of
-// every step, one thread a row; each half's P or dS is multiplied as soon as it is there;
-// warp 8 loads (lane 0) and zeroes rows past the valid length (lanes 1-31, where 0 x NaN
-// would reach a sum); one thread each of warps 9 and 10 issues products, so that a chain of
-// products that waits for arithmetic does not hold up the other one.
+// Both are chains of product -> arithmetic -> product, about 350 cycles from a product's last
+// cycle to the arithmetic, so they go in steps of 64 columns with several in flight: tensor
+// memory holds, beside the sums, as many slots as fit (64 columns of S and 64 of dP each; two
+// or three), and every slot has a warpgroup of its own, one thread a row, 64 columns a thread.
+// Whole steps of 128 columns, one in flight and half a step a warpgroup, took 1.25 times as long
+// (d = 64).  The last warpgroup issues: warp 0 of it loads (lane 0) and zeroes rows past the
+// valid length (lanes 1-31, where 0 x NaN would reach a sum); one thread each of the other
+// three issues S, dP and the sums, since such a thread takes about 300 cycles from one product
+// to the next (short code that runs now and then, fetched anew each time) and the tensor cores
+// would wait for a single one.
+// Measured (b h = 76, n = 4096, alone on the GPU at 2070 MHz): d = 64: rows 17 us (4.7 TB/s),
+// dQ 382 us (1.28 PFLOP/s of its three products), dK and dV 460 us (1.42 PFLOP/s of four);
+// d = 128: 33, 684 (1.43) and 800 us (1.63).  Back to back they draw the board's full power and
+// the clock settles at 1650 to 1900 MHz.
 #include <algorithm>
 #include <cmath>
 
@@ -155,58 +164,6 @@ __device__ __forceinline__ void load_rows(uint8_t *dst, const CUtensorMap *m, ui
             tma_load_5d(dst + (c * N + r) * 8192, m, bar, c * 64, row + 64 * r, head, group, batch);
 }
 
-// Waits by shared-memory address (the issuing threads' few instructions between a barrier and
-// a product are what the tensor cores wait for).
-__device__ __forceinline__ bool try_at(uint32_t bar, uint32_t parity) {
-    uint32_t ok;
-    asm volatile(
-        "{\n\t.reg .pred p;\n\tmbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2;\n\t"
-        "selp.u32 %0, 1, 0, p;\n\t}"
-        : "=r"(ok)
-        : "r"(bar), "r"(parity)
-        : "memory");
-    return ok != 0;
-}
-static __device__ __noinline__ bool spin_on(uint32_t bar, uint32_t parity, int *status, int code,
-                                            volatile int *abort) {
-    const uint64_t t0 = globaltimer();
-    while (!try_at(bar, parity)) {
-        if (*abort) return false;
-        if (globaltimer() - t0 > kWaitLimitNs) {
-            *abort = 1;
-            if (status) atomicExch(status, code);
-            return false;
-        }
-    }
-    return true;
-}
-__device__ __forceinline__ bool spin_at(uint32_t bar, uint32_t parity, int *status, int code,
-                                        volatile int *abort) {
-    return try_at(bar, parity) || spin_on(bar, parity, status, code, abort);
-}
-static __device__ __noinline__ bool warp_spin_on_at(uint32_t bar, uint32_t parity, int *status, int code,
-                                                    volatile int *abort) {
-    const uint64_t t0 = globaltimer();
-    while (!__any_sync(0xffffffffu, try_at(bar, parity))) {
-        if (__any_sync(0xffffffffu, *abort != 0)) return false;
-        if (__any_sync(0xffffffffu, globaltimer() - t0 > kWaitLimitNs)) {
-            *abort = 1;
-            if (status) atomicExch(status, code);
-            return false;
-        }
-    }
-    return true;
-}
-__device__ __forceinline__ bool warp_spin_at(uint32_t bar, uint32_t parity, int *status, int code,
-                                             volatile int *abort) {
-    return __any_sync(0xffffffffu, try_at(bar, parity)) || warp_spin_on_at(bar, parity, status, code, abort);
-}
-__device__ __forceinline__ void arrive_at(uint32_t bar) {
-    asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];" ::"r"(bar) : "memory");
-}
-__device__ __forceinline__ void commit_at(uint32_t bar) {
-    asm volatile("tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(bar) : "memory");
-}
 // Where a step stands in a ring of N = some times G positions: the position (its stage and its
 // barriers of every kind), the ring's phase, and the slot.
 template <int G, int N>
@@ -323,7 +280,7 @@ softmax_attn_dq_kernel(const __grid_constant__ CUtensorMap tQ, const __grid_cons
     extern __shared__ uint8_t raw[];
     uint8_t *smem = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(raw) + 1023) & ~uintptr_t(1023));
     uint8_t *sQ = smem, *sdO = smem + C::kTileBytes, *sKV = smem + 2 * C::kTileBytes;
-    DqBarriers *bar = reinterpret_cast<DqBarriers *>(sKV + C::kStages * 2 * C::kStepBytes);
+    DqBarriers *bar = reinterpret_cast<DqBarriers *>(sKV + C::kStages * 2 * C::kStepBytes);  // [K, V] a stage
     volatile int *abort_flag = &bar->abort;
     const int tid = threadIdx.x, warp = __shfl_sync(0xffffffffu, tid >> 5, 0), lane = tid & 31;
 
@@ -430,16 +387,16 @@ softmax_attn_dq_kernel(const __grid_constant__ CUtensorMap tQ, const __grid_cons
                 const bool fix = it.sp.Lk < p.nk && it.hi * kHalf > it.sp.Lk;
                 ok = thread_spin(&bar->q_full, items & 1, p.status, 91, abort_flag);
                 for (int j = steps; j > 0 && ok; --j, at.next()) {
-                    ok = spin_at(loaded + 8 * at.pos, at.phase, p.status, 86, abort_flag) &&
-                         spin_at(free + 8 * at.before(), at.phase_before(), p.status, 88, abort_flag);
+                    ok = thread_spin(loaded + 8 * at.pos, at.phase, p.status, 86, abort_flag) &&
+                         thread_spin(free + 8 * at.before(), at.phase_before(), p.status, 88, abort_flag);
                     if (ok && fix && j == 1) {
                         mbar_arrive(&bar->fix_wanted);
-                        ok = spin_at(fixed, nfix++ & 1, p.status, 87, abort_flag);
+                        ok = thread_spin(fixed, nfix++ & 1, p.status, 87, abort_flag);
                     }
                     if (!ok) break;
                     tc_fence_after();
                     mma_scores<DP>(slots + 128 * at.slot, a, b + at.pos * (2 * C::kStepBytes));
-                    commit_at(out + 8 * at.pos);
+                    mma_commit(out + 8 * at.pos);
                 }
                 mma_commit(&bar->q_free);
                 ++items;
@@ -461,11 +418,11 @@ softmax_attn_dq_kernel(const __grid_constant__ CUtensorMap tQ, const __grid_cons
                 if (items > 0) ok = thread_spin(&bar->acc_free, (items - 1) & 1, p.status, 93, abort_flag);
                 for (int j = 0; j < steps && ok; ++j, at.next()) {
                     // (dS says that S has been formed, so the block of K has landed)
-                    ok = spin_at(ready + 8 * at.pos, at.phase, p.status, 92, abort_flag);
+                    ok = thread_spin(ready + 8 * at.pos, at.phase, p.status, 92, abort_flag);
                     if (!ok) break;
                     tc_fence_after();
                     mma_sum<DP>(tmem + C::kDq, tmem + 128 * at.slot + 64, b + at.pos * (2 * C::kStepBytes), j > 0 ? 1u : 0u);
-                    commit_at(done + 8 * at.pos);
+                    mma_commit(done + 8 * at.pos);
                 }
                 mma_commit(&bar->acc_full);
                 ++items;
@@ -503,7 +460,7 @@ softmax_attn_dq_kernel(const __grid_constant__ CUtensorMap tQ, const __grid_cons
             bool ok = true;
             const int skip = (w + G - n % G) % G;
             for (int j = skip; j < steps; j += G) {
-                if (!warp_spin_at(s_full + 8 * pos, phase, p.status, 94, abort_flag)) {
+                if (!warp_spin(s_full + 8 * pos, phase, p.status, 94, abort_flag)) {
                     ok = false;
                     break;
                 }
@@ -516,7 +473,7 @@ softmax_attn_dq_kernel(const __grid_constant__ CUtensorMap tQ, const __grid_cons
                 load_columns(tS, v);
                 tc_fence_before();
                 __syncwarp();
-                if (lane == 0) arrive_at(s_free + 8 * pos);
+                if (lane == 0) mbar_arrive(s_free + 8 * pos);
                 const float2 off2 = make_float2(nl, nl);
 #pragma unroll
                 for (int c = 0; c < 2; ++c)
@@ -527,7 +484,7 @@ softmax_attn_dq_kernel(const __grid_constant__ CUtensorMap tQ, const __grid_cons
                         v[c][e] = __float_as_uint(ex2_approx(y.x));
                         v[c][e + 1] = __float_as_uint(ex2_approx(y.y));
                     }
-                if (!warp_spin_at(dp_full + 8 * pos, phase, p.status, 95, abort_flag)) {
+                if (!warp_spin(dp_full + 8 * pos, phase, p.status, 95, abort_flag)) {
                     ok = false;
                     break;
                 }
@@ -549,7 +506,7 @@ softmax_attn_dq_kernel(const __grid_constant__ CUtensorMap tQ, const __grid_cons
                 tmem_wait_st();
                 tc_fence_before();
                 __syncwarp();
-                if (lane == 0) arrive_at(ds_full + 8 * pos);
+                if (lane == 0) mbar_arrive(ds_full + 8 * pos);
                 pos += G;
                 if (pos >= C::kStages) pos = w, phase ^= 1u;
             }
@@ -763,18 +720,18 @@ softmax_attn_dkv_kernel(const __grid_constant__ CUtensorMap tQ, const __grid_con
                 int in_head = per;
                 ok = thread_spin(&bar->kv_full[kb], (items / C::kKv) & 1, p.status, 107, abort_flag);
                 for (int j = per * p.group; j > 0 && ok; --j, at.next()) {
-                    ok = spin_at(loaded + 8 * at.pos, at.phase, p.status, 103, abort_flag) &&
-                         spin_at(done + 8 * at.before(), at.phase_before(), p.status, 105, abort_flag);
+                    ok = thread_spin(loaded + 8 * at.pos, at.phase, p.status, 103, abort_flag) &&
+                         thread_spin(done + 8 * at.before(), at.phase_before(), p.status, 105, abort_flag);
                     if (ok && fix && --in_head == 0) {
                         in_head = per;
                         if (first) mbar_arrive(&bar->fix_wanted);
-                        ok = spin_at(fixed + 8 * at.pos, fixes >> at.pos & 1, p.status, 104, abort_flag);
+                        ok = thread_spin(fixed + 8 * at.pos, fixes >> at.pos & 1, p.status, 104, abort_flag);
                         fixes ^= 1u << at.pos;
                     }
                     if (!ok) break;
                     tc_fence_after();
                     mma_scores<DP>(slots + 128 * at.slot, a, b + at.pos * (2 * C::kStepBytes));
-                    commit_at(out + 8 * at.pos);
+                    mma_commit(out + 8 * at.pos);
                 }
                 mma_commit(&bar->kv_free[kb]);
                 ++items;
@@ -798,21 +755,21 @@ softmax_attn_dkv_kernel(const __grid_constant__ CUtensorMap tQ, const __grid_con
                 if (items > 0) ok = thread_spin(&bar->acc_free, (items - 1) & 1, p.status, 109, abort_flag);
                 for (int j = 0; j < steps + kLag && ok; ++j) {
                     if (j < steps) {
-                        ok = spin_at(p_full + 8 * av.pos, av.phase, p.status, 106, abort_flag);
+                        ok = thread_spin(p_full + 8 * av.pos, av.phase, p.status, 106, abort_flag);
                         if (!ok) break;
                         tc_fence_after();
                         mma_sum<DP>(tmem + C::kDv, tmem + 128 * av.slot, b + av.pos * (2 * C::kStepBytes) + C::kStepBytes,
                                     j > 0 ? 1u : 0u);
-                        commit_at(pv_done + 8 * av.pos);
+                        mma_commit(pv_done + 8 * av.pos);
                         av.next();
                     }
                     if (j >= kLag) {
-                        ok = spin_at(ds_full + 8 * ak.pos, ak.phase, p.status, 108, abort_flag);
+                        ok = thread_spin(ds_full + 8 * ak.pos, ak.phase, p.status, 108, abort_flag);
                         if (!ok) break;
                         tc_fence_after();
                         mma_sum<DP>(tmem + C::kDk, tmem + 128 * ak.slot + 64, b + ak.pos * (2 * C::kStepBytes),
                                     j > kLag ? 1u : 0u);
-                        commit_at(ds_done + 8 * ak.pos);
+                        mma_commit(ds_done + 8 * ak.pos);
                         ak.next();
                     }
                 }
@@ -849,8 +806,8 @@ softmax_attn_dkv_kernel(const __grid_constant__ CUtensorMap tQ, const __grid_con
             for (; h < n; h += G, j += G) {
                 while (j >= hi) j -= per;  // the next head
                 const uint32_t aR = rows + pos * 512;  // -lse and, 256 on, -delta
-                if (!warp_spin_at(s_full + 8 * pos, phase, p.status, 112, abort_flag) ||
-                    !warp_spin_at(loaded + 8 * pos, phase, p.status, 111, abort_flag)) {
+                if (!warp_spin(s_full + 8 * pos, phase, p.status, 112, abort_flag) ||
+                    !warp_spin(loaded + 8 * pos, phase, p.status, 111, abort_flag)) {
                     ok = false;
                     break;
                 }
@@ -881,8 +838,8 @@ softmax_attn_dkv_kernel(const __grid_constant__ CUtensorMap tQ, const __grid_con
                 tmem_wait_st();
                 tc_fence_before();
                 __syncwarp();
-                if (lane == 0) arrive_at(p_full + 8 * pos);
-                if (!warp_spin_at(dp_full + 8 * pos, phase, p.status, 113, abort_flag)) {
+                if (lane == 0) mbar_arrive(p_full + 8 * pos);
+                if (!warp_spin(dp_full + 8 * pos, phase, p.status, 113, abort_flag)) {
                     ok = false;
                     break;
                 }
@@ -909,7 +866,7 @@ softmax_attn_dkv_kernel(const __grid_constant__ CUtensorMap tQ, const __grid_con
                 tmem_wait_st();
                 tc_fence_before();
                 __syncwarp();
-                if (lane == 0) arrive_at(ds_full + 8 * pos);
+                if (lane == 0) mbar_arrive(ds_full + 8 * pos);
                 pos += G;
                 if (pos >= C::kStages) pos = w, phase ^= 1u;
             }
