@@ -131,6 +131,25 @@ def test_backward(name):
         within(g, r, e, n, w)
 
 
+MORE = {  # steps of 64: heads of one step, lengths that end in a step or on its edge, many of each
+    "one_step_heads": (2, 24, 2, 40, 300, 64, dict(q=[33, 7], k=[300, 129])),
+    "one_step_heads_wide": (2, 24, 2, 40, 300, 128, dict(q=[33, 7], k=[300, 129])),
+    "two_step_heads": (3, 14, 2, 100, 70, 72, dict(q=[100, 64, 65], k=[70, 64, 65])),
+    "step_edges": (3, 4, 2, 192, 192, 64, dict(causal=True, q=[192, 65, 64], k=[192, 65, 64])),
+    "step_edges_wide": (3, 4, 2, 192, 192, 128, dict(causal=True, q=[191, 63, 1], k=[191, 63, 1])),
+    "window_of_a_step": (1, 6, 3, 200, 330, 64, dict(causal=True, window=65, q=[131])),
+    "long_ring": (1, 3, 1, 200, 2000, 128, dict(k=[1985])),
+    "long_ring_of_queries": (1, 12, 1, 700, 70, 64, dict(q=[650])),
+}
+
+
+@pytest.mark.parametrize("name", MORE)
+def test_steps_and_their_edges(name):
+    CASES[name] = MORE[name]
+    test_forward(name)
+    test_backward(name)
+
+
 # --- ways of calling ----------------------------------------------------------------------
 
 def same(a, b):
