@@ -5,7 +5,7 @@
 //     dV = P^T dO,   dK = scale dS^T Q,   dQ = scale dS K,
 //
 // two kernels after a small one, each a sum that one CTA owns, so that no gradient is added up
-// by atomics and every result repeats bit for bit:
+// by atomics and every result repeats bit for bit (an item of few is split into parts, joined in their order):
 //   rows_kernel  -lse log2(e) and -delta of every query row, for the other two.
 //   dq_kernel    a 128-row query tile against its keys: S, dP, then dQ += dS.K.
 //   dkv_kernel   a 128-key block against the queries of every head of its group:
@@ -67,6 +67,9 @@ struct BwdParams {
     int b, hq, hk, group, nq, nk, d, causal, window;
     int qtiles, kblocks;
     int wide;  // bits: dQ, dK, dV take 32-byte stores
+    // parts of the steps that an item is split into, and the parts' sums, fp32 [part][b][heads][n][DP]
+    int qsplit, ksplit;
+    float *part_q, *part_k, *part_v;
     int items;
     float scale, scale_log2;
     int *status;
@@ -118,10 +121,24 @@ __device__ __forceinline__ void store_row(__nv_bfloat16 *dst, const uint32_t (&o
         }
     }
 }
+// The same into a part's sums.
+__device__ __forceinline__ void store_part(float *dst, const uint32_t (&o)[32], bool zero) {
+#pragma unroll
+    for (int x = 0; x < 32; x += 8) {
+        uint32_t w[8];
+#pragma unroll
+        for (int e = 0; e < 8; ++e) w[e] = zero ? 0u : o[x + e];
+        store32(dst + x, w);
+    }
+}
 // The first d columns of a row as zero.
 __device__ __forceinline__ void zero_row(__nv_bfloat16 *dst, int d) {
 #pragma unroll 1
     for (int c = 0; c < d; c += 8) *reinterpret_cast<uint4 *>(dst + c) = make_uint4(0u, 0u, 0u, 0u);
+}
+__device__ __forceinline__ void zero_part(float *dst, int d) {
+#pragma unroll 1
+    for (int c = 0; c < d; c += 4) *reinterpret_cast<float4 *>(dst + c) = make_float4(0.f, 0.f, 0.f, 0.f);
 }
 // 32 N columns of tensor memory, one wait for all.
 template <int N>
@@ -233,14 +250,27 @@ struct DqLayout {
     static constexpr uint32_t kDq = 128 * G;
     static constexpr uint32_t kSmem = 1024 + 2 * kTileBytes + kStages * 2 * kStepBytes + 1024 + 1024;
 };
+// Part i of n of the steps [lo, hi).
+__device__ __forceinline__ void take_part(int &lo, int &hi, int i, int n) {
+    const int steps = hi - lo;
+    hi = lo + steps * (i + 1) / n;
+    lo += steps * i / n;
+}
 struct DqItem {
-    int batch, head, q0, lo, hi;  // steps [lo, hi) of 64 keys
+    int batch, head, q0, lo, hi, part;  // steps [lo, hi) of 64 keys
     Span sp;
 };
 __device__ __forceinline__ DqItem dq_item(const BwdParams &p, int idx) {
     DqItem it;
     const int units = p.b * p.hq;
-    const int rank = idx / units, u = idx - rank * units;
+    int rank = idx / units;
+    const int u = idx - rank * units;
+    it.part = 0;
+    if (p.qsplit > 1) {
+        const int x = rank;
+        rank = x / p.qsplit;
+        it.part = x - rank * p.qsplit;
+    }
     const int tile = p.causal ? p.qtiles - 1 - rank : rank;  // longest first
     it.batch = u / p.hq;
     it.head = u - it.batch * p.hq;
@@ -254,6 +284,7 @@ __device__ __forceinline__ DqItem dq_item(const BwdParams &p, int idx) {
         if (e > f) {
             it.lo = f / kHalf;
             it.hi = (e + kHalf - 1) / kHalf;
+            if (p.qsplit > 1) take_part(it.lo, it.hi, it.part, p.qsplit);
         }
     }
     return it;
@@ -516,6 +547,7 @@ softmax_attn_dq_kernel(const __grid_constant__ CUtensorMap tQ, const __grid_cons
             const int i = it.q0 + row;
             const bool exists = i < p.nq, valid = i < it.sp.Lq;
             __nv_bfloat16 *dst = p.dQ + it.batch * p.sdQ.b + it.head * p.sdQ.h + (int64_t)i * p.sdQ.n;
+            float *part = p.part_q + ((((int64_t)it.part * p.b + it.batch) * p.hq + it.head) * p.nq + i) * DP;
             if (w < 2 && steps) {  // half of the columns each
                 if (!warp_spin(&bar->acc_full, (items - 1) & 1, p.status, 96, abort_flag)) break;
                 tc_fence_after();
@@ -526,10 +558,14 @@ softmax_attn_dq_kernel(const __grid_constant__ CUtensorMap tQ, const __grid_cons
                 if (lane == 0) mbar_arrive(&bar->acc_free);
                 if (exists)
 #pragma unroll
-                    for (int c = 0; c < DP / 64; ++c)
-                        store_row(dst, o[c], w * (DP / 2) + 32 * c, p.d, p.scale, !valid, p.wide & 1);
+                    for (int c = 0; c < DP / 64; ++c) {
+                        const int at = w * (DP / 2) + 32 * c;
+                        if (p.qsplit > 1) store_part(part + at, o[c], !valid);
+                        else store_row(dst, o[c], at, p.d, p.scale, !valid, p.wide & 1);
+                    }
             } else if (w == 0 && exists) {
-                zero_row(dst, p.d);
+                if (p.qsplit > 1) zero_part(part, DP);
+                else zero_row(dst, p.d);
             }
             it = next;
         }
@@ -552,13 +588,20 @@ struct DkvLayout {
     static constexpr uint32_t kSmem = 1024 + kKv * 2 * kTileBytes + kStages * (2 * kStepBytes + 512) + 1024;
 };
 struct DkvItem {
-    int batch, kvh, k0, lo, hi;  // steps [lo, hi) of 64 queries of each head of the group
+    int batch, kvh, k0, part, lo, hi;  // steps [lo, hi) of 64 queries of each head of the group
     Span sp;
 };
 __device__ __forceinline__ DkvItem dkv_item(const BwdParams &p, int idx) {
     DkvItem it;
     const int units = p.b * p.hk;
-    const int block = idx / units, u = idx - block * units;
+    int block = idx / units;
+    const int u = idx - block * units;
+    it.part = 0;
+    if (p.ksplit > 1) {
+        const int x = block;
+        block = x / p.ksplit;
+        it.part = x - block * p.ksplit;
+    }
     it.k0 = block * kTile;  // causal: early keys are seen by the most queries
     it.batch = u / p.hk;
     it.kvh = u - it.batch * p.hk;
@@ -572,6 +615,7 @@ __device__ __forceinline__ DkvItem dkv_item(const BwdParams &p, int idx) {
         if (z > a) {
             it.lo = a / kHalf;
             it.hi = (z + kHalf - 1) / kHalf;
+            if (p.ksplit > 1) take_part(it.lo, it.hi, it.part, p.ksplit);
         }
     }
     return it;
@@ -877,6 +921,8 @@ softmax_attn_dkv_kernel(const __grid_constant__ CUtensorMap tQ, const __grid_con
             __nv_bfloat16 *dst =
                 w ? p.dK + it.batch * p.sdK.b + it.kvh * p.sdK.h + (int64_t)key * p.sdK.n
                   : p.dV + it.batch * p.sdV.b + it.kvh * p.sdV.h + (int64_t)key * p.sdV.n;
+            float *part = (w ? p.part_k : p.part_v) +
+                          ((((int64_t)it.part * p.b + it.batch) * p.hk + it.kvh) * p.nk + key) * DP;
             if (w < 2 && steps) {
                 if (!warp_spin(&bar->acc_full, items & 1, p.status, 114, abort_flag)) break;
                 tc_fence_after();
@@ -888,10 +934,13 @@ softmax_attn_dkv_kernel(const __grid_constant__ CUtensorMap tQ, const __grid_con
                 if (lane == 0) mbar_arrive(&bar->acc_free);
                 if (exists)
 #pragma unroll
-                    for (int c = 0; c < DP / 32; ++c)
-                        store_row(dst, o[c], 32 * c, p.d, w ? p.scale : 1.f, !valid, p.wide >> (w ? 1 : 2) & 1);
+                    for (int c = 0; c < DP / 32; ++c) {
+                        if (p.ksplit > 1) store_part(part + 32 * c, o[c], !valid);
+                        else store_row(dst, o[c], 32 * c, p.d, w ? p.scale : 1.f, !valid, p.wide >> (w ? 1 : 2) & 1);
+                    }
             } else if (w < 2 && exists) {
-                zero_row(dst, p.d);
+                if (p.ksplit > 1) zero_part(part, DP);
+                else zero_row(dst, p.d);
             }
             it = next;
         }
@@ -901,6 +950,37 @@ softmax_attn_dkv_kernel(const __grid_constant__ CUtensorMap tQ, const __grid_con
     __syncthreads();
     tc_fence_after();
     if (warp == kMmaWarp) tmem_dealloc(tmem, 512);
+}
+
+// Adds up the parts of dQ, dK and dV (blockIdx.y) in their order, four columns a thread.
+constexpr int kJoinThreads = 128;
+template <int DP>
+__global__ void __launch_bounds__(kJoinThreads) join_parts_kernel(const BwdParams p) {
+    const int which = blockIdx.y, parts = which ? p.ksplit : p.qsplit;
+    if (parts <= 1) return;
+    const int heads = which ? p.hk : p.hq, n = which ? p.nk : p.nq;
+    const int64_t rows = (int64_t)p.b * heads * n, t = (int64_t)blockIdx.x * kJoinThreads + threadIdx.x;
+    const int64_t r = t / (DP / 4);
+    const int col = (int)(t % (DP / 4)) * 4;
+    if (r >= rows || col >= p.d) return;
+    const float *src = (which == 0 ? p.part_q : which == 1 ? p.part_k : p.part_v) + r * DP + col;
+    float4 sum = make_float4(0.f, 0.f, 0.f, 0.f);
+    for (int i = 0; i < parts; ++i) {
+        const float4 x = *reinterpret_cast<const float4 *>(src + i * rows * DP);
+        sum.x += x.x, sum.y += x.y, sum.z += x.z, sum.w += x.w;
+    }
+    const int row = (int)(r % n), head = (int)(r / n % heads), batch = (int)(r / ((int64_t)n * heads));
+    const Strides &st = which == 0 ? p.sdQ : which == 1 ? p.sdK : p.sdV;
+    __nv_bfloat16 *dst = (which == 0 ? p.dQ : which == 1 ? p.dK : p.dV) + batch * st.b + head * st.h + row * st.n + col;
+    const float f = which < 2 ? p.scale : 1.f;
+    *reinterpret_cast<uint2 *>(dst) = make_uint2(pack2(sum.x * f, sum.y * f), pack2(sum.z * f, sum.w * f));
+}
+
+// Parts of an item of `steps` steps where `items` leave SMs idle: at least kMinSteps each, and
+// only where whole items take longer than writing and joining parts (about 8 us) costs.
+int parts_of(int64_t items, int64_t steps, int sms) {
+    constexpr int kMinSteps = 16, kFirst = 48;
+    return steps < kFirst ? 1 : (int)std::max<int64_t>(1, std::min<int64_t>(sms / items, steps / kMinSteps));
 }
 
 template <int DP>
@@ -919,9 +999,18 @@ int launch(const Call &c, BwdParams &p) {
     void *ws = nullptr;
     const int64_t qitems = (int64_t)c.b * c.hq * p.qtiles, kitems = (int64_t)c.b * c.hk * p.kblocks;
     if (qitems > kMaxItems || kitems > kMaxItems) return LINFORMER_ERR_SIZE;
-    if (workspace_alloc(&ws, (size_t)qitems * 1024, c.stream) != LINFORMER_OK) return LINFORMER_ERR_ALLOC;
-    p.rows = static_cast<float *>(ws);
     const int sms = device_sms();
+    auto steps_of = [&](int n) { return ((c.window ? std::min(n, c.window + kTile) : n) + kHalf - 1) / kHalf; };
+    p.qsplit = parts_of(qitems, steps_of(c.nk), sms);
+    p.ksplit = std::min(parts_of(kitems, (int64_t)steps_of(c.nq) * p.group, sms), steps_of(c.nq));
+    const int64_t qrows = (int64_t)c.b * c.hq * c.nq, krows = (int64_t)c.b * c.hk * c.nk;
+    const int64_t qparts = p.qsplit > 1 ? p.qsplit * qrows * DP : 0, kparts = p.ksplit > 1 ? p.ksplit * krows * DP : 0;
+    if (workspace_alloc(&ws, (size_t)(qitems * 256 + qparts + 2 * kparts) * sizeof(float), c.stream) != LINFORMER_OK)
+        return LINFORMER_ERR_ALLOC;
+    p.rows = static_cast<float *>(ws);
+    p.part_q = p.rows + qitems * 256;
+    p.part_k = p.part_q + qparts;
+    p.part_v = p.part_k + kparts;
     {
         KernelScope scope(LINFORMER_KERNEL_SOFTMAX_BWD, c.stream);
         rows_kernel<DP><<<(unsigned)qitems, kRowsThreads, 0, c.stream>>>(p);
@@ -939,8 +1028,8 @@ int launch(const Call &c, BwdParams &p) {
     cfg.numAttrs = 1;
     if (!st) {
         KernelScope scope(LINFORMER_KERNEL_SOFTMAX_BWD, c.stream);
-        p.items = (int)qitems;
-        cfg.gridDim = dim3((unsigned)std::min<int64_t>(qitems, sms));
+        p.items = (int)qitems * p.qsplit;
+        cfg.gridDim = dim3((unsigned)std::min(p.items, sms));
         cfg.blockDim = dim3(threads_of(Cq::G));
         cfg.dynamicSmemBytes = Cq::kSmem;
         if (cudaLaunchKernelEx(&cfg, softmax_attn_dq_kernel<DP>, tQ, tK, tV, tdO, p) != cudaSuccess)
@@ -948,12 +1037,19 @@ int launch(const Call &c, BwdParams &p) {
     }
     if (!st) {
         KernelScope scope(LINFORMER_KERNEL_SOFTMAX_BWD, c.stream);
-        p.items = (int)kitems;
-        cfg.gridDim = dim3((unsigned)std::min<int64_t>(kitems, sms));
+        p.items = (int)kitems * p.ksplit;
+        cfg.gridDim = dim3((unsigned)std::min(p.items, sms));
         cfg.blockDim = dim3(threads_of(Ck::G));
         cfg.dynamicSmemBytes = Ck::kSmem;
         if (cudaLaunchKernelEx(&cfg, softmax_attn_dkv_kernel<DP>, tQ, tK, tV, tdO, p) != cudaSuccess)
             st = LINFORMER_ERR_LAUNCH;
+    }
+    if (!st && (p.qsplit > 1 || p.ksplit > 1)) {
+        KernelScope scope(LINFORMER_KERNEL_SOFTMAX_BWD, c.stream);
+        const int64_t rows = std::max(p.qsplit > 1 ? qrows : 0, p.ksplit > 1 ? krows : 0);
+        const unsigned blocks = (unsigned)((rows * (DP / 4) + kJoinThreads - 1) / kJoinThreads);
+        join_parts_kernel<DP><<<dim3(blocks, 3), kJoinThreads, 0, c.stream>>>(p);
+        if (cudaPeekAtLastError() != cudaSuccess) st = LINFORMER_ERR_LAUNCH;
     }
     if (st) cudaGetLastError();
     workspace_free(ws, c.stream);

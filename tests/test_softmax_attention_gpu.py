@@ -139,6 +139,11 @@ MORE = {  # steps of 64: heads of one step, lengths that end in a step or on its
     "step_edges_wide": (3, 4, 2, 192, 192, 128, dict(causal=True, q=[191, 63, 1], k=[191, 63, 1])),
     "window_of_a_step": (1, 6, 3, 200, 330, 64, dict(causal=True, window=65, q=[131])),
     "long_ring": (1, 3, 1, 200, 2000, 128, dict(k=[1985])),
+    # few items with many steps: split into parts
+    "few_keys": (2, 16, 2, 600, 46, 96, dict(q=[600, 155])),
+    "few_keys_causal": (1, 8, 1, 1100, 200, 64, dict(causal=True, q=[1090], k=[170])),
+    "few_queries": (1, 4, 2, 40, 5000, 64, dict(k=[4990])),
+    "few_queries_window": (2, 2, 1, 300, 5000, 128, dict(causal=True, window=3500, q=[300, 7], k=[5000, 200])),
     "long_ring_of_queries": (1, 12, 1, 700, 70, 64, dict(q=[650])),
 }
 
