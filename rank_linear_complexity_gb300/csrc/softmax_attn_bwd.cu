@@ -5,7 +5,8 @@
 //     dV = P^T dO,   dK = scale dS^T Q,   dQ = scale dS K,
 //
 // two kernels after a small one, each a sum that one CTA owns, so that no gradient is added up
-// by atomics and every result repeats bit for bit (an item of few is split into parts, joined in their order):
+// by atomics and every result repeats bit for bit (where there are few of them they are split
+// into parts, which a fourth kernel adds up in their order):
 //   rows_kernel  -lse log2(e) and -delta of every query row, for the other two.
 //   dq_kernel    a 128-row query tile against its keys: S, dP, then dQ += dS.K.
 //   dkv_kernel   a 128-key block against the queries of every head of its group:
@@ -977,10 +978,14 @@ __global__ void __launch_bounds__(kJoinThreads) join_parts_kernel(const BwdParam
 }
 
 // Parts of an item of `steps` steps where `items` leave SMs idle: at least kMinSteps each, and
-// only where whole items take longer than writing and joining parts (about 8 us) costs.
+// only where an item gets shorter by kGain steps, about what the launch that joins costs.  (8
+// items, whole and in parts: d = 64: 16 steps 19.4 and 21.9 us, 32 steps 23.1 and 21.4, 64 steps
+// 39.8 and 24.8; d = 128: 20.6 and 21.6, 30.6 and 26.5, 55.4 and 29.3 us; in parts of 16 steps
+// 30.7 and 31.0 at 32 and 64.  64 items of up to 32 steps: 25.1 whole, 29.0 halved.)
 int parts_of(int64_t items, int64_t steps, int sms) {
-    constexpr int kMinSteps = 16, kFirst = 48;
-    return steps < kFirst ? 1 : (int)std::max<int64_t>(1, std::min<int64_t>(sms / items, steps / kMinSteps));
+    constexpr int kMinSteps = 8, kGain = 24;
+    const int64_t n = std::min<int64_t>(sms / items, steps / kMinSteps);
+    return n > 1 && steps - steps / n >= kGain ? (int)n : 1;
 }
 
 template <int DP>
