@@ -70,6 +70,7 @@ struct BwdParams {
     int wide;  // bits: dQ, dK, dV take 32-byte stores
     // parts of the steps that an item is split into, and the parts' sums, fp32 [part][b][heads][n][DP]
     int qsplit, ksplit;
+    int qsome, ksome;  // heads at a time
     float *part_q, *part_k, *part_v;
     int items;
     float scale, scale_log2;
@@ -264,8 +265,8 @@ struct DqItem {
 __device__ __forceinline__ DqItem dq_item(const BwdParams &p, int idx) {
     DqItem it;
     const int units = p.b * p.hq;
-    int rank = idx / units;
-    const int u = idx - rank * units;
+    int rank, u;
+    place<true>(idx, p.qtiles * p.qsplit, units, p.qsome, rank, u);
     it.part = 0;
     if (p.qsplit > 1) {
         const int x = rank;
@@ -595,8 +596,8 @@ struct DkvItem {
 __device__ __forceinline__ DkvItem dkv_item(const BwdParams &p, int idx) {
     DkvItem it;
     const int units = p.b * p.hk;
-    int block = idx / units;
-    const int u = idx - block * units;
+    int block, u;
+    place<true>(idx, p.kblocks * p.ksplit, units, p.ksome, block, u);
     it.part = 0;
     if (p.ksplit > 1) {
         const int x = block;
@@ -1008,6 +1009,8 @@ int launch(const Call &c, BwdParams &p) {
     auto steps_of = [&](int n) { return ((c.window ? std::min(n, c.window + kTile) : n) + kHalf - 1) / kHalf; };
     p.qsplit = parts_of(qitems, steps_of(c.nk), sms);
     p.ksplit = std::min(parts_of(kitems, (int64_t)steps_of(c.nq) * p.group, sms), steps_of(c.nq));
+    p.qsome = units_at_once(p.qtiles, c.b * c.hq, ((int64_t)c.nk * c.d * 4 + p.group - 1) / p.group);
+    p.ksome = units_at_once(p.kblocks, c.b * c.hk, (int64_t)p.group * c.nq * c.d * 4);
     const int64_t qrows = (int64_t)c.b * c.hq * c.nq, krows = (int64_t)c.b * c.hk * c.nk;
     const int64_t qparts = p.qsplit > 1 ? p.qsplit * qrows * DP : 0, kparts = p.ksplit > 1 ? p.ksplit * krows * DP : 0;
     if (workspace_alloc(&ws, (size_t)(qitems * 256 + qparts + 2 * kparts) * sizeof(float), c.stream) != LINFORMER_OK)

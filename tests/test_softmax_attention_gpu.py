@@ -172,6 +172,26 @@ def test_results_repeat_bit_for_bit():
     status()
 
 
+@pytest.mark.parametrize("nq,nk,causal", [(300, 2048, False), (2048, 300, False), (2048, 2048, True)])
+def test_heads_in_sets(nq, nk, causal):
+    """A batch that streams more than L2 holds (its heads are taken in sets) gives each entry what
+    halves of it (which are not) give."""
+    b, h, d = 17, 16, 64
+    g = torch.Generator(device=DEV).manual_seed(nq)
+    Q, K, V, dO = (torch.randn(b, h, n, d, generator=g, device=DEV).to(BF) for n in (nq, nk, nk, nq))
+    q = torch.randint(1, nq + 1, (b,), generator=g, device=DEV, dtype=torch.int32)
+    k = torch.randint(1, nk + 1, (b,), generator=g, device=DEV, dtype=torch.int32)
+
+    def run(at):
+        x = [t[at].contiguous() for t in (Q, K, V, dO, q, k)]
+        O, lse = lf.softmax_attention(*x[:3], *x[4:], causal=causal)
+        return (O, lse, *lf.softmax_attention_backward(*x[:3], O, x[3], lse, *x[4:], causal=causal))
+
+    whole, halves = run(slice(0, b)), [run(slice(0, 8)), run(slice(8, b))]
+    status()
+    assert same(whole, [torch.cat(x) for x in zip(*halves)])
+
+
 def test_outputs_only_where_they_belong():
     """Slices of wider buffers (rows, heads, columns around them untouched), lse in a longer one."""
     b, hq, hk, n, d = 2, 4, 2, 150, 64
