@@ -61,15 +61,18 @@ __device__ __forceinline__ void place(int idx, int ranks, int units, int some, i
         unit = idx - rank * units;
     }
 }
-// Heads at a time: as many as stream 32 MB, all of them where nothing is read twice or all
-// together stream no more than L2 holds.  (Of `bytes` a head.  b h = 192, n = 4096, d = 64: 201 MB,
-// forward 811 -> 739 us, backward 2700 -> 2309 us: less DRAM traffic, and less power, which
-// bounds them; sets of 16 and 64 MB: 739 and 760, 2307 and 2351.  16 causal heads of 8191, 67 MB:
-// backward 1441 us all at once, 1610 in sets of 32 MB, where the last tiles of every set leave
-// SMs waiting.)
-inline int units_at_once(int ranks, int units, int64_t bytes) {
-    constexpr int64_t kStreamed = 32 << 20, kHeld = 128 << 20;
-    if (ranks <= 1 || bytes * units <= kHeld) return units;
+// Heads at a time: as many as stream 32 MB; all of them where nothing is read twice, or all
+// together stream little enough to stay in L2 without (`bytes` a head).  Measured, forward and
+// backward, in sets and all at once: b h = 192, n = 4096, d = 64 (201 MB) 741 and 801, 2310 and
+// 2686 us: less DRAM traffic, and less of the power that bounds them (sets of 16 and 64 MB: 739
+// and 760, 2307 and 2351); 76 heads (80 MB) 288 and 299, 871 and 906.  With few tiles a head
+// (480 heads of 512, 63 MB) the tail of each set costs more: 56 and 51, 157 and 151; and so do the
+// unequal tiles of few causal heads (backward of 32 heads over 8 of 8191, d = 128, 34 and 134 MB:
+// 1610 and 1441), less so of many (128 heads of 4096, d = 128: 1390 and 1555).
+inline int units_at_once(int ranks, int units, int64_t bytes, bool causal) {
+    constexpr int64_t kStreamed = 32 << 20;
+    const int64_t held = causal || ranks < 16 ? 128 << 20 : 48 << 20;
+    if (ranks <= 1 || bytes * units <= held) return units;
     return (int)std::max<int64_t>(1, std::min<int64_t>(units, kStreamed / bytes));
 }
 

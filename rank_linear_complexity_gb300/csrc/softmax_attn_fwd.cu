@@ -801,7 +801,7 @@ int forward(const Call &c) {
     const int64_t wanted = p.qbox * p.hbox <= kFewRows ? (kWaves * (int64_t)sms + whole - 1) / whole : sms / whole;
     p.nsplit = blocks < kFirst ? 1 : (int)std::max<int64_t>(1, std::min<int64_t>(wanted, blocks / kMinBlocks));
     p.items = (int)whole * p.nsplit;
-    p.some = units_at_once(p.npairs, p.units, (int64_t)c.nk * c.d * 4);
+    p.some = units_at_once(p.npairs, p.units, (int64_t)c.nk * c.d * 4, c.causal);
     return c.d <= 64 ? launch<64>(c, p) : launch<128>(c, p);
 }
 
