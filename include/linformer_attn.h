@@ -275,7 +275,8 @@ LINFORMER_API int linformer_softmax_attn_fwd(
  * dK and dV summed over the query heads that share the key/value head; rows past the
  * lengths get zero.  Same argument rules; dO and dQ are shaped like O, dK and dV like K.
  * Sums are formed in a fixed order (no atomics): repeated calls agree bit for bit.  The
- * workspace is 8 bytes per query row, rows rounded up to 128 per head.
+ * workspace is 8 bytes per query row, rows rounded up to 128 per head, and where few tiles
+ * have long sums, which are then split, fp32 partial sums (at most 152 tiles of 128 rows of each gradient).
  */
 LINFORMER_API int linformer_softmax_attn_bwd(
     const void *Q, const int64_t *Q_strides, const void *K, const int64_t *K_strides,

@@ -9,7 +9,7 @@
 // exact as that of position 1, without 64-bit floating point.
 //
 // Bound by memory: every element read and written once (bf16, 4 x 16384 rows of 32 heads of 64:
-// 97 us, 5.5 TB/s; sines shared by a block in shared memory instead: 123 us, the barrier and
+// 94 us, 5.7 TB/s; sines shared by a block in shared memory instead: 123 us, the barrier and
 // the second phase cost more than the sines).  A thread keeps the 8 (bf16) or 4
 // (fp32) sines and cosines of its pairs in registers and goes through several heads of both
 // tensors with them, 16-byte pieces at a time.

@@ -28,10 +28,10 @@
 // three issues S, dP and the sums, since such a thread takes about 300 cycles from one product
 // to the next (short code that runs now and then, fetched anew each time) and the tensor cores
 // would wait for a single one.
-// Measured (b h = 76, n = 4096, alone on the GPU at 2070 MHz): d = 64: rows 17 us (4.7 TB/s),
-// dQ 382 us (1.28 PFLOP/s of its three products), dK and dV 460 us (1.42 PFLOP/s of four);
-// d = 128: 33, 684 (1.43) and 800 us (1.63).  Back to back they draw the board's full power and
-// the clock settles at 1650 to 1900 MHz.
+// Measured (b h = 76, n = 4096, each launch alone): d = 64: rows 16 us (5.2 TB/s), dQ 395 us
+// (1.24 PFLOP/s of its three products, tensor pipe 54 %), dK and dV 485 us (1.35 PFLOP/s of four,
+// 59 %); d = 128: 30, 670 (1.46, 62 %) and 788 us (1.66, 71 %).  Back to back they draw the
+// board's full power and the clock settles at 1650 to 1950 MHz of 2070.
 #include <algorithm>
 #include <cmath>
 
