@@ -71,6 +71,7 @@ struct BwdParams {
     // parts of the steps that an item is split into, and the parts' sums, fp32 [part][b][heads][n][DP]
     int qsplit, ksplit;
     int qsome, ksome;  // heads at a time
+    int *queue;        // items taken so far beyond each CTA's first: of the dQ kernel, of the other
     float *part_q, *part_k, *part_v;
     int items;
     float scale, scale_log2;
@@ -199,6 +200,49 @@ struct Ring {
     }
 };
 
+// ---------------------------------------------------------------- work items
+// A CTA begins with the item of its number; the loading thread takes each further one from a
+// counter and tells the other roles, two items ahead at most.  (Items differ in length, under a
+// causal mask and with ragged lengths.  Taken in turn instead, item i by CTA i modulo the CTAs: 32
+// causal heads over 8 of 8191 1424 us against 1353, 32 ragged entries of 12 heads of 512 120
+// against 115.)
+struct Queue {
+    uint64_t full[2], free[2];
+    int next[2];
+};
+__device__ __forceinline__ void init_queue(Queue &q, int readers) {
+    for (int i = 0; i < 2; ++i) {
+        mbar_init(&q.full[i], 1);
+        mbar_init(&q.free[i], readers);
+    }
+}
+__device__ __forceinline__ bool tell(Queue &q, int &t, int idx, int *status, volatile int *abort) {
+    const int s = t & 1;
+    if (!thread_spin(&q.free[s], ((t >> 1) & 1) ^ 1, status, 81, abort)) return false;
+    *(volatile int *)&q.next[s] = idx;
+    mbar_arrive(&q.full[s]);
+    ++t;
+    return true;
+}
+// A single thread's next item, and a warp's.
+__device__ __forceinline__ bool thread_next(Queue &q, int &t, int &idx, int *status, volatile int *abort) {
+    const int s = t & 1;
+    if (!thread_spin(&q.full[s], (t >> 1) & 1, status, 82, abort)) return false;
+    idx = *(volatile int *)&q.next[s];
+    mbar_arrive(&q.free[s]);
+    ++t;
+    return true;
+}
+__device__ __forceinline__ bool warp_next(Queue &q, int &t, int &idx, int *status, volatile int *abort) {
+    const int s = t & 1;
+    if (!warp_spin(&q.full[s], (t >> 1) & 1, status, 82, abort)) return false;
+    idx = *(volatile int *)&q.next[s];
+    __syncwarp();
+    if ((threadIdx.x & 31) == 0) mbar_arrive(&q.free[s]);
+    ++t;
+    return true;
+}
+
 // ---------------------------------------------------------------- row values
 // -lse log2(e) and -delta = -dO.O of a query tile's 128 rows, eight warps of sixteen rows; a row
 // is read by DP / 8 lanes, 16 bytes each.  Bound by memory: O and dO once.
@@ -206,6 +250,7 @@ constexpr int kRowsThreads = 256;
 template <int DP>
 __global__ void __launch_bounds__(kRowsThreads) rows_kernel(const BwdParams p) {
     launch_dependents();
+    if (blockIdx.x == 0 && threadIdx.x < 2) p.queue[threadIdx.x] = 0;
     constexpr int kLanes = DP / 8, kAtOnce = 32 / kLanes, kTurns = 16 / kAtOnce;
     const int unit = blockIdx.x / p.qtiles, tile = blockIdx.x - unit * p.qtiles;
     const int batch = unit / p.hq, head = unit - batch * p.hq;
@@ -296,6 +341,7 @@ __device__ __forceinline__ DqItem dq_item(const BwdParams &p, int idx) {
 struct DqBarriers {
     uint64_t k_full[12], v_full[12], s_full[12], s_free[12], dp_full[12], ds_full[12], dq_done[12];
     uint64_t q_full, q_free, acc_full, acc_free, fix_wanted, fixed_k, fixed_v, drain[3];
+    Queue queue;
     uint32_t tmem;
     int abort;
     alignas(16) float rows[2 * kTile];  // the item's rows, loaded with Q and dO
@@ -335,6 +381,7 @@ softmax_attn_dq_kernel(const __grid_constant__ CUtensorMap tQ, const __grid_cons
         mbar_init(&bar->fixed_k, 31);
         mbar_init(&bar->fixed_v, 31);
         for (int i = 0; i < 3; ++i) mbar_init(&bar->drain[i], 1);
+        init_queue(bar->queue, (p.k_lengths ? 31 : 0) + 3 + 4 * G);  // zeroing lanes, issuing threads, warps
         bar->abort = 0;
         fence_mbar_init();
     }
@@ -352,39 +399,45 @@ softmax_attn_dq_kernel(const __grid_constant__ CUtensorMap tQ, const __grid_cons
         if (lane == 0) {
             wait_prerequisites();  // the row values; and only then may the third kernel start
             launch_dependents();
-            int steps = 0, nq = 0;
+            int steps = 0, nq = 0, t = 0;
             Ring<G, C::kStages> at;
             bool ok = true;
-            for (int idx = blockIdx.x; idx < p.items && ok; idx += gridDim.x) {
+            for (int idx = blockIdx.x; idx < p.items && ok;) {
+                const int following = gridDim.x + atomicAdd(p.queue, 1);
                 const DqItem it = dq_item(p, idx);
-                if (it.hi <= it.lo) continue;
-                if (nq > 0 && !thread_spin(&bar->q_free, (nq - 1) & 1, p.status, 83, abort_flag)) break;
-                mbar_arrive_expect_tx(&bar->q_full, 2 * C::kTileBytes + 1024);
-                const int g = it.head % p.group, kvh = it.head / p.group;
-                bulk_load(bar->rows, p.rows + (((int64_t)it.batch * p.hq + it.head) * p.qtiles + it.q0 / kTile) * 256,
-                          1024, &bar->q_full);
-                load_rows<DP, 2>(sQ, &tQ, &bar->q_full, it.q0, g, kvh, it.batch);
-                load_rows<DP, 2>(sdO, &tdO, &bar->q_full, it.q0, g, kvh, it.batch);
-                ++nq;
-                for (int j = it.lo; j < it.hi; ++j, ++steps, at.next()) {
-                    uint8_t *st = sKV + at.pos * 2 * C::kStepBytes;
-                    // (dQ comes last: with it all products of a step have been formed)
-                    ok = thread_spin(&bar->dq_done[at.pos], at.phase ^ 1, p.status, 84, abort_flag);
-                    if (!ok) break;
-                    mbar_arrive_expect_tx(&bar->k_full[at.pos], C::kStepBytes);
-                    load_rows<DP, 1>(st, &tK, &bar->k_full[at.pos], j * kHalf, 0, kvh, it.batch);
-                    mbar_arrive_expect_tx(&bar->v_full[at.pos], C::kStepBytes);
-                    load_rows<DP, 1>(st + C::kStepBytes, &tV, &bar->v_full[at.pos], j * kHalf, 0, kvh, it.batch);
+                if (it.hi > it.lo) {
+                    if (nq > 0 && !thread_spin(&bar->q_free, (nq - 1) & 1, p.status, 83, abort_flag)) break;
+                    mbar_arrive_expect_tx(&bar->q_full, 2 * C::kTileBytes + 1024);
+                    const int g = it.head % p.group, kvh = it.head / p.group;
+                    bulk_load(bar->rows, p.rows + (((int64_t)it.batch * p.hq + it.head) * p.qtiles + it.q0 / kTile) * 256,
+                              1024, &bar->q_full);
+                    load_rows<DP, 2>(sQ, &tQ, &bar->q_full, it.q0, g, kvh, it.batch);
+                    load_rows<DP, 2>(sdO, &tdO, &bar->q_full, it.q0, g, kvh, it.batch);
+                    ++nq;
+                    for (int j = it.lo; j < it.hi; ++j, ++steps, at.next()) {
+                        uint8_t *st = sKV + at.pos * 2 * C::kStepBytes;
+                        // (dQ comes last: with it all products of a step have been formed)
+                        ok = thread_spin(&bar->dq_done[at.pos], at.phase ^ 1, p.status, 84, abort_flag);
+                        if (!ok) break;
+                        mbar_arrive_expect_tx(&bar->k_full[at.pos], C::kStepBytes);
+                        load_rows<DP, 1>(st, &tK, &bar->k_full[at.pos], j * kHalf, 0, kvh, it.batch);
+                        mbar_arrive_expect_tx(&bar->v_full[at.pos], C::kStepBytes);
+                        load_rows<DP, 1>(st + C::kStepBytes, &tV, &bar->v_full[at.pos], j * kHalf, 0, kvh, it.batch);
+                    }
                 }
+                ok = ok && tell(bar->queue, t, following, p.status, abort_flag);
+                idx = following;
             }
             if (nq > 0) mbar_wait_drain(&bar->q_full, (nq - 1) & 1);
             for (int i = max(0, steps - C::kStages); i < steps; ++i) {
                 mbar_wait_drain(&bar->k_full[i % C::kStages], (i / C::kStages) & 1);
                 mbar_wait_drain(&bar->v_full[i % C::kStages], (i / C::kStages) & 1);
             }
-        } else {  // K and V rows past the valid length: P and dS are 0 there, but 0 x NaN is not
+        } else if (p.k_lengths) {  // K and V rows past the valid length: P and dS are 0 there, but 0 x NaN is not
             int ring = 0, nfix = 0;
-            for (int idx = blockIdx.x; idx < p.items; idx += gridDim.x) {
+            bool ok = true;
+            for (int idx = blockIdx.x, t = 0; idx < p.items && ok;
+                 ok = ok && thread_next(bar->queue, t, idx, p.status, abort_flag)) {
                 const DqItem it = dq_item(p, idx);
                 if (it.hi <= it.lo) continue;
                 ring += it.hi - it.lo;
@@ -413,7 +466,8 @@ softmax_attn_dq_kernel(const __grid_constant__ CUtensorMap tQ, const __grid_cons
                            free = smem_u32(first ? bar->s_free : bar->dq_done),
                            out = smem_u32(first ? bar->s_full : bar->dp_full),
                            fixed = smem_u32(first ? &bar->fixed_k : &bar->fixed_v);
-            for (int idx = blockIdx.x; idx < p.items && ok; idx += gridDim.x) {
+            for (int idx = blockIdx.x, t = 0; idx < p.items && ok;
+                 ok = ok && thread_next(bar->queue, t, idx, p.status, abort_flag)) {
                 const DqItem it = dq_item(p, idx);
                 const int steps = it.hi - it.lo;
                 if (steps <= 0) continue;
@@ -444,7 +498,8 @@ softmax_attn_dq_kernel(const __grid_constant__ CUtensorMap tQ, const __grid_cons
             Ring<G, C::kStages> at;
             bool ok = true;
             const uint32_t b = smem_u32(sKV), ready = smem_u32(bar->ds_full), done = smem_u32(bar->dq_done);
-            for (int idx = blockIdx.x; idx < p.items && ok; idx += gridDim.x) {
+            for (int idx = blockIdx.x, t = 0; idx < p.items && ok;
+                 ok = ok && thread_next(bar->queue, t, idx, p.status, abort_flag)) {
                 const DqItem it = dq_item(p, idx);
                 const int steps = it.hi - it.lo;
                 if (steps <= 0) continue;
@@ -476,7 +531,7 @@ softmax_attn_dq_kernel(const __grid_constant__ CUtensorMap tQ, const __grid_cons
         int n = 0, items = 0;
         uint32_t pos = w, phase = 0;  // in the ring; the warpgroup's steps are at w, w + G and so on
         DqItem it = dq_item(p, min((int)blockIdx.x, p.items - 1));
-        for (int idx = blockIdx.x; idx < p.items; idx += gridDim.x) {
+        for (int idx = blockIdx.x, t = 0; idx < p.items;) {
             const int steps = max(0, it.hi - it.lo);
             float nl = 0.f, nd = 0.f;
             if (steps) {  // the row values come with Q and dO
@@ -545,7 +600,9 @@ softmax_attn_dq_kernel(const __grid_constant__ CUtensorMap tQ, const __grid_cons
             }
             n += steps;
             if (!ok) break;
-            const DqItem next = dq_item(p, min(idx + (int)gridDim.x, p.items - 1));  // while dQ ends
+            int following = 0;
+            if (!warp_next(bar->queue, t, following, p.status, abort_flag)) break;
+            const DqItem next = dq_item(p, min(following, p.items - 1));  // while dQ ends
             const int i = it.q0 + row;
             const bool exists = i < p.nq, valid = i < it.sp.Lq;
             __nv_bfloat16 *dst = p.dQ + it.batch * p.sdQ.b + it.head * p.sdQ.h + (int64_t)i * p.sdQ.n;
@@ -570,6 +627,7 @@ softmax_attn_dq_kernel(const __grid_constant__ CUtensorMap tQ, const __grid_cons
                 else zero_row(dst, p.d);
             }
             it = next;
+            idx = following;
         }
     }
     tc_fence_before();
@@ -626,6 +684,7 @@ __device__ __forceinline__ DkvItem dkv_item(const BwdParams &p, int idx) {
 struct DkvBarriers {
     uint64_t full[9], fixed[9], s_full[9], p_full[9], pv_done[9], dp_full[9], ds_full[9], ds_done[9];
     uint64_t kv_full[2], kv_free[2], acc_full, acc_free, fix_wanted, drain[3];
+    Queue queue;
     uint32_t tmem;
     int abort;
 };
@@ -667,6 +726,7 @@ softmax_attn_dkv_kernel(const __grid_constant__ CUtensorMap tQ, const __grid_con
         mbar_init(&bar->acc_full, 1);
         mbar_init(&bar->acc_free, 8);
         mbar_init(&bar->fix_wanted, 1);
+        init_queue(bar->queue, (p.q_lengths ? 31 : 0) + 3 + 4 * G);  // zeroing lanes, issuing threads, warps
         bar->abort = 0;
         fence_mbar_init();
     }
@@ -683,45 +743,50 @@ softmax_attn_dkv_kernel(const __grid_constant__ CUtensorMap tQ, const __grid_con
     setmaxnreg_dec<issue_regs(G)>();
     if (warp == kLoadWarp) {
         if (lane == 0) {
-            int ring = 0, items = 0;
+            int ring = 0, items = 0, t = 0;
             Ring<G, C::kStages> at;
             bool ok = true;
-            for (int idx = blockIdx.x; idx < p.items && ok; idx += gridDim.x) {
+            for (int idx = blockIdx.x; idx < p.items && ok;) {
+                const int following = gridDim.x + atomicAdd(p.queue + 1, 1);
                 const DkvItem it = dkv_item(p, idx);
-                if (it.hi <= it.lo) continue;
-                const int kb = items % C::kKv;
-                if (items >= C::kKv &&
-                    !thread_spin(&bar->kv_free[kb], (items / C::kKv - 1) & 1, p.status, 100, abort_flag))
-                    break;
-                uint8_t *kv = sK + kb * 2 * C::kTileBytes;
-                mbar_arrive_expect_tx(&bar->kv_full[kb], 2 * C::kTileBytes);
-                load_rows<DP, 2>(kv, &tK, &bar->kv_full[kb], it.k0, 0, it.kvh, it.batch);
-                load_rows<DP, 2>(kv + C::kTileBytes, &tV, &bar->kv_full[kb], it.k0, 0, it.kvh, it.batch);
-                ++items;
-                for (int g = 0; g < p.group && ok; ++g)
-                    for (int j = it.lo; j < it.hi; ++j, ++ring, at.next()) {
-                        const int s = at.pos;
-                        // (dK comes last: with it all products of a step have been formed)
-                        if (!thread_spin(&bar->ds_done[s], at.phase ^ 1, p.status, 101, abort_flag)) {
-                            ok = false;
-                            break;
+                if (it.hi > it.lo) {
+                    const int kb = items % C::kKv;
+                    if (items >= C::kKv &&
+                        !thread_spin(&bar->kv_free[kb], (items / C::kKv - 1) & 1, p.status, 100, abort_flag))
+                        break;
+                    uint8_t *kv = sK + kb * 2 * C::kTileBytes;
+                    mbar_arrive_expect_tx(&bar->kv_full[kb], 2 * C::kTileBytes);
+                    load_rows<DP, 2>(kv, &tK, &bar->kv_full[kb], it.k0, 0, it.kvh, it.batch);
+                    load_rows<DP, 2>(kv + C::kTileBytes, &tV, &bar->kv_full[kb], it.k0, 0, it.kvh, it.batch);
+                    ++items;
+                    for (int g = 0; g < p.group && ok; ++g)
+                        for (int j = it.lo; j < it.hi; ++j, ++ring, at.next()) {
+                            const int s = at.pos;
+                            // (dK comes last: with it all products of a step have been formed)
+                            if (!thread_spin(&bar->ds_done[s], at.phase ^ 1, p.status, 101, abort_flag)) {
+                                ok = false;
+                                break;
+                            }
+                            uint8_t *st = sT + s * 2 * C::kStepBytes;
+                            mbar_arrive_expect_tx(&bar->full[s], 2 * C::kStepBytes + 512);
+                            load_rows<DP, 1>(st, &tQ, &bar->full[s], j * kHalf, g, it.kvh, it.batch);
+                            load_rows<DP, 1>(st + C::kStepBytes, &tdO, &bar->full[s], j * kHalf, g, it.kvh, it.batch);
+                            const int64_t head = (int64_t)it.batch * p.hq + it.kvh * p.group + g;
+                            bulk_load(sR + s * 512, p.rows + (head * 2 * p.qtiles + j) * 128, 512, &bar->full[s]);
                         }
-                        uint8_t *st = sT + s * 2 * C::kStepBytes;
-                        mbar_arrive_expect_tx(&bar->full[s], 2 * C::kStepBytes + 512);
-                        load_rows<DP, 1>(st, &tQ, &bar->full[s], j * kHalf, g, it.kvh, it.batch);
-                        load_rows<DP, 1>(st + C::kStepBytes, &tdO, &bar->full[s], j * kHalf, g, it.kvh, it.batch);
-                        const int64_t head = (int64_t)it.batch * p.hq + it.kvh * p.group + g;
-                        bulk_load(sR + s * 512, p.rows + (head * 2 * p.qtiles + j) * 128, 512, &bar->full[s]);
-                    }
+                }
+                ok = ok && tell(bar->queue, t, following, p.status, abort_flag);
+                idx = following;
             }
             for (int i = max(0, items - C::kKv); i < items; ++i)
                 mbar_wait_drain(&bar->kv_full[i % C::kKv], (i / C::kKv) & 1);
             for (int i = max(0, ring - C::kStages); i < ring; ++i)
                 mbar_wait_drain(&bar->full[i % C::kStages], (i / C::kStages) & 1);
-        } else {  // Q and dO rows past the valid length: P and dS are 0 there, but 0 x NaN is not
+        } else if (p.q_lengths) {  // Q and dO rows past the valid length: P and dS are 0 there, but 0 x NaN is not
             int ring = 0, nfix = 0;
             bool ok = true;
-            for (int idx = blockIdx.x; idx < p.items && ok; idx += gridDim.x) {
+            for (int idx = blockIdx.x, t = 0; idx < p.items && ok;
+                 ok = ok && thread_next(bar->queue, t, idx, p.status, abort_flag)) {
                 const DkvItem it = dkv_item(p, idx);
                 if (it.hi <= it.lo) continue;
                 if (it.sp.Lq >= p.nq || it.hi * kHalf <= it.sp.Lq) {
@@ -756,7 +821,8 @@ softmax_attn_dkv_kernel(const __grid_constant__ CUtensorMap tQ, const __grid_con
                            slots = tmem + (first ? 0 : 64), loaded = smem_u32(bar->full),
                            done = smem_u32(first ? bar->pv_done : bar->ds_done),
                            out = smem_u32(first ? bar->s_full : bar->dp_full), fixed = smem_u32(bar->fixed);
-            for (int idx = blockIdx.x; idx < p.items && ok; idx += gridDim.x) {
+            for (int idx = blockIdx.x, t = 0; idx < p.items && ok;
+                 ok = ok && thread_next(bar->queue, t, idx, p.status, abort_flag)) {
                 const DkvItem it = dkv_item(p, idx);
                 const int per = it.hi - it.lo;
                 if (per <= 0) continue;
@@ -794,7 +860,8 @@ softmax_attn_dkv_kernel(const __grid_constant__ CUtensorMap tQ, const __grid_con
             bool ok = true;
             const uint32_t b = smem_u32(sT), p_full = smem_u32(bar->p_full), ds_full = smem_u32(bar->ds_full),
                            pv_done = smem_u32(bar->pv_done), ds_done = smem_u32(bar->ds_done);
-            for (int idx = blockIdx.x; idx < p.items && ok; idx += gridDim.x) {
+            for (int idx = blockIdx.x, t = 0; idx < p.items && ok;
+                 ok = ok && thread_next(bar->queue, t, idx, p.status, abort_flag)) {
                 const DkvItem it = dkv_item(p, idx);
                 const int steps = (it.hi - it.lo) * p.group;
                 if (steps <= 0) continue;
@@ -839,7 +906,7 @@ softmax_attn_dkv_kernel(const __grid_constant__ CUtensorMap tQ, const __grid_con
         uint32_t pos = w, phase = 0;  // in the ring; the warpgroup's steps are at w, w + G and so on
         bool ok = true;
         DkvItem it = dkv_item(p, min((int)blockIdx.x, p.items - 1));
-        for (int idx = blockIdx.x; idx < p.items && ok; idx += gridDim.x) {
+        for (int idx = blockIdx.x, t = 0; idx < p.items && ok;) {
             const int key = it.k0 + row, off = it.sp.Lk - it.sp.Lq, hi = it.hi, per = max(0, hi - it.lo),
                       steps = per * p.group;
             // queries [first, end) see this key (the rows past the length need no mask: their
@@ -917,7 +984,9 @@ softmax_attn_dkv_kernel(const __grid_constant__ CUtensorMap tQ, const __grid_con
                 if (pos >= C::kStages) pos = w, phase ^= 1u;
             }
             if (!ok) break;
-            const DkvItem next = dkv_item(p, min(idx + (int)gridDim.x, p.items - 1));  // while the sums end
+            int following = 0;
+            if (!warp_next(bar->queue, t, following, p.status, abort_flag)) break;
+            const DkvItem next = dkv_item(p, min(following, p.items - 1));  // while the sums end
             const bool exists = key < p.nk, valid = key < it.sp.Lk;
             // the first two warpgroups write dV and dK
             __nv_bfloat16 *dst =
@@ -945,6 +1014,7 @@ softmax_attn_dkv_kernel(const __grid_constant__ CUtensorMap tQ, const __grid_con
                 else zero_row(dst, p.d);
             }
             it = next;
+            idx = following;
         }
     }
     if (warp == kLoadWarp) wait_prerequisites();  // no later kernel before the second one has ended
@@ -1013,12 +1083,13 @@ int launch(const Call &c, BwdParams &p) {
     p.ksome = units_at_once(p.kblocks, c.b * c.hk, (int64_t)p.group * c.nq * c.d * 4, c.causal);
     const int64_t qrows = (int64_t)c.b * c.hq * c.nq, krows = (int64_t)c.b * c.hk * c.nk;
     const int64_t qparts = p.qsplit > 1 ? p.qsplit * qrows * DP : 0, kparts = p.ksplit > 1 ? p.ksplit * krows * DP : 0;
-    if (workspace_alloc(&ws, (size_t)(qitems * 256 + qparts + 2 * kparts) * sizeof(float), c.stream) != LINFORMER_OK)
+    if (workspace_alloc(&ws, (size_t)(qitems * 256 + qparts + 2 * kparts + 2) * sizeof(float), c.stream) != LINFORMER_OK)
         return LINFORMER_ERR_ALLOC;
     p.rows = static_cast<float *>(ws);
     p.part_q = p.rows + qitems * 256;
     p.part_k = p.part_q + qparts;
     p.part_v = p.part_k + kparts;
+    p.queue = reinterpret_cast<int *>(p.part_v + kparts);
     {
         KernelScope scope(LINFORMER_KERNEL_SOFTMAX_BWD, c.stream);
         rows_kernel<DP><<<(unsigned)qitems, kRowsThreads, 0, c.stream>>>(p);
