@@ -28,10 +28,10 @@
 // three issues S, dP and the sums, since such a thread takes about 300 cycles from one product
 // to the next (short code that runs now and then, fetched anew each time) and the tensor cores
 // would wait for a single one.
-// Measured (b h = 76, n = 4096, each launch alone): d = 64: rows 16 us (5.2 TB/s), dQ 395 us
-// (1.24 PFLOP/s of its three products, tensor pipe 54 %), dK and dV 485 us (1.35 PFLOP/s of four,
-// 59 %); d = 128: 30, 670 (1.46, 62 %) and 788 us (1.66, 71 %).  Back to back they draw the
-// board's full power and the clock settles at 1650 to 1950 MHz of 2070.
+// Measured (b h = 76, n = 4096, each launch alone): d = 64: rows 16 us (5.2 TB/s), dQ 373 us
+// (1.31 PFLOP/s of its three products), dK and dV 460 to 485 us (1.35 to 1.42 PFLOP/s of four,
+// tensor pipe 59 %); d = 128: 30, 664 (1.47, 62 %) and 788 us (1.66, 71 %).  Back to back they draw
+// the board's full power and the clock settles at 1650 to 1950 MHz of 2070.
 #include <algorithm>
 #include <cmath>
 
@@ -293,9 +293,12 @@ struct DqLayout {
     // slots, one of each warpgroup: S in 64 columns, dP in 64
     static constexpr int G = DP == 64 ? 3 : 2;
     static constexpr uint32_t kTileBytes = kTile * DP * 2, kStepBytes = kHalf * DP * 2;
-    static constexpr int kStages = DP == 64 ? 12 : 4;  // of a step's K and V
+    static constexpr int kStages = DP == 64 ? 9 : 4;  // of a step's K and V
+    // Items whose Q, dO and dQ are held: with two the next one starts while dQ of the last one is
+    // formed and written (384 heads of 512: 48 us against 58).  No room at DP = 128.
+    static constexpr int kItems = DP == 64 ? 2 : 1;
     static constexpr uint32_t kDq = 128 * G;
-    static constexpr uint32_t kSmem = 1024 + 2 * kTileBytes + kStages * 2 * kStepBytes + 1024 + 1024;
+    static constexpr uint32_t kSmem = 1024 + kItems * 2 * kTileBytes + kStages * 2 * kStepBytes + 3072;
 };
 // Part i of n of the steps [lo, hi).
 __device__ __forceinline__ void take_part(int &lo, int &hi, int i, int n) {
@@ -339,15 +342,15 @@ __device__ __forceinline__ DqItem dq_item(const BwdParams &p, int idx) {
 
 // Barriers of steps: one of each kind for every position of the ring.
 struct DqBarriers {
-    uint64_t k_full[12], v_full[12], s_full[12], s_free[12], dp_full[12], ds_full[12], dq_done[12];
-    uint64_t q_full, q_free, acc_full, acc_free, fix_wanted, fixed_k, fixed_v, drain[3];
+    uint64_t k_full[9], v_full[9], s_full[9], s_free[9], dp_full[9], ds_full[9], dq_done[9];
+    uint64_t q_full[2], q_free[2], acc_full[2], acc_free[2], fix_wanted, fixed_k, fixed_v, drain[3];
     Queue queue;
     uint32_t tmem;
     int abort;
-    alignas(16) float rows[2 * kTile];  // the item's rows, loaded with Q and dO
+    alignas(16) float rows[2][2 * kTile];  // an item's rows, loaded with its Q and dO
 };
 
-static_assert(sizeof(DqBarriers) <= 2048, "room for the barriers");
+static_assert(sizeof(DqBarriers) <= 3072, "room for the barriers");
 
 template <int DP>
 __global__ void __launch_bounds__(threads_of(DqLayout<DP>::G), 1)
@@ -358,14 +361,13 @@ softmax_attn_dq_kernel(const __grid_constant__ CUtensorMap tQ, const __grid_cons
     constexpr int G = C::G, kLoadWarp = 4 * G, kMmaWarp = 4 * G + 1;
     extern __shared__ uint8_t raw[];
     uint8_t *smem = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(raw) + 1023) & ~uintptr_t(1023));
-    uint8_t *sQ = smem, *sdO = smem + C::kTileBytes, *sKV = smem + 2 * C::kTileBytes;
+    // Q and dO of an item at smem + (item % kItems) 2 tiles
+    uint8_t *sQ = smem, *sdO = smem + C::kTileBytes, *sKV = smem + C::kItems * 2 * C::kTileBytes;
     DqBarriers *bar = reinterpret_cast<DqBarriers *>(sKV + C::kStages * 2 * C::kStepBytes);  // [K, V] a stage
     volatile int *abort_flag = &bar->abort;
     const int tid = threadIdx.x, warp = __shfl_sync(0xffffffffu, tid >> 5, 0), lane = tid & 31;
 
     if (tid == 0) {
-        mbar_init(&bar->q_full, 1);
-        mbar_init(&bar->q_free, 2 + 4 * G);  // the products, and the rows read
         for (int i = 0; i < C::kStages; ++i) {
             mbar_init(&bar->k_full[i], 1);
             mbar_init(&bar->v_full[i], 1);
@@ -375,8 +377,12 @@ softmax_attn_dq_kernel(const __grid_constant__ CUtensorMap tQ, const __grid_cons
             mbar_init(&bar->ds_full[i], 4);
             mbar_init(&bar->dq_done[i], 1);
         }
-        mbar_init(&bar->acc_full, 1);
-        mbar_init(&bar->acc_free, 8);
+        for (int i = 0; i < C::kItems; ++i) {
+            mbar_init(&bar->q_full[i], 1);
+            mbar_init(&bar->q_free[i], 2 + 4 * G);  // the products, and the rows read
+            mbar_init(&bar->acc_full[i], 1);
+            mbar_init(&bar->acc_free[i], 8);
+        }
         mbar_init(&bar->fix_wanted, 2);
         mbar_init(&bar->fixed_k, 31);
         mbar_init(&bar->fixed_v, 31);
@@ -406,13 +412,17 @@ softmax_attn_dq_kernel(const __grid_constant__ CUtensorMap tQ, const __grid_cons
                 const int following = gridDim.x + atomicAdd(p.queue, 1);
                 const DqItem it = dq_item(p, idx);
                 if (it.hi > it.lo) {
-                    if (nq > 0 && !thread_spin(&bar->q_free, (nq - 1) & 1, p.status, 83, abort_flag)) break;
-                    mbar_arrive_expect_tx(&bar->q_full, 2 * C::kTileBytes + 1024);
+                    const int qb = nq % C::kItems;
+                    if (nq >= C::kItems &&
+                        !thread_spin(&bar->q_free[qb], (nq / C::kItems - 1) & 1, p.status, 83, abort_flag))
+                        break;
+                    uint64_t *q_full = &bar->q_full[qb];
+                    mbar_arrive_expect_tx(q_full, 2 * C::kTileBytes + 1024);
                     const int g = it.head % p.group, kvh = it.head / p.group;
-                    bulk_load(bar->rows, p.rows + (((int64_t)it.batch * p.hq + it.head) * p.qtiles + it.q0 / kTile) * 256,
-                              1024, &bar->q_full);
-                    load_rows<DP, 2>(sQ, &tQ, &bar->q_full, it.q0, g, kvh, it.batch);
-                    load_rows<DP, 2>(sdO, &tdO, &bar->q_full, it.q0, g, kvh, it.batch);
+                    bulk_load(bar->rows[qb], p.rows + (((int64_t)it.batch * p.hq + it.head) * p.qtiles + it.q0 / kTile) * 256,
+                              1024, q_full);
+                    load_rows<DP, 2>(sQ + qb * 2 * C::kTileBytes, &tQ, q_full, it.q0, g, kvh, it.batch);
+                    load_rows<DP, 2>(sdO + qb * 2 * C::kTileBytes, &tdO, q_full, it.q0, g, kvh, it.batch);
                     ++nq;
                     for (int j = it.lo; j < it.hi; ++j, ++steps, at.next()) {
                         uint8_t *st = sKV + at.pos * 2 * C::kStepBytes;
@@ -428,7 +438,8 @@ softmax_attn_dq_kernel(const __grid_constant__ CUtensorMap tQ, const __grid_cons
                 ok = ok && tell(bar->queue, t, following, p.status, abort_flag);
                 idx = following;
             }
-            if (nq > 0) mbar_wait_drain(&bar->q_full, (nq - 1) & 1);
+            for (int i = max(0, nq - C::kItems); i < nq; ++i)
+                mbar_wait_drain(&bar->q_full[i % C::kItems], (i / C::kItems) & 1);
             for (int i = max(0, steps - C::kStages); i < steps; ++i) {
                 mbar_wait_drain(&bar->k_full[i % C::kStages], (i / C::kStages) & 1);
                 mbar_wait_drain(&bar->v_full[i % C::kStages], (i / C::kStages) & 1);
@@ -461,7 +472,7 @@ softmax_attn_dq_kernel(const __grid_constant__ CUtensorMap tQ, const __grid_cons
             uint32_t nfix = 0;
             Ring<G, C::kStages> at;
             bool ok = true;
-            const uint32_t a = smem_u32(first ? sQ : sdO), b = smem_u32(sKV) + (first ? 0 : C::kStepBytes),
+            const uint32_t a0 = smem_u32(first ? sQ : sdO), b = smem_u32(sKV) + (first ? 0 : C::kStepBytes),
                            slots = tmem + (first ? 0 : 64), loaded = smem_u32(first ? bar->k_full : bar->v_full),
                            free = smem_u32(first ? bar->s_free : bar->dq_done),
                            out = smem_u32(first ? bar->s_full : bar->dp_full),
@@ -472,7 +483,9 @@ softmax_attn_dq_kernel(const __grid_constant__ CUtensorMap tQ, const __grid_cons
                 const int steps = it.hi - it.lo;
                 if (steps <= 0) continue;
                 const bool fix = it.sp.Lk < p.nk && it.hi * kHalf > it.sp.Lk;
-                ok = thread_spin(&bar->q_full, items & 1, p.status, 91, abort_flag);
+                const int qb = items % C::kItems;
+                const uint32_t a = a0 + qb * 2 * C::kTileBytes;
+                ok = thread_spin(&bar->q_full[qb], (items / C::kItems) & 1, p.status, 91, abort_flag);
                 for (int j = steps; j > 0 && ok; --j, at.next()) {
                     ok = thread_spin(loaded + 8 * at.pos, at.phase, p.status, 86, abort_flag) &&
                          thread_spin(free + 8 * at.before(), at.phase_before(), p.status, 88, abort_flag);
@@ -485,7 +498,7 @@ softmax_attn_dq_kernel(const __grid_constant__ CUtensorMap tQ, const __grid_cons
                     mma_scores<DP>(slots + 128 * at.slot, a, b + at.pos * (2 * C::kStepBytes));
                     mma_commit(out + 8 * at.pos);
                 }
-                mma_commit(&bar->q_free);
+                mma_commit(&bar->q_free[qb]);
                 ++items;
             }
             mma_commit(&bar->drain[first ? 0 : 1]);
@@ -503,16 +516,19 @@ softmax_attn_dq_kernel(const __grid_constant__ CUtensorMap tQ, const __grid_cons
                 const DqItem it = dq_item(p, idx);
                 const int steps = it.hi - it.lo;
                 if (steps <= 0) continue;
-                if (items > 0) ok = thread_spin(&bar->acc_free, (items - 1) & 1, p.status, 93, abort_flag);
+                const int ab = items % C::kItems;
+                const uint32_t acc = tmem + C::kDq + ab * DP;
+                if (items >= C::kItems)
+                    ok = thread_spin(&bar->acc_free[ab], (items / C::kItems - 1) & 1, p.status, 93, abort_flag);
                 for (int j = 0; j < steps && ok; ++j, at.next()) {
                     // (dS says that S has been formed, so the block of K has landed)
                     ok = thread_spin(ready + 8 * at.pos, at.phase, p.status, 92, abort_flag);
                     if (!ok) break;
                     tc_fence_after();
-                    mma_sum<DP>(tmem + C::kDq, tmem + 128 * at.slot + 64, b + at.pos * (2 * C::kStepBytes), j > 0 ? 1u : 0u);
+                    mma_sum<DP>(acc, tmem + 128 * at.slot + 64, b + at.pos * (2 * C::kStepBytes), j > 0 ? 1u : 0u);
                     mma_commit(done + 8 * at.pos);
                 }
-                mma_commit(&bar->acc_full);
+                mma_commit(&bar->acc_full[ab]);
                 ++items;
             }
             mma_commit(&bar->drain[2]);
@@ -530,22 +546,53 @@ softmax_attn_dq_kernel(const __grid_constant__ CUtensorMap tQ, const __grid_cons
                        ds_full = smem_u32(bar->ds_full);
         int n = 0, items = 0;
         uint32_t pos = w, phase = 0;  // in the ring; the warpgroup's steps are at w, w + G and so on
+        // writes dQ of an item, the nth with steps
+        auto finish = [&](const DqItem &x, int nth) {
+            const int i = x.q0 + row;
+            const bool exists = i < p.nq, valid = i < x.sp.Lq;
+            __nv_bfloat16 *dst = p.dQ + x.batch * p.sdQ.b + x.head * p.sdQ.h + (int64_t)i * p.sdQ.n;
+            float *part = p.part_q + ((((int64_t)x.part * p.b + x.batch) * p.hq + x.head) * p.nq + i) * DP;
+            if (w < 2 && x.hi > x.lo) {  // half of the columns each
+                const int ab = (nth - 1) % C::kItems;
+                if (!warp_spin(&bar->acc_full[ab], ((nth - 1) / C::kItems) & 1, p.status, 96, abort_flag)) return false;
+                tc_fence_after();
+                uint32_t o[DP / 64][32];
+                load_columns(tmem + C::kDq + ab * DP + w * (DP / 2) + lanes, o);
+                tc_fence_before();
+                __syncwarp();
+                if (lane == 0) mbar_arrive(&bar->acc_free[ab]);
+                if (exists)
+#pragma unroll
+                    for (int c = 0; c < DP / 64; ++c) {
+                        const int at = w * (DP / 2) + 32 * c;
+                        if (p.qsplit > 1) store_part(part + at, o[c], !valid);
+                        else store_row(dst, o[c], at, p.d, p.scale, !valid, p.wide & 1);
+                    }
+            } else if (w == 0 && exists) {
+                if (p.qsplit > 1) zero_part(part, DP);
+                else zero_row(dst, p.d);
+            }
+            return true;
+        };
         DqItem it = dq_item(p, min((int)blockIdx.x, p.items - 1));
+        DqItem last = it;
+        int held = -1;
+        bool ok = true;
         for (int idx = blockIdx.x, t = 0; idx < p.items;) {
             const int steps = max(0, it.hi - it.lo);
             float nl = 0.f, nd = 0.f;
             if (steps) {  // the row values come with Q and dO
-                if (!warp_spin(&bar->q_full, items & 1, p.status, 97, abort_flag)) break;
-                nl = bar->rows[(row >> 6) * 128 + (row & 63)];
-                nd = bar->rows[(row >> 6) * 128 + 64 + (row & 63)];
+                const int qb = items % C::kItems;
+                if (!warp_spin(&bar->q_full[qb], (items / C::kItems) & 1, p.status, 97, abort_flag)) break;
+                nl = bar->rows[qb][(row >> 6) * 128 + (row & 63)];
+                nd = bar->rows[qb][(row >> 6) * 128 + 64 + (row & 63)];
                 __syncwarp();
-                if (lane == 0) mbar_arrive(&bar->q_free);
+                if (lane == 0) mbar_arrive(&bar->q_free[qb]);
                 ++items;
             }
             const bool seen = it.q0 + row < it.sp.Lq;
             const int first = seen ? it.sp.first(it.q0 + row) : 0, end = seen ? it.sp.end(it.q0 + row) : 0;
             const unsigned width = end > first ? (unsigned)(end - first) : 0u;
-            bool ok = true;
             const int skip = (w + G - n % G) % G;
             for (int j = skip; j < steps; j += G) {
                 if (!warp_spin(s_full + 8 * pos, phase, p.status, 94, abort_flag)) {
@@ -603,32 +650,17 @@ softmax_attn_dq_kernel(const __grid_constant__ CUtensorMap tQ, const __grid_cons
             int following = 0;
             if (!warp_next(bar->queue, t, following, p.status, abort_flag)) break;
             const DqItem next = dq_item(p, min(following, p.items - 1));  // while dQ ends
-            const int i = it.q0 + row;
-            const bool exists = i < p.nq, valid = i < it.sp.Lq;
-            __nv_bfloat16 *dst = p.dQ + it.batch * p.sdQ.b + it.head * p.sdQ.h + (int64_t)i * p.sdQ.n;
-            float *part = p.part_q + ((((int64_t)it.part * p.b + it.batch) * p.hq + it.head) * p.nq + i) * DP;
-            if (w < 2 && steps) {  // half of the columns each
-                if (!warp_spin(&bar->acc_full, (items - 1) & 1, p.status, 96, abort_flag)) break;
-                tc_fence_after();
-                uint32_t o[DP / 64][32];
-                load_columns(tmem + C::kDq + w * (DP / 2) + lanes, o);
-                tc_fence_before();
-                __syncwarp();
-                if (lane == 0) mbar_arrive(&bar->acc_free);
-                if (exists)
-#pragma unroll
-                    for (int c = 0; c < DP / 64; ++c) {
-                        const int at = w * (DP / 2) + 32 * c;
-                        if (p.qsplit > 1) store_part(part + at, o[c], !valid);
-                        else store_row(dst, o[c], at, p.d, p.scale, !valid, p.wide & 1);
-                    }
-            } else if (w == 0 && exists) {
-                if (p.qsplit > 1) zero_part(part, DP);
-                else zero_row(dst, p.d);
-            }
+            // with two items held, the last one's dQ is written after this one's steps: its
+            // sums have ended by then
+            if (C::kItems == 1) ok = finish(it, items);
+            else if (held >= 0) ok = finish(last, held);
+            if (!ok) break;
+            last = it;
+            held = items;
             it = next;
             idx = following;
         }
+        if (C::kItems > 1 && ok && held >= 0) finish(last, held);
     }
     tc_fence_before();
     __syncthreads();
