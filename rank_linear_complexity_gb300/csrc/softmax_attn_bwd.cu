@@ -298,7 +298,7 @@ struct DqLayout {
     // formed and written (384 heads of 512: 48 us against 58).  No room at DP = 128.
     static constexpr int kItems = DP == 64 ? 2 : 1;
     static constexpr uint32_t kDq = 128 * G;
-    static constexpr uint32_t kSmem = 1024 + kItems * 2 * kTileBytes + kStages * 2 * kStepBytes + 3072;
+    static constexpr uint32_t kSmem = 1024 + kItems * 2 * kTileBytes + kStages * 2 * kStepBytes + 2048 + 1024;
 };
 // Part i of n of the steps [lo, hi).
 __device__ __forceinline__ void take_part(int &lo, int &hi, int i, int n) {
@@ -350,7 +350,7 @@ struct DqBarriers {
     alignas(16) float rows[2][2 * kTile];  // an item's rows, loaded with its Q and dO
 };
 
-static_assert(sizeof(DqBarriers) <= 3072, "room for the barriers");
+static_assert(sizeof(DqBarriers) <= 2048 + 1024, "room for the barriers");
 
 template <int DP>
 __global__ void __launch_bounds__(threads_of(DqLayout<DP>::G), 1)
