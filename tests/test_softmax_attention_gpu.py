@@ -144,6 +144,8 @@ MORE = {  # steps of 64: heads of one step, lengths that end in a step or on its
     "few_keys_causal": (1, 8, 1, 1100, 200, 64, dict(causal=True, q=[1090], k=[170])),
     "few_queries": (1, 4, 2, 40, 5000, 64, dict(k=[4990])),
     "few_queries_window": (2, 2, 1, 300, 5000, 128, dict(causal=True, window=3500, q=[300, 7], k=[5000, 200])),
+    "few_keys_none": (3, 8, 2, 700, 40, 64, dict(q=[700, 0, 1], k=[0, 40, 40])),
+    "few_queries_none": (3, 2, 1, 30, 4500, 64, dict(causal=True, q=[0, 30, 29], k=[4500, 0, 4437])),
     "long_ring_of_queries": (1, 12, 1, 700, 70, 64, dict(q=[650])),
 }
 
