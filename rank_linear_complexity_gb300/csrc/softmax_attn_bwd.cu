@@ -37,6 +37,7 @@
 
 #include "softmax_attn.cuh"
 #include "sm100_ptx.cuh"
+#include "work_queue.cuh"
 
 namespace linformer {
 namespace sattn {
@@ -199,49 +200,6 @@ struct Ring {
         if (pos == N) pos = 0, phase ^= 1u;
     }
 };
-
-// ---------------------------------------------------------------- work items
-// A CTA begins with the item of its number; the loading thread takes each further one from a
-// counter and tells the other roles, two items ahead at most.  (Items differ in length, under a
-// causal mask and with ragged lengths.  Taken in turn instead, item i by CTA i modulo the CTAs: 32
-// causal heads over 8 of 8191 1424 us against 1353, 32 ragged entries of 12 heads of 512 120
-// against 115.)
-struct Queue {
-    uint64_t full[2], free[2];
-    int next[2];
-};
-__device__ __forceinline__ void init_queue(Queue &q, int readers) {
-    for (int i = 0; i < 2; ++i) {
-        mbar_init(&q.full[i], 1);
-        mbar_init(&q.free[i], readers);
-    }
-}
-__device__ __forceinline__ bool tell(Queue &q, int &t, int idx, int *status, volatile int *abort) {
-    const int s = t & 1;
-    if (!thread_spin(&q.free[s], ((t >> 1) & 1) ^ 1, status, 81, abort)) return false;
-    *(volatile int *)&q.next[s] = idx;
-    mbar_arrive(&q.full[s]);
-    ++t;
-    return true;
-}
-// A single thread's next item, and a warp's.
-__device__ __forceinline__ bool thread_next(Queue &q, int &t, int &idx, int *status, volatile int *abort) {
-    const int s = t & 1;
-    if (!thread_spin(&q.full[s], (t >> 1) & 1, status, 82, abort)) return false;
-    idx = *(volatile int *)&q.next[s];
-    mbar_arrive(&q.free[s]);
-    ++t;
-    return true;
-}
-__device__ __forceinline__ bool warp_next(Queue &q, int &t, int &idx, int *status, volatile int *abort) {
-    const int s = t & 1;
-    if (!warp_spin(&q.full[s], (t >> 1) & 1, status, 82, abort)) return false;
-    idx = *(volatile int *)&q.next[s];
-    __syncwarp();
-    if ((threadIdx.x & 31) == 0) mbar_arrive(&q.free[s]);
-    ++t;
-    return true;
-}
 
 // ---------------------------------------------------------------- row values
 // -lse log2(e) and -delta = -dO.O of a query tile's 128 rows, eight warps of sixteen rows; a row
@@ -1101,8 +1059,8 @@ int launch(const Call &c, BwdParams &p) {
         !encode_rows(&tK, c.K, c.sK, c.b, c.hk, 1, c.nk, c.d, kHalf, 1) ||
         !encode_rows(&tV, c.V, c.sV, c.b, c.hk, 1, c.nk, c.d, kHalf, 1))
         return LINFORMER_ERR_LAUNCH;
-    int st = allow_smem(reinterpret_cast<const void *>(softmax_attn_dq_kernel<DP>), Cq::kSmem, DP == 64 ? 2 : 3);
-    if (!st) st = allow_smem(reinterpret_cast<const void *>(softmax_attn_dkv_kernel<DP>), Ck::kSmem, DP == 64 ? 4 : 5);
+    int st = allow_smem(reinterpret_cast<const void *>(softmax_attn_dq_kernel<DP>), Cq::kSmem, DP == 64 ? 0 : 1);
+    if (!st) st = allow_smem(reinterpret_cast<const void *>(softmax_attn_dkv_kernel<DP>), Ck::kSmem, DP == 64 ? 2 : 3);
     if (st) return st;
     void *ws = nullptr;
     const int64_t qitems = (int64_t)c.b * c.hq * p.qtiles, kitems = (int64_t)c.b * c.hk * p.kblocks;

@@ -40,6 +40,7 @@
 
 #include "softmax_attn.cuh"
 #include "sm100_ptx.cuh"
+#include "work_queue.cuh"
 
 namespace linformer {
 namespace sattn {
@@ -63,12 +64,16 @@ struct FwdParams {
     float *lse;
     float *part_o, *part_lse;  // with splits: [split][b][hq][nq][DP] and [split][b][hq][nq]
     int b, hq, hk, group, nq, nk, d, causal, window;
-    int qbox, hbox, nch, ntiles, npairs, nsplit, units, some;
+    int qbox, hbox, nch, ntiles, npairs, nsplit, units, some, order;
     int items;
     float scale, scale_log2;
     int wide;  // O takes 32-byte stores
+    int *queue;  // items taken so far beyond each CTA's first
     int *status;
 };
+
+// How a CTA comes by its items: in turn, in turn and in sets of heads, from a counter.
+enum { kInTurn, kInSets, kFromQueue };
 
 template <int DP>
 struct Layout {
@@ -160,9 +165,12 @@ struct Barriers {
     uint64_t q_full[2], q_free[2], s_full[2], s_free[2], p_full[2], p_half[2], pv_done[2], o_free[2];
     uint64_t fix_wanted, fixed, drain[2];
     uint64_t full[10], empty[10];
+    Queue queue;
     uint32_t tmem;
     int abort;
 };
+
+static_assert(sizeof(Barriers) <= 512, "room for the barriers");
 
 // 2^(s sl + off) of 32 scores, summed and packed.
 __device__ __forceinline__ void exp_chunk(const uint32_t (&v)[32], uint32_t (&o)[16], float sl, float off,
@@ -217,11 +225,12 @@ __device__ __forceinline__ float max_chunk(const uint32_t (&v)[32]) {
     return fmaxf(max3(m0, __uint_as_float(v[30]), __uint_as_float(v[31])), m1);
 }
 
-template <int DP, bool kSets>
+template <int DP, int kOrder>
 __global__ void __launch_bounds__(kThreads, 1)
 softmax_attn_fwd_kernel(const __grid_constant__ CUtensorMap tQ, const __grid_constant__ CUtensorMap tK,
                         const __grid_constant__ CUtensorMap tV, const FwdParams p) {
     using C = Layout<DP>;
+    constexpr bool kSets = kOrder == kInSets, kQueue = kOrder == kFromQueue;
     extern __shared__ uint8_t raw[];
     uint8_t *smem = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(raw) + 1023) & ~uintptr_t(1023));
     uint8_t *sQ = smem, *sKV = smem + 2 * C::kTileBytes;
@@ -248,6 +257,7 @@ softmax_attn_fwd_kernel(const __grid_constant__ CUtensorMap tQ, const __grid_con
             mbar_init(&bar->full[s], 1);
             mbar_init(&bar->empty[s], 2);  // one arrival from each tile's products
         }
+        if (kQueue) init_queue(bar->queue, 31 + 2 + 8);  // zeroing lanes, issuing threads, warps
         bar->abort = 0;
         fence_mbar_init();
         prefetch_tmap(&tQ);
@@ -262,15 +272,23 @@ softmax_attn_fwd_kernel(const __grid_constant__ CUtensorMap tQ, const __grid_con
     __syncthreads();
     tc_fence_after();
     const uint32_t tmem = bar->tmem;
+    // a single thread's next item
+    auto advance = [&](int &idx, int &turn) {
+        if (kQueue) return thread_next(bar->queue, turn, idx, p.status, abort_flag);
+        idx += gridDim.x;
+        return true;
+    };
     if (p.nsplit > 1 && tid == 0) launch_dependents();  // the join, which waits for this grid's end
 
     if (warp >= kLoadWarp) {
     setmaxnreg_dec<kIssueRegs>();
     if (warp == kLoadWarp) {
         if (lane == 0) {  // ---------------- loads
-            int ring = 0, nq[2] = {0, 0};
+            if (kQueue) wait_prerequisites();  // the counter
+            int ring = 0, nq[2] = {0, 0}, turn = 0;
             bool ok = true;
-            for (int idx = blockIdx.x; idx < p.items && ok; idx += gridDim.x) {
+            for (int idx = blockIdx.x; idx < p.items && ok;) {
+                const int following = gridDim.x + (kQueue ? atomicAdd(p.queue, 1) : idx);
                 const Item it = load_item<kSets>(p, idx);
                 for (int t = 0; t < 2 && ok; ++t) {
                     if (it.t[t].hi <= it.t[t].lo) continue;
@@ -297,6 +315,8 @@ softmax_attn_fwd_kernel(const __grid_constant__ CUtensorMap tQ, const __grid_con
                             tma_load_5d(sKV + s * C::kTileBytes + h * 16384, kv ? &tV : &tK, &bar->full[s],
                                         h * 64, j * kTile, 0, it.kvh, it.batch);
                     }
+                if (kQueue) ok = ok && tell(bar->queue, turn, following, p.status, abort_flag);
+                idx = following;
             }
             // no copy outlives the CTA
             for (int t = 0; t < 2; ++t)
@@ -305,7 +325,8 @@ softmax_attn_fwd_kernel(const __grid_constant__ CUtensorMap tQ, const __grid_con
                 mbar_wait_drain(&bar->full[i % C::kStages], (i / C::kStages) & 1);
         } else {  // ---------------- V rows past the valid length
             int ring = 0, nfix = 0;
-            for (int idx = blockIdx.x; idx < p.items; idx += gridDim.x) {
+            bool ok = true;
+            for (int idx = blockIdx.x, turn = 0; idx < p.items && ok; ok = advance(idx, turn)) {
                 const Item it = load_item<kSets>(p, idx);
                 const int blocks = max(0, it.hi - it.lo);
                 ring += 2 * blocks;
@@ -345,7 +366,7 @@ softmax_attn_fwd_kernel(const __grid_constant__ CUtensorMap tQ, const __grid_con
                            dv0 = sdesc(smem_u32(sKV) + C::kTileBytes, 16384, 1024, kSwizzle128B);
             int nfix = 0, n = 0, items = 0;  // fixed blocks, the tile's blocks and items
             bool ok = true;
-            for (int idx = blockIdx.x; idx < p.items && ok; idx += gridDim.x) {
+            for (int idx = blockIdx.x, turn = 0; idx < p.items && ok; ok = ok && advance(idx, turn)) {
                 const Item it = load_item<kSets>(p, idx);
                 const int lo = t ? it.t[1].lo : it.t[0].lo, hi = t ? it.t[1].hi : it.t[0].hi;
                 const bool fix = ragged_end(it, p.nk);
@@ -464,10 +485,17 @@ softmax_attn_fwd_kernel(const __grid_constant__ CUtensorMap tQ, const __grid_con
             return r;
         };
         Row next = row_of(blockIdx.x);
-        for (int idx = blockIdx.x; idx < p.items && ok; idx += gridDim.x) {
+        // a warp's next item
+        auto following = [&](int idx, int &turn) {
+            if (kQueue) ok = warp_next(bar->queue, turn, idx, p.status, abort_flag);
+            else idx += gridDim.x;
+            return idx;
+        };
+        for (int idx = blockIdx.x, turn = 0; idx < p.items && ok;) {
             const Row now = next;
             if (!now.live) {
-                next = row_of(idx + gridDim.x);
+                idx = following(idx, turn);
+                next = row_of(idx);
                 continue;
             }
             const int lo = now.lo, hi = now.hi, first = now.first, end = now.end;
@@ -559,7 +587,9 @@ rescale_output(tO, DP, f);
             const Tile x = t ? it.t[1] : it.t[0];
             const int i = x.q0 + qi, hg = x.h0 + hi_;
             const bool exists = hi_ < p.hbox && hg < p.group && i < p.nq;
-            next = row_of(idx + gridDim.x);
+            idx = following(idx, turn);
+            if (!ok) break;
+            next = row_of(idx);
             const bool dead = !valid || l == 0.f;
             const float inv = dead ? 0.f : 1.f / l;
             const float lse = dead ? -INFINITY : m * p.scale + logf(l);
@@ -665,6 +695,11 @@ std::once_flag g_encode_once;
 constexpr int kMaxDev = 64;
 std::atomic<int> g_sms[kMaxDev] = {};
 
+__global__ void zero_queue_kernel(int *queue) {
+    launch_dependents();
+    *queue = 0;
+}
+
 template <int DP>
 int launch(const Call &c, FwdParams &p) {
     using C = Layout<DP>;
@@ -674,34 +709,48 @@ int launch(const Call &c, FwdParams &p) {
         !encode_rows(&tV, c.V, c.sV, c.b, c.hk, 1, c.nk, c.d, kTile, 1))
         return LINFORMER_ERR_LAUNCH;
     char *ws = nullptr;
-    if (p.nsplit > 1) {
-        const size_t rows = (size_t)c.b * c.hq * c.nq * p.nsplit;
-        if (workspace_alloc(reinterpret_cast<void **>(&ws), rows * (DP + 1) * sizeof(float), c.stream) !=
+    const size_t parts = p.nsplit > 1 ? (size_t)c.b * c.hq * c.nq * p.nsplit : 0;
+    const bool queue = p.order == kFromQueue;
+    if ((parts || queue) &&
+        workspace_alloc(reinterpret_cast<void **>(&ws), (parts * (DP + 1) + (queue ? 1 : 0)) * sizeof(float), c.stream) !=
             LINFORMER_OK)
-            return LINFORMER_ERR_ALLOC;
-        p.part_o = reinterpret_cast<float *>(ws);
-        p.part_lse = p.part_o + rows * DP;
+        return LINFORMER_ERR_ALLOC;
+    p.part_o = reinterpret_cast<float *>(ws);
+    p.part_lse = p.part_o + parts * DP;
+    p.queue = reinterpret_cast<int *>(p.part_lse + parts);
+    const auto kernel = queue ? softmax_attn_fwd_kernel<DP, kFromQueue>
+                        : p.order == kInSets ? softmax_attn_fwd_kernel<DP, kInSets>
+                                             : softmax_attn_fwd_kernel<DP, kInTurn>;
+    int st = allow_smem(reinterpret_cast<const void *>(kernel), C::kSmem, (DP == 64 ? 4 : 7) + p.order);
+    cudaLaunchConfig_t cfg{};
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    cfg.stream = c.stream;
+    cfg.attrs = attr;
+    if (!st && queue) {
+        KernelScope scope(LINFORMER_KERNEL_SOFTMAX, c.stream);
+        zero_queue_kernel<<<1, 1, 0, c.stream>>>(p.queue);
+        if (cudaGetLastError() != cudaSuccess) st = LINFORMER_ERR_LAUNCH;
     }
-    const auto kernel = p.some < p.units ? softmax_attn_fwd_kernel<DP, true> : softmax_attn_fwd_kernel<DP, false>;
-    int st = allow_smem(reinterpret_cast<const void *>(kernel), C::kSmem, (DP == 64 ? 0 : 1) + (p.some < p.units ? 6 : 0));
     if (!st) {
         KernelScope scope(LINFORMER_KERNEL_SOFTMAX, c.stream);
-        const int grid = (int)std::min(p.items, device_sms());
-        kernel<<<grid, kThreads, C::kSmem, c.stream>>>(tQ, tK, tV, p);
-        if (cudaGetLastError() != cudaSuccess) st = LINFORMER_ERR_LAUNCH;
+        cfg.gridDim = dim3((unsigned)std::min(p.items, device_sms()));
+        cfg.blockDim = dim3(kThreads);
+        cfg.dynamicSmemBytes = C::kSmem;
+        cfg.numAttrs = queue ? 1 : 0;  // set up beside the kernel that zeroes the counter
+        if (cudaLaunchKernelEx(&cfg, kernel, tQ, tK, tV, p) != cudaSuccess) {
+            cudaGetLastError();
+            st = LINFORMER_ERR_LAUNCH;
+        }
     }
     if (!st && p.nsplit > 1) {
         KernelScope scope(LINFORMER_KERNEL_SOFTMAX, c.stream);
         const int64_t rows = (int64_t)c.b * c.hq * c.nq;
         // set up while the parts are computed; it waits for them before it reads
-        cudaLaunchConfig_t cfg{};
-        cudaLaunchAttribute attr[1];
-        attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-        attr[0].val.programmaticStreamSerializationAllowed = 1;
         cfg.gridDim = dim3((unsigned)((rows + 3) / 4));
         cfg.blockDim = dim3(128);
-        cfg.stream = c.stream;
-        cfg.attrs = attr;
+        cfg.dynamicSmemBytes = 0;
         cfg.numAttrs = 1;
         if (cudaLaunchKernelEx(&cfg, join_kernel<DP>, p) != cudaSuccess) {
             cudaGetLastError();
@@ -752,7 +801,7 @@ int device_sms() {
 
 // The kernel's shared memory, allowed once per device (slot: one per kernel).
 int allow_smem(const void *kernel, uint32_t bytes, int slot) {
-    static std::atomic<uint8_t> done[kMaxDev][8];
+    static std::atomic<uint8_t> done[kMaxDev][10];
     int dev = 0;
     cudaGetDevice(&dev);
     if (dev >= 0 && dev < kMaxDev && done[dev][slot].load(std::memory_order_acquire)) return LINFORMER_OK;
@@ -807,6 +856,7 @@ int forward(const Call &c) {
     p.nsplit = blocks < kFirst ? 1 : (int)std::max<int64_t>(1, std::min<int64_t>(wanted, blocks / kMinBlocks));
     p.items = (int)whole * p.nsplit;
     p.some = units_at_once(p.npairs, p.units, (int64_t)c.nk * c.d * 4, c.causal);
+    p.order = p.some < p.units ? kInSets : p.items > 2 * sms && (c.k_lengths || c.q_lengths || c.causal) ? kFromQueue : kInTurn;
     return c.d <= 64 ? launch<64>(c, p) : launch<128>(c, p);
 }
 
