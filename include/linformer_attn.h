@@ -256,7 +256,7 @@ LINFORMER_API int linformer_dense_attn_fwd(const void *Q, const void *K, const v
  * all heads (else LINFORMER_ERR_SIZE).  Pointers are
  * 16-byte aligned (lse and the lengths: 4) and strides multiples of 8.  A few query rows
  * (single tokens over a cache) are served by splitting the keys over the GPU; the parts are
- * joined in a stream-ordered workspace.  The result of a call does not depend on timing.
+ * joined in a stream-ordered workspace; long calls with masks or lengths keep a counter there.  The result of a call does not depend on timing.
  */
 LINFORMER_API int linformer_softmax_attn_fwd(
     const void *Q, const int64_t *Q_strides, const void *K, const int64_t *K_strides,

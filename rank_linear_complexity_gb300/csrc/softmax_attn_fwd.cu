@@ -29,7 +29,7 @@
 //
 // Bound by the chain product -> exponentials -> product and, back to back, by the board's
 // power: b h = 192, n = 4096, d = 64: 740 us, 1.11 PFLOP/s (special-function unit and tensor pipe
-// 50 % busy each); 64 causal heads of 8192, d = 128: 877 us, 1.25 PFLOP/s (tensor pipe 57 %).  One
+// 50 % busy each); 64 causal heads of 8192, d = 128: 782 us, 1.40 PFLOP/s.  One
 // token over 8192 keys, d = 128: bound by memory, 82 % of its peak (keys split six ways an SM).
 #include <cudaTypedefs.h>
 

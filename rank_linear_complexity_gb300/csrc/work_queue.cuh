@@ -13,8 +13,8 @@ using namespace ptx;
 // not change its result.  (Items differ in length, under a causal mask and with ragged
 // lengths.  Taken in turn instead, item i by CTA i modulo the CTAs: backward of 32 causal heads
 // over 8 of 8191 1424 us against 1353, of 32 ragged entries of 12 heads of 512 120 against 115;
-// forward of 64 causal heads of 8192 887 and 824, with a window of 2048 246 and 229, one token
-// over 8192 ragged keys 147 and 139.)
+// forward of 64 causal heads of 8192 887 and 782 to 824, with a window of 2048 246 and 226, one
+// token over 8192 ragged keys 147 and 139.)
 struct Queue {
     uint64_t full[2], free[2];
     int next[2];

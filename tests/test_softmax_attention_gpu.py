@@ -194,6 +194,24 @@ def test_heads_in_sets(nq, nk, causal):
     assert same(whole, [torch.cat(x) for x in zip(*halves)])
 
 
+def test_wide_heads_in_sets_from_the_counter():
+    """The same for heads of 128 under a causal mask with ragged lengths, twice."""
+    b, h, n, d = 9, 16, 2048, 128
+    g = torch.Generator(device=DEV).manual_seed(128)
+    x = [torch.randn(b, h, n, d, generator=g, device=DEV).to(BF) for _ in range(4)]
+    x += [torch.randint(1, n + 1, (b,), generator=g, device=DEV, dtype=torch.int32) for _ in range(2)]
+
+    def run(at):
+        Q, K, V, dO, q, k = (t[at].contiguous() for t in x)
+        O, lse = lf.softmax_attention(Q, K, V, q, k, causal=True)
+        return (O, lse, *lf.softmax_attention_backward(Q, K, V, O, dO, lse, q, k, causal=True))
+
+    halves = [run(slice(0, 4)), run(slice(4, b))]
+    for _ in range(2):
+        assert same(run(slice(0, b)), [torch.cat(t) for t in zip(*halves)])
+    status()
+
+
 def test_outputs_only_where_they_belong():
     """Slices of wider buffers (rows, heads, columns around them untouched), lse in a longer one."""
     b, hq, hk, n, d = 2, 4, 2, 150, 64
