@@ -320,6 +320,10 @@ def dense_attention(Q, K, V, lengths=None, out=None, stream=None):
 # Calls of a few microseconds, so these marshal with care: no closures, strides by value from a
 # small table, the current stream from the binding that torch.cuda.current_stream() wraps
 # (1 us instead of 6), one comparison of shapes where one says it all.
+#
+# The calls return once launched.  A wait inside a kernel that ran out (2 s) leaves rows of the
+# outputs unwritten and is recorded in the device status word: linformer_debug_read_device_status()
+# synchronises, reads and clears it.
 
 _stride_table = {}  # (batch, head, row) strides -> int64[3]
 
