@@ -324,6 +324,10 @@ def dense_attention(Q, K, V, lengths=None, out=None, stream=None):
 # The calls return once launched.  A wait inside a kernel that ran out (2 s) leaves rows of the
 # outputs unwritten and is recorded in the device status word: linformer_debug_read_device_status()
 # synchronises, reads and clears it.
+#
+# A call given a stream (an object or a handle) runs with that stream as the current one: tensors
+# that it makes belong to the stream, as those of any torch operation would.  Its inputs have to be
+# ready there, and kept until the stream has read them.
 
 _stride_table = {}  # (batch, head, row) strides -> int64[3]
 
@@ -343,17 +347,31 @@ def _strides(x):
     return arr
 
 
-def _stream_of(device, stream, *tensors):
-    """The stream handle, after a check that the tensors (None: not given) are on `device`."""
+def _current_on(device, stream):
+    """Context that makes `stream` the current one."""
+    import torch
+    if device.type != "cuda":
+        raise ValueError(f"CUDA tensors are needed, got {device}")
+    if not isinstance(stream, torch.cuda.Stream):
+        handle = _stream_handle(stream)
+        # (0 and 1 are the default stream's handles, under its own name in torch)
+        stream = (torch.cuda.default_stream(device) if handle in (0, 1)
+                  else torch.cuda.ExternalStream(handle, device))
+    if device.index is not None and stream.device != device:
+        raise ValueError(f"a stream of {stream.device} for tensors on {device}")
+    return torch.cuda.stream(stream)
+
+
+def _stream_of(device, *tensors):
+    """The current stream's handle, after a check that the tensors (None: not given) are on
+    `device`."""
     if device.type != "cuda":
         raise ValueError(f"CUDA tensors are needed, got {device}")
     for t in tensors:
         if t is not None and t.device != device:
             raise ValueError(f"tensors on {device} and {t.device}")
-    if stream is None:
-        import torch
-        return torch._C._cuda_getCurrentRawStream(device.index)
-    return _stream_handle(stream)
+    import torch
+    return torch._C._cuda_getCurrentRawStream(device.index)
 
 
 def _call(fn, device, args, name):
@@ -395,10 +413,13 @@ def softmax_attention(Q, K, V, q_lengths=None, k_lengths=None, causal: bool = Fa
     causal: the valid parts end together (the last query sees every key), with window > 0
     only the last `window` keys up to its own.  scale defaults to 1 / sqrt(d)."""
     import torch
+    if stream is not None:
+        with _current_on(Q.device, stream):
+            return softmax_attention(Q, K, V, q_lengths, k_lengths, causal, window, scale, out, lse)
     shape, kv, dtype, device = Q.shape, K.shape, Q.dtype, Q.device
     b, hq, n, d = shape
     _, hk, m, _ = kv
-    handle = _stream_of(device, stream, K, V, q_lengths, k_lengths, out, lse)
+    handle = _stream_of(device, K, V, q_lengths, k_lengths, out, lse)
     if kv[0] != b or kv[3] != d or K.dtype != dtype:
         _check("K", K, (b, hk, m, d), dtype)
     _check("V", V, kv, dtype)
@@ -430,10 +451,14 @@ def softmax_attention_backward(Q, K, V, O, dO, lse, q_lengths=None, k_lengths=No
                                dK=None, dV=None, stream=None):
     """(dQ, dK, dV) from the inputs and results of softmax_attention and dO = dLoss/dO."""
     import torch
+    if stream is not None:
+        with _current_on(Q.device, stream):
+            return softmax_attention_backward(Q, K, V, O, dO, lse, q_lengths, k_lengths, causal,
+                                              window, scale, dQ, dK, dV)
     shape, kv, dtype, device = Q.shape, K.shape, Q.dtype, Q.device
     b, hq, n, d = shape
     _, hk, m, _ = kv
-    handle = _stream_of(device, stream, K, V, O, dO, lse, q_lengths, k_lengths, dQ, dK, dV)
+    handle = _stream_of(device, K, V, O, dO, lse, q_lengths, k_lengths, dQ, dK, dV)
     if kv[0] != b or kv[3] != d or K.dtype != dtype:
         _check("K", K, (b, hk, m, d), dtype)
     _check("V", V, kv, dtype)
@@ -473,8 +498,12 @@ def rotary_phase(rot: int, base: float = 10000.0, scaling: int = ROTARY_PLAIN,
                  beta_slow: float = 1.0, device="cuda", stream=None):
     """The table of `rot / 2` frequencies that rotary() takes (int64, made once and kept)."""
     import torch
+    if stream is not None:
+        with _current_on(torch.device(device), stream):
+            return rotary_phase(rot, base, scaling, factor, original_length, beta_fast, beta_slow,
+                                device)
     phase = torch.empty(max(rot // 2, 1), dtype=torch.int64, device=device)
-    handle = _stream_of(phase.device, stream)
+    handle = _stream_of(phase.device)
     _call(lib().linformer_rotary_phase, phase.device,
           (phase.data_ptr(), rot, base, scaling, factor, original_length, beta_fast, beta_slow, handle),
           "linformer_rotary_phase")
@@ -489,11 +518,14 @@ def rotary(x, x2=None, phase=None, positions=None, start: int = 0, rot=None,
     positions int32 [b][n], or None for start + row; rot defaults to d.  inverse=True maps
     gradients of the results to gradients of the inputs.  out may be x (in place)."""
     import torch
+    if stream is not None:
+        with _current_on(x.device, stream):
+            return rotary(x, x2, phase, positions, start, rot, layout, amplitude, inverse, out, out2)
     shape, dtype, device = x.shape, x.dtype, x.device
     b, h, n, d = shape
     if rot is None:
         rot = d
-    handle = _stream_of(device, stream, x2, phase, positions, out, out2)
+    handle = _stream_of(device, x2, phase, positions, out, out2)
     if phase is None:
         raise ValueError("phase: the table of rotary_phase() is needed")
     _check_dense("phase", phase, (rot // 2,), torch.int64)
