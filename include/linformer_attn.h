@@ -247,7 +247,8 @@ LINFORMER_API int linformer_dense_attn_fwd(const void *Q, const void *K, const v
  * own position, with window > 0 only the last `window` of them (itself included).  A row
  * that sees no key, and rows i >= Lq, get O = 0 and lse = -infinity; rows of Q, K and V
  * past the lengths may hold anything.  Rows within the lengths have to be finite, also
- * those that a causal mask hides.
+ * those that a causal mask hides (0 x NaN would reach a sum).  Sums are fp32, in range while
+ * |V| < 2^112 / nk and the terms of Q_i.K_j, also times scale log2(e), add up to less than 2^127.
  *
  * Q, O: [b][hq][nq][d]; K, V: [b][hk][nk][d], hq a multiple of hk; lse: dense fp32
  * [b][hq][nq].  dtype LINFORMER_BF16 (else LINFORMER_ERR_UNSUPPORTED), d a multiple of 8 up
