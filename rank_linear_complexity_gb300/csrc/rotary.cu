@@ -9,7 +9,7 @@
 // exact as that of position 1, without 64-bit floating point.
 //
 // Bound by memory: every element read and written once (bf16, 4 x 16384 rows of 32 heads of 64:
-// 94 us, 5.7 TB/s; sines shared by a block in shared memory instead: 123 us, the barrier and
+// 95 us, 5.7 TB/s; sines shared by a block in shared memory instead: 123 us, the barrier and
 // the second phase cost more than the sines).  A thread keeps the 8 (bf16) or 4
 // (fp32) sines and cosines of its pairs in registers and goes through several heads of both
 // tensors with them, 16-byte pieces at a time.
@@ -80,10 +80,13 @@ __global__ void __launch_bounds__(kThreads) rotary_kernel(const Params p) {
         for (int v = 0; v < V; ++v) {
             const uint64_t turns = __ldg(p.phase + V * c + v) * (uint64_t)(int64_t)pos;
             float s, k;
-            // the top 32 bits as a signed fraction: half turns in [-1, 1)
-            sincospif((float)(int32_t)(turns >> 32) * 0x1p-31f, &s, &k);
-            cs[v] = k * p.amplitude;
-            sn[v] = s * p.sign;
+            // the top 32 bits of a turn as the nearest quarter and a signed rest of at most an
+            // eighth, which a float holds to 2^-27 half turns (the whole turn: to 2^-25)
+            const uint32_t t = (uint32_t)(turns >> 32), quarter = (t + 0x20000000u) >> 30;
+            sincospif((float)(int32_t)(t - (quarter << 30)) * 0x1p-31f, &s, &k);
+            const float c0 = quarter & 1 ? -s : k, s0 = quarter & 1 ? k : s;
+            cs[v] = (quarter & 2 ? -c0 : c0) * p.amplitude;
+            sn[v] = (quarter & 2 ? -s0 : s0) * p.sign;
         }
     }
 #pragma unroll 4
