@@ -318,8 +318,8 @@ typedef enum {
  *
  * positions: device int32 [b][n] (dense), or NULL for start + row.  phase: device, rot / 2
  * entries, each the pair's turns per position f_i / 2 pi modulo 1 as a 64-bit binary fraction
- * (linformer_rotary_phase fills it; it is kept and used again by the caller).  Angles are
- * exact to fp32 at every int32 position.  dtype LINFORMER_F32 or LINFORMER_BF16 (the turn in
+ * (linformer_rotary_phase fills it, to the last bit; it is kept and used again by the caller).
+ * Angles are exact to fp32 at every int32 position.  dtype LINFORMER_F32 or LINFORMER_BF16 (the turn in
  * fp32, rounded once).  2 <= rot <= d, even; a finite amplitude; start + n <= 2^31 (else
  * LINFORMER_ERR_VALUE).  X, Y, X2, Y2 16-byte aligned, phase 8; any strides (multiples of 16
  * bytes, d and rot / 2 multiples of 16 bytes run fastest).

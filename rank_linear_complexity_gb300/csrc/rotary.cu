@@ -112,22 +112,69 @@ __global__ void __launch_bounds__(kThreads) rotary_kernel(const Params p) {
     }
 }
 
+// Sums of two doubles (Dekker's and Knuth's error-free sums and products), relative precision
+// about 2^-102: a double alone keeps 53 of a phase word's 64 bits, and position 2^31 would be off
+// by 2^-22 turns.
+struct Pair {
+    double hi, lo;
+};
+__device__ __forceinline__ Pair add_exact(double a, double b) {
+    const double s = a + b, c = s - a;
+    return {s, (a - (s - c)) + (b - c)};
+}
+__device__ __forceinline__ Pair add(Pair a, Pair b) {
+    const Pair s = add_exact(a.hi, b.hi);
+    return add_exact(s.hi, s.lo + (a.lo + b.lo));
+}
+__device__ __forceinline__ Pair mul(Pair a, Pair b) {
+    const double p = __dmul_rn(a.hi, b.hi);  // (not to be merged into the sum below)
+    return add_exact(p, fma(a.hi, b.hi, -p) + (a.hi * b.lo + a.lo * b.hi));
+}
+__device__ __forceinline__ Pair div(Pair a, Pair b) {
+    const double q = a.hi / b.hi;
+    const Pair r = add(a, mul({-q, 0.0}, b));
+    return add_exact(q, r.hi / b.hi);
+}
+__device__ Pair power(Pair x, int n) {
+    Pair y{1.0, 0.0};
+    for (; n; n >>= 1) {
+        if (n & 1) y = mul(y, x);
+        if (n > 1) x = mul(x, x);
+    }
+    return y;
+}
+// base^(-1 / n): Newton steps from the double's value, each of which squares its error.
+__device__ Pair inverse_root(double base, int n) {
+    Pair r{pow(base, -1.0 / n), 0.0};
+    for (int i = 0; i < 2; ++i) {
+        const Pair e = add(mul(power(r, n), {base, 0.0}), {-1.0, 0.0});
+        if (!isfinite(e.hi)) break;  // a base next to the ends of a double's range
+        r = add(r, mul({-r.hi / n, 0.0}, e));
+    }
+    return r;
+}
+
 // One thread a pair: f_i = base^(-2 i / rot), scaled, as a 64-bit fraction of a turn.
 __global__ void phase_kernel(uint64_t *phase, int pairs, double base, int scaling, double factor,
                              double original, double beta_fast, double beta_slow) {
     const int i = blockIdx.x * blockDim.x + threadIdx.x;
     if (i >= pairs) return;
-    const double two_pi = 6.283185307179586476925286766559;
-    if (scaling == LINFORMER_ROTARY_BASE && pairs > 1) base *= pow(factor, pairs / (pairs - 1.0));
-    double turns = pow(base, -(double)i / pairs) / two_pi;
-    if (scaling == LINFORMER_ROTARY_LINEAR) turns /= factor;
+    const Pair per_radian{0.15915494309189535, -9.839338337591243e-18};  // 1 / (2 pi)
+    Pair turns = mul(power(inverse_root(base, pairs), i), per_radian);
+    // the base times factor^(rot / (rot - 2)), to the power -2 i / rot
+    if (scaling == LINFORMER_ROTARY_BASE && pairs > 1) turns = mul(turns, power(inverse_root(factor, pairs - 1), i));
+    if (scaling == LINFORMER_ROTARY_LINEAR) turns = div(turns, {factor, 0.0});
     if (scaling == LINFORMER_ROTARY_BY_PARTS) {
-        double keep = (original * turns - beta_slow) / (beta_fast - beta_slow);
-        keep = keep < 0 ? 0 : (keep > 1 ? 1 : keep);
-        turns *= keep + (1 - keep) / factor;
+        Pair keep = div(add(mul(turns, {original, 0.0}), {-beta_slow, 0.0}), add_exact(beta_fast, -beta_slow));
+        if (keep.hi < 0.0) keep = {0.0, 0.0};
+        if (keep.hi > 1.0 || (keep.hi == 1.0 && keep.lo > 0.0)) keep = {1.0, 0.0};
+        const Pair rest = div(add({1.0, 0.0}, {-keep.hi, -keep.lo}), {factor, 0.0});
+        turns = mul(turns, add(keep, rest));
     }
-    turns -= floor(turns);
-    phase[i] = (uint64_t)rint(ldexp(turns, 64));
+    // the fraction of both parts in units of 2^-64, modulo 2^64
+    const double units = ldexp(turns.hi - floor(turns.hi), 64), whole = floor(units);
+    const double low = ldexp(turns.lo - rint(turns.lo), 64);
+    phase[i] = (uint64_t)whole + (uint64_t)(int64_t)rint((units - whole) + low);
 }
 
 template <typename T, int V>
