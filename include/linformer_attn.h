@@ -277,7 +277,7 @@ LINFORMER_API int linformer_softmax_attn_fwd(
  * lengths get zero.  Same argument rules; dO and dQ are shaped like O, dK and dV like K.
  * Sums are formed in a fixed order (no atomics): repeated calls agree bit for bit.  The
  * workspace is 8 bytes per query row, rows rounded up to 128 per head, and where few tiles
- * have long sums, which are then split, fp32 partial sums (at most 152 tiles of 128 rows of each gradient).
+ * have long sums, which are then split, fp32 partial sums (at most a tile of 128 rows an SM, of each gradient).
  */
 LINFORMER_API int linformer_softmax_attn_bwd(
     const void *Q, const int64_t *Q_strides, const void *K, const int64_t *K_strides,

@@ -58,6 +58,9 @@ int validate_forward(const void *Q, const void *K, const void *V, const void *E,
                      const int32_t *pad_lengths, const void *O, int b, int h, int n, int d, int k,
                      int share_mode, int dtype);
 
+// Number of SMs of the current device.
+int device_sms();
+
 // Device status word of the current device (set by bounded waits that ran out).
 int *device_status_ptr();
 

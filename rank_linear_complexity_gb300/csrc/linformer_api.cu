@@ -160,6 +160,19 @@ int *device_status_ptr() {
     return g_status_addr[dev];
 }
 
+int device_sms() {
+    static std::atomic<int> sms[kMaxDevices];
+    int dev = 0;
+    cudaGetDevice(&dev);
+    if (dev < 0 || dev >= kMaxDevices) return 148;
+    int v = sms[dev].load(std::memory_order_relaxed);
+    if (!v) {
+        cudaDeviceGetAttribute(&v, cudaDevAttrMultiProcessorCount, dev);
+        sms[dev].store(v = v > 0 ? v : 148, std::memory_order_relaxed);
+    }
+    return v;
+}
+
 int pv_terms_setting() { return g_pv_terms.load(std::memory_order_relaxed); }
 
 }  // namespace linformer

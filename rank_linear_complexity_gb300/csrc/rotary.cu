@@ -222,7 +222,8 @@ int turn(const Call &c) {
     // heads as leave two full waves of threads, at most kMaxHeads.
     const int heads = c.heads[0] + c.heads[1];
     const int64_t rows = (int64_t)c.b * c.n * p.chunks;
-    int64_t per = rows * heads / (2LL * 152 * 2048);
+    constexpr int64_t kSmThreads = 2048;
+    const int64_t per = rows * heads / (2 * device_sms() * kSmThreads);
     p.per_thread = (int)std::max<int64_t>(1, std::min<int64_t>(std::min(heads, kMaxHeads), per));
     p.splits = (heads + p.per_thread - 1) / p.per_thread;
     p.threads = rows * p.splits;

@@ -117,7 +117,6 @@ __device__ __forceinline__ void zero_rows(uint8_t *tile, int row0, int idx, int 
 // heads of a group of `group`: coordinates (column, row, head in group, group, batch).
 bool encode_rows(CUtensorMap *m, const void *base, const Strides &s, int b, int heads, int group,
                  int n, int d, int rows, int hrows);
-int device_sms();
 int allow_smem(const void *kernel, uint32_t bytes, int slot);
 
 int forward(const Call &c);

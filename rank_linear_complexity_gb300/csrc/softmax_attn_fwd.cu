@@ -701,7 +701,6 @@ PFN_cuTensorMapEncodeTiled_v12000 g_encode = nullptr;
 std::once_flag g_encode_once;
 
 constexpr int kMaxDev = 64;
-std::atomic<int> g_sms[kMaxDev] = {};
 
 __global__ void zero_queue_kernel(int *queue) {
     launch_dependents();
@@ -793,18 +792,6 @@ bool encode_rows(CUtensorMap *m, const void *base, const Strides &s, int b, int 
     return g_encode(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 5, const_cast<void *>(base), dims, strides, box,
                     one, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
                     CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
-}
-
-int device_sms() {
-    int dev = 0;
-    cudaGetDevice(&dev);
-    if (dev < 0 || dev >= kMaxDev) return 148;
-    int v = g_sms[dev].load(std::memory_order_relaxed);
-    if (!v) {
-        cudaDeviceGetAttribute(&v, cudaDevAttrMultiProcessorCount, dev);
-        g_sms[dev].store(v = v > 0 ? v : 148, std::memory_order_relaxed);
-    }
-    return v;
 }
 
 // The kernel's shared memory, allowed once per device (slot: one per kernel).
