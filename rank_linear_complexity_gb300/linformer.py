@@ -393,6 +393,11 @@ def _int32(name, x):
     return x
 
 
+def _sizes(name, shape):
+    if max(shape) > 0x7fffffff:
+        raise ValueError(f"{name}: a size of {tuple(shape)} is outside the 32-bit range")
+
+
 def _check(name, x, shape, dtype):
     if x.shape != shape or x.dtype != dtype:
         raise ValueError(f"{name}: {dtype} of shape {tuple(shape)} is needed, got {x.dtype} of "
@@ -419,6 +424,8 @@ def softmax_attention(Q, K, V, q_lengths=None, k_lengths=None, causal: bool = Fa
     shape, kv, dtype, device = Q.shape, K.shape, Q.dtype, Q.device
     b, hq, n, d = shape
     _, hk, m, _ = kv
+    _sizes("Q", shape)
+    _sizes("K", kv)
     handle = _stream_of(device, K, V, q_lengths, k_lengths, out, lse)
     if kv[0] != b or kv[3] != d or K.dtype != dtype:
         _check("K", K, (b, hk, m, d), dtype)
@@ -458,6 +465,8 @@ def softmax_attention_backward(Q, K, V, O, dO, lse, q_lengths=None, k_lengths=No
     shape, kv, dtype, device = Q.shape, K.shape, Q.dtype, Q.device
     b, hq, n, d = shape
     _, hk, m, _ = kv
+    _sizes("Q", shape)
+    _sizes("K", kv)
     handle = _stream_of(device, K, V, O, dO, lse, q_lengths, k_lengths, dQ, dK, dV)
     if kv[0] != b or kv[3] != d or K.dtype != dtype:
         _check("K", K, (b, hk, m, d), dtype)
@@ -502,6 +511,8 @@ def rotary_phase(rot: int, base: float = 10000.0, scaling: int = ROTARY_PLAIN,
         with _current_on(torch.device(device), stream):
             return rotary_phase(rot, base, scaling, factor, original_length, beta_fast, beta_slow,
                                 device)
+    for name, x in (("rot", rot), ("scaling", scaling), ("original_length", original_length)):
+        _int32(name, x)
     phase = torch.empty(max(rot // 2, 1), dtype=torch.int64, device=device)
     handle = _stream_of(phase.device)
     _call(lib().linformer_rotary_phase, phase.device,
@@ -525,6 +536,10 @@ def rotary(x, x2=None, phase=None, positions=None, start: int = 0, rot=None,
     b, h, n, d = shape
     if rot is None:
         rot = d
+    _sizes("x", shape)
+    _int32("rot", rot)
+    _int32("layout", layout)
+    _int32("start", start)
     handle = _stream_of(device, x2, phase, positions, out, out2)
     if phase is None:
         raise ValueError("phase: the table of rotary_phase() is needed")
@@ -539,7 +554,7 @@ def rotary(x, x2=None, phase=None, positions=None, start: int = 0, rot=None,
     px2 = sx2 = py2 = sy2 = None
     h2 = 0
     if x2 is not None:
-        h2 = x2.shape[1]
+        h2 = _int32("x2's heads", x2.shape[1])
         _check("x2", x2, (b, h2, n, d), dtype)
         if out2 is None:
             out2 = torch.empty_like(x2)
@@ -548,7 +563,7 @@ def rotary(x, x2=None, phase=None, positions=None, start: int = 0, rot=None,
         px2, sx2, py2, sy2 = x2.data_ptr(), _strides(x2), out2.data_ptr(), _strides(out2)
     _call(lib().linformer_rotary, device,
           (x.data_ptr(), _strides(x), out.data_ptr(), _strides(out), h, px2, sx2, py2, sy2, h2,
-           phase.data_ptr(), positions, _int32("start", start), b, n, d, rot, layout, amplitude,
+           phase.data_ptr(), positions, start, b, n, d, rot, layout, amplitude,
            1 if inverse else 0, dtype_code(x), handle),
           "linformer_rotary")
     return out if x2 is None else (out, out2)
