@@ -371,13 +371,20 @@ def _stream_of(device, *tensors):
         if t is not None and t.device != device:
             raise ValueError(f"tensors on {device} and {t.device}")
     import torch
-    return torch._C._cuda_getCurrentRawStream(device.index)
+    try:
+        return torch._C._cuda_getCurrentRawStream(device.index)
+    except AttributeError:  # a private name
+        return torch.cuda.current_stream(device).cuda_stream
 
 
 def _call(fn, device, args, name):
     """fn(*args) with `device` current (the library works on the current device)."""
     import torch
-    if torch._C._cuda_getDevice() == device.index:
+    try:
+        current = torch._C._cuda_getDevice()
+    except AttributeError:  # a private name
+        current = torch.cuda.current_device()
+    if current == device.index:
         st = fn(*args)
     else:
         with torch.cuda.device(device):

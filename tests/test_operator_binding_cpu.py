@@ -35,3 +35,20 @@ def test_sizes_past_32_bits(shape):
 def test_wide_integers_of_the_turn(kw):
     with pytest.raises(ValueError, match="32-bit"):
         lf.rotary(long((1, 2, 4, 64)), phase=torch.zeros(32, dtype=torch.int64), **kw)
+
+
+def test_without_torchs_private_names(monkeypatch):
+    """The quick names of the current stream and device are torch's own: without them the public
+    ones serve."""
+    class Stream:
+        cuda_stream = 77
+
+    monkeypatch.delattr(torch._C, "_cuda_getCurrentRawStream", raising=False)
+    monkeypatch.delattr(torch._C, "_cuda_getDevice", raising=False)
+    monkeypatch.setattr(torch.cuda, "current_stream", lambda device=None: Stream())
+    monkeypatch.setattr(torch.cuda, "current_device", lambda: 0)
+    device = torch.device("cuda:0")
+    assert lf._stream_of(device) == 77
+    done = []
+    lf._call(lambda x: done.append(x) or 0, device, (5,), "call")
+    assert done == [5]
