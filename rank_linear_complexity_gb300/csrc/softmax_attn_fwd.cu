@@ -432,7 +432,7 @@ softmax_attn_fwd_kernel(const __grid_constant__ CUtensorMap tQ, const __grid_con
                     for (int x = 0; x < 4; ++x)
                         mma_ts(tO, tP + 8 * x, v + (uint64_t)(128 * x), idesc_o, (j > lo || x > 0) ? 1u : 0u);
                     if (!C::kSep) {
-                        if (!thread_spin(&bar->p_full[t], n & 1, p.status, 78, abort_flag)) return false;
+                        if (!thread_spin(&bar->p_full[t], n & 1, p.status, 68, abort_flag)) return false;
                         tc_fence_after();
                     }
                     ++n;
@@ -529,7 +529,7 @@ softmax_attn_fwd_kernel(const __grid_constant__ CUtensorMap tQ, const __grid_con
                 // few blocks at a mask's edge must not widen the code of the others.
                 const int k0 = j * kTile;
                 if (__any_sync(0xffffffffu, first > k0 || end < k0 + kTile)) {
-mask_block(tS, first - k0, first < end ? end - first : 0);
+                    mask_block(tS, first - k0, first < end ? end - first : 0);
                 }
                 uint32_t v[4][32];
 #pragma unroll
@@ -551,9 +551,7 @@ mask_block(tS, first - k0, first < end ? end - first : 0);
                     const float f = mn == -INFINITY ? 1.f : ex2_approx((m - mn) * sl);
                     l *= f;
                     m = mn;
-                    if (j > lo) {
-rescale_output(tO, DP, f);
-                    }
+                    if (j > lo) rescale_output(tO, DP, f);
                 }
                 const float off = m == -INFINITY ? 0.f : -m * sl;
                 float2 sum0 = make_float2(0.f, 0.f), sum1 = sum0;

@@ -27,7 +27,7 @@ __device__ __forceinline__ void init_queue(Queue &q, int readers) {
 }
 __device__ __forceinline__ bool tell(Queue &q, int &t, int idx, int *status, volatile int *abort) {
     const int s = t & 1;
-    if (!thread_spin(&q.free[s], ((t >> 1) & 1) ^ 1, status, 81, abort)) return false;
+    if (!thread_spin(&q.free[s], ((t >> 1) & 1) ^ 1, status, 65, abort)) return false;
     *(volatile int *)&q.next[s] = idx;
     mbar_arrive(&q.full[s]);
     ++t;
@@ -36,7 +36,7 @@ __device__ __forceinline__ bool tell(Queue &q, int &t, int idx, int *status, vol
 // A single thread's next item, and a warp's.
 __device__ __forceinline__ bool thread_next(Queue &q, int &t, int &idx, int *status, volatile int *abort) {
     const int s = t & 1;
-    if (!thread_spin(&q.full[s], (t >> 1) & 1, status, 82, abort)) return false;
+    if (!thread_spin(&q.full[s], (t >> 1) & 1, status, 66, abort)) return false;
     idx = *(volatile int *)&q.next[s];
     mbar_arrive(&q.free[s]);
     ++t;
@@ -44,7 +44,7 @@ __device__ __forceinline__ bool thread_next(Queue &q, int &t, int &idx, int *sta
 }
 __device__ __forceinline__ bool warp_next(Queue &q, int &t, int &idx, int *status, volatile int *abort) {
     const int s = t & 1;
-    if (!warp_spin(&q.full[s], (t >> 1) & 1, status, 82, abort)) return false;
+    if (!warp_spin(&q.full[s], (t >> 1) & 1, status, 67, abort)) return false;
     idx = *(volatile int *)&q.next[s];
     __syncwarp();
     if ((threadIdx.x & 31) == 0) mbar_arrive(&q.free[s]);

@@ -52,3 +52,16 @@ def test_without_torchs_private_names(monkeypatch):
     done = []
     lf._call(lambda x: done.append(x) or 0, device, (5,), "call")
     assert done == [5]
+
+
+def test_every_wait_of_the_attention_kernels_has_a_code_of_its_own():
+    """The code in the device status word names one wait in the sources."""
+    import os
+    import re
+    from rank_linear_complexity_gb300 import build
+    codes = []
+    for name in ("softmax_attn_fwd.cu", "softmax_attn_bwd.cu", "work_queue.cuh"):
+        with open(os.path.join(build.CSRC, name)) as f:
+            codes += re.findall(r"_spin\([^;]*?status, (\d+),", f.read())
+    assert len(codes) >= 40
+    assert sorted(codes) == sorted(set(codes))
