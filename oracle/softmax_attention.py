@@ -106,7 +106,8 @@ def backward(Q, K, V, dO, q_lengths=None, k_lengths=None, causal=False, window=0
         out[0][bi, h] += scale * (ds @ k)
         out[1][bi, kv] += scale * (ds.T @ q)
         out[2][bi, kv] += p.T @ g
-        sums = _sums(max(q.shape[0], k.shape[0] * (Q.shape[1] // K.shape[1])))
+        # dK and dV sum over the queries of every head of the group, dQ over the keys
+        sums = _sums(max(q.shape[0] * (Q.shape[1] // K.shape[1]), k.shape[0]))
         # delta from the rounded O, dP and delta as fp32 sums of d products
         o = p @ v
         e_delta = (np.abs(g) * np.abs(o)).sum(1, keepdims=True) * (U + d * 2.0 ** -23)
