@@ -87,10 +87,15 @@ def forward(Q, K, V, q_lengths=None, k_lengths=None, causal=False, window=0, sca
     return O, lse, bO, bl
 
 
-def backward(Q, K, V, dO, q_lengths=None, k_lengths=None, causal=False, window=0, scale=None):
+def backward(Q, K, V, dO, q_lengths=None, k_lengths=None, causal=False, window=0, scale=None,
+             O=None):
     """((dQ, dK, dV), their bounds, the part of the bounds that comes from delta = dO.O with O
-    rounded to bf16: one error for a whole row, which sums over keys do not average out)."""
+    rounded to bf16: one error for a whole row, which sums over keys do not average out).
+
+    With O, the forward's result as the kernel was given it, delta is taken from that: then its
+    rounding is no error, and that part is zero."""
     Q, K, V, dO = host64(Q), host64(K), host64(V), host64(dO)
+    O = None if O is None else host64(O)
     d = Q.shape[3]
     scale = d ** -0.5 if scale is None else scale
     out = [np.zeros(Q.shape), np.zeros(K.shape), np.zeros(K.shape)]
@@ -101,22 +106,24 @@ def backward(Q, K, V, dO, q_lengths=None, k_lengths=None, causal=False, window=0
         k, v = _valid_rows(K[bi, kv], lk), _valid_rows(V[bi, kv], lk)
         p, _, eps = _probabilities(q, k, m, scale, d)
         dp = g @ v.T
-        delta = (p * dp).sum(1, keepdims=True)
+        o = p @ v if O is None else _valid_rows(O[bi, h], lq)
+        delta = ((p * dp) if O is None else g * o).sum(1, keepdims=True)
         ds = p * (dp - delta)
         out[0][bi, h] += scale * (ds @ k)
         out[1][bi, kv] += scale * (ds.T @ q)
         out[2][bi, kv] += p.T @ g
         # dK and dV sum over the queries of every head of the group, dQ over the keys
         sums = _sums(max(q.shape[0] * (Q.shape[1] // K.shape[1]), k.shape[0]))
-        # delta from the rounded O, dP and delta as fp32 sums of d products
-        o = p @ v
-        e_delta = (np.abs(g) * np.abs(o)).sum(1, keepdims=True) * (U + d * 2.0 ** -23)
+        # delta from the rounded O (none where it is the one given), dP and delta as fp32 sums of
+        # d products
+        e_delta = (np.abs(g) * np.abs(o)).sum(1, keepdims=True) * ((U if O is None else 0.0) + d * 2.0 ** -23)
         e_dp = d * 2.0 ** -23 * (np.abs(g) @ np.abs(v).T)
         e_ds = (U + eps + sums) * np.abs(ds) + p * (e_delta + e_dp) * (1 + U) + eps * p * np.abs(delta)
         bound[0][bi, h] += scale * (e_ds @ np.abs(k))
         bound[1][bi, kv] += scale * (e_ds.T @ np.abs(q))
-        rows[0][bi, h] += scale * ((p * e_delta) @ np.abs(k))
-        rows[1][bi, kv] += scale * ((p * e_delta).T @ np.abs(q))
+        if O is None:
+            rows[0][bi, h] += scale * ((p * e_delta) @ np.abs(k))
+            rows[1][bi, kv] += scale * ((p * e_delta).T @ np.abs(q))
         bound[2][bi, kv] += (U + eps + sums) * (p.T @ np.abs(g))
     for x, y in zip(bound, out):
         x += U * np.abs(y) * (1 + U)
