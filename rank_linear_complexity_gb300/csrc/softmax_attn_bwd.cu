@@ -1066,11 +1066,12 @@ int launch(const Call &c, BwdParams &p) {
     const int64_t qitems = (int64_t)c.b * c.hq * p.qtiles, kitems = (int64_t)c.b * c.hk * p.kblocks;
     if (qitems > kMaxItems || kitems > kMaxItems) return LINFORMER_ERR_SIZE;
     const int sms = device_sms();
-    auto steps_of = [&](int n) { return ((c.window ? std::min(n, c.window + kTile) : n) + kHalf - 1) / kHalf; };
+    auto reach = [&](int n) { return c.window ? std::min(n, c.window + kTile) : n; };
+    auto steps_of = [&](int n) { return (reach(n) + kHalf - 1) / kHalf; };
     p.qsplit = parts_of(qitems, steps_of(c.nk), sms);
     p.ksplit = std::min(parts_of(kitems, (int64_t)steps_of(c.nq) * p.group, sms), steps_of(c.nq));
-    p.qsome = units_at_once(p.qtiles, c.b * c.hq, ((int64_t)c.nk * c.d * 4 + p.group - 1) / p.group, c.causal);
-    p.ksome = units_at_once(p.kblocks, c.b * c.hk, (int64_t)p.group * c.nq * c.d * 4, c.causal);
+    p.qsome = units_at_once(p.qtiles, c.b * c.hq, ((int64_t)reach(c.nk) * c.d * 4 + p.group - 1) / p.group, c.causal, sms);
+    p.ksome = units_at_once(p.kblocks, c.b * c.hk, (int64_t)p.group * reach(c.nq) * c.d * 4, c.causal, sms);
     const int64_t qrows = (int64_t)c.b * c.hq * c.nq, krows = (int64_t)c.b * c.hk * c.nk;
     const int64_t qparts = p.qsplit > 1 ? p.qsplit * qrows * DP : 0, kparts = p.ksplit > 1 ? p.ksplit * krows * DP : 0;
     if (workspace_alloc(&ws, (size_t)(qitems * 256 + qparts + 2 * kparts + 2) * sizeof(float), c.stream) != LINFORMER_OK)

@@ -848,12 +848,16 @@ int forward(const Call &c) {
     const int64_t wanted = p.qbox * p.hbox <= kFewRows ? (kWaves * (int64_t)sms + whole - 1) / whole : sms / whole;
     p.nsplit = blocks < kFirst ? 1 : (int)std::max<int64_t>(1, std::min<int64_t>(wanted, blocks / kMinBlocks));
     p.items = (int)whole * p.nsplit;
-    p.some = units_at_once(p.npairs, p.units, (int64_t)c.nk * c.d * 4, c.causal);
+    // Causal calls take all heads at once (in sets: 2 x 8192 with 32 heads over 8, d = 128, 801 us
+    // against 767, 8 x 4096 885 against 824), and so do ragged ones with heads of up to 64 (384
+    // heads of 4096: 845 against 760; d = 128: 1226 against 1264).
+    const bool uneven = c.k_lengths || c.q_lengths || c.causal;
+    p.some = c.causal || (uneven && c.d <= 64)
+                 ? p.units
+                 : units_at_once(p.npairs, p.units, (int64_t)c.nk * c.d * 4, false, sms);
     // Masked and ragged items differ in length and come from a counter, in calls long enough for
-    // the launch that zeroes it.  Sets of heads of up to 64 are taken in turn all the same (768
-    // causal heads of 1024, d = 64: 187 us against 197; 128 of 4096, d = 128: 557 against 483).
-    const bool uneven = c.k_lengths || c.q_lengths || c.causal, sets = p.some < p.units;
-    p.order = uneven && p.items > 2 * sms && !(sets && c.d <= 64) ? kFromQueue : sets ? kInSets : kInTurn;
+    // the launch that zeroes it.
+    p.order = uneven && p.items > 2 * sms ? kFromQueue : p.some < p.units ? kInSets : kInTurn;
     return c.d <= 64 ? launch<64>(c, p) : launch<128>(c, p);
 }
 

@@ -168,21 +168,25 @@ def test_several_items_a_cta(name):
     against_oracle(b, hq, hk, nq, nk, d, 3, q, k, samples=20, **kw)
 
 
-SETS = {  # heads that stream more than L2 keeps: 48 MB, or 128 MB under a causal mask
-    "wide_all_keys": ((25, 8, 4, 2048, 1024, 128), {}),
-    "all_keys": ((13, 16, 16, 4096, 1024, 64), {}),
-    "causal": ((17, 16, 16, 2048, 2048, 64), dict(causal=True)),
-    "wide_causal": ((9, 16, 16, 2048, 2048, 128), dict(causal=True)),
+SETS = {  # heads that stream more than L2 keeps (48 MB): forward in sets without a causal mask
+    # (ragged ones from the counter, wide heads only), backward also with one
+    "wide_all_keys": ((25, 8, 4, 2048, 1024, 128), False, {}),
+    "wide_ragged": ((25, 8, 4, 2048, 1024, 128), True, {}),
+    "all_keys": ((13, 16, 16, 4096, 1024, 64), False, {}),
+    "ragged": ((13, 16, 16, 4096, 1024, 64), True, {}),
+    "causal": ((17, 16, 16, 2048, 2048, 64), False, dict(causal=True)),
+    "wide_causal": ((9, 16, 16, 2048, 2048, 128), True, dict(causal=True)),
 }
 
 
 @pytest.mark.parametrize("name", SETS)
 def test_heads_in_sets_against_the_oracle(name):
-    (b, hq, hk, nq, nk, d), kw = SETS[name]
+    (b, hq, hk, nq, nk, d), ragged, kw = SETS[name]
     items, sms, split = plan(b, hq, hk, nq, nk, d, **kw)
     streamed = 4 * b * hk * nk * d
-    assert items > 2 * sms and streamed > ((128 if kw else 48) << 20) and items // (b * hk) >= 16 - 8 * bool(kw)
-    against_oracle(b, hq, hk, nq, nk, d, 5, samples=3, **kw)
+    assert items > 2 * sms and streamed > 48 << 20 and (kw or items // (b * hk) >= 16)
+    q, k = (mixed(b, nq, 3), mixed(b, nk, 4)) if ragged else (None, None)
+    against_oracle(b, hq, hk, nq, nk, d, 5, q, k, samples=4, **kw)
 
 
 @pytest.mark.parametrize("d", [64, 128])
