@@ -358,142 +358,142 @@ softmax_attn_dq_kernel(const __grid_constant__ CUtensorMap tQ, const __grid_cons
     tc_fence_after();
     const uint32_t tmem = bar->tmem;
     if (warp >= kLoadWarp) {
-    setmaxnreg_dec<issue_regs(G)>();
-    if (warp == kLoadWarp) {
-        if (lane == 0) {
-            wait_prerequisites();  // the row values; and only then may the third kernel start
-            launch_dependents();
-            int steps = 0, nq = 0, t = 0;
-            Ring<G, C::kStages> at;
-            bool ok = true;
-            for (int idx = blockIdx.x; idx < p.items && ok;) {
-                const int following = gridDim.x + atomicAdd(p.queue, 1);
-                const DqItem it = dq_item(p, idx);
-                if (it.hi > it.lo) {
-                    const int qb = nq % C::kItems;
-                    if (nq >= C::kItems &&
-                        !thread_spin(&bar->q_free[qb], (nq / C::kItems - 1) & 1, p.status, 83, abort_flag))
-                        break;
-                    uint64_t *q_full = &bar->q_full[qb];
-                    mbar_arrive_expect_tx(q_full, 2 * C::kTileBytes + 1024);
-                    const int g = it.head % p.group, kvh = it.head / p.group;
-                    bulk_load(bar->rows[qb], p.rows + (((int64_t)it.batch * p.hq + it.head) * p.qtiles + it.q0 / kTile) * 256,
-                              1024, q_full);
-                    load_rows<DP, 2>(sQ + qb * 2 * C::kTileBytes, &tQ, q_full, it.q0, g, kvh, it.batch);
-                    load_rows<DP, 2>(sdO + qb * 2 * C::kTileBytes, &tdO, q_full, it.q0, g, kvh, it.batch);
-                    ++nq;
-                    for (int j = it.lo; j < it.hi; ++j, ++steps, at.next()) {
-                        uint8_t *st = sKV + at.pos * 2 * C::kStepBytes;
-                        // (dQ comes last: with it all products of a step have been formed)
-                        ok = thread_spin(&bar->dq_done[at.pos], at.phase ^ 1, p.status, 84, abort_flag);
+        setmaxnreg_dec<issue_regs(G)>();
+        if (warp == kLoadWarp) {
+            if (lane == 0) {
+                wait_prerequisites();  // the row values; and only then may the third kernel start
+                launch_dependents();
+                int steps = 0, nq = 0, t = 0;
+                Ring<G, C::kStages> at;
+                bool ok = true;
+                for (int idx = blockIdx.x; idx < p.items && ok;) {
+                    const int following = gridDim.x + atomicAdd(p.queue, 1);
+                    const DqItem it = dq_item(p, idx);
+                    if (it.hi > it.lo) {
+                        const int qb = nq % C::kItems;
+                        if (nq >= C::kItems &&
+                            !thread_spin(&bar->q_free[qb], (nq / C::kItems - 1) & 1, p.status, 83, abort_flag))
+                            break;
+                        uint64_t *q_full = &bar->q_full[qb];
+                        mbar_arrive_expect_tx(q_full, 2 * C::kTileBytes + 1024);
+                        const int g = it.head % p.group, kvh = it.head / p.group;
+                        bulk_load(bar->rows[qb], p.rows + (((int64_t)it.batch * p.hq + it.head) * p.qtiles + it.q0 / kTile) * 256,
+                                  1024, q_full);
+                        load_rows<DP, 2>(sQ + qb * 2 * C::kTileBytes, &tQ, q_full, it.q0, g, kvh, it.batch);
+                        load_rows<DP, 2>(sdO + qb * 2 * C::kTileBytes, &tdO, q_full, it.q0, g, kvh, it.batch);
+                        ++nq;
+                        for (int j = it.lo; j < it.hi; ++j, ++steps, at.next()) {
+                            uint8_t *st = sKV + at.pos * 2 * C::kStepBytes;
+                            // (dQ comes last: with it all products of a step have been formed)
+                            ok = thread_spin(&bar->dq_done[at.pos], at.phase ^ 1, p.status, 84, abort_flag);
+                            if (!ok) break;
+                            mbar_arrive_expect_tx(&bar->k_full[at.pos], C::kStepBytes);
+                            load_rows<DP, 1>(st, &tK, &bar->k_full[at.pos], j * kHalf, 0, kvh, it.batch);
+                            mbar_arrive_expect_tx(&bar->v_full[at.pos], C::kStepBytes);
+                            load_rows<DP, 1>(st + C::kStepBytes, &tV, &bar->v_full[at.pos], j * kHalf, 0, kvh, it.batch);
+                        }
+                    }
+                    ok = ok && tell(bar->queue, t, following, p.status, abort_flag);
+                    idx = following;
+                }
+                for (int i = max(0, nq - C::kItems); i < nq; ++i)
+                    mbar_wait_drain(&bar->q_full[i % C::kItems], (i / C::kItems) & 1);
+                for (int i = max(0, steps - C::kStages); i < steps; ++i) {
+                    mbar_wait_drain(&bar->k_full[i % C::kStages], (i / C::kStages) & 1);
+                    mbar_wait_drain(&bar->v_full[i % C::kStages], (i / C::kStages) & 1);
+                }
+            } else if (p.k_lengths) {  // K and V rows past the valid length: P and dS are 0 there, but 0 x NaN is not
+                int ring = 0, nfix = 0;
+                bool ok = true;
+                for (int idx = blockIdx.x, t = 0; idx < p.items && ok;
+                     ok = ok && thread_next(bar->queue, t, idx, p.status, abort_flag)) {
+                    const DqItem it = dq_item(p, idx);
+                    if (it.hi <= it.lo) continue;
+                    ring += it.hi - it.lo;
+                    if (it.sp.Lk >= p.nk || it.hi * kHalf <= it.sp.Lk) continue;
+                    if (!thread_spin(&bar->fix_wanted, nfix & 1, p.status, 85, abort_flag)) break;
+                    ++nfix;
+                    const int row0 = it.sp.Lk - (it.hi - 1) * kHalf;
+                    uint8_t *st = sKV + (ring - 1) % C::kStages * 2 * C::kStepBytes;
+                    zero_rows<DP, kHalf>(st, row0, lane - 1, 31);
+                    zero_rows<DP, kHalf>(st + C::kStepBytes, row0, lane - 1, 31);
+                    fence_proxy_async_smem();
+                    mbar_arrive(&bar->fixed_k);
+                    mbar_arrive(&bar->fixed_v);
+                }
+            }
+            __syncwarp();
+        } else if (warp <= kMmaWarp + 1) {
+            const bool first = warp == kMmaWarp;  // S = Q K^T; the other thread: dP = dO V^T
+            if (elect_one()) {
+                int items = 0;
+                uint32_t nfix = 0;
+                Ring<G, C::kStages> at;
+                bool ok = true;
+                const uint32_t a0 = smem_u32(first ? sQ : sdO), b = smem_u32(sKV) + (first ? 0 : C::kStepBytes),
+                               slots = tmem + (first ? 0 : 64), loaded = smem_u32(first ? bar->k_full : bar->v_full),
+                               free = smem_u32(first ? bar->s_free : bar->dq_done),
+                               out = smem_u32(first ? bar->s_full : bar->dp_full),
+                               fixed = smem_u32(first ? &bar->fixed_k : &bar->fixed_v);
+                for (int idx = blockIdx.x, t = 0; idx < p.items && ok;
+                     ok = ok && thread_next(bar->queue, t, idx, p.status, abort_flag)) {
+                    const DqItem it = dq_item(p, idx);
+                    const int steps = it.hi - it.lo;
+                    if (steps <= 0) continue;
+                    const bool fix = it.sp.Lk < p.nk && it.hi * kHalf > it.sp.Lk;
+                    const int qb = items % C::kItems;
+                    const uint32_t a = a0 + qb * 2 * C::kTileBytes;
+                    ok = thread_spin(&bar->q_full[qb], (items / C::kItems) & 1, p.status, 91, abort_flag);
+                    for (int j = steps; j > 0 && ok; --j, at.next()) {
+                        ok = thread_spin(loaded + 8 * at.pos, at.phase, p.status, 86, abort_flag) &&
+                             thread_spin(free + 8 * at.before(), at.phase_before(), p.status, 88, abort_flag);
+                        if (ok && fix && j == 1) {
+                            mbar_arrive(&bar->fix_wanted);
+                            ok = thread_spin(fixed, nfix++ & 1, p.status, 87, abort_flag);
+                        }
                         if (!ok) break;
-                        mbar_arrive_expect_tx(&bar->k_full[at.pos], C::kStepBytes);
-                        load_rows<DP, 1>(st, &tK, &bar->k_full[at.pos], j * kHalf, 0, kvh, it.batch);
-                        mbar_arrive_expect_tx(&bar->v_full[at.pos], C::kStepBytes);
-                        load_rows<DP, 1>(st + C::kStepBytes, &tV, &bar->v_full[at.pos], j * kHalf, 0, kvh, it.batch);
+                        tc_fence_after();
+                        mma_scores<DP>(slots + 128 * at.slot, a, b + at.pos * (2 * C::kStepBytes));
+                        mma_commit(out + 8 * at.pos);
                     }
+                    mma_commit(&bar->q_free[qb]);
+                    ++items;
                 }
-                ok = ok && tell(bar->queue, t, following, p.status, abort_flag);
-                idx = following;
+                mma_commit(&bar->drain[first ? 0 : 1]);
+                mbar_wait_drain(&bar->drain[first ? 0 : 1], 0);
             }
-            for (int i = max(0, nq - C::kItems); i < nq; ++i)
-                mbar_wait_drain(&bar->q_full[i % C::kItems], (i / C::kItems) & 1);
-            for (int i = max(0, steps - C::kStages); i < steps; ++i) {
-                mbar_wait_drain(&bar->k_full[i % C::kStages], (i / C::kStages) & 1);
-                mbar_wait_drain(&bar->v_full[i % C::kStages], (i / C::kStages) & 1);
-            }
-        } else if (p.k_lengths) {  // K and V rows past the valid length: P and dS are 0 there, but 0 x NaN is not
-            int ring = 0, nfix = 0;
-            bool ok = true;
-            for (int idx = blockIdx.x, t = 0; idx < p.items && ok;
-                 ok = ok && thread_next(bar->queue, t, idx, p.status, abort_flag)) {
-                const DqItem it = dq_item(p, idx);
-                if (it.hi <= it.lo) continue;
-                ring += it.hi - it.lo;
-                if (it.sp.Lk >= p.nk || it.hi * kHalf <= it.sp.Lk) continue;
-                if (!thread_spin(&bar->fix_wanted, nfix & 1, p.status, 85, abort_flag)) break;
-                ++nfix;
-                const int row0 = it.sp.Lk - (it.hi - 1) * kHalf;
-                uint8_t *st = sKV + (ring - 1) % C::kStages * 2 * C::kStepBytes;
-                zero_rows<DP, kHalf>(st, row0, lane - 1, 31);
-                zero_rows<DP, kHalf>(st + C::kStepBytes, row0, lane - 1, 31);
-                fence_proxy_async_smem();
-                mbar_arrive(&bar->fixed_k);
-                mbar_arrive(&bar->fixed_v);
-            }
-        }
-        __syncwarp();
-    } else if (warp <= kMmaWarp + 1) {
-        const bool first = warp == kMmaWarp;  // S = Q K^T; the other thread: dP = dO V^T
-        if (elect_one()) {
-            int items = 0;
-            uint32_t nfix = 0;
-            Ring<G, C::kStages> at;
-            bool ok = true;
-            const uint32_t a0 = smem_u32(first ? sQ : sdO), b = smem_u32(sKV) + (first ? 0 : C::kStepBytes),
-                           slots = tmem + (first ? 0 : 64), loaded = smem_u32(first ? bar->k_full : bar->v_full),
-                           free = smem_u32(first ? bar->s_free : bar->dq_done),
-                           out = smem_u32(first ? bar->s_full : bar->dp_full),
-                           fixed = smem_u32(first ? &bar->fixed_k : &bar->fixed_v);
-            for (int idx = blockIdx.x, t = 0; idx < p.items && ok;
-                 ok = ok && thread_next(bar->queue, t, idx, p.status, abort_flag)) {
-                const DqItem it = dq_item(p, idx);
-                const int steps = it.hi - it.lo;
-                if (steps <= 0) continue;
-                const bool fix = it.sp.Lk < p.nk && it.hi * kHalf > it.sp.Lk;
-                const int qb = items % C::kItems;
-                const uint32_t a = a0 + qb * 2 * C::kTileBytes;
-                ok = thread_spin(&bar->q_full[qb], (items / C::kItems) & 1, p.status, 91, abort_flag);
-                for (int j = steps; j > 0 && ok; --j, at.next()) {
-                    ok = thread_spin(loaded + 8 * at.pos, at.phase, p.status, 86, abort_flag) &&
-                         thread_spin(free + 8 * at.before(), at.phase_before(), p.status, 88, abort_flag);
-                    if (ok && fix && j == 1) {
-                        mbar_arrive(&bar->fix_wanted);
-                        ok = thread_spin(fixed, nfix++ & 1, p.status, 87, abort_flag);
+            __syncwarp();
+        } else {
+            if (elect_one()) {  // dQ += dS K
+                int items = 0;
+                Ring<G, C::kStages> at;
+                bool ok = true;
+                const uint32_t b = smem_u32(sKV), ready = smem_u32(bar->ds_full), done = smem_u32(bar->dq_done);
+                for (int idx = blockIdx.x, t = 0; idx < p.items && ok;
+                     ok = ok && thread_next(bar->queue, t, idx, p.status, abort_flag)) {
+                    const DqItem it = dq_item(p, idx);
+                    const int steps = it.hi - it.lo;
+                    if (steps <= 0) continue;
+                    const int ab = items % C::kItems;
+                    const uint32_t acc = tmem + C::kDq + ab * DP;
+                    if (items >= C::kItems)
+                        ok = thread_spin(&bar->acc_free[ab], (items / C::kItems - 1) & 1, p.status, 93, abort_flag);
+                    for (int j = 0; j < steps && ok; ++j, at.next()) {
+                        // (dS says that S has been formed, so the block of K has landed)
+                        ok = thread_spin(ready + 8 * at.pos, at.phase, p.status, 92, abort_flag);
+                        if (!ok) break;
+                        tc_fence_after();
+                        mma_sum<DP>(acc, tmem + 128 * at.slot + 64, b + at.pos * (2 * C::kStepBytes), j > 0 ? 1u : 0u);
+                        mma_commit(done + 8 * at.pos);
                     }
-                    if (!ok) break;
-                    tc_fence_after();
-                    mma_scores<DP>(slots + 128 * at.slot, a, b + at.pos * (2 * C::kStepBytes));
-                    mma_commit(out + 8 * at.pos);
+                    mma_commit(&bar->acc_full[ab]);
+                    ++items;
                 }
-                mma_commit(&bar->q_free[qb]);
-                ++items;
+                mma_commit(&bar->drain[2]);
+                mbar_wait_drain(&bar->drain[2], 0);
             }
-            mma_commit(&bar->drain[first ? 0 : 1]);
-            mbar_wait_drain(&bar->drain[first ? 0 : 1], 0);
+            __syncwarp();
         }
-        __syncwarp();
-    } else {
-        if (elect_one()) {  // dQ += dS K
-            int items = 0;
-            Ring<G, C::kStages> at;
-            bool ok = true;
-            const uint32_t b = smem_u32(sKV), ready = smem_u32(bar->ds_full), done = smem_u32(bar->dq_done);
-            for (int idx = blockIdx.x, t = 0; idx < p.items && ok;
-                 ok = ok && thread_next(bar->queue, t, idx, p.status, abort_flag)) {
-                const DqItem it = dq_item(p, idx);
-                const int steps = it.hi - it.lo;
-                if (steps <= 0) continue;
-                const int ab = items % C::kItems;
-                const uint32_t acc = tmem + C::kDq + ab * DP;
-                if (items >= C::kItems)
-                    ok = thread_spin(&bar->acc_free[ab], (items / C::kItems - 1) & 1, p.status, 93, abort_flag);
-                for (int j = 0; j < steps && ok; ++j, at.next()) {
-                    // (dS says that S has been formed, so the block of K has landed)
-                    ok = thread_spin(ready + 8 * at.pos, at.phase, p.status, 92, abort_flag);
-                    if (!ok) break;
-                    tc_fence_after();
-                    mma_sum<DP>(acc, tmem + 128 * at.slot + 64, b + at.pos * (2 * C::kStepBytes), j > 0 ? 1u : 0u);
-                    mma_commit(done + 8 * at.pos);
-                }
-                mma_commit(&bar->acc_full[ab]);
-                ++items;
-            }
-            mma_commit(&bar->drain[2]);
-            mbar_wait_drain(&bar->drain[2], 0);
-        }
-        __syncwarp();
-    }
     } else {
         setmaxnreg_inc<math_regs(G)>();
         const int w = warp >> 2, row = tid & 127;
@@ -730,160 +730,160 @@ softmax_attn_dkv_kernel(const __grid_constant__ CUtensorMap tQ, const __grid_con
     const uint32_t tmem = bar->tmem;
 
     if (warp >= kLoadWarp) {
-    setmaxnreg_dec<issue_regs(G)>();
-    if (warp == kLoadWarp) {
-        if (lane == 0) {
-            int ring = 0, items = 0, t = 0;
-            Ring<G, C::kStages> at;
-            bool ok = true;
-            for (int idx = blockIdx.x; idx < p.items && ok;) {
-                const int following = gridDim.x + atomicAdd(p.queue + 1, 1);
-                const DkvItem it = dkv_item(p, idx);
-                if (it.hi > it.lo) {
-                    const int kb = items % C::kKv;
-                    if (items >= C::kKv &&
-                        !thread_spin(&bar->kv_free[kb], (items / C::kKv - 1) & 1, p.status, 100, abort_flag))
-                        break;
-                    uint8_t *kv = sK + kb * 2 * C::kTileBytes;
-                    mbar_arrive_expect_tx(&bar->kv_full[kb], 2 * C::kTileBytes);
-                    load_rows<DP, 2>(kv, &tK, &bar->kv_full[kb], it.k0, 0, it.kvh, it.batch);
-                    load_rows<DP, 2>(kv + C::kTileBytes, &tV, &bar->kv_full[kb], it.k0, 0, it.kvh, it.batch);
-                    ++items;
-                    for (int g = 0; g < p.group && ok; ++g)
-                        for (int j = it.lo; j < it.hi; ++j, ++ring, at.next()) {
-                            const int s = at.pos;
-                            // (dK comes last: with it all products of a step have been formed)
-                            if (!thread_spin(&bar->ds_done[s], at.phase ^ 1, p.status, 101, abort_flag)) {
-                                ok = false;
-                                break;
+        setmaxnreg_dec<issue_regs(G)>();
+        if (warp == kLoadWarp) {
+            if (lane == 0) {
+                int ring = 0, items = 0, t = 0;
+                Ring<G, C::kStages> at;
+                bool ok = true;
+                for (int idx = blockIdx.x; idx < p.items && ok;) {
+                    const int following = gridDim.x + atomicAdd(p.queue + 1, 1);
+                    const DkvItem it = dkv_item(p, idx);
+                    if (it.hi > it.lo) {
+                        const int kb = items % C::kKv;
+                        if (items >= C::kKv &&
+                            !thread_spin(&bar->kv_free[kb], (items / C::kKv - 1) & 1, p.status, 100, abort_flag))
+                            break;
+                        uint8_t *kv = sK + kb * 2 * C::kTileBytes;
+                        mbar_arrive_expect_tx(&bar->kv_full[kb], 2 * C::kTileBytes);
+                        load_rows<DP, 2>(kv, &tK, &bar->kv_full[kb], it.k0, 0, it.kvh, it.batch);
+                        load_rows<DP, 2>(kv + C::kTileBytes, &tV, &bar->kv_full[kb], it.k0, 0, it.kvh, it.batch);
+                        ++items;
+                        for (int g = 0; g < p.group && ok; ++g)
+                            for (int j = it.lo; j < it.hi; ++j, ++ring, at.next()) {
+                                const int s = at.pos;
+                                // (dK comes last: with it all products of a step have been formed)
+                                if (!thread_spin(&bar->ds_done[s], at.phase ^ 1, p.status, 101, abort_flag)) {
+                                    ok = false;
+                                    break;
+                                }
+                                uint8_t *st = sT + s * 2 * C::kStepBytes;
+                                mbar_arrive_expect_tx(&bar->full[s], 2 * C::kStepBytes + 512);
+                                load_rows<DP, 1>(st, &tQ, &bar->full[s], j * kHalf, g, it.kvh, it.batch);
+                                load_rows<DP, 1>(st + C::kStepBytes, &tdO, &bar->full[s], j * kHalf, g, it.kvh, it.batch);
+                                const int64_t head = (int64_t)it.batch * p.hq + it.kvh * p.group + g;
+                                bulk_load(sR + s * 512, p.rows + (head * 2 * p.qtiles + j) * 128, 512, &bar->full[s]);
                             }
-                            uint8_t *st = sT + s * 2 * C::kStepBytes;
-                            mbar_arrive_expect_tx(&bar->full[s], 2 * C::kStepBytes + 512);
-                            load_rows<DP, 1>(st, &tQ, &bar->full[s], j * kHalf, g, it.kvh, it.batch);
-                            load_rows<DP, 1>(st + C::kStepBytes, &tdO, &bar->full[s], j * kHalf, g, it.kvh, it.batch);
-                            const int64_t head = (int64_t)it.batch * p.hq + it.kvh * p.group + g;
-                            bulk_load(sR + s * 512, p.rows + (head * 2 * p.qtiles + j) * 128, 512, &bar->full[s]);
+                    }
+                    ok = ok && tell(bar->queue, t, following, p.status, abort_flag);
+                    idx = following;
+                }
+                for (int i = max(0, items - C::kKv); i < items; ++i)
+                    mbar_wait_drain(&bar->kv_full[i % C::kKv], (i / C::kKv) & 1);
+                for (int i = max(0, ring - C::kStages); i < ring; ++i)
+                    mbar_wait_drain(&bar->full[i % C::kStages], (i / C::kStages) & 1);
+            } else if (p.q_lengths) {  // Q and dO rows past the valid length: P and dS are 0 there, but 0 x NaN is not
+                int ring = 0, nfix = 0;
+                bool ok = true;
+                for (int idx = blockIdx.x, t = 0; idx < p.items && ok;
+                     ok = ok && thread_next(bar->queue, t, idx, p.status, abort_flag)) {
+                    const DkvItem it = dkv_item(p, idx);
+                    if (it.hi <= it.lo) continue;
+                    if (it.sp.Lq >= p.nq || it.hi * kHalf <= it.sp.Lq) {
+                        ring += p.group * (it.hi - it.lo);
+                        continue;
+                    }
+                    for (int g = 0; g < p.group; ++g) {
+                        ring += it.hi - it.lo;
+                        if (!thread_spin(&bar->fix_wanted, nfix & 1, p.status, 102, abort_flag)) {
+                            ok = false;
+                            break;
                         }
-                }
-                ok = ok && tell(bar->queue, t, following, p.status, abort_flag);
-                idx = following;
-            }
-            for (int i = max(0, items - C::kKv); i < items; ++i)
-                mbar_wait_drain(&bar->kv_full[i % C::kKv], (i / C::kKv) & 1);
-            for (int i = max(0, ring - C::kStages); i < ring; ++i)
-                mbar_wait_drain(&bar->full[i % C::kStages], (i / C::kStages) & 1);
-        } else if (p.q_lengths) {  // Q and dO rows past the valid length: P and dS are 0 there, but 0 x NaN is not
-            int ring = 0, nfix = 0;
-            bool ok = true;
-            for (int idx = blockIdx.x, t = 0; idx < p.items && ok;
-                 ok = ok && thread_next(bar->queue, t, idx, p.status, abort_flag)) {
-                const DkvItem it = dkv_item(p, idx);
-                if (it.hi <= it.lo) continue;
-                if (it.sp.Lq >= p.nq || it.hi * kHalf <= it.sp.Lq) {
-                    ring += p.group * (it.hi - it.lo);
-                    continue;
-                }
-                for (int g = 0; g < p.group; ++g) {
-                    ring += it.hi - it.lo;
-                    if (!thread_spin(&bar->fix_wanted, nfix & 1, p.status, 102, abort_flag)) {
-                        ok = false;
-                        break;
+                        ++nfix;
+                        const int s = (ring - 1) % C::kStages, row0 = it.sp.Lq - (it.hi - 1) * kHalf;
+                        uint8_t *st = sT + s * 2 * C::kStepBytes;
+                        zero_rows<DP, kHalf>(st, row0, lane - 1, 31);
+                        zero_rows<DP, kHalf>(st + C::kStepBytes, row0, lane - 1, 31);
+                        fence_proxy_async_smem();
+                        mbar_arrive(&bar->fixed[s]);
                     }
-                    ++nfix;
-                    const int s = (ring - 1) % C::kStages, row0 = it.sp.Lq - (it.hi - 1) * kHalf;
-                    uint8_t *st = sT + s * 2 * C::kStepBytes;
-                    zero_rows<DP, kHalf>(st, row0, lane - 1, 31);
-                    zero_rows<DP, kHalf>(st + C::kStepBytes, row0, lane - 1, 31);
-                    fence_proxy_async_smem();
-                    mbar_arrive(&bar->fixed[s]);
                 }
             }
-        }
-        __syncwarp();
-    } else if (warp <= kMmaWarp + 1) {
-        const bool first = warp == kMmaWarp;  // S = K Q^T; the other thread: dP = V dO^T
-        if (elect_one()) {
-            int items = 0;
-            uint32_t fixes = 0;  // bit s: parity of stage s's next fix
-            Ring<G, C::kStages> at;
-            bool ok = true;
-            const uint32_t a0 = smem_u32(sK) + (first ? 0 : C::kTileBytes), b = smem_u32(sT) + (first ? 0 : C::kStepBytes),
-                           slots = tmem + (first ? 0 : 64), loaded = smem_u32(bar->full),
-                           done = smem_u32(first ? bar->pv_done : bar->ds_done),
-                           out = smem_u32(first ? bar->s_full : bar->dp_full), fixed = smem_u32(bar->fixed);
-            for (int idx = blockIdx.x, t = 0; idx < p.items && ok;
-                 ok = ok && thread_next(bar->queue, t, idx, p.status, abort_flag)) {
-                const DkvItem it = dkv_item(p, idx);
-                const int per = it.hi - it.lo;
-                if (per <= 0) continue;
-                const bool fix = it.sp.Lq < p.nq && it.hi * kHalf > it.sp.Lq;
-                const int kb = items % C::kKv;
-                const uint32_t a = a0 + kb * 2 * C::kTileBytes;
-                int in_head = per;
-                ok = thread_spin(&bar->kv_full[kb], (items / C::kKv) & 1, p.status, 107, abort_flag);
-                for (int j = per * p.group; j > 0 && ok; --j, at.next()) {
-                    ok = thread_spin(loaded + 8 * at.pos, at.phase, p.status, 103, abort_flag) &&
-                         thread_spin(done + 8 * at.before(), at.phase_before(), p.status, 105, abort_flag);
-                    if (ok && fix && --in_head == 0) {
-                        in_head = per;
-                        if (first) mbar_arrive(&bar->fix_wanted);
-                        ok = thread_spin(fixed + 8 * at.pos, fixes >> at.pos & 1, p.status, 104, abort_flag);
-                        fixes ^= 1u << at.pos;
-                    }
-                    if (!ok) break;
-                    tc_fence_after();
-                    mma_scores<DP>(slots + 128 * at.slot, a, b + at.pos * (2 * C::kStepBytes));
-                    mma_commit(out + 8 * at.pos);
-                }
-                mma_commit(&bar->kv_free[kb]);
-                ++items;
-            }
-            mma_commit(&bar->drain[first ? 0 : 1]);
-            mbar_wait_drain(&bar->drain[first ? 0 : 1], 0);
-        }
-        __syncwarp();
-    } else {
-        if (elect_one()) {  // dV += P^T dO of each step, then dK += dS^T Q, with three slots of the step before
-            constexpr int kLag = G - 2;
-            int items = 0;
-            Ring<G, C::kStages> av, ak;
-            bool ok = true;
-            const uint32_t b = smem_u32(sT), p_full = smem_u32(bar->p_full), ds_full = smem_u32(bar->ds_full),
-                           pv_done = smem_u32(bar->pv_done), ds_done = smem_u32(bar->ds_done);
-            for (int idx = blockIdx.x, t = 0; idx < p.items && ok;
-                 ok = ok && thread_next(bar->queue, t, idx, p.status, abort_flag)) {
-                const DkvItem it = dkv_item(p, idx);
-                const int steps = (it.hi - it.lo) * p.group;
-                if (steps <= 0) continue;
-                if (items > 0) ok = thread_spin(&bar->acc_free, (items - 1) & 1, p.status, 109, abort_flag);
-                for (int j = 0; j < steps + kLag && ok; ++j) {
-                    if (j < steps) {
-                        ok = thread_spin(p_full + 8 * av.pos, av.phase, p.status, 106, abort_flag);
+            __syncwarp();
+        } else if (warp <= kMmaWarp + 1) {
+            const bool first = warp == kMmaWarp;  // S = K Q^T; the other thread: dP = V dO^T
+            if (elect_one()) {
+                int items = 0;
+                uint32_t fixes = 0;  // bit s: parity of stage s's next fix
+                Ring<G, C::kStages> at;
+                bool ok = true;
+                const uint32_t a0 = smem_u32(sK) + (first ? 0 : C::kTileBytes), b = smem_u32(sT) + (first ? 0 : C::kStepBytes),
+                               slots = tmem + (first ? 0 : 64), loaded = smem_u32(bar->full),
+                               done = smem_u32(first ? bar->pv_done : bar->ds_done),
+                               out = smem_u32(first ? bar->s_full : bar->dp_full), fixed = smem_u32(bar->fixed);
+                for (int idx = blockIdx.x, t = 0; idx < p.items && ok;
+                     ok = ok && thread_next(bar->queue, t, idx, p.status, abort_flag)) {
+                    const DkvItem it = dkv_item(p, idx);
+                    const int per = it.hi - it.lo;
+                    if (per <= 0) continue;
+                    const bool fix = it.sp.Lq < p.nq && it.hi * kHalf > it.sp.Lq;
+                    const int kb = items % C::kKv;
+                    const uint32_t a = a0 + kb * 2 * C::kTileBytes;
+                    int in_head = per;
+                    ok = thread_spin(&bar->kv_full[kb], (items / C::kKv) & 1, p.status, 107, abort_flag);
+                    for (int j = per * p.group; j > 0 && ok; --j, at.next()) {
+                        ok = thread_spin(loaded + 8 * at.pos, at.phase, p.status, 103, abort_flag) &&
+                             thread_spin(done + 8 * at.before(), at.phase_before(), p.status, 105, abort_flag);
+                        if (ok && fix && --in_head == 0) {
+                            in_head = per;
+                            if (first) mbar_arrive(&bar->fix_wanted);
+                            ok = thread_spin(fixed + 8 * at.pos, fixes >> at.pos & 1, p.status, 104, abort_flag);
+                            fixes ^= 1u << at.pos;
+                        }
                         if (!ok) break;
                         tc_fence_after();
-                        mma_sum<DP>(tmem + C::kDv, tmem + 128 * av.slot, b + av.pos * (2 * C::kStepBytes) + C::kStepBytes,
-                                    j > 0 ? 1u : 0u);
-                        mma_commit(pv_done + 8 * av.pos);
-                        av.next();
+                        mma_scores<DP>(slots + 128 * at.slot, a, b + at.pos * (2 * C::kStepBytes));
+                        mma_commit(out + 8 * at.pos);
                     }
-                    if (j >= kLag) {
-                        ok = thread_spin(ds_full + 8 * ak.pos, ak.phase, p.status, 108, abort_flag);
-                        if (!ok) break;
-                        tc_fence_after();
-                        mma_sum<DP>(tmem + C::kDk, tmem + 128 * ak.slot + 64, b + ak.pos * (2 * C::kStepBytes),
-                                    j > kLag ? 1u : 0u);
-                        mma_commit(ds_done + 8 * ak.pos);
-                        ak.next();
-                    }
+                    mma_commit(&bar->kv_free[kb]);
+                    ++items;
                 }
-                mma_commit(&bar->acc_full);
-                ++items;
+                mma_commit(&bar->drain[first ? 0 : 1]);
+                mbar_wait_drain(&bar->drain[first ? 0 : 1], 0);
             }
-            mma_commit(&bar->drain[2]);
-            mbar_wait_drain(&bar->drain[2], 0);
+            __syncwarp();
+        } else {
+            if (elect_one()) {  // dV += P^T dO of each step, then dK += dS^T Q, with three slots of the step before
+                constexpr int kLag = G - 2;
+                int items = 0;
+                Ring<G, C::kStages> av, ak;
+                bool ok = true;
+                const uint32_t b = smem_u32(sT), p_full = smem_u32(bar->p_full), ds_full = smem_u32(bar->ds_full),
+                               pv_done = smem_u32(bar->pv_done), ds_done = smem_u32(bar->ds_done);
+                for (int idx = blockIdx.x, t = 0; idx < p.items && ok;
+                     ok = ok && thread_next(bar->queue, t, idx, p.status, abort_flag)) {
+                    const DkvItem it = dkv_item(p, idx);
+                    const int steps = (it.hi - it.lo) * p.group;
+                    if (steps <= 0) continue;
+                    if (items > 0) ok = thread_spin(&bar->acc_free, (items - 1) & 1, p.status, 109, abort_flag);
+                    for (int j = 0; j < steps + kLag && ok; ++j) {
+                        if (j < steps) {
+                            ok = thread_spin(p_full + 8 * av.pos, av.phase, p.status, 106, abort_flag);
+                            if (!ok) break;
+                            tc_fence_after();
+                            mma_sum<DP>(tmem + C::kDv, tmem + 128 * av.slot, b + av.pos * (2 * C::kStepBytes) + C::kStepBytes,
+                                        j > 0 ? 1u : 0u);
+                            mma_commit(pv_done + 8 * av.pos);
+                            av.next();
+                        }
+                        if (j >= kLag) {
+                            ok = thread_spin(ds_full + 8 * ak.pos, ak.phase, p.status, 108, abort_flag);
+                            if (!ok) break;
+                            tc_fence_after();
+                            mma_sum<DP>(tmem + C::kDk, tmem + 128 * ak.slot + 64, b + ak.pos * (2 * C::kStepBytes),
+                                        j > kLag ? 1u : 0u);
+                            mma_commit(ds_done + 8 * ak.pos);
+                            ak.next();
+                        }
+                    }
+                    mma_commit(&bar->acc_full);
+                    ++items;
+                }
+                mma_commit(&bar->drain[2]);
+                mbar_wait_drain(&bar->drain[2], 0);
+            }
+            __syncwarp();
         }
-        __syncwarp();
-    }
     } else {
         setmaxnreg_inc<math_regs(G)>();
         const int w = warp >> 2, row = tid & 127;

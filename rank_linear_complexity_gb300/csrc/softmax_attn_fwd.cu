@@ -288,175 +288,175 @@ softmax_attn_fwd_kernel(const __grid_constant__ CUtensorMap tQ, const __grid_con
     if (p.nsplit > 1 && tid == 0) launch_dependents();  // the join, which waits for this grid's end
 
     if (warp >= kLoadWarp) {
-    setmaxnreg_dec<kIssueRegs>();
-    if (warp == kLoadWarp) {
-        if (lane == 0) {  // ---------------- loads
-            if (kQueue) wait_prerequisites();  // the counter
-            int ring = 0, nq[2] = {0, 0}, turn = 0;
-            bool ok = true;
-            for (int idx = blockIdx.x; idx < p.items && ok;) {
-                const int following = gridDim.x + (kQueue ? atomicAdd(p.queue, 1) : idx);
-                const Item it = load_item<kSets>(p, idx);
-                for (int t = 0; t < 2 && ok; ++t) {
-                    if (it.t[t].hi <= it.t[t].lo) continue;
-                    if (nq[t] > 0 && !thread_spin(&bar->q_free[t], (nq[t] - 1) & 1, p.status, 70, abort_flag)) {
-                        ok = false;
-                        break;
-                    }
-                    mbar_arrive_expect_tx(&bar->q_full[t], (uint32_t)(p.qbox * p.hbox * DP * 2));
-                    for (int h = 0; h < DP / 64; ++h)
-                        tma_load_5d(sQ + t * C::kTileBytes + h * 16384, &tQ, &bar->q_full[t], h * 64,
-                                    it.t[t].q0, it.t[t].h0, it.kvh, it.batch);
-                    ++nq[t];
-                }
-                for (int j = it.lo; j < it.hi && ok; ++j)
-                    for (int kv = 0; kv < 2; ++kv, ++ring) {
-                        const int s = ring % C::kStages;
-                        if (ring >= C::kStages &&
-                            !thread_spin(&bar->empty[s], (ring / C::kStages - 1) & 1, p.status, 71, abort_flag)) {
+        setmaxnreg_dec<kIssueRegs>();
+        if (warp == kLoadWarp) {
+            if (lane == 0) {  // ---------------- loads
+                if (kQueue) wait_prerequisites();  // the counter
+                int ring = 0, nq[2] = {0, 0}, turn = 0;
+                bool ok = true;
+                for (int idx = blockIdx.x; idx < p.items && ok;) {
+                    const int following = gridDim.x + (kQueue ? atomicAdd(p.queue, 1) : idx);
+                    const Item it = load_item<kSets>(p, idx);
+                    for (int t = 0; t < 2 && ok; ++t) {
+                        if (it.t[t].hi <= it.t[t].lo) continue;
+                        if (nq[t] > 0 && !thread_spin(&bar->q_free[t], (nq[t] - 1) & 1, p.status, 70, abort_flag)) {
                             ok = false;
                             break;
                         }
-                        mbar_arrive_expect_tx(&bar->full[s], C::kTileBytes);
+                        mbar_arrive_expect_tx(&bar->q_full[t], (uint32_t)(p.qbox * p.hbox * DP * 2));
                         for (int h = 0; h < DP / 64; ++h)
-                            tma_load_5d(sKV + s * C::kTileBytes + h * 16384, kv ? &tV : &tK, &bar->full[s],
-                                        h * 64, j * kTile, 0, it.kvh, it.batch);
+                            tma_load_5d(sQ + t * C::kTileBytes + h * 16384, &tQ, &bar->q_full[t], h * 64,
+                                        it.t[t].q0, it.t[t].h0, it.kvh, it.batch);
+                        ++nq[t];
                     }
-                if (kQueue) ok = ok && tell(bar->queue, turn, following, p.status, abort_flag);
-                idx = following;
-            }
-            // no copy outlives the CTA
-            for (int t = 0; t < 2; ++t)
-                if (nq[t] > 0) mbar_wait_drain(&bar->q_full[t], (nq[t] - 1) & 1);
-            for (int i = max(0, ring - C::kStages); i < ring; ++i)
-                mbar_wait_drain(&bar->full[i % C::kStages], (i / C::kStages) & 1);
-        } else {  // ---------------- V rows past the valid length
-            int ring = 0, nfix = 0;
-            bool ok = true;
-            for (int idx = blockIdx.x, turn = 0; idx < p.items && ok; ok = advance(idx, turn)) {
-                const Item it = load_item<kSets>(p, idx);
-                const int blocks = max(0, it.hi - it.lo);
-                ring += 2 * blocks;
-                if (!ragged_end(it, p.nk)) continue;
-                // the issuing threads have seen the block land
-                if (!thread_spin(&bar->fix_wanted, nfix & 1, p.status, 72, abort_flag)) break;
-                ++nfix;
-                const int s = (ring - 1) % C::kStages;
-                zero_rows<DP, kTile>(sKV + s * C::kTileBytes, it.sp.Lk - (it.hi - 1) * kTile, lane - 1, 31);
-                fence_proxy_async_smem();
-                mbar_arrive(&bar->fixed);
-            }
-        }
-        __syncwarp();
-    } else if (warp == kMmaWarp || warp == kMmaWarp + 1) {
-        const int t = warp - kMmaWarp;
-        if (elect_one()) {  // ---------------- products of tile t
-            const uint32_t idesc_s = idesc_f16(128, 128, 1, 0, 0), idesc_o = idesc_f16(128, DP, 1, 0, 1);
-            const uint64_t dq = sdesc(smem_u32(sQ + t * C::kTileBytes), 16, 1024, kSwizzle128B);
-            const uint32_t tS = tmem + C::kS + 128 * t, tP = tmem + C::kP + C::kPStep * t,
-                           tO = tmem + C::kO + DP * t;
-            // The ring's entries in pairs, K and V of a block: where the next K and the next V
-            // stand (counted up, not divided out: this thread's own instructions are on the
-            // path from one product to the next).
-            constexpr int kPairs = C::kStages / 2;
-            struct At {
-                int s = 0;
-                uint32_t parity = 0;
-                __device__ __forceinline__ void next() {
-                    if (++s == kPairs) {
-                        s = 0;
-                        parity ^= 1u;
-                    }
+                    for (int j = it.lo; j < it.hi && ok; ++j)
+                        for (int kv = 0; kv < 2; ++kv, ++ring) {
+                            const int s = ring % C::kStages;
+                            if (ring >= C::kStages &&
+                                !thread_spin(&bar->empty[s], (ring / C::kStages - 1) & 1, p.status, 71, abort_flag)) {
+                                ok = false;
+                                break;
+                            }
+                            mbar_arrive_expect_tx(&bar->full[s], C::kTileBytes);
+                            for (int h = 0; h < DP / 64; ++h)
+                                tma_load_5d(sKV + s * C::kTileBytes + h * 16384, kv ? &tV : &tK, &bar->full[s],
+                                            h * 64, j * kTile, 0, it.kvh, it.batch);
+                        }
+                    if (kQueue) ok = ok && tell(bar->queue, turn, following, p.status, abort_flag);
+                    idx = following;
                 }
-            } ak, av;
-            const uint64_t dk0 = sdesc(smem_u32(sKV), 16, 1024, kSwizzle128B),
-                           dv0 = sdesc(smem_u32(sKV) + C::kTileBytes, 16384, 1024, kSwizzle128B);
-            int n = 0, items = 0;  // the tile's blocks and items
-            int nfix = 0;
-            bool ok = true;
-            for (int idx = blockIdx.x, turn = 0; idx < p.items && ok; ok = ok && advance(idx, turn)) {
-                const Item it = load_item<kSets>(p, idx);
-                const int lo = t ? it.t[1].lo : it.t[0].lo, hi = t ? it.t[1].hi : it.t[0].hi;
-                const bool fix = ragged_end(it, p.nk);
-                int ns = n;  // blocks of the tile whose S has been issued
-                // S of block j: once the last S has been read and, with P over S, its product
-                // is done
-                auto score = [&](int j) {
-                    uint64_t *full = &bar->full[2 * ak.s], *empty = &bar->empty[2 * ak.s];
-                    if (!thread_spin(full, ak.parity, p.status, 73, abort_flag)) return false;
-                    const uint64_t k = dk0 + (uint64_t)(ak.s * (int)(2 * C::kTileBytes >> 4));
-                    ak.next();
-                    if (j < lo || j >= hi) {
-                        mbar_arrive(empty);
-                        return true;
+                // no copy outlives the CTA
+                for (int t = 0; t < 2; ++t)
+                    if (nq[t] > 0) mbar_wait_drain(&bar->q_full[t], (nq[t] - 1) & 1);
+                for (int i = max(0, ring - C::kStages); i < ring; ++i)
+                    mbar_wait_drain(&bar->full[i % C::kStages], (i / C::kStages) & 1);
+            } else {  // ---------------- V rows past the valid length
+                int ring = 0, nfix = 0;
+                bool ok = true;
+                for (int idx = blockIdx.x, turn = 0; idx < p.items && ok; ok = advance(idx, turn)) {
+                    const Item it = load_item<kSets>(p, idx);
+                    const int blocks = max(0, it.hi - it.lo);
+                    ring += 2 * blocks;
+                    if (!ragged_end(it, p.nk)) continue;
+                    // the issuing threads have seen the block land
+                    if (!thread_spin(&bar->fix_wanted, nfix & 1, p.status, 72, abort_flag)) break;
+                    ++nfix;
+                    const int s = (ring - 1) % C::kStages;
+                    zero_rows<DP, kTile>(sKV + s * C::kTileBytes, it.sp.Lk - (it.hi - 1) * kTile, lane - 1, 31);
+                    fence_proxy_async_smem();
+                    mbar_arrive(&bar->fixed);
+                }
+            }
+            __syncwarp();
+        } else if (warp == kMmaWarp || warp == kMmaWarp + 1) {
+            const int t = warp - kMmaWarp;
+            if (elect_one()) {  // ---------------- products of tile t
+                const uint32_t idesc_s = idesc_f16(128, 128, 1, 0, 0), idesc_o = idesc_f16(128, DP, 1, 0, 1);
+                const uint64_t dq = sdesc(smem_u32(sQ + t * C::kTileBytes), 16, 1024, kSwizzle128B);
+                const uint32_t tS = tmem + C::kS + 128 * t, tP = tmem + C::kP + C::kPStep * t,
+                               tO = tmem + C::kO + DP * t;
+                // The ring's entries in pairs, K and V of a block: where the next K and the next V
+                // stand (counted up, not divided out: this thread's own instructions are on the
+                // path from one product to the next).
+                constexpr int kPairs = C::kStages / 2;
+                struct At {
+                    int s = 0;
+                    uint32_t parity = 0;
+                    __device__ __forceinline__ void next() {
+                        if (++s == kPairs) {
+                            s = 0;
+                            parity ^= 1u;
+                        }
                     }
-                    if (j == lo && !thread_spin(&bar->q_full[t], items & 1, p.status, 74, abort_flag)) return false;
-                    if (ns > 0 && !thread_spin(C::kSep ? &bar->s_free[t] : &bar->pv_done[t], (ns - 1) & 1,
-                                               p.status, 75, abort_flag))
-                        return false;
-                    ++ns;
-                    tc_fence_after();
-#pragma unroll
-                    for (int x = 0; x < DP / 16; ++x) {
-                        const uint64_t off = (uint64_t)((x >> 2) * 1024 + (x & 3) * 2);
-                        mma_ss(tS, dq + off, k + off, idesc_s, x > 0 ? 1u : 0u);
-                    }
-                    mma_commit(&bar->s_full[t]);
-                    mma_commit(empty);
-                    if (j == hi - 1) mma_commit(&bar->q_free[t]);
-                    return true;
-                };
-                // O += P.V of block j
-                auto output = [&](int j) {
-                    uint64_t *full = &bar->full[2 * av.s + 1], *empty = &bar->empty[2 * av.s + 1];
-                    if (!thread_spin(full, av.parity, p.status, 76, abort_flag)) return false;
-                    const uint64_t v = dv0 + (uint64_t)(av.s * (int)(2 * C::kTileBytes >> 4));
-                    if (fix && j == it.hi - 1) {
-                        mbar_arrive(&bar->fix_wanted);
-                        if (!thread_spin(&bar->fixed, nfix++ & 1, p.status, 77, abort_flag)) return false;
-                    }
-                    av.next();
-                    if (j < lo || j >= hi) {
-                        mbar_arrive(empty);
-                        return true;
-                    }
-                    // P over S comes in halves of 64 keys: the first half's products run while
-                    // the other is in its exponentials
-                    if (!thread_spin(C::kSep ? &bar->p_full[t] : &bar->p_half[t], n & 1, p.status, 78, abort_flag))
-                        return false;
-                    if (j == lo && items > 0 &&
-                        !thread_spin(&bar->o_free[t], (items - 1) & 1, p.status, 79, abort_flag))
-                        return false;
-                    tc_fence_after();
-#pragma unroll
-                    for (int x = 0; x < 4; ++x)
-                        mma_ts(tO, tP + 8 * x, v + (uint64_t)(128 * x), idesc_o, (j > lo || x > 0) ? 1u : 0u);
-                    if (!C::kSep) {
-                        if (!thread_spin(&bar->p_full[t], n & 1, p.status, 68, abort_flag)) return false;
+                } ak, av;
+                const uint64_t dk0 = sdesc(smem_u32(sKV), 16, 1024, kSwizzle128B),
+                               dv0 = sdesc(smem_u32(sKV) + C::kTileBytes, 16384, 1024, kSwizzle128B);
+                int n = 0, items = 0;  // the tile's blocks and items
+                int nfix = 0;
+                bool ok = true;
+                for (int idx = blockIdx.x, turn = 0; idx < p.items && ok; ok = ok && advance(idx, turn)) {
+                    const Item it = load_item<kSets>(p, idx);
+                    const int lo = t ? it.t[1].lo : it.t[0].lo, hi = t ? it.t[1].hi : it.t[0].hi;
+                    const bool fix = ragged_end(it, p.nk);
+                    int ns = n;  // blocks of the tile whose S has been issued
+                    // S of block j: once the last S has been read and, with P over S, its product
+                    // is done
+                    auto score = [&](int j) {
+                        uint64_t *full = &bar->full[2 * ak.s], *empty = &bar->empty[2 * ak.s];
+                        if (!thread_spin(full, ak.parity, p.status, 73, abort_flag)) return false;
+                        const uint64_t k = dk0 + (uint64_t)(ak.s * (int)(2 * C::kTileBytes >> 4));
+                        ak.next();
+                        if (j < lo || j >= hi) {
+                            mbar_arrive(empty);
+                            return true;
+                        }
+                        if (j == lo && !thread_spin(&bar->q_full[t], items & 1, p.status, 74, abort_flag)) return false;
+                        if (ns > 0 && !thread_spin(C::kSep ? &bar->s_free[t] : &bar->pv_done[t], (ns - 1) & 1,
+                                                   p.status, 75, abort_flag))
+                            return false;
+                        ++ns;
                         tc_fence_after();
+    #pragma unroll
+                        for (int x = 0; x < DP / 16; ++x) {
+                            const uint64_t off = (uint64_t)((x >> 2) * 1024 + (x & 3) * 2);
+                            mma_ss(tS, dq + off, k + off, idesc_s, x > 0 ? 1u : 0u);
+                        }
+                        mma_commit(&bar->s_full[t]);
+                        mma_commit(empty);
+                        if (j == hi - 1) mma_commit(&bar->q_free[t]);
+                        return true;
+                    };
+                    // O += P.V of block j
+                    auto output = [&](int j) {
+                        uint64_t *full = &bar->full[2 * av.s + 1], *empty = &bar->empty[2 * av.s + 1];
+                        if (!thread_spin(full, av.parity, p.status, 76, abort_flag)) return false;
+                        const uint64_t v = dv0 + (uint64_t)(av.s * (int)(2 * C::kTileBytes >> 4));
+                        if (fix && j == it.hi - 1) {
+                            mbar_arrive(&bar->fix_wanted);
+                            if (!thread_spin(&bar->fixed, nfix++ & 1, p.status, 77, abort_flag)) return false;
+                        }
+                        av.next();
+                        if (j < lo || j >= hi) {
+                            mbar_arrive(empty);
+                            return true;
+                        }
+                        // P over S comes in halves of 64 keys: the first half's products run while
+                        // the other is in its exponentials
+                        if (!thread_spin(C::kSep ? &bar->p_full[t] : &bar->p_half[t], n & 1, p.status, 78, abort_flag))
+                            return false;
+                        if (j == lo && items > 0 &&
+                            !thread_spin(&bar->o_free[t], (items - 1) & 1, p.status, 79, abort_flag))
+                            return false;
+                        tc_fence_after();
+    #pragma unroll
+                        for (int x = 0; x < 4; ++x)
+                            mma_ts(tO, tP + 8 * x, v + (uint64_t)(128 * x), idesc_o, (j > lo || x > 0) ? 1u : 0u);
+                        if (!C::kSep) {
+                            if (!thread_spin(&bar->p_full[t], n & 1, p.status, 68, abort_flag)) return false;
+                            tc_fence_after();
+                        }
+                        ++n;
+    #pragma unroll
+                        for (int x = 4; x < 8; ++x) mma_ts(tO, tP + 8 * x, v + (uint64_t)(128 * x), idesc_o, 1u);
+                        mma_commit(&bar->pv_done[t]);
+                        mma_commit(empty);
+                        return true;
+                    };
+                    // P beside S: S(j + 1) before O(j); P over S: after it
+                    if (C::kSep && it.hi > it.lo) ok = score(it.lo);
+                    for (int j = it.lo; j < it.hi && ok; ++j) {
+                        if (C::kSep) ok = (j + 1 >= it.hi || score(j + 1)) && output(j);
+                        else ok = score(j) && output(j);
                     }
-                    ++n;
-#pragma unroll
-                    for (int x = 4; x < 8; ++x) mma_ts(tO, tP + 8 * x, v + (uint64_t)(128 * x), idesc_o, 1u);
-                    mma_commit(&bar->pv_done[t]);
-                    mma_commit(empty);
-                    return true;
-                };
-                // P beside S: S(j + 1) before O(j); P over S: after it
-                if (C::kSep && it.hi > it.lo) ok = score(it.lo);
-                for (int j = it.lo; j < it.hi && ok; ++j) {
-                    if (C::kSep) ok = (j + 1 >= it.hi || score(j + 1)) && output(j);
-                    else ok = score(j) && output(j);
+                    if (hi > lo) ++items;
                 }
-                if (hi > lo) ++items;
+                mma_commit(&bar->drain[t]);
+                mbar_wait_drain(&bar->drain[t], 0);
             }
-            mma_commit(&bar->drain[t]);
-            mbar_wait_drain(&bar->drain[t], 0);
+            __syncwarp();
         }
-        __syncwarp();
-    }
     } else {
-    setmaxnreg_inc<kMathRegs>();  // ---------------- softmax of one tile, one thread a row
+        setmaxnreg_inc<kMathRegs>();  // ---------------- softmax of one tile, one thread a row
         const int t = warp >> 2, row = tid & 127;
         const uint32_t lanes = (uint32_t)((warp & 3) * 32) << 16;
         const uint32_t tS = tmem + C::kS + 128 * t + lanes, tP = tmem + C::kP + C::kPStep * t + lanes,
