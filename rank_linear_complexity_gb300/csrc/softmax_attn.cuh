@@ -68,13 +68,14 @@ __device__ __forceinline__ void place(int idx, int ranks, int units, int some, i
 // and 760, 2307 and 2351); 76 heads (80 MB) 288 and 299, 871 and 906.  With few tiles a head
 // (480 heads of 512, 63 MB) the tail of each set costs more: 56 and 51, 157 and 151.
 // Tiles under a causal mask are unequal, and all heads' longest go first where they come all at
-// once: in sets only where a set holds two items an SM, so that its short ones fill its end.
-// Backward of 32 heads over 8, d = 128, sets of one key/value head of 64 to 128 blocks and all at
-// once: 8193 rows 1617 and 1314, 12288 rows 3328 and 2886, 16384 rows 5618 and 5086; 256 heads of
-// 2048 (sets of 512 items) 853 and 941, of 4096 (480) 2950 and 3230.
+// once: in sets from 128 MB on (backward of 19 heads of 8191, d = 128, 80 MB: 830 and 780; 100 heads
+// of 4096, d = 64, 105 MB: 696 and 665), and only where a set holds two items an SM, so that its
+// short ones fill its end (32 heads over 8, sets of one key/value head of 64 to 128 blocks: 8193
+// rows 1617 and 1314, 12288 rows 3328 and 2886, 16384 rows 5618 and 5086; 256 heads of 2048, sets of
+// 512 items: 853 and 941; of 4096, of 480: 2950 and 3230).
 inline int units_at_once(int ranks, int units, int64_t bytes, bool causal, int sms) {
     constexpr int64_t kStreamed = 32 << 20;
-    const int64_t held = ranks < 16 ? 128 << 20 : 48 << 20;
+    const int64_t held = causal || ranks < 16 ? 128 << 20 : 48 << 20;
     if (ranks <= 1 || bytes * units <= held) return units;
     const int64_t some = std::max<int64_t>(1, std::min<int64_t>(units, kStreamed / bytes));
     return causal && some * ranks < 2 * sms ? units : (int)some;

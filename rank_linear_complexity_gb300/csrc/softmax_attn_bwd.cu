@@ -15,8 +15,10 @@
 //                them for the tensor memory of the next product: no transpose, no shared
 //                memory.
 // Seven products instead of five: S and dP are formed twice, which costs less than adding
-// partial dQ through memory in a fixed order.  P and dS are rounded to bf16 as operands
-// (relative 2^-9, in sums of many terms); sums are fp32 in tensor memory.
+// partial dQ through memory in a fixed order.  P and dS are rounded to bf16 as operands, since
+// the tensor cores take them at the rate of Q's and K's type only so (at most 2^-8 of each term; fp32
+// operands would cost several products for one), and delta takes the O that the forward rounded,
+// which is what its caller has.  Sums are fp32 in tensor memory.
 //
 // Both are chains of product -> arithmetic -> product, about 350 cycles from a product's last
 // cycle to the arithmetic, so they go in steps of 64 columns with several in flight: tensor

@@ -169,7 +169,7 @@ def test_several_items_a_cta(name):
 
 
 SETS = {  # heads that stream more than L2 keeps (48 MB): forward in sets without a causal mask
-    # (ragged ones from the counter, wide heads only), backward also with one
+    # (ragged ones from the counter, wide heads only), backward also with one (from 128 MB)
     "wide_all_keys": ((25, 8, 4, 2048, 1024, 128), False, {}),
     "wide_ragged": ((25, 8, 4, 2048, 1024, 128), True, {}),
     "all_keys": ((13, 16, 16, 4096, 1024, 64), False, {}),
