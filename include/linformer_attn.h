@@ -56,8 +56,8 @@
  *
  * Errors: every function returns LINFORMER_OK (0) or a negative status; no call
  * traps or aborts.  Argument errors are detected on the host before anything is
- * launched.  Device-side failures (a bounded wait that ran out) set a device
- * status word that linformer_debug_read_device_status() reads and clears.
+ * launched.  Device-side failures (a bounded wait that ran out; a page, path or tree
+ * that the device found wrong) set a device status word that linformer_debug_read_device_status() reads and clears.
  */
 #ifndef LINFORMER_ATTN_H
 #define LINFORMER_ATTN_H
@@ -99,7 +99,8 @@ typedef enum {
                                        missing in PER_HEAD / HEADWISE mode */
     LINFORMER_ERR_ALLOC = -7,       /* workspace allocation failed */
     LINFORMER_ERR_LAUNCH = -8,      /* a CUDA call or kernel launch failed */
-    LINFORMER_ERR_DEVICE = -9,      /* a device-side bounded wait ran out */
+    LINFORMER_ERR_DEVICE = -9,      /* a device-side bounded wait ran out, or a table, path or
+                                       tree on the device named what is not there */
     LINFORMER_ERR_VALUE = -10       /* a parameter or a stride is out of its range */
 } linformer_status;
 
@@ -122,7 +123,11 @@ typedef enum {
     LINFORMER_KERNEL_ROTARY = 7,    /* the kernels of linformer_rotary */
     LINFORMER_KERNEL_SOFTMAX = 8,   /* the kernels of linformer_softmax_attn_fwd */
     LINFORMER_KERNEL_SOFTMAX_BWD = 9, /* the kernels of linformer_softmax_attn_bwd */
-    LINFORMER_KERNEL_COUNT = 10
+    LINFORMER_KERNEL_CACHE = 10,    /* the kernels of linformer_cache_append, _keep and
+                                       linformer_tree_mask */
+    LINFORMER_KERNEL_PAGED = 11,    /* the kernels of linformer_paged_attn_fwd and
+                                       linformer_tree_attn_fwd */
+    LINFORMER_KERNEL_COUNT = 12
 } linformer_kernel_id;
 
 /*
@@ -336,6 +341,90 @@ LINFORMER_API int linformer_rotary(const void *X, const int64_t *X_strides, void
 LINFORMER_API int linformer_rotary_phase(uint64_t *phase, int rot, double base, int scaling,
                                          double factor, int original_length, double beta_fast,
                                          double beta_slow, void *stream);
+
+/*
+ * Paged key/value cache.  The rows of b sequences stand in pages, K_pages and V_pages
+ * [pages][hk][page][d], given with element strides {page, head, row} as int64_t[3] (NULL:
+ * dense; a cache laid out [pages][page][hk][d], or with keys and values side by side, is the
+ * same memory with other strides).  table (device int32, dense [b][width]) says which page holds
+ * rows [x page, (x + 1) page) of a sequence: table[beta][x].  Entries behind the rows in use are
+ * not read.  page is a power of two from 8 to 65536, and width page at most 2^29 (else
+ * LINFORMER_ERR_SIZE).  Several sequences may share pages that a call only reads.
+ *
+ * An entry outside [0, pages) where a row is needed, or a row behind the table's end, records a
+ * failure in the device status word; no memory outside the cache is touched.
+ */
+
+/*
+ * Appends rows: row i < counts[beta] (device int32[b]; NULL: n) of K and V [b][hk][n][d] goes to
+ * row starts[beta] + i (device int32[b]) of sequence beta.  With phase, keys are turned on the way
+ * as linformer_rotary turns them (rot, layout, amplitude, to the position positions[beta][i],
+ * device int32 dense [b][n], or starts[beta] + i where positions is NULL), and with hq > 0 the
+ * queries Q [b][hq][n][d] that stand at the same positions, all n rows of them, to Y (which may be
+ * Q, with the same strides).  Without phase the keys are copied, and hq has to be 0.
+ *
+ * Nothing else in the cache is written: not the rows behind counts, and a row that the table has
+ * no page for is dropped (and recorded).  No two rows of a call may go to one place.  dtype of all
+ * tensors LINFORMER_F32 or LINFORMER_BF16.  Pointers 16-byte aligned (phase 8; table, starts, counts and
+ * positions 4); any strides (multiples of 16 bytes, d and rot / 2 multiples of 16 bytes run fastest).
+ */
+LINFORMER_API int linformer_cache_append(
+    const void *K, const int64_t *K_strides, const void *V, const int64_t *V_strides, void *K_pages,
+    const int64_t *K_pages_strides, void *V_pages, const int64_t *V_pages_strides, const void *Q,
+    const int64_t *Q_strides, void *Y, const int64_t *Y_strides, const int32_t *table,
+    const int32_t *starts, const int32_t *counts, const uint64_t *phase, const int32_t *positions,
+    int b, int hq, int hk, int n, int d, int pages, int page, int width, int rot, int layout,
+    float amplitude, int dtype, void *stream);
+
+/*
+ * Keeps the accepted rows of a tree of drafted tokens: row starts[beta] + path[beta][i] of the
+ * cache moves to row starts[beta] + i, for i < counts[beta] (device int32[b], clamped to [0, m];
+ * NULL: m), path device int32 dense [b][m] with path[beta][i] >= i (a path from a tree's root down,
+ * nodes numbered before their children, is one).  Sources are read as they were before the call.
+ * An entry below its place is skipped and recorded in the device status word.  dtype LINFORMER_F32 or LINFORMER_BF16.
+ */
+LINFORMER_API int linformer_cache_keep(void *K_pages, const int64_t *K_pages_strides, void *V_pages,
+                                       const int64_t *V_pages_strides, const int32_t *table,
+                                       const int32_t *starts, const int32_t *path,
+                                       const int32_t *counts, int b, int hk, int m, int d, int pages,
+                                       int page, int width, int dtype, void *stream);
+
+/*
+ * Exact softmax attention over a paged cache: linformer_softmax_attn_fwd with the keys and values
+ * of sequence beta in its pages, Lk = k_lengths[beta] of them (device int32[b], clamped to
+ * [0, width page]; the new tokens' rows among them), and Lq = q_lengths[beta] queries (NULL: nq).
+ * Masks, rows without keys, rows past the lengths, sums and types are that call's: bf16, d a
+ * multiple of 8 up to 128, strides multiples of 8.  Rows of the pages behind the length may hold
+ * anything.  A page that is not there (see above) counts as rows of zeros.
+ */
+LINFORMER_API int linformer_paged_attn_fwd(
+    const void *Q, const int64_t *Q_strides, const void *K_pages, const int64_t *K_pages_strides,
+    const void *V_pages, const int64_t *V_pages_strides, void *O, const int64_t *O_strides, float *lse,
+    const int32_t *table, const int32_t *k_lengths, const int32_t *q_lengths, int b, int hq, int hk,
+    int nq, int d, int pages, int page, int width, float scale, int causal, int window, int dtype,
+    void *stream);
+
+/* Nodes of a tree of drafted tokens at most. */
+#define LINFORMER_TREE_NODES 1024
+
+/*
+ * The same for a tree of drafted tokens, the sequence's last Lq rows: query i sees every row before
+ * the tree, and node j of the tree where bit j % 64 of mask[beta][i][j / 64] is set (device, dense
+ * [b][nq][ceil(nq / 64)]; bits from Lq on are ignored).  A node's mask holds its own bit and its
+ * ancestors' as linformer_tree_mask makes it; any other mask serves as well, one that leaves a row
+ * empty among them.  nq up to LINFORMER_TREE_NODES (else LINFORMER_ERR_SIZE).
+ */
+LINFORMER_API int linformer_tree_attn_fwd(
+    const void *Q, const int64_t *Q_strides, const void *K_pages, const int64_t *K_pages_strides,
+    const void *V_pages, const int64_t *V_pages_strides, void *O, const int64_t *O_strides, float *lse,
+    const int32_t *table, const int32_t *k_lengths, const int32_t *q_lengths, const uint64_t *mask,
+    int b, int hq, int hk, int nq, int d, int pages, int page, int width, float scale, int dtype,
+    void *stream);
+
+/* mask[beta][i] for linformer_tree_attn_fwd, of trees given by each node's parent: device int32
+ * dense [b][n], -1 for a root (a tree may have several), else a node before it (an entry that is
+ * neither counts as a root and is recorded in the device status word).  n up to LINFORMER_TREE_NODES. */
+LINFORMER_API int linformer_tree_mask(const int32_t *parents, uint64_t *mask, int b, int n, void *stream);
 
 /*
  * Largest number of bytes the library's workspace pool on the current device has had

@@ -1,0 +1,290 @@
+// Rows on their way into a paged key/value cache, and within it.
+//
+// append: the new rows of each sequence go to the rows of the cache that follow its `start`,
+// keys turned to their positions, and the queries that stand at the same positions are turned
+// beside them (the turn of rotary.cu, formed in fp32 and rounded once).  Bound by memory: every
+// element read and written once.  A thread keeps the sines of its pairs and goes through several
+// heads with them, loading kBatch of them before it stores the first.
+//
+// keep: of a tree of drafted tokens, the rows of the accepted ones move up behind the sequence's
+// start.  A thread moves one piece of every row, in order, so that no other thread's store can
+// reach what it has yet to read; path[i] >= i, so neither can its own.
+//
+// tree_mask: which nodes each node of a tree sees, itself and its ancestors.
+#include <algorithm>
+#include <cuda_bf16.h>
+
+#include "internal.cuh"
+#include "paged.cuh"
+#include "rotary.cuh"
+
+namespace linformer {
+namespace paged {
+namespace {
+
+using rotary::from_float;
+using rotary::to_float;
+using rotary::Vec;
+
+constexpr int kThreads = 128;
+constexpr int kBatch = 4;      // heads in flight
+constexpr int kMaxHeads = 16;  // heads of one thread
+
+struct AppendParams {
+    Cache cache;
+    const void *x[3];
+    Strides sx[3];
+    void *y;
+    Strides sy;
+    const int32_t *starts, *counts, *positions;
+    const uint64_t *phase;
+    int hq, hk, heads, n, rot, chunks, rot_chunks, per_thread, splits;
+    int64_t threads;
+    float amplitude;
+    int *status;
+};
+
+// V pairs a thread (V = 1: any strides and sizes; otherwise 16-byte pieces).
+template <typename T, int V, bool kInterleaved>
+__global__ void __launch_bounds__(kThreads) append_kernel(const AppendParams p) {
+    using Piece = Vec<T, V>;
+    const int64_t tid = (int64_t)blockIdx.x * kThreads + threadIdx.x;
+    if (tid >= p.threads) return;
+    const int c = (int)(tid % p.chunks);
+    const int64_t r = tid / p.chunks;
+    const int i = (int)(r % p.n);
+    const int64_t r2 = r / p.n;
+    const int split = (int)(r2 % p.splits), b = (int)(r2 / p.splits);
+    const int h0 = split * p.per_thread, h1 = min(h0 + p.per_thread, p.heads);
+    const int start = __ldg(p.starts + b);
+    // rows behind the sequence's last, and those without a page, leave the cache as it was
+    int page = 0, row = 0;
+    bool kept = h1 > p.hq && (!p.counts || i < __ldg(p.counts + b));
+    if (kept) kept = find_row(p.cache, b, (int64_t)start + i, p.status, page, row);
+    const bool turn = c < p.rot_chunks;
+    // the two pieces of the thread's pairs (of the copied rest: one)
+    const int at0 = turn ? (kInterleaved ? 2 * V * c : V * c) : p.rot + V * (c - p.rot_chunks);
+    const int at1 = turn ? (kInterleaved ? at0 + V : at0 + p.rot / 2) : at0;
+    float cs[V], sn[V];
+    if (turn && h0 < p.hq + p.hk) {
+        const int pos = p.positions ? __ldg(p.positions + (int64_t)b * p.n + i) : (int)((unsigned)start + (unsigned)i);
+#pragma unroll
+        for (int v = 0; v < V; ++v) {
+            rotary::turn_of(__ldg(p.phase + V * c + v), pos, cs[v], sn[v]);
+            cs[v] *= p.amplitude;
+            sn[v] *= p.amplitude;
+        }
+    }
+    for (int h = h0; h < h1; h += kBatch) {
+        Piece u0[kBatch], u1[kBatch];
+        T *to[kBatch];
+#pragma unroll
+        for (int k = 0; k < kBatch; ++k) {
+            const int hh = h + k;
+            const int w = hh < p.hq ? 0 : hh < p.hq + p.hk ? 1 : 2;
+            const int head = hh - (w == 0 ? 0 : w == 1 ? p.hq : p.hq + p.hk);
+            to[k] = nullptr;
+            if (hh >= h1 || (w && !kept)) continue;
+            const T *x = static_cast<const T *>(p.x[w]) + b * p.sx[w].b + head * p.sx[w].h + i * p.sx[w].n;
+            const Strides &s = w == 0 ? p.sy : w == 1 ? p.cache.sk : p.cache.sv;
+            to[k] = static_cast<T *>(w == 0 ? p.y : w == 1 ? p.cache.k : p.cache.v) +
+                    (w == 0 ? b * s.b + head * s.h + i * s.n : page * s.b + head * s.h + row * s.n);
+            u0[k] = *reinterpret_cast<const Piece *>(x + at0);
+            if (turn) u1[k] = *reinterpret_cast<const Piece *>(x + at1);
+        }
+#pragma unroll
+        for (int k = 0; k < kBatch; ++k) {
+            if (!to[k]) continue;
+            if (turn) {
+                if (h + k < p.hq + p.hk) {
+#pragma unroll
+                    for (int v = 0; v < V; ++v) {
+                        // interleaved: elements 2 v and 2 v + 1 of the two pieces in a row
+                        T &a = kInterleaved ? (2 * v < V ? u0[k].e[(2 * v) % V] : u1[k].e[(2 * v) % V]) : u0[k].e[v];
+                        T &z = kInterleaved ? (2 * v + 1 < V ? u0[k].e[(2 * v + 1) % V] : u1[k].e[(2 * v + 1) % V])
+                                            : u1[k].e[v];
+                        const float fa = to_float(a), fz = to_float(z);
+                        a = from_float<T>(fa * cs[v] - fz * sn[v]);
+                        z = from_float<T>(fz * cs[v] + fa * sn[v]);
+                    }
+                }
+                *reinterpret_cast<Piece *>(to[k] + at1) = u1[k];
+            }
+            *reinterpret_cast<Piece *>(to[k] + at0) = u0[k];
+        }
+    }
+}
+
+struct KeepParams {
+    Cache cache;
+    const int32_t *starts, *path, *counts;
+    int hk, m, chunks;
+    int64_t threads;
+    int *status;
+};
+
+// One piece of every accepted row of one head of one sequence, of the keys or of the values.
+template <typename T, int V>
+__global__ void __launch_bounds__(kThreads) keep_kernel(const KeepParams p) {
+    using Piece = Vec<T, V>;
+    const int64_t tid = (int64_t)blockIdx.x * kThreads + threadIdx.x;
+    if (tid >= p.threads) return;
+    const int c = (int)(tid % p.chunks);
+    int64_t r = tid / p.chunks;
+    const int head = (int)(r % p.hk);
+    r /= p.hk;
+    const bool value = r & 1;
+    const int b = (int)(r >> 1);
+    const Strides s = value ? p.cache.sv : p.cache.sk;
+    T *base = static_cast<T *>(value ? p.cache.v : p.cache.k) + head * s.h + V * c;
+    const int64_t start = __ldg(p.starts + b);
+    const int count = p.counts ? min(max(__ldg(p.counts + b), 0), p.m) : p.m;
+    const int32_t *path = p.path + (int64_t)b * p.m;
+    constexpr int kRows = 8;  // rows in flight: sources of later rows lie behind all their targets
+    for (int i = 0; i < count; i += kRows) {
+        Piece u[kRows];
+        T *to[kRows];
+#pragma unroll
+        for (int k = 0; k < kRows; ++k) {
+            to[k] = nullptr;
+            if (i + k >= count) continue;
+            const int node = __ldg(path + i + k);
+            if (node == i + k) continue;  // in its place
+            int page, row, page2, row2;
+            if (node < i + k) {
+                if (p.status) atomicExch(p.status, kBadPath);
+                continue;
+            }
+            if (!find_row(p.cache, b, start + i + k, p.status, page, row) ||
+                !find_row(p.cache, b, start + node, p.status, page2, row2))
+                continue;
+            to[k] = base + page * s.b + row * s.n;
+            u[k] = *reinterpret_cast<const Piece *>(base + page2 * s.b + row2 * s.n);
+        }
+#pragma unroll
+        for (int k = 0; k < kRows; ++k)
+            if (to[k]) *reinterpret_cast<Piece *>(to[k]) = u[k];
+    }
+}
+
+// A sequence a block, a node a thread: its ancestors come in falling order, so their bits are
+// gathered a word at a time.
+__global__ void __launch_bounds__(1024) tree_mask_kernel(const int32_t *parents, uint64_t *mask, int n, int words,
+                                                         int *status) {
+    __shared__ int parent[1024];
+    const int i = threadIdx.x;
+    const int64_t b = blockIdx.x;
+    if (i < n) {
+        int x = __ldg(parents + b * n + i);
+        if (x < -1 || x >= i) {
+            if (status) atomicExch(status, kBadParent);
+            x = -1;
+        }
+        parent[i] = x;
+    }
+    __syncthreads();
+    if (i >= n) return;
+    uint64_t *row = mask + (b * n + i) * words;
+    int at = i;
+    for (int w = words - 1; w >= 0; --w) {
+        uint64_t bits = 0;
+        for (; at >= 64 * w; at = parent[at]) bits |= 1ull << (at & 63);  // (-1 is below every word)
+        row[w] = bits;
+    }
+}
+
+template <typename T, int V>
+int launch_append(const AppendParams &p, bool interleaved, cudaStream_t s) {
+    const int64_t blocks = (p.threads + kThreads - 1) / kThreads;
+    if (blocks > 0x7fffffffLL) return LINFORMER_ERR_SIZE;
+    KernelScope scope(LINFORMER_KERNEL_CACHE, s);
+    if (interleaved) append_kernel<T, V, true><<<(unsigned)blocks, kThreads, 0, s>>>(p);
+    else append_kernel<T, V, false><<<(unsigned)blocks, kThreads, 0, s>>>(p);
+    return cudaGetLastError() == cudaSuccess ? LINFORMER_OK : LINFORMER_ERR_LAUNCH;
+}
+
+template <typename T, int V>
+int launch_keep(const KeepParams &p, cudaStream_t s) {
+    const int64_t blocks = (p.threads + kThreads - 1) / kThreads;
+    if (blocks > 0x7fffffffLL) return LINFORMER_ERR_SIZE;
+    KernelScope scope(LINFORMER_KERNEL_CACHE, s);
+    keep_kernel<T, V><<<(unsigned)blocks, kThreads, 0, s>>>(p);
+    return cudaGetLastError() == cudaSuccess ? LINFORMER_OK : LINFORMER_ERR_LAUNCH;
+}
+
+// Whether 16-byte pieces of V elements stay aligned over the dimensions of more than one entry.
+bool pieces(const Strides &s, int b, int heads, int n, int V) {
+    return (b == 1 || s.b % V == 0) && (heads == 1 || s.h % V == 0) && (n == 1 || s.n % V == 0);
+}
+bool pieces(const Cache &c, int hk, int V) {
+    return pieces(c.sk, c.pages, hk, c.page, V) && pieces(c.sv, c.pages, hk, c.page, V);
+}
+
+}  // namespace
+
+int append(const AppendCall &c) {
+    AppendParams p{};
+    const int V = c.dtype == LINFORMER_F32 ? 4 : 8;
+    bool wide = c.d % V == 0 && c.rot % (2 * V) == 0 && pieces(c.cache, c.hk, V);
+    for (int w = 0; w < 3; ++w) {
+        p.x[w] = c.x[w];
+        p.sx[w] = c.sx[w];
+        if (w || c.hq) wide = wide && pieces(c.sx[w], c.b, w ? c.hk : c.hq, c.n, V);
+    }
+    if (c.hq) wide = wide && pieces(c.sy, c.b, c.hq, c.n, V);
+    const int v = wide ? V : 1;
+    p.cache = c.cache;
+    p.y = c.y;
+    p.sy = c.sy;
+    p.starts = c.starts;
+    p.counts = c.counts;
+    p.positions = c.positions;
+    p.phase = c.phase;
+    p.hq = c.hq;
+    p.hk = c.hk;
+    p.heads = c.hq + 2 * c.hk;
+    p.n = c.n;
+    p.rot = c.rot;
+    p.rot_chunks = c.rot / 2 / v;
+    p.chunks = p.rot_chunks + (c.d - c.rot) / v;
+    p.amplitude = c.amplitude;
+    p.status = device_status_ptr();
+    // Heads a thread: as in rotary.cu, as many as leave two full waves of threads.
+    const int64_t rows = (int64_t)c.b * c.n * p.chunks;
+    constexpr int64_t kSmThreads = 2048;
+    const int64_t per = rows * p.heads / (2 * device_sms() * kSmThreads);
+    p.per_thread = (int)std::max<int64_t>(1, std::min<int64_t>(std::min(p.heads, kMaxHeads), per));
+    p.splits = (p.heads + p.per_thread - 1) / p.per_thread;
+    p.threads = rows * p.splits;
+    if (c.dtype == LINFORMER_F32)
+        return wide ? launch_append<float, 4>(p, c.interleaved, c.stream)
+                    : launch_append<float, 1>(p, c.interleaved, c.stream);
+    return wide ? launch_append<__nv_bfloat16, 8>(p, c.interleaved, c.stream)
+                : launch_append<__nv_bfloat16, 1>(p, c.interleaved, c.stream);
+}
+
+int keep(const KeepCall &c) {
+    KeepParams p{};
+    const int V = c.dtype == LINFORMER_F32 ? 4 : 8;
+    const bool wide = c.d % V == 0 && pieces(c.cache, c.hk, V);
+    p.cache = c.cache;
+    p.starts = c.starts;
+    p.path = c.path;
+    p.counts = c.counts;
+    p.hk = c.hk;
+    p.m = c.m;
+    p.chunks = wide ? c.d / V : c.d;
+    p.threads = (int64_t)c.b * 2 * c.hk * p.chunks;
+    p.status = device_status_ptr();
+    if (c.dtype == LINFORMER_F32) return wide ? launch_keep<float, 4>(p, c.stream) : launch_keep<float, 1>(p, c.stream);
+    return wide ? launch_keep<__nv_bfloat16, 8>(p, c.stream) : launch_keep<__nv_bfloat16, 1>(p, c.stream);
+}
+
+int tree_mask(const int32_t *parents, uint64_t *mask, int b, int n, cudaStream_t s) {
+    KernelScope scope(LINFORMER_KERNEL_CACHE, s);
+    tree_mask_kernel<<<b, (n + 31) / 32 * 32, 0, s>>>(parents, mask, n, (n + 63) / 64, device_status_ptr());
+    return cudaGetLastError() == cudaSuccess ? LINFORMER_OK : LINFORMER_ERR_LAUNCH;
+}
+
+}  // namespace paged
+}  // namespace linformer

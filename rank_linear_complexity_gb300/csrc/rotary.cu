@@ -39,24 +39,6 @@ struct Params {
     float amplitude, sign;
 };
 
-template <typename T>
-__device__ __forceinline__ float to_float(T x);
-template <>
-__device__ __forceinline__ float to_float(float x) { return x; }
-template <>
-__device__ __forceinline__ float to_float(__nv_bfloat16 x) { return __bfloat162float(x); }
-template <typename T>
-__device__ __forceinline__ T from_float(float x);
-template <>
-__device__ __forceinline__ float from_float(float x) { return x; }
-template <>
-__device__ __forceinline__ __nv_bfloat16 from_float(float x) { return __float2bfloat16_rn(x); }
-
-template <typename T, int V>
-struct alignas(sizeof(T) * V) Vec {
-    T e[V];
-};
-
 // V pairs a thread (V = 1: any strides and sizes; otherwise 16-byte pieces).
 template <typename T, int V, bool kInterleaved>
 __global__ void __launch_bounds__(kThreads) rotary_kernel(const Params p) {
@@ -78,15 +60,10 @@ __global__ void __launch_bounds__(kThreads) rotary_kernel(const Params p) {
         const int pos = p.positions ? __ldg(p.positions + (int64_t)b * p.n + i) : p.start + i;
 #pragma unroll
         for (int v = 0; v < V; ++v) {
-            const uint64_t turns = __ldg(p.phase + V * c + v) * (uint64_t)(int64_t)pos;
-            float s, k;
-            // the top 32 bits of a turn as the nearest quarter and a signed rest of at most an
-            // eighth, which a float holds to 2^-27 half turns (the whole turn: to 2^-25)
-            const uint32_t t = (uint32_t)(turns >> 32), quarter = (t + 0x20000000u) >> 30;
-            sincospif((float)(int32_t)(t - (quarter << 30)) * 0x1p-31f, &s, &k);
-            const float c0 = quarter & 1 ? -s : k, s0 = quarter & 1 ? k : s;
-            cs[v] = (quarter & 2 ? -c0 : c0) * p.amplitude;
-            sn[v] = (quarter & 2 ? -s0 : s0) * p.sign;
+            float c0, s0;
+            turn_of(__ldg(p.phase + V * c + v), pos, c0, s0);
+            cs[v] = c0 * p.amplitude;
+            sn[v] = s0 * p.sign;
         }
     }
 #pragma unroll 4

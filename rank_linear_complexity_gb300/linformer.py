@@ -17,7 +17,7 @@ from . import build as _build
 PER_HEAD, KV, HEADWISE, LAYERWISE = 0, 1, 2, 3
 F32, BF16, BF16_F32OUT = 0, 1, 2
 PATH_SIMT, PATH_TENSOR = 0, 1
-KERNEL_COUNT = 10
+KERNEL_COUNT = 12
 ROTARY_HALVES, ROTARY_INTERLEAVED = 0, 1
 ROTARY_PLAIN, ROTARY_LINEAR, ROTARY_BASE, ROTARY_BY_PARTS = 0, 1, 2, 3
 
@@ -37,6 +37,8 @@ SYMBOLS = [
     "linformer_window_projection", "linformer_attn_bwd", "linformer_dense_attn_fwd",
     "linformer_pool_peak_bytes", "linformer_debug_wait_probe", "linformer_softmax_attn_fwd",
     "linformer_softmax_attn_bwd", "linformer_rotary", "linformer_rotary_phase",
+    "linformer_cache_append", "linformer_cache_keep", "linformer_paged_attn_fwd",
+    "linformer_tree_attn_fwd", "linformer_tree_mask",
 ]
 
 
@@ -108,6 +110,16 @@ def lib() -> ctypes.CDLL:
             L.linformer_rotary.restype = _i
             L.linformer_rotary_phase.argtypes = [_vp, _i, _d, _i, _d, _i, _d, _d, _vp]
             L.linformer_rotary_phase.restype = _i
+            L.linformer_cache_append.argtypes = [_vp] * 17 + [_i] * 10 + [_f, _i, _vp]
+            L.linformer_cache_append.restype = _i
+            L.linformer_cache_keep.argtypes = [_vp] * 8 + [_i] * 8 + [_vp]
+            L.linformer_cache_keep.restype = _i
+            L.linformer_paged_attn_fwd.argtypes = [_vp] * 12 + [_i] * 8 + [_f] + [_i] * 3 + [_vp]
+            L.linformer_paged_attn_fwd.restype = _i
+            L.linformer_tree_attn_fwd.argtypes = [_vp] * 13 + [_i] * 8 + [_f, _i, _vp]
+            L.linformer_tree_attn_fwd.restype = _i
+            L.linformer_tree_mask.argtypes = [_vp] * 2 + [_i] * 2 + [_vp]
+            L.linformer_tree_mask.restype = _i
             L.linformer_kernel_name.argtypes = [_i]
             L.linformer_kernel_name.restype = ctypes.c_char_p
             _lib = L
@@ -574,3 +586,192 @@ def rotary(x, x2=None, phase=None, positions=None, start: int = 0, rot=None,
            1 if inverse else 0, dtype_code(x), handle),
           "linformer_rotary")
     return out if x2 is None else (out, out2)
+
+
+# --- a paged key/value cache ----------------------------------------------------------------
+#
+# k_cache and v_cache [pages][hk][page][d] (any strides: a cache laid out [pages][page][hk][d] is
+# its transpose(1, 2), one with keys and values side by side two slices), table int32 [b][width]:
+# the pages of each sequence in order.  A page, path or tree on the device that is not there is
+# recorded in the device status word, as a wait that ran out is.
+
+def _check_cache(k_cache, v_cache, table, b, hk, d, dtype):
+    """(pages, page, width) of a cache that fits the call's tensors."""
+    import torch
+    shape = k_cache.shape
+    pages, heads, page, dim = shape
+    if heads != hk or dim != d or k_cache.dtype != dtype:
+        _check("k_cache", k_cache, (pages, hk, page, d), dtype)
+    _check("v_cache", v_cache, shape, dtype)
+    width = table.shape[-1]
+    _check_dense("table", table, (b, width), torch.int32)
+    if pages > 0x7fffffff or page > 0x7fffffff or width > 0x7fffffff:
+        _sizes("k_cache", shape)
+        _sizes("table", table.shape)
+    return pages, page, width
+
+
+def cache_append(K, V, k_cache, v_cache, table, starts, counts=None, Q=None, phase=None,
+                 positions=None, rot=None, layout: int = ROTARY_HALVES, amplitude: float = 1.0,
+                 out=None, stream=None):
+    """Rows i < counts[b] (None: all) of K and V [b][hk][n][d] into rows starts[b] + i of the
+    cache, keys turned to their positions where phase is given (the table of rotary_phase();
+    positions int32 [b][n], or None for starts[b] + i).  Q [b][hq][n][d], at the same positions, is
+    turned in the same call: returns it (in `out`, which may be Q), or None without Q."""
+    import torch
+    if stream is not None:
+        with _current_on(K.device, stream):
+            return cache_append(K, V, k_cache, v_cache, table, starts, counts, Q, phase, positions,
+                                rot, layout, amplitude, out)
+    shape, dtype, device = K.shape, K.dtype, K.device
+    b, hk, n, d = shape
+    _sizes("K", shape)
+    handle = _stream_of(device, V, k_cache, v_cache, table, starts, counts, Q, phase, positions, out)
+    _check("V", V, shape, dtype)
+    pages, page, width = _check_cache(k_cache, v_cache, table, b, hk, d, dtype)
+    _check_dense("starts", starts, (b,), torch.int32)
+    if counts is not None:
+        _check_dense("counts", counts, (b,), torch.int32)
+        counts = counts.data_ptr()
+    if phase is not None:
+        rot = d if rot is None else _int32("rot", rot)
+        _int32("layout", layout)
+        _check_dense("phase", phase, (rot // 2,), torch.int64)
+        phase = phase.data_ptr()
+        if positions is not None:
+            _check_dense("positions", positions, (b, n), torch.int32)
+            positions = positions.data_ptr()
+    elif Q is not None or positions is not None or rot is not None:
+        raise ValueError("phase: the table of rotary_phase() is needed to turn keys and queries")
+    else:
+        rot = 0
+    pq = sq = py = sy = None
+    hq = 0
+    if Q is not None:
+        hq = _int32("Q's heads", Q.shape[1])
+        _check("Q", Q, (b, hq, n, d), dtype)
+        if out is None:
+            out = torch.empty_like(Q)
+        else:
+            _check("out", out, Q.shape, dtype)
+        pq, sq, py, sy = Q.data_ptr(), _strides(Q), out.data_ptr(), _strides(out)
+    elif out is not None:
+        raise ValueError("out: Q is needed")
+    _call(lib().linformer_cache_append, device,
+          (K.data_ptr(), _strides(K), V.data_ptr(), _strides(V), k_cache.data_ptr(),
+           _strides(k_cache), v_cache.data_ptr(), _strides(v_cache), pq, sq, py, sy,
+           table.data_ptr(), starts.data_ptr(), counts, phase, positions, b, hq, hk, n, d, pages,
+           page, width, rot, layout, amplitude, dtype_code(K), handle),
+          "linformer_cache_append")
+    return out
+
+
+def cache_keep(k_cache, v_cache, table, starts, path, counts=None, stream=None):
+    """Moves the accepted rows of each sequence's tree, starts[b] + path[b][i], to starts[b] + i,
+    for i < counts[b] (None: all of path int32 [b][m]), path[b][i] >= i."""
+    import torch
+    if stream is not None:
+        with _current_on(k_cache.device, stream):
+            return cache_keep(k_cache, v_cache, table, starts, path, counts)
+    device, dtype = k_cache.device, k_cache.dtype
+    _, hk, _, d = k_cache.shape
+    b, m = path.shape
+    _sizes("path", path.shape)
+    handle = _stream_of(device, v_cache, table, starts, path, counts)
+    _sizes("k_cache", k_cache.shape)
+    pages, page, width = _check_cache(k_cache, v_cache, table, b, hk, d, dtype)
+    _check_dense("starts", starts, (b,), torch.int32)
+    _check_dense("path", path, (b, m), torch.int32)
+    if counts is not None:
+        _check_dense("counts", counts, (b,), torch.int32)
+        counts = counts.data_ptr()
+    _call(lib().linformer_cache_keep, device,
+          (k_cache.data_ptr(), _strides(k_cache), v_cache.data_ptr(), _strides(v_cache),
+           table.data_ptr(), starts.data_ptr(), path.data_ptr(), counts, b, hk, m, d, pages, page,
+           width, dtype_code(k_cache), handle),
+          "linformer_cache_keep")
+
+
+def _over_pages(Q, k_cache, v_cache, table, k_lengths, q_lengths, scale, out, lse, mask, masks,
+                call, name):
+    """What paged_attention and tree_attention share; masks: the integers between scale and
+    dtype."""
+    import torch
+    shape, dtype, device = Q.shape, Q.dtype, Q.device
+    b, hq, n, d = shape
+    _sizes("Q", shape)
+    handle = _stream_of(device, k_cache, v_cache, table, k_lengths, q_lengths, out, lse, mask)
+    hk = _int32("k_cache's heads", k_cache.shape[1])
+    pages, page, width = _check_cache(k_cache, v_cache, table, b, hk, d, dtype)
+    if out is None:
+        out = torch.empty(shape, dtype=dtype, device=device)
+    else:
+        _check("out", out, shape, dtype)
+    if lse is None:
+        lse = torch.empty((b, hq, n), dtype=torch.float32, device=device)
+    else:
+        _check_dense("lse", lse, (b, hq, n), torch.float32)
+    _check_dense("k_lengths", k_lengths, (b,), torch.int32)
+    if q_lengths is not None:
+        _check_dense("q_lengths", q_lengths, (b,), torch.int32)
+        q_lengths = q_lengths.data_ptr()
+    head = (Q.data_ptr(), _strides(Q), k_cache.data_ptr(), _strides(k_cache), v_cache.data_ptr(),
+            _strides(v_cache), out.data_ptr(), _strides(out), lse.data_ptr(), table.data_ptr(),
+            k_lengths.data_ptr(), q_lengths)
+    if mask is not None:
+        _check_dense("mask", mask, (b, n, (n + 63) // 64), torch.int64)
+        head += (mask.data_ptr(),)
+    _call(call, device,
+          head + (b, hq, hk, n, d, pages, page, width, d ** -0.5 if scale is None else scale)
+          + masks + (dtype_code(Q), handle), name)
+    return out, lse
+
+
+def paged_attention(Q, k_cache, v_cache, table, k_lengths, q_lengths=None, causal: bool = True,
+                    window: int = 0, scale=None, out=None, lse=None, stream=None):
+    """(O, lse) of the exact attention of Q [b][hq][n][d], the last n (or q_lengths[b]) tokens of
+    each sequence, over the k_lengths[b] (int32 [b]) rows that it has in the cache: single tokens, a
+    few, or a chunk of a prompt.  Masks and results are softmax_attention's."""
+    if stream is not None:
+        with _current_on(Q.device, stream):
+            return paged_attention(Q, k_cache, v_cache, table, k_lengths, q_lengths, causal, window,
+                                   scale, out, lse)
+    return _over_pages(Q, k_cache, v_cache, table, k_lengths, q_lengths, scale, out, lse, None,
+                       (1 if causal else 0, _int32("window", window)),
+                       lib().linformer_paged_attn_fwd, "linformer_paged_attn_fwd")
+
+
+def tree_attention(Q, k_cache, v_cache, table, k_lengths, mask, q_lengths=None, scale=None,
+                   out=None, lse=None, stream=None):
+    """(O, lse) as paged_attention, for a tree of drafted tokens: query i sees every row before the
+    tree, and the nodes of the tree whose bits are set in mask[b][i] (int64 [b][n][ceil(n / 64)],
+    tree_mask())."""
+    if stream is not None:
+        with _current_on(Q.device, stream):
+            return tree_attention(Q, k_cache, v_cache, table, k_lengths, mask, q_lengths, scale, out,
+                                  lse)
+    if mask is None:
+        raise ValueError("mask: the words of tree_mask() are needed")
+    return _over_pages(Q, k_cache, v_cache, table, k_lengths, q_lengths, scale, out, lse, mask, (),
+                       lib().linformer_tree_attn_fwd, "linformer_tree_attn_fwd")
+
+
+def tree_mask(parents, out=None, stream=None):
+    """int64 [b][n][ceil(n / 64)]: bit j of row i where j is i or one of its ancestors, of trees
+    given by parents int32 [b][n] (-1 for a root, else a node before)."""
+    import torch
+    if stream is not None:
+        with _current_on(parents.device, stream):
+            return tree_mask(parents, out)
+    b, n = parents.shape
+    _sizes("parents", parents.shape)
+    handle = _stream_of(parents.device, out)
+    _check_dense("parents", parents, (b, n), torch.int32)
+    shape = (b, n, (n + 63) // 64)
+    if out is None:
+        out = torch.empty(shape, dtype=torch.int64, device=parents.device)
+    else:
+        _check_dense("out", out, shape, torch.int64)
+    _call(lib().linformer_tree_mask, parents.device,
+          (parents.data_ptr(), out.data_ptr(), b, n, handle), "linformer_tree_mask")
+    return out

@@ -1,0 +1,474 @@
+"""GPU tests of the paged key/value cache against its fp64 oracle: rows appended and kept, trees,
+attention over the pages, and all of them together."""
+import numpy as np
+import pytest
+import torch
+
+import rank_linear_complexity_gb300.linformer as lf
+from oracle import paged, rotary
+from oracle.softmax_attention import host64
+from tests.paged_cases import bits, cache, ints, random_tree
+
+pytestmark = pytest.mark.gpu
+DEV = torch.device("cuda:0")
+BF = torch.bfloat16
+
+
+def status():
+    torch.cuda.synchronize()
+    assert lf.linformer_debug_read_device_status() == 0
+
+
+def error_code():
+    torch.cuda.synchronize()
+    return lf.linformer_debug_read_device_status()
+
+
+# --- append ---------------------------------------------------------------------------------
+
+def check_append(b=3, hq=4, hk=2, n=5, d=64, page=16, starts=(0, 15, 33), counts=None, layout="rows",
+                 dtype="bf16", rot=None, interleaved=False, amplitude=1.0, turn=True, queries=True,
+                 placed=False, in_place=False, odd=False, seed=0, far=0):
+    """Every element of the caches and of the turned queries against the oracle; whatever is not
+    written keeps its bits (NaN among them)."""
+    lengths = [s + n for s in starts]
+    kc, vc, table = cache(b, hk, d, page, lengths, layout, dtype, seed, device=DEV)
+    if odd:  # strides that are no multiples of 16 bytes
+        wide = torch.full((*kc.shape[:3], d + 1), float("nan"), dtype=kc.dtype, device=DEV)
+        wide[..., :d] = kc
+        kc = wide[..., :d]
+    g = torch.Generator(device=DEV).manual_seed(seed + 1)
+    K, V, Q = (torch.randn(b, n, h, d, generator=g, device=DEV).to(kc.dtype).transpose(1, 2)
+               for h in (hk, hk, hq))
+    rot = d if rot is None else rot
+    f = rotary.frequencies(rot)
+    positions = None
+    if placed:
+        positions = torch.randint(far, far + 1000, (b, n), generator=g, device=DEV, dtype=torch.int32)
+    before = kc.clone(), vc.clone()
+    kw = {}
+    if turn:
+        kw = dict(phase=torch.from_numpy(rotary.phase_words(f)).to(DEV), rot=rot, positions=positions,
+                  layout=lf.ROTARY_INTERLEAVED if interleaved else lf.ROTARY_HALVES,
+                  amplitude=amplitude)
+    want = paged.append(K, V, kc, vc, table.tolist(), starts, counts, f if turn else None,
+                        None if positions is None else positions.cpu().numpy(), rot, interleaved,
+                        amplitude, Q if turn and queries else None)
+    if turn and queries:
+        kw["Q"] = Q
+        if in_place:
+            kw["out"] = Q
+    got = lf.cache_append(K, V, kc, vc, table, ints(starts, DEV),
+                          counts=None if counts is None else ints(counts, DEV), **kw)
+    status()
+    # the turn in fp32 (angle and sines to 2^-22, two products and a sum), rounded once: half a step
+    half = 2.0 ** -8 if dtype == "bf16" else 2.0 ** -24
+
+    def near(x, y, turned):
+        x = host64(x)
+        assert np.array_equal(np.isnan(x), np.isnan(y))
+        x, y = np.nan_to_num(x), np.nan_to_num(y)
+        if not turned:
+            assert np.array_equal(x, y)
+            return
+        # |x_a| + |x_z| < 10: sines off by 2^-23 each, a product rounded by 2^-24, so 15 2^-23; the
+        # oracle's angle at position 2^31, a double, by 2 x 2^-22, so another 20 2^-22
+        reach = amplitude * (24.0 if far else 8.0)
+        assert (np.abs(x - y) <= half * np.abs(y) + 2.0 ** -21 * reach).all()
+    near(kc, want[0], turn)
+    near(vc, want[1], False)
+    if turn and queries:
+        assert got is (Q if in_place else got)
+        near(got, want[2], True)
+    else:
+        assert got is None
+    # rows that no sequence got keep their bits
+    touched = np.zeros((kc.shape[0], page), dtype=bool)
+    for bi in range(b):
+        for i in range(n if counts is None else min(max(counts[bi], 0), n)):
+            p, r = paged.place(kc, table.tolist()[bi], starts[bi] + i)
+            touched[p, r] = True
+    rest = torch.from_numpy(~touched).to(DEV)[:, None, :, None].expand(kc.shape)
+    for x, y in zip((kc, vc), before):
+        assert torch.equal(bits(x)[rest], bits(y)[rest])
+
+
+@pytest.mark.parametrize("layout", ["rows", "heads", "fused"])
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("interleaved", [False, True])
+def test_append(layout, dtype, interleaved):
+    check_append(layout=layout, dtype=dtype, interleaved=interleaved)
+
+
+@pytest.mark.parametrize("kw", [
+    dict(n=1, starts=(0, 15, 16)), dict(n=40, starts=(0, 7, 130), page=8), dict(n=3, page=256),
+    dict(rot=32), dict(d=40, rot=40), dict(d=40, rot=20, dtype="f32"), dict(d=5, rot=4), dict(d=80, rot=16),
+    dict(d=128, hq=32, hk=8, n=7), dict(hq=1, hk=1), dict(b=1, starts=(3,)),
+    dict(counts=(0, 5, 3)), dict(counts=(-2, 9, 1)), dict(turn=False), dict(queries=False),
+    dict(placed=True), dict(placed=True, far=2 ** 31 - 2000), dict(amplitude=1.2), dict(in_place=True),
+    dict(odd=True), dict(odd=True, dtype="f32", interleaved=True), dict(n=700, starts=(0, 1, 2), d=128),
+    dict(b=70, starts=tuple(range(70)), n=1),
+])
+def test_append_shapes(kw):
+    check_append(**kw)
+
+
+def test_append_rows_without_a_page():
+    """A table entry that names no page, a row behind the table, a start below zero: dropped and
+    recorded, everything else written."""
+    for starts, table_row, bad in (((14,), [0, 9], 0), ((14,), [0, -1], 0), ((30,), [0, 1], 1), ((-1,), [0, 1], 1)):
+        kc = torch.full((2, 2, 16, 64), 7.0, dtype=BF, device=DEV)
+        vc = kc.clone()
+        K, V = torch.ones(2, 1, 2, 4, 64, dtype=BF, device=DEV)
+        lf.cache_append(K, V, kc, vc, ints([table_row], DEV), ints(starts, DEV))
+        assert error_code() != 0
+        want = paged.append(K, V, torch.full_like(kc, 7.0), torch.full_like(kc, 7.0), [table_row], starts)
+        assert np.array_equal(host64(kc), want[0]) and np.array_equal(host64(vc), want[1])
+    status()
+
+
+# --- keep -----------------------------------------------------------------------------------
+
+@pytest.mark.parametrize("layout", ["rows", "heads", "fused"])
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("kw", [dict(), dict(page=8, m=20, nodes=60), dict(d=40), dict(d=5, m=3), dict(m=1),
+                                dict(counts=(0, 3, 9, -4))])
+def test_keep(layout, dtype, kw):
+    kw = dict(dict(page=16, m=7, nodes=30, d=64, counts=None), **kw)
+    page, m, nodes, d, counts = (kw[x] for x in ("page", "m", "nodes", "d", "counts"))
+    starts = (0, 5, 31, 100)
+    kc, vc, table = cache(4, 3, d, page, [s + nodes for s in starts], layout, dtype, 3, device=DEV)
+    rng = np.random.default_rng(5)
+    # rising paths, one of them in place from its start to its end
+    path = np.stack([np.sort(rng.choice(nodes, m, replace=False)) for _ in range(3)] + [np.arange(m)])
+    want = paged.keep(kc, vc, table.tolist(), starts, path, counts)
+    lf.cache_keep(kc, vc, table, ints(starts, DEV), ints(path.tolist(), DEV),
+                  counts=None if counts is None else ints(counts, DEV))
+    status()
+    for x, y in zip((kc, vc), want):
+        assert np.array_equal(host64(x), y, equal_nan=True)
+
+
+def test_keep_the_same_node_twice_and_nodes_below_their_places():
+    kc, vc, table = cache(1, 2, 64, 16, [40], device=DEV)
+    for path, bad in (([3, 3, 3, 20, 20], False), ([0, 0, 5, 1, 9], True), ([4, 39, 40, 5, -1], True)):
+        want = paged.keep(kc, vc, table.tolist(), (0,), np.array([path]))
+        lf.cache_keep(kc, vc, table, ints([0], DEV), ints([path], DEV))
+        assert (error_code() != 0) == bad
+        for x, y in zip((kc, vc), want):
+            assert np.array_equal(host64(x), y, equal_nan=True)
+
+
+# --- trees ----------------------------------------------------------------------------------
+
+@pytest.mark.parametrize("n", [1, 2, 31, 64, 65, 128, 200, 1024])
+def test_tree_mask(n):
+    for deep in (False, True):
+        up = random_tree(3, n, seed=n, deep=deep)
+        got = lf.tree_mask(up.to(DEV))
+        status()
+        assert np.array_equal(got.cpu().numpy(), paged.words(paged.ancestors(up.numpy())))
+
+
+def test_tree_mask_of_a_chain_and_of_wrong_parents():
+    chain = torch.arange(-1, 99, dtype=torch.int32)[None]
+    assert np.array_equal(lf.tree_mask(chain.to(DEV)).cpu().numpy(),
+                          paged.words(np.tril(np.ones((1, 100, 100), dtype=bool))))
+    status()
+    for wrong in (5, 6, -2, 2 ** 31 - 1):
+        up = chain.clone()
+        up[0, 5] = wrong
+        got = lf.tree_mask(up.to(DEV))
+        assert error_code() != 0
+        assert np.array_equal(got.cpu().numpy(), paged.words(paged.ancestors(up.numpy())))
+
+
+# --- attention ------------------------------------------------------------------------------
+
+def check_attention(b=3, hq=4, hk=2, nq=1, d=64, page=16, k_lengths=(70, 1, 130), q_lengths=None,
+                    causal=True, window=0, scale=None, layout="rows", tree=None, seed=0, gain=1.5,
+                    width=None, clean=True):
+    kc, vc, table = cache(b, hk, d, page, [max(0, x) for x in k_lengths], layout, "bf16", seed, device=DEV,
+                          width=width, gain=gain)
+    g = torch.Generator(device=DEV).manual_seed(seed + 1)
+    Q = (torch.randn(b, nq, hq, d, generator=g, device=DEV) * gain).to(BF).transpose(1, 2)
+    if q_lengths is not None:
+        for i, x in enumerate(q_lengths):
+            Q[i, :, max(0, x):] = float("nan")
+    kw = dict(q_lengths=None if q_lengths is None else ints(q_lengths, DEV), scale=scale)
+    out = torch.full((b, hq, nq, d), 3.0, dtype=BF, device=DEV)
+    lse = torch.full((b, hq, nq), 3.0, device=DEV)
+    if tree is None:
+        got = lf.paged_attention(Q, kc, vc, table, ints(k_lengths, DEV), causal=causal, window=window,
+                                 out=out, lse=lse, **kw)
+        want = paged.forward(Q, kc, vc, table.tolist(), k_lengths, q_lengths, causal, window, scale)
+    else:
+        got = lf.tree_attention(Q, kc, vc, table, ints(k_lengths, DEV),
+                                torch.from_numpy(paged.words(tree)).to(DEV), out=out, lse=lse, **kw)
+        want = paged.forward(Q, kc, vc, table.tolist(), k_lengths, q_lengths, scale=scale, tree=tree)
+    if clean:
+        status()
+    assert got[0] is out and got[1] is lse
+    O, l = host64(out), host64(lse)
+    assert np.isfinite(O).all()
+    assert (np.abs(O - want[0]) <= want[2]).all(), float((np.abs(O - want[0]) - want[2]).max())
+    none = np.isneginf(want[1])
+    assert np.array_equal(np.isneginf(l), none) and (O[none] == 0).all()
+    assert (np.abs(l - want[1])[~none] <= want[3][~none]).all()
+    # three independent roundings of rms 2^-8 / sqrt 3 (P, O, the reference's none) stay below 5e-3
+    norm = np.linalg.norm(want[0])
+    assert np.linalg.norm(O - want[0]) <= 5e-3 * norm
+    return out, lse, (Q, kc, vc, table)
+
+
+@pytest.mark.parametrize("layout", ["rows", "heads", "fused"])
+@pytest.mark.parametrize("page", [8, 16, 32, 64, 128, 256])
+def test_single_tokens(layout, page):
+    check_attention(layout=layout, page=page)
+
+
+@pytest.mark.parametrize("d", [8, 40, 64, 72, 80, 96, 120, 128])
+def test_head_sizes(d):
+    check_attention(d=d)
+    check_attention(d=d, nq=70, k_lengths=(70, 200, 130))
+
+
+@pytest.mark.parametrize("hq,hk", [(1, 1), (3, 3), (12, 12), (6, 2), (8, 1), (7, 1), (32, 8), (24, 3), (32, 1), (128, 1),
+                                   (200, 1)])
+@pytest.mark.parametrize("nq", [1, 5])
+def test_heads(hq, hk, nq):
+    check_attention(hq=hq, hk=hk, nq=nq, k_lengths=(70, 6, 140))
+
+
+@pytest.mark.parametrize("k_lengths", [(1, 2, 3), (0, 0, 0), (127, 128, 129), (255, 256, 257), (0, 1000, 64),
+                                       (5, -3, 2000), (4096, 100, 3333)])
+@pytest.mark.parametrize("nq", [1, 3, 33])
+def test_lengths(k_lengths, nq):
+    """Sequences shorter than their new tokens among them: the first rows then see nothing."""
+    check_attention(k_lengths=k_lengths, nq=nq)
+    check_attention(k_lengths=k_lengths, nq=nq, causal=False, page=64, layout="heads")
+
+
+def test_lengths_past_the_table_are_cut():
+    check_attention(k_lengths=(64, 50, 64), width=4)
+    kc, vc, table = cache(1, 2, 64, 16, [64], device=DEV)
+    Q = torch.randn(1, 2, 1, 64, device=DEV).to(BF)
+    got = [lf.paged_attention(Q, kc, vc, table, ints([x], DEV)) for x in (64, 65, 2 ** 31 - 1)]
+    status()
+    for x in got[1:]:
+        assert torch.equal(bits(x[0]), bits(got[0][0])) and torch.equal(x[1], got[0][1])
+
+
+@pytest.mark.parametrize("nq,q_lengths", [(1, (1, 0, 1)), (7, (7, 0, 3)), (40, (1, 40, -5)), (300, (300, 129, 0))])
+def test_query_lengths(nq, q_lengths):
+    for kw in (dict(), dict(causal=False), dict(window=11)):
+        check_attention(nq=nq, q_lengths=q_lengths, k_lengths=(400, 130, 77), **kw)
+
+
+@pytest.mark.parametrize("window", [1, 2, 16, 127, 128, 129, 1000])
+@pytest.mark.parametrize("nq", [1, 9, 150])
+def test_windows(window, nq):
+    check_attention(nq=nq, window=window, k_lengths=(1111, 150, 333), page=32)
+
+
+@pytest.mark.parametrize("nq", [16, 63, 64, 65, 127, 128, 129, 257, 600])
+def test_chunks(nq):
+    check_attention(nq=nq, k_lengths=(nq, nq + 1, 700), d=128, page=64)
+    check_attention(nq=nq, k_lengths=(nq, nq + 77, 700), hq=8, hk=1)
+
+
+@pytest.mark.parametrize("n", [1, 2, 25, 32, 64, 65, 100, 130])
+@pytest.mark.parametrize("kw", [dict(), dict(hq=8, hk=1, d=128, page=64), dict(hq=3, hk=3, d=40, layout="fused")])
+def test_trees(n, kw):
+    tree = paged.ancestors(random_tree(3, n, seed=n).numpy())
+    check_attention(nq=n, tree=tree, k_lengths=(n, n + 130, 600), **kw)
+    check_attention(nq=n, tree=tree, k_lengths=(n, n + 130, 600), q_lengths=(n // 2, n, 0), **kw)
+
+
+def test_any_mask_serves():
+    """Masks that are no trees: random bits, none at all, every one, bits past the valid nodes; a
+    tree longer than the rows of the cache."""
+    r = np.random.default_rng(7)
+    for n in (5, 70, 140):
+        for m in (r.random((3, n, n)) < 0.3, np.zeros((3, n, n), bool), np.ones((3, n, n), bool)):
+            check_attention(nq=n, tree=m, k_lengths=(n, 3 * n, n // 2))
+            check_attention(nq=n, tree=m, k_lengths=(n, 3 * n, n // 2), q_lengths=(n, n - 2, 1), hq=8, hk=1)
+
+
+def test_large_trees():
+    n = 1024
+    tree = paged.ancestors(random_tree(1, n, seed=1, deep=True).numpy())
+    check_attention(b=1, nq=n, tree=tree, k_lengths=(n + 333,), page=128)
+
+
+@pytest.mark.parametrize("scale", [0.01, 0.5, 3.0])
+def test_scales(scale):
+    check_attention(scale=scale, nq=4, k_lengths=(500, 90, 1300))
+    check_attention(scale=scale, nq=200, k_lengths=(500, 200, 1300))
+
+
+def test_growing_logits():
+    """Maxima that rise from block to block, far past what an exponent holds unscaled."""
+    for nq, hq in ((1, 4), (3, 16), (60, 8)):
+        kc, vc, table = cache(1, 1, 64, 16, [1500], device=DEV, seed=4)
+        rise = torch.linspace(0.0, 60.0, 1500, device=DEV)
+        k = kc.transpose(1, 2).clone()
+        for j in range(1500):
+            k[table[0, j // 16].long(), j % 16] *= rise[j] / 8
+        kc = k.transpose(1, 2)
+        Q = (torch.randn(1, hq, nq, 64, device=DEV, generator=torch.Generator(device=DEV).manual_seed(2)) * 2).to(BF)
+        O, lse = lf.paged_attention(Q, kc, vc, table, ints([1500], DEV))
+        status()
+        want = paged.forward(Q, kc, vc, table.tolist(), (1500,), causal=True)
+        assert (np.abs(host64(O) - want[0]) <= want[2]).all()
+        assert (np.abs(host64(lse) - want[1]) <= want[3]).all()
+
+
+def test_many_sequences():
+    r = np.random.default_rng(3)
+    lengths = tuple(int(x) for x in r.integers(0, 300, 150))
+    check_attention(b=150, k_lengths=lengths, hq=2, hk=1)
+    check_attention(b=150, k_lengths=lengths, nq=3, hq=2, hk=2, page=8)
+
+
+def test_pages_that_are_not_there():
+    """They count as rows of zeros, are recorded, and nothing outside the cache is read."""
+    for nq, bad in ((1, 99), (1, -1), (40, 2 ** 31 - 1), (300, -7)):
+        kc, vc, table = cache(2, 2, 64, 16, [400, 390], device=DEV, seed=6)
+        Q = torch.randn(2, 4, nq, 64, device=DEV, generator=torch.Generator(device=DEV).manual_seed(nq)).to(BF)
+        table[1, 3] = bad
+        O, lse = lf.paged_attention(Q, kc, vc, table, ints([400, 390], DEV))
+        assert error_code() != 0
+        want = paged.forward(Q, kc, vc, table.tolist(), (400, 390), causal=True)
+        assert (np.abs(host64(O) - want[0]) <= want[2]).all()
+        assert (np.abs(host64(lse) - want[1]) <= want[3]).all()
+
+
+def test_pages_shared_by_sequences():
+    kc, vc, table = cache(1, 2, 64, 16, [200], device=DEV, seed=8)
+    Q = torch.randn(3, 4, 1, 64, device=DEV, generator=torch.Generator(device=DEV).manual_seed(1)).to(BF)
+    shared = table.expand(3, -1).contiguous()
+    O, lse = lf.paged_attention(Q, kc, vc, shared, ints([200, 100, 17], DEV))
+    status()
+    want = paged.forward(Q, kc, vc, shared.tolist(), (200, 100, 17), causal=True)
+    assert (np.abs(host64(O) - want[0]) <= want[2]).all()
+
+
+def test_repeated_calls_agree():
+    for nq in (1, 6, 64, 200):
+        args = check_attention(nq=nq, hq=8, k_lengths=(3000, 700, 2050))[2]
+        got = [lf.paged_attention(*args, ints((3000, 700, 2050), DEV)) for _ in range(3)]
+        status()
+        for x in got[1:]:
+            assert torch.equal(bits(x[0]), bits(got[0][0])) and torch.equal(x[1], got[0][1])
+
+
+def test_a_cache_past_32_bits():
+    """Pages whose offsets pass 2^32 elements, and 2^31 rows."""
+    pages, page, hk, d = 2 ** 17 + 8, 256, 1, 128  # 2^32 + elements, 8.6 GB each
+    kc, vc = (torch.empty(pages, hk, page, d, dtype=BF, device=DEV) for _ in range(2))
+    ids = [pages - 1, 5, pages - 3, 2 ** 17]
+    g = torch.Generator(device=DEV).manual_seed(0)
+    table = ints([ids], DEV)
+    K, V = (torch.randn(1, hk, 1000, d, device=DEV, generator=g).to(BF) for _ in range(2))
+    lf.cache_append(K, V, kc, vc, table, ints([0], DEV))
+    for i, x in enumerate(ids):
+        rows = min(page, 1000 - i * page)
+        assert torch.equal(kc[x, 0, :rows], K[0, 0, i * page:i * page + rows])
+        assert torch.equal(vc[x, 0, :rows], V[0, 0, i * page:i * page + rows])
+    for nq in (1, 80):
+        Q = torch.randn(1, 4, nq, d, device=DEV, generator=g).to(BF)
+        O, lse = lf.paged_attention(Q, kc, vc, table, ints([1000], DEV))
+        want, wl = lf.softmax_attention(Q, K, V, causal=True)
+        status()
+        # each side is within the rounding of P and of O of the same sums
+        assert (O.float() - want.float()).norm() <= 6e-3 * want.float().norm()
+        assert torch.allclose(lse, wl, atol=1e-4)
+    lf.cache_keep(kc, vc, table, ints([0], DEV), ints([[900, 950, 999]], DEV))
+    status()
+    for i, j in enumerate((900, 950, 999)):
+        assert torch.equal(kc[ids[0], 0, i], K[0, 0, j]) and torch.equal(vc[ids[0], 0, i], V[0, 0, j])
+
+
+# --- together -------------------------------------------------------------------------------
+
+def test_a_conversation():
+    """Prompts, single tokens, a drafted tree and its accepted path, against one dense attention
+    over the same tokens."""
+    b, hq, hk, d, page, rot = 3, 8, 2, 64, 16, 64
+    width, pages = 20, 70
+    g = torch.Generator(device=DEV).manual_seed(11)
+    kc, vc = (torch.full((pages, page, hk, d), float("nan"), dtype=BF, device=DEV).transpose(1, 2) for _ in range(2))
+    table = torch.randperm(pages, generator=torch.Generator().manual_seed(1))[:b * width].view(b, width).to(torch.int32).to(DEV)
+    phase = lf.rotary_phase(rot)
+    total = 200
+
+    def tokens(n):
+        return [torch.randn(b, h, n, d, generator=g, device=DEV).to(BF) for h in (hq, hk, hk)]
+    # the accepted tokens of every sequence, unturned
+    kept = [[x[i:i + 1, :, :0] for x in tokens(1)] for i in range(b)]
+    lengths = [0] * b
+
+    def extend(i, x, rows):
+        kept[i] = [torch.cat([a, y[i:i + 1, :, rows]], 2) for a, y in zip(kept[i], x)]
+
+    def compare(O, i, queries, first):
+        """Rows of O that stand at positions first.. of sequence i against the dense attention."""
+        q, k, v = kept[i]
+        tq, tk = lf.rotary(q, k, phase)
+        want, _ = lf.softmax_attention(tq, tk, v, causal=True)
+        got = O[i, :, queries].float()
+        w = want[0, :, first:first + got.shape[1]].float()
+        assert (got - w).norm() <= 6e-3 * w.norm()
+
+    # prompts of differing lengths, in one padded call
+    counts = [120, 1, 77]
+    x = tokens(120)
+    q = lf.cache_append(x[1], x[2], kc, vc, table, ints([0] * b, DEV), counts=ints(counts, DEV), Q=x[0],
+                        phase=phase)
+    O, _ = lf.paged_attention(q, kc, vc, table, ints(counts, DEV), q_lengths=ints(counts, DEV))
+    for i in range(b):
+        extend(i, x, slice(0, counts[i]))
+        lengths[i] = counts[i]
+        compare(O, i, slice(0, counts[i]), 0)
+    for _ in range(3):  # tokens one by one
+        x = tokens(1)
+        q = lf.cache_append(x[1], x[2], kc, vc, table, ints(lengths, DEV), Q=x[0], phase=phase)
+        lengths = [y + 1 for y in lengths]
+        O, _ = lf.paged_attention(q, kc, vc, table, ints(lengths, DEV))
+        for i in range(b):
+            extend(i, x, slice(0, 1))
+            compare(O, i, slice(0, 1), lengths[i] - 1)
+    # a tree of drafted tokens, each at its depth behind the sequence
+    n = 12
+    up = random_tree(b, n, seed=5)
+    depth = torch.zeros(b, n, dtype=torch.int32)
+    for i in range(n):
+        for s in range(b):
+            depth[s, i] = 0 if up[s, i] < 0 else depth[s, up[s, i]] + 1
+    x = tokens(n)
+    q = lf.cache_append(x[1], x[2], kc, vc, table, ints(lengths, DEV), Q=x[0], phase=phase,
+                        positions=(ints(lengths)[:, None] + depth).to(DEV))
+    O, _ = lf.tree_attention(q, kc, vc, table, ints([y + n for y in lengths], DEV), lf.tree_mask(up.to(DEV)))
+    paths = []
+    for i in range(b):
+        node = int(depth[i].argmax())  # the deepest branch is accepted
+        path = []
+        while node >= 0:
+            path.insert(0, node)
+            node = int(up[i, node])
+        paths.append(path)
+        extend(i, x, path)
+        compare(O, i, path, lengths[i])
+    m = max(len(p) for p in paths)
+    lf.cache_keep(kc, vc, table, ints(lengths, DEV), ints([p + [0] * (m - len(p)) for p in paths], DEV),
+                  counts=ints([len(p) for p in paths], DEV))
+    lengths = [y + len(p) for y, p in zip(lengths, paths)]
+    x = tokens(1)  # and on
+    q = lf.cache_append(x[1], x[2], kc, vc, table, ints(lengths, DEV), Q=x[0], phase=phase)
+    lengths = [y + 1 for y in lengths]
+    O, _ = lf.paged_attention(q, kc, vc, table, ints(lengths, DEV))
+    for i in range(b):
+        extend(i, x, slice(0, 1))
+        compare(O, i, slice(0, 1), lengths[i] - 1)
+    status()
