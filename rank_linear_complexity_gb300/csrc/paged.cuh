@@ -12,7 +12,7 @@ namespace paged {
 
 // Codes in the device status word: a table entry that is needed and names no page, a row beyond
 // the table, an accepted node before its place, a parent that is not before its node.
-constexpr int kBadPage = 90, kBadRow = 91, kBadPath = 92, kBadParent = 93;
+constexpr int kBadPage = 200, kBadRow = 201, kBadPath = 202, kBadParent = 203;
 
 // Keys and values of all sequences, [pages][hk][page][d] each by strides (b: a page's), and which
 // page holds rows [page x, page (x + 1)) of sequence beta: table[beta][x].

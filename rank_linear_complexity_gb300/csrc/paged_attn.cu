@@ -1,105 +1,767 @@
-// Exact softmax attention of new tokens over a paged cache, with trees of drafted tokens: the
-// sums of softmax_attn_fwd.cu over the rows that the table leads to.
+// Exact softmax attention of new tokens over a paged cache, with trees of drafted tokens: for
+// every query row i of every head
+//
+//     O_i = sum_j p_ij V_j,   p_ij = exp(scale Q_i.K_j - lse_i),   lse_i = log sum_j exp(scale Q_i.K_j)
+//
+// over the cache rows j that the row sees, in one pass over the pages.
+//
+// New tokens are few beside the rows that they look at, so the products are turned round: keys
+// take the 128 rows of a product and queries its columns, of which there can be as few as 16,
+//
+//     S^T = K Q^T   (128 keys x N rows),   O^T += V^T P^T   (d x N rows),
+//
+// and a thread has one key and N / 2 queries: what a length or a page hides is a thread's own
+// business, sums over keys stay in the thread until a row ends, and only a maximum that outgrows
+// its reference by 2^kOutgrown makes threads exchange anything but a vote (the reference is any m
+// near the maximum; P = 2^(s - m) is rounded to bf16, at most 2^-8 of each term, as the tensor cores
+// take it; sums and statistics are fp32).  Tiles of 128 keys come by TMA, a box a page, through a
+// ring in shared memory.
+//
+// The blocks of 128 keys of all rows form one long list, sequence by sequence, and each CTA takes an
+// equal run of it, so that differing lengths cost nothing; a row whose run is cut is joined from
+// its parts, in order, by a second kernel.
+//   warps 0-7   softmax: two groups of four warps, each half of the columns
+//   warp 8      loads: looks the pages up and issues a box a lane
+//   warp 9      one thread issues the products
+#include <algorithm>
 #include <cmath>
-#include <cuda_bf16.h>
 
-#include "internal.cuh"
 #include "paged.cuh"
+#include "sm100_ptx.cuh"
 #include "softmax_attn.cuh"
 
 namespace linformer {
 namespace paged {
 namespace {
 
-constexpr int kMaxD = 128;
+using namespace ptx;
+using sattn::clamp_length;
+using sattn::pack2;
+using sattn::Span;
+
+constexpr int kTile = 128;  // keys of a block
+constexpr int kThreads = 320, kLoadWarp = 8, kMmaWarp = 9;
+constexpr int kMaxSeqs = 512;  // sequences of a launch
+constexpr float kOutgrown = 16.f, kLog2e = 1.4426950408889634f;
+constexpr int kMinRun = 1;  // blocks of a CTA at least
 
 struct AttnParams {
-    Cache cache;
-    const __nv_bfloat16 *q;
-    __nv_bfloat16 *out;
-    Strides sq, so;
-    float *lse;
-    const int32_t *q_lengths, *k_lengths;
+    const int32_t *q_lengths, *k_lengths, *table;
     const uint64_t *mask;
-    int words, b, hq, hk, nq, d, causal, window;
-    float scale;
+    __nv_bfloat16 *out;
+    Strides so;
+    float *lse;
+    float *part_o, *part_lse;  // [2 per CTA][N][DP], [2 per CTA][N]
+    int64_t *first;            // [b + 1]: where the blocks of each sequence begin in the list
+    int words, b, hq, hk, group, nq, d, causal, window;
+    int qbox, hbox, nch, ntiles, N, ctas;
+    int pages, page, width, shift, box, nbox;
+    float scale, scale_log2;
     int *status;
 };
 
-// A warp a query row: the running maximum m and sum l of the softmax, and the output so far, a
-// lane holding every 32nd element.
-__global__ void __launch_bounds__(128) paged_attn_kernel(const AttnParams p) {
-    const int64_t r = (int64_t)blockIdx.x * 4 + (threadIdx.x >> 5);
+// The rows of a tile: qbox positions of hbox heads of a group.
+struct Rows {
+    int q0, h0;
+    __device__ __forceinline__ Rows(const AttnParams &p, int tile) {
+        const int qt = p.nch > 1 ? tile / p.nch : tile;
+        q0 = qt * p.qbox;
+        h0 = (tile - qt * p.nch) * p.hbox;
+    }
+};
+
+// The key blocks that a tile's rows see.
+__device__ __forceinline__ void blocks_of(const AttnParams &p, const Span &sp, int q0, int &lo, int &hi) {
+    lo = hi = 0;
+    const int last = min(q0 + p.qbox, sp.Lq) - 1;
+    if (last < q0) return;
+    const int e = sp.end(last), f = sp.first(q0);
+    if (e <= f) return;
+    lo = f / kTile;
+    hi = (e + kTile - 1) / kTile;
+}
+__device__ __forceinline__ Span span_of(const AttnParams &p, int seq) {
+    return Span{clamp_length(p.q_lengths, seq, p.nq), clamp_length(p.k_lengths, seq, p.width * p.page), p.causal,
+                p.window};
+}
+__device__ __forceinline__ int64_t run_begin(int64_t total, int cta, int ctas) { return total * cta / ctas; }
+__device__ __forceinline__ int runs(int64_t total, int ctas) {
+    return (int)min((int64_t)ctas, max((int64_t)1, total / kMinRun));
+}
+
+// A CTA's part of the list, tile by tile: sequence-major, then tile, then key/value head.
+struct Item {
+    int seq, tile, kvh, lo, hi;  // blocks [lo, hi) of it
+    Span sp;
+    int slot;  // where its partial result goes; -1: the row is whole
+};
+struct Walk {
+    int64_t at, end;
+    int seq, tile, kvh, blk, lo, hi, slot;
+    Span sp;
+    __device__ __forceinline__ Walk(const AttnParams &p, const int64_t *first, int cta) {
+        const int n = runs(first[p.b], p.ctas);
+        at = end = 0;
+        if (cta >= n) return;
+        at = run_begin(first[p.b], cta, n);
+        end = run_begin(first[p.b], cta + 1, n);
+        if (at >= end) return;
+        int a = 0, z = p.b;  // first[a] <= at < first[z]
+        while (z - a > 1) {
+            const int m = (a + z) / 2;
+            if (first[m] <= at) a = m;
+            else z = m;
+        }
+        seq = a;
+        sp = span_of(p, seq);
+        int64_t off = at - first[seq];
+        for (tile = 0;; ++tile) {
+            blocks_of(p, sp, Rows(p, tile).q0, lo, hi);
+            const int64_t c = (int64_t)(hi - lo) * p.hk;
+            if (off < c) break;
+            off -= c;
+        }
+        kvh = (int)(off / (hi - lo));
+        blk = (int)(off - (int64_t)kvh * (hi - lo));
+        slot = 2 * cta;
+    }
+    // The next item, while there is one.
+    __device__ __forceinline__ bool next(const AttnParams &p, Item &it) {
+        if (at >= end) return false;
+        const int n = (int)min((int64_t)(hi - lo - blk), end - at);
+        it.seq = seq;
+        it.tile = tile;
+        it.kvh = kvh;
+        it.lo = lo + blk;
+        it.hi = it.lo + n;
+        it.sp = sp;
+        it.slot = blk == 0 && it.hi == hi ? -1 : blk ? slot : slot + 1;
+        at += n;
+        blk = 0;
+        if (at < end && ++kvh == p.hk) {
+            kvh = 0;
+            do {
+                if (++tile == p.ntiles) {
+                    tile = 0;
+                    ++seq;
+                    sp = span_of(p, seq);
+                }
+                blocks_of(p, sp, Rows(p, tile).q0, lo, hi);
+            } while (hi <= lo);
+        }
+        return true;
+    }
+};
+
+template <int DP, int N>
+struct Layout {
+    static constexpr uint32_t kTileBytes = kTile * DP * 2;
+    // DP = 64: K and V of a block share an entry of the ring, V first (the product takes 128 rows of
+    // V^T, of which the second half falls on K and is not used)
+    static constexpr bool kPair = DP == 64;
+    static constexpr int kEntries = kPair ? (N == 128 ? 4 : 5) : (N == 128 ? 4 : 5);
+    static constexpr uint32_t kEntryBytes = kPair ? 2 * kTileBytes : kTileBytes;
+    static constexpr int kPBufs = N == 128 ? 1 : 2;
+    static constexpr int kGroups = N > 64 ? 2 : 1;  // of 64 columns
+    static constexpr uint32_t kPBytes = kGroups * kTile * 128;
+    static constexpr uint32_t kQHalf = N * 128, kQBytes = kQHalf * (DP / 64);
+    static constexpr uint32_t kP = kEntries * kEntryBytes, kQ = kP + kPBufs * kPBytes, kEnd = kQ + kQBytes;
+    static constexpr uint32_t kS = 0, kO = 2 * N;  // tensor memory: S, S, O
+};
+
+struct Shared {
+    uint64_t full[5], empty[5], q_full, q_free, s_full[2], s_free[2], p_full[2], pv_done[2], o_free, drain;
+    uint32_t tmem;
+    int abort;
+    alignas(16) float m[128];
+    alignas(16) float off[128];
+    alignas(16) float f[128];
+    float part[2][4][64];  // a value a column, by warp of each group
+    int64_t first[kMaxSeqs + 1];
+    int64_t sums[32];
+};
+
+template <int C>
+__device__ __forceinline__ void tmem_load(uint32_t t, uint32_t (&v)[C]) {
+    if constexpr (C == 8) tmem_ld8(t, v);
+    else if constexpr (C == 16) tmem_ld16(t, v);
+    else if constexpr (C == 32) tmem_ld32(t, v);
+    else tmem_ld64(t, v);
+}
+
+// Reduces C columns over the 32 lanes of a warp; column(lane) of lane's result.  Each exchange
+// halves the columns that a lane still holds.
+template <int C, typename F>
+__device__ __forceinline__ float reduce_columns(float (&v)[C], int lane, F f) {
+    static_assert(C <= 32, "a column a lane");
+    int w = 16;
+#pragma unroll
+    for (int c = C / 2; c >= 1; c /= 2, w /= 2) {
+        const bool upper = lane & w;
+#pragma unroll
+        for (int i = 0; i < c; ++i) {
+            const float send = upper ? v[i] : v[i + c], keep = upper ? v[i + c] : v[i];
+            v[i] = f(keep, __shfl_xor_sync(0xffffffffu, send, w));
+        }
+    }
+    float r = v[0];
+    for (; w >= 1; w /= 2) r = f(r, __shfl_xor_sync(0xffffffffu, r, w));
+    return r;
+}
+// Over a warp, into part[0 .. C).
+template <int C, typename F>
+__device__ __forceinline__ void reduce_to(const float (&v)[C], float *part, int lane, F f) {
+    constexpr int H = C < 32 ? C : 32;
+#pragma unroll
+    for (int h = 0; h < C; h += H) {
+        float x[H];
+#pragma unroll
+        for (int i = 0; i < H; ++i) x[i] = v[h + i];
+        const float r = reduce_columns(x, lane, f);
+        if (lane % (32 / H) == 0) part[h + lane / (32 / H)] = r;
+    }
+}
+
+// The scores of a block that key `key` may not give become -inf in tensor memory: the few blocks
+// at a mask's edge keep out of the code of the others.
+__device__ __noinline__ void mask_columns(uint32_t t, int c0, int columns, int key, Span sp, int i0, int positions,
+                                          const uint64_t *mask, int words) {
+    const int node = key - (sp.Lk - sp.Lq);
+    const bool tree = mask && node >= 0;
+#pragma unroll 1
+    for (int c = 0; c < columns; c += 8) {
+        uint32_t v[8];
+        tmem_ld8(t + c, v);
+#pragma unroll
+        for (int e = 0; e < 8; ++e) {
+            const int i = i0 + ((c0 + c + e) & (positions - 1));
+            bool see = i < sp.Lq && key >= sp.first(i) && key < sp.end(i);
+            if (see && tree) see = __ldg(mask + (int64_t)i * words + (node >> 6)) >> (node & 63) & 1;
+            if (!see) v[e] = 0xff800000u;
+        }
+        tmem_st8_async(t + c, v);
+        tmem_wait_st();
+    }
+}
+
+template <int DP, int N>
+__global__ void __launch_bounds__(kThreads, 1)
+paged_attn_kernel(const __grid_constant__ CUtensorMap tQ, const __grid_constant__ CUtensorMap tK,
+                  const __grid_constant__ CUtensorMap tV, const __grid_constant__ AttnParams p) {
+    using L = Layout<DP, N>;
+    constexpr int C = N / 2;  // columns of a thread
+    extern __shared__ uint8_t raw[];
+    uint8_t *smem = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(raw) + 1023) & ~uintptr_t(1023));
+    Shared *sh = reinterpret_cast<Shared *>(smem + L::kEnd);
+    volatile int *abort_flag = &sh->abort;
+    const int tid = threadIdx.x, warp = __shfl_sync(0xffffffffu, tid >> 5, 0), lane = tid & 31;
+
+    if (tid == 0) {
+        for (int s = 0; s < L::kEntries; ++s) {
+            mbar_init(&sh->full[s], 1);
+            mbar_init(&sh->empty[s], 1);
+        }
+        mbar_init(&sh->q_full, 1);
+        mbar_init(&sh->q_free, 1);
+        for (int s = 0; s < 2; ++s) {
+            mbar_init(&sh->s_full[s], 1);
+            mbar_init(&sh->s_free[s], 8);
+            mbar_init(&sh->p_full[s], 8);
+            mbar_init(&sh->pv_done[s], 1);
+        }
+        mbar_init(&sh->o_free, 8);
+        mbar_init(&sh->drain, 1);
+        sh->abort = 0;
+        fence_mbar_init();
+        prefetch_tmap(&tQ);
+        prefetch_tmap(&tK);
+        prefetch_tmap(&tV);
+        launch_dependents();  // the join, which waits for this grid's end
+    }
+    if (warp == kMmaWarp) {
+        tmem_alloc(&sh->tmem, 512);
+        tmem_relinquish();
+    }
+    // rows of Q that no box fills
+    for (uint32_t x = tid * 16; x < L::kQBytes; x += kThreads * 16)
+        *reinterpret_cast<uint4 *>(smem + L::kQ + x) = make_uint4(0u, 0u, 0u, 0u);
+    fence_proxy_async_smem();
+    // where each sequence begins in the list of blocks
+    for (int s = tid; s < p.b; s += kThreads) {
+        const Span sp = span_of(p, s);
+        int64_t sum = 0;
+        for (int t = 0; t < p.ntiles; ++t) {
+            int lo, hi;
+            blocks_of(p, sp, Rows(p, t).q0, lo, hi);
+            sum += (int64_t)(hi - lo) * p.hk;
+        }
+        sh->first[s + 1] = sum;
+    }
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    if (warp == 0) {
+        constexpr int kEach = kMaxSeqs / 32;
+        int64_t sum = 0;
+        const int s0 = lane * kEach, s1 = min(s0 + kEach, p.b);
+        for (int s = s0; s < s1; ++s) sum += sh->first[s + 1];
+        int64_t run = sum;
+        for (int o = 1; o < 32; o *= 2) {
+            const int64_t x = __shfl_up_sync(0xffffffffu, run, o);
+            if (lane >= o) run += x;
+        }
+        run -= sum;
+        for (int s = s0; s < s1; ++s) sh->first[s + 1] = run += sh->first[s + 1];
+        if (lane == 0) sh->first[0] = 0;
+    }
+    __syncthreads();
+    if (blockIdx.x == 0)
+        for (int s = tid; s <= p.b; s += kThreads) p.first[s] = sh->first[s];
+    const uint32_t tmem = sh->tmem;
+    Walk walk(p, sh->first, blockIdx.x);
+    Item it;
+
+    if (warp == kLoadWarp) {  // ---------------- loads
+        // a lane's box of a tile: `box` rows of a page, 64 columns
+        const int bi = lane / (DP / 64), half = lane % (DP / 64);
+        const bool mine = bi < p.nbox;
+        const int row = bi * p.box;
+        const uint32_t dst = half * 16384u + row * 128u;
+        int ring = 0, nq = 0;
+        bool ok = true;
+        while (ok && walk.next(p, it)) {
+            const Rows r(p, it.tile);
+            if (nq > 0 && !warp_spin(&sh->q_free, (nq - 1) & 1, p.status, 120, abort_flag)) break;
+            if (lane == 0) {
+                mbar_arrive_expect_tx(&sh->q_full, (uint32_t)(p.qbox * p.hbox * DP * 2));
+                for (int h = 0; h < DP / 64; ++h)
+                    tma_load_5d(smem + L::kQ + h * L::kQHalf, &tQ, &sh->q_full, h * 64, r.q0, r.h0, it.kvh, it.seq);
+            }
+            ++nq;
+            const int32_t *table = p.table + (int64_t)it.seq * p.width;
+            // the page of this lane's rows in block j; p.pages, which is outside the map and comes
+            // as zeros, where there is none
+            auto look = [&](int j) {
+                const int at = j * kTile + row;
+                if (!mine || at >= it.sp.Lk) return p.pages;
+                const int x = __ldg(table + (at >> p.shift));
+                if ((unsigned)x < (unsigned)p.pages) return x;
+                if (p.status) atomicExch(p.status, kBadPage);
+                return p.pages;
+            };
+            int page = look(it.lo);
+            for (int j = it.lo; j < it.hi; ++j) {
+                const int now = page, at = (j * kTile + row) & (p.page - 1);
+                if (j + 1 < it.hi) page = look(j + 1);
+#pragma unroll
+                for (int kv = 0; kv < 2; ++kv) {
+                    const int e = ring % L::kEntries;
+                    if (!L::kPair || kv == 0) {
+                        if (ring >= L::kEntries &&
+                            !warp_spin(&sh->empty[e], (ring / L::kEntries - 1) & 1, p.status, 121, abort_flag)) {
+                            ok = false;
+                            break;
+                        }
+                        if (lane == 0) mbar_arrive_expect_tx(&sh->full[e], L::kEntryBytes);
+                        __syncwarp();
+                    }
+                    if (mine)
+                        tma_load_5d(smem + e * L::kEntryBytes + (L::kPair && kv == 0 ? L::kTileBytes : 0) + dst,
+                                    kv ? &tV : &tK, &sh->full[e], half * 64, at, 0, it.kvh, now);
+                    if (!L::kPair || kv == 1) ++ring;
+                }
+                if (!ok) break;
+            }
+        }
+        // no copy outlives the CTA
+        if (lane == 0) {
+            if (nq > 0) mbar_wait_drain(&sh->q_full, (nq - 1) & 1);
+            for (int i = max(0, ring - L::kEntries); i < ring; ++i)
+                mbar_wait_drain(&sh->full[i % L::kEntries], (i / L::kEntries) & 1);
+        }
+        __syncwarp();
+    } else if (warp == kMmaWarp) {
+        if (elect_one()) {  // ---------------- products
+            const uint32_t idesc_s = idesc_f16(128, N, 1, 0, 0), idesc_o = idesc_f16(128, N, 1, 1, 1);
+            const uint64_t dq = sdesc(smem_u32(smem + L::kQ), 16, 1024, kSwizzle128B);
+            int ns = 0, no = 0, items = 0;  // blocks whose S, whose O has been issued
+            bool ok = true;
+            while (ok && walk.next(p, it)) {
+                auto score = [&](int j) {
+                    const int r = L::kPair ? ns : 2 * ns, e = r % L::kEntries, s = ns & 1;
+                    if (!thread_spin(&sh->full[e], (r / L::kEntries) & 1, p.status, 122, abort_flag)) return false;
+                    if (j == it.lo && !thread_spin(&sh->q_full, items & 1, p.status, 123, abort_flag)) return false;
+                    if (ns > 1 && !thread_spin(&sh->s_free[s], ((ns >> 1) - 1) & 1, p.status, 124, abort_flag)) return false;
+                    tc_fence_after();
+                    const uint64_t dk = sdesc(smem_u32(smem + e * L::kEntryBytes + (L::kPair ? L::kTileBytes : 0)), 16, 1024,
+                                              kSwizzle128B);
+#pragma unroll
+                    for (int x = 0; x < DP / 16; ++x)
+                        mma_ss(tmem + L::kS + N * s, dk + (uint64_t)((x >> 2) * 1024 + (x & 3) * 2),
+                               dq + (uint64_t)((x >> 2) * (L::kQHalf >> 4) + (x & 3) * 2), idesc_s, x > 0 ? 1u : 0u);
+                    mma_commit(&sh->s_full[s]);
+                    if (!L::kPair) mma_commit(&sh->empty[e]);
+                    if (j == it.hi - 1) mma_commit(&sh->q_free);
+                    ++ns;
+                    return true;
+                };
+                auto output = [&](int j) {
+                    const int r = L::kPair ? no : 2 * no + 1, e = r % L::kEntries, b = no % L::kPBufs;
+                    if (!L::kPair && !thread_spin(&sh->full[e], (r / L::kEntries) & 1, p.status, 125, abort_flag)) return false;
+                    if (!thread_spin(&sh->p_full[b], (no / L::kPBufs) & 1, p.status, 126, abort_flag)) return false;
+                    if (j == it.lo && items > 0 && !thread_spin(&sh->o_free, (items - 1) & 1, p.status, 127, abort_flag))
+                        return false;
+                    tc_fence_after();
+                    const uint64_t dv = sdesc(smem_u32(smem + e * L::kEntryBytes), 16384, 1024, kSwizzle128B);
+                    const uint64_t dp = sdesc(smem_u32(smem + L::kP + b * L::kPBytes), 16384, 1024, kSwizzle128B);
+#pragma unroll
+                    for (int x = 0; x < kTile / 16; ++x)
+                        mma_ss(tmem + L::kO, dv + (uint64_t)(128 * x), dp + (uint64_t)(128 * x), idesc_o,
+                               (j > it.lo || x > 0) ? 1u : 0u);
+                    mma_commit(&sh->pv_done[b]);
+                    mma_commit(&sh->empty[e]);
+                    ++no;
+                    return true;
+                };
+                ok = score(it.lo);
+                for (int j = it.lo; j < it.hi && ok; ++j) ok = (j + 1 >= it.hi || score(j + 1)) && output(j);
+                ++items;
+            }
+            mma_commit(&sh->drain);
+            mbar_wait_drain(&sh->drain, 0);
+        }
+        __syncwarp();
+    } else {  // ---------------- softmax: one key a thread, C of the rows
+        const int w = warp >> 2, key0 = tid & 127, c0 = w * C;
+        const uint32_t lanes = (uint32_t)((warp & 3) * 32) << 16;
+        const uint32_t tO = tmem + L::kO + c0 + lanes;
+        const float sl = p.scale_log2;
+        float *part = sh->part[w][warp & 3];
+        int n = 0;
+        bool ok = true;
+        // the product of block x and P is done; with a barrier a buffer of P, no waiting warp is ever two
+        // phases behind: the next product from a buffer waits for every warp's P
+        auto product = [&](int x, int code) {
+            return warp_spin(&sh->pv_done[x % L::kPBufs], (x / L::kPBufs) & 1, p.status, code, abort_flag);
+        };
+        // The group's warps leave together: what a wait of one came to is ANDed at a barrier.
+        auto agree = [&] { return ok = named_barrier_and(1 + w, 128, ok); };
+        while (walk.next(p, it)) {
+            float l[C];
+#pragma unroll
+            for (int c = 0; c < C; ++c) l[c] = 0.f;
+            const Rows r(p, it.tile);
+            const int before = it.sp.Lk - it.sp.Lq;
+            const uint64_t *mask = p.mask ? p.mask + (int64_t)it.seq * p.nq * p.words : nullptr;
+            for (int j = it.lo; j < it.hi; ++j, ++n) {
+                const int s = n & 1, b = n % L::kPBufs, k0 = j * kTile, key = k0 + key0;
+                const uint32_t tS = tmem + L::kS + N * s + c0 + lanes;
+                ok = ok && warp_spin(&sh->s_full[s], (n >> 1) & 1, p.status, 128, abort_flag);
+                tc_fence_after();
+                const bool ragged = k0 + kTile > it.sp.Lk;
+                // (rows that the tile does not have see nothing or anything)
+                if (ragged || (p.causal && k0 + kTile > r.q0 + before + 1) || (p.mask && k0 + kTile > before) ||
+                    (p.window && k0 < it.sp.first(min(r.q0 + p.qbox, it.sp.Lq) - 1)))
+                    mask_columns(tS, c0, C, key, it.sp, r.q0, p.qbox, mask, p.words);
+                float y[C], top = -INFINITY;
+                auto exponents = [&] {
+                    uint32_t v[C];
+                    tmem_load(tS, v);
+#pragma unroll
+                    for (int c = 0; c < C; c += 4) {
+                        const float4 off = *reinterpret_cast<const float4 *>(&sh->off[c0 + c]);
+                        const float2 a = ffma2(make_float2(__uint_as_float(v[c]), __uint_as_float(v[c + 1])),
+                                               make_float2(sl, sl), make_float2(off.x, off.y));
+                        const float2 z = ffma2(make_float2(__uint_as_float(v[c + 2]), __uint_as_float(v[c + 3])),
+                                               make_float2(sl, sl), make_float2(off.z, off.w));
+                        y[c] = a.x, y[c + 1] = a.y, y[c + 2] = z.x, y[c + 3] = z.y;
+                        top = fmaxf(max3(top, a.x, a.y), fmaxf(z.x, z.y));
+                    }
+                };
+                if (j > it.lo) exponents();
+                if (named_barrier_or(1 + w, 128, j == it.lo || top > kOutgrown || !ok)) {
+                    // a new reference for every column, and O and l to it
+                    if (!agree()) break;
+#pragma unroll 1
+                    for (int c = 0; c < C; c += 8) {
+                        uint32_t v[8];
+                        tmem_ld8(tS + c, v);
+                        float x[8];
+#pragma unroll
+                        for (int e = 0; e < 8; ++e) x[e] = __uint_as_float(v[e]);
+                        reduce_to(x, part + c, lane, [](float a, float z) { return fmaxf(a, z); });
+                    }
+                    if (j > it.lo) ok = product(n - 1, 129);
+                    if (!agree()) break;
+                    if (key0 < C) {
+                        const float mo = j > it.lo ? sh->m[c0 + key0] : -INFINITY;
+                        float mn = mo;
+                        for (int x = 0; x < 4; ++x) mn = fmaxf(mn, sh->part[w][x][key0]);
+                        sh->m[c0 + key0] = mn;
+                        sh->off[c0 + key0] = mn == -INFINITY ? 0.f : -mn * sl;
+                        sh->f[c0 + key0] = mn == -INFINITY ? 1.f : ex2_approx((mo - mn) * sl);
+                    }
+                    named_barrier_sync(1 + w, 128);
+                    if (j > it.lo) {
+                        tc_fence_after();
+#pragma unroll
+                        for (int c = 0; c < C; ++c) l[c] *= sh->f[c0 + c];
+#pragma unroll 1
+                        for (int c = 0; c < C; c += 8) {
+                            uint32_t q[8];
+                            tmem_ld8(tO + c, q);
+#pragma unroll
+                            for (int e = 0; e < 8; ++e) q[e] = __float_as_uint(__uint_as_float(q[e]) * sh->f[c0 + c + e]);
+                            tmem_st8_async(tO + c, q);
+                        }
+                        tmem_wait_st();
+                    }
+                    exponents();
+                }
+                tc_fence_before();
+                __syncwarp();
+                if (lane == 0) mbar_arrive(&sh->s_free[s]);
+#pragma unroll
+                for (int c = 0; c < C; ++c) {
+                    y[c] = ex2_approx(y[c]);
+                    l[c] += y[c];
+                }
+                // the buffer's last product is done
+                if (ok && n >= L::kPBufs) ok = product(n - L::kPBufs, 130);
+                uint8_t *row = smem + L::kP + b * L::kPBytes + key0 * 128;
+#pragma unroll
+                for (int c = 0; c < C; c += 8) {
+                    const int g = (c0 + c) / 64, ch = ((c0 + c) % 64) / 8;
+                    *reinterpret_cast<uint4 *>(row + g * 16384 + ((ch ^ (key0 & 7)) * 16)) =
+                        make_uint4(pack2(y[c], y[c + 1]), pack2(y[c + 2], y[c + 3]), pack2(y[c + 4], y[c + 5]),
+                                   pack2(y[c + 6], y[c + 7]));
+                }
+                if (ragged && w == 0) {
+                    // rows of V past the length may hold anything: P is 0 there, but 0 x NaN is not
+                    const int rr = L::kPair ? n : 2 * n + 1, e = rr % L::kEntries;
+                    ok = ok && warp_spin(&sh->full[e], (rr / L::kEntries) & 1, p.status, 131, abort_flag);
+                    if (ok && key >= it.sp.Lk) {
+                        uint8_t *at = smem + e * L::kEntryBytes + key0 * 128;
+#pragma unroll
+                        for (int x = 0; x < DP / 8; ++x)
+                            *reinterpret_cast<uint4 *>(at + (x / 8) * 16384 + (x % 8) * 16) = make_uint4(0u, 0u, 0u, 0u);
+                    }
+                }
+                fence_proxy_async_smem();
+                __syncwarp();
+                if (lane == 0) mbar_arrive(&sh->p_full[b]);
+            }
+            // O / l out of tensor memory, a row of O^T an element of d
+            ok = ok && product(n - 1, 132);
+            reduce_to(l, part, lane, [](float a, float z) { return a + z; });
+            if (!agree()) break;
+            tc_fence_after();
+            if (key0 < C) {
+                const int c = c0 + key0, i = r.q0 + (c & (p.qbox - 1)), hg = r.h0 + c / p.qbox;
+                float sum = 0.f;
+                for (int x = 0; x < 4; ++x) sum += sh->part[w][x][key0];
+                const bool dead = i >= it.sp.Lq || sum == 0.f;
+                const float lse = dead ? -INFINITY : sh->m[c] * p.scale + logf(sum);
+                sh->f[c] = dead ? 0.f : 1.f / sum;
+                if (it.slot >= 0) p.part_lse[(int64_t)it.slot * N + c] = lse;
+                else if (c < p.qbox * p.hbox && hg < p.group && i < p.nq)
+                    p.lse[((int64_t)it.seq * p.hq + it.kvh * p.group + hg) * p.nq + i] = lse;
+            }
+            named_barrier_sync(1 + w, 128);
+            if (key0 - lane < p.d) {
+#pragma unroll 1
+                for (int c = 0; c < C; c += 8) {
+                    uint32_t q[8];
+                    tmem_ld8(tO + c, q);
+#pragma unroll
+                    for (int e = 0; e < 8; ++e) {
+                        const int x = c0 + c + e, i = r.q0 + (x & (p.qbox - 1)), hg = r.h0 + x / p.qbox;
+                        const float f = sh->f[x], o = f == 0.f ? 0.f : __uint_as_float(q[e]) * f;
+                        if (x >= p.qbox * p.hbox || hg >= p.group || i >= p.nq || key0 >= p.d) continue;
+                        if (it.slot >= 0) p.part_o[((int64_t)it.slot * N + x) * DP + key0] = o;
+                        else
+                            p.out[it.seq * p.so.b + ((int64_t)it.kvh * p.group + hg) * p.so.h + (int64_t)i * p.so.n + key0] =
+                                __float2bfloat16_rn(o);
+                    }
+                }
+            }
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&sh->o_free);
+        }
+    }
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    if (warp == kMmaWarp) tmem_dealloc(tmem, 512);
+}
+
+// Joins the parts of the rows whose run of blocks was cut: lse = log sum_s exp(lse_s), O = sum_s
+// exp(lse_s - lse) O_s; rows without blocks get O = 0 and lse = -inf.  A block a tile of a key/value
+// head, a warp a row.
+template <int DP>
+__global__ void __launch_bounds__(128) join_kernel(const AttnParams p) {
+    wait_prerequisites();
+    const int unit = blockIdx.x, kvh = unit % p.hk, tile = unit / p.hk % p.ntiles, seq = unit / p.hk / p.ntiles;
     const int lane = threadIdx.x & 31;
-    if (r >= (int64_t)p.b * p.hq * p.nq) return;
-    const int i = (int)(r % p.nq), h = (int)(r / p.nq % p.hq), b = (int)(r / ((int64_t)p.nq * p.hq));
-    const int kvh = h / (p.hq / p.hk);
-    const int Lq = sattn::clamp_length(p.q_lengths, b, p.nq);
-    const int Lk = sattn::clamp_length(p.k_lengths, b, p.cache.width * p.cache.page);
-    const sattn::Span sp{Lq, Lk, p.causal, p.window};
-    constexpr int E = kMaxD / 32;
-    float q[E], o[E] = {};
-#pragma unroll
-    for (int e = 0; e < E; ++e) {
-        const int x = lane + 32 * e;
-        q[e] = x < p.d && i < Lq ? __bfloat162float(p.q[b * p.sq.b + h * p.sq.h + i * p.sq.n + x]) : 0.f;
+    const Span sp = span_of(p, seq);
+    const Rows r(p, tile);
+    int lo, hi;
+    blocks_of(p, sp, r.q0, lo, hi);
+    const int64_t total = p.first[p.b];
+    const int n = runs(total, p.ctas);
+    int c0 = 0, c1 = -1;  // CTAs whose runs hold its blocks
+    if (hi > lo) {
+        int64_t at = p.first[seq];
+        for (int t = 0; t < tile; ++t) {
+            int a, z;
+            blocks_of(p, sp, Rows(p, t).q0, a, z);
+            at += (int64_t)(z - a) * p.hk;
+        }
+        at += (int64_t)kvh * (hi - lo);
+        // the run that holds block x: the last that begins at or before it
+        auto run_of = [&](int64_t x) {
+            int c = (int)(x * n / total);
+            while (c + 1 < n && run_begin(total, c + 1, n) <= x) ++c;
+            while (run_begin(total, c, n) > x) --c;
+            return c;
+        };
+        c0 = run_of(at);
+        c1 = run_of(at + (hi - lo) - 1);
+        if (c0 == c1) return;  // whole
     }
-    float m = -INFINITY, l = 0.f;
-    const int end = i < Lq ? sp.end(i) : 0;
-    for (int j = i < Lq ? sp.first(i) : 0; j < end; ++j) {
-        const int node = j - (Lk - Lq);
-        if (p.mask && node >= 0 && !(p.mask[((int64_t)b * p.nq + i) * p.words + node / 64] >> (node % 64) & 1)) continue;
-        int page, row;
-        const bool there = find_row(p.cache, b, j, p.status, page, row);
-        const __nv_bfloat16 *k = static_cast<const __nv_bfloat16 *>(p.cache.k) + page * p.cache.sk.b +
-                                 kvh * p.cache.sk.h + row * p.cache.sk.n;
-        const __nv_bfloat16 *v = static_cast<const __nv_bfloat16 *>(p.cache.v) + page * p.cache.sv.b +
-                                 kvh * p.cache.sv.h + row * p.cache.sv.n;
-        float s = 0.f;
+    constexpr int E = DP / 32;
+    for (int x = threadIdx.x >> 5; x < p.qbox * p.hbox; x += 4) {
+        const int i = r.q0 + (x & (p.qbox - 1)), hg = r.h0 + x / p.qbox;
+        if (hg >= p.group || i >= p.nq) continue;
+        // (a row begins at the end of its first CTA's run, and goes on at the start of the others')
+        auto slot = [&](int c) { return (int64_t)(2 * c + (c == c0 ? 1 : 0)) * p.N + x; };
+        float m = -INFINITY;
+        for (int c = c0 + lane; c <= c1; c += 32) m = fmaxf(m, p.part_lse[slot(c)]);
+        for (int o = 16; o; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
+        float acc[E] = {}, sum = 0.f;
+        if (m != -INFINITY)
+            for (int c = c0; c <= c1; ++c) {
+                const float w = __expf(p.part_lse[slot(c)] - m);
+                sum += w;
+                const float *src = p.part_o + slot(c) * DP + lane * E;
 #pragma unroll
-        for (int e = 0; e < E; ++e)
-            if (there && lane + 32 * e < p.d) s += q[e] * __bfloat162float(k[lane + 32 * e]);
+                for (int e = 0; e < E; ++e) acc[e] += lane * E + e < p.d ? w * src[e] : 0.f;
+            }
+        const float inv = sum > 0.f ? 1.f / sum : 0.f;
+        const int64_t h = (int64_t)kvh * p.group + hg;
+        __nv_bfloat16 *dst = p.out + seq * p.so.b + h * p.so.h + (int64_t)i * p.so.n;
+        if (lane * E < p.d) {
 #pragma unroll
-        for (int x = 16; x; x >>= 1) s += __shfl_xor_sync(0xffffffffu, s, x);
-        s *= p.scale;
-        const float mn = fmaxf(m, s), f = expf(m - mn), w = expf(s - mn);
-        l = l * f + w;
-        m = mn;
-#pragma unroll
-        for (int e = 0; e < E; ++e)
-            o[e] = o[e] * f + (there && lane + 32 * e < p.d ? w * __bfloat162float(v[lane + 32 * e]) : 0.f);
+            for (int e = 0; e < E; e += 2)
+                *reinterpret_cast<uint32_t *>(dst + lane * E + e) = pack2(acc[e] * inv, acc[e + 1] * inv);
+        }
+        if (lane == 0) p.lse[(seq * (int64_t)p.hq + h) * p.nq + i] = m == -INFINITY ? -INFINITY : m + logf(sum);
     }
-#pragma unroll
-    for (int e = 0; e < E; ++e)
-        if (lane + 32 * e < p.d)
-            p.out[b * p.so.b + h * p.so.h + i * p.so.n + lane + 32 * e] = __float2bfloat16_rn(l > 0.f ? o[e] / l : 0.f);
-    if (lane == 0) p.lse[r] = l > 0.f ? m + logf(l) : -INFINITY;
+}
+
+template <int DP, int N>
+int launch(const AttnCall &c, AttnParams &p) {
+    using L = Layout<DP, N>;
+    constexpr uint32_t kSmem = 1024 + L::kEnd + sizeof(Shared);
+    static_assert(kSmem <= 227 * 1024, "shared memory");
+    CUtensorMap tQ, tK, tV;
+    if (!sattn::encode_rows(&tQ, c.q, c.sq, c.b, c.hq, p.group, c.nq, c.d, p.qbox, p.hbox) ||
+        !sattn::encode_rows(&tK, c.cache.k, c.cache.sk, c.cache.pages, c.hk, 1, c.cache.page, c.d, p.box, 1) ||
+        !sattn::encode_rows(&tV, c.cache.v, c.cache.sv, c.cache.pages, c.hk, 1, c.cache.page, c.d, p.box, 1))
+        return LINFORMER_ERR_LAUNCH;
+    const int64_t most = (int64_t)c.b * c.hk * p.ntiles * (((int64_t)c.cache.width * c.cache.page + kTile - 1) / kTile);
+    p.N = N;
+    p.ctas = (int)std::min<int64_t>(device_sms(), most);
+    char *ws = nullptr;
+    const size_t parts = (size_t)2 * p.ctas * N, head = (kMaxSeqs + 1) * sizeof(int64_t);
+    if (workspace_alloc(reinterpret_cast<void **>(&ws), head + parts * (DP + 1) * sizeof(float), c.stream) != LINFORMER_OK)
+        return LINFORMER_ERR_ALLOC;
+    p.first = reinterpret_cast<int64_t *>(ws);
+    p.part_lse = reinterpret_cast<float *>(ws + head);
+    p.part_o = p.part_lse + parts;
+    const auto kernel = paged_attn_kernel<DP, N>;
+    constexpr int kSlot = 10 + (DP == 128 ? 4 : 0) + (N == 16 ? 0 : N == 32 ? 1 : N == 64 ? 2 : 3);
+    int st = sattn::allow_smem(reinterpret_cast<const void *>(kernel), kSmem, kSlot);
+    if (!st) {
+        KernelScope scope(LINFORMER_KERNEL_PAGED, c.stream);
+        kernel<<<p.ctas, kThreads, kSmem, c.stream>>>(tQ, tK, tV, p);
+        if (cudaGetLastError() != cudaSuccess) st = LINFORMER_ERR_LAUNCH;
+    }
+    if (!st) {
+        KernelScope scope(LINFORMER_KERNEL_PAGED, c.stream);
+        cudaLaunchConfig_t cfg{};
+        cudaLaunchAttribute attr[1];
+        attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+        attr[0].val.programmaticStreamSerializationAllowed = 1;
+        cfg.stream = c.stream;
+        cfg.attrs = attr;
+        cfg.numAttrs = 1;
+        cfg.gridDim = dim3((unsigned)(c.b * p.ntiles * c.hk));
+        cfg.blockDim = dim3(128);
+        if (cudaLaunchKernelEx(&cfg, join_kernel<DP>, p) != cudaSuccess) {
+            cudaGetLastError();
+            st = LINFORMER_ERR_LAUNCH;
+        }
+    }
+    workspace_free(ws, c.stream);
+    return st;
+}
+
+template <int DP>
+int launch_rows(const AttnCall &c, AttnParams &p) {
+    const int rows = p.qbox * p.hbox;
+    if (rows <= 16) return launch<DP, 16>(c, p);
+    if (rows <= 32) return launch<DP, 32>(c, p);
+    if (rows <= 64) return launch<DP, 64>(c, p);
+    return launch<DP, 128>(c, p);
 }
 
 }  // namespace
 
-int attention(const AttnCall &c) {
+int attention(const AttnCall &call) {
     AttnParams p{};
-    p.cache = c.cache;
-    p.q = static_cast<const __nv_bfloat16 *>(c.q);
-    p.out = static_cast<__nv_bfloat16 *>(c.out);
-    p.sq = c.sq;
-    p.so = c.so;
-    p.lse = c.lse;
-    p.q_lengths = c.q_lengths;
-    p.k_lengths = c.k_lengths;
-    p.mask = c.mask;
-    p.words = c.words;
-    p.b = c.b, p.hq = c.hq, p.hk = c.hk, p.nq = c.nq, p.d = c.d;
-    p.causal = c.causal;
-    p.window = c.window;
-    p.scale = c.scale;
+    p.words = call.words;
+    p.hq = call.hq;
+    p.hk = call.hk;
+    p.group = call.hq / call.hk;
+    p.nq = call.nq;
+    p.d = call.d;
+    p.causal = call.causal;
+    p.window = call.window;
+    p.scale = call.scale;
+    p.scale_log2 = call.scale * kLog2e;
+    p.so = call.so;
     p.status = device_status_ptr();
-    const int64_t blocks = ((int64_t)c.b * c.hq * c.nq + 3) / 4;
-    if (blocks > 0x7fffffffLL) return LINFORMER_ERR_SIZE;
-    KernelScope scope(LINFORMER_KERNEL_PAGED, c.stream);
-    paged_attn_kernel<<<(unsigned)blocks, 128, 0, c.stream>>>(p);
-    return cudaGetLastError() == cudaSuccess ? LINFORMER_OK : LINFORMER_ERR_LAUNCH;
+    p.pages = call.cache.pages;
+    p.page = call.cache.page;
+    p.width = call.cache.width;
+    p.shift = call.cache.shift;
+    p.box = std::min(call.cache.page, kTile);
+    p.nbox = kTile / p.box;
+    // Rows of a tile: 128 positions of one head, or the smallest power of two that holds all
+    // positions times as many heads of the group as fit.
+    p.qbox = kTile;
+    while (p.qbox > 1 && p.qbox / 2 >= call.nq) p.qbox /= 2;
+    p.hbox = std::min(kTile / p.qbox, p.group);
+    p.nch = (p.group + p.hbox - 1) / p.hbox;
+    const int64_t ntiles = ((int64_t)call.nq + p.qbox - 1) / p.qbox * p.nch;
+    if (ntiles * call.hk * std::min(call.b, kMaxSeqs) > 0x7fffffffLL) return LINFORMER_ERR_SIZE;
+    p.ntiles = (int)ntiles;
+    int st = LINFORMER_OK;
+    for (int b0 = 0; b0 < call.b && !st; b0 += kMaxSeqs) {
+        AttnCall c = call;
+        c.b = p.b = std::min(call.b - b0, kMaxSeqs);
+        c.q = static_cast<const __nv_bfloat16 *>(call.q) + b0 * call.sq.b;
+        p.out = static_cast<__nv_bfloat16 *>(call.out) + b0 * call.so.b;
+        p.lse = call.lse + (int64_t)b0 * call.hq * call.nq;
+        p.table = call.cache.table + (int64_t)b0 * call.cache.width;
+        p.k_lengths = call.k_lengths + b0;
+        p.q_lengths = call.q_lengths ? call.q_lengths + b0 : nullptr;
+        p.mask = call.mask ? call.mask + (int64_t)b0 * call.nq * call.words : nullptr;
+        st = call.d <= 64 ? launch_rows<64>(c, p) : launch_rows<128>(c, p);
+    }
+    return st;
 }
 
 }  // namespace paged

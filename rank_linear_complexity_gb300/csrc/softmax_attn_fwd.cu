@@ -794,7 +794,7 @@ bool encode_rows(CUtensorMap *m, const void *base, const Strides &s, int b, int 
 
 // The kernel's shared memory, allowed once per device (slot: one per kernel).
 int allow_smem(const void *kernel, uint32_t bytes, int slot) {
-    static std::atomic<uint8_t> done[kMaxDev][10];
+    static std::atomic<uint8_t> done[kMaxDev][18];
     int dev = 0;
     cudaGetDevice(&dev);
     if (dev >= 0 && dev < kMaxDev && done[dev][slot].load(std::memory_order_acquire)) return LINFORMER_OK;
