@@ -23,6 +23,7 @@
 //   warps 0-7   softmax: two groups of four warps, each half of the columns
 //   warp 8      loads: looks the pages up and issues a box a lane
 //   warp 9      one thread issues the products
+//   warps 10 11 rows without keys: O = 0, lse = -inf
 #include <algorithm>
 #include <cmath>
 
@@ -40,7 +41,7 @@ using sattn::pack2;
 using sattn::Span;
 
 constexpr int kTile = 128;  // keys of a block
-constexpr int kThreads = 320, kLoadWarp = 8, kMmaWarp = 9;
+constexpr int kThreads = 384, kLoadWarp = 8, kMmaWarp = 9, kEmptyWarp = 10;
 constexpr int kMaxSeqs = 512;  // sequences of a launch
 constexpr float kOutgrown = 16.f, kLog2e = 1.4426950408889634f;
 constexpr int kMinRun = 1;  // blocks of a CTA at least
@@ -431,6 +432,24 @@ paged_attn_kernel(const __grid_constant__ CUtensorMap tQ, const __grid_constant_
             mbar_wait_drain(&sh->drain, 0);
         }
         __syncwarp();
+    } else if (warp >= kEmptyWarp) {  // ---------------- tiles without blocks, a share a CTA
+        const int units = p.b * p.ntiles * p.hk;
+        for (int u = blockIdx.x; u < units; u += gridDim.x) {
+            const int kvh = u % p.hk, tile = u / p.hk % p.ntiles, seq = u / p.hk / p.ntiles;
+            const Rows r(p, tile);
+            int lo, hi;
+            blocks_of(p, span_of(p, seq), r.q0, lo, hi);
+            if (hi > lo) continue;
+            for (int x = warp - kEmptyWarp; x < p.qbox * p.hbox; x += 2) {
+                const int i = r.q0 + (x & (p.qbox - 1)), hg = r.h0 + x / p.qbox;
+                if (hg >= p.group || i >= p.nq) continue;
+                const int64_t h = (int64_t)kvh * p.group + hg;
+                if (8 * lane < p.d)
+                    *reinterpret_cast<uint4 *>(p.out + seq * p.so.b + h * p.so.h + (int64_t)i * p.so.n + 8 * lane) =
+                        make_uint4(0u, 0u, 0u, 0u);
+                if (lane == 0) p.lse[(seq * (int64_t)p.hq + h) * p.nq + i] = -INFINITY;
+            }
+        }
     } else {  // ---------------- softmax: one key a thread, C of the rows
         const int w = warp >> 2, key0 = tid & 127, c0 = w * C;
         const uint32_t lanes = (uint32_t)((warp & 3) * 32) << 16;
@@ -597,67 +616,59 @@ paged_attn_kernel(const __grid_constant__ CUtensorMap tQ, const __grid_constant_
 }
 
 // Joins the parts of the rows whose run of blocks was cut: lse = log sum_s exp(lse_s), O = sum_s
-// exp(lse_s - lse) O_s; rows without blocks get O = 0 and lse = -inf.  A block a tile of a key/value
-// head, a warp a row.
+// exp(lse_s - lse) O_s.  blockIdx.x: the CTA that did the last part (any other's blocks leave at
+// once); a warp a row.
+constexpr int kJoinWarps = 4;
 template <int DP>
-__global__ void __launch_bounds__(128) join_kernel(const AttnParams p) {
+__global__ void __launch_bounds__(kJoinWarps * 32) join_kernel(const __grid_constant__ AttnParams p) {
     wait_prerequisites();
-    const int unit = blockIdx.x, kvh = unit % p.hk, tile = unit / p.hk % p.ntiles, seq = unit / p.hk / p.ntiles;
-    const int lane = threadIdx.x & 31;
-    const Span sp = span_of(p, seq);
-    const Rows r(p, tile);
-    int lo, hi;
-    blocks_of(p, sp, r.q0, lo, hi);
-    const int64_t total = p.first[p.b];
-    const int n = runs(total, p.ctas);
-    int c0 = 0, c1 = -1;  // CTAs whose runs hold its blocks
-    if (hi > lo) {
-        int64_t at = p.first[seq];
-        for (int t = 0; t < tile; ++t) {
-            int a, z;
-            blocks_of(p, sp, Rows(p, t).q0, a, z);
-            at += (int64_t)(z - a) * p.hk;
-        }
-        at += (int64_t)kvh * (hi - lo);
-        // the run that holds block x: the last that begins at or before it
-        auto run_of = [&](int64_t x) {
-            int c = (int)(x * n / total);
-            while (c + 1 < n && run_begin(total, c + 1, n) <= x) ++c;
-            while (run_begin(total, c, n) > x) --c;
-            return c;
-        };
-        c0 = run_of(at);
-        c1 = run_of(at + (hi - lo) - 1);
-        if (c0 == c1) return;  // whole
-    }
+    const int x = blockIdx.y * kJoinWarps + (threadIdx.x >> 5), lane = threadIdx.x & 31;
+    const Walk at(p, p.first, blockIdx.x);
+    if (at.at >= at.end || at.blk == 0 || at.end - at.at < at.hi - at.lo - at.blk) return;
+    const Rows r(p, at.tile);
+    const int i = r.q0 + (x & (p.qbox - 1)), hg = r.h0 + x / p.qbox;
+    if (x >= p.qbox * p.hbox || hg >= p.group || i >= p.nq) return;
+    const int64_t total = p.first[p.b], begin = at.at - at.blk;
+    const int n = runs(total, p.ctas), c1 = blockIdx.x;
+    int c0 = c1 - 1;  // the CTA whose run holds the first block
+    while (run_begin(total, c0, n) > begin) --c0;
+    // a row is cut at the end of its first CTA's run, and goes on at the start of the others'
+    auto slot = [&](int c) { return (int64_t)(2 * c + (c == c0 ? 1 : 0)) * p.N + x; };
+    float m = -INFINITY;
+    for (int c = c0 + lane; c <= c1; c += 32) m = fmaxf(m, p.part_lse[slot(c)]);
+#pragma unroll
+    for (int o = 16; o; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
     constexpr int E = DP / 32;
-    for (int x = threadIdx.x >> 5; x < p.qbox * p.hbox; x += 4) {
-        const int i = r.q0 + (x & (p.qbox - 1)), hg = r.h0 + x / p.qbox;
-        if (hg >= p.group || i >= p.nq) continue;
-        // (a row begins at the end of its first CTA's run, and goes on at the start of the others')
-        auto slot = [&](int c) { return (int64_t)(2 * c + (c == c0 ? 1 : 0)) * p.N + x; };
-        float m = -INFINITY;
-        for (int c = c0 + lane; c <= c1; c += 32) m = fmaxf(m, p.part_lse[slot(c)]);
-        for (int o = 16; o; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
-        float acc[E] = {}, sum = 0.f;
-        if (m != -INFINITY)
-            for (int c = c0; c <= c1; ++c) {
-                const float w = __expf(p.part_lse[slot(c)] - m);
+    float acc[E] = {}, sum = 0.f;
+    if (m != -INFINITY)
+        for (int c = c0; c <= c1; c += 32) {
+            const int some = min(32, c1 + 1 - c);
+            const float mine = lane < some ? __expf(p.part_lse[slot(c + lane)] - m) : 0.f;
+#pragma unroll 8
+            for (int k = 0; k < some; ++k) {
+                const float w = __shfl_sync(0xffffffffu, mine, k);
                 sum += w;
-                const float *src = p.part_o + slot(c) * DP + lane * E;
+                float v[E];
+                if constexpr (E == 4) {
+                    const float4 t = *reinterpret_cast<const float4 *>(p.part_o + slot(c + k) * DP + lane * E);
+                    v[0] = t.x, v[1] = t.y, v[2] = t.z, v[3] = t.w;
+                } else {
+                    const float2 t = *reinterpret_cast<const float2 *>(p.part_o + slot(c + k) * DP + lane * E);
+                    v[0] = t.x, v[1] = t.y;
+                }
 #pragma unroll
-                for (int e = 0; e < E; ++e) acc[e] += lane * E + e < p.d ? w * src[e] : 0.f;
+                for (int e = 0; e < E; ++e) acc[e] += w * v[e];
             }
-        const float inv = sum > 0.f ? 1.f / sum : 0.f;
-        const int64_t h = (int64_t)kvh * p.group + hg;
-        __nv_bfloat16 *dst = p.out + seq * p.so.b + h * p.so.h + (int64_t)i * p.so.n;
-        if (lane * E < p.d) {
-#pragma unroll
-            for (int e = 0; e < E; e += 2)
-                *reinterpret_cast<uint32_t *>(dst + lane * E + e) = pack2(acc[e] * inv, acc[e + 1] * inv);
         }
-        if (lane == 0) p.lse[(seq * (int64_t)p.hq + h) * p.nq + i] = m == -INFINITY ? -INFINITY : m + logf(sum);
+    const float inv = sum > 0.f ? 1.f / sum : 0.f;
+    const int64_t h = (int64_t)at.kvh * p.group + hg;
+    __nv_bfloat16 *dst = p.out + at.seq * p.so.b + h * p.so.h + (int64_t)i * p.so.n;
+    if (lane * E < p.d) {
+#pragma unroll
+        for (int e = 0; e < E; e += 2)
+            *reinterpret_cast<uint32_t *>(dst + lane * E + e) = pack2(acc[e] * inv, acc[e + 1] * inv);
     }
+    if (lane == 0) p.lse[(at.seq * (int64_t)p.hq + h) * p.nq + i] = m == -INFINITY ? -INFINITY : m + logf(sum);
 }
 
 template <int DP, int N>
@@ -674,7 +685,7 @@ int launch(const AttnCall &c, AttnParams &p) {
     p.N = N;
     p.ctas = (int)std::min<int64_t>(device_sms(), most);
     char *ws = nullptr;
-    const size_t parts = (size_t)2 * p.ctas * N, head = (kMaxSeqs + 1) * sizeof(int64_t);
+    const size_t parts = (size_t)2 * p.ctas * N, head = (kMaxSeqs + 2) * sizeof(int64_t);  // (a multiple of 16)
     if (workspace_alloc(reinterpret_cast<void **>(&ws), head + parts * (DP + 1) * sizeof(float), c.stream) != LINFORMER_OK)
         return LINFORMER_ERR_ALLOC;
     p.first = reinterpret_cast<int64_t *>(ws);
@@ -697,8 +708,8 @@ int launch(const AttnCall &c, AttnParams &p) {
         cfg.stream = c.stream;
         cfg.attrs = attr;
         cfg.numAttrs = 1;
-        cfg.gridDim = dim3((unsigned)(c.b * p.ntiles * c.hk));
-        cfg.blockDim = dim3(128);
+        cfg.gridDim = dim3((unsigned)p.ctas, (unsigned)((p.qbox * p.hbox + kJoinWarps - 1) / kJoinWarps));
+        cfg.blockDim = dim3(kJoinWarps * 32);
         if (cudaLaunchKernelEx(&cfg, join_kernel<DP>, p) != cudaSuccess) {
             cudaGetLastError();
             st = LINFORMER_ERR_LAUNCH;
