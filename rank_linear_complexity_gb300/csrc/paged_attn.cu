@@ -27,132 +27,13 @@
 #include <algorithm>
 #include <cmath>
 
-#include "paged.cuh"
-#include "sm100_ptx.cuh"
-#include "softmax_attn.cuh"
+#include "paged_attn.cuh"
 
 namespace linformer {
 namespace paged {
 namespace {
 
-using namespace ptx;
-using sattn::clamp_length;
-using sattn::pack2;
-using sattn::Span;
-
-constexpr int kTile = 128;  // keys of a block
 constexpr int kThreads = 384, kLoadWarp = 8, kMmaWarp = 9, kEmptyWarp = 10;
-constexpr int kMaxSeqs = 512;  // sequences of a launch
-constexpr float kOutgrown = 16.f, kLog2e = 1.4426950408889634f;
-constexpr int kMinRun = 1;  // blocks of a CTA at least
-
-struct AttnParams {
-    const int32_t *q_lengths, *k_lengths, *table;
-    const uint64_t *mask;
-    __nv_bfloat16 *out;
-    Strides so;
-    float *lse;
-    float *part_o, *part_lse;  // [2 per CTA][N][DP], [2 per CTA][N]
-    int64_t *first;            // [b + 1]: where the blocks of each sequence begin in the list
-    int words, b, hq, hk, group, nq, d, causal, window;
-    int qbox, hbox, nch, ntiles, N, ctas;
-    int pages, page, width, shift, box, nbox;
-    float scale, scale_log2;
-    int *status;
-};
-
-// The rows of a tile: qbox positions of hbox heads of a group.
-struct Rows {
-    int q0, h0;
-    __device__ __forceinline__ Rows(const AttnParams &p, int tile) {
-        const int qt = p.nch > 1 ? tile / p.nch : tile;
-        q0 = qt * p.qbox;
-        h0 = (tile - qt * p.nch) * p.hbox;
-    }
-};
-
-// The key blocks that a tile's rows see.
-__device__ __forceinline__ void blocks_of(const AttnParams &p, const Span &sp, int q0, int &lo, int &hi) {
-    lo = hi = 0;
-    const int last = min(q0 + p.qbox, sp.Lq) - 1;
-    if (last < q0) return;
-    const int e = sp.end(last), f = sp.first(q0);
-    if (e <= f) return;
-    lo = f / kTile;
-    hi = (e + kTile - 1) / kTile;
-}
-__device__ __forceinline__ Span span_of(const AttnParams &p, int seq) {
-    return Span{clamp_length(p.q_lengths, seq, p.nq), clamp_length(p.k_lengths, seq, p.width * p.page), p.causal,
-                p.window};
-}
-__device__ __forceinline__ int64_t run_begin(int64_t total, int cta, int ctas) { return total * cta / ctas; }
-__device__ __forceinline__ int runs(int64_t total, int ctas) {
-    return (int)min((int64_t)ctas, max((int64_t)1, total / kMinRun));
-}
-
-// A CTA's part of the list, tile by tile: sequence-major, then tile, then key/value head.
-struct Item {
-    int seq, tile, kvh, lo, hi;  // blocks [lo, hi) of it
-    Span sp;
-    int slot;  // where its partial result goes; -1: the row is whole
-};
-struct Walk {
-    int64_t at, end;
-    int seq, tile, kvh, blk, lo, hi, slot;
-    Span sp;
-    __device__ __forceinline__ Walk(const AttnParams &p, const int64_t *first, int cta) {
-        const int n = runs(first[p.b], p.ctas);
-        at = end = 0;
-        if (cta >= n) return;
-        at = run_begin(first[p.b], cta, n);
-        end = run_begin(first[p.b], cta + 1, n);
-        if (at >= end) return;
-        int a = 0, z = p.b;  // first[a] <= at < first[z]
-        while (z - a > 1) {
-            const int m = (a + z) / 2;
-            if (first[m] <= at) a = m;
-            else z = m;
-        }
-        seq = a;
-        sp = span_of(p, seq);
-        int64_t off = at - first[seq];
-        for (tile = 0;; ++tile) {
-            blocks_of(p, sp, Rows(p, tile).q0, lo, hi);
-            const int64_t c = (int64_t)(hi - lo) * p.hk;
-            if (off < c) break;
-            off -= c;
-        }
-        kvh = (int)(off / (hi - lo));
-        blk = (int)(off - (int64_t)kvh * (hi - lo));
-        slot = 2 * cta;
-    }
-    // The next item, while there is one.
-    __device__ __forceinline__ bool next(const AttnParams &p, Item &it) {
-        if (at >= end) return false;
-        const int n = (int)min((int64_t)(hi - lo - blk), end - at);
-        it.seq = seq;
-        it.tile = tile;
-        it.kvh = kvh;
-        it.lo = lo + blk;
-        it.hi = it.lo + n;
-        it.sp = sp;
-        it.slot = blk == 0 && it.hi == hi ? -1 : blk ? slot : slot + 1;
-        at += n;
-        blk = 0;
-        if (at < end && ++kvh == p.hk) {
-            kvh = 0;
-            do {
-                if (++tile == p.ntiles) {
-                    tile = 0;
-                    ++seq;
-                    sp = span_of(p, seq);
-                }
-                blocks_of(p, sp, Rows(p, tile).q0, lo, hi);
-            } while (hi <= lo);
-        }
-        return true;
-    }
-};
 
 template <int DP, int N>
 struct Layout {
@@ -178,8 +59,7 @@ struct Shared {
     alignas(16) float off[128];
     alignas(16) float f[128];
     float part[2][4][64];  // a value a column, by warp of each group
-    int64_t first[kMaxSeqs + 1];
-    int64_t sums[32];
+    int first[kMaxSeqs + 1];
 };
 
 template <int C>
@@ -287,35 +167,10 @@ paged_attn_kernel(const __grid_constant__ CUtensorMap tQ, const __grid_constant_
     for (uint32_t x = tid * 16; x < L::kQBytes; x += kThreads * 16)
         *reinterpret_cast<uint4 *>(smem + L::kQ + x) = make_uint4(0u, 0u, 0u, 0u);
     fence_proxy_async_smem();
-    // where each sequence begins in the list of blocks
-    for (int s = tid; s < p.b; s += kThreads) {
-        const Span sp = span_of(p, s);
-        int64_t sum = 0;
-        for (int t = 0; t < p.ntiles; ++t) {
-            int lo, hi;
-            blocks_of(p, sp, Rows(p, t).q0, lo, hi);
-            sum += (int64_t)(hi - lo) * p.hk;
-        }
-        sh->first[s + 1] = sum;
-    }
     tc_fence_before();
+    fill_first(p, sh->first, tid, kThreads);
     __syncthreads();
     tc_fence_after();
-    if (warp == 0) {
-        constexpr int kEach = kMaxSeqs / 32;
-        int64_t sum = 0;
-        const int s0 = lane * kEach, s1 = min(s0 + kEach, p.b);
-        for (int s = s0; s < s1; ++s) sum += sh->first[s + 1];
-        int64_t run = sum;
-        for (int o = 1; o < 32; o *= 2) {
-            const int64_t x = __shfl_up_sync(0xffffffffu, run, o);
-            if (lane >= o) run += x;
-        }
-        run -= sum;
-        for (int s = s0; s < s1; ++s) sh->first[s + 1] = run += sh->first[s + 1];
-        if (lane == 0) sh->first[0] = 0;
-    }
-    __syncthreads();
     if (blockIdx.x == 0)
         for (int s = tid; s <= p.b; s += kThreads) p.first[s] = sh->first[s];
     const uint32_t tmem = sh->tmem;
@@ -331,7 +186,7 @@ paged_attn_kernel(const __grid_constant__ CUtensorMap tQ, const __grid_constant_
         int ring = 0, nq = 0;
         bool ok = true;
         while (ok && walk.next(p, it)) {
-            const Rows r(p, it.tile);
+            const Rows r(p, it.unit);
             if (nq > 0 && !warp_spin(&sh->q_free, (nq - 1) & 1, p.status, 120, abort_flag)) break;
             if (lane == 0) {
                 mbar_arrive_expect_tx(&sh->q_full, (uint32_t)(p.qbox * p.hbox * DP * 2));
@@ -340,16 +195,7 @@ paged_attn_kernel(const __grid_constant__ CUtensorMap tQ, const __grid_constant_
             }
             ++nq;
             const int32_t *table = p.table + (int64_t)it.seq * p.width;
-            // the page of this lane's rows in block j; p.pages, which is outside the map and comes
-            // as zeros, where there is none
-            auto look = [&](int j) {
-                const int at = j * kTile + row;
-                if (!mine || at >= it.sp.Lk) return p.pages;
-                const int x = __ldg(table + (at >> p.shift));
-                if ((unsigned)x < (unsigned)p.pages) return x;
-                if (p.status) atomicExch(p.status, kBadPage);
-                return p.pages;
-            };
+            auto look = [&](int j) { return mine ? page_of(p, table, j, row, it.sp.Lk) : 0; };
             int page = look(it.lo);
             for (int j = it.lo; j < it.hi; ++j) {
                 const int now = page, at = (j * kTile + row) & (p.page - 1);
@@ -432,24 +278,8 @@ paged_attn_kernel(const __grid_constant__ CUtensorMap tQ, const __grid_constant_
             mbar_wait_drain(&sh->drain, 0);
         }
         __syncwarp();
-    } else if (warp >= kEmptyWarp) {  // ---------------- tiles without blocks, a share a CTA
-        const int units = p.b * p.ntiles * p.hk;
-        for (int u = blockIdx.x; u < units; u += gridDim.x) {
-            const int kvh = u % p.hk, tile = u / p.hk % p.ntiles, seq = u / p.hk / p.ntiles;
-            const Rows r(p, tile);
-            int lo, hi;
-            blocks_of(p, span_of(p, seq), r.q0, lo, hi);
-            if (hi > lo) continue;
-            for (int x = warp - kEmptyWarp; x < p.qbox * p.hbox; x += 2) {
-                const int i = r.q0 + (x & (p.qbox - 1)), hg = r.h0 + x / p.qbox;
-                if (hg >= p.group || i >= p.nq) continue;
-                const int64_t h = (int64_t)kvh * p.group + hg;
-                if (8 * lane < p.d)
-                    *reinterpret_cast<uint4 *>(p.out + seq * p.so.b + h * p.so.h + (int64_t)i * p.so.n + 8 * lane) =
-                        make_uint4(0u, 0u, 0u, 0u);
-                if (lane == 0) p.lse[(seq * (int64_t)p.hq + h) * p.nq + i] = -INFINITY;
-            }
-        }
+    } else if (warp >= kEmptyWarp) {  // ---------------- rows without keys
+        write_empty(p, warp - kEmptyWarp, kThreads / 32 - kEmptyWarp, lane);
     } else {  // ---------------- softmax: one key a thread, C of the rows
         const int w = warp >> 2, key0 = tid & 127, c0 = w * C;
         const uint32_t lanes = (uint32_t)((warp & 3) * 32) << 16;
@@ -469,7 +299,7 @@ paged_attn_kernel(const __grid_constant__ CUtensorMap tQ, const __grid_constant_
             float l[C];
 #pragma unroll
             for (int c = 0; c < C; ++c) l[c] = 0.f;
-            const Rows r(p, it.tile);
+            const Rows r(p, it.unit);
             const int before = it.sp.Lk - it.sp.Lq;
             const uint64_t *mask = p.mask ? p.mask + (int64_t)it.seq * p.nq * p.words : nullptr;
             for (int j = it.lo; j < it.hi; ++j, ++n) {
@@ -622,18 +452,23 @@ constexpr int kJoinWarps = 4;
 template <int DP>
 __global__ void __launch_bounds__(kJoinWarps * 32) join_kernel(const __grid_constant__ AttnParams p) {
     wait_prerequisites();
-    const int x = blockIdx.y * kJoinWarps + (threadIdx.x >> 5), lane = threadIdx.x & 31;
+    const int rows = p.qbox * p.hbox, lane = threadIdx.x & 31;
+    int x = blockIdx.y * kJoinWarps + (threadIdx.x >> 5);
+    const int t = x / rows;
+    x -= t * rows;
     const Walk at(p, p.first, blockIdx.x);
     if (at.at >= at.end || at.blk == 0 || at.end - at.at < at.hi - at.lo - at.blk) return;
-    const Rows r(p, at.tile);
+    const int tile = at.unit * p.per + t;
+    if (t >= p.per || tile >= p.ntiles) return;
+    const Rows r(p, tile);
     const int i = r.q0 + (x & (p.qbox - 1)), hg = r.h0 + x / p.qbox;
-    if (x >= p.qbox * p.hbox || hg >= p.group || i >= p.nq) return;
-    const int64_t total = p.first[p.b], begin = at.at - at.blk;
+    if (hg >= p.group || i >= p.nq) return;
+    const int total = p.first[p.b], begin = at.at - at.blk;
     const int n = runs(total, p.ctas), c1 = blockIdx.x;
     int c0 = c1 - 1;  // the CTA whose run holds the first block
     while (run_begin(total, c0, n) > begin) --c0;
     // a row is cut at the end of its first CTA's run, and goes on at the start of the others'
-    auto slot = [&](int c) { return (int64_t)(2 * c + (c == c0 ? 1 : 0)) * p.N + x; };
+    auto slot = [&](int c) { return ((int64_t)(2 * c + (c == c0 ? 1 : 0)) * p.per + t) * p.N + x; };
     float m = -INFINITY;
     for (int c = c0 + lane; c <= c1; c += 32) m = fmaxf(m, p.part_lse[slot(c)]);
 #pragma unroll
@@ -648,6 +483,7 @@ __global__ void __launch_bounds__(kJoinWarps * 32) join_kernel(const __grid_cons
             for (int k = 0; k < some; ++k) {
                 const float w = __shfl_sync(0xffffffffu, mine, k);
                 sum += w;
+                if (w == 0.f) continue;  // (a part without keys wrote no O)
                 float v[E];
                 if constexpr (E == 4) {
                     const float4 t = *reinterpret_cast<const float4 *>(p.part_o + slot(c + k) * DP + lane * E);
@@ -676,45 +512,21 @@ int launch(const AttnCall &c, AttnParams &p) {
     using L = Layout<DP, N>;
     constexpr uint32_t kSmem = 1024 + L::kEnd + sizeof(Shared);
     static_assert(kSmem <= 227 * 1024, "shared memory");
-    CUtensorMap tQ, tK, tV;
-    if (!sattn::encode_rows(&tQ, c.q, c.sq, c.b, c.hq, p.group, c.nq, c.d, p.qbox, p.hbox) ||
-        !sattn::encode_rows(&tK, c.cache.k, c.cache.sk, c.cache.pages, c.hk, 1, c.cache.page, c.d, p.box, 1) ||
-        !sattn::encode_rows(&tV, c.cache.v, c.cache.sv, c.cache.pages, c.hk, 1, c.cache.page, c.d, p.box, 1))
-        return LINFORMER_ERR_LAUNCH;
-    const int64_t most = (int64_t)c.b * c.hk * p.ntiles * (((int64_t)c.cache.width * c.cache.page + kTile - 1) / kTile);
+    Maps m;
+    if (!encode_maps(c, p, m)) return LINFORMER_ERR_LAUNCH;
     p.N = N;
-    p.ctas = (int)std::min<int64_t>(device_sms(), most);
-    char *ws = nullptr;
-    const size_t parts = (size_t)2 * p.ctas * N, head = (kMaxSeqs + 2) * sizeof(int64_t);  // (a multiple of 16)
-    if (workspace_alloc(reinterpret_cast<void **>(&ws), head + parts * (DP + 1) * sizeof(float), c.stream) != LINFORMER_OK)
-        return LINFORMER_ERR_ALLOC;
-    p.first = reinterpret_cast<int64_t *>(ws);
-    p.part_lse = reinterpret_cast<float *>(ws + head);
-    p.part_o = p.part_lse + parts;
+    void *ws = nullptr;
+    int st = take_workspace(p, DP, &ws, c.stream);
+    if (st) return st;
     const auto kernel = paged_attn_kernel<DP, N>;
     constexpr int kSlot = 10 + (DP == 128 ? 4 : 0) + (N == 16 ? 0 : N == 32 ? 1 : N == 64 ? 2 : 3);
-    int st = sattn::allow_smem(reinterpret_cast<const void *>(kernel), kSmem, kSlot);
+    st = sattn::allow_smem(reinterpret_cast<const void *>(kernel), kSmem, kSlot);
     if (!st) {
         KernelScope scope(LINFORMER_KERNEL_PAGED, c.stream);
-        kernel<<<p.ctas, kThreads, kSmem, c.stream>>>(tQ, tK, tV, p);
+        kernel<<<p.ctas, kThreads, kSmem, c.stream>>>(m.q, m.k, m.v, p);
         if (cudaGetLastError() != cudaSuccess) st = LINFORMER_ERR_LAUNCH;
     }
-    if (!st) {
-        KernelScope scope(LINFORMER_KERNEL_PAGED, c.stream);
-        cudaLaunchConfig_t cfg{};
-        cudaLaunchAttribute attr[1];
-        attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-        attr[0].val.programmaticStreamSerializationAllowed = 1;
-        cfg.stream = c.stream;
-        cfg.attrs = attr;
-        cfg.numAttrs = 1;
-        cfg.gridDim = dim3((unsigned)p.ctas, (unsigned)((p.qbox * p.hbox + kJoinWarps - 1) / kJoinWarps));
-        cfg.blockDim = dim3(kJoinWarps * 32);
-        if (cudaLaunchKernelEx(&cfg, join_kernel<DP>, p) != cudaSuccess) {
-            cudaGetLastError();
-            st = LINFORMER_ERR_LAUNCH;
-        }
-    }
+    if (!st) st = launch_join(p, DP, c.stream);
     workspace_free(ws, c.stream);
     return st;
 }
@@ -724,11 +536,44 @@ int launch_rows(const AttnCall &c, AttnParams &p) {
     const int rows = p.qbox * p.hbox;
     if (rows <= 16) return launch<DP, 16>(c, p);
     if (rows <= 32) return launch<DP, 32>(c, p);
-    if (rows <= 64) return launch<DP, 64>(c, p);
-    return launch<DP, 128>(c, p);
+    return launch<DP, 64>(c, p);
 }
 
 }  // namespace
+
+bool encode_maps(const AttnCall &c, const AttnParams &p, Maps &m) {
+    const Cache &k = c.cache;
+    return sattn::encode_rows(&m.q, c.q, c.sq, c.b, c.hq, p.group, c.nq, c.d, p.qbox, p.hbox) &&
+           sattn::encode_rows(&m.k, k.k, k.sk, k.pages, c.hk, 1, k.page, c.d, p.box, 1) &&
+           sattn::encode_rows(&m.v, k.v, k.sv, k.pages, c.hk, 1, k.page, c.d, p.box, 1);
+}
+
+int take_workspace(AttnParams &p, int dp, void **ws, cudaStream_t s) {
+    constexpr size_t kHead = (kMaxSeqs + 4) * sizeof(int);
+    static_assert(kHead % 16 == 0, "parts are read 16 bytes at a time");
+    const size_t parts = (size_t)2 * p.ctas * p.per * p.N;
+    if (workspace_alloc(ws, kHead + parts * (dp + 1) * sizeof(float), s) != LINFORMER_OK) return LINFORMER_ERR_ALLOC;
+    p.first = static_cast<int *>(*ws);
+    p.part_o = reinterpret_cast<float *>(static_cast<char *>(*ws) + kHead);
+    p.part_lse = p.part_o + parts * dp;
+    return LINFORMER_OK;
+}
+
+int launch_join(const AttnParams &p, int dp, cudaStream_t s) {
+    KernelScope scope(LINFORMER_KERNEL_PAGED, s);
+    cudaLaunchConfig_t cfg{};
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    cfg.stream = s;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    cfg.gridDim = dim3((unsigned)p.ctas, (unsigned)((p.per * p.qbox * p.hbox + kJoinWarps - 1) / kJoinWarps));
+    cfg.blockDim = dim3(kJoinWarps * 32);
+    if (cudaLaunchKernelEx(&cfg, dp == 64 ? join_kernel<64> : join_kernel<128>, p) == cudaSuccess) return LINFORMER_OK;
+    cudaGetLastError();
+    return LINFORMER_ERR_LAUNCH;
+}
 
 int attention(const AttnCall &call) {
     AttnParams p{};
@@ -743,6 +588,7 @@ int attention(const AttnCall &call) {
     p.scale = call.scale;
     p.scale_log2 = call.scale * kLog2e;
     p.so = call.so;
+    p.wide_stores = sattn::wide_stores(call.out, call.so, call.d);
     p.status = device_status_ptr();
     p.pages = call.cache.pages;
     p.page = call.cache.page;
@@ -757,12 +603,20 @@ int attention(const AttnCall &call) {
     p.hbox = std::min(kTile / p.qbox, p.group);
     p.nch = (p.group + p.hbox - 1) / p.hbox;
     const int64_t ntiles = ((int64_t)call.nq + p.qbox - 1) / p.qbox * p.nch;
-    if (ntiles * call.hk * std::min(call.b, kMaxSeqs) > 0x7fffffffLL) return LINFORMER_ERR_SIZE;
+    const bool wide = p.qbox * p.hbox > 64;
+    p.per = wide ? 2 : 1;
+    const int64_t units = (ntiles + p.per - 1) / p.per;
+    // the list of blocks is counted in 32 bits: at most kMaxSeqs sequences a launch, fewer where they
+    // are huge
+    const int64_t most = units * call.hk * (((int64_t)p.width * p.page + kTile - 1) / kTile);
+    if (most > 0x7fffffffLL) return LINFORMER_ERR_SIZE;
+    const int seqs = (int)std::min<int64_t>(kMaxSeqs, 0x7fffffffLL / most);
     p.ntiles = (int)ntiles;
+    p.units = (int)units;
     int st = LINFORMER_OK;
-    for (int b0 = 0; b0 < call.b && !st; b0 += kMaxSeqs) {
+    for (int b0 = 0; b0 < call.b && !st; b0 += seqs) {
         AttnCall c = call;
-        c.b = p.b = std::min(call.b - b0, kMaxSeqs);
+        c.b = p.b = std::min(call.b - b0, seqs);
         c.q = static_cast<const __nv_bfloat16 *>(call.q) + b0 * call.sq.b;
         p.out = static_cast<__nv_bfloat16 *>(call.out) + b0 * call.so.b;
         p.lse = call.lse + (int64_t)b0 * call.hq * call.nq;
@@ -770,7 +624,9 @@ int attention(const AttnCall &call) {
         p.k_lengths = call.k_lengths + b0;
         p.q_lengths = call.q_lengths ? call.q_lengths + b0 : nullptr;
         p.mask = call.mask ? call.mask + (int64_t)b0 * call.nq * call.words : nullptr;
-        st = call.d <= 64 ? launch_rows<64>(c, p) : launch_rows<128>(c, p);
+        p.ctas = (int)std::min<int64_t>(device_sms(), most * c.b);
+        if (wide) st = launch_wide(c, p);
+        else st = call.d <= 64 ? launch_rows<64>(c, p) : launch_rows<128>(c, p);
     }
     return st;
 }

@@ -1,0 +1,221 @@
+// What the kernels of the attention over pages share (paged_attn.cu, paged_attn_wide.cu): the list of
+// key blocks, the runs of it that CTAs take, pages of a block.
+#pragma once
+
+#include <algorithm>
+
+#include "paged.cuh"
+#include "sm100_ptx.cuh"
+#include "softmax_attn.cuh"
+
+namespace linformer {
+namespace paged {
+
+using namespace ptx;
+using sattn::clamp_length;
+using sattn::kTile;  // keys of a block
+using sattn::pack2;
+using sattn::Span;
+
+constexpr int kMaxSeqs = 512;  // sequences of a launch
+constexpr int kMinRun = 1;     // blocks of a CTA at least
+constexpr float kOutgrown = 16.f, kLog2e = 1.4426950408889634f;
+
+struct AttnParams {
+    const int32_t *q_lengths, *k_lengths, *table;
+    const uint64_t *mask;
+    __nv_bfloat16 *out;
+    Strides so;
+    float *lse;
+    float *part_o, *part_lse;  // [2 per CTA][per][N][DP], [2 per CTA][per][N]
+    int *first;                // [b + 1]: where the blocks of each sequence begin in the list
+    int words, b, hq, hk, group, nq, d, causal, window;
+    // tiles of qbox positions of hbox heads (nch tiles to a group), `per` of them to a unit of work;
+    // N: rows of a tile in the workspace
+    int qbox, hbox, nch, ntiles, per, units, N, ctas;
+    int pages, page, width, shift, box, nbox;  // nbox boxes of `box` rows make a block of keys
+    float scale, scale_log2;
+    int wide_stores;
+    int *status;
+};
+
+// The rows of a tile.
+struct Rows {
+    int q0, h0;
+    __device__ __forceinline__ Rows(const AttnParams &p, int tile) {
+        const int qt = p.nch > 1 ? tile / p.nch : tile;
+        q0 = qt * p.qbox;
+        h0 = (tile - qt * p.nch) * p.hbox;
+    }
+};
+
+// The key blocks that a tile's rows see.
+__device__ __forceinline__ void blocks_of(const AttnParams &p, const Span &sp, int q0, int &lo, int &hi) {
+    lo = hi = 0;
+    const int last = min(q0 + p.qbox, sp.Lq) - 1;
+    if (last < q0) return;
+    const int e = sp.end(last), f = sp.first(q0);
+    if (e <= f) return;
+    lo = f / kTile;
+    hi = (e + kTile - 1) / kTile;
+}
+// Those of a unit's tiles together.
+__device__ __forceinline__ void blocks_of_unit(const AttnParams &p, const Span &sp, int unit, int &lo, int &hi) {
+    blocks_of(p, sp, Rows(p, unit * p.per).q0, lo, hi);
+    if (p.per == 2 && 2 * unit + 1 < p.ntiles) {
+        int a, z;
+        blocks_of(p, sp, Rows(p, 2 * unit + 1).q0, a, z);
+        if (z > a) {
+            lo = hi > lo ? min(lo, a) : a;
+            hi = max(hi, z);
+        }
+    }
+}
+__device__ __forceinline__ Span span_of(const AttnParams &p, int seq) {
+    return Span{clamp_length(p.q_lengths, seq, p.nq), clamp_length(p.k_lengths, seq, p.width * p.page), p.causal,
+                p.window};
+}
+__device__ __forceinline__ int run_begin(int total, int cta, int ctas) { return (int)((int64_t)total * cta / ctas); }
+__device__ __forceinline__ int runs(int total, int ctas) { return min(ctas, max(1, total / kMinRun)); }
+
+// first[s] for all sequences, by a whole CTA (between two of its barriers: it has one).
+__device__ __forceinline__ void fill_first(const AttnParams &p, int *first, int tid, int threads) {
+    for (int s = tid; s < p.b; s += threads) {
+        const Span sp = span_of(p, s);
+        int sum = 0;
+        for (int u = 0; u < p.units; ++u) {
+            int lo, hi;
+            blocks_of_unit(p, sp, u, lo, hi);
+            sum += (hi - lo) * p.hk;
+        }
+        first[s + 1] = sum;
+    }
+    __syncthreads();
+    if (tid < 32) {
+        constexpr int kEach = kMaxSeqs / 32;
+        const int s0 = tid * kEach, s1 = min(s0 + kEach, p.b);
+        int sum = 0;
+        for (int s = s0; s < s1; ++s) sum += first[s + 1];
+        int run = sum;
+        for (int o = 1; o < 32; o *= 2) {
+            const int x = __shfl_up_sync(0xffffffffu, run, o);
+            if (tid >= o) run += x;
+        }
+        run -= sum;
+        for (int s = s0; s < s1; ++s) first[s + 1] = run += first[s + 1];
+        if (tid == 0) first[0] = 0;
+    }
+}
+
+// A CTA's part of the list, unit by unit: sequence-major, then unit, then key/value head.
+struct Item {
+    int seq, unit, kvh, lo, hi;  // blocks [lo, hi) of it
+    Span sp;
+    int slot;  // where its partial result goes; -1: the unit is whole
+};
+struct Walk {
+    int at, end;
+    int seq, unit, kvh, blk, lo, hi, slot;
+    Span sp;
+    __device__ __forceinline__ Walk(const AttnParams &p, const int *first, int cta) {
+        const int total = first[p.b], n = runs(total, p.ctas);
+        at = end = 0;
+        if (cta >= n) return;
+        at = run_begin(total, cta, n);
+        end = run_begin(total, cta + 1, n);
+        if (at >= end) return;
+        int a = 0, z = p.b;  // first[a] <= at < first[z]
+        while (z - a > 1) {
+            const int m = (a + z) / 2;
+            if (first[m] <= at) a = m;
+            else z = m;
+        }
+        seq = a;
+        sp = span_of(p, seq);
+        int off = at - first[seq];
+        for (unit = 0;; ++unit) {
+            blocks_of_unit(p, sp, unit, lo, hi);
+            const int c = (hi - lo) * p.hk;
+            if (off < c) break;
+            off -= c;
+        }
+        kvh = off / (hi - lo);
+        blk = off - kvh * (hi - lo);
+        slot = 2 * cta;
+    }
+    // The next item, while there is one.
+    __device__ __forceinline__ bool next(const AttnParams &p, Item &it) {
+        if (at >= end) return false;
+        const int n = min(hi - lo - blk, end - at);
+        it.seq = seq;
+        it.unit = unit;
+        it.kvh = kvh;
+        it.lo = lo + blk;
+        it.hi = it.lo + n;
+        it.sp = sp;
+        it.slot = blk == 0 && it.hi == hi ? -1 : blk ? slot : slot + 1;
+        at += n;
+        blk = 0;
+        if (at < end && ++kvh == p.hk) {
+            kvh = 0;
+            do {
+                if (++unit == p.units) {
+                    unit = 0;
+                    ++seq;
+                    sp = span_of(p, seq);
+                }
+                blocks_of_unit(p, sp, unit, lo, hi);
+            } while (hi <= lo);
+        }
+        return true;
+    }
+};
+
+// Units without blocks, a share a CTA, by `warps` warps: O = 0, lse = -inf.
+__device__ __forceinline__ void write_empty(const AttnParams &p, int warp, int warps, int lane) {
+    const int all = p.b * p.units * p.hk;
+    for (int u = blockIdx.x; u < all; u += gridDim.x) {
+        const int kvh = u % p.hk, unit = u / p.hk % p.units, seq = u / p.hk / p.units;
+        int lo, hi;
+        blocks_of_unit(p, span_of(p, seq), unit, lo, hi);
+        if (hi > lo) continue;
+        for (int t = unit * p.per; t < min(p.ntiles, (unit + 1) * p.per); ++t) {
+            const Rows r(p, t);
+            for (int x = warp; x < p.qbox * p.hbox; x += warps) {
+                const int i = r.q0 + (x & (p.qbox - 1)), hg = r.h0 + x / p.qbox;
+                if (hg >= p.group || i >= p.nq) continue;
+                const int64_t h = (int64_t)kvh * p.group + hg;
+                if (8 * lane < p.d)
+                    *reinterpret_cast<uint4 *>(p.out + seq * p.so.b + h * p.so.h + (int64_t)i * p.so.n + 8 * lane) =
+                        make_uint4(0u, 0u, 0u, 0u);
+                if (lane == 0) p.lse[(seq * (int64_t)p.hq + h) * p.nq + i] = -INFINITY;
+            }
+        }
+    }
+}
+
+// The page of rows `row` on of key block j of a sequence; p.pages, which lies outside the tensor map
+// and comes as zeros, where there is none.
+__device__ __forceinline__ int page_of(const AttnParams &p, const int32_t *table, int j, int row, int Lk) {
+    const int at = j * kTile + row;
+    if (at >= Lk) return p.pages;
+    const int x = __ldg(table + (at >> p.shift));
+    if ((unsigned)x < (unsigned)p.pages) return x;
+    if (p.status) atomicExch(p.status, kBadPage);
+    return p.pages;
+}
+
+// Host side (paged_attn.cu).
+struct Maps {
+    CUtensorMap q, k, v;
+};
+bool encode_maps(const AttnCall &c, const AttnParams &p, Maps &m);
+// Workspace of a launch of rows of `dp` elements (p.N, p.per, p.ctas set): *ws to be freed.
+int take_workspace(AttnParams &p, int dp, void **ws, cudaStream_t s);
+int launch_join(const AttnParams &p, int dp, cudaStream_t s);
+
+// Tiles of 128 rows in pairs (paged_attn_wide.cu).
+int launch_wide(const AttnCall &c, AttnParams &p);
+
+}  // namespace paged
+}  // namespace linformer

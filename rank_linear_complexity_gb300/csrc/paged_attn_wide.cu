@@ -1,0 +1,539 @@
+// Attention over pages where a key/value head's new tokens fill more than 64 rows: trees and chunks
+// of prompts.  The products are those of softmax_attn_fwd.cu, queries as the 128 rows of a product
+// and a thread a row, two tiles of rows to a unit of work, which share the key blocks in shared
+// memory; blocks come page by page, and CTAs take equal runs of the list of blocks (paged_attn.cuh).
+//   warps 0-3, 4-7  softmax of tile 0 and tile 1: S out of tensor memory, P back
+//   warp 8          loads: looks the pages up and issues a box a lane
+//   warps 9, 10     one thread each issues a tile's S = Q.K^T and O += P.V
+//   warp 11         goes through the CTA's run and tells the others each item; rows without keys
+#include <cmath>
+
+#include "paged_attn.cuh"
+#include "softmax_rows.cuh"
+
+namespace linformer {
+namespace paged {
+namespace {
+
+// Twelve warps, 168 registers each at launch; the two warpgroups that do the arithmetic take registers
+// from the third.
+constexpr int kThreads = 384, kLoadWarp = 8, kMmaWarp = 9, kPlanWarp = 11;
+constexpr uint32_t kLaunchRegs = 168, kMathRegs = 208, kIssueRegs = 88;
+static_assert(2 * kMathRegs + kIssueRegs == 3 * kLaunchRegs, "register split");
+
+// Tensor memory as in softmax_attn_fwd.cu: S of the next block beside P up to 64 elements, P over S
+// up to 128.
+template <int DP>
+struct Layout {
+    static constexpr bool kSep = DP == 64;
+    static constexpr int kStages = DP == 64 ? 8 : 4;
+    static constexpr uint32_t kTileBytes = kTile * DP * 2;
+    static constexpr uint32_t kP = kSep ? 256 : 0, kPStep = kSep ? 64 : 128, kO = kSep ? 384 : 256;
+    static constexpr uint32_t kEnd = (2 + kStages) * kTileBytes;
+};
+
+constexpr int kAhead = 4;            // items told ahead
+constexpr int kReaders = 1 + 2 + 8;  // load warp, issuing threads, softmax warps
+
+struct Shared {
+    uint64_t full[8], empty[8], q_full[2], q_free[2], s_full[2], s_free[2], p_full[2], p_half[2], pv_done[2],
+        o_free[2], drain[2], told[kAhead], taken[kAhead];
+    Item items[kAhead];  // (in shared memory: the softmax has no registers to spare for a walk)
+    uint32_t tmem;
+    int abort;
+    int pages[kTile / 8];
+    int first[kMaxSeqs + 1];
+};
+
+// A tile's part of an item.
+struct Part {
+    int q0, h0, lo, hi;
+    bool live;
+    __device__ __forceinline__ Part(const AttnParams &p, const Item &it, int t) {
+        const int tile = 2 * it.unit + t;
+        live = tile < p.ntiles;
+        const Rows r(p, tile);
+        q0 = r.q0;
+        h0 = r.h0;
+        lo = hi = 0;
+        if (live) blocks_of(p, it.sp, q0, lo, hi);
+        lo = max(lo, it.lo);
+        hi = max(lo, min(hi, it.hi));
+    }
+};
+
+// The scores of a block whose nodes a row's mask hides become -inf in tensor memory; node: of the
+// block's first column (below 0: rows before the tree, which it sees).
+__device__ __noinline__ void mask_nodes(uint32_t t, int node, const uint64_t *mask, int words) {
+    auto word = [&](int w) { return w < 0 ? ~0ull : w < words ? __ldg(mask + w) : 0ull; };
+#pragma unroll 1
+    for (int c = 0; c < kTile; c += 32) {
+        const int w = (node + c) >> 6, off = (node + c) & 63;
+        const uint64_t low = mask ? word(w) >> off : 0, high = mask && off ? word(w + 1) << (64 - off) : 0;
+        const uint32_t see = (uint32_t)(low | high);
+        uint32_t v[32];
+        tmem_ld32(t + c, v);
+#pragma unroll
+        for (int e = 0; e < 32; ++e)
+            if (!(see >> e & 1)) v[e] = 0xff800000u;
+        tmem_st32(t + c, v);
+    }
+}
+
+template <int DP>
+__global__ void __launch_bounds__(kThreads, 1)
+paged_wide_kernel(const __grid_constant__ CUtensorMap tQ, const __grid_constant__ CUtensorMap tK,
+                  const __grid_constant__ CUtensorMap tV, const __grid_constant__ AttnParams p) {
+    using L = Layout<DP>;
+    extern __shared__ uint8_t raw[];
+    uint8_t *smem = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(raw) + 1023) & ~uintptr_t(1023));
+    uint8_t *sQ = smem, *sKV = smem + 2 * L::kTileBytes;
+    Shared *sh = reinterpret_cast<Shared *>(smem + L::kEnd);
+    volatile int *abort_flag = &sh->abort;
+    const int tid = threadIdx.x, warp = __shfl_sync(0xffffffffu, tid >> 5, 0), lane = tid & 31;
+
+    if (tid == 0) {
+        for (int t = 0; t < 2; ++t) {
+            mbar_init(&sh->q_full[t], 1);
+            mbar_init(&sh->q_free[t], 1);
+            mbar_init(&sh->s_full[t], 1);
+            mbar_init(&sh->s_free[t], 4);
+            mbar_init(&sh->p_full[t], 4);
+            mbar_init(&sh->p_half[t], 4);
+            mbar_init(&sh->pv_done[t], 1);
+            mbar_init(&sh->o_free[t], 4);
+            mbar_init(&sh->drain[t], 1);
+        }
+        for (int s = 0; s < L::kStages; ++s) {
+            mbar_init(&sh->full[s], 1);
+            mbar_init(&sh->empty[s], 2);  // one arrival from each tile's products
+        }
+        for (int s = 0; s < kAhead; ++s) {
+            mbar_init(&sh->told[s], 1);
+            mbar_init(&sh->taken[s], kReaders);
+        }
+        sh->abort = 0;
+        fence_mbar_init();
+        prefetch_tmap(&tQ);
+        prefetch_tmap(&tK);
+        prefetch_tmap(&tV);
+        launch_dependents();  // the join, which waits for this grid's end
+    }
+    if (warp == kMmaWarp) {
+        tmem_alloc(&sh->tmem, 512);
+        tmem_relinquish();
+    }
+    tc_fence_before();
+    fill_first(p, sh->first, tid, kThreads);
+    __syncthreads();
+    tc_fence_after();
+    if (blockIdx.x == 0)
+        for (int s = tid; s <= p.b; s += kThreads) p.first[s] = sh->first[s];
+    const uint32_t tmem = sh->tmem;
+
+    if (warp >= kLoadWarp) {
+        setmaxnreg_dec<kIssueRegs>();
+        if (warp == kLoadWarp) {  // ---------------- loads
+            // a lane knows the page of one of a block's boxes of `box` rows, one thread issues them all
+            // (the copy's operands are the warp's: lanes with their own would take turns)
+            const bool mine = lane < p.nbox;
+            const int row = lane * p.box;
+            int ring = 0, nq[2] = {0, 0};
+            bool ok = true;
+            // (one lane waits: a function that is not inlined may not be called from warps of both register
+            // budgets, and the softmax calls the warps' wait)
+            auto spin = [&](uint64_t *bar, uint32_t parity, int code) {
+                const bool done = lane != 0 || thread_spin(bar, parity, p.status, code, abort_flag);
+                return __shfl_sync(0xffffffffu, (int)done, 0) != 0;
+            };
+            for (int k = 0; ok; ++k) {
+                if (!spin(&sh->told[k % kAhead], (k / kAhead) & 1, 153)) break;
+                const Item &it = sh->items[k % kAhead];
+                if (it.seq < 0) break;
+                for (int t = 0; t < 2 && ok; ++t) {
+                    const Part x(p, it, t);
+                    if (x.hi <= x.lo) continue;
+                    ok = nq[t] == 0 || spin(&sh->q_free[t], (nq[t] - 1) & 1, 140);
+                    if (!ok) break;
+                    if (lane == 0) {
+                        mbar_arrive_expect_tx(&sh->q_full[t], (uint32_t)(p.qbox * p.hbox * DP * 2));
+                        for (int h = 0; h < DP / 64; ++h)
+                            tma_load_5d(sQ + t * L::kTileBytes + h * 16384, &tQ, &sh->q_full[t], h * 64, x.q0, x.h0,
+                                        it.kvh, it.seq);
+                    }
+                    ++nq[t];
+                }
+                const int32_t *table = p.table + (int64_t)it.seq * p.width;
+                const int lo = it.lo, hi = it.hi, kvh = it.kvh, Lk = it.sp.Lk;
+                __syncwarp();
+                if (lane == 0) mbar_arrive(&sh->taken[k % kAhead]);
+                int page = mine ? page_of(p, table, lo, row, Lk) : 0;
+                for (int j = lo; j < hi && ok; ++j) {
+                    const int now = page, at = (j * kTile) & (p.page - 1);  // (0 where a block has several pages)
+                    if (j + 1 < hi && mine) page = page_of(p, table, j + 1, row, Lk);
+                    if (mine) sh->pages[lane] = now;
+                    __syncwarp();
+                    if (lane == 0) {
+                        for (int kv = 0; kv < 2 && ok; ++kv, ++ring) {
+                            const int s = ring % L::kStages;
+                            if (ring >= L::kStages &&
+                                !thread_spin(&sh->empty[s], (ring / L::kStages - 1) & 1, p.status, 141, abort_flag)) {
+                                ok = false;
+                                break;
+                            }
+                            mbar_arrive_expect_tx(&sh->full[s], L::kTileBytes);
+                            uint8_t *dst = sKV + s * L::kTileBytes;
+                            for (int x = 0; x < p.nbox; ++x, dst += p.box * 128)
+#pragma unroll
+                                for (int h = 0; h < DP / 64; ++h)
+                                    tma_load_5d(dst + h * 16384, kv ? &tV : &tK, &sh->full[s], h * 64, at, 0, kvh,
+                                                sh->pages[x]);
+                        }
+                    }
+                    ok = __shfl_sync(0xffffffffu, ok, 0);
+                }
+            }
+            // no copy outlives the CTA
+            if (lane == 0) {
+                for (int t = 0; t < 2; ++t)
+                    if (nq[t] > 0) mbar_wait_drain(&sh->q_full[t], (nq[t] - 1) & 1);
+                for (int i = max(0, ring - L::kStages); i < ring; ++i)
+                    mbar_wait_drain(&sh->full[i % L::kStages], (i / L::kStages) & 1);
+            }
+            __syncwarp();
+        } else if (warp == kPlanWarp) {
+            if (elect_one()) {
+                Walk walk(p, sh->first, blockIdx.x);
+                Item it;
+                for (int k = 0;; ++k) {
+                    const int s = k % kAhead;
+                    const bool more = walk.next(p, it);
+                    if (!more) it.seq = -1;
+                    if (k >= kAhead && !thread_spin(&sh->taken[s], (k / kAhead - 1) & 1, p.status, 156, abort_flag)) break;
+                    sh->items[s] = it;
+                    mbar_arrive(&sh->told[s]);
+                    if (!more) break;
+                }
+            }
+            __syncwarp();
+            write_empty(p, 0, 1, lane);
+        } else if (elect_one()) {  // ---------------- products of tile t
+            const int t = warp - kMmaWarp;
+            const uint32_t idesc_s = idesc_f16(128, 128, 1, 0, 0), idesc_o = idesc_f16(128, DP, 1, 0, 1);
+            const uint64_t dq = sdesc(smem_u32(sQ + t * L::kTileBytes), 16, 1024, kSwizzle128B);
+            const uint32_t tS = tmem + 128 * t, tP = tmem + L::kP + L::kPStep * t, tO = tmem + L::kO + DP * t;
+            // the next K and the next V of the ring, whose entries come in pairs
+            constexpr int kPairs = L::kStages / 2;
+            struct At {
+                int s = 0;
+                uint32_t parity = 0;
+                __device__ __forceinline__ void next() {
+                    if (++s == kPairs) {
+                        s = 0;
+                        parity ^= 1u;
+                    }
+                }
+            } ak, av;
+            const uint64_t dk0 = sdesc(smem_u32(sKV), 16, 1024, kSwizzle128B),
+                           dv0 = sdesc(smem_u32(sKV) + L::kTileBytes, 16384, 1024, kSwizzle128B);
+            int n = 0, ns = 0, items = 0;  // the tile's blocks with O, with S, and its items
+            bool ok = true;
+            for (int k = 0; ok; ++k) {
+                const int slot = k % kAhead;
+                if (!thread_spin(&sh->told[slot], (k / kAhead) & 1, p.status, 154, abort_flag)) break;
+                const Item it = sh->items[slot];
+                mbar_arrive(&sh->taken[slot]);
+                if (it.seq < 0) break;
+                const Part x(p, it, t);
+                const int lo = x.lo, hi = x.hi;
+                // S of block j: once the last S has been read and, with P over S, its product is done
+                auto score = [&](int j) {
+                    uint64_t *full = &sh->full[2 * ak.s], *empty = &sh->empty[2 * ak.s];
+                    if (!thread_spin(full, ak.parity, p.status, 142, abort_flag)) return false;
+                    const uint64_t k = dk0 + (uint64_t)(ak.s * (int)(2 * L::kTileBytes >> 4));
+                    ak.next();
+                    if (j < lo || j >= hi) {
+                        mbar_arrive(empty);
+                        return true;
+                    }
+                    if (j == lo && !thread_spin(&sh->q_full[t], items & 1, p.status, 143, abort_flag)) return false;
+                    if (ns > 0 && !thread_spin(L::kSep ? &sh->s_free[t] : &sh->pv_done[t], (ns - 1) & 1, p.status, 144,
+                                               abort_flag))
+                        return false;
+                    ++ns;
+                    tc_fence_after();
+#pragma unroll
+                    for (int y = 0; y < DP / 16; ++y) {
+                        const uint64_t off = (uint64_t)((y >> 2) * 1024 + (y & 3) * 2);
+                        mma_ss(tS, dq + off, k + off, idesc_s, y > 0 ? 1u : 0u);
+                    }
+                    mma_commit(&sh->s_full[t]);
+                    mma_commit(empty);
+                    if (j == hi - 1) mma_commit(&sh->q_free[t]);
+                    return true;
+                };
+                // O += P.V of block j
+                auto output = [&](int j) {
+                    uint64_t *full = &sh->full[2 * av.s + 1], *empty = &sh->empty[2 * av.s + 1];
+                    if (!thread_spin(full, av.parity, p.status, 145, abort_flag)) return false;
+                    const uint64_t v = dv0 + (uint64_t)(av.s * (int)(2 * L::kTileBytes >> 4));
+                    av.next();
+                    if (j < lo || j >= hi) {
+                        mbar_arrive(empty);
+                        return true;
+                    }
+                    // P over S comes in halves of 64 keys: the first half's products run while the
+                    // other is in its exponentials
+                    if (!thread_spin(L::kSep ? &sh->p_full[t] : &sh->p_half[t], n & 1, p.status, 146, abort_flag))
+                        return false;
+                    if (j == lo && items > 0 && !thread_spin(&sh->o_free[t], (items - 1) & 1, p.status, 147, abort_flag))
+                        return false;
+                    tc_fence_after();
+#pragma unroll
+                    for (int y = 0; y < 4; ++y)
+                        mma_ts(tO, tP + 8 * y, v + (uint64_t)(128 * y), idesc_o, (j > lo || y > 0) ? 1u : 0u);
+                    if (!L::kSep) {
+                        if (!thread_spin(&sh->p_full[t], n & 1, p.status, 148, abort_flag)) return false;
+                        tc_fence_after();
+                    }
+                    ++n;
+#pragma unroll
+                    for (int y = 4; y < 8; ++y) mma_ts(tO, tP + 8 * y, v + (uint64_t)(128 * y), idesc_o, 1u);
+                    mma_commit(&sh->pv_done[t]);
+                    mma_commit(empty);
+                    return true;
+                };
+                // P beside S: S(j + 1) before O(j); P over S: after it
+                if (L::kSep) ok = score(it.lo);
+                for (int j = it.lo; j < it.hi && ok; ++j) {
+                    if (L::kSep) ok = (j + 1 >= it.hi || score(j + 1)) && output(j);
+                    else ok = score(j) && output(j);
+                }
+                if (hi > lo) ++items;
+            }
+            mma_commit(&sh->drain[t]);
+            mbar_wait_drain(&sh->drain[t], 0);
+        }
+        __syncwarp();
+    } else {
+        setmaxnreg_inc<kMathRegs>();  // ---------------- softmax of one tile, one thread a row
+        const int t = warp >> 2, row = tid & 127;
+        const uint32_t lanes = (uint32_t)((warp & 3) * 32) << 16;
+        const uint32_t tS = tmem + 128 * t + lanes, tP = tmem + L::kP + L::kPStep * t + lanes,
+                       tO = tmem + L::kO + DP * t + lanes;
+        const float sl = p.scale_log2;
+        const int qi = row & (p.qbox - 1), head = row / p.qbox;  // position and head within the tile
+        int n = 0, before = 0;  // the tile's blocks, and those of the items before this one
+        bool ok = true;
+        // P.V of the tile's block before this one is done: P may be written over, O rescaled
+        auto last_product = [&](bool any) {
+            if (any) {
+                ok = warp_spin(&sh->pv_done[t], (n - 1) & 1, p.status, 149, abort_flag);
+                tc_fence_after();
+            }
+            return ok;
+        };
+        for (int k = 0;; ++k) {
+            if (!warp_spin(&sh->told[k % kAhead], (k / kAhead) & 1, p.status, 155, abort_flag)) break;
+            const Item &it = sh->items[k % kAhead];
+            if (it.seq < 0) break;
+            int xlo, xhi, first, end, node0;
+            bool valid, warp_valid;
+            const int base = before - it.lo, Lk = it.sp.Lk;
+            before += it.hi - it.lo;
+            {
+                const Part x(p, it, t);
+                const int i = x.q0 + qi;
+                xlo = x.lo;
+                xhi = x.hi;
+                valid = x.live && head < p.hbox && x.h0 + head < p.group && i < it.sp.Lq;
+                warp_valid = __any_sync(0xffffffffu, valid);
+                first = valid ? it.sp.first(i) : 0;
+                end = valid ? it.sp.end(i) : (1 << 30);
+                node0 = p.mask ? Lk - it.sp.Lq : 1 << 30;  // where the tree begins
+            }
+            float m = -INFINITY, l = 0.f;  // reference (of the raw scores), sum of 2^((s - m) sl)
+            for (int j = xlo; j < xhi; ++j, ++n) {
+                if (!warp_spin(&sh->s_full[t], n & 1, p.status, 150, abort_flag)) {
+                    ok = false;
+                    break;
+                }
+                tc_fence_after();
+                const int k0 = j * kTile;
+                if (k0 + kTile > Lk) {
+                    // rows of V past the length may hold anything: P is 0 there, but 0 x NaN is not
+                    // (both tiles' threads write the zeros; a product that reads them by then needs
+                    // no others)
+                    const int v = 2 * (base + j) + 1, s = v % L::kStages;
+                    if (!warp_spin(&sh->full[s], (v / L::kStages) & 1, p.status, 151, abort_flag)) {
+                        ok = false;
+                        break;
+                    }
+                    if (k0 + row >= Lk) {
+                        uint8_t *at = sKV + s * L::kTileBytes + row * 128;
+#pragma unroll 1
+                        for (int y = 0; y < DP / 8; ++y)
+                            *reinterpret_cast<uint4 *>(at + (y / 8) * 16384 + (y % 8) * 16) = make_uint4(0u, 0u, 0u, 0u);
+                    }
+                    fence_proxy_async_smem();
+                }
+                if (!warp_valid) {  // only takes part in the barriers
+                    __syncwarp();
+                    if (L::kSep && lane == 0) mbar_arrive(&sh->s_free[t]);
+                    // no second arrival on p_full before the other warps' first
+                    if (L::kSep && !last_product(j > xlo)) break;
+                    __syncwarp();
+                    if (!L::kSep && lane == 0) mbar_arrive(&sh->p_half[t]);
+                    if (lane == 0) mbar_arrive(&sh->p_full[t]);
+                    continue;
+                }
+                // Masked keys (whatever they hold) become -inf in place, out of line: the few blocks at
+                // a mask's edge must not widen the code of the others.
+                if (__any_sync(0xffffffffu, first > k0 || end < k0 + kTile))
+                    sattn::mask_block(tS, first - k0, first < end ? end - first : 0);
+                if (k0 + kTile > node0) {
+                    const int64_t r = (int64_t)it.seq * p.nq + Part(p, it, t).q0 + qi;
+                    mask_nodes(tS, k0 - node0, valid ? p.mask + r * p.words : nullptr, p.words);
+                }
+                uint32_t v[4][32];
+#pragma unroll
+                for (int c = 0; c < 4; ++c) tmem_ld32_async(tS + 32 * c, v[c]);
+                tmem_wait_ld(v[0]);
+                tie32(v[1]);
+                tie32(v[2]);
+                tie32(v[3]);
+                if (L::kSep) {
+                    tc_fence_before();
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive(&sh->s_free[t]);
+                }
+                const float mx = fmaxf(fmaxf(sattn::max_chunk(v[0]), sattn::max_chunk(v[1])),
+                                       fmaxf(sattn::max_chunk(v[2]), sattn::max_chunk(v[3])));
+                if (__any_sync(0xffffffffu, valid && (mx - m) * sl > kOutgrown)) {
+                    if (!last_product(j > xlo)) break;
+                    const float mn = fmaxf(m, mx);
+                    const float f = mn == -INFINITY ? 1.f : ex2_approx((m - mn) * sl);
+                    l *= f;
+                    m = mn;
+                    if (j > xlo) sattn::rescale_output(tO, DP, f);
+                }
+                const float off = m == -INFINITY ? 0.f : -m * sl;
+                float2 sum0 = make_float2(0.f, 0.f), sum1 = sum0;
+                if (L::kSep) {
+                    // P beside S is written at the end: until then the last block's is in use
+                    uint32_t o[4][16];
+#pragma unroll
+                    for (int c = 0; c < 4; ++c) sattn::exp_chunk(v[c], o[c], sl, off, sum0, sum1);
+                    if (!last_product(j > xlo)) break;
+#pragma unroll
+                    for (int c = 0; c < 4; ++c) tmem_st16_async(tP + 16 * c, o[c]);
+                } else {
+#pragma unroll
+                    for (int c = 0; c < 4; ++c) {
+                        uint32_t o[16];
+                        sattn::exp_chunk(v[c], o, sl, off, sum0, sum1);
+                        tmem_st16_async(tP + 16 * c, o);
+                        if (c == 1) {
+                            tmem_wait_st();
+                            tc_fence_before();
+                            __syncwarp();
+                            if (lane == 0) mbar_arrive(&sh->p_half[t]);
+                        }
+                    }
+                }
+                tmem_wait_st();
+                tc_fence_before();
+                __syncwarp();
+                if (lane == 0) mbar_arrive(&sh->p_full[t]);
+                l += (sum0.x + sum0.y) + (sum1.x + sum1.y);
+            }
+            if (!ok) break;
+            // O / l out of tensor memory; rows without keys give O = 0 and lse = -inf
+            const bool dead = !valid || l == 0.f, some = xhi > xlo, whole = it.slot < 0;
+            const float inv = dead ? 0.f : 1.f / l;
+            const Part x(p, it, t);
+            const int i = x.q0 + qi, hg = x.h0 + head;
+            const bool exists = x.live && head < p.hbox && hg < p.group && i < p.nq;
+            const int64_t h = (int64_t)it.kvh * p.group + hg, pr = ((int64_t)it.slot * 2 + t) * kTile + row;
+            __nv_bfloat16 *dst = p.out + it.seq * p.so.b + h * p.so.h + (int64_t)i * p.so.n;
+            if (some) {
+                if (!warp_spin(&sh->pv_done[t], (n - 1) & 1, p.status, 152, abort_flag)) break;
+                tc_fence_after();
+#pragma unroll 1
+                for (int c = 0; c < DP && warp_valid; c += 32) {
+                    uint32_t o[32];
+                    tmem_ld32(tO + c, o);
+#pragma unroll
+                    for (int e = 0; e < 32; ++e) o[e] = __float_as_uint(dead ? 0.f : __uint_as_float(o[e]) * inv);
+                    if (!whole) {
+                        if (dead) continue;
+#pragma unroll
+                        for (int e = 0; e < 32; e += 4)
+                            *reinterpret_cast<uint4 *>(p.part_o + pr * DP + c + e) =
+                                make_uint4(o[e], o[e + 1], o[e + 2], o[e + 3]);
+                    } else if (exists) {
+#pragma unroll
+                        for (int e = 0; e < 32; e += 16) {
+                            if (c + e >= p.d) continue;
+                            uint32_t w[8];
+#pragma unroll
+                            for (int y = 0; y < 8; ++y)
+                                w[y] = pack2(__uint_as_float(o[e + 2 * y]), __uint_as_float(o[e + 2 * y + 1]));
+                            if (p.wide_stores) {
+                                sattn::store32(dst + c + e, w);
+                            } else {
+                                *reinterpret_cast<uint4 *>(dst + c + e) = make_uint4(w[0], w[1], w[2], w[3]);
+                                if (c + e + 8 < p.d)
+                                    *reinterpret_cast<uint4 *>(dst + c + e + 8) = make_uint4(w[4], w[5], w[6], w[7]);
+                            }
+                        }
+                    }
+                }
+                tc_fence_before();
+                __syncwarp();
+                if (lane == 0) mbar_arrive(&sh->o_free[t]);
+            }
+            if (whole && exists && !(some && warp_valid))
+#pragma unroll 1
+                for (int c = 0; c < p.d; c += 8) *reinterpret_cast<uint4 *>(dst + c) = make_uint4(0u, 0u, 0u, 0u);
+            const float lse = dead ? -INFINITY : m * p.scale + logf(l);
+            if (!whole) p.part_lse[pr] = lse;
+            else if (exists) p.lse[((int64_t)it.seq * p.hq + h) * p.nq + i] = lse;
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&sh->taken[k % kAhead]);
+        }
+    }
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    if (warp == kMmaWarp) tmem_dealloc(tmem, 512);
+}
+
+template <int DP>
+int launch(const AttnCall &c, AttnParams &p) {
+    constexpr uint32_t kSmem = 1024 + Layout<DP>::kEnd + sizeof(Shared);
+    static_assert(kSmem <= 227 * 1024, "shared memory");
+    Maps m;
+    if (!encode_maps(c, p, m)) return LINFORMER_ERR_LAUNCH;
+    p.N = kTile;
+    void *ws = nullptr;
+    int st = take_workspace(p, DP, &ws, c.stream);
+    if (st) return st;
+    const auto kernel = paged_wide_kernel<DP>;
+    st = sattn::allow_smem(reinterpret_cast<const void *>(kernel), kSmem, DP == 64 ? 18 : 19);
+    if (!st) {
+        KernelScope scope(LINFORMER_KERNEL_PAGED, c.stream);
+        kernel<<<p.ctas, kThreads, kSmem, c.stream>>>(m.q, m.k, m.v, p);
+        if (cudaGetLastError() != cudaSuccess) st = LINFORMER_ERR_LAUNCH;
+    }
+    if (!st) st = launch_join(p, DP, c.stream);
+    workspace_free(ws, c.stream);
+    return st;
+}
+
+}  // namespace
+
+int launch_wide(const AttnCall &c, AttnParams &p) { return c.d <= 64 ? launch<64>(c, p) : launch<128>(c, p); }
+
+}  // namespace paged
+}  // namespace linformer
