@@ -171,8 +171,6 @@ paged_attn_kernel(const __grid_constant__ CUtensorMap tQ, const __grid_constant_
     fill_first(p, sh->first, tid, kThreads);
     __syncthreads();
     tc_fence_after();
-    if (blockIdx.x == 0)
-        for (int s = tid; s <= p.b; s += kThreads) p.first[s] = sh->first[s];
     const uint32_t tmem = sh->tmem;
     Walk walk(p, sh->first, blockIdx.x);
     Item it;
@@ -279,6 +277,8 @@ paged_attn_kernel(const __grid_constant__ CUtensorMap tQ, const __grid_constant_
         }
         __syncwarp();
     } else if (warp >= kEmptyWarp) {  // ---------------- rows without keys
+        if (warp == kEmptyWarp && lane == 0) write_cut(p, walk, sh->first[p.b]);
+        __syncwarp();
         write_empty(p, warp - kEmptyWarp, kThreads / 32 - kEmptyWarp, lane);
     } else {  // ---------------- softmax: one key a thread, C of the rows
         const int w = warp >> 2, key0 = tid & 127, c0 = w * C;
@@ -446,65 +446,78 @@ paged_attn_kernel(const __grid_constant__ CUtensorMap tQ, const __grid_constant_
 }
 
 // Joins the parts of the rows whose run of blocks was cut: lse = log sum_s exp(lse_s), O = sum_s
-// exp(lse_s - lse) O_s.  blockIdx.x: the CTA that did the last part (any other's blocks leave at
-// once); a warp a row.
+// exp(lse_s - lse) O_s, in the parts' order.  blockIdx.x: the CTA that did the last part (any other's
+// blocks leave at once).  kEach warps a row: more than one where units are few and their parts many
+// (4 units of 1024 blocks, 38 parts each: 20 us with one warp, 8 with four).
 constexpr int kJoinWarps = 4;
-template <int DP>
+template <int DP, int kEach>
 __global__ void __launch_bounds__(kJoinWarps * 32) join_kernel(const __grid_constant__ AttnParams p) {
+    constexpr int E = DP / 32;
+    __shared__ float shared[kEach > 1 ? kJoinWarps : 1][E + 1][32];
     wait_prerequisites();
-    const int rows = p.qbox * p.hbox, lane = threadIdx.x & 31;
-    int x = blockIdx.y * kJoinWarps + (threadIdx.x >> 5);
+    const int rows = p.qbox * p.hbox, lane = threadIdx.x & 31, warp = threadIdx.x >> 5, mine = warp % kEach;
+    int x = blockIdx.y * (kJoinWarps / kEach) + warp / kEach;
     const int t = x / rows;
     x -= t * rows;
-    const Walk at(p, p.first, blockIdx.x);
-    if (at.at >= at.end || at.blk == 0 || at.end - at.at < at.hi - at.lo - at.blk) return;
-    const int tile = at.unit * p.per + t;
+    const int4 cut = p.cuts[blockIdx.x];
+    if (cut.x < 0) return;
+    const int seq = cut.x, kvh = cut.z, c0 = cut.w, c1 = blockIdx.x, tile = cut.y * p.per + t;
     if (t >= p.per || tile >= p.ntiles) return;
     const Rows r(p, tile);
     const int i = r.q0 + (x & (p.qbox - 1)), hg = r.h0 + x / p.qbox;
-    if (hg >= p.group || i >= p.nq) return;
-    const int total = p.first[p.b], begin = at.at - at.blk;
-    const int n = runs(total, p.ctas), c1 = blockIdx.x;
-    int c0 = c1 - 1;  // the CTA whose run holds the first block
-    while (run_begin(total, c0, n) > begin) --c0;
+    if (hg >= p.group || i >= p.nq) return;  // (all warps of a row alike)
     // a row is cut at the end of its first CTA's run, and goes on at the start of the others'
     auto slot = [&](int c) { return ((int64_t)(2 * c + (c == c0 ? 1 : 0)) * p.per + t) * p.N + x; };
     float m = -INFINITY;
     for (int c = c0 + lane; c <= c1; c += 32) m = fmaxf(m, p.part_lse[slot(c)]);
 #pragma unroll
     for (int o = 16; o; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
-    constexpr int E = DP / 32;
     float acc[E] = {}, sum = 0.f;
-    if (m != -INFINITY)
-        for (int c = c0; c <= c1; c += 32) {
-            const int some = min(32, c1 + 1 - c);
-            const float mine = lane < some ? __expf(p.part_lse[slot(c + lane)] - m) : 0.f;
+    if (m != -INFINITY) {
+        // this warp's parts
+        const int per = (c1 + 1 - c0 + kEach - 1) / kEach, first = c0 + mine * per, last = min(c1 + 1, first + per);
+        for (int c = first; c < last; c += 32) {
+            const int some = min(32, last - c);
+            const float weight = lane < some ? __expf(p.part_lse[slot(c + lane)] - m) : 0.f;
 #pragma unroll 8
             for (int k = 0; k < some; ++k) {
-                const float w = __shfl_sync(0xffffffffu, mine, k);
+                const float w = __shfl_sync(0xffffffffu, weight, k);
                 sum += w;
-                if (w == 0.f) continue;  // (a part without keys wrote no O)
                 float v[E];
+                const float *from = p.part_o + slot(c + k) * DP + lane * E;
                 if constexpr (E == 4) {
-                    const float4 t = *reinterpret_cast<const float4 *>(p.part_o + slot(c + k) * DP + lane * E);
-                    v[0] = t.x, v[1] = t.y, v[2] = t.z, v[3] = t.w;
+                    const float4 y = *reinterpret_cast<const float4 *>(from);
+                    v[0] = y.x, v[1] = y.y, v[2] = y.z, v[3] = y.w;
                 } else {
-                    const float2 t = *reinterpret_cast<const float2 *>(p.part_o + slot(c + k) * DP + lane * E);
-                    v[0] = t.x, v[1] = t.y;
+                    const float2 y = *reinterpret_cast<const float2 *>(from);
+                    v[0] = y.x, v[1] = y.y;
                 }
 #pragma unroll
-                for (int e = 0; e < E; ++e) acc[e] += w * v[e];
+                for (int e = 0; e < E; ++e) acc[e] += w == 0.f ? 0.f : w * v[e];  // (a part without keys wrote no O)
             }
         }
+    }
+    if constexpr (kEach > 1) {
+#pragma unroll
+        for (int e = 0; e < E; ++e) shared[warp][e][lane] = acc[e];
+        shared[warp][E][lane] = sum;
+        __syncthreads();
+        if (mine) return;
+        for (int o = 1; o < kEach; ++o) {
+#pragma unroll
+            for (int e = 0; e < E; ++e) acc[e] += shared[warp + o][e][lane];
+            sum += shared[warp + o][E][lane];
+        }
+    }
     const float inv = sum > 0.f ? 1.f / sum : 0.f;
-    const int64_t h = (int64_t)at.kvh * p.group + hg;
-    __nv_bfloat16 *dst = p.out + at.seq * p.so.b + h * p.so.h + (int64_t)i * p.so.n;
+    const int64_t h = (int64_t)kvh * p.group + hg;
+    __nv_bfloat16 *dst = p.out + seq * p.so.b + h * p.so.h + (int64_t)i * p.so.n;
     if (lane * E < p.d) {
 #pragma unroll
         for (int e = 0; e < E; e += 2)
             *reinterpret_cast<uint32_t *>(dst + lane * E + e) = pack2(acc[e] * inv, acc[e + 1] * inv);
     }
-    if (lane == 0) p.lse[(at.seq * (int64_t)p.hq + h) * p.nq + i] = m == -INFINITY ? -INFINITY : m + logf(sum);
+    if (lane == 0) p.lse[(seq * (int64_t)p.hq + h) * p.nq + i] = m == -INFINITY ? -INFINITY : m + logf(sum);
 }
 
 template <int DP, int N>
@@ -549,12 +562,11 @@ bool encode_maps(const AttnCall &c, const AttnParams &p, Maps &m) {
 }
 
 int take_workspace(AttnParams &p, int dp, void **ws, cudaStream_t s) {
-    constexpr size_t kHead = (kMaxSeqs + 4) * sizeof(int);
-    static_assert(kHead % 16 == 0, "parts are read 16 bytes at a time");
+    const size_t head = p.ctas * sizeof(int4);  // (parts are read 16 bytes at a time)
     const size_t parts = (size_t)2 * p.ctas * p.per * p.N;
-    if (workspace_alloc(ws, kHead + parts * (dp + 1) * sizeof(float), s) != LINFORMER_OK) return LINFORMER_ERR_ALLOC;
-    p.first = static_cast<int *>(*ws);
-    p.part_o = reinterpret_cast<float *>(static_cast<char *>(*ws) + kHead);
+    if (workspace_alloc(ws, head + parts * (dp + 1) * sizeof(float), s) != LINFORMER_OK) return LINFORMER_ERR_ALLOC;
+    p.cuts = static_cast<int4 *>(*ws);
+    p.part_o = reinterpret_cast<float *>(static_cast<char *>(*ws) + head);
     p.part_lse = p.part_o + parts * dp;
     return LINFORMER_OK;
 }
@@ -568,9 +580,14 @@ int launch_join(const AttnParams &p, int dp, cudaStream_t s) {
     cfg.stream = s;
     cfg.attrs = attr;
     cfg.numAttrs = 1;
-    cfg.gridDim = dim3((unsigned)p.ctas, (unsigned)((p.per * p.qbox * p.hbox + kJoinWarps - 1) / kJoinWarps));
+    // many parts where a unit's blocks, all units alike, would fill eight runs
+    const bool many = (int64_t)p.b * p.units * p.hk * 8 <= p.ctas;
+    const int rows = p.per * p.qbox * p.hbox, at_once = many ? 1 : kJoinWarps;
+    cfg.gridDim = dim3((unsigned)p.ctas, (unsigned)((rows + at_once - 1) / at_once));
     cfg.blockDim = dim3(kJoinWarps * 32);
-    if (cudaLaunchKernelEx(&cfg, dp == 64 ? join_kernel<64> : join_kernel<128>, p) == cudaSuccess) return LINFORMER_OK;
+    const auto kernel = dp == 64 ? (many ? join_kernel<64, kJoinWarps> : join_kernel<64, 1>)
+                                 : (many ? join_kernel<128, kJoinWarps> : join_kernel<128, 1>);
+    if (cudaLaunchKernelEx(&cfg, kernel, p) == cudaSuccess) return LINFORMER_OK;
     cudaGetLastError();
     return LINFORMER_ERR_LAUNCH;
 }

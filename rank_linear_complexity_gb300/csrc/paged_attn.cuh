@@ -28,7 +28,7 @@ struct AttnParams {
     Strides so;
     float *lse;
     float *part_o, *part_lse;  // [2 per CTA][per][N][DP], [2 per CTA][per][N]
-    int *first;                // [b + 1]: where the blocks of each sequence begin in the list
+    int4 *cuts;                // a CTA's: see join_kernel
     int words, b, hq, hk, group, nq, d, causal, window;
     // tiles of qbox positions of hbox heads (nch tiles to a group), `per` of them to a unit of work;
     // N: rows of a tile in the workspace
@@ -170,6 +170,19 @@ struct Walk {
         return true;
     }
 };
+
+// What the join has to know of a CTA, by one thread of it, from its walk's start: the unit whose last
+// part the CTA does, and the CTA that does the first; x = -1 where it ends no cut unit.
+__device__ __forceinline__ void write_cut(const AttnParams &p, const Walk &w, int total) {
+    int4 cut = make_int4(-1, 0, 0, 0);
+    if (w.at < w.end && w.blk > 0 && w.end - w.at >= w.hi - w.lo - w.blk) {
+        const int n = runs(total, p.ctas);
+        int c0 = blockIdx.x - 1;
+        while (run_begin(total, c0, n) > w.at - w.blk) --c0;
+        cut = make_int4(w.seq, w.unit, w.kvh, c0);
+    }
+    p.cuts[blockIdx.x] = cut;
+}
 
 // Units without blocks, a share a CTA, by `warps` warps: O = 0, lse = -inf.
 __device__ __forceinline__ void write_empty(const AttnParams &p, int warp, int warps, int lane) {

@@ -127,8 +127,6 @@ paged_wide_kernel(const __grid_constant__ CUtensorMap tQ, const __grid_constant_
     fill_first(p, sh->first, tid, kThreads);
     __syncthreads();
     tc_fence_after();
-    if (blockIdx.x == 0)
-        for (int s = tid; s <= p.b; s += kThreads) p.first[s] = sh->first[s];
     const uint32_t tmem = sh->tmem;
 
     if (warp >= kLoadWarp) {
@@ -204,6 +202,7 @@ paged_wide_kernel(const __grid_constant__ CUtensorMap tQ, const __grid_constant_
         } else if (warp == kPlanWarp) {
             if (elect_one()) {
                 Walk walk(p, sh->first, blockIdx.x);
+                write_cut(p, walk, sh->first[p.b]);
                 Item it;
                 for (int k = 0;; ++k) {
                     const int s = k % kAhead;
