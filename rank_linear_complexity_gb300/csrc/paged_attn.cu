@@ -59,7 +59,8 @@ struct Shared {
     alignas(16) float off[128];
     alignas(16) float f[128];
     float part[2][4][64];  // a value a column, by warp of each group
-    int first[kMaxSeqs + 1];
+    alignas(16) int64_t row[128];  // where a column's row of O begins, -1: nowhere
+    Marks marks;
 };
 
 template <int C>
@@ -137,7 +138,7 @@ paged_attn_kernel(const __grid_constant__ CUtensorMap tQ, const __grid_constant_
     volatile int *abort_flag = &sh->abort;
     const int tid = threadIdx.x, warp = __shfl_sync(0xffffffffu, tid >> 5, 0), lane = tid & 31;
 
-    if (tid == 0) {
+    if (tid == 32) {
         for (int s = 0; s < L::kEntries; ++s) {
             mbar_init(&sh->full[s], 1);
             mbar_init(&sh->empty[s], 1);
@@ -157,7 +158,6 @@ paged_attn_kernel(const __grid_constant__ CUtensorMap tQ, const __grid_constant_
         prefetch_tmap(&tQ);
         prefetch_tmap(&tK);
         prefetch_tmap(&tV);
-        launch_dependents();  // the join, which waits for this grid's end
     }
     if (warp == kMmaWarp) {
         tmem_alloc(&sh->tmem, 512);
@@ -168,11 +168,13 @@ paged_attn_kernel(const __grid_constant__ CUtensorMap tQ, const __grid_constant_
         *reinterpret_cast<uint4 *>(smem + L::kQ + x) = make_uint4(0u, 0u, 0u, 0u);
     fence_proxy_async_smem();
     tc_fence_before();
-    fill_first(p, sh->first, tid, kThreads);
+    wait_prerequisites();
+    if (tid == 0) launch_dependents();  // the join, which waits for this grid's end
+    fill(p, sh->marks, tid, kThreads);
     __syncthreads();
     tc_fence_after();
     const uint32_t tmem = sh->tmem;
-    Walk walk(p, sh->first, blockIdx.x);
+    Walk walk(p, sh->marks, blockIdx.x);
     Item it;
 
     if (warp == kLoadWarp) {  // ---------------- loads
@@ -183,8 +185,11 @@ paged_attn_kernel(const __grid_constant__ CUtensorMap tQ, const __grid_constant_
         const uint32_t dst = half * 16384u + row * 128u;
         int ring = 0, nq = 0;
         bool ok = true;
-        while (ok && walk.next(p, it)) {
+        while (ok && walk.next(p, sh->marks, it)) {
             const Rows r(p, it.unit);
+            const int32_t *table = p.table + (int64_t)it.seq * p.width;
+            auto look = [&](int j) { return mine ? page_of(p, table, j, row, it.sp.Lk) : 0; };
+            int page = look(it.lo);
             if (nq > 0 && !warp_spin(&sh->q_free, (nq - 1) & 1, p.status, 120, abort_flag)) break;
             if (lane == 0) {
                 mbar_arrive_expect_tx(&sh->q_full, (uint32_t)(p.qbox * p.hbox * DP * 2));
@@ -192,9 +197,6 @@ paged_attn_kernel(const __grid_constant__ CUtensorMap tQ, const __grid_constant_
                     tma_load_5d(smem + L::kQ + h * L::kQHalf, &tQ, &sh->q_full, h * 64, r.q0, r.h0, it.kvh, it.seq);
             }
             ++nq;
-            const int32_t *table = p.table + (int64_t)it.seq * p.width;
-            auto look = [&](int j) { return mine ? page_of(p, table, j, row, it.sp.Lk) : 0; };
-            int page = look(it.lo);
             for (int j = it.lo; j < it.hi; ++j) {
                 const int now = page, at = (j * kTile + row) & (p.page - 1);
                 if (j + 1 < it.hi) page = look(j + 1);
@@ -231,7 +233,7 @@ paged_attn_kernel(const __grid_constant__ CUtensorMap tQ, const __grid_constant_
             const uint64_t dq = sdesc(smem_u32(smem + L::kQ), 16, 1024, kSwizzle128B);
             int ns = 0, no = 0, items = 0;  // blocks whose S, whose O has been issued
             bool ok = true;
-            while (ok && walk.next(p, it)) {
+            while (ok && walk.next(p, sh->marks, it)) {
                 auto score = [&](int j) {
                     const int r = L::kPair ? ns : 2 * ns, e = r % L::kEntries, s = ns & 1;
                     if (!thread_spin(&sh->full[e], (r / L::kEntries) & 1, p.status, 122, abort_flag)) return false;
@@ -277,9 +279,9 @@ paged_attn_kernel(const __grid_constant__ CUtensorMap tQ, const __grid_constant_
         }
         __syncwarp();
     } else if (warp >= kEmptyWarp) {  // ---------------- rows without keys
-        if (warp == kEmptyWarp && lane == 0) write_cut(p, walk, sh->first[p.b]);
+        if (warp == kEmptyWarp && lane == 0) write_cut(p, walk, sh->marks.first[p.b]);
         __syncwarp();
-        write_empty(p, warp - kEmptyWarp, kThreads / 32 - kEmptyWarp, lane);
+        write_empty(p, sh->marks, warp - kEmptyWarp, kThreads / 32 - kEmptyWarp, lane);
     } else {  // ---------------- softmax: one key a thread, C of the rows
         const int w = warp >> 2, key0 = tid & 127, c0 = w * C;
         const uint32_t lanes = (uint32_t)((warp & 3) * 32) << 16;
@@ -295,10 +297,11 @@ paged_attn_kernel(const __grid_constant__ CUtensorMap tQ, const __grid_constant_
         };
         // The group's warps leave together: what a wait of one came to is ANDed at a barrier.
         auto agree = [&] { return ok = named_barrier_and(1 + w, 128, ok); };
-        while (walk.next(p, it)) {
+        while (walk.next(p, sh->marks, it)) {
             float l[C];
 #pragma unroll
             for (int c = 0; c < C; ++c) l[c] = 0.f;
+            bool unset = true;  // some row has seen no key yet: its first one is its reference, however small
             const Rows r(p, it.unit);
             const int before = it.sp.Lk - it.sp.Lq;
             const uint64_t *mask = p.mask ? p.mask + (int64_t)it.seq * p.nq * p.words : nullptr;
@@ -328,7 +331,7 @@ paged_attn_kernel(const __grid_constant__ CUtensorMap tQ, const __grid_constant_
                     }
                 };
                 if (j > it.lo) exponents();
-                if (named_barrier_or(1 + w, 128, j == it.lo || top > kOutgrown || !ok)) {
+                if (named_barrier_or(1 + w, 128, unset || top > kOutgrown || !ok)) {
                     // a new reference for every column, and O and l to it
                     if (!agree()) break;
 #pragma unroll 1
@@ -342,6 +345,7 @@ paged_attn_kernel(const __grid_constant__ CUtensorMap tQ, const __grid_constant_
                     }
                     if (j > it.lo) ok = product(n - 1, 129);
                     if (!agree()) break;
+                    bool none = false;
                     if (key0 < C) {
                         const float mo = j > it.lo ? sh->m[c0 + key0] : -INFINITY;
                         float mn = mo;
@@ -349,8 +353,11 @@ paged_attn_kernel(const __grid_constant__ CUtensorMap tQ, const __grid_constant_
                         sh->m[c0 + key0] = mn;
                         sh->off[c0 + key0] = mn == -INFINITY ? 0.f : -mn * sl;
                         sh->f[c0 + key0] = mn == -INFINITY ? 1.f : ex2_approx((mo - mn) * sl);
+                        const int c = c0 + key0;
+                        none = mn == -INFINITY && c < p.qbox * p.hbox && r.h0 + c / p.qbox < p.group &&
+                               r.q0 + (c & (p.qbox - 1)) < it.sp.Lq;
                     }
-                    named_barrier_sync(1 + w, 128);
+                    unset = named_barrier_or(1 + w, 128, none);
                     if (j > it.lo) {
                         tc_fence_after();
 #pragma unroll
@@ -401,42 +408,41 @@ paged_attn_kernel(const __grid_constant__ CUtensorMap tQ, const __grid_constant_
                 if (lane == 0) mbar_arrive(&sh->p_full[b]);
             }
             // O / l out of tensor memory, a row of O^T an element of d
-            ok = ok && product(n - 1, 132);
             reduce_to(l, part, lane, [](float a, float z) { return a + z; });
+            ok = ok && product(n - 1, 132);
             if (!agree()) break;
             tc_fence_after();
+            uint32_t o[C];
+            const bool stores = key0 - lane < p.d;  // (of the warp)
+            if (stores) tmem_load(tO, o);
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&sh->o_free);
             if (key0 < C) {
                 const int c = c0 + key0, i = r.q0 + (c & (p.qbox - 1)), hg = r.h0 + c / p.qbox;
                 float sum = 0.f;
                 for (int x = 0; x < 4; ++x) sum += sh->part[w][x][key0];
                 const bool dead = i >= it.sp.Lq || sum == 0.f;
                 const float lse = dead ? -INFINITY : sh->m[c] * p.scale + logf(sum);
+                const int64_t h = (int64_t)it.kvh * p.group + hg;
+                const bool exists = c < p.qbox * p.hbox && hg < p.group && i < p.nq;
                 sh->f[c] = dead ? 0.f : 1.f / sum;
+                sh->row[c] = !exists ? -1 : it.slot >= 0 ? ((int64_t)it.slot * N + c) * DP
+                                                         : it.seq * p.so.b + h * p.so.h + (int64_t)i * p.so.n;
                 if (it.slot >= 0) p.part_lse[(int64_t)it.slot * N + c] = lse;
-                else if (c < p.qbox * p.hbox && hg < p.group && i < p.nq)
-                    p.lse[((int64_t)it.seq * p.hq + it.kvh * p.group + hg) * p.nq + i] = lse;
+                else if (exists) p.lse[(it.seq * (int64_t)p.hq + h) * p.nq + i] = lse;
             }
             named_barrier_sync(1 + w, 128);
-            if (key0 - lane < p.d) {
-#pragma unroll 1
-                for (int c = 0; c < C; c += 8) {
-                    uint32_t q[8];
-                    tmem_ld8(tO + c, q);
+            if (stores && key0 < p.d) {
 #pragma unroll
-                    for (int e = 0; e < 8; ++e) {
-                        const int x = c0 + c + e, i = r.q0 + (x & (p.qbox - 1)), hg = r.h0 + x / p.qbox;
-                        const float f = sh->f[x], o = f == 0.f ? 0.f : __uint_as_float(q[e]) * f;
-                        if (x >= p.qbox * p.hbox || hg >= p.group || i >= p.nq || key0 >= p.d) continue;
-                        if (it.slot >= 0) p.part_o[((int64_t)it.slot * N + x) * DP + key0] = o;
-                        else
-                            p.out[it.seq * p.so.b + ((int64_t)it.kvh * p.group + hg) * p.so.h + (int64_t)i * p.so.n + key0] =
-                                __float2bfloat16_rn(o);
-                    }
+                for (int c = 0; c < C; ++c) {
+                    const int64_t at = sh->row[c0 + c];
+                    if (at < 0) continue;
+                    const float f = sh->f[c0 + c], y = f == 0.f ? 0.f : __uint_as_float(o[c]) * f;
+                    if (it.slot >= 0) p.part_o[at + key0] = y;
+                    else p.out[at + key0] = __float2bfloat16_rn(y);
                 }
             }
-            tc_fence_before();
-            __syncwarp();
-            if (lane == 0) mbar_arrive(&sh->o_free);
         }
     }
     tc_fence_before();
@@ -454,6 +460,7 @@ template <int DP, int kEach>
 __global__ void __launch_bounds__(kJoinWarps * 32) join_kernel(const __grid_constant__ AttnParams p) {
     constexpr int E = DP / 32;
     __shared__ float shared[kEach > 1 ? kJoinWarps : 1][E + 1][32];
+    launch_dependents();
     wait_prerequisites();
     const int rows = p.qbox * p.hbox, lane = threadIdx.x & 31, warp = threadIdx.x >> 5, mine = warp % kEach;
     int x = blockIdx.y * (kJoinWarps / kEach) + warp / kEach;
@@ -522,26 +529,11 @@ __global__ void __launch_bounds__(kJoinWarps * 32) join_kernel(const __grid_cons
 
 template <int DP, int N>
 int launch(const AttnCall &c, AttnParams &p) {
-    using L = Layout<DP, N>;
-    constexpr uint32_t kSmem = 1024 + L::kEnd + sizeof(Shared);
+    constexpr uint32_t kSmem = 1024 + Layout<DP, N>::kEnd + sizeof(Shared);
     static_assert(kSmem <= 227 * 1024, "shared memory");
-    Maps m;
-    if (!encode_maps(c, p, m)) return LINFORMER_ERR_LAUNCH;
+    constexpr int kSlot = 10 + (DP == 128 ? 3 : 0) + (N == 16 ? 0 : N == 32 ? 1 : 2);
     p.N = N;
-    void *ws = nullptr;
-    int st = take_workspace(p, DP, &ws, c.stream);
-    if (st) return st;
-    const auto kernel = paged_attn_kernel<DP, N>;
-    constexpr int kSlot = 10 + (DP == 128 ? 4 : 0) + (N == 16 ? 0 : N == 32 ? 1 : N == 64 ? 2 : 3);
-    st = sattn::allow_smem(reinterpret_cast<const void *>(kernel), kSmem, kSlot);
-    if (!st) {
-        KernelScope scope(LINFORMER_KERNEL_PAGED, c.stream);
-        kernel<<<p.ctas, kThreads, kSmem, c.stream>>>(m.q, m.k, m.v, p);
-        if (cudaGetLastError() != cudaSuccess) st = LINFORMER_ERR_LAUNCH;
-    }
-    if (!st) st = launch_join(p, DP, c.stream);
-    workspace_free(ws, c.stream);
-    return st;
+    return launch_with_join(paged_attn_kernel<DP, N>, kThreads, kSmem, kSlot, c, p, DP);
 }
 
 template <int DP>
@@ -554,42 +546,60 @@ int launch_rows(const AttnCall &c, AttnParams &p) {
 
 }  // namespace
 
-bool encode_maps(const AttnCall &c, const AttnParams &p, Maps &m) {
-    const Cache &k = c.cache;
-    return sattn::encode_rows(&m.q, c.q, c.sq, c.b, c.hq, p.group, c.nq, c.d, p.qbox, p.hbox) &&
-           sattn::encode_rows(&m.k, k.k, k.sk, k.pages, c.hk, 1, k.page, c.d, p.box, 1) &&
-           sattn::encode_rows(&m.v, k.v, k.sv, k.pages, c.hk, 1, k.page, c.d, p.box, 1);
-}
-
-int take_workspace(AttnParams &p, int dp, void **ws, cudaStream_t s) {
-    const size_t head = p.ctas * sizeof(int4);  // (parts are read 16 bytes at a time)
-    const size_t parts = (size_t)2 * p.ctas * p.per * p.N;
-    if (workspace_alloc(ws, head + parts * (dp + 1) * sizeof(float), s) != LINFORMER_OK) return LINFORMER_ERR_ALLOC;
-    p.cuts = static_cast<int4 *>(*ws);
-    p.part_o = reinterpret_cast<float *>(static_cast<char *>(*ws) + head);
-    p.part_lse = p.part_o + parts * dp;
-    return LINFORMER_OK;
-}
-
-int launch_join(const AttnParams &p, int dp, cudaStream_t s) {
-    KernelScope scope(LINFORMER_KERNEL_PAGED, s);
+int launch_with_join(Kernel kernel, int threads, uint32_t smem, int slot, const AttnCall &c, AttnParams &p, int dp) {
+    CUtensorMap q, k, v;
+    const Cache &cache = c.cache;
+    if (!sattn::encode_rows(&q, c.q, c.sq, c.b, c.hq, p.group, c.nq, c.d, p.qbox, p.hbox) ||
+        !sattn::encode_rows(&k, cache.k, cache.sk, cache.pages, c.hk, 1, cache.page, c.d, p.box, 1) ||
+        !sattn::encode_rows(&v, cache.v, cache.sv, cache.pages, c.hk, 1, cache.page, c.d, p.box, 1))
+        return LINFORMER_ERR_LAUNCH;
+    char *ws = nullptr;
+    if (!p.whole) {
+        const size_t head = p.ctas * sizeof(int4);  // (parts are read 16 bytes at a time)
+        const size_t parts = (size_t)2 * p.ctas * p.per * p.N;
+        if (workspace_alloc(reinterpret_cast<void **>(&ws), head + parts * (dp + 1) * sizeof(float), c.stream) !=
+            LINFORMER_OK)
+            return LINFORMER_ERR_ALLOC;
+        p.cuts = reinterpret_cast<int4 *>(ws);
+        p.part_o = reinterpret_cast<float *>(ws + head);
+        p.part_lse = p.part_o + parts * dp;
+    }
+    // each kernel is set up while the one before it ends, and waits for that before it reads
     cudaLaunchConfig_t cfg{};
     cudaLaunchAttribute attr[1];
     attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
     attr[0].val.programmaticStreamSerializationAllowed = 1;
-    cfg.stream = s;
+    cfg.stream = c.stream;
     cfg.attrs = attr;
     cfg.numAttrs = 1;
-    // many parts where a unit's blocks, all units alike, would fill eight runs
-    const bool many = (int64_t)p.b * p.units * p.hk * 8 <= p.ctas;
-    const int rows = p.per * p.qbox * p.hbox, at_once = many ? 1 : kJoinWarps;
-    cfg.gridDim = dim3((unsigned)p.ctas, (unsigned)((rows + at_once - 1) / at_once));
-    cfg.blockDim = dim3(kJoinWarps * 32);
-    const auto kernel = dp == 64 ? (many ? join_kernel<64, kJoinWarps> : join_kernel<64, 1>)
-                                 : (many ? join_kernel<128, kJoinWarps> : join_kernel<128, 1>);
-    if (cudaLaunchKernelEx(&cfg, kernel, p) == cudaSuccess) return LINFORMER_OK;
-    cudaGetLastError();
-    return LINFORMER_ERR_LAUNCH;
+    int st = sattn::allow_smem(reinterpret_cast<const void *>(kernel), smem, slot);
+    if (!st) {
+        KernelScope scope(LINFORMER_KERNEL_PAGED, c.stream);
+        cfg.gridDim = dim3((unsigned)p.ctas);
+        cfg.blockDim = dim3((unsigned)threads);
+        cfg.dynamicSmemBytes = smem;
+        if (cudaLaunchKernelEx(&cfg, kernel, q, k, v, p) != cudaSuccess) {
+            cudaGetLastError();
+            st = LINFORMER_ERR_LAUNCH;
+        }
+    }
+    if (!st && !p.whole) {
+        KernelScope scope(LINFORMER_KERNEL_PAGED, c.stream);
+        // many parts where a unit's blocks, all units alike, would fill eight runs
+        const bool many = (int64_t)p.b * p.units * p.hk * 8 <= p.ctas;
+        const int rows = p.per * p.qbox * p.hbox, at_once = many ? 1 : kJoinWarps;
+        cfg.gridDim = dim3((unsigned)p.ctas, (unsigned)((rows + at_once - 1) / at_once));
+        cfg.blockDim = dim3(kJoinWarps * 32);
+        cfg.dynamicSmemBytes = 0;
+        const auto join = dp == 64 ? (many ? join_kernel<64, kJoinWarps> : join_kernel<64, 1>)
+                                   : (many ? join_kernel<128, kJoinWarps> : join_kernel<128, 1>);
+        if (cudaLaunchKernelEx(&cfg, join, p) != cudaSuccess) {
+            cudaGetLastError();
+            st = LINFORMER_ERR_LAUNCH;
+        }
+    }
+    if (ws) workspace_free(ws, c.stream);
+    return st;
 }
 
 int attention(const AttnCall &call) {
@@ -627,6 +637,9 @@ int attention(const AttnCall &call) {
     // are huge
     const int64_t most = units * call.hk * (((int64_t)p.width * p.page + kTile - 1) / kTile);
     if (most > 0x7fffffffLL) return LINFORMER_ERR_SIZE;
+    // Units of a few blocks at most stay whole: no workspace, no second kernel.
+    constexpr int kWholeBlocks = 8;
+    p.whole = (int64_t)p.width * p.page <= kWholeBlocks * kTile;
     const int seqs = (int)std::min<int64_t>(kMaxSeqs, 0x7fffffffLL / most);
     p.ntiles = (int)ntiles;
     p.units = (int)units;

@@ -12,7 +12,6 @@ namespace linformer {
 namespace paged {
 
 using namespace ptx;
-using sattn::clamp_length;
 using sattn::kTile;  // keys of a block
 using sattn::pack2;
 using sattn::Span;
@@ -33,6 +32,7 @@ struct AttnParams {
     // tiles of qbox positions of hbox heads (nch tiles to a group), `per` of them to a unit of work;
     // N: rows of a tile in the workspace
     int qbox, hbox, nch, ntiles, per, units, N, ctas;
+    int whole;  // no unit is cut
     int pages, page, width, shift, box, nbox;  // nbox boxes of `box` rows make a block of keys
     float scale, scale_log2;
     int wide_stores;
@@ -71,17 +71,34 @@ __device__ __forceinline__ void blocks_of_unit(const AttnParams &p, const Span &
         }
     }
 }
-__device__ __forceinline__ Span span_of(const AttnParams &p, int seq) {
-    return Span{clamp_length(p.q_lengths, seq, p.nq), clamp_length(p.k_lengths, seq, p.width * p.page), p.causal,
-                p.window};
+// A sequence's length (not by __ldg: a load of what is taken to be constant may be moved up, past the
+// wait for the kernel that writes it).
+__device__ __forceinline__ int read_length(const int32_t *lengths, int seq, int most) {
+    if (!lengths) return most;
+    int x;
+    asm volatile("ld.global.b32 %0, [%1];" : "=r"(x) : "l"(lengths + seq) : "memory");
+    return min(max(x, 0), most);
 }
-__device__ __forceinline__ int run_begin(int total, int cta, int ctas) { return (int)((int64_t)total * cta / ctas); }
+// The lengths and the list's marks, in shared memory.
+struct Marks {
+    int2 length[kMaxSeqs];    // queries, cache rows
+    int first[kMaxSeqs + 1];  // where the blocks of each sequence begin in the list
+    __device__ __forceinline__ Span span(const AttnParams &p, int seq) const {
+        return Span{length[seq].x, length[seq].y, p.causal, p.window};
+    }
+};
+__device__ __forceinline__ int run_begin(int total, int cta, int ctas) {
+    const int each = total / ctas;
+    return each * cta + min(cta, total - each * ctas);
+}
 __device__ __forceinline__ int runs(int total, int ctas) { return min(ctas, max(1, total / kMinRun)); }
 
-// first[s] for all sequences, by a whole CTA (between two of its barriers: it has one).
-__device__ __forceinline__ void fill_first(const AttnParams &p, int *first, int tid, int threads) {
+// Fills the marks, by a whole CTA (it has one of the CTA's barriers; one has to follow).
+__device__ __forceinline__ void fill(const AttnParams &p, Marks &marks, int tid, int threads) {
+    int *first = marks.first;
     for (int s = tid; s < p.b; s += threads) {
-        const Span sp = span_of(p, s);
+        marks.length[s] = make_int2(read_length(p.q_lengths, s, p.nq), read_length(p.k_lengths, s, p.width * p.page));
+        const Span sp = marks.span(p, s);
         int sum = 0;
         for (int u = 0; u < p.units; ++u) {
             int lo, hi;
@@ -92,8 +109,7 @@ __device__ __forceinline__ void fill_first(const AttnParams &p, int *first, int 
     }
     __syncthreads();
     if (tid < 32) {
-        constexpr int kEach = kMaxSeqs / 32;
-        const int s0 = tid * kEach, s1 = min(s0 + kEach, p.b);
+        const int each = (p.b + 31) / 32, s0 = min(tid * each, p.b), s1 = min(s0 + each, p.b);
         int sum = 0;
         for (int s = s0; s < s1; ++s) sum += first[s + 1];
         int run = sum;
@@ -117,7 +133,8 @@ struct Walk {
     int at, end;
     int seq, unit, kvh, blk, lo, hi, slot;
     Span sp;
-    __device__ __forceinline__ Walk(const AttnParams &p, const int *first, int cta) {
+    __device__ __forceinline__ Walk(const AttnParams &p, const Marks &marks, int cta) {
+        const int *first = marks.first;
         const int total = first[p.b], n = runs(total, p.ctas);
         at = end = 0;
         if (cta >= n) return;
@@ -131,7 +148,7 @@ struct Walk {
             else z = m;
         }
         seq = a;
-        sp = span_of(p, seq);
+        sp = marks.span(p, seq);
         int off = at - first[seq];
         for (unit = 0;; ++unit) {
             blocks_of_unit(p, sp, unit, lo, hi);
@@ -142,11 +159,30 @@ struct Walk {
         kvh = off / (hi - lo);
         blk = off - kvh * (hi - lo);
         slot = 2 * cta;
+        if (p.whole && blk > 0) {  // the CTA before this one takes all of that unit
+            at += hi - lo - blk;
+            blk = 0;
+            advance(p, marks);
+        }
+    }
+    // To the unit at `at`, the one after this.
+    __device__ __forceinline__ void advance(const AttnParams &p, const Marks &marks) {
+        if (at < end && ++kvh == p.hk) {
+            kvh = 0;
+            do {
+                if (++unit == p.units) {
+                    unit = 0;
+                    ++seq;
+                    sp = marks.span(p, seq);
+                }
+                blocks_of_unit(p, sp, unit, lo, hi);
+            } while (hi <= lo);
+        }
     }
     // The next item, while there is one.
-    __device__ __forceinline__ bool next(const AttnParams &p, Item &it) {
+    __device__ __forceinline__ bool next(const AttnParams &p, const Marks &marks, Item &it) {
         if (at >= end) return false;
-        const int n = min(hi - lo - blk, end - at);
+        const int n = p.whole ? hi - lo : min(hi - lo - blk, end - at);
         it.seq = seq;
         it.unit = unit;
         it.kvh = kvh;
@@ -156,17 +192,7 @@ struct Walk {
         it.slot = blk == 0 && it.hi == hi ? -1 : blk ? slot : slot + 1;
         at += n;
         blk = 0;
-        if (at < end && ++kvh == p.hk) {
-            kvh = 0;
-            do {
-                if (++unit == p.units) {
-                    unit = 0;
-                    ++seq;
-                    sp = span_of(p, seq);
-                }
-                blocks_of_unit(p, sp, unit, lo, hi);
-            } while (hi <= lo);
-        }
+        advance(p, marks);
         return true;
     }
 };
@@ -174,6 +200,7 @@ struct Walk {
 // What the join has to know of a CTA, by one thread of it, from its walk's start: the unit whose last
 // part the CTA does, and the CTA that does the first; x = -1 where it ends no cut unit.
 __device__ __forceinline__ void write_cut(const AttnParams &p, const Walk &w, int total) {
+    if (p.whole) return;
     int4 cut = make_int4(-1, 0, 0, 0);
     if (w.at < w.end && w.blk > 0 && w.end - w.at >= w.hi - w.lo - w.blk) {
         const int n = runs(total, p.ctas);
@@ -185,12 +212,12 @@ __device__ __forceinline__ void write_cut(const AttnParams &p, const Walk &w, in
 }
 
 // Units without blocks, a share a CTA, by `warps` warps: O = 0, lse = -inf.
-__device__ __forceinline__ void write_empty(const AttnParams &p, int warp, int warps, int lane) {
+__device__ __forceinline__ void write_empty(const AttnParams &p, const Marks &marks, int warp, int warps, int lane) {
     const int all = p.b * p.units * p.hk;
     for (int u = blockIdx.x; u < all; u += gridDim.x) {
         const int kvh = u % p.hk, unit = u / p.hk % p.units, seq = u / p.hk / p.units;
         int lo, hi;
-        blocks_of_unit(p, span_of(p, seq), unit, lo, hi);
+        blocks_of_unit(p, marks.span(p, seq), unit, lo, hi);
         if (hi > lo) continue;
         for (int t = unit * p.per; t < min(p.ntiles, (unit + 1) * p.per); ++t) {
             const Rows r(p, t);
@@ -219,13 +246,9 @@ __device__ __forceinline__ int page_of(const AttnParams &p, const int32_t *table
 }
 
 // Host side (paged_attn.cu).
-struct Maps {
-    CUtensorMap q, k, v;
-};
-bool encode_maps(const AttnCall &c, const AttnParams &p, Maps &m);
-// Workspace of a launch of rows of `dp` elements (p.N, p.per, p.ctas set): *ws to be freed.
-int take_workspace(AttnParams &p, int dp, void **ws, cudaStream_t s);
-int launch_join(const AttnParams &p, int dp, cudaStream_t s);
+// Launches a kernel for rows of `dp` elements (p.N, p.per, p.ctas set), and the join after it.
+using Kernel = void (*)(CUtensorMap, CUtensorMap, CUtensorMap, AttnParams);
+int launch_with_join(Kernel kernel, int threads, uint32_t smem, int slot, const AttnCall &c, AttnParams &p, int dp);
 
 // Tiles of 128 rows in pairs (paged_attn_wide.cu).
 int launch_wide(const AttnCall &c, AttnParams &p);

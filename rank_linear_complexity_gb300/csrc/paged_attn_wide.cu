@@ -42,7 +42,7 @@ struct Shared {
     uint32_t tmem;
     int abort;
     int pages[kTile / 8];
-    int first[kMaxSeqs + 1];
+    Marks marks;
 };
 
 // A tile's part of an item.
@@ -92,7 +92,7 @@ paged_wide_kernel(const __grid_constant__ CUtensorMap tQ, const __grid_constant_
     volatile int *abort_flag = &sh->abort;
     const int tid = threadIdx.x, warp = __shfl_sync(0xffffffffu, tid >> 5, 0), lane = tid & 31;
 
-    if (tid == 0) {
+    if (tid == 32) {
         for (int t = 0; t < 2; ++t) {
             mbar_init(&sh->q_full[t], 1);
             mbar_init(&sh->q_free[t], 1);
@@ -117,14 +117,15 @@ paged_wide_kernel(const __grid_constant__ CUtensorMap tQ, const __grid_constant_
         prefetch_tmap(&tQ);
         prefetch_tmap(&tK);
         prefetch_tmap(&tV);
-        launch_dependents();  // the join, which waits for this grid's end
     }
     if (warp == kMmaWarp) {
         tmem_alloc(&sh->tmem, 512);
         tmem_relinquish();
     }
     tc_fence_before();
-    fill_first(p, sh->first, tid, kThreads);
+    wait_prerequisites();
+    if (tid == 0) launch_dependents();  // the join, which waits for this grid's end
+    fill(p, sh->marks, tid, kThreads);
     __syncthreads();
     tc_fence_after();
     const uint32_t tmem = sh->tmem;
@@ -201,21 +202,22 @@ paged_wide_kernel(const __grid_constant__ CUtensorMap tQ, const __grid_constant_
             __syncwarp();
         } else if (warp == kPlanWarp) {
             if (elect_one()) {
-                Walk walk(p, sh->first, blockIdx.x);
-                write_cut(p, walk, sh->first[p.b]);
+                Walk walk(p, sh->marks, blockIdx.x);
+                const Walk begin = walk;
                 Item it;
                 for (int k = 0;; ++k) {
                     const int s = k % kAhead;
-                    const bool more = walk.next(p, it);
+                    const bool more = walk.next(p, sh->marks, it);
                     if (!more) it.seq = -1;
                     if (k >= kAhead && !thread_spin(&sh->taken[s], (k / kAhead - 1) & 1, p.status, 156, abort_flag)) break;
                     sh->items[s] = it;
                     mbar_arrive(&sh->told[s]);
+                    if (k == 0) write_cut(p, begin, sh->marks.first[p.b]);
                     if (!more) break;
                 }
             }
             __syncwarp();
-            write_empty(p, 0, 1, lane);
+            write_empty(p, sh->marks, 0, 1, lane);
         } else if (elect_one()) {  // ---------------- products of tile t
             const int t = warp - kMmaWarp;
             const uint32_t idesc_s = idesc_f16(128, 128, 1, 0, 0), idesc_o = idesc_f16(128, DP, 1, 0, 1);
@@ -512,22 +514,8 @@ template <int DP>
 int launch(const AttnCall &c, AttnParams &p) {
     constexpr uint32_t kSmem = 1024 + Layout<DP>::kEnd + sizeof(Shared);
     static_assert(kSmem <= 227 * 1024, "shared memory");
-    Maps m;
-    if (!encode_maps(c, p, m)) return LINFORMER_ERR_LAUNCH;
     p.N = kTile;
-    void *ws = nullptr;
-    int st = take_workspace(p, DP, &ws, c.stream);
-    if (st) return st;
-    const auto kernel = paged_wide_kernel<DP>;
-    st = sattn::allow_smem(reinterpret_cast<const void *>(kernel), kSmem, DP == 64 ? 18 : 19);
-    if (!st) {
-        KernelScope scope(LINFORMER_KERNEL_PAGED, c.stream);
-        kernel<<<p.ctas, kThreads, kSmem, c.stream>>>(m.q, m.k, m.v, p);
-        if (cudaGetLastError() != cudaSuccess) st = LINFORMER_ERR_LAUNCH;
-    }
-    if (!st) st = launch_join(p, DP, c.stream);
-    workspace_free(ws, c.stream);
-    return st;
+    return launch_with_join(paged_wide_kernel<DP>, kThreads, kSmem, DP == 64 ? 16 : 17, c, p, DP);
 }
 
 }  // namespace

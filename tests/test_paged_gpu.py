@@ -324,6 +324,31 @@ def test_growing_logits():
         assert (np.abs(host64(lse) - want[1]) <= want[3]).all()
 
 
+@pytest.mark.parametrize("level", [-300.0, 0.0, 300.0])
+def test_rows_whose_first_keys_come_late(level):
+    """Blocks in which some rows of a tile see nothing, before blocks in which they do, at logits far
+    from zero: windows that begin past a block's edge, trees whose nodes see no row before them."""
+    for nq, hq, hk, lk, window in ((7, 4, 2, 400, 11), (60, 2, 2, 500, 20), (5, 8, 1, 1300, 9), (200, 4, 2, 900, 40)):
+        kc, vc, table = cache(1, hk, 64, 16, [lk], device=DEV, seed=9)
+        kc[..., 0] = torch.where(kc[..., 0].isnan(), kc[..., 0], level / 4)
+        Q = torch.randn(1, hq, nq, 64, device=DEV, generator=torch.Generator(device=DEV).manual_seed(2)).to(BF)
+        Q[..., 0] = 32.0  # level logits on top of the others, scale 1 / 8
+        O, lse = lf.paged_attention(Q, kc, vc, table, ints([lk], DEV), window=window)
+        status()
+        want = paged.forward(Q, kc, vc, table.tolist(), (lk,), causal=True, window=window)
+        assert (np.abs(host64(O) - want[0]) <= want[2]).all() and (np.abs(host64(lse) - want[1]) <= want[3]).all()
+        n = min(nq, 100)
+        tree = paged.ancestors(random_tree(1, n, seed=3).numpy())
+        Q = Q[:, :, :n].contiguous()
+        for k in (n, n // 2):
+            O, lse = lf.tree_attention(Q, kc, vc, table, ints([k], DEV), torch.from_numpy(paged.words(tree)).to(DEV))
+            status()
+            want = paged.forward(Q, kc, vc, table.tolist(), (k,), tree=tree)
+            some = np.isfinite(want[1])
+            assert np.array_equal(np.isneginf(host64(lse)), ~some)
+            assert (np.abs(host64(O) - want[0]) <= want[2]).all() and (np.abs(host64(lse)[some] - want[1][some]) <= want[3][some]).all()
+
+
 def test_many_sequences():
     r = np.random.default_rng(3)
     lengths = tuple(int(x) for x in r.integers(0, 300, 150))
