@@ -41,11 +41,10 @@ struct Layout {
     // DP = 64: K and V of a block share an entry of the ring, V first (the product takes 128 rows of
     // V^T, of which the second half falls on K and is not used)
     static constexpr bool kPair = DP == 64;
-    static constexpr int kEntries = kPair ? (N == 128 ? 4 : 5) : (N == 128 ? 4 : 5);
+    static constexpr int kEntries = 5;
     static constexpr uint32_t kEntryBytes = kPair ? 2 * kTileBytes : kTileBytes;
-    static constexpr int kPBufs = N == 128 ? 1 : 2;
-    static constexpr int kGroups = N > 64 ? 2 : 1;  // of 64 columns
-    static constexpr uint32_t kPBytes = kGroups * kTile * 128;
+    static constexpr int kPBufs = 2;
+    static constexpr uint32_t kPBytes = kTile * 128;  // (rows of 64 columns)
     static constexpr uint32_t kQHalf = N * 128, kQBytes = kQHalf * (DP / 64);
     static constexpr uint32_t kP = kEntries * kEntryBytes, kQ = kP + kPBufs * kPBytes, kEnd = kQ + kQBytes;
     static constexpr uint32_t kS = 0, kO = 2 * N;  // tensor memory: S, S, O
@@ -55,11 +54,14 @@ struct Shared {
     uint64_t full[5], empty[5], q_full, q_free, s_full[2], s_free[2], p_full[2], pv_done[2], o_free, drain;
     uint32_t tmem;
     int abort;
-    alignas(16) float m[128];
-    alignas(16) float off[128];
-    alignas(16) float f[128];
-    float part[2][4][64];  // a value a column, by warp of each group
-    alignas(16) int64_t row[128];  // where a column's row of O begins, -1: nowhere
+    // of each column: the reference (log2; -infinity where no key has been seen), what is added to the
+    // scores for it, what the reference moves by, and what l and O take for that, or 1 / l
+    alignas(16) float m[64];
+    alignas(16) float off[64];
+    alignas(16) float up[64];
+    alignas(16) float f[64];
+    float part[2][4][32];  // a value a column, by warp of each group
+    alignas(16) int64_t row[64];  // where a column's row of O begins, -1: nowhere
     Marks marks;
 };
 
@@ -67,8 +69,7 @@ template <int C>
 __device__ __forceinline__ void tmem_load(uint32_t t, uint32_t (&v)[C]) {
     if constexpr (C == 8) tmem_ld8(t, v);
     else if constexpr (C == 16) tmem_ld16(t, v);
-    else if constexpr (C == 32) tmem_ld32(t, v);
-    else tmem_ld64(t, v);
+    else tmem_ld32(t, v);
 }
 
 // Reduces C columns over the 32 lanes of a warp; column(lane) of lane's result.  Each exchange
@@ -93,7 +94,7 @@ __device__ __forceinline__ float reduce_columns(float (&v)[C], int lane, F f) {
 // Over a warp, into part[0 .. C).
 template <int C, typename F>
 __device__ __forceinline__ void reduce_to(const float (&v)[C], float *part, int lane, F f) {
-    constexpr int H = C < 32 ? C : 32;
+    constexpr int H = C < 16 ? C : 16;
 #pragma unroll
     for (int h = 0; h < C; h += H) {
         float x[H];
@@ -104,26 +105,14 @@ __device__ __forceinline__ void reduce_to(const float (&v)[C], float *part, int 
     }
 }
 
-// The scores of a block that key `key` may not give become -inf in tensor memory: the few blocks
-// at a mask's edge keep out of the code of the others.
-__device__ __noinline__ void mask_columns(uint32_t t, int c0, int columns, int key, Span sp, int i0, int positions,
-                                          const uint64_t *mask, int words) {
-    const int node = key - (sp.Lk - sp.Lq);
-    const bool tree = mask && node >= 0;
-#pragma unroll 1
-    for (int c = 0; c < columns; c += 8) {
-        uint32_t v[8];
-        tmem_ld8(t + c, v);
-#pragma unroll
-        for (int e = 0; e < 8; ++e) {
-            const int i = i0 + ((c0 + c + e) & (positions - 1));
-            bool see = i < sp.Lq && key >= sp.first(i) && key < sp.end(i);
-            if (see && tree) see = __ldg(mask + (int64_t)i * words + (node >> 6)) >> (node & 63) & 1;
-            if (!see) v[e] = 0xff800000u;
-        }
-        tmem_st8_async(t + c, v);
-        tmem_wait_st();
-    }
+// Which of `positions` rows from q0 on see node `node` of a tree, a bit a row.
+__device__ __noinline__ uint64_t tree_bits(const uint64_t *mask, int words, int node, int q0, int positions, int Lq) {
+    uint64_t see = 0;
+    mask += (int64_t)q0 * words + (node >> 6);
+#pragma unroll 8
+    for (int x = 0; x < positions; ++x)
+        if (q0 + x < Lq) see |= (__ldg(mask + (int64_t)x * words) >> (node & 63) & 1) << x;
+    return see;
 }
 
 template <int DP, int N>
@@ -302,6 +291,8 @@ paged_attn_kernel(const __grid_constant__ CUtensorMap tQ, const __grid_constant_
 #pragma unroll
             for (int c = 0; c < C; ++c) l[c] = 0.f;
             bool unset = true;  // some row has seen no key yet: its first one is its reference, however small
+            if (key0 < C) sh->off[c0 + key0] = 0.f;
+            named_barrier_sync(1 + w, 128);
             const Rows r(p, it.unit);
             const int before = it.sp.Lk - it.sp.Lq;
             const uint64_t *mask = p.mask ? p.mask + (int64_t)it.seq * p.nq * p.words : nullptr;
@@ -310,13 +301,8 @@ paged_attn_kernel(const __grid_constant__ CUtensorMap tQ, const __grid_constant_
                 const uint32_t tS = tmem + L::kS + N * s + c0 + lanes;
                 ok = ok && warp_spin(&sh->s_full[s], (n >> 1) & 1, p.status, 128, abort_flag);
                 tc_fence_after();
-                const bool ragged = k0 + kTile > it.sp.Lk;
-                // (rows that the tile does not have see nothing or anything)
-                if (ragged || (p.causal && k0 + kTile > r.q0 + before + 1) || (p.mask && k0 + kTile > before) ||
-                    (p.window && k0 < it.sp.first(min(r.q0 + p.qbox, it.sp.Lq) - 1)))
-                    mask_columns(tS, c0, C, key, it.sp, r.q0, p.qbox, mask, p.words);
-                float y[C], top = -INFINITY;
-                auto exponents = [&] {
+                float y[C];  // log2 of p, from the reference
+                {
                     uint32_t v[C];
                     tmem_load(tS, v);
 #pragma unroll
@@ -327,41 +313,78 @@ paged_attn_kernel(const __grid_constant__ CUtensorMap tQ, const __grid_constant_
                         const float2 z = ffma2(make_float2(__uint_as_float(v[c + 2]), __uint_as_float(v[c + 3])),
                                                make_float2(sl, sl), make_float2(off.z, off.w));
                         y[c] = a.x, y[c + 1] = a.y, y[c + 2] = z.x, y[c + 3] = z.y;
-                        top = fmaxf(max3(top, a.x, a.y), fmaxf(z.x, z.y));
                     }
-                };
-                if (j > it.lo) exponents();
-                if (named_barrier_or(1 + w, 128, unset || top > kOutgrown || !ok)) {
-                    // a new reference for every column, and O and l to it
-                    if (!agree()) break;
-#pragma unroll 1
-                    for (int c = 0; c < C; c += 8) {
-                        uint32_t v[8];
-                        tmem_ld8(tS + c, v);
-                        float x[8];
+                }
+                tc_fence_before();
+                __syncwarp();
+                if (lane == 0) mbar_arrive(&sh->s_free[s]);
+                // which columns see the key, a bit each: rows [key, key + window) of the new tokens, or
+                // those whose masks have the node
+                const bool ragged = k0 + kTile > it.sp.Lk;
+                const bool edge = p.mask ? k0 + kTile > before
+                                         : p.causal && (it.sp.end(r.q0) < min(k0 + kTile, it.sp.Lk) ||
+                                                        k0 < it.sp.first(min(r.q0 + p.qbox, it.sp.Lq) - 1));
+                if (ragged || edge) {
+                    uint32_t see = key < it.sp.Lk ? 0xffffffffu : 0u;
+                    if (edge) {
+                        uint64_t rows = ~0ull;  // of the tile's positions
+                        const int at = key - before - r.q0;
+                        if (p.mask) {
+                            if (key >= before && key < it.sp.Lk)
+                                rows = tree_bits(mask, p.words, key - before, r.q0, p.qbox, it.sp.Lq);
+                        } else {
+                            if (at > 0) rows = at < 64 ? rows << at : 0;
+                            const int z = p.window ? at + p.window : 64;  // (at + window fits: both are below 2^30)
+                            if (z < 64) rows = z > 0 ? rows & ~(~0ull << z) : 0;
+                        }
+                        // the positions come again for each head
+                        see &= p.qbox >= C ? (uint32_t)(rows >> (c0 & (p.qbox - 1)))
+                                           : ((uint32_t)rows & ((1u << p.qbox) - 1)) * (0xffffffffu / ((1u << p.qbox) - 1));
+                    }
 #pragma unroll
-                        for (int e = 0; e < 8; ++e) x[e] = __uint_as_float(v[e]);
-                        reduce_to(x, part + c, lane, [](float a, float z) { return fmaxf(a, z); });
-                    }
+                    for (int c = 0; c < C; ++c)
+                        if (!(see >> c & 1)) y[c] = -INFINITY;  // (whatever it was)
+                }
+                float top = y[0];
+#pragma unroll
+                for (int c = 1; c < C; ++c) top = fmaxf(top, y[c]);
+                if (named_barrier_or(1 + w, 128, unset || top > kOutgrown || !ok)) {
+                    // references move up by the columns' maxima (where there is none yet, to it); y, l and O
+                    // with them
+                    if (!agree()) break;
+                    reduce_to(y, part, lane, [](float a, float z) { return fmaxf(a, z); });
                     if (j > it.lo) ok = product(n - 1, 129);
                     if (!agree()) break;
                     bool none = false;
                     if (key0 < C) {
-                        const float mo = j > it.lo ? sh->m[c0 + key0] : -INFINITY;
-                        float mn = mo;
-                        for (int x = 0; x < 4; ++x) mn = fmaxf(mn, sh->part[w][x][key0]);
-                        sh->m[c0 + key0] = mn;
-                        sh->off[c0 + key0] = mn == -INFINITY ? 0.f : -mn * sl;
-                        sh->f[c0 + key0] = mn == -INFINITY ? 1.f : ex2_approx((mo - mn) * sl);
                         const int c = c0 + key0;
-                        none = mn == -INFINITY && c < p.qbox * p.hbox && r.h0 + c / p.qbox < p.group &&
+                        float up = sh->part[w][0][key0];
+                        for (int x = 1; x < 4; ++x) up = fmaxf(up, sh->part[w][x][key0]);
+                        const float m = j > it.lo ? sh->m[c] : -INFINITY;
+                        none = m == -INFINITY && up == -INFINITY;
+                        // (a reference of 0 stands for none)
+                        if (m != -INFINITY) up = fmaxf(up, 0.f);
+                        if (!none) {
+                            const float mn = m == -INFINITY ? up : m + up;
+                            sh->m[c] = mn;
+                            sh->off[c] = -mn;
+                        } else {
+                            sh->m[c] = -INFINITY;
+                            up = 0.f;
+                        }
+                        sh->up[c] = up;
+                        sh->f[c] = m == -INFINITY ? 1.f : ex2_approx(-up);  // (l and O are 0 where there was none)
+                        none = none && c < p.qbox * p.hbox && r.h0 + c / p.qbox < p.group &&
                                r.q0 + (c & (p.qbox - 1)) < it.sp.Lq;
                     }
                     unset = named_barrier_or(1 + w, 128, none);
+#pragma unroll
+                    for (int c = 0; c < C; ++c) {
+                        y[c] -= sh->up[c0 + c];
+                        l[c] *= sh->f[c0 + c];
+                    }
                     if (j > it.lo) {
                         tc_fence_after();
-#pragma unroll
-                        for (int c = 0; c < C; ++c) l[c] *= sh->f[c0 + c];
 #pragma unroll 1
                         for (int c = 0; c < C; c += 8) {
                             uint32_t q[8];
@@ -371,12 +394,9 @@ paged_attn_kernel(const __grid_constant__ CUtensorMap tQ, const __grid_constant_
                             tmem_st8_async(tO + c, q);
                         }
                         tmem_wait_st();
+                        tc_fence_before();
                     }
-                    exponents();
                 }
-                tc_fence_before();
-                __syncwarp();
-                if (lane == 0) mbar_arrive(&sh->s_free[s]);
 #pragma unroll
                 for (int c = 0; c < C; ++c) {
                     y[c] = ex2_approx(y[c]);
@@ -387,8 +407,7 @@ paged_attn_kernel(const __grid_constant__ CUtensorMap tQ, const __grid_constant_
                 uint8_t *row = smem + L::kP + b * L::kPBytes + key0 * 128;
 #pragma unroll
                 for (int c = 0; c < C; c += 8) {
-                    const int g = (c0 + c) / 64, ch = ((c0 + c) % 64) / 8;
-                    *reinterpret_cast<uint4 *>(row + g * 16384 + ((ch ^ (key0 & 7)) * 16)) =
+                    *reinterpret_cast<uint4 *>(row + (((c0 + c) / 8 ^ (key0 & 7)) * 16)) =
                         make_uint4(pack2(y[c], y[c + 1]), pack2(y[c + 2], y[c + 3]), pack2(y[c + 4], y[c + 5]),
                                    pack2(y[c + 6], y[c + 7]));
                 }
@@ -423,7 +442,7 @@ paged_attn_kernel(const __grid_constant__ CUtensorMap tQ, const __grid_constant_
                 float sum = 0.f;
                 for (int x = 0; x < 4; ++x) sum += sh->part[w][x][key0];
                 const bool dead = i >= it.sp.Lq || sum == 0.f;
-                const float lse = dead ? -INFINITY : sh->m[c] * p.scale + logf(sum);
+                const float lse = dead ? -INFINITY : sh->m[c] * kLn2 + logf(sum);
                 const int64_t h = (int64_t)it.kvh * p.group + hg;
                 const bool exists = c < p.qbox * p.hbox && hg < p.group && i < p.nq;
                 sh->f[c] = dead ? 0.f : 1.f / sum;

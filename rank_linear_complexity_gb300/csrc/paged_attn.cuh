@@ -18,7 +18,7 @@ using sattn::Span;
 
 constexpr int kMaxSeqs = 512;  // sequences of a launch
 constexpr int kMinRun = 1;     // blocks of a CTA at least
-constexpr float kOutgrown = 16.f, kLog2e = 1.4426950408889634f;
+constexpr float kOutgrown = 16.f, kLog2e = 1.4426950408889634f, kLn2 = 0.6931471805599453f;
 
 struct AttnParams {
     const int32_t *q_lengths, *k_lengths, *table;
