@@ -426,17 +426,23 @@ paged_attn_kernel(const __grid_constant__ CUtensorMap tQ, const __grid_constant_
                 __syncwarp();
                 if (lane == 0) mbar_arrive(&sh->p_full[b]);
             }
-            // O / l out of tensor memory, a row of O^T an element of d
+            // O / l out of tensor memory, where a thread has an element of every row, and through the
+            // buffers of P, a row a warp, to memory (in a short loop: at a CTA's end its instructions come
+            // from far, and a store a column in line took 2.6 us)
             reduce_to(l, part, lane, [](float a, float z) { return a + z; });
             ok = ok && product(n - 1, 132);
-            if (!agree()) break;
+            // (both groups: each stores over what the other may still write as P)
+            if (!(ok = named_barrier_and(3, 256, ok))) break;
             tc_fence_after();
             uint32_t o[C];
-            const bool stores = key0 - lane < p.d;  // (of the warp)
-            if (stores) tmem_load(tO, o);
+            tmem_load(tO, o);
             tc_fence_before();
             __syncwarp();
             if (lane == 0) mbar_arrive(&sh->o_free);
+            float *stage = reinterpret_cast<float *>(smem + L::kP) + c0 * DP;
+            if (key0 < DP)
+#pragma unroll
+                for (int c = 0; c < C; ++c) stage[c * DP + key0] = __uint_as_float(o[c]);
             if (key0 < C) {
                 const int c = c0 + key0, i = r.q0 + (c & (p.qbox - 1)), hg = r.h0 + c / p.qbox;
                 float sum = 0.f;
@@ -452,16 +458,29 @@ paged_attn_kernel(const __grid_constant__ CUtensorMap tQ, const __grid_constant_
                 else if (exists) p.lse[(it.seq * (int64_t)p.hq + h) * p.nq + i] = lse;
             }
             named_barrier_sync(1 + w, 128);
-            if (stores && key0 < p.d) {
+            constexpr int E = DP / 32;  // elements of a lane
+#pragma unroll 1
+            for (int x = warp & 3; x < C; x += 4) {
+                const int64_t at = sh->row[c0 + x];
+                if (at < 0 || lane * E >= p.d) continue;
+                const float f = sh->f[c0 + x];
+                float y[E];
 #pragma unroll
-                for (int c = 0; c < C; ++c) {
-                    const int64_t at = sh->row[c0 + c];
-                    if (at < 0) continue;
-                    const float f = sh->f[c0 + c], y = f == 0.f ? 0.f : __uint_as_float(o[c]) * f;
-                    if (it.slot >= 0) p.part_o[at + key0] = y;
-                    else p.out[at + key0] = __float2bfloat16_rn(y);
+                for (int e = 0; e < E; ++e) {
+                    y[e] = stage[x * DP + lane * E + e];
+                    y[e] = f == 0.f ? 0.f : y[e] * f;
+                }
+                if (it.slot >= 0) {
+#pragma unroll
+                    for (int e = 0; e < E; e += 2)
+                        *reinterpret_cast<float2 *>(p.part_o + at + lane * E + e) = make_float2(y[e], y[e + 1]);
+                } else {
+#pragma unroll
+                    for (int e = 0; e < E; e += 2)
+                        *reinterpret_cast<uint32_t *>(p.out + at + lane * E + e) = pack2(y[e], y[e + 1]);
                 }
             }
+            named_barrier_sync(3, 256);
         }
     }
     tc_fence_before();
