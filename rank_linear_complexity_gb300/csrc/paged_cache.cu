@@ -3,8 +3,8 @@
 // append: the new rows of each sequence go to the rows of the cache that follow its `start`,
 // keys turned to their positions, and the queries that stand at the same positions are turned
 // beside them (the turn of rotary.cu, formed in fp32 and rounded once).  Bound by memory: every
-// element read and written once.  A thread keeps the sines of its pairs and goes through several
-// heads with them, loading kBatch of them before it stores the first.
+// element read and written once (8 x 4096 ragged rows of 32 + 8 + 8 heads of 128, bf16: 129 us, 5.5
+// TB/s).  A thread keeps the sines of its pairs and goes through several heads with them.
 //
 // keep: of a tree of drafted tokens, the rows of the accepted ones move up behind the sequence's
 // start.  A thread moves one piece of every row, in order, so that no other thread's store can
@@ -27,7 +27,10 @@ using rotary::to_float;
 using rotary::Vec;
 
 constexpr int kThreads = 128;
-constexpr int kBatch = 4;      // heads in flight
+// Heads of a thread in flight, and blocks of an SM: registers for 32 warps (8 x 4096 ragged rows of 32 + 8
+// + 8 heads of 128: 129 us; one head 155, four heads and the registers that they take 158, in 80
+// registers 212; 40 warps 160).
+constexpr int kBatch = 2, kBlocks = 8;
 constexpr int kMaxHeads = 16;  // heads of one thread
 
 struct AppendParams {
@@ -46,7 +49,7 @@ struct AppendParams {
 
 // V pairs a thread (V = 1: any strides and sizes; otherwise 16-byte pieces).
 template <typename T, int V, bool kInterleaved>
-__global__ void __launch_bounds__(kThreads) append_kernel(const AppendParams p) {
+__global__ void __launch_bounds__(kThreads, kBlocks) append_kernel(const AppendParams p) {
     using Piece = Vec<T, V>;
     const int64_t tid = (int64_t)blockIdx.x * kThreads + threadIdx.x;
     if (tid >= p.threads) return;
@@ -75,43 +78,47 @@ __global__ void __launch_bounds__(kThreads) append_kernel(const AppendParams p) 
             sn[v] *= p.amplitude;
         }
     }
-    for (int h = h0; h < h1; h += kBatch) {
-        Piece u0[kBatch], u1[kBatch];
-        T *to[kBatch];
+    // The thread's heads among `heads` of one tensor, the first of which is head `base` of all.
+    auto move = [&](const void *from, const Strides &sx, void *to, const Strides &sy, int64_t at_y, int base, int heads,
+                    bool turned) {
+        const int first = max(h0 - base, 0), last = min(h1 - base, heads);
+        const T *x = static_cast<const T *>(from) + b * sx.b + i * sx.n + first * sx.h;
+        T *y = static_cast<T *>(to) + at_y + first * sy.h;
+        for (int h = first; h < last; h += kBatch, x += kBatch * sx.h, y += kBatch * sy.h) {
+            Piece u0[kBatch], u1[kBatch];
 #pragma unroll
-        for (int k = 0; k < kBatch; ++k) {
-            const int hh = h + k;
-            const int w = hh < p.hq ? 0 : hh < p.hq + p.hk ? 1 : 2;
-            const int head = hh - (w == 0 ? 0 : w == 1 ? p.hq : p.hq + p.hk);
-            to[k] = nullptr;
-            if (hh >= h1 || (w && !kept)) continue;
-            const T *x = static_cast<const T *>(p.x[w]) + b * p.sx[w].b + head * p.sx[w].h + i * p.sx[w].n;
-            const Strides &s = w == 0 ? p.sy : w == 1 ? p.cache.sk : p.cache.sv;
-            to[k] = static_cast<T *>(w == 0 ? p.y : w == 1 ? p.cache.k : p.cache.v) +
-                    (w == 0 ? b * s.b + head * s.h + i * s.n : page * s.b + head * s.h + row * s.n);
-            u0[k] = *reinterpret_cast<const Piece *>(x + at0);
-            if (turn) u1[k] = *reinterpret_cast<const Piece *>(x + at1);
-        }
-#pragma unroll
-        for (int k = 0; k < kBatch; ++k) {
-            if (!to[k]) continue;
-            if (turn) {
-                if (h + k < p.hq + p.hk) {
-#pragma unroll
-                    for (int v = 0; v < V; ++v) {
-                        // interleaved: elements 2 v and 2 v + 1 of the two pieces in a row
-                        T &a = kInterleaved ? (2 * v < V ? u0[k].e[(2 * v) % V] : u1[k].e[(2 * v) % V]) : u0[k].e[v];
-                        T &z = kInterleaved ? (2 * v + 1 < V ? u0[k].e[(2 * v + 1) % V] : u1[k].e[(2 * v + 1) % V])
-                                            : u1[k].e[v];
-                        const float fa = to_float(a), fz = to_float(z);
-                        a = from_float<T>(fa * cs[v] - fz * sn[v]);
-                        z = from_float<T>(fz * cs[v] + fa * sn[v]);
-                    }
-                }
-                *reinterpret_cast<Piece *>(to[k] + at1) = u1[k];
+            for (int k = 0; k < kBatch; ++k) {
+                if (h + k >= last) continue;
+                u0[k] = *reinterpret_cast<const Piece *>(x + k * sx.h + at0);
+                if (turn) u1[k] = *reinterpret_cast<const Piece *>(x + k * sx.h + at1);
             }
-            *reinterpret_cast<Piece *>(to[k] + at0) = u0[k];
+#pragma unroll
+            for (int k = 0; k < kBatch; ++k) {
+                if (h + k >= last) continue;
+                if (turn) {
+                    if (turned) {
+#pragma unroll
+                        for (int v = 0; v < V; ++v) {
+                            // interleaved: elements 2 v and 2 v + 1 of the two pieces in a row
+                            T &a = kInterleaved ? (2 * v < V ? u0[k].e[(2 * v) % V] : u1[k].e[(2 * v) % V]) : u0[k].e[v];
+                            T &z = kInterleaved ? (2 * v + 1 < V ? u0[k].e[(2 * v + 1) % V] : u1[k].e[(2 * v + 1) % V])
+                                                : u1[k].e[v];
+                            const float fa = to_float(a), fz = to_float(z);
+                            a = from_float<T>(fa * cs[v] - fz * sn[v]);
+                            z = from_float<T>(fz * cs[v] + fa * sn[v]);
+                        }
+                    }
+                    *reinterpret_cast<Piece *>(y + k * sy.h + at1) = u1[k];
+                }
+                *reinterpret_cast<Piece *>(y + k * sy.h + at0) = u0[k];
+            }
         }
+    };
+    if (h0 < p.hq) move(p.x[0], p.sx[0], p.y, p.sy, b * p.sy.b + i * p.sy.n, 0, p.hq, true);
+    if (kept) {
+        const Cache &c = p.cache;
+        if (h0 < p.hq + p.hk) move(p.x[1], p.sx[1], c.k, c.sk, page * c.sk.b + row * c.sk.n, p.hq, p.hk, true);
+        move(p.x[2], p.sx[2], c.v, c.sv, page * c.sv.b + row * c.sv.n, p.hq + p.hk, p.hk, false);
     }
 }
 
@@ -140,31 +147,45 @@ __global__ void __launch_bounds__(kThreads) keep_kernel(const KeepParams p) {
     const int64_t start = __ldg(p.starts + b);
     const int count = p.counts ? min(max(__ldg(p.counts + b), 0), p.m) : p.m;
     const int32_t *path = p.path + (int64_t)b * p.m;
-    constexpr int kRows = 8;  // rows in flight: sources of later rows lie behind all their targets
+    // Rows in flight, each step for all of them before the next, so that a batch waits once for the
+    // path, the table and the rows (64 sequences, 8 heads of 128, up to 16 rows: 7.6 us row by row).
+    // Sources of later rows lie behind all targets before them.
+    constexpr int kRows = 8;
+    const int32_t *table = p.cache.table + (int64_t)b * p.cache.width;
+    int bad = 0;
     for (int i = 0; i < count; i += kRows) {
         Piece u[kRows];
-        T *to[kRows];
+        int node[kRows], from[kRows], to[kRows];
+#pragma unroll
+        for (int k = 0; k < kRows; ++k) node[k] = i + k < count ? __ldg(path + i + k) : i + k;
+        auto page_at = [&](int64_t at, bool wanted) {
+            const int64_t entry = at >> p.cache.shift;
+            if (!wanted) return -2;
+            return at >= 0 && entry < p.cache.width ? __ldg(table + entry) : -1;
+        };
 #pragma unroll
         for (int k = 0; k < kRows; ++k) {
-            to[k] = nullptr;
-            if (i + k >= count) continue;
-            const int node = __ldg(path + i + k);
-            if (node == i + k) continue;  // in its place
-            int page, row, page2, row2;
-            if (node < i + k) {
-                if (p.status) atomicExch(p.status, kBadPath);
+            const bool moves = node[k] > i + k;  // (a node in its place stays)
+            from[k] = page_at(start + node[k], moves);
+            to[k] = page_at(start + i + k, moves);
+            if (node[k] < i + k) bad = kBadPath;
+        }
+#pragma unroll
+        for (int k = 0; k < kRows; ++k) {
+            const bool there = (unsigned)from[k] < (unsigned)p.cache.pages && (unsigned)to[k] < (unsigned)p.cache.pages;
+            if (!there) {
+                if (from[k] != -2) bad = kBadPage;
+                to[k] = -1;
                 continue;
             }
-            if (!find_row(p.cache, b, start + i + k, p.status, page, row) ||
-                !find_row(p.cache, b, start + node, p.status, page2, row2))
-                continue;
-            to[k] = base + page * s.b + row * s.n;
-            u[k] = *reinterpret_cast<const Piece *>(base + page2 * s.b + row2 * s.n);
+            u[k] = *reinterpret_cast<const Piece *>(base + from[k] * s.b + ((int)(start + node[k]) & (p.cache.page - 1)) * s.n);
         }
 #pragma unroll
         for (int k = 0; k < kRows; ++k)
-            if (to[k]) *reinterpret_cast<Piece *>(to[k]) = u[k];
+            if (to[k] >= 0)
+                *reinterpret_cast<Piece *>(base + to[k] * s.b + ((int)(start + i + k) & (p.cache.page - 1)) * s.n) = u[k];
     }
+    if (bad && p.status) atomicExch(p.status, bad);
 }
 
 // A sequence a block, a node a thread: its ancestors come in falling order, so their bits are

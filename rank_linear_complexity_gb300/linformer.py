@@ -379,12 +379,13 @@ def _stream_of(device, *tensors):
     `device`."""
     if device.type != "cuda":
         raise ValueError(f"CUDA tensors are needed, got {device}")
+    index = device.index
     for t in tensors:
-        if t is not None and t.device != device:
+        if t is not None and t.get_device() != index:
             raise ValueError(f"tensors on {device} and {t.device}")
     import torch
     try:
-        return torch._C._cuda_getCurrentRawStream(device.index)
+        return torch._C._cuda_getCurrentRawStream(index)
     except AttributeError:  # a private name
         return torch.cuda.current_stream(device).cuda_stream
 
@@ -602,13 +603,26 @@ def _check_cache(k_cache, v_cache, table, b, hk, d, dtype):
     pages, heads, page, dim = shape
     if heads != hk or dim != d or k_cache.dtype != dtype:
         _check("k_cache", k_cache, (pages, hk, page, d), dtype)
-    _check("v_cache", v_cache, shape, dtype)
+    if v_cache.shape != shape or v_cache.dtype != dtype:
+        _check("v_cache", v_cache, shape, dtype)
     width = table.shape[-1]
-    _check_dense("table", table, (b, width), torch.int32)
-    if pages > 0x7fffffff or page > 0x7fffffff or width > 0x7fffffff:
+    if table.shape != (b, width) or table.dtype != torch.int32 or not table.is_contiguous():
+        _check_dense("table", table, (b, width), torch.int32)
+    # (a size past 32 bits comes with as many elements, or with a size of zero, which is refused)
+    if k_cache.numel() > 0x7fffffff or width > 0x7fffffff:
         _sizes("k_cache", shape)
         _sizes("table", table.shape)
     return pages, page, width
+
+
+def _int32s(name, x, shape):
+    """Address of a dense int32 tensor, None for None."""
+    import torch
+    if x is None:
+        return None
+    if x.shape != shape or x.dtype != torch.int32 or not x.is_contiguous():
+        _check_dense(name, x, shape, torch.int32)
+    return x.data_ptr()
 
 
 def cache_append(K, V, k_cache, v_cache, table, starts, counts=None, Q=None, phase=None,
@@ -625,22 +639,17 @@ def cache_append(K, V, k_cache, v_cache, table, starts, counts=None, Q=None, pha
                                 rot, layout, amplitude, out)
     shape, dtype, device = K.shape, K.dtype, K.device
     b, hk, n, d = shape
-    _sizes("K", shape)
+    if K.numel() > 0x7fffffff:
+        _sizes("K", shape)
     handle = _stream_of(device, V, k_cache, v_cache, table, starts, counts, Q, phase, positions, out)
-    _check("V", V, shape, dtype)
+    if V.shape != shape or V.dtype != dtype:
+        _check("V", V, shape, dtype)
     pages, page, width = _check_cache(k_cache, v_cache, table, b, hk, d, dtype)
-    _check_dense("starts", starts, (b,), torch.int32)
-    if counts is not None:
-        _check_dense("counts", counts, (b,), torch.int32)
-        counts = counts.data_ptr()
     if phase is not None:
         rot = d if rot is None else _int32("rot", rot)
         _int32("layout", layout)
         _check_dense("phase", phase, (rot // 2,), torch.int64)
         phase = phase.data_ptr()
-        if positions is not None:
-            _check_dense("positions", positions, (b, n), torch.int32)
-            positions = positions.data_ptr()
     elif Q is not None or positions is not None or rot is not None:
         raise ValueError("phase: the table of rotary_phase() is needed to turn keys and queries")
     else:
@@ -648,20 +657,24 @@ def cache_append(K, V, k_cache, v_cache, table, starts, counts=None, Q=None, pha
     pq = sq = py = sy = None
     hq = 0
     if Q is not None:
-        hq = _int32("Q's heads", Q.shape[1])
-        _check("Q", Q, (b, hq, n, d), dtype)
+        turned = Q.shape
+        hq = turned[1]
+        if turned != (b, hq, n, d) or Q.dtype != dtype:
+            _check("Q", Q, (b, hq, n, d), dtype)
+        _int32("Q's heads", hq)
         if out is None:
             out = torch.empty_like(Q)
-        else:
-            _check("out", out, Q.shape, dtype)
+        elif out.shape != turned or out.dtype != dtype:
+            _check("out", out, turned, dtype)
         pq, sq, py, sy = Q.data_ptr(), _strides(Q), out.data_ptr(), _strides(out)
     elif out is not None:
         raise ValueError("out: Q is needed")
     _call(lib().linformer_cache_append, device,
           (K.data_ptr(), _strides(K), V.data_ptr(), _strides(V), k_cache.data_ptr(),
            _strides(k_cache), v_cache.data_ptr(), _strides(v_cache), pq, sq, py, sy,
-           table.data_ptr(), starts.data_ptr(), counts, phase, positions, b, hq, hk, n, d, pages,
-           page, width, rot, layout, amplitude, dtype_code(K), handle),
+           table.data_ptr(), _int32s("starts", starts, (b,)), _int32s("counts", counts, (b,)), phase,
+           _int32s("positions", positions, (b, n)), b, hq, hk, n, d, pages, page, width, rot, layout,
+           amplitude, dtype_code(K), handle),
           "linformer_cache_append")
     return out
 
@@ -676,19 +689,15 @@ def cache_keep(k_cache, v_cache, table, starts, path, counts=None, stream=None):
     device, dtype = k_cache.device, k_cache.dtype
     _, hk, _, d = k_cache.shape
     b, m = path.shape
-    _sizes("path", path.shape)
+    if path.numel() > 0x7fffffff:
+        _sizes("path", path.shape)
     handle = _stream_of(device, v_cache, table, starts, path, counts)
-    _sizes("k_cache", k_cache.shape)
     pages, page, width = _check_cache(k_cache, v_cache, table, b, hk, d, dtype)
-    _check_dense("starts", starts, (b,), torch.int32)
-    _check_dense("path", path, (b, m), torch.int32)
-    if counts is not None:
-        _check_dense("counts", counts, (b,), torch.int32)
-        counts = counts.data_ptr()
     _call(lib().linformer_cache_keep, device,
           (k_cache.data_ptr(), _strides(k_cache), v_cache.data_ptr(), _strides(v_cache),
-           table.data_ptr(), starts.data_ptr(), path.data_ptr(), counts, b, hk, m, d, pages, page,
-           width, dtype_code(k_cache), handle),
+           table.data_ptr(), _int32s("starts", starts, (b,)), _int32s("path", path, (b, m)),
+           _int32s("counts", counts, (b,)), b, hk, m, d, pages, page, width, dtype_code(k_cache),
+           handle),
           "linformer_cache_keep")
 
 
@@ -699,31 +708,30 @@ def _over_pages(Q, k_cache, v_cache, table, k_lengths, q_lengths, scale, out, ls
     import torch
     shape, dtype, device = Q.shape, Q.dtype, Q.device
     b, hq, n, d = shape
-    _sizes("Q", shape)
+    if Q.numel() > 0x7fffffff:
+        _sizes("Q", shape)
     handle = _stream_of(device, k_cache, v_cache, table, k_lengths, q_lengths, out, lse, mask)
     hk = _int32("k_cache's heads", k_cache.shape[1])
     pages, page, width = _check_cache(k_cache, v_cache, table, b, hk, d, dtype)
     if out is None:
         out = torch.empty(shape, dtype=dtype, device=device)
-    else:
+    elif out.shape != shape or out.dtype != dtype:
         _check("out", out, shape, dtype)
     if lse is None:
         lse = torch.empty((b, hq, n), dtype=torch.float32, device=device)
     else:
         _check_dense("lse", lse, (b, hq, n), torch.float32)
-    _check_dense("k_lengths", k_lengths, (b,), torch.int32)
-    if q_lengths is not None:
-        _check_dense("q_lengths", q_lengths, (b,), torch.int32)
-        q_lengths = q_lengths.data_ptr()
-    head = (Q.data_ptr(), _strides(Q), k_cache.data_ptr(), _strides(k_cache), v_cache.data_ptr(),
-            _strides(v_cache), out.data_ptr(), _strides(out), lse.data_ptr(), table.data_ptr(),
-            k_lengths.data_ptr(), q_lengths)
     if mask is not None:
         _check_dense("mask", mask, (b, n, (n + 63) // 64), torch.int64)
-        head += (mask.data_ptr(),)
+        mask = (mask.data_ptr(),)
+    if k_lengths is None:
+        raise ValueError("k_lengths: the rows of each sequence are needed")
     _call(call, device,
-          head + (b, hq, hk, n, d, pages, page, width, d ** -0.5 if scale is None else scale)
-          + masks + (dtype_code(Q), handle), name)
+          (Q.data_ptr(), _strides(Q), k_cache.data_ptr(), _strides(k_cache), v_cache.data_ptr(),
+           _strides(v_cache), out.data_ptr(), _strides(out), lse.data_ptr(), table.data_ptr(),
+           _int32s("k_lengths", k_lengths, (b,)), _int32s("q_lengths", q_lengths, (b,)),
+           *(mask or ()), b, hq, hk, n, d, pages, page, width,
+           d ** -0.5 if scale is None else scale, *masks, dtype_code(Q), handle), name)
     return out, lse
 
 
