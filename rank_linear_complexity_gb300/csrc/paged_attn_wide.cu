@@ -38,7 +38,9 @@ constexpr int kReaders = 1 + 2 + 8;  // load warp, issuing threads, softmax warp
 struct Shared {
     uint64_t full[8], empty[8], q_full[2], q_free[2], s_full[2], s_free[2], p_full[2], p_half[2], pv_done[2],
         o_free[2], drain[2], told[kAhead], taken[kAhead];
-    Item items[kAhead];  // (in shared memory: the softmax has no registers to spare for a walk)
+    struct Told : Item {
+        int before;  // blocks of the items before it
+    } items[kAhead];  // (in shared memory: the softmax has no registers to spare for a walk)
     uint32_t tmem;
     int abort;
     int pages[kTile / 8];
@@ -147,7 +149,7 @@ paged_wide_kernel(const __grid_constant__ CUtensorMap tQ, const __grid_constant_
             };
             for (int k = 0; ok; ++k) {
                 if (!spin(&sh->told[k % kAhead], (k / kAhead) & 1, 153)) break;
-                const Item &it = sh->items[k % kAhead];
+                const auto &it = sh->items[k % kAhead];
                 if (it.seq < 0) break;
                 for (int t = 0; t < 2 && ok; ++t) {
                     const Part x(p, it, t);
@@ -204,13 +206,15 @@ paged_wide_kernel(const __grid_constant__ CUtensorMap tQ, const __grid_constant_
             if (elect_one()) {
                 Walk walk(p, sh->marks, blockIdx.x);
                 const Walk begin = walk;
-                Item it;
+                Shared::Told it;
+                it.before = 0;
                 for (int k = 0;; ++k) {
                     const int s = k % kAhead;
                     const bool more = walk.next(p, sh->marks, it);
                     if (!more) it.seq = -1;
                     if (k >= kAhead && !thread_spin(&sh->taken[s], (k / kAhead - 1) & 1, p.status, 156, abort_flag)) break;
                     sh->items[s] = it;
+                    if (more) it.before += it.hi - it.lo;
                     mbar_arrive(&sh->told[s]);
                     if (k == 0) write_cut(p, begin, sh->marks.first[p.b]);
                     if (!more) break;
@@ -324,7 +328,7 @@ paged_wide_kernel(const __grid_constant__ CUtensorMap tQ, const __grid_constant_
                        tO = tmem + L::kO + DP * t + lanes;
         const float sl = p.scale_log2;
         const int qi = row & (p.qbox - 1), head = row / p.qbox;  // position and head within the tile
-        int n = 0, before = 0;  // the tile's blocks, and those of the items before this one
+        int n = 0;  // the tile's blocks
         bool ok = true;
         // P.V of the tile's block before this one is done: P may be written over, O rescaled
         auto last_product = [&](bool any) {
@@ -336,22 +340,20 @@ paged_wide_kernel(const __grid_constant__ CUtensorMap tQ, const __grid_constant_
         };
         for (int k = 0;; ++k) {
             if (!warp_spin(&sh->told[k % kAhead], (k / kAhead) & 1, p.status, 155, abort_flag)) break;
-            const Item &it = sh->items[k % kAhead];
+            const auto &it = sh->items[k % kAhead];
             if (it.seq < 0) break;
-            int xlo, xhi, first, end, node0;
-            bool valid, warp_valid;
-            const int base = before - it.lo, Lk = it.sp.Lk;
-            before += it.hi - it.lo;
+            // [clean_lo, clean_hi): blocks that every row of the tile sees all of
+            int xlo, xhi, clean_lo, clean_hi;
+            bool warp_valid;
             {
                 const Part x(p, it, t);
                 const int i = x.q0 + qi;
                 xlo = x.lo;
                 xhi = x.hi;
-                valid = x.live && head < p.hbox && x.h0 + head < p.group && i < it.sp.Lq;
-                warp_valid = __any_sync(0xffffffffu, valid);
-                first = valid ? it.sp.first(i) : 0;
-                end = valid ? it.sp.end(i) : (1 << 30);
-                node0 = p.mask ? Lk - it.sp.Lq : 1 << 30;  // where the tree begins
+                warp_valid = __any_sync(0xffffffffu, x.live && head < p.hbox && x.h0 + head < p.group && i < it.sp.Lq);
+                const int end = min(it.sp.end(x.q0), p.mask ? it.sp.Lk - it.sp.Lq : it.sp.Lk);
+                clean_hi = max(end, 0) / kTile;
+                clean_lo = (it.sp.first(max(min(x.q0 + p.qbox, it.sp.Lq) - 1, 0)) + kTile - 1) / kTile;
             }
             float m = -INFINITY, l = 0.f;  // reference (of the raw scores), sum of 2^((s - m) sl)
             for (int j = xlo; j < xhi; ++j, ++n) {
@@ -360,17 +362,17 @@ paged_wide_kernel(const __grid_constant__ CUtensorMap tQ, const __grid_constant_
                     break;
                 }
                 tc_fence_after();
-                const int k0 = j * kTile;
-                if (k0 + kTile > Lk) {
+                const bool clean = j >= clean_lo && j < clean_hi;
+                if (!clean && (j + 1) * kTile > it.sp.Lk) {
                     // rows of V past the length may hold anything: P is 0 there, but 0 x NaN is not
                     // (both tiles' threads write the zeros; a product that reads them by then needs
                     // no others)
-                    const int v = 2 * (base + j) + 1, s = v % L::kStages;
+                    const int v = 2 * (it.before + j - it.lo) + 1, s = v % L::kStages;
                     if (!warp_spin(&sh->full[s], (v / L::kStages) & 1, p.status, 151, abort_flag)) {
                         ok = false;
                         break;
                     }
-                    if (k0 + row >= Lk) {
+                    if (j * kTile + row >= it.sp.Lk) {
                         uint8_t *at = sKV + s * L::kTileBytes + row * 128;
 #pragma unroll 1
                         for (int y = 0; y < DP / 8; ++y)
@@ -388,13 +390,18 @@ paged_wide_kernel(const __grid_constant__ CUtensorMap tQ, const __grid_constant_
                     if (lane == 0) mbar_arrive(&sh->p_full[t]);
                     continue;
                 }
-                // Masked keys (whatever they hold) become -inf in place, out of line: the few blocks at
-                // a mask's edge must not widen the code of the others.
-                if (__any_sync(0xffffffffu, first > k0 || end < k0 + kTile))
-                    sattn::mask_block(tS, first - k0, first < end ? end - first : 0);
-                if (k0 + kTile > node0) {
-                    const int64_t r = (int64_t)it.seq * p.nq + Part(p, it, t).q0 + qi;
-                    mask_nodes(tS, k0 - node0, valid ? p.mask + r * p.words : nullptr, p.words);
+                if (!clean) {
+                    // Masked keys (whatever they hold) become -inf in place, out of line: the few blocks
+                    // at a mask's edge must not widen the code of the others.
+                    const Part x(p, it, t);
+                    const int k0 = j * kTile, i = x.q0 + qi, node0 = it.sp.Lk - it.sp.Lq;
+                    const bool valid = head < p.hbox && x.h0 + head < p.group && i < it.sp.Lq;
+                    const int first = valid ? it.sp.first(i) : 0, end = valid ? it.sp.end(i) : (1 << 30);
+                    if (__any_sync(0xffffffffu, first > k0 || end < k0 + kTile))
+                        sattn::mask_block(tS, first - k0, first < end ? end - first : 0);
+                    if (p.mask && k0 + kTile > node0)
+                        mask_nodes(tS, k0 - node0, valid ? p.mask + ((int64_t)it.seq * p.nq + i) * p.words : nullptr,
+                                   p.words);
                 }
                 uint32_t v[4][32];
 #pragma unroll
@@ -410,7 +417,7 @@ paged_wide_kernel(const __grid_constant__ CUtensorMap tQ, const __grid_constant_
                 }
                 const float mx = fmaxf(fmaxf(sattn::max_chunk(v[0]), sattn::max_chunk(v[1])),
                                        fmaxf(sattn::max_chunk(v[2]), sattn::max_chunk(v[3])));
-                if (__any_sync(0xffffffffu, valid && (mx - m) * sl > kOutgrown)) {
+                if (__any_sync(0xffffffffu, (mx - m) * sl > kOutgrown)) {
                     if (!last_product(j > xlo)) break;
                     const float mn = fmaxf(m, mx);
                     const float f = mn == -INFINITY ? 1.f : ex2_approx((m - mn) * sl);
@@ -450,11 +457,11 @@ paged_wide_kernel(const __grid_constant__ CUtensorMap tQ, const __grid_constant_
             }
             if (!ok) break;
             // O / l out of tensor memory; rows without keys give O = 0 and lse = -inf
-            const bool dead = !valid || l == 0.f, some = xhi > xlo, whole = it.slot < 0;
-            const float inv = dead ? 0.f : 1.f / l;
             const Part x(p, it, t);
             const int i = x.q0 + qi, hg = x.h0 + head;
             const bool exists = x.live && head < p.hbox && hg < p.group && i < p.nq;
+            const bool dead = !exists || i >= it.sp.Lq || l == 0.f, some = xhi > xlo, whole = it.slot < 0;
+            const float inv = dead ? 0.f : 1.f / l;
             const int64_t h = (int64_t)it.kvh * p.group + hg, pr = ((int64_t)it.slot * 2 + t) * kTile + row;
             __nv_bfloat16 *dst = p.out + it.seq * p.so.b + h * p.so.h + (int64_t)i * p.so.n;
             if (some) {
