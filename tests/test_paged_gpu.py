@@ -356,6 +356,16 @@ def test_many_sequences():
     check_attention(b=150, k_lengths=lengths, nq=3, hq=2, hk=2, page=8)
 
 
+@pytest.mark.parametrize("kw", [dict(nq=1, hq=4, hk=4), dict(nq=1, hq=8, hk=4, d=128, layout="heads"),
+                                dict(nq=12, hq=16, hk=4, d=40), dict(nq=40, hq=8, hk=4),
+                                dict(nq=3, hq=4, hk=4, causal=False)])
+def test_long_lists(kw):
+    """Hundreds of blocks a CTA, units cut in the middle."""
+    lengths = (40000, 1, 31234, 0, 36000, 29999, 33333, 35000, 38000, 12345)
+    out = [check_attention(b=10, page=128, k_lengths=lengths, **kw) for _ in range(2)]
+    assert torch.equal(bits(out[0][0]), bits(out[1][0])) and torch.equal(out[0][1], out[1][1])
+
+
 def test_pages_that_are_not_there():
     """They count as rows of zeros, are recorded, and nothing outside the cache is read."""
     for nq, bad in ((1, 99), (1, -1), (40, 2 ** 31 - 1), (300, -7)):
