@@ -151,23 +151,28 @@ paged_wide_kernel(const __grid_constant__ CUtensorMap tQ, const __grid_constant_
                 if (!spin(&sh->told[k % kAhead], (k / kAhead) & 1, 153)) break;
                 const auto &it = sh->items[k % kAhead];
                 if (it.seq < 0) break;
-                for (int t = 0; t < 2 && ok; ++t) {
-                    const Part x(p, it, t);
-                    if (x.hi <= x.lo) continue;
-                    ok = nq[t] == 0 || spin(&sh->q_free[t], (nq[t] - 1) & 1, 140);
-                    if (!ok) break;
-                    if (lane == 0) {
-                        mbar_arrive_expect_tx(&sh->q_full[t], (uint32_t)(p.qbox * p.hbox * DP * 2));
-                        for (int h = 0; h < DP / 64; ++h)
-                            tma_load_5d(sQ + t * L::kTileBytes + h * 16384, &tQ, &sh->q_full[t], h * 64, x.q0, x.h0,
-                                        it.kvh, it.seq);
+                // The first item's Q before its keys, the others' after their first block's: the last
+                // item's scores may still need theirs, and the keys are not to wait for that.
+                auto load_q = [&] {
+                    for (int t = 0; t < 2 && ok; ++t) {
+                        const Part x(p, it, t);
+                        if (x.hi <= x.lo) continue;
+                        ok = nq[t] == 0 || spin(&sh->q_free[t], (nq[t] - 1) & 1, 140);
+                        if (!ok) break;
+                        if (lane == 0) {
+                            mbar_arrive_expect_tx(&sh->q_full[t], (uint32_t)(p.qbox * p.hbox * DP * 2));
+                            for (int h = 0; h < DP / 64; ++h)
+                                tma_load_5d(sQ + t * L::kTileBytes + h * 16384, &tQ, &sh->q_full[t], h * 64, x.q0, x.h0,
+                                            it.kvh, it.seq);
+                        }
+                        ++nq[t];
                     }
-                    ++nq[t];
-                }
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive(&sh->taken[k % kAhead]);
+                };
                 const int32_t *table = p.table + (int64_t)it.seq * p.width;
                 const int lo = it.lo, hi = it.hi, kvh = it.kvh, Lk = it.sp.Lk;
-                __syncwarp();
-                if (lane == 0) mbar_arrive(&sh->taken[k % kAhead]);
+                if (k == 0) load_q();
                 int page = mine ? page_of(p, table, lo, row, Lk) : 0;
                 for (int j = lo; j < hi && ok; ++j) {
                     const int now = page, at = (j * kTile) & (p.page - 1);  // (0 where a block has several pages)
@@ -192,6 +197,7 @@ paged_wide_kernel(const __grid_constant__ CUtensorMap tQ, const __grid_constant_
                         }
                     }
                     ok = __shfl_sync(0xffffffffu, ok, 0);
+                    if (ok && j == lo && k > 0) load_q();
                 }
             }
             // no copy outlives the CTA
