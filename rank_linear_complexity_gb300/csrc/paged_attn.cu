@@ -13,8 +13,8 @@
 // and a thread has one key and N / 2 queries: what a length or a page hides is a thread's own
 // business, sums over keys stay in the thread until a row ends, and only a maximum that outgrows
 // its reference by 2^kOutgrown makes threads exchange anything but a vote (the reference is any m
-// near the maximum; P = 2^(s - m) is rounded to bf16, at most 2^-8 of each term, as the tensor cores
-// take it; sums and statistics are fp32).  Tiles of 128 keys come by TMA, a box a page, through a
+// near the maximum; P = 2^(s - m) goes to the tensor cores as bf16, in two parts where that is cheap,
+// else rounded, at most 2^-8 of each term; sums and statistics are fp32).  Tiles of 128 keys come by TMA, a box a page, through a
 // ring in shared memory.
 //
 // The blocks of 128 keys of all rows form one long list, sequence by sequence, and each CTA takes an
@@ -43,8 +43,13 @@ struct Layout {
     static constexpr bool kPair = DP == 64;
     static constexpr int kEntries = 5;
     static constexpr uint32_t kEntryBytes = kPair ? 2 * kTileBytes : kTileBytes;
-    static constexpr int kPBufs = 2;
-    static constexpr uint32_t kPBytes = kTile * 128;  // (rows of 64 columns)
+    // P in two parts of bf16 each, the rounded and the rest, as columns beside each other, where the
+    // products cost next to nothing (N = 16, 32: 1 % more time, and the result is off by its own rounding
+    // alone, 1.7e-3 against 2.3e-3; N = 64: 4 %, left at one).
+    static constexpr bool kSplit = N < 64;
+    static constexpr int kCols = kSplit ? 2 * N : N;  // of P and of O
+    static constexpr int kPBufs = kCols > 64 ? 1 : 2;
+    static constexpr uint32_t kPBytes = (kCols > 64 ? 2 : 1) * kTile * 128;  // (rows of 64 columns)
     static constexpr uint32_t kQHalf = N * 128, kQBytes = kQHalf * (DP / 64);
     static constexpr uint32_t kP = kEntries * kEntryBytes, kQ = kP + kPBufs * kPBytes, kEnd = kQ + kQBytes;
     static constexpr uint32_t kS = 0, kO = 2 * N;  // tensor memory: S, S, O
@@ -226,7 +231,7 @@ paged_attn_kernel(const __grid_constant__ CUtensorMap tQ, const __grid_constant_
         __syncwarp();
     } else if (warp == kMmaWarp) {
         if (elect_one()) {  // ---------------- products
-            const uint32_t idesc_s = idesc_f16(128, N, 1, 0, 0), idesc_o = idesc_f16(128, N, 1, 1, 1);
+            const uint32_t idesc_s = idesc_f16(128, N, 1, 0, 0), idesc_o = idesc_f16(128, L::kCols, 1, 1, 1);
             const uint64_t dq = sdesc(smem_u32(smem + L::kQ), 16, 1024, kSwizzle128B);
             int ns = 0, no = 0, items = 0;  // blocks whose S, whose O has been issued
             bool ok = true;
@@ -394,12 +399,14 @@ paged_attn_kernel(const __grid_constant__ CUtensorMap tQ, const __grid_constant_
                     if (j > it.lo) {
                         tc_fence_after();
 #pragma unroll 1
-                        for (int c = 0; c < C; c += 8) {
+                        for (int x = 0; x < (L::kSplit ? 2 : 1) * C; x += 8) {
+                            const int c = x % C;
+                            const uint32_t at = tO + c + (x < C ? 0 : N);
                             uint32_t q[8];
-                            tmem_ld8(tO + c, q);
+                            tmem_ld8(at, q);
 #pragma unroll
                             for (int e = 0; e < 8; ++e) q[e] = __float_as_uint(__uint_as_float(q[e]) * sh->f[c0 + c + e]);
-                            tmem_st8_async(tO + c, q);
+                            tmem_st8_async(at, q);
                         }
                         tmem_wait_st();
                         tc_fence_before();
@@ -415,9 +422,16 @@ paged_attn_kernel(const __grid_constant__ CUtensorMap tQ, const __grid_constant_
                 uint8_t *row = smem + L::kP + b * L::kPBytes + key0 * 128;
 #pragma unroll
                 for (int c = 0; c < C; c += 8) {
-                    *reinterpret_cast<uint4 *>(row + (((c0 + c) / 8 ^ (key0 & 7)) * 16)) =
-                        make_uint4(pack2(y[c], y[c + 1]), pack2(y[c + 2], y[c + 3]), pack2(y[c + 4], y[c + 5]),
-                                   pack2(y[c + 6], y[c + 7]));
+                    uint32_t hi[4], lo[4];
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) {
+                        const float a = y[c + 2 * e], z = y[c + 2 * e + 1];
+                        hi[e] = pack2(a, z);
+                        lo[e] = pack2(a - __uint_as_float(hi[e] << 16), z - __uint_as_float(hi[e] & 0xffff0000u));
+                    }
+                    auto at = [&](int col) { return row + col / 64 * 16384 + ((col % 64 / 8 ^ (key0 & 7)) * 16); };
+                    *reinterpret_cast<uint4 *>(at(c0 + c)) = make_uint4(hi[0], hi[1], hi[2], hi[3]);
+                    if (L::kSplit) *reinterpret_cast<uint4 *>(at(N + c0 + c)) = make_uint4(lo[0], lo[1], lo[2], lo[3]);
                 }
                 if (ragged && w == 0) {
                     // rows of V past the length may hold anything: P is 0 there, but 0 x NaN is not
@@ -444,6 +458,12 @@ paged_attn_kernel(const __grid_constant__ CUtensorMap tQ, const __grid_constant_
             tc_fence_after();
             uint32_t o[C];
             tmem_load(tO, o);
+            if (L::kSplit) {
+                uint32_t rest[C];
+                tmem_load(tO + N, rest);
+#pragma unroll
+                for (int c = 0; c < C; ++c) o[c] = __float_as_uint(__uint_as_float(o[c]) + __uint_as_float(rest[c]));
+            }
             tc_fence_before();
             __syncwarp();
             if (lane == 0) mbar_arrive(&sh->o_free);
