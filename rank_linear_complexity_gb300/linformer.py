@@ -596,18 +596,20 @@ def rotary(x, x2=None, phase=None, positions=None, start: int = 0, rot=None,
 # the pages of each sequence in order.  A page, path or tree on the device that is not there is
 # recorded in the device status word, as a wait that ran out is.
 
-def _check_cache(k_cache, v_cache, table, b, hk, d, dtype):
+# (torch's types are passed along: an import in each helper costs as much as its check)
+
+def _check_cache(k_cache, v_cache, table, b, hk, d, dtype, int32):
     """(pages, page, width) of a cache that fits the call's tensors."""
-    import torch
     shape = k_cache.shape
     pages, heads, page, dim = shape
     if heads != hk or dim != d or k_cache.dtype != dtype:
         _check("k_cache", k_cache, (pages, hk, page, d), dtype)
     if v_cache.shape != shape or v_cache.dtype != dtype:
         _check("v_cache", v_cache, shape, dtype)
-    width = table.shape[-1]
-    if table.shape != (b, width) or table.dtype != torch.int32 or not table.is_contiguous():
-        _check_dense("table", table, (b, width), torch.int32)
+    entries = table.shape
+    width = entries[-1]
+    if entries != (b, width) or table.dtype != int32 or not table.is_contiguous():
+        _check_dense("table", table, (b, width), int32)
     # (a size past 32 bits comes with as many elements, or with a size of zero, which is refused)
     if k_cache.numel() > 0x7fffffff or width > 0x7fffffff:
         _sizes("k_cache", shape)
@@ -615,13 +617,12 @@ def _check_cache(k_cache, v_cache, table, b, hk, d, dtype):
     return pages, page, width
 
 
-def _int32s(name, x, shape):
+def _int32s(name, x, shape, int32):
     """Address of a dense int32 tensor, None for None."""
-    import torch
     if x is None:
         return None
-    if x.shape != shape or x.dtype != torch.int32 or not x.is_contiguous():
-        _check_dense(name, x, shape, torch.int32)
+    if x.shape != shape or x.dtype != int32 or not x.is_contiguous():
+        _check_dense(name, x, shape, int32)
     return x.data_ptr()
 
 
@@ -637,18 +638,19 @@ def cache_append(K, V, k_cache, v_cache, table, starts, counts=None, Q=None, pha
         with _current_on(K.device, stream):
             return cache_append(K, V, k_cache, v_cache, table, starts, counts, Q, phase, positions,
                                 rot, layout, amplitude, out)
-    shape, dtype, device = K.shape, K.dtype, K.device
+    shape, dtype, device, int32 = K.shape, K.dtype, K.device, torch.int32
     b, hk, n, d = shape
     if K.numel() > 0x7fffffff:
         _sizes("K", shape)
     handle = _stream_of(device, V, k_cache, v_cache, table, starts, counts, Q, phase, positions, out)
     if V.shape != shape or V.dtype != dtype:
         _check("V", V, shape, dtype)
-    pages, page, width = _check_cache(k_cache, v_cache, table, b, hk, d, dtype)
+    pages, page, width = _check_cache(k_cache, v_cache, table, b, hk, d, dtype, int32)
     if phase is not None:
         rot = d if rot is None else _int32("rot", rot)
         _int32("layout", layout)
-        _check_dense("phase", phase, (rot // 2,), torch.int64)
+        if phase.shape != (rot // 2,) or phase.dtype != torch.int64 or not phase.is_contiguous():
+            _check_dense("phase", phase, (rot // 2,), torch.int64)
         phase = phase.data_ptr()
     elif Q is not None or positions is not None or rot is not None:
         raise ValueError("phase: the table of rotary_phase() is needed to turn keys and queries")
@@ -672,9 +674,9 @@ def cache_append(K, V, k_cache, v_cache, table, starts, counts=None, Q=None, pha
     _call(lib().linformer_cache_append, device,
           (K.data_ptr(), _strides(K), V.data_ptr(), _strides(V), k_cache.data_ptr(),
            _strides(k_cache), v_cache.data_ptr(), _strides(v_cache), pq, sq, py, sy,
-           table.data_ptr(), _int32s("starts", starts, (b,)), _int32s("counts", counts, (b,)), phase,
-           _int32s("positions", positions, (b, n)), b, hq, hk, n, d, pages, page, width, rot, layout,
-           amplitude, dtype_code(K), handle),
+           table.data_ptr(), _int32s("starts", starts, (b,), int32), _int32s("counts", counts, (b,), int32), phase,
+           _int32s("positions", positions, (b, n), int32), b, hq, hk, n, d, pages, page, width, rot, layout,
+           amplitude, BF16 if dtype is torch.bfloat16 else dtype_code(K), handle),
           "linformer_cache_append")
     return out
 
@@ -686,18 +688,18 @@ def cache_keep(k_cache, v_cache, table, starts, path, counts=None, stream=None):
     if stream is not None:
         with _current_on(k_cache.device, stream):
             return cache_keep(k_cache, v_cache, table, starts, path, counts)
-    device, dtype = k_cache.device, k_cache.dtype
+    device, dtype, int32 = k_cache.device, k_cache.dtype, torch.int32
     _, hk, _, d = k_cache.shape
     b, m = path.shape
     if path.numel() > 0x7fffffff:
         _sizes("path", path.shape)
     handle = _stream_of(device, v_cache, table, starts, path, counts)
-    pages, page, width = _check_cache(k_cache, v_cache, table, b, hk, d, dtype)
+    pages, page, width = _check_cache(k_cache, v_cache, table, b, hk, d, dtype, int32)
     _call(lib().linformer_cache_keep, device,
           (k_cache.data_ptr(), _strides(k_cache), v_cache.data_ptr(), _strides(v_cache),
-           table.data_ptr(), _int32s("starts", starts, (b,)), _int32s("path", path, (b, m)),
-           _int32s("counts", counts, (b,)), b, hk, m, d, pages, page, width, dtype_code(k_cache),
-           handle),
+           table.data_ptr(), _int32s("starts", starts, (b,), int32), _int32s("path", path, (b, m), int32),
+           _int32s("counts", counts, (b,), int32), b, hk, m, d, pages, page, width,
+           BF16 if dtype is torch.bfloat16 else dtype_code(k_cache), handle),
           "linformer_cache_keep")
 
 
@@ -706,32 +708,35 @@ def _over_pages(Q, k_cache, v_cache, table, k_lengths, q_lengths, scale, out, ls
     """What paged_attention and tree_attention share; masks: the integers between scale and
     dtype."""
     import torch
-    shape, dtype, device = Q.shape, Q.dtype, Q.device
+    shape, dtype, device, int32 = Q.shape, Q.dtype, Q.device, torch.int32
     b, hq, n, d = shape
     if Q.numel() > 0x7fffffff:
         _sizes("Q", shape)
     handle = _stream_of(device, k_cache, v_cache, table, k_lengths, q_lengths, out, lse, mask)
     hk = _int32("k_cache's heads", k_cache.shape[1])
-    pages, page, width = _check_cache(k_cache, v_cache, table, b, hk, d, dtype)
+    pages, page, width = _check_cache(k_cache, v_cache, table, b, hk, d, dtype, int32)
     if out is None:
         out = torch.empty(shape, dtype=dtype, device=device)
     elif out.shape != shape or out.dtype != dtype:
         _check("out", out, shape, dtype)
     if lse is None:
         lse = torch.empty((b, hq, n), dtype=torch.float32, device=device)
-    else:
+    elif lse.shape != (b, hq, n) or lse.dtype != torch.float32 or not lse.is_contiguous():
         _check_dense("lse", lse, (b, hq, n), torch.float32)
     if mask is not None:
-        _check_dense("mask", mask, (b, n, (n + 63) // 64), torch.int64)
+        words = (b, n, (n + 63) // 64)
+        if mask.shape != words or mask.dtype != torch.int64 or not mask.is_contiguous():
+            _check_dense("mask", mask, words, torch.int64)
         mask = (mask.data_ptr(),)
     if k_lengths is None:
         raise ValueError("k_lengths: the rows of each sequence are needed")
     _call(call, device,
           (Q.data_ptr(), _strides(Q), k_cache.data_ptr(), _strides(k_cache), v_cache.data_ptr(),
            _strides(v_cache), out.data_ptr(), _strides(out), lse.data_ptr(), table.data_ptr(),
-           _int32s("k_lengths", k_lengths, (b,)), _int32s("q_lengths", q_lengths, (b,)),
+           _int32s("k_lengths", k_lengths, (b,), int32), _int32s("q_lengths", q_lengths, (b,), int32),
            *(mask or ()), b, hq, hk, n, d, pages, page, width,
-           d ** -0.5 if scale is None else scale, *masks, dtype_code(Q), handle), name)
+           d ** -0.5 if scale is None else scale, *masks,
+           BF16 if dtype is torch.bfloat16 else dtype_code(Q), handle), name)
     return out, lse
 
 
@@ -771,15 +776,18 @@ def tree_mask(parents, out=None, stream=None):
     if stream is not None:
         with _current_on(parents.device, stream):
             return tree_mask(parents, out)
-    b, n = parents.shape
-    _sizes("parents", parents.shape)
-    handle = _stream_of(parents.device, out)
-    _check_dense("parents", parents, (b, n), torch.int32)
+    entries, device = parents.shape, parents.device
+    b, n = entries
+    if parents.numel() > 0x7fffffff:
+        _sizes("parents", entries)
+    handle = _stream_of(device, out)
+    if parents.dtype != torch.int32 or not parents.is_contiguous():
+        _check_dense("parents", parents, entries, torch.int32)
     shape = (b, n, (n + 63) // 64)
     if out is None:
-        out = torch.empty(shape, dtype=torch.int64, device=parents.device)
+        out = torch.empty(shape, dtype=torch.int64, device=device)
     else:
         _check_dense("out", out, shape, torch.int64)
-    _call(lib().linformer_tree_mask, parents.device,
+    _call(lib().linformer_tree_mask, device,
           (parents.data_ptr(), out.data_ptr(), b, n, handle), "linformer_tree_mask")
     return out
