@@ -17,6 +17,7 @@
 #include "internal.cuh"
 #include "paged.cuh"
 #include "rotary.cuh"
+#include "sm100_ptx.cuh"
 
 namespace linformer {
 namespace paged {
@@ -51,6 +52,7 @@ struct AppendParams {
 template <typename T, int V, bool kInterleaved>
 __global__ void __launch_bounds__(kThreads, kBlocks) append_kernel(const AppendParams p) {
     using Piece = Vec<T, V>;
+    ptx::launch_dependents();  // (here and below: the attention after it is set up meanwhile, and waits)
     const int64_t tid = (int64_t)blockIdx.x * kThreads + threadIdx.x;
     if (tid >= p.threads) return;
     const int c = (int)(tid % p.chunks);
@@ -134,6 +136,7 @@ struct KeepParams {
 template <typename T, int V>
 __global__ void __launch_bounds__(kThreads) keep_kernel(const KeepParams p) {
     using Piece = Vec<T, V>;
+    ptx::launch_dependents();
     const int64_t tid = (int64_t)blockIdx.x * kThreads + threadIdx.x;
     if (tid >= p.threads) return;
     const int c = (int)(tid % p.chunks);
@@ -193,6 +196,7 @@ __global__ void __launch_bounds__(kThreads) keep_kernel(const KeepParams p) {
 __global__ void __launch_bounds__(1024) tree_mask_kernel(const int32_t *parents, uint64_t *mask, int n, int words,
                                                          int *status) {
     __shared__ int parent[1024];
+    ptx::launch_dependents();
     const int i = threadIdx.x;
     const int64_t b = blockIdx.x;
     if (i < n) {
