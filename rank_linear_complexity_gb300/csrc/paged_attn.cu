@@ -184,20 +184,15 @@ paged_attn_kernel(const __grid_constant__ CUtensorMap tQ, const __grid_constant_
             const int32_t *table = p.table + (int64_t)it.seq * p.width;
             auto look = [&](int j) { return mine ? page_of(p, table, j, row, it.sp.Lk) : 0; };
             int page = look(it.lo);
-            // The first item's Q before its keys, the others' after their first block's: the last item's
-            // scores may still need theirs, and the keys are not to wait for that.
-            auto load_q = [&] {
-                if (nq > 0 && !warp_spin(&sh->q_free, (nq - 1) & 1, p.status, 120, abort_flag)) return false;
-                if (lane == 0) {
-                    mbar_arrive_expect_tx(&sh->q_full, (uint32_t)(p.qbox * p.hbox * DP * 2));
-                    for (int h = 0; h < DP / 64; ++h)
-                        tma_load_5d(smem + L::kQ + h * L::kQHalf, &tQ, &sh->q_full, h * 64, r.q0, r.h0, it.kvh, it.seq);
-                }
-                ++nq;
-                return true;
-            };
-            const bool at_once = nq == 0;
-            if (at_once) load_q();
+            // (one token over 62 caches: 228 us; Q after the next item's first keys, which then do not wait for
+            // the last scores, 232; Q in two buffers 229)
+            if (nq > 0 && !warp_spin(&sh->q_free, (nq - 1) & 1, p.status, 120, abort_flag)) break;
+            if (lane == 0) {
+                mbar_arrive_expect_tx(&sh->q_full, (uint32_t)(p.qbox * p.hbox * DP * 2));
+                for (int h = 0; h < DP / 64; ++h)
+                    tma_load_5d(smem + L::kQ + h * L::kQHalf, &tQ, &sh->q_full, h * 64, r.q0, r.h0, it.kvh, it.seq);
+            }
+            ++nq;
             for (int j = it.lo; j < it.hi; ++j) {
                 const int now = page, at = (j * kTile + row) & (p.page - 1);
                 if (j + 1 < it.hi) page = look(j + 1);
@@ -218,7 +213,6 @@ paged_attn_kernel(const __grid_constant__ CUtensorMap tQ, const __grid_constant_
                                     kv ? &tV : &tK, &sh->full[e], half * 64, at, 0, it.kvh, now);
                     if (!L::kPair || kv == 1) ++ring;
                 }
-                if (ok && j == it.lo && !at_once) ok = load_q();
                 if (!ok) break;
             }
         }
