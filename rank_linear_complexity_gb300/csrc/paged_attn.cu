@@ -126,8 +126,12 @@ paged_attn_kernel(const __grid_constant__ CUtensorMap tQ, const __grid_constant_
                   const __grid_constant__ CUtensorMap tV, const __grid_constant__ AttnParams p) {
     using L = Layout<DP, N>;
     constexpr int C = N / 2;  // columns of a thread
-    extern __shared__ uint8_t raw[];
-    uint8_t *smem = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(raw) + 1023) & ~uintptr_t(1023));
+    // (addresses in it are constants then, and take no registers)
+    extern __shared__ __align__(1024) uint8_t smem[];
+    if (smem_u32(smem) & 1023u) {
+        if (threadIdx.x == 0 && p.status) atomicExch(p.status, 133);
+        return;
+    }
     Shared *sh = reinterpret_cast<Shared *>(smem + L::kEnd);
     volatile int *abort_flag = &sh->abort;
     const int tid = threadIdx.x, warp = __shfl_sync(0xffffffffu, tid >> 5, 0), lane = tid & 31;
@@ -164,11 +168,12 @@ paged_attn_kernel(const __grid_constant__ CUtensorMap tQ, const __grid_constant_
     tc_fence_before();
     wait_prerequisites();
     if (tid == 0) launch_dependents();  // the join, which waits for this grid's end
-    fill(p, sh->marks, tid, kThreads);
+    Walk walk = p.direct ? Walk(p) : Walk();
+    if (!p.direct) fill(p, sh->marks, tid, kThreads);
     __syncthreads();
     tc_fence_after();
     const uint32_t tmem = sh->tmem;
-    Walk walk(p, sh->marks, blockIdx.x);
+    if (!p.direct) walk = Walk(p, sh->marks, blockIdx.x);
     Item it;
 
     if (warp == kLoadWarp) {  // ---------------- loads
@@ -275,9 +280,9 @@ paged_attn_kernel(const __grid_constant__ CUtensorMap tQ, const __grid_constant_
         }
         __syncwarp();
     } else if (warp >= kEmptyWarp) {  // ---------------- rows without keys
-        if (warp == kEmptyWarp && lane == 0) write_cut(p, walk, sh->marks.first[p.b]);
+        if (warp == kEmptyWarp && lane == 0) write_cut(p, walk, sh->marks);
         __syncwarp();
-        write_empty(p, sh->marks, warp - kEmptyWarp, kThreads / 32 - kEmptyWarp, lane);
+        write_empty(p, sh->marks, p.direct ? &walk : nullptr, warp - kEmptyWarp, kThreads / 32 - kEmptyWarp, lane);
     } else {  // ---------------- softmax: one key a thread, C of the rows
         const int w = warp >> 2, key0 = tid & 127, c0 = w * C;
         const uint32_t lanes = (uint32_t)((warp & 3) * 32) << 16;
@@ -589,7 +594,7 @@ __global__ void __launch_bounds__(kJoinWarps * 32) join_kernel(const __grid_cons
 
 template <int DP, int N>
 int launch(const AttnCall &c, AttnParams &p) {
-    constexpr uint32_t kSmem = 1024 + Layout<DP, N>::kEnd + sizeof(Shared);
+    constexpr uint32_t kSmem = Layout<DP, N>::kEnd + sizeof(Shared);
     static_assert(kSmem <= 227 * 1024, "shared memory");
     constexpr int kSlot = 10 + (DP == 128 ? 3 : 0) + (N == 16 ? 0 : N == 32 ? 1 : 2);
     p.N = N;
@@ -700,6 +705,7 @@ int attention(const AttnCall &call) {
     // Units of a few blocks at most stay whole: no workspace, no second kernel.
     constexpr int kWholeBlocks = 8;
     p.whole = (int64_t)p.width * p.page <= kWholeBlocks * kTile;
+    p.direct = p.whole && !wide && units * call.hk * call.b <= device_sms();
     const int seqs = (int)std::min<int64_t>(kMaxSeqs, 0x7fffffffLL / most);
     p.ntiles = (int)ntiles;
     p.units = (int)units;
@@ -714,7 +720,7 @@ int attention(const AttnCall &call) {
         p.k_lengths = call.k_lengths + b0;
         p.q_lengths = call.q_lengths ? call.q_lengths + b0 : nullptr;
         p.mask = call.mask ? call.mask + (int64_t)b0 * call.nq * call.words : nullptr;
-        p.ctas = (int)std::min<int64_t>(device_sms(), most * c.b);
+        p.ctas = (int)(p.direct ? units * call.hk * call.b : std::min<int64_t>(device_sms(), most * c.b));
         if (wide) st = launch_wide(c, p);
         else st = call.d <= 64 ? launch_rows<64>(c, p) : launch_rows<128>(c, p);
     }

@@ -32,7 +32,9 @@ struct AttnParams {
     // tiles of qbox positions of hbox heads (nch tiles to a group), `per` of them to a unit of work;
     // N: rows of a tile in the workspace
     int qbox, hbox, nch, ntiles, per, units, N, ctas;
-    int whole;  // no unit is cut
+    int whole;   // no unit is cut
+    int direct;  // and each has a CTA of its own, by number (not in the wide kernel, which has no
+                 // register to spare: a chunk of 2048 764 us against 790)
     int pages, page, width, shift, box, nbox;  // nbox boxes of `box` rows make a block of keys
     float scale, scale_log2;
     int wide_stores;
@@ -130,13 +132,25 @@ struct Item {
     int slot;  // where its partial result goes; -1: the unit is whole
 };
 struct Walk {
-    int at, end;
+    int at = 0, end = 0;
     int seq, unit, kvh, blk, lo, hi, slot;
     Span sp;
+    Walk() = default;
+    // A unit a CTA.
+    __device__ __forceinline__ explicit Walk(const AttnParams &p) {
+        seq = blockIdx.x / (p.units * p.hk);
+        const int r = blockIdx.x - seq * (p.units * p.hk);
+        unit = r / p.hk;
+        kvh = r - unit * p.hk;
+        sp = Span{read_length(p.q_lengths, seq, p.nq), read_length(p.k_lengths, seq, p.width * p.page), p.causal,
+                  p.window};
+        blocks_of_unit(p, sp, unit, lo, hi);
+        blk = 0;
+        end = hi > lo ? 1 : 0;
+    }
     __device__ __forceinline__ Walk(const AttnParams &p, const Marks &marks, int cta) {
         const int *first = marks.first;
         const int total = first[p.b], n = runs(total, p.ctas);
-        at = end = 0;
         if (cta >= n) return;
         at = run_begin(total, cta, n);
         end = run_begin(total, cta + 1, n);
@@ -199,8 +213,9 @@ struct Walk {
 
 // What the join has to know of a CTA, by one thread of it, from its walk's start: the unit whose last
 // part the CTA does, and the CTA that does the first; x = -1 where it ends no cut unit.
-__device__ __forceinline__ void write_cut(const AttnParams &p, const Walk &w, int total) {
+__device__ __forceinline__ void write_cut(const AttnParams &p, const Walk &w, const Marks &marks) {
     if (p.whole) return;
+    const int total = marks.first[p.b];
     int4 cut = make_int4(-1, 0, 0, 0);
     if (w.at < w.end && w.blk > 0 && w.end - w.at >= w.hi - w.lo - w.blk) {
         const int n = runs(total, p.ctas);
@@ -212,12 +227,18 @@ __device__ __forceinline__ void write_cut(const AttnParams &p, const Walk &w, in
 }
 
 // Units without blocks, a share a CTA, by `warps` warps: O = 0, lse = -inf.
-__device__ __forceinline__ void write_empty(const AttnParams &p, const Marks &marks, int warp, int warps, int lane) {
+__device__ __forceinline__ void write_empty(const AttnParams &p, const Marks &marks, const Walk *own, int warp, int warps,
+                                            int lane) {
     const int all = p.b * p.units * p.hk;
     for (int u = blockIdx.x; u < all; u += gridDim.x) {
         const int kvh = u % p.hk, unit = u / p.hk % p.units, seq = u / p.hk / p.units;
         int lo, hi;
-        blocks_of_unit(p, marks.span(p, seq), unit, lo, hi);
+        if (own) {
+            lo = own->lo;
+            hi = own->hi;
+        } else {
+            blocks_of_unit(p, marks.span(p, seq), unit, lo, hi);
+        }
         if (hi > lo) continue;
         for (int t = unit * p.per; t < min(p.ntiles, (unit + 1) * p.per); ++t) {
             const Rows r(p, t);

@@ -87,8 +87,12 @@ __global__ void __launch_bounds__(kThreads, 1)
 paged_wide_kernel(const __grid_constant__ CUtensorMap tQ, const __grid_constant__ CUtensorMap tK,
                   const __grid_constant__ CUtensorMap tV, const __grid_constant__ AttnParams p) {
     using L = Layout<DP>;
-    extern __shared__ uint8_t raw[];
-    uint8_t *smem = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(raw) + 1023) & ~uintptr_t(1023));
+    // (addresses in it are constants then, and take no registers)
+    extern __shared__ __align__(1024) uint8_t smem[];
+    if (smem_u32(smem) & 1023u) {
+        if (threadIdx.x == 0 && p.status) atomicExch(p.status, 157);
+        return;
+    }
     uint8_t *sQ = smem, *sKV = smem + 2 * L::kTileBytes;
     Shared *sh = reinterpret_cast<Shared *>(smem + L::kEnd);
     volatile int *abort_flag = &sh->abort;
@@ -222,12 +226,12 @@ paged_wide_kernel(const __grid_constant__ CUtensorMap tQ, const __grid_constant_
                     sh->items[s] = it;
                     if (more) it.before += it.hi - it.lo;
                     mbar_arrive(&sh->told[s]);
-                    if (k == 0) write_cut(p, begin, sh->marks.first[p.b]);
+                    if (k == 0) write_cut(p, begin, sh->marks);
                     if (!more) break;
                 }
             }
             __syncwarp();
-            write_empty(p, sh->marks, 0, 1, lane);
+            write_empty(p, sh->marks, nullptr, 0, 1, lane);
         } else if (elect_one()) {  // ---------------- products of tile t
             const int t = warp - kMmaWarp;
             const uint32_t idesc_s = idesc_f16(128, 128, 1, 0, 0), idesc_o = idesc_f16(128, DP, 1, 0, 1);
@@ -333,7 +337,14 @@ paged_wide_kernel(const __grid_constant__ CUtensorMap tQ, const __grid_constant_
         const uint32_t tS = tmem + 128 * t + lanes, tP = tmem + L::kP + L::kPStep * t + lanes,
                        tO = tmem + L::kO + DP * t + lanes;
         const float sl = p.scale_log2;
-        const int qi = row & (p.qbox - 1), head = row / p.qbox;  // position and head within the tile
+        // The row's position and head within the tile, worked out where they are needed (kept through the
+        // loop they would cost registers there).
+        auto place = [&](int &qi, int &head) {
+            int r = row;
+            asm volatile("" : "+r"(r));
+            qi = r & (p.qbox - 1);
+            head = r / p.qbox;
+        };
         int n = 0;  // the tile's blocks
         bool ok = true;
         // P.V of the tile's block before this one is done: P may be written over, O rescaled
@@ -353,6 +364,8 @@ paged_wide_kernel(const __grid_constant__ CUtensorMap tQ, const __grid_constant_
             bool warp_valid;
             {
                 const Part x(p, it, t);
+                int qi, head;
+                place(qi, head);
                 const int i = x.q0 + qi;
                 xlo = x.lo;
                 xhi = x.hi;
@@ -400,6 +413,8 @@ paged_wide_kernel(const __grid_constant__ CUtensorMap tQ, const __grid_constant_
                     // Masked keys (whatever they hold) become -inf in place, out of line: the few blocks
                     // at a mask's edge must not widen the code of the others.
                     const Part x(p, it, t);
+                    int qi, head;
+                    place(qi, head);
                     const int k0 = j * kTile, i = x.q0 + qi, node0 = it.sp.Lk - it.sp.Lq;
                     const bool valid = head < p.hbox && x.h0 + head < p.group && i < it.sp.Lq;
                     const int first = valid ? it.sp.first(i) : 0, end = valid ? it.sp.end(i) : (1 << 30);
@@ -464,6 +479,8 @@ paged_wide_kernel(const __grid_constant__ CUtensorMap tQ, const __grid_constant_
             if (!ok) break;
             // O / l out of tensor memory; rows without keys give O = 0 and lse = -inf
             const Part x(p, it, t);
+            int qi, head;
+            place(qi, head);
             const int i = x.q0 + qi, hg = x.h0 + head;
             const bool exists = x.live && head < p.hbox && hg < p.group && i < p.nq;
             const bool dead = !exists || i >= it.sp.Lq || l == 0.f, some = xhi > xlo, whole = it.slot < 0;
@@ -525,7 +542,7 @@ paged_wide_kernel(const __grid_constant__ CUtensorMap tQ, const __grid_constant_
 
 template <int DP>
 int launch(const AttnCall &c, AttnParams &p) {
-    constexpr uint32_t kSmem = 1024 + Layout<DP>::kEnd + sizeof(Shared);
+    constexpr uint32_t kSmem = Layout<DP>::kEnd + sizeof(Shared);
     static_assert(kSmem <= 227 * 1024, "shared memory");
     p.N = kTile;
     return launch_with_join(paged_wide_kernel<DP>, kThreads, kSmem, DP == 64 ? 16 : 17, c, p, DP);
