@@ -3,9 +3,10 @@
 // and a thread a row, two tiles of rows to a unit of work, which share the key blocks in shared
 // memory; blocks come page by page, and CTAs take equal runs of the list of blocks (paged_attn.cuh).
 //   warps 0-3, 4-7  softmax of tile 0 and tile 1: S out of tensor memory, P back
-//   warp 8          loads: looks the pages up and issues a box a lane
+//   warp 8          loads: goes through the CTA's run, tells the others each item, looks the pages up,
+//                   one thread issues the copies
 //   warps 9, 10     one thread each issues a tile's S = Q.K^T and O += P.V
-//   warp 11         goes through the CTA's run and tells the others each item; rows without keys
+//   warp 11         rows without keys: O = 0, lse = -inf
 #include <cmath>
 
 #include "paged_attn.cuh"
@@ -17,7 +18,7 @@ namespace {
 
 // Twelve warps, 168 registers each at launch; the two warpgroups that do the arithmetic take registers
 // from the third.
-constexpr int kThreads = 384, kLoadWarp = 8, kMmaWarp = 9, kPlanWarp = 11;
+constexpr int kThreads = 384, kLoadWarp = 8, kMmaWarp = 9, kEmptyWarp = 11;
 constexpr uint32_t kLaunchRegs = 168, kMathRegs = 208, kIssueRegs = 88;
 static_assert(2 * kMathRegs + kIssueRegs == 3 * kLaunchRegs, "register split");
 
@@ -32,8 +33,8 @@ struct Layout {
     static constexpr uint32_t kEnd = (2 + kStages) * kTileBytes;
 };
 
-constexpr int kAhead = 4;            // items told ahead
-constexpr int kReaders = 1 + 2 + 8;  // load warp, issuing threads, softmax warps
+constexpr int kAhead = 4;        // items told ahead
+constexpr int kReaders = 2 + 8;  // issuing threads, softmax warps
 
 struct Shared {
     uint64_t full[8], empty[8], q_full[2], q_free[2], s_full[2], s_free[2], p_full[2], p_half[2], pv_done[2],
@@ -151,10 +152,24 @@ paged_wide_kernel(const __grid_constant__ CUtensorMap tQ, const __grid_constant_
                 const bool done = lane != 0 || thread_spin(bar, parity, p.status, code, abort_flag);
                 return __shfl_sync(0xffffffffu, (int)done, 0) != 0;
             };
+            Walk walk(p, sh->marks, blockIdx.x);
+            const Walk begin = walk;
+            Shared::Told it;
+            it.before = 0;
             for (int k = 0; ok; ++k) {
-                if (!spin(&sh->told[k % kAhead], (k / kAhead) & 1, 153)) break;
-                const auto &it = sh->items[k % kAhead];
-                if (it.seq < 0) break;
+                const int slot = k % kAhead;
+                const bool more = walk.next(p, sh->marks, it);
+                int page = more && mine ? page_of(p, p.table + (int64_t)it.seq * p.width, it.lo, row, it.sp.Lk) : 0;
+                if (!more) it.seq = -1;
+                ok = k < kAhead || spin(&sh->taken[slot], (k / kAhead - 1) & 1, 153);
+                if (!ok) break;
+                if (lane == 0) {
+                    sh->items[slot] = it;
+                    mbar_arrive(&sh->told[slot]);
+                    if (!more && k == 0) write_cut(p, begin, sh->marks);
+                }
+                __syncwarp();
+                if (!more) break;
                 // The first item's Q before its keys, the others' after their first block's: the last
                 // item's scores may still need theirs, and the keys are not to wait for that.
                 auto load_q = [&] {
@@ -171,13 +186,10 @@ paged_wide_kernel(const __grid_constant__ CUtensorMap tQ, const __grid_constant_
                         }
                         ++nq[t];
                     }
-                    __syncwarp();
-                    if (lane == 0) mbar_arrive(&sh->taken[k % kAhead]);
                 };
                 const int32_t *table = p.table + (int64_t)it.seq * p.width;
                 const int lo = it.lo, hi = it.hi, kvh = it.kvh, Lk = it.sp.Lk;
                 if (k == 0) load_q();
-                int page = mine ? page_of(p, table, lo, row, Lk) : 0;
                 for (int j = lo; j < hi && ok; ++j) {
                     const int now = page, at = (j * kTile) & (p.page - 1);  // (0 where a block has several pages)
                     if (j + 1 < hi && mine) page = page_of(p, table, j + 1, row, Lk);
@@ -203,6 +215,8 @@ paged_wide_kernel(const __grid_constant__ CUtensorMap tQ, const __grid_constant_
                     ok = __shfl_sync(0xffffffffu, ok, 0);
                     if (ok && j == lo && k > 0) load_q();
                 }
+                if (k == 0 && lane == 0) write_cut(p, begin, sh->marks);
+                it.before += hi - lo;
             }
             // no copy outlives the CTA
             if (lane == 0) {
@@ -212,25 +226,7 @@ paged_wide_kernel(const __grid_constant__ CUtensorMap tQ, const __grid_constant_
                     mbar_wait_drain(&sh->full[i % L::kStages], (i / L::kStages) & 1);
             }
             __syncwarp();
-        } else if (warp == kPlanWarp) {
-            if (elect_one()) {
-                Walk walk(p, sh->marks, blockIdx.x);
-                const Walk begin = walk;
-                Shared::Told it;
-                it.before = 0;
-                for (int k = 0;; ++k) {
-                    const int s = k % kAhead;
-                    const bool more = walk.next(p, sh->marks, it);
-                    if (!more) it.seq = -1;
-                    if (k >= kAhead && !thread_spin(&sh->taken[s], (k / kAhead - 1) & 1, p.status, 156, abort_flag)) break;
-                    sh->items[s] = it;
-                    if (more) it.before += it.hi - it.lo;
-                    mbar_arrive(&sh->told[s]);
-                    if (k == 0) write_cut(p, begin, sh->marks);
-                    if (!more) break;
-                }
-            }
-            __syncwarp();
+        } else if (warp == kEmptyWarp) {
             write_empty(p, sh->marks, nullptr, 0, 1, lane);
         } else if (elect_one()) {  // ---------------- products of tile t
             const int t = warp - kMmaWarp;
