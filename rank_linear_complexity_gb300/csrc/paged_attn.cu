@@ -520,7 +520,7 @@ paged_attn_kernel(const __grid_constant__ CUtensorMap tQ, const __grid_constant_
 // exp(lse_s - lse) O_s, in the parts' order.  blockIdx.x: the CTA that did the last part (any other's
 // blocks leave at once).  kEach warps a row: more than one where units are few and their parts many
 // (4 units of 1024 blocks, 38 parts each: 20 us with one warp, 8 with four).
-constexpr int kJoinWarps = 4;
+constexpr int kJoinWarps = 4, kJoinBlocks = 32;
 template <int DP, int kEach>
 __global__ void __launch_bounds__(kJoinWarps * 32) join_kernel(const __grid_constant__ AttnParams p) {
     constexpr int E = DP / 32;
@@ -528,68 +528,69 @@ __global__ void __launch_bounds__(kJoinWarps * 32) join_kernel(const __grid_cons
     launch_dependents();
     wait_prerequisites();
     const int rows = p.qbox * p.hbox, lane = threadIdx.x & 31, warp = threadIdx.x >> 5, mine = warp % kEach;
-    int x = blockIdx.y * (kJoinWarps / kEach) + warp / kEach;
-    const int t = x / rows;
-    x -= t * rows;
     const int4 cut = p.cuts[blockIdx.x];
     if (cut.x < 0) return;
-    const int seq = cut.x, kvh = cut.z, c0 = cut.w, c1 = blockIdx.x, tile = cut.y * p.per + t;
-    if (t >= p.per || tile >= p.ntiles) return;
-    const Rows r(p, tile);
-    const int i = r.q0 + (x & (p.qbox - 1)), hg = r.h0 + x / p.qbox;
-    if (hg >= p.group || i >= p.nq) return;  // (all warps of a row alike)
-    // a row is cut at the end of its first CTA's run, and goes on at the start of the others'
-    auto slot = [&](int c) { return ((int64_t)(2 * c + (c == c0 ? 1 : 0)) * p.per + t) * p.N + x; };
-    float m = -INFINITY;
-    for (int c = c0 + lane; c <= c1; c += 32) m = fmaxf(m, p.part_lse[slot(c)]);
+    const int seq = cut.x, kvh = cut.z, c0 = cut.w, c1 = blockIdx.x;
+    constexpr int kRows = kJoinWarps / kEach;  // of a block at a time
+#pragma unroll 1
+    for (int y = blockIdx.y * kRows + warp / kEach; y < p.per * rows; y += gridDim.y * kRows) {
+        const int t = y / rows, x = y - t * rows, tile = cut.y * p.per + t;
+        const Rows r(p, tile);
+        const int i = r.q0 + (x & (p.qbox - 1)), hg = r.h0 + x / p.qbox;
+        if (tile >= p.ntiles || hg >= p.group || i >= p.nq) continue;  // (all warps of a row alike)
+        // a row is cut at the end of its first CTA's run, and goes on at the start of the others'
+        auto slot = [&](int c) { return ((int64_t)(2 * c + (c == c0 ? 1 : 0)) * p.per + t) * p.N + x; };
+        float m = -INFINITY;
+        for (int c = c0 + lane; c <= c1; c += 32) m = fmaxf(m, p.part_lse[slot(c)]);
 #pragma unroll
-    for (int o = 16; o; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
-    float acc[E] = {}, sum = 0.f;
-    if (m != -INFINITY) {
-        // this warp's parts
-        const int per = (c1 + 1 - c0 + kEach - 1) / kEach, first = c0 + mine * per, last = min(c1 + 1, first + per);
-        for (int c = first; c < last; c += 32) {
-            const int some = min(32, last - c);
-            const float weight = lane < some ? __expf(p.part_lse[slot(c + lane)] - m) : 0.f;
+        for (int o = 16; o; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
+        float acc[E] = {}, sum = 0.f;
+        if (m != -INFINITY) {
+            // this warp's parts
+            const int per = (c1 + 1 - c0 + kEach - 1) / kEach, first = c0 + mine * per, last = min(c1 + 1, first + per);
+            for (int c = first; c < last; c += 32) {
+                const int some = min(32, last - c);
+                const float weight = lane < some ? __expf(p.part_lse[slot(c + lane)] - m) : 0.f;
 #pragma unroll 8
-            for (int k = 0; k < some; ++k) {
-                const float w = __shfl_sync(0xffffffffu, weight, k);
-                sum += w;
-                float v[E];
-                const float *from = p.part_o + slot(c + k) * DP + lane * E;
-                if constexpr (E == 4) {
-                    const float4 y = *reinterpret_cast<const float4 *>(from);
-                    v[0] = y.x, v[1] = y.y, v[2] = y.z, v[3] = y.w;
-                } else {
-                    const float2 y = *reinterpret_cast<const float2 *>(from);
-                    v[0] = y.x, v[1] = y.y;
-                }
+                for (int k = 0; k < some; ++k) {
+                    const float w = __shfl_sync(0xffffffffu, weight, k);
+                    sum += w;
+                    float v[E];
+                    const float *from = p.part_o + slot(c + k) * DP + lane * E;
+                    if constexpr (E == 4) {
+                        const float4 y = *reinterpret_cast<const float4 *>(from);
+                        v[0] = y.x, v[1] = y.y, v[2] = y.z, v[3] = y.w;
+                    } else {
+                        const float2 y = *reinterpret_cast<const float2 *>(from);
+                        v[0] = y.x, v[1] = y.y;
+                    }
 #pragma unroll
-                for (int e = 0; e < E; ++e) acc[e] += w == 0.f ? 0.f : w * v[e];  // (a part without keys wrote no O)
+                    for (int e = 0; e < E; ++e) acc[e] += w == 0.f ? 0.f : w * v[e];  // (a part without keys wrote no O)
+                }
             }
         }
-    }
-    if constexpr (kEach > 1) {
+        if constexpr (kEach > 1) {
 #pragma unroll
-        for (int e = 0; e < E; ++e) shared[warp][e][lane] = acc[e];
-        shared[warp][E][lane] = sum;
-        __syncthreads();
-        if (mine) return;
-        for (int o = 1; o < kEach; ++o) {
+            for (int e = 0; e < E; ++e) shared[warp][e][lane] = acc[e];
+            shared[warp][E][lane] = sum;
+            __syncthreads();
+            for (int o = 1; o < kEach && !mine; ++o) {
 #pragma unroll
-            for (int e = 0; e < E; ++e) acc[e] += shared[warp + o][e][lane];
-            sum += shared[warp + o][E][lane];
+                for (int e = 0; e < E; ++e) acc[e] += shared[warp + o][e][lane];
+                sum += shared[warp + o][E][lane];
+            }
         }
-    }
-    const float inv = sum > 0.f ? 1.f / sum : 0.f;
-    const int64_t h = (int64_t)kvh * p.group + hg;
-    __nv_bfloat16 *dst = p.out + seq * p.so.b + h * p.so.h + (int64_t)i * p.so.n;
-    if (lane * E < p.d) {
+        const float inv = sum > 0.f ? 1.f / sum : 0.f;
+        const int64_t h = (int64_t)kvh * p.group + hg;
+        __nv_bfloat16 *dst = p.out + seq * p.so.b + h * p.so.h + (int64_t)i * p.so.n;
+        if (!mine && lane * E < p.d) {
 #pragma unroll
-        for (int e = 0; e < E; e += 2)
-            *reinterpret_cast<uint32_t *>(dst + lane * E + e) = pack2(acc[e] * inv, acc[e + 1] * inv);
+            for (int e = 0; e < E; e += 2)
+                *reinterpret_cast<uint32_t *>(dst + lane * E + e) = pack2(acc[e] * inv, acc[e + 1] * inv);
+        }
+        if (!mine && lane == 0) p.lse[(seq * (int64_t)p.hq + h) * p.nq + i] = m == -INFINITY ? -INFINITY : m + logf(sum);
+        if (kEach > 1) __syncthreads();  // `shared` again
     }
-    if (lane == 0) p.lse[(seq * (int64_t)p.hq + h) * p.nq + i] = m == -INFINITY ? -INFINITY : m + logf(sum);
 }
 
 template <int DP, int N>
@@ -653,7 +654,9 @@ int launch_with_join(Kernel kernel, int threads, uint32_t smem, int slot, const 
         // many parts where a unit's blocks, all units alike, would fill eight runs
         const bool many = (int64_t)p.b * p.units * p.hk * 8 <= p.ctas;
         const int rows = p.per * p.qbox * p.hbox, at_once = many ? 1 : kJoinWarps;
-        cfg.gridDim = dim3((unsigned)p.ctas, (unsigned)((rows + at_once - 1) / at_once));
+        // (blocks of most runs leave at once, but 30000 of them, one a row, took 25 us to do so; trees of 79
+        // nodes, 6 parts a unit: 37.5 us in all with 32 blocks a run, 41.8 with 16, 38.8 with 64)
+        cfg.gridDim = dim3((unsigned)p.ctas, (unsigned)std::min(kJoinBlocks, (rows + at_once - 1) / at_once));
         cfg.blockDim = dim3(kJoinWarps * 32);
         cfg.dynamicSmemBytes = 0;
         const auto join = dp == 64 ? (many ? join_kernel<64, kJoinWarps> : join_kernel<64, 1>)

@@ -17,7 +17,6 @@ using sattn::pack2;
 using sattn::Span;
 
 constexpr int kMaxSeqs = 512;  // sequences of a launch
-constexpr int kMinRun = 1;     // blocks of a CTA at least
 constexpr float kOutgrown = 16.f, kLog2e = 1.4426950408889634f, kLn2 = 0.6931471805599453f;
 
 struct AttnParams {
@@ -93,7 +92,9 @@ __device__ __forceinline__ int run_begin(int total, int cta, int ctas) {
     const int each = total / ctas;
     return each * cta + min(cta, total - each * ctas);
 }
-__device__ __forceinline__ int runs(int total, int ctas) { return min(ctas, max(1, total / kMinRun)); }
+__device__ __forceinline__ int runs(const AttnParams &p, int total) {
+    return min(p.ctas, max(1, total));
+}
 
 // Fills the marks, by a whole CTA (it has one of the CTA's barriers; one has to follow).
 __device__ __forceinline__ void fill(const AttnParams &p, Marks &marks, int tid, int threads) {
@@ -150,7 +151,7 @@ struct Walk {
     }
     __device__ __forceinline__ Walk(const AttnParams &p, const Marks &marks, int cta) {
         const int *first = marks.first;
-        const int total = first[p.b], n = runs(total, p.ctas);
+        const int total = first[p.b], n = runs(p, total);
         if (cta >= n) return;
         at = run_begin(total, cta, n);
         end = run_begin(total, cta + 1, n);
@@ -218,7 +219,7 @@ __device__ __forceinline__ void write_cut(const AttnParams &p, const Walk &w, co
     const int total = marks.first[p.b];
     int4 cut = make_int4(-1, 0, 0, 0);
     if (w.at < w.end && w.blk > 0 && w.end - w.at >= w.hi - w.lo - w.blk) {
-        const int n = runs(total, p.ctas);
+        const int n = runs(p, total);
         int c0 = blockIdx.x - 1;
         while (run_begin(total, c0, n) > w.at - w.blk) --c0;
         cut = make_int4(w.seq, w.unit, w.kvh, c0);
@@ -226,11 +227,14 @@ __device__ __forceinline__ void write_cut(const AttnParams &p, const Walk &w, co
     p.cuts[blockIdx.x] = cut;
 }
 
-// Units without blocks, a share a CTA, by `warps` warps: O = 0, lse = -inf.
+// Units without blocks: O = 0, lse = -inf.  Every CTA takes some rows of each, by `warps` warps of it.
 __device__ __forceinline__ void write_empty(const AttnParams &p, const Marks &marks, const Walk *own, int warp, int warps,
                                             int lane) {
-    const int all = p.b * p.units * p.hk;
-    for (int u = blockIdx.x; u < all; u += gridDim.x) {
+    constexpr int kRows = 16;  // (a whole unit a warp: a batch with idle sequences waited 40 us for its end)
+    const int rows = p.per * p.qbox * p.hbox, chunks = own ? 1 : (rows + kRows - 1) / kRows;
+    const int64_t all = (int64_t)p.b * p.units * p.hk * chunks;
+    for (int64_t x = blockIdx.x; x < all; x += gridDim.x) {
+        const int u = (int)(x / chunks), chunk = (int)(x - (int64_t)u * chunks);
         const int kvh = u % p.hk, unit = u / p.hk % p.units, seq = u / p.hk / p.units;
         int lo, hi;
         if (own) {
@@ -240,17 +244,17 @@ __device__ __forceinline__ void write_empty(const AttnParams &p, const Marks &ma
             blocks_of_unit(p, marks.span(p, seq), unit, lo, hi);
         }
         if (hi > lo) continue;
-        for (int t = unit * p.per; t < min(p.ntiles, (unit + 1) * p.per); ++t) {
-            const Rows r(p, t);
-            for (int x = warp; x < p.qbox * p.hbox; x += warps) {
-                const int i = r.q0 + (x & (p.qbox - 1)), hg = r.h0 + x / p.qbox;
-                if (hg >= p.group || i >= p.nq) continue;
-                const int64_t h = (int64_t)kvh * p.group + hg;
-                if (8 * lane < p.d)
-                    *reinterpret_cast<uint4 *>(p.out + seq * p.so.b + h * p.so.h + (int64_t)i * p.so.n + 8 * lane) =
-                        make_uint4(0u, 0u, 0u, 0u);
-                if (lane == 0) p.lse[(seq * (int64_t)p.hq + h) * p.nq + i] = -INFINITY;
-            }
+        const int last = own ? rows : min(rows, (chunk + 1) * kRows);
+        for (int r = chunk * kRows + warp; r < last; r += warps) {
+            const int t = r / (p.qbox * p.hbox), y = r - t * (p.qbox * p.hbox), tile = unit * p.per + t;
+            const Rows at(p, tile);
+            const int i = at.q0 + (y & (p.qbox - 1)), hg = at.h0 + y / p.qbox;
+            if (tile >= p.ntiles || hg >= p.group || i >= p.nq) continue;
+            const int64_t h = (int64_t)kvh * p.group + hg;
+            if (8 * lane < p.d)
+                *reinterpret_cast<uint4 *>(p.out + seq * p.so.b + h * p.so.h + (int64_t)i * p.so.n + 8 * lane) =
+                    make_uint4(0u, 0u, 0u, 0u);
+            if (lane == 0) p.lse[(seq * (int64_t)p.hq + h) * p.nq + i] = -INFINITY;
         }
     }
 }
