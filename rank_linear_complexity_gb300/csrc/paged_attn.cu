@@ -651,8 +651,8 @@ int launch_with_join(Kernel kernel, int threads, uint32_t smem, int slot, const 
     }
     if (!st && !p.whole) {
         KernelScope scope(LINFORMER_KERNEL_PAGED, c.stream);
-        // many parts where a unit's blocks, all units alike, would fill eight runs
-        const bool many = (int64_t)p.b * p.units * p.hk * 8 <= p.ctas;
+        // many parts where a unit's blocks, all units alike, would fill sixteen runs
+        const bool many = (int64_t)p.b * p.units * p.hk * 16 <= p.ctas;
         const int rows = p.per * p.qbox * p.hbox, at_once = many ? 1 : kJoinWarps;
         // (blocks of most runs leave at once, but 30000 of them, one a row, took 25 us to do so; trees of 79
         // nodes, 6 parts a unit: 37.5 us in all with 32 blocks a run, 41.8 with 16, 38.8 with 64)

@@ -84,6 +84,7 @@ __device__ __forceinline__ int read_length(const int32_t *lengths, int seq, int 
 struct Marks {
     int2 length[kMaxSeqs];    // queries, cache rows
     int first[kMaxSeqs + 1];  // where the blocks of each sequence begin in the list
+    bool empty[kMaxSeqs];     // some unit has none
     __device__ __forceinline__ Span span(const AttnParams &p, int seq) const {
         return Span{length[seq].x, length[seq].y, p.causal, p.window};
     }
@@ -103,11 +104,14 @@ __device__ __forceinline__ void fill(const AttnParams &p, Marks &marks, int tid,
         marks.length[s] = make_int2(read_length(p.q_lengths, s, p.nq), read_length(p.k_lengths, s, p.width * p.page));
         const Span sp = marks.span(p, s);
         int sum = 0;
+        bool empty = false;
         for (int u = 0; u < p.units; ++u) {
             int lo, hi;
             blocks_of_unit(p, sp, u, lo, hi);
             sum += (hi - lo) * p.hk;
+            empty |= hi <= lo;
         }
+        marks.empty[s] = empty;
         first[s + 1] = sum;
     }
     __syncthreads();
@@ -227,34 +231,46 @@ __device__ __forceinline__ void write_cut(const AttnParams &p, const Walk &w, co
     p.cuts[blockIdx.x] = cut;
 }
 
-// Units without blocks: O = 0, lse = -inf.  Every CTA takes some rows of each, by `warps` warps of it.
+// Units without blocks: O = 0, lse = -inf.  A unit a CTA in turn, by `warps` warps of it, 16 bytes a thread;
+// own: of a unit a CTA.
 __device__ __forceinline__ void write_empty(const AttnParams &p, const Marks &marks, const Walk *own, int warp, int warps,
                                             int lane) {
-    constexpr int kRows = 16;  // (a whole unit a warp: a batch with idle sequences waited 40 us for its end)
-    const int rows = p.per * p.qbox * p.hbox, chunks = own ? 1 : (rows + kRows - 1) / kRows;
-    const int64_t all = (int64_t)p.b * p.units * p.hk * chunks;
-    for (int64_t x = blockIdx.x; x < all; x += gridDim.x) {
-        const int u = (int)(x / chunks), chunk = (int)(x - (int64_t)u * chunks);
-        const int kvh = u % p.hk, unit = u / p.hk % p.units, seq = u / p.hk / p.units;
-        int lo, hi;
-        if (own) {
-            lo = own->lo;
-            hi = own->hi;
-        } else {
-            blocks_of_unit(p, marks.span(p, seq), unit, lo, hi);
-        }
-        if (hi > lo) continue;
-        const int last = own ? rows : min(rows, (chunk + 1) * kRows);
-        for (int r = chunk * kRows + warp; r < last; r += warps) {
-            const int t = r / (p.qbox * p.hbox), y = r - t * (p.qbox * p.hbox), tile = unit * p.per + t;
+    const int tile_rows = p.qbox * p.hbox, pieces = p.d / 8, all = p.per * tile_rows * pieces;
+    auto write = [&](int seq, int kvh, int unit) {
+#pragma unroll 2
+        for (int e = warp * 32 + lane; e < all; e += warps * 32) {
+            const int r = e / pieces, piece = e - r * pieces, t = r >= tile_rows ? 1 : 0, y = r - t * tile_rows,
+                      tile = unit * p.per + t;
             const Rows at(p, tile);
             const int i = at.q0 + (y & (p.qbox - 1)), hg = at.h0 + y / p.qbox;
             if (tile >= p.ntiles || hg >= p.group || i >= p.nq) continue;
             const int64_t h = (int64_t)kvh * p.group + hg;
-            if (8 * lane < p.d)
-                *reinterpret_cast<uint4 *>(p.out + seq * p.so.b + h * p.so.h + (int64_t)i * p.so.n + 8 * lane) =
-                    make_uint4(0u, 0u, 0u, 0u);
-            if (lane == 0) p.lse[(seq * (int64_t)p.hq + h) * p.nq + i] = -INFINITY;
+            *reinterpret_cast<uint4 *>(p.out + seq * p.so.b + h * p.so.h + (int64_t)i * p.so.n + 8 * piece) =
+                make_uint4(0u, 0u, 0u, 0u);
+            if (piece == 0) p.lse[(seq * (int64_t)p.hq + h) * p.nq + i] = -INFINITY;
+        }
+    };
+    if (own) {
+        if (own->hi <= own->lo) write(own->seq, own->kvh, own->unit);
+        return;
+    }
+    const int ctas = gridDim.x;
+    int turn = 0;  // the CTA whose turn the next unit is
+    for (int s0 = 0; s0 < p.b; s0 += 32) {
+        unsigned some = __ballot_sync(0xffffffffu, s0 + lane < p.b && marks.empty[min(s0 + lane, p.b - 1)]);
+        for (; some; some &= some - 1) {
+            const int seq = s0 + __ffs(some) - 1;
+            const Span sp = marks.span(p, seq);
+            for (int u0 = 0; u0 < p.units; u0 += 32) {
+                int lo = 0, hi = 1;
+                if (u0 + lane < p.units) blocks_of_unit(p, sp, u0 + lane, lo, hi);
+                unsigned none = __ballot_sync(0xffffffffu, hi <= lo);
+                for (; none; none &= none - 1) {
+                    const int ahead = blockIdx.x - turn, first = ahead < 0 ? ahead + ctas : ahead;
+                    for (int kvh = first; kvh < p.hk; kvh += ctas) write(seq, kvh, u0 + __ffs(none) - 1);
+                    turn = (turn + p.hk) % ctas;
+                }
+            }
         }
     }
 }

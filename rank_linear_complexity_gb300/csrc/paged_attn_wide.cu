@@ -44,7 +44,6 @@ struct Shared {
     } items[kAhead];  // (in shared memory: the softmax has no registers to spare for a walk)
     uint32_t tmem;
     int abort;
-    int pages[kTile / 8];
     Marks marks;
 };
 
@@ -140,10 +139,11 @@ paged_wide_kernel(const __grid_constant__ CUtensorMap tQ, const __grid_constant_
     if (warp >= kLoadWarp) {
         setmaxnreg_dec<kIssueRegs>();
         if (warp == kLoadWarp) {  // ---------------- loads
-            // a lane knows the page of one of a block's boxes of `box` rows, one thread issues them all
-            // (the copy's operands are the warp's: lanes with their own would take turns)
-            const bool mine = lane < p.nbox;
-            const int row = lane * p.box;
+            // a lane's box of a tile: `box` rows of a page, 64 columns
+            const int bi = lane / (DP / 64), half = lane % (DP / 64);
+            const bool mine = bi < p.nbox;
+            const int row = bi * p.box;
+            const uint32_t dst = half * 16384u + row * 128u;
             int ring = 0, nq[2] = {0, 0};
             bool ok = true;
             // (one lane waits: a function that is not inlined may not be called from warps of both register
@@ -191,28 +191,18 @@ paged_wide_kernel(const __grid_constant__ CUtensorMap tQ, const __grid_constant_
                 const int lo = it.lo, hi = it.hi, kvh = it.kvh, Lk = it.sp.Lk;
                 if (k == 0) load_q();
                 for (int j = lo; j < hi && ok; ++j) {
-                    const int now = page, at = (j * kTile) & (p.page - 1);  // (0 where a block has several pages)
+                    const int now = page, at = (j * kTile + row) & (p.page - 1);
                     if (j + 1 < hi && mine) page = page_of(p, table, j + 1, row, Lk);
-                    if (mine) sh->pages[lane] = now;
-                    __syncwarp();
-                    if (lane == 0) {
-                        for (int kv = 0; kv < 2 && ok; ++kv, ++ring) {
-                            const int s = ring % L::kStages;
-                            if (ring >= L::kStages &&
-                                !thread_spin(&sh->empty[s], (ring / L::kStages - 1) & 1, p.status, 141, abort_flag)) {
-                                ok = false;
-                                break;
-                            }
-                            mbar_arrive_expect_tx(&sh->full[s], L::kTileBytes);
-                            uint8_t *dst = sKV + s * L::kTileBytes;
-                            for (int x = 0; x < p.nbox; ++x, dst += p.box * 128)
-#pragma unroll
-                                for (int h = 0; h < DP / 64; ++h)
-                                    tma_load_5d(dst + h * 16384, kv ? &tV : &tK, &sh->full[s], h * 64, at, 0, kvh,
-                                                sh->pages[x]);
-                        }
+                    for (int kv = 0; kv < 2 && ok; ++kv, ++ring) {
+                        const int s = ring % L::kStages;
+                        if (ring >= L::kStages) ok = spin(&sh->empty[s], (ring / L::kStages - 1) & 1, 141);
+                        if (!ok) break;
+                        if (lane == 0) mbar_arrive_expect_tx(&sh->full[s], L::kTileBytes);
+                        __syncwarp();
+                        if (mine)
+                            tma_load_5d(sKV + s * L::kTileBytes + dst, kv ? &tV : &tK, &sh->full[s], half * 64, at, 0,
+                                        kvh, now);
                     }
-                    ok = __shfl_sync(0xffffffffu, ok, 0);
                     if (ok && j == lo && k > 0) load_q();
                 }
                 if (k == 0 && lane == 0) write_cut(p, begin, sh->marks);
