@@ -279,3 +279,22 @@ def test_oracle_rows_appended_and_kept():
     assert paged.place(np.zeros((3, 1, 8, 1)), [0], -1) is None and paged.place(np.zeros((3, 1, 8, 1)), [1], 7) == (1, 7)
     same, _ = paged.keep(kc, vc, table.tolist(), [2, 0], np.array([[0, 0, 1], [0, 0, 1]]))
     assert np.array_equal(same, kc.double().numpy(), equal_nan=True)
+
+
+def test_every_wait_of_the_kernels_over_pages_has_a_code_of_its_own():
+    """The code in the device status word names one place in the sources."""
+    import os
+    import re
+    codes = []
+    for name in ("paged_attn.cu", "paged_attn_wide.cu"):
+        with open(os.path.join(libbuild.CSRC, name)) as f:
+            src = f.read()
+        codes += re.findall(r"spin\([^;]*?(1[2-5]\d)[,)]", src) + re.findall(r"product\([^;]*?(1[2-5]\d)\)", src)
+        codes += re.findall(r"atomicExch\(p\.status, (\d+)\)", src)
+    assert len(codes) >= 20
+    assert sorted(codes) == sorted(set(codes))
+    others = []
+    for name in ("softmax_attn_fwd.cu", "softmax_attn_bwd.cu", "work_queue.cuh"):
+        with open(os.path.join(libbuild.CSRC, name)) as f:
+            others += re.findall(r"_spin\([^;]*?status, (\d+),", f.read())
+    assert not set(codes) & set(others)
