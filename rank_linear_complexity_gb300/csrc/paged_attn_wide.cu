@@ -22,14 +22,13 @@ constexpr int kThreads = 384, kLoadWarp = 8, kMmaWarp = 9, kEmptyWarp = 11;
 constexpr uint32_t kLaunchRegs = 168, kMathRegs = 208, kIssueRegs = 88;
 static_assert(2 * kMathRegs + kIssueRegs == 3 * kLaunchRegs, "register split");
 
-// Tensor memory as in softmax_attn_fwd.cu: S of the next block beside P up to 64 elements, P over S
-// up to 128.
+constexpr int kStep = kTile / 2;  // keys of a step
+// Tensor memory: of each tile S of two steps (64 columns each), P over its own S, then O.
 template <int DP>
 struct Layout {
-    static constexpr bool kSep = DP == 64;
     static constexpr int kStages = DP == 64 ? 8 : 4;
     static constexpr uint32_t kTileBytes = kTile * DP * 2;
-    static constexpr uint32_t kP = kSep ? 256 : 0, kPStep = kSep ? 64 : 128, kO = kSep ? 384 : 256;
+    static constexpr uint32_t kO = 256;
     static constexpr uint32_t kEnd = (2 + kStages) * kTileBytes;
 };
 
@@ -37,8 +36,8 @@ constexpr int kAhead = 4;        // items told ahead
 constexpr int kReaders = 2 + 8;  // issuing threads, softmax warps
 
 struct Shared {
-    uint64_t full[8], empty[8], q_full[2], q_free[2], s_full[2], s_free[2], p_full[2], p_half[2], pv_done[2],
-        o_free[2], drain[2], told[kAhead], taken[kAhead];
+    uint64_t full[8], empty[8], q_full[2], q_free[2], s_full[2][2], p_full[2][2], pv_done[2][2], o_free[2],
+        drain[2], told[kAhead], taken[kAhead];
     struct Told : Item {
         int before;  // blocks of the items before it
     } items[kAhead];  // (in shared memory: the softmax has no registers to spare for a walk)
@@ -64,22 +63,11 @@ struct Part {
     }
 };
 
-// The scores of a block whose nodes a row's mask hides become -inf in tensor memory; node: of the
-// block's first column (below 0: rows before the tree, which it sees).
-__device__ __noinline__ void mask_nodes(uint32_t t, int node, const uint64_t *mask, int words) {
+// Which of 64 nodes from `node` on (below 0: rows before the tree) a row's mask leaves.
+__device__ __forceinline__ uint64_t nodes_seen(const uint64_t *mask, int words, int node) {
     auto word = [&](int w) { return w < 0 ? ~0ull : w < words ? __ldg(mask + w) : 0ull; };
-#pragma unroll 1
-    for (int c = 0; c < kTile; c += 32) {
-        const int w = (node + c) >> 6, off = (node + c) & 63;
-        const uint64_t low = mask ? word(w) >> off : 0, high = mask && off ? word(w + 1) << (64 - off) : 0;
-        const uint32_t see = (uint32_t)(low | high);
-        uint32_t v[32];
-        tmem_ld32(t + c, v);
-#pragma unroll
-        for (int e = 0; e < 32; ++e)
-            if (!(see >> e & 1)) v[e] = 0xff800000u;
-        tmem_st32(t + c, v);
-    }
+    const int w = node >> 6, off = node & 63;
+    return word(w) >> off | (off ? word(w + 1) << (64 - off) : 0ull);
 }
 
 template <int DP>
@@ -102,11 +90,11 @@ paged_wide_kernel(const __grid_constant__ CUtensorMap tQ, const __grid_constant_
         for (int t = 0; t < 2; ++t) {
             mbar_init(&sh->q_full[t], 1);
             mbar_init(&sh->q_free[t], 1);
-            mbar_init(&sh->s_full[t], 1);
-            mbar_init(&sh->s_free[t], 4);
-            mbar_init(&sh->p_full[t], 4);
-            mbar_init(&sh->p_half[t], 4);
-            mbar_init(&sh->pv_done[t], 1);
+            for (int h = 0; h < 2; ++h) {
+                mbar_init(&sh->s_full[t][h], 1);
+                mbar_init(&sh->p_full[t][h], 4);
+                mbar_init(&sh->pv_done[t][h], 1);
+            }
             mbar_init(&sh->o_free[t], 4);
             mbar_init(&sh->drain[t], 1);
         }
@@ -220,9 +208,9 @@ paged_wide_kernel(const __grid_constant__ CUtensorMap tQ, const __grid_constant_
             write_empty(p, sh->marks, nullptr, 0, 1, lane);
         } else if (elect_one()) {  // ---------------- products of tile t
             const int t = warp - kMmaWarp;
-            const uint32_t idesc_s = idesc_f16(128, 128, 1, 0, 0), idesc_o = idesc_f16(128, DP, 1, 0, 1);
+            const uint32_t idesc_s = idesc_f16(128, kStep, 1, 0, 0), idesc_o = idesc_f16(128, DP, 1, 0, 1);
             const uint64_t dq = sdesc(smem_u32(sQ + t * L::kTileBytes), 16, 1024, kSwizzle128B);
-            const uint32_t tS = tmem + 128 * t, tP = tmem + L::kP + L::kPStep * t, tO = tmem + L::kO + DP * t;
+            const uint32_t tS = tmem + 128 * t, tO = tmem + L::kO + DP * t;
             // the next K and the next V of the ring, whose entries come in pairs
             constexpr int kPairs = L::kStages / 2;
             struct At {
@@ -237,7 +225,7 @@ paged_wide_kernel(const __grid_constant__ CUtensorMap tQ, const __grid_constant_
             } ak, av;
             const uint64_t dk0 = sdesc(smem_u32(sKV), 16, 1024, kSwizzle128B),
                            dv0 = sdesc(smem_u32(sKV) + L::kTileBytes, 16384, 1024, kSwizzle128B);
-            int n = 0, ns = 0, items = 0;  // the tile's blocks with O, with S, and its items
+            int nb = 0, mb = 0, items = 0;  // the tile's blocks with S, with O, and its items
             bool ok = true;
             for (int k = 0; ok; ++k) {
                 const int slot = k % kAhead;
@@ -247,70 +235,68 @@ paged_wide_kernel(const __grid_constant__ CUtensorMap tQ, const __grid_constant_
                 if (it.seq < 0) break;
                 const Part x(p, it, t);
                 const int lo = x.lo, hi = x.hi;
-                // S of block j: once the last S has been read and, with P over S, its product is done
-                auto score = [&](int j) {
-                    uint64_t *full = &sh->full[2 * ak.s], *empty = &sh->empty[2 * ak.s];
-                    if (!thread_spin(full, ak.parity, p.status, 142, abort_flag)) return false;
-                    const uint64_t k = dk0 + (uint64_t)(ak.s * (int)(2 * L::kTileBytes >> 4));
-                    ak.next();
-                    if (j < lo || j >= hi) {
-                        mbar_arrive(empty);
-                        return true;
-                    }
-                    if (j == lo && !thread_spin(&sh->q_full[t], items & 1, p.status, 143, abort_flag)) return false;
-                    if (ns > 0 && !thread_spin(L::kSep ? &sh->s_free[t] : &sh->pv_done[t], (ns - 1) & 1, p.status, 144,
-                                               abort_flag))
-                        return false;
-                    ++ns;
+                // S of half h of block j, once the last product from that half's P is done
+                auto score = [&](int j, int h) {
+                    if (h == 0 && !thread_spin(&sh->full[2 * ak.s], ak.parity, p.status, 142, abort_flag)) return false;
+                    if (h == 0 && j == lo && !thread_spin(&sh->q_full[t], items & 1, p.status, 143, abort_flag)) return false;
+                    if (nb > 0 && !thread_spin(&sh->pv_done[t][h], (nb - 1) & 1, p.status, 144, abort_flag)) return false;
                     tc_fence_after();
+                    const uint64_t key = dk0 + (uint64_t)(ak.s * (int)(2 * L::kTileBytes >> 4) + h * (kStep * 128 >> 4));
 #pragma unroll
                     for (int y = 0; y < DP / 16; ++y) {
                         const uint64_t off = (uint64_t)((y >> 2) * 1024 + (y & 3) * 2);
-                        mma_ss(tS, dq + off, k + off, idesc_s, y > 0 ? 1u : 0u);
+                        mma_ss(tS + kStep * h, dq + off, key + off, idesc_s, y > 0 ? 1u : 0u);
                     }
-                    mma_commit(&sh->s_full[t]);
-                    mma_commit(empty);
-                    if (j == hi - 1) mma_commit(&sh->q_free[t]);
+                    mma_commit(&sh->s_full[t][h]);
+                    if (h == 1) {
+                        mma_commit(&sh->empty[2 * ak.s]);
+                        if (j == hi - 1) mma_commit(&sh->q_free[t]);
+                        ak.next();
+                        ++nb;
+                    }
                     return true;
                 };
-                // O += P.V of block j
-                auto output = [&](int j) {
-                    uint64_t *full = &sh->full[2 * av.s + 1], *empty = &sh->empty[2 * av.s + 1];
-                    if (!thread_spin(full, av.parity, p.status, 145, abort_flag)) return false;
-                    const uint64_t v = dv0 + (uint64_t)(av.s * (int)(2 * L::kTileBytes >> 4));
-                    av.next();
-                    if (j < lo || j >= hi) {
-                        mbar_arrive(empty);
-                        return true;
-                    }
-                    // P over S comes in halves of 64 keys: the first half's products run while the
-                    // other is in its exponentials
-                    if (!thread_spin(L::kSep ? &sh->p_full[t] : &sh->p_half[t], n & 1, p.status, 146, abort_flag))
-                        return false;
-                    if (j == lo && items > 0 && !thread_spin(&sh->o_free[t], (items - 1) & 1, p.status, 147, abort_flag))
+                // O += P.V of half h of block j
+                auto output = [&](int j, int h) {
+                    if (h == 0 && !thread_spin(&sh->full[2 * av.s + 1], av.parity, p.status, 145, abort_flag)) return false;
+                    if (!thread_spin(&sh->p_full[t][h], mb & 1, p.status, 146, abort_flag)) return false;
+                    if (h == 0 && j == lo && items > 0 &&
+                        !thread_spin(&sh->o_free[t], (items - 1) & 1, p.status, 147, abort_flag))
                         return false;
                     tc_fence_after();
+                    const uint64_t v = dv0 + (uint64_t)(av.s * (int)(2 * L::kTileBytes >> 4) + h * (kStep * 128 >> 4));
 #pragma unroll
-                    for (int y = 0; y < 4; ++y)
-                        mma_ts(tO, tP + 8 * y, v + (uint64_t)(128 * y), idesc_o, (j > lo || y > 0) ? 1u : 0u);
-                    if (!L::kSep) {
-                        if (!thread_spin(&sh->p_full[t], n & 1, p.status, 148, abort_flag)) return false;
-                        tc_fence_after();
+                    for (int y = 0; y < kStep / 16; ++y)
+                        mma_ts(tO, tS + kStep * h + 8 * y, v + (uint64_t)(128 * y), idesc_o, (j > lo || h > 0 || y > 0) ? 1u : 0u);
+                    mma_commit(&sh->pv_done[t][h]);
+                    if (h == 1) {
+                        mma_commit(&sh->empty[2 * av.s + 1]);
+                        av.next();
+                        ++mb;
                     }
-                    ++n;
-#pragma unroll
-                    for (int y = 4; y < 8; ++y) mma_ts(tO, tP + 8 * y, v + (uint64_t)(128 * y), idesc_o, 1u);
-                    mma_commit(&sh->pv_done[t]);
-                    mma_commit(empty);
                     return true;
                 };
-                // P beside S: S(j + 1) before O(j); P over S: after it
-                if (L::kSep) ok = score(it.lo);
-                for (int j = it.lo; j < it.hi && ok; ++j) {
-                    if (L::kSep) ok = (j + 1 >= it.hi || score(j + 1)) && output(j);
-                    else ok = score(j) && output(j);
+                // blocks that only the other tile sees
+                auto skip = [&](int from, int to) {
+                    for (int j = from; j < to; ++j) {
+                        if (!thread_spin(&sh->full[2 * ak.s], ak.parity, p.status, 148, abort_flag)) return false;
+                        mbar_arrive(&sh->empty[2 * ak.s]);
+                        ak.next();
+                        if (!thread_spin(&sh->full[2 * av.s + 1], av.parity, p.status, 158, abort_flag)) return false;
+                        mbar_arrive(&sh->empty[2 * av.s + 1]);
+                        av.next();
+                    }
+                    return true;
+                };
+                if (hi <= lo) {
+                    ok = skip(it.lo, it.hi);
+                    continue;
                 }
-                if (hi > lo) ++items;
+                ok = skip(it.lo, lo) && score(lo, 0);
+                for (int j = lo; j < hi && ok; ++j)
+                    ok = score(j, 1) && output(j, 0) && (j + 1 >= hi || score(j + 1, 0)) && output(j, 1);
+                ok = ok && skip(hi, it.hi);
+                ++items;
             }
             mma_commit(&sh->drain[t]);
             mbar_wait_drain(&sh->drain[t], 0);
@@ -320,8 +306,7 @@ paged_wide_kernel(const __grid_constant__ CUtensorMap tQ, const __grid_constant_
         setmaxnreg_inc<kMathRegs>();  // ---------------- softmax of one tile, one thread a row
         const int t = warp >> 2, row = tid & 127;
         const uint32_t lanes = (uint32_t)((warp & 3) * 32) << 16;
-        const uint32_t tS = tmem + 128 * t + lanes, tP = tmem + L::kP + L::kPStep * t + lanes,
-                       tO = tmem + L::kO + DP * t + lanes;
+        const uint32_t tS = tmem + 128 * t + lanes, tO = tmem + L::kO + DP * t + lanes;
         const float sl = p.scale_log2;
         // The row's position and head within the tile, worked out where they are needed (kept through the
         // loop they would cost registers there).
@@ -331,14 +316,12 @@ paged_wide_kernel(const __grid_constant__ CUtensorMap tQ, const __grid_constant_
             qi = r & (p.qbox - 1);
             head = r / p.qbox;
         };
-        int n = 0;  // the tile's blocks
+        int n = 0;  // the tile's steps: two a block
         bool ok = true;
-        // P.V of the tile's block before this one is done: P may be written over, O rescaled
-        auto last_product = [&](bool any) {
-            if (any) {
-                ok = warp_spin(&sh->pv_done[t], (n - 1) & 1, p.status, 149, abort_flag);
-                tc_fence_after();
-            }
+        // the product of the step before this one is done, and with it all of O so far
+        auto last_product = [&](int code) {
+            ok = warp_spin(&sh->pv_done[t][(n - 1) & 1], ((n - 1) >> 1) & 1, p.status, code, abort_flag);
+            tc_fence_after();
             return ok;
         };
         for (int k = 0;; ++k) {
@@ -361,14 +344,15 @@ paged_wide_kernel(const __grid_constant__ CUtensorMap tQ, const __grid_constant_
                 clean_lo = (it.sp.first(max(min(x.q0 + p.qbox, it.sp.Lq) - 1, 0)) + kTile - 1) / kTile;
             }
             float m = -INFINITY, l = 0.f;  // reference (of the raw scores), sum of 2^((s - m) sl)
-            for (int j = xlo; j < xhi; ++j, ++n) {
-                if (!warp_spin(&sh->s_full[t], n & 1, p.status, 150, abort_flag)) {
+            for (int u = 2 * xlo; u < 2 * xhi; ++u, ++n) {
+                const int j = u >> 1, h = u & 1;
+                if (!warp_spin(&sh->s_full[t][h], (n >> 1) & 1, p.status, 150, abort_flag)) {
                     ok = false;
                     break;
                 }
                 tc_fence_after();
                 const bool clean = j >= clean_lo && j < clean_hi;
-                if (!clean && (j + 1) * kTile > it.sp.Lk) {
+                if (!clean && h == 0 && (j + 1) * kTile > it.sp.Lk) {
                     // rows of V past the length may hold anything: P is 0 there, but 0 x NaN is not
                     // (both tiles' threads write the zeros; a product that reads them by then needs
                     // no others)
@@ -385,82 +369,55 @@ paged_wide_kernel(const __grid_constant__ CUtensorMap tQ, const __grid_constant_
                     }
                     fence_proxy_async_smem();
                 }
-                if (!warp_valid) {  // only takes part in the barriers
-                    __syncwarp();
-                    if (L::kSep && lane == 0) mbar_arrive(&sh->s_free[t]);
-                    // no second arrival on p_full before the other warps' first
-                    if (L::kSep && !last_product(j > xlo)) break;
-                    __syncwarp();
-                    if (!L::kSep && lane == 0) mbar_arrive(&sh->p_half[t]);
-                    if (lane == 0) mbar_arrive(&sh->p_full[t]);
-                    continue;
-                }
-                if (!clean) {
-                    // Masked keys (whatever they hold) become -inf in place, out of line: the few blocks
-                    // at a mask's edge must not widen the code of the others.
-                    const Part x(p, it, t);
-                    int qi, head;
-                    place(qi, head);
-                    const int k0 = j * kTile, i = x.q0 + qi, node0 = it.sp.Lk - it.sp.Lq;
-                    const bool valid = head < p.hbox && x.h0 + head < p.group && i < it.sp.Lq;
-                    const int first = valid ? it.sp.first(i) : 0, end = valid ? it.sp.end(i) : (1 << 30);
-                    if (__any_sync(0xffffffffu, first > k0 || end < k0 + kTile))
-                        sattn::mask_block(tS, first - k0, first < end ? end - first : 0);
-                    if (p.mask && k0 + kTile > node0)
-                        mask_nodes(tS, k0 - node0, valid ? p.mask + ((int64_t)it.seq * p.nq + i) * p.words : nullptr,
-                                   p.words);
-                }
-                uint32_t v[4][32];
+                if (warp_valid) {
+                    uint32_t va[32], vb[32];
+                    tmem_ld32_async(tS + kStep * h, va);
+                    tmem_ld32_async(tS + kStep * h + 32, vb);
+                    tmem_wait_ld(va);
+                    tie32(vb);
+                    if (!clean) {
+                        const Part x(p, it, t);
+                        int qi, head;
+                        place(qi, head);
+                        const int k0 = u * kStep, i = x.q0 + qi;
+                        if (head < p.hbox && x.h0 + head < p.group && i < it.sp.Lq) {
+                            const int a = it.sp.first(i) - k0, z = it.sp.end(i) - k0;
+                            uint64_t see = a <= 0 ? ~0ull : a < 64 ? ~0ull << a : 0ull;
+                            if (z < 64) see &= z > 0 ? ~(~0ull << z) : 0ull;
+                            if (p.mask)
+                                see &= nodes_seen(p.mask + ((int64_t)it.seq * p.nq + i) * p.words, p.words,
+                                                  k0 - (it.sp.Lk - it.sp.Lq));
+                            const uint32_t sa = (uint32_t)see, sb = (uint32_t)(see >> 32);
 #pragma unroll
-                for (int c = 0; c < 4; ++c) tmem_ld32_async(tS + 32 * c, v[c]);
-                tmem_wait_ld(v[0]);
-                tie32(v[1]);
-                tie32(v[2]);
-                tie32(v[3]);
-                if (L::kSep) {
-                    tc_fence_before();
-                    __syncwarp();
-                    if (lane == 0) mbar_arrive(&sh->s_free[t]);
-                }
-                const float mx = fmaxf(fmaxf(sattn::max_chunk(v[0]), sattn::max_chunk(v[1])),
-                                       fmaxf(sattn::max_chunk(v[2]), sattn::max_chunk(v[3])));
-                if (__any_sync(0xffffffffu, (mx - m) * sl > kOutgrown)) {
-                    if (!last_product(j > xlo)) break;
-                    const float mn = fmaxf(m, mx);
-                    const float f = mn == -INFINITY ? 1.f : ex2_approx((m - mn) * sl);
-                    l *= f;
-                    m = mn;
-                    if (j > xlo) sattn::rescale_output(tO, DP, f);
-                }
-                const float off = m == -INFINITY ? 0.f : -m * sl;
-                float2 sum0 = make_float2(0.f, 0.f), sum1 = sum0;
-                if (L::kSep) {
-                    // P beside S is written at the end: until then the last block's is in use
-                    uint32_t o[4][16];
-#pragma unroll
-                    for (int c = 0; c < 4; ++c) sattn::exp_chunk(v[c], o[c], sl, off, sum0, sum1);
-                    if (!last_product(j > xlo)) break;
-#pragma unroll
-                    for (int c = 0; c < 4; ++c) tmem_st16_async(tP + 16 * c, o[c]);
-                } else {
-#pragma unroll
-                    for (int c = 0; c < 4; ++c) {
-                        uint32_t o[16];
-                        sattn::exp_chunk(v[c], o, sl, off, sum0, sum1);
-                        tmem_st16_async(tP + 16 * c, o);
-                        if (c == 1) {
-                            tmem_wait_st();
-                            tc_fence_before();
-                            __syncwarp();
-                            if (lane == 0) mbar_arrive(&sh->p_half[t]);
+                            for (int e = 0; e < 32; ++e) {  // (whatever they hold)
+                                if (!(sa >> e & 1)) va[e] = 0xff800000u;
+                                if (!(sb >> e & 1)) vb[e] = 0xff800000u;
+                            }
                         }
                     }
+                    const float mx = fmaxf(sattn::max_chunk(va), sattn::max_chunk(vb));
+                    if (__any_sync(0xffffffffu, (mx - m) * sl > kOutgrown)) {
+                        const bool any = u > 2 * xlo;
+                        if (any && !last_product(149)) break;
+                        const float mn = fmaxf(m, mx);
+                        const float f = mn == -INFINITY ? 1.f : ex2_approx((m - mn) * sl);
+                        l *= f;
+                        m = mn;
+                        if (any) sattn::rescale_output(tO, DP, f);
+                    }
+                    const float off = m == -INFINITY ? 0.f : -m * sl;
+                    float2 sum0 = make_float2(0.f, 0.f), sum1 = sum0;
+                    uint32_t o[16];
+                    sattn::exp_chunk(va, o, sl, off, sum0, sum1);
+                    tmem_st16_async(tS + kStep * h, o);
+                    sattn::exp_chunk(vb, o, sl, off, sum0, sum1);
+                    tmem_st16_async(tS + kStep * h + 16, o);
+                    tmem_wait_st();
+                    l += (sum0.x + sum0.y) + (sum1.x + sum1.y);
                 }
-                tmem_wait_st();
                 tc_fence_before();
                 __syncwarp();
-                if (lane == 0) mbar_arrive(&sh->p_full[t]);
-                l += (sum0.x + sum0.y) + (sum1.x + sum1.y);
+                if (lane == 0) mbar_arrive(&sh->p_full[t][h]);
             }
             if (!ok) break;
             // O / l out of tensor memory; rows without keys give O = 0 and lse = -inf
@@ -474,8 +431,7 @@ paged_wide_kernel(const __grid_constant__ CUtensorMap tQ, const __grid_constant_
             const int64_t h = (int64_t)it.kvh * p.group + hg, pr = ((int64_t)it.slot * 2 + t) * kTile + row;
             __nv_bfloat16 *dst = p.out + it.seq * p.so.b + h * p.so.h + (int64_t)i * p.so.n;
             if (some) {
-                if (!warp_spin(&sh->pv_done[t], (n - 1) & 1, p.status, 152, abort_flag)) break;
-                tc_fence_after();
+                if (!last_product(152)) break;
 #pragma unroll 1
                 for (int c = 0; c < DP && warp_valid; c += 32) {
                     uint32_t o[32];
