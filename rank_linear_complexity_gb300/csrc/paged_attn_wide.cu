@@ -2,9 +2,18 @@
 // of prompts.  The products are those of softmax_attn_fwd.cu, queries as the 128 rows of a product
 // and a thread a row, two tiles of rows to a unit of work, which share the key blocks in shared
 // memory; blocks come page by page, and CTAs take equal runs of the list of blocks (paged_attn.cuh).
+//
+// A block of 128 keys is two steps of 64.  P stands over its own scores, and the other step's scores
+// are computed meanwhile; the chain product, softmax, product of one step hides behind the other's and
+// the other tile's (in blocks of 128 the next scores wait for the last product: a chunk of 2048 tokens
+// over 16384, 32 over 8 heads of 128, 770 us against 726, 1.42 PFLOP/s, at the power limit; trees of 64
+// nodes over 16 caches of up to 8192: 101 us against 99).  What bounds it then is the tensor pipe with
+// scores of 64 columns, whose query operand is loaded again for each (an estimated 3250 cycles of the
+// 3400 that a block of two tiles takes).  Two threads a row instead of one: 874 us (the scores do not
+// fit in the registers of sixteen warps and are read twice).
 //   warps 0-3, 4-7  softmax of tile 0 and tile 1: S out of tensor memory, P back
-//   warp 8          loads: goes through the CTA's run, tells the others each item, looks the pages up,
-//                   one thread issues the copies
+//   warp 8          loads: goes through the CTA's run, tells the others each item, looks the pages up
+//                   and issues a box a lane (one thread issuing all: tree, pages of 16, 116 us against 105)
 //   warps 9, 10     one thread each issues a tile's S = Q.K^T and O += P.V
 //   warp 11         rows without keys: O = 0, lse = -inf
 #include <cmath>
@@ -16,12 +25,7 @@ namespace linformer {
 namespace paged {
 namespace {
 
-// Twelve warps, 168 registers each at launch; the two warpgroups that do the arithmetic take registers
-// from the third.
 constexpr int kThreads = 384, kLoadWarp = 8, kMmaWarp = 9, kEmptyWarp = 11;
-constexpr uint32_t kLaunchRegs = 168, kMathRegs = 208, kIssueRegs = 88;
-static_assert(2 * kMathRegs + kIssueRegs == 3 * kLaunchRegs, "register split");
-
 constexpr int kStep = kTile / 2;  // keys of a step
 // Tensor memory: of each tile S of two steps (64 columns each), P over its own S, then O.
 template <int DP>
@@ -125,7 +129,6 @@ paged_wide_kernel(const __grid_constant__ CUtensorMap tQ, const __grid_constant_
     const uint32_t tmem = sh->tmem;
 
     if (warp >= kLoadWarp) {
-        setmaxnreg_dec<kIssueRegs>();
         if (warp == kLoadWarp) {  // ---------------- loads
             // a lane's box of a tile: `box` rows of a page, 64 columns
             const int bi = lane / (DP / 64), half = lane % (DP / 64);
@@ -134,11 +137,8 @@ paged_wide_kernel(const __grid_constant__ CUtensorMap tQ, const __grid_constant_
             const uint32_t dst = half * 16384u + row * 128u;
             int ring = 0, nq[2] = {0, 0};
             bool ok = true;
-            // (one lane waits: a function that is not inlined may not be called from warps of both register
-            // budgets, and the softmax calls the warps' wait)
             auto spin = [&](uint64_t *bar, uint32_t parity, int code) {
-                const bool done = lane != 0 || thread_spin(bar, parity, p.status, code, abort_flag);
-                return __shfl_sync(0xffffffffu, (int)done, 0) != 0;
+                return warp_spin(bar, parity, p.status, code, abort_flag);
             };
             Walk walk(p, sh->marks, blockIdx.x);
             const Walk begin = walk;
@@ -303,7 +303,7 @@ paged_wide_kernel(const __grid_constant__ CUtensorMap tQ, const __grid_constant_
         }
         __syncwarp();
     } else {
-        setmaxnreg_inc<kMathRegs>();  // ---------------- softmax of one tile, one thread a row
+        // ---------------- softmax of one tile, one thread a row
         const int t = warp >> 2, row = tid & 127;
         const uint32_t lanes = (uint32_t)((warp & 3) * 32) << 16;
         const uint32_t tS = tmem + 128 * t + lanes, tO = tmem + L::kO + DP * t + lanes;
