@@ -708,7 +708,7 @@ int attention(const AttnCall &call) {
     // Units of a few blocks at most stay whole: no workspace, no second kernel.
     constexpr int kWholeBlocks = 8;
     p.whole = (int64_t)p.width * p.page <= kWholeBlocks * kTile;
-    p.direct = p.whole && !wide && units * call.hk * call.b <= device_sms();
+    p.direct = p.whole && units * call.hk * call.b <= device_sms();
     const int seqs = (int)std::min<int64_t>(kMaxSeqs, 0x7fffffffLL / most);
     p.ntiles = (int)ntiles;
     p.units = (int)units;

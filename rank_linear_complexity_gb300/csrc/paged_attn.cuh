@@ -32,8 +32,7 @@ struct AttnParams {
     // N: rows of a tile in the workspace
     int qbox, hbox, nch, ntiles, per, units, N, ctas;
     int whole;   // no unit is cut
-    int direct;  // and each has a CTA of its own, by number (not in the wide kernel, which has no
-                 // register to spare: a chunk of 2048 764 us against 790)
+    int direct;  // and each has a CTA of its own, by number
     int pages, page, width, shift, box, nbox;  // nbox boxes of `box` rows make a block of keys
     float scale, scale_log2;
     int wide_stores;

@@ -123,7 +123,8 @@ paged_wide_kernel(const __grid_constant__ CUtensorMap tQ, const __grid_constant_
     tc_fence_before();
     wait_prerequisites();
     if (tid == 0) launch_dependents();  // the join, which waits for this grid's end
-    fill(p, sh->marks, tid, kThreads);
+    const Walk own = p.direct ? Walk(p) : Walk();
+    if (!p.direct) fill(p, sh->marks, tid, kThreads);
     __syncthreads();
     tc_fence_after();
     const uint32_t tmem = sh->tmem;
@@ -140,7 +141,7 @@ paged_wide_kernel(const __grid_constant__ CUtensorMap tQ, const __grid_constant_
             auto spin = [&](uint64_t *bar, uint32_t parity, int code) {
                 return warp_spin(bar, parity, p.status, code, abort_flag);
             };
-            Walk walk(p, sh->marks, blockIdx.x);
+            Walk walk = p.direct ? own : Walk(p, sh->marks, blockIdx.x);
             const Walk begin = walk;
             Shared::Told it;
             it.before = 0;
@@ -205,7 +206,7 @@ paged_wide_kernel(const __grid_constant__ CUtensorMap tQ, const __grid_constant_
             }
             __syncwarp();
         } else if (warp == kEmptyWarp) {
-            write_empty(p, sh->marks, nullptr, 0, 1, lane);
+            write_empty(p, sh->marks, p.direct ? &own : nullptr, 0, 1, lane);
         } else if (elect_one()) {  // ---------------- products of tile t
             const int t = warp - kMmaWarp;
             const uint32_t idesc_s = idesc_f16(128, kStep, 1, 0, 0), idesc_o = idesc_f16(128, DP, 1, 0, 1);
