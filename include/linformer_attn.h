@@ -353,6 +353,10 @@ LINFORMER_API int linformer_rotary_phase(uint64_t *phase, int rot, double base, 
  *
  * An entry outside [0, pages) where a row is needed, or a row behind the table's end, records a
  * failure in the device status word; no memory outside the cache is touched.
+ *
+ * The kernels of these calls let the next kernel in the stream launch early, and the attention's are
+ * launched with programmatic stream serialisation themselves; they wait before they read or write
+ * anything (as the forward's do, see Ownership above).
  */
 
 /*
@@ -395,7 +399,11 @@ LINFORMER_API int linformer_cache_keep(void *K_pages, const int64_t *K_pages_str
  * [0, width page]; the new tokens' rows among them), and Lq = q_lengths[beta] queries (NULL: nq).
  * Masks, rows without keys, rows past the lengths, sums and types are that call's: bf16, d a
  * multiple of 8 up to 128, strides multiples of 8.  Rows of the pages behind the length may hold
- * anything.  A page that is not there (see above) counts as rows of zeros.
+ * anything.  A page that is not there (see above) counts as rows of zeros.  Work is cut by rows of
+ * keys, not by sequences: units of work whose table holds more than 1024 rows may be joined from parts
+ * in a stream-ordered workspace.  The result of a call does not depend on timing.  The blocks of 128
+ * rows that the queries of one sequence go through, all tiles of queries and heads counted, have to be
+ * fewer than 2^31 (else LINFORMER_ERR_SIZE).
  */
 LINFORMER_API int linformer_paged_attn_fwd(
     const void *Q, const int64_t *Q_strides, const void *K_pages, const int64_t *K_pages_strides,

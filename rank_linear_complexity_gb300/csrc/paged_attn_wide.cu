@@ -6,11 +6,11 @@
 // A block of 128 keys is two steps of 64.  P stands over its own scores, and the other step's scores
 // are computed meanwhile; the chain product, softmax, product of one step hides behind the other's and
 // the other tile's (in blocks of 128 the next scores wait for the last product: a chunk of 2048 tokens
-// over 16384, 32 over 8 heads of 128, 770 us against 726, 1.42 PFLOP/s, at the power limit; trees of 64
-// nodes over 16 caches of up to 8192: 101 us against 99).  What bounds it then is the tensor pipe with
-// scores of 64 columns, whose query operand is loaded again for each (an estimated 3250 cycles of the
-// 3400 that a block of two tiles takes).  Two threads a row instead of one: 874 us (the scores do not
-// fit in the registers of sixteen warps and are read twice).
+// over 2 x 16384, 32 over 8 heads of 128, 770 us against 700 to 726, 1.42 to 1.47 PFLOP/s, at the power limit;
+// trees of 64 nodes over 16 caches of up to 8192: 101 us against 99).  The tensor pipe's arithmetic takes
+// 2048 of the about 3300 cycles of a block of two tiles; scores of 64 columns load their query operand
+// twice as often as scores of 128.  Two threads a row instead of one: 874 us (the scores do not fit in
+// the registers of sixteen warps and are read twice).
 //   warps 0-3, 4-7  softmax of tile 0 and tile 1: S out of tensor memory, P back
 //   warp 8          loads: goes through the CTA's run, tells the others each item, looks the pages up
 //                   and issues a box a lane (one thread issuing all: tree, pages of 16, 116 us against 105)
