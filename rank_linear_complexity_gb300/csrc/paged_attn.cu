@@ -195,7 +195,8 @@ paged_attn_kernel(const __grid_constant__ CUtensorMap tQ, const __grid_constant_
         while (ok && walk.next(p, sh->marks, it)) {
             const Rows r(p, it.unit);
             const int32_t *table = p.table + (int64_t)it.seq * p.width;
-            auto look = [&](int j) { return mine ? page_of(p, table, j, row, it.sp.Lk) : 0; };
+            const int low = it.sp.first(r.q0);
+            auto look = [&](int j) { return mine ? page_of(p, table, j, row, low, it.sp.Lk) : 0; };
             int page = look(it.lo);
             // (one token over 62 caches: 228 us; Q after the next item's first keys, which then do not wait for
             // the last scores, 232; Q in two buffers 229)

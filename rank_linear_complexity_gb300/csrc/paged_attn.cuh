@@ -275,10 +275,11 @@ __device__ __forceinline__ void write_empty(const AttnParams &p, const Marks &ma
 }
 
 // The page of rows `row` on of key block j of a sequence; p.pages, which lies outside the tensor map
-// and comes as zeros, where there is none.
-__device__ __forceinline__ int page_of(const AttnParams &p, const int32_t *table, int j, int row, int Lk) {
+// and comes as zeros, where there is none, or where every row is hidden: behind the length, or before
+// `low`, where the window of the unit's first query begins (such pages may long be another sequence's).
+__device__ __forceinline__ int page_of(const AttnParams &p, const int32_t *table, int j, int row, int low, int Lk) {
     const int at = j * kTile + row;
-    if (at >= Lk) return p.pages;
+    if (at >= Lk || at + p.box <= low) return p.pages;
     const int x = __ldg(table + (at >> p.shift));
     if ((unsigned)x < (unsigned)p.pages) return x;
     if (p.status) atomicExch(p.status, kBadPage);

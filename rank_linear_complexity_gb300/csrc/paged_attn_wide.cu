@@ -148,7 +148,8 @@ paged_wide_kernel(const __grid_constant__ CUtensorMap tQ, const __grid_constant_
             for (int k = 0; ok; ++k) {
                 const int slot = k % kAhead;
                 const bool more = walk.next(p, sh->marks, it);
-                int page = more && mine ? page_of(p, p.table + (int64_t)it.seq * p.width, it.lo, row, it.sp.Lk) : 0;
+                const int low = more ? it.sp.first(Rows(p, 2 * it.unit).q0) : 0;
+                int page = more && mine ? page_of(p, p.table + (int64_t)it.seq * p.width, it.lo, row, low, it.sp.Lk) : 0;
                 if (!more) it.seq = -1;
                 ok = k < kAhead || spin(&sh->taken[slot], (k / kAhead - 1) & 1, 153);
                 if (!ok) break;
@@ -181,7 +182,7 @@ paged_wide_kernel(const __grid_constant__ CUtensorMap tQ, const __grid_constant_
                 if (k == 0) load_q();
                 for (int j = lo; j < hi && ok; ++j) {
                     const int now = page, at = (j * kTile + row) & (p.page - 1);
-                    if (j + 1 < hi && mine) page = page_of(p, table, j + 1, row, Lk);
+                    if (j + 1 < hi && mine) page = page_of(p, table, j + 1, row, low, Lk);
                     for (int kv = 0; kv < 2 && ok; ++kv, ++ring) {
                         const int s = ring % L::kStages;
                         if (ring >= L::kStages) ok = spin(&sh->empty[s], (ring / L::kStages - 1) & 1, 141);

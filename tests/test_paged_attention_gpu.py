@@ -239,6 +239,28 @@ def test_pages_that_are_not_there():
         assert (np.abs(host64(lse) - want[1]) <= want[3]).all()
 
 
+@pytest.mark.parametrize("nq", [1, 5, 70, 300])
+@pytest.mark.parametrize("page", [8, 16, 64, 128])
+@pytest.mark.parametrize("gone", [-1, 0, 10 ** 6])
+def test_pages_before_the_window_may_be_gone(nq, page, gone):
+    """Entries of pages that no query's window reaches are another sequence's by now, or nobody's."""
+    for window, lengths in ((20, (1000, 333)), (129, (900, 1024)), (nq + 64, (1500, 700))):
+        kc, vc, table = cache(2, 2, 64, page, lengths, device=DEV, seed=3)
+        kc, vc = (torch.cat([x, torch.full_like(x[:1], float("nan"))]) for x in (kc, vc))
+        for i, n in enumerate(lengths):
+            first = max(0, n - nq + 1 - window)  # that the first query sees
+            table[i, :first // page] = kc.shape[0] - 1 if gone == 0 else gone
+        table = long_table(table, page)
+        Q = torch.randn(2, 4, nq, 64, device=DEV, generator=torch.Generator(device=DEV).manual_seed(nq)).to(BF)
+        O, lse = lf.paged_attention(Q, kc, vc, table, ints(list(lengths), DEV), window=window)
+        status()
+        # (hidden rows count as zeros in the oracle)
+        clean = [torch.nan_to_num(x) for x in (kc, vc)]
+        want = paged.forward(Q, *clean, table.tolist(), lengths, causal=True, window=window)
+        assert (np.abs(host64(O) - want[0]) <= want[2]).all()
+        assert (np.abs(host64(lse) - want[1]) <= want[3]).all()
+
+
 def test_pages_shared_by_sequences():
     kc, vc, table = cache(1, 2, 64, 16, [200], device=DEV, seed=8)
     table = long_table(table, 16)
