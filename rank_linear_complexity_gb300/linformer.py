@@ -341,7 +341,8 @@ def dense_attention(Q, K, V, lengths=None, out=None, stream=None):
 # that it makes belong to the stream, as those of any torch operation would.  Its inputs have to be
 # ready there, and kept until the stream has read them.
 
-_stride_table = {}  # (batch, head, row) strides -> int64[3]
+_stride_table = {}   # (batch, head, row) strides -> address of an int64[3]
+_stride_arrays = []  # which holds them
 
 
 def _strides(x):
@@ -349,14 +350,16 @@ def _strides(x):
     if x.is_contiguous():
         return None
     key = x.stride()
-    arr = _stride_table.get(key)
-    if arr is None:
+    at = _stride_table.get(key)
+    if at is None:
         if key[3] != 1:
             raise ValueError("the last dimension has to be contiguous")
+        arr = (ctypes.c_int64 * 3)(*key[:3])
         if len(_stride_table) >= 4096:
-            _stride_table.clear()
-        arr = _stride_table[key] = (ctypes.c_int64 * 3)(*key[:3])
-    return arr
+            return arr  # for this call alone: no entry is ever taken out, another call may hold it
+        _stride_arrays.append(arr)
+        at = _stride_table[key] = ctypes.addressof(arr)
+    return at
 
 
 def _current_on(device, stream):
