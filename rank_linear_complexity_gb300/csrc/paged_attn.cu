@@ -550,9 +550,15 @@ __global__ void __launch_bounds__(kJoinWarps * 32) join_kernel(const __grid_cons
         // a row is cut at the end of its first CTA's run, and goes on at the start of the others'
         auto slot = [&](int c) { return ((int64_t)(2 * c + (c == c0 ? 1 : 0)) * p.per + t) * p.N + x; };
         float m = -INFINITY;
-        for (int c = c0 + lane; c <= c1; c += 32) m = fmaxf(m, p.part_lse[slot(c)]);
+        bool nan = false;  // (fmaxf drops one, and a row of nothing else would pass for one without keys)
+        for (int c = c0 + lane; c <= c1; c += 32) {
+            const float part = p.part_lse[slot(c)];
+            m = fmaxf(m, part);
+            nan |= part != part;
+        }
 #pragma unroll
         for (int o = 16; o; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
+        if (__any_sync(0xffffffffu, nan)) m = NAN;
         float acc[E] = {}, sum = 0.f;
         if (m != -INFINITY) {
             // this warp's parts
@@ -589,7 +595,7 @@ __global__ void __launch_bounds__(kJoinWarps * 32) join_kernel(const __grid_cons
                 sum += shared[warp + o][E][lane];
             }
         }
-        const float inv = sum > 0.f ? 1.f / sum : 0.f;
+        const float inv = sum == 0.f ? 0.f : 1.f / sum;
         const int64_t h = (int64_t)kvh * p.group + hg;
         __nv_bfloat16 *dst = p.out + seq * p.so.b + h * p.so.h + (int64_t)i * p.so.n;
         if (!mine && lane * E < p.d) {

@@ -306,3 +306,30 @@ def test_a_cache_past_32_bits():
     status()
     for i, j in enumerate((900, 950, 999)):
         assert torch.equal(kc[ids[0], 0, i], K[0, 0, j]) and torch.equal(vc[ids[0], 0, i], V[0, 0, j])
+
+
+@pytest.mark.parametrize("nq", [1, 5, 70])
+def test_nan_queries_and_keys(nq):
+    """A row with NaN scores is NaN, whole or joined from parts; no other row is."""
+    kw = dict(b=2, hq=4, hk=2, nq=nq, k_lengths=(3000, 900), d=64, page=64)
+    _, _, (Q, kc, vc, table) = check_attention(**kw)
+    want = paged.forward(Q, kc, vc, table.tolist(), (3000, 900), causal=True)
+    bad = np.zeros((2, 4, nq), dtype=bool)
+
+    def check():
+        O, l = (host64(x) for x in lf.paged_attention(Q, kc, vc, table, ints((3000, 900), DEV)))
+        assert np.array_equal(np.isnan(O), np.broadcast_to(bad[..., None], O.shape))
+        assert np.array_equal(np.isnan(l), bad)
+        assert (np.abs(O - want[0])[~bad] <= want[2][~bad]).all()
+        assert (np.abs(l - want[1])[~bad] <= want[3][~bad]).all()
+        status()
+
+    Q = Q.clone()
+    Q[0, 1, nq - 1, 3] = float("nan")
+    bad[0, 1, nq - 1] = True
+    check()
+    # a key that the last query alone sees
+    kc = kc.clone()
+    kc[table[1, 899 // 64].long(), 1, 899 % 64, 5] = float("nan")
+    bad[1, 2:, nq - 1] = True
+    check()
