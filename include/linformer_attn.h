@@ -435,6 +435,23 @@ LINFORMER_API int linformer_tree_attn_fwd(
  * neither counts as a root and is recorded in the device status word).  n up to LINFORMER_TREE_NODES. */
 LINFORMER_API int linformer_tree_mask(const int32_t *parents, uint64_t *mask, int b, int n, void *stream);
 
+/* Calls that linformer_cache_packed makes. */
+typedef enum {
+    LINFORMER_PACKED_APPEND = 0, /* linformer_cache_append: 42 words */
+    LINFORMER_PACKED_KEEP = 1,   /* linformer_cache_keep: 21 words */
+    LINFORMER_PACKED_ATTN = 2,   /* linformer_paged_attn_fwd: 33 words */
+    LINFORMER_PACKED_TREE = 3    /* linformer_tree_attn_fwd: 32 words */
+} linformer_packed_call;
+
+/*
+ * The same calls with their arguments in one block of 64-bit words, for bindings that pay by the
+ * argument.  The words follow the call's own order: a pointer its address, strides three words behind
+ * their tensor's (always given; those of an absent tensor are not read), an integer its value (one
+ * that an int does not hold: LINFORMER_ERR_SIZE), amplitude and scale the bits of a double.  count:
+ * words in the block (else LINFORMER_ERR_VALUE).  The block is read before the call returns.
+ */
+LINFORMER_API int linformer_cache_packed(int call, const void *words, int count);
+
 /*
  * Largest number of bytes the library's workspace pool on the current device has had
  * in use at once since the pool was created or last reset; reset != 0 then sets the

@@ -1,6 +1,7 @@
 // Entry points of the paged key/value cache: argument checks, all on the host, before anything
 // is launched.
 #include <cmath>
+#include <cstring>
 
 #include "internal.cuh"
 #include "paged.cuh"
@@ -67,6 +68,27 @@ int check_attention(paged::AttnCall &c, const void *Q, const int64_t *Q_strides,
     c.scale = scale;
     return LINFORMER_OK;
 }
+
+// A block of arguments, one after the other.
+struct Words {
+    int64_t w[64];
+    int at = 0;
+    bool fits = true;  // every integer so far fits an int
+
+    template <typename T>
+    T *pointer() { return reinterpret_cast<T *>((uintptr_t)w[at++]); }
+    const int64_t *strides() { return w + (at += 3) - 3; }
+    int integer() {
+        const int64_t x = w[at++];
+        fits = fits && x >= INT32_MIN && x <= INT32_MAX;
+        return (int)x;
+    }
+    float real() {
+        double x;
+        std::memcpy(&x, w + at++, sizeof x);
+        return (float)x;
+    }
+};
 
 }  // namespace
 }  // namespace linformer
@@ -200,4 +222,71 @@ extern "C" int linformer_tree_mask(const int32_t *parents, uint64_t *mask, int b
     if (b < 1 || n < 1 || n > LINFORMER_TREE_NODES) return LINFORMER_ERR_SIZE;
     if (unaligned(parents, 4) || unaligned(mask, 8)) return LINFORMER_ERR_ALIGN;
     return paged::tree_mask(parents, mask, b, n, reinterpret_cast<cudaStream_t>(stream));
+}
+
+extern "C" int linformer_cache_packed(int call, const void *words, int count) {
+    if (!words) return LINFORMER_ERR_NULL;
+    static constexpr int kCount[] = {42, 21, 33, 32};
+    if (call < LINFORMER_PACKED_APPEND || call > LINFORMER_PACKED_TREE) return LINFORMER_ERR_ENUM;
+    if (count != kCount[call]) return LINFORMER_ERR_VALUE;
+    Words a;
+    std::memcpy(a.w, words, count * sizeof(int64_t));
+    if (call == LINFORMER_PACKED_APPEND) {
+        void *x[6];
+        const int64_t *sx[6];
+        for (int i = 0; i < 6; ++i) {  // K, V, K_pages, V_pages, Q, Y
+            x[i] = a.pointer<void>();
+            sx[i] = a.strides();
+        }
+        const auto table = a.pointer<int32_t>(), starts = a.pointer<int32_t>(), counts = a.pointer<int32_t>();
+        const auto phase = a.pointer<uint64_t>();
+        const auto positions = a.pointer<int32_t>();
+        int n[10];  // b, hq, hk, n, d, pages, page, width, rot, layout
+        for (int &y : n) y = a.integer();
+        const float amplitude = a.real();
+        const int dtype = a.integer();
+        const auto stream = a.pointer<void>();
+        if (!a.fits) return LINFORMER_ERR_SIZE;
+        return linformer_cache_append(x[0], sx[0], x[1], sx[1], x[2], sx[2], x[3], sx[3], x[4], sx[4], x[5], sx[5],
+                                      table, starts, counts, phase, positions, n[0], n[1], n[2], n[3], n[4], n[5],
+                                      n[6], n[7], n[8], n[9], amplitude, dtype, stream);
+    }
+    if (call == LINFORMER_PACKED_KEEP) {
+        const auto K = a.pointer<void>();
+        const auto sK = a.strides();
+        const auto V = a.pointer<void>();
+        const auto sV = a.strides();
+        const auto table = a.pointer<int32_t>(), starts = a.pointer<int32_t>(), path = a.pointer<int32_t>(),
+                   counts = a.pointer<int32_t>();
+        int n[8];  // b, hk, m, d, pages, page, width, dtype
+        for (int &y : n) y = a.integer();
+        const auto stream = a.pointer<void>();
+        if (!a.fits) return LINFORMER_ERR_SIZE;
+        return linformer_cache_keep(K, sK, V, sV, table, starts, path, counts, n[0], n[1], n[2], n[3], n[4], n[5],
+                                    n[6], n[7], stream);
+    }
+    const bool tree = call == LINFORMER_PACKED_TREE;
+    void *x[4];
+    const int64_t *sx[4];
+    for (int i = 0; i < 4; ++i) {  // Q, K_pages, V_pages, O
+        x[i] = a.pointer<void>();
+        sx[i] = a.strides();
+    }
+    const auto lse = a.pointer<float>();
+    const auto table = a.pointer<int32_t>(), k_lengths = a.pointer<int32_t>(), q_lengths = a.pointer<int32_t>();
+    const auto mask = tree ? a.pointer<uint64_t>() : nullptr;
+    int n[8];  // b, hq, hk, nq, d, pages, page, width
+    for (int &y : n) y = a.integer();
+    const float scale = a.real();
+    const int causal = tree ? 0 : a.integer(), window = tree ? 0 : a.integer();
+    const int dtype = a.integer();
+    const auto stream = a.pointer<void>();
+    if (!a.fits) return LINFORMER_ERR_SIZE;
+    if (tree)
+        return linformer_tree_attn_fwd(x[0], sx[0], x[1], sx[1], x[2], sx[2], x[3], sx[3], lse, table, k_lengths,
+                                       q_lengths, mask, n[0], n[1], n[2], n[3], n[4], n[5], n[6], n[7], scale, dtype,
+                                       stream);
+    return linformer_paged_attn_fwd(x[0], sx[0], x[1], sx[1], x[2], sx[2], x[3], sx[3], lse, table, k_lengths,
+                                    q_lengths, n[0], n[1], n[2], n[3], n[4], n[5], n[6], n[7], scale, causal, window,
+                                    dtype, stream);
 }

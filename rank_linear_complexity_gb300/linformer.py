@@ -10,6 +10,7 @@ from __future__ import annotations
 
 import ctypes
 import os
+import struct
 import threading
 
 from . import build as _build
@@ -38,7 +39,7 @@ SYMBOLS = [
     "linformer_pool_peak_bytes", "linformer_debug_wait_probe", "linformer_softmax_attn_fwd",
     "linformer_softmax_attn_bwd", "linformer_rotary", "linformer_rotary_phase",
     "linformer_cache_append", "linformer_cache_keep", "linformer_paged_attn_fwd",
-    "linformer_tree_attn_fwd", "linformer_tree_mask",
+    "linformer_tree_attn_fwd", "linformer_tree_mask", "linformer_cache_packed",
 ]
 
 
@@ -120,6 +121,8 @@ def lib() -> ctypes.CDLL:
             L.linformer_tree_attn_fwd.restype = _i
             L.linformer_tree_mask.argtypes = [_vp] * 2 + [_i] * 2 + [_vp]
             L.linformer_tree_mask.restype = _i
+            L.linformer_cache_packed.argtypes = [_i, ctypes.c_char_p, _i]
+            L.linformer_cache_packed.restype = _i
             L.linformer_kernel_name.argtypes = [_i]
             L.linformer_kernel_name.restype = ctypes.c_char_p
             _lib = L
@@ -599,7 +602,22 @@ def rotary(x, x2=None, phase=None, positions=None, start: int = 0, rot=None,
 # the pages of each sequence in order.  A page, path or tree on the device that is not there is
 # recorded in the device status word, as a wait that ran out is.
 
-# (torch's types are passed along: an import in each helper costs as much as its check)
+# (torch's types are passed along: an import in each helper costs as much as its check; arguments go in
+# one block: thirty of them one by one cost more than the call's launch)
+
+_PACKED_APPEND, _PACKED_KEEP, _PACKED_ATTN, _PACKED_TREE = 0, 1, 2, 3
+_append_words = struct.Struct("=39qd2q")
+_keep_words = struct.Struct("=21q")
+_attn_words = struct.Struct("=28qd4q")
+_tree_words = struct.Struct("=29qd2q")
+
+
+def _rows(x):
+    """A tensor's address and (batch or page, head, row) strides."""
+    batch, head, row, last = x.stride()
+    if last != 1 and not x.is_contiguous():
+        raise ValueError("the last dimension has to be contiguous")
+    return x.data_ptr(), batch, head, row
 
 def _check_cache(k_cache, v_cache, table, b, hk, d, dtype, int32):
     """(pages, page, width) of a cache that fits the call's tensors."""
@@ -621,9 +639,9 @@ def _check_cache(k_cache, v_cache, table, b, hk, d, dtype, int32):
 
 
 def _int32s(name, x, shape, int32):
-    """Address of a dense int32 tensor, None for None."""
+    """Address of a dense int32 tensor, 0 for None."""
     if x is None:
-        return None
+        return 0
     if x.shape != shape or x.dtype != int32 or not x.is_contiguous():
         _check_dense(name, x, shape, int32)
     return x.data_ptr()
@@ -658,9 +676,8 @@ def cache_append(K, V, k_cache, v_cache, table, starts, counts=None, Q=None, pha
     elif Q is not None or positions is not None or rot is not None:
         raise ValueError("phase: the table of rotary_phase() is needed to turn keys and queries")
     else:
-        rot = 0
-    pq = sq = py = sy = None
-    hq = 0
+        rot = phase = 0
+    hq, turned_rows = 0, (0,) * 8
     if Q is not None:
         turned = Q.shape
         hq = turned[1]
@@ -671,16 +688,15 @@ def cache_append(K, V, k_cache, v_cache, table, starts, counts=None, Q=None, pha
             out = torch.empty_like(Q)
         elif out.shape != turned or out.dtype != dtype:
             _check("out", out, turned, dtype)
-        pq, sq, py, sy = Q.data_ptr(), _strides(Q), out.data_ptr(), _strides(out)
+        turned_rows = _rows(Q) + _rows(out)
     elif out is not None:
         raise ValueError("out: Q is needed")
-    _call(lib().linformer_cache_append, device,
-          (K.data_ptr(), _strides(K), V.data_ptr(), _strides(V), k_cache.data_ptr(),
-           _strides(k_cache), v_cache.data_ptr(), _strides(v_cache), pq, sq, py, sy,
-           table.data_ptr(), _int32s("starts", starts, (b,), int32), _int32s("counts", counts, (b,), int32), phase,
-           _int32s("positions", positions, (b, n), int32), b, hq, hk, n, d, pages, page, width, rot, layout,
-           amplitude, BF16 if dtype is torch.bfloat16 else dtype_code(K), handle),
-          "linformer_cache_append")
+    words = _append_words.pack(
+        *_rows(K), *_rows(V), *_rows(k_cache), *_rows(v_cache), *turned_rows, table.data_ptr(),
+        _int32s("starts", starts, (b,), int32), _int32s("counts", counts, (b,), int32), phase,
+        _int32s("positions", positions, (b, n), int32), b, hq, hk, n, d, pages, page, width, rot, layout,
+        amplitude, BF16 if dtype is torch.bfloat16 else dtype_code(K), handle)
+    _call(lib().linformer_cache_packed, device, (_PACKED_APPEND, words, 42), "linformer_cache_append")
     return out
 
 
@@ -698,18 +714,17 @@ def cache_keep(k_cache, v_cache, table, starts, path, counts=None, stream=None):
         _sizes("path", path.shape)
     handle = _stream_of(device, v_cache, table, starts, path, counts)
     pages, page, width = _check_cache(k_cache, v_cache, table, b, hk, d, dtype, int32)
-    _call(lib().linformer_cache_keep, device,
-          (k_cache.data_ptr(), _strides(k_cache), v_cache.data_ptr(), _strides(v_cache),
-           table.data_ptr(), _int32s("starts", starts, (b,), int32), _int32s("path", path, (b, m), int32),
-           _int32s("counts", counts, (b,), int32), b, hk, m, d, pages, page, width,
-           BF16 if dtype is torch.bfloat16 else dtype_code(k_cache), handle),
-          "linformer_cache_keep")
+    words = _keep_words.pack(
+        *_rows(k_cache), *_rows(v_cache), table.data_ptr(), _int32s("starts", starts, (b,), int32),
+        _int32s("path", path, (b, m), int32), _int32s("counts", counts, (b,), int32), b, hk, m, d, pages, page, width,
+        BF16 if dtype is torch.bfloat16 else dtype_code(k_cache), handle)
+    _call(lib().linformer_cache_packed, device, (_PACKED_KEEP, words, 21), "linformer_cache_keep")
 
 
 def _over_pages(Q, k_cache, v_cache, table, k_lengths, q_lengths, scale, out, lse, mask, masks,
-                call, name):
+                call, block, name):
     """What paged_attention and tree_attention share; masks: the integers between scale and
-    dtype."""
+    dtype; block: the form of the packed call's arguments."""
     import torch
     shape, dtype, device, int32 = Q.shape, Q.dtype, Q.device, torch.int32
     b, hq, n, d = shape
@@ -733,13 +748,12 @@ def _over_pages(Q, k_cache, v_cache, table, k_lengths, q_lengths, scale, out, ls
         mask = (mask.data_ptr(),)
     if k_lengths is None:
         raise ValueError("k_lengths: the rows of each sequence are needed")
-    _call(call, device,
-          (Q.data_ptr(), _strides(Q), k_cache.data_ptr(), _strides(k_cache), v_cache.data_ptr(),
-           _strides(v_cache), out.data_ptr(), _strides(out), lse.data_ptr(), table.data_ptr(),
-           _int32s("k_lengths", k_lengths, (b,), int32), _int32s("q_lengths", q_lengths, (b,), int32),
-           *(mask or ()), b, hq, hk, n, d, pages, page, width,
-           d ** -0.5 if scale is None else scale, *masks,
-           BF16 if dtype is torch.bfloat16 else dtype_code(Q), handle), name)
+    words = block.pack(
+        *_rows(Q), *_rows(k_cache), *_rows(v_cache), *_rows(out), lse.data_ptr(), table.data_ptr(),
+        _int32s("k_lengths", k_lengths, (b,), int32), _int32s("q_lengths", q_lengths, (b,), int32),
+        *(mask or ()), b, hq, hk, n, d, pages, page, width, d ** -0.5 if scale is None else scale, *masks,
+        BF16 if dtype is torch.bfloat16 else dtype_code(Q), handle)
+    _call(lib().linformer_cache_packed, device, (call, words, block.size // 8), name)
     return out, lse
 
 
@@ -754,7 +768,7 @@ def paged_attention(Q, k_cache, v_cache, table, k_lengths, q_lengths=None, causa
                                    scale, out, lse)
     return _over_pages(Q, k_cache, v_cache, table, k_lengths, q_lengths, scale, out, lse, None,
                        (1 if causal else 0, _int32("window", window)),
-                       lib().linformer_paged_attn_fwd, "linformer_paged_attn_fwd")
+                       _PACKED_ATTN, _attn_words, "linformer_paged_attn_fwd")
 
 
 def tree_attention(Q, k_cache, v_cache, table, k_lengths, mask, q_lengths=None, scale=None,
@@ -769,7 +783,7 @@ def tree_attention(Q, k_cache, v_cache, table, k_lengths, mask, q_lengths=None, 
     if mask is None:
         raise ValueError("mask: the words of tree_mask() are needed")
     return _over_pages(Q, k_cache, v_cache, table, k_lengths, q_lengths, scale, out, lse, mask, (),
-                       lib().linformer_tree_attn_fwd, "linformer_tree_attn_fwd")
+                       _PACKED_TREE, _tree_words, "linformer_tree_attn_fwd")
 
 
 def tree_mask(parents, out=None, stream=None):

@@ -244,3 +244,59 @@ def test_kernels_are_counted():
         lf.linformer_profile_enable(False)
     assert seen["cache_kernels"][1] == 2 and seen["paged_attention_kernels"][1] == 6
     status()
+
+
+@pytest.mark.parametrize("dense", [False, True])
+def test_the_librarys_calls_one_argument_each(dense):
+    """The entry points themselves, which the binding reaches with its arguments in one block."""
+    import ctypes
+    L = lf.lib()
+    Q, kc, vc, table, lengths = problem(nq=20)
+    if dense:
+        kc, vc = kc.contiguous(), vc.contiguous()
+    b, hq, hk, n, d, page, width = 3, 8, 2, 20, 64, 16, table.shape[1]
+    K, V = (torch.randn(b, hk, n, d, device=DEV).to(BF) for _ in range(2))
+    starts, counts, phase = ints([600, 3, 1400], DEV), ints([20, 0, 7], DEV), lf.rotary_phase(d, device=DEV)
+    up = random_tree(3, n, seed=4)
+    mask, path = lf.tree_mask(up.to(DEV)), ints([[0, 3, 9]] * 3, DEV)
+
+    def strides(x):
+        return None if dense else ctypes.addressof(keep_alive.setdefault(id(x), (ctypes.c_int64 * 3)(*x.stride()[:3])))
+    keep_alive = {}
+
+    def run(own):
+        k, v = kc.clone(), vc.clone()
+        out, lse, turned = torch.empty_like(Q), torch.empty(b, hq, n, device=DEV), torch.empty_like(Q)
+        out2, lse2 = torch.empty_like(Q), torch.empty_like(lse)
+        stream = torch.cuda.current_stream().cuda_stream
+        pages = k.shape[0]
+        if own:
+            cache_args = [k.data_ptr(), strides(k), v.data_ptr(), strides(v)]
+            assert L.linformer_cache_append(
+                K.data_ptr(), None, V.data_ptr(), None, *cache_args, Q.data_ptr(), None, turned.data_ptr(), None,
+                table.data_ptr(), starts.data_ptr(), counts.data_ptr(), phase.data_ptr(), None, b, hq, hk, n, d, pages,
+                page, width, 32, 1, 1.25, 1, stream) == 0
+            head = [turned.data_ptr(), None, *cache_args]
+            tail = [b, hq, hk, n, d, pages, page, width, 0.2]
+            assert L.linformer_paged_attn_fwd(
+                *head, out.data_ptr(), None, lse.data_ptr(), table.data_ptr(), lengths.data_ptr(), counts.data_ptr(),
+                *tail, 1, 50, 1, stream) == 0
+            assert L.linformer_tree_attn_fwd(
+                *head, out2.data_ptr(), None, lse2.data_ptr(), table.data_ptr(), lengths.data_ptr(), None,
+                mask.data_ptr(), *tail, 1, stream) == 0
+            assert L.linformer_cache_keep(
+                *cache_args, table.data_ptr(), starts.data_ptr(), path.data_ptr(), counts.data_ptr(), b, hk, 3, d,
+                pages, page, width, 1, stream) == 0
+        else:
+            lf.cache_append(K, V, k, v, table, starts, counts=counts, Q=Q, phase=phase_words(32), rot=32,
+                            layout=lf.ROTARY_INTERLEAVED, amplitude=1.25, out=turned)
+            lf.paged_attention(turned, k, v, table, lengths, q_lengths=counts, window=50, scale=0.2, out=out, lse=lse)
+            lf.tree_attention(turned, k, v, table, lengths, mask, scale=0.2, out=out2, lse=lse2)
+            lf.cache_keep(k, v, table, starts, path, counts=counts)
+        status()
+        return k, v, turned, out, out2, lse, lse2
+
+    def phase_words(rot):
+        return phase[:rot // 2].contiguous()
+    for x, y in zip(run(True), run(False)):
+        assert torch.equal(bits(x), bits(y))

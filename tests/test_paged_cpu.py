@@ -119,6 +119,65 @@ def test_refusals_of_one_of_the_two(L):
         assert L.linformer_tree_mask(*args, 0) == want
 
 
+def packed(L, call, words, count=None):
+    import struct
+    block = b"".join(struct.pack("=d" if isinstance(x, float) else "=q", x) for x in words)
+    return L.linformer_cache_packed(call, block, len(words) if count is None else count)
+
+
+def rows(address, *s):
+    return [address, *(s or (6144, 1024, 64))]
+
+
+PACKED = {
+    "append": (0, rows(A) + rows(2 * A) + rows(3 * A) + rows(4 * A) + rows(5 * A) + rows(6 * A) + [A, A, 0, A, 0]
+               + [2, 4, 2, 3, 64, 9, 16, 4, 64, 0, 1.0, 1, 0]),
+    "keep": (1, rows(A) + rows(2 * A) + [A, A, A, 0] + [2, 2, 3, 64, 9, 16, 4, 1, 0]),
+    "attend": (2, rows(A) + rows(2 * A) + rows(3 * A) + rows(4 * A) + [A, A, A, 0]
+               + [2, 4, 2, 3, 64, 9, 16, 4, 0.1, 1, 0, 1, 0]),
+    "tree": (3, rows(A) + rows(2 * A) + rows(3 * A) + rows(4 * A) + [A, A, A, 0, A]
+             + [2, 4, 2, 3, 64, 9, 16, 4, 0.1, 1, 0]),
+}
+
+
+@pytest.mark.parametrize("name", PACKED)
+def test_packed_refusals(L, name):
+    """Every word is where the call's own argument is: a wrong value there gives that call's status."""
+    call, words = PACKED[name]
+    n = len(words)
+
+    def wrong(at, value):
+        return packed(L, call, [value if i == at else x for i, x in enumerate(words)])
+    tensors = {"append": 6, "keep": 2}.get(name, 4)
+    ints_from = next(i for i, x in enumerate(words) if i >= 4 * tensors and 0 < x < A)
+    real = {"append": n - 3, "attend": n - 5, "tree": n - 3}.get(name)
+    dtype = n - 2
+    for t in range(tensors):
+        assert wrong(4 * t, 0) == NULL and wrong(4 * t, words[4 * t] + 8) == ALIGN
+        for k in range(3):
+            assert wrong(4 * t + 1 + k, -64) == VALUE, (t, k)
+    for at in range(4 * tensors, ints_from):
+        assert wrong(at, A + 1) == ALIGN
+        if words[at]:
+            assert wrong(at, 0) == NULL
+    for at in range(ints_from, n - 1):
+        if at != real:
+            for x in (1 << 31, -(1 << 31) - 1, 1 << 32, (1 << 32) + words[at]):
+                assert wrong(at, x) == SIZE, at
+    sizes = 8 if name != "keep" else 7
+    for at in range(ints_from, ints_from + sizes):
+        assert wrong(at, -1) == SIZE
+    if real:
+        assert wrong(real, math.nan) == VALUE
+    assert wrong(dtype, 9) == ENUM
+    for at, x in {"append": ((n - 5, 65), (n - 4, 2)), "attend": ((n - 4, 2), (n - 3, -1)), "tree": ((ints_from + 3, 1025),),
+                  "keep": ()}[name]:
+        assert wrong(at, x) in (VALUE, ENUM, SIZE)
+    assert packed(L, call, words, n - 1) == VALUE and packed(L, call, words + [0]) == VALUE
+    assert packed(L, 4, words) == ENUM and packed(L, -1, words) == ENUM
+    assert L.linformer_cache_packed(call, None, n) == NULL
+
+
 # --- refusals of the binding -----------------------------------------------------------------
 
 def test_binding_refuses_host_tensors():
