@@ -636,7 +636,7 @@ int launch_with_join(Kernel kernel, int threads, uint32_t smem, int slot, const 
         return LINFORMER_ERR_LAUNCH;
     char *ws = nullptr;
     if (!p.whole) {
-        const size_t head = p.ctas * sizeof(int4);  // (parts are read 16 bytes at a time)
+        const size_t head = (p.ctas * sizeof(int4) + 31) / 32 * 32;  // (parts are written 32 bytes at a time)
         const size_t parts = (size_t)2 * p.ctas * p.per * p.N;
         if (workspace_alloc(reinterpret_cast<void **>(&ws), head + parts * (dp + 1) * sizeof(float), c.stream) !=
             LINFORMER_OK)

@@ -443,9 +443,10 @@ paged_wide_kernel(const __grid_constant__ CUtensorMap tQ, const __grid_constant_
                     if (!whole) {
                         if (dead) continue;
 #pragma unroll
-                        for (int e = 0; e < 32; e += 4)
-                            *reinterpret_cast<uint4 *>(p.part_o + pr * DP + c + e) =
-                                make_uint4(o[e], o[e + 1], o[e + 2], o[e + 3]);
+                        for (int e = 0; e < 32; e += 8) {
+                            const uint32_t w[8] = {o[e], o[e + 1], o[e + 2], o[e + 3], o[e + 4], o[e + 5], o[e + 6], o[e + 7]};
+                            sattn::store32(p.part_o + pr * DP + c + e, w);
+                        }
                     } else if (exists) {
 #pragma unroll
                         for (int e = 0; e < 32; e += 16) {
