@@ -3,7 +3,7 @@
 // append: the new rows of each sequence go to the rows of the cache that follow its `start`,
 // keys turned to their positions, and the queries that stand at the same positions are turned
 // beside them (the turn of rotary.cu, formed in fp32 and rounded once).  Bound by memory: every
-// element read and written once (8 x 4096 ragged rows of 32 + 8 + 8 heads of 128, bf16: 129 us, 5.5
+// element read and written once (8 x 4096 ragged rows of 32 + 8 + 8 heads of 128, bf16: 122 us, 5.9
 // TB/s).  A thread keeps the sines of its pairs and goes through several heads with them.
 //
 // keep: of a tree of drafted tokens, the rows of the accepted ones move up behind the sequence's
@@ -12,6 +12,7 @@
 //
 // tree_mask: which nodes each node of a tree sees, itself and its ancestors.
 #include <algorithm>
+#include <cstring>
 #include <cuda_bf16.h>
 
 #include "internal.cuh"
@@ -29,8 +30,8 @@ using rotary::Vec;
 
 constexpr int kThreads = 128;
 // Heads of a thread in flight, and blocks of an SM: registers for 32 warps (8 x 4096 ragged rows of 32 + 8
-// + 8 heads of 128: 129 us; one head 155, four heads and the registers that they take 158, in 80
-// registers 212; 40 warps 160).
+// + 8 heads of 128, before the stores past L1: 129 us; one head 155, four heads and the registers that they
+// take 158, in 80 registers 212; 40 warps 160).
 constexpr int kBatch = 2, kBlocks = 8;
 constexpr int kMaxHeads = 16;  // heads of one thread
 
@@ -47,6 +48,28 @@ struct AppendParams {
     float amplitude;
     int *status;
 };
+
+// A piece as one access of 16 bytes, stores past L1 (8 x 4096 ragged rows as above: 131 us with plain ones,
+// 122 so, 123 with stores that L2 is to drop first).
+template <typename Piece>
+__device__ __forceinline__ Piece load_piece(const void *from) {
+    if constexpr (sizeof(Piece) != 16) return *static_cast<const Piece *>(from);
+    else {
+        const uint4 w = *static_cast<const uint4 *>(from);
+        Piece x;
+        memcpy(&x, &w, sizeof x);
+        return x;
+    }
+}
+template <typename Piece>
+__device__ __forceinline__ void store_piece(void *to, const Piece &x) {
+    if constexpr (sizeof(Piece) != 16) *static_cast<Piece *>(to) = x;
+    else {
+        uint4 w;
+        memcpy(&w, &x, sizeof w);
+        __stcg(static_cast<uint4 *>(to), w);
+    }
+}
 
 // V pairs a thread (V = 1: any strides and sizes; otherwise 16-byte pieces).
 template <typename T, int V, bool kInterleaved>
@@ -91,8 +114,8 @@ __global__ void __launch_bounds__(kThreads, kBlocks) append_kernel(const AppendP
 #pragma unroll
             for (int k = 0; k < kBatch; ++k) {
                 if (h + k >= last) continue;
-                u0[k] = *reinterpret_cast<const Piece *>(x + k * sx.h + at0);
-                if (turn) u1[k] = *reinterpret_cast<const Piece *>(x + k * sx.h + at1);
+                u0[k] = load_piece<Piece>(x + k * sx.h + at0);
+                if (turn) u1[k] = load_piece<Piece>(x + k * sx.h + at1);
             }
 #pragma unroll
             for (int k = 0; k < kBatch; ++k) {
@@ -110,9 +133,9 @@ __global__ void __launch_bounds__(kThreads, kBlocks) append_kernel(const AppendP
                             z = from_float<T>(fz * cs[v] + fa * sn[v]);
                         }
                     }
-                    *reinterpret_cast<Piece *>(y + k * sy.h + at1) = u1[k];
+                    store_piece(y + k * sy.h + at1, u1[k]);
                 }
-                *reinterpret_cast<Piece *>(y + k * sy.h + at0) = u0[k];
+                store_piece(y + k * sy.h + at0, u0[k]);
             }
         }
     };
