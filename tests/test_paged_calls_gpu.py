@@ -300,3 +300,25 @@ def test_the_librarys_calls_one_argument_each(dense):
         return phase[:rot // 2].contiguous()
     for x, y in zip(run(True), run(False)):
         assert torch.equal(bits(x), bits(y))
+
+
+@pytest.mark.parametrize("nq", [1, 80])
+def test_dimensions_of_one_entry_may_have_any_stride(nq):
+    """Their strides are never used: those that views leave there are no multiples of anything."""
+    Q, kc, vc, table, lengths = problem(b=1, hq=4, hk=1, nq=nq, lengths=(500,))
+    phase, K = lf.rotary_phase(64, device=DEV), torch.randn(1, 1, 1, 64, device=DEV).to(BF)
+
+    def odd(x):
+        return x.as_strided(x.shape, [s if n > 1 or i == 3 else 5 - 5 * (i == 1)
+                                      for i, (n, s) in enumerate(zip(x.shape, x.stride()))])
+    got = []
+    for view in (lambda x: x, odd):
+        k, v, q, x = kc.clone(), vc.clone(), Q.clone(), K.clone()
+        turned = lf.cache_append(view(x), view(x), view(k), view(v), table, ints([499], DEV),
+                                 Q=view(q[:, :, :1].contiguous()), phase=phase)
+        out = lf.paged_attention(view(q), view(k), view(v), table, lengths, out=view(torch.empty_like(q)))
+        lf.cache_keep(view(k), view(v), table, ints([490], DEV), ints([[0, 4]], DEV))
+        status()
+        got.append((turned, *out, k, v))
+    for a, b in zip(*got):
+        assert torch.equal(bits(a), bits(b))
