@@ -630,9 +630,13 @@ int launch_rows(const AttnCall &c, AttnParams &p) {
 int launch_with_join(Kernel kernel, int threads, uint32_t smem, int slot, const AttnCall &c, AttnParams &p, int dp) {
     CUtensorMap q, k, v;
     const Cache &cache = c.cache;
+    // Rows of the caches are fetched 64 bytes at a time, not 256: what lies behind a short row is another
+    // head's, or comes with its own box (one token, rows of 64 elements side by side with 11 other heads: 104
+    // us and 84; of 40 with 7: 204 and 143, with 128 bytes 176; of 96 with 2: 72 and 62; of 128: 231 both).
+    constexpr CUtensorMapL2promotion kFetch = CU_TENSOR_MAP_L2_PROMOTION_L2_64B;
     if (!sattn::encode_rows(&q, c.q, c.sq, c.b, c.hq, p.group, c.nq, c.d, p.qbox, p.hbox) ||
-        !sattn::encode_rows(&k, cache.k, cache.sk, cache.pages, c.hk, 1, cache.page, c.d, p.box, 1) ||
-        !sattn::encode_rows(&v, cache.v, cache.sv, cache.pages, c.hk, 1, cache.page, c.d, p.box, 1))
+        !sattn::encode_rows(&k, cache.k, cache.sk, cache.pages, c.hk, 1, cache.page, c.d, p.box, 1, kFetch) ||
+        !sattn::encode_rows(&v, cache.v, cache.sv, cache.pages, c.hk, 1, cache.page, c.d, p.box, 1, kFetch))
         return LINFORMER_ERR_LAUNCH;
     char *ws = nullptr;
     if (!p.whole) {

@@ -119,9 +119,11 @@ __device__ __forceinline__ void zero_rows(uint8_t *tile, int row0, int idx, int 
 
 // Host helpers (softmax_attn_fwd.cu).
 // Map of a [b][heads][n][d] bf16 tensor for boxes of 64 columns x `rows` rows x `hrows`
-// heads of a group of `group`: coordinates (column, row, head in group, group, batch).
+// heads of a group of `group`: coordinates (column, row, head in group, group, batch).  promotion: what
+// L2 fetches at a time.
 bool encode_rows(CUtensorMap *m, const void *base, const Strides &s, int b, int heads, int group,
-                 int n, int d, int rows, int hrows);
+                 int n, int d, int rows, int hrows,
+                 CUtensorMapL2promotion promotion = CU_TENSOR_MAP_L2_PROMOTION_L2_256B);
 int allow_smem(const void *kernel, uint32_t bytes, int slot);
 
 int forward(const Call &c);

@@ -717,7 +717,7 @@ int launch(const Call &c, FwdParams &p) {
 }  // namespace
 
 bool encode_rows(CUtensorMap *m, const void *base, const Strides &s, int b, int heads, int group,
-                 int n, int d, int rows, int hrows) {
+                 int n, int d, int rows, int hrows, CUtensorMapL2promotion promotion) {
     std::call_once(g_encode_once, [] {
         void *fn = nullptr;
         cudaDriverEntryPointQueryResult q{};
@@ -737,7 +737,7 @@ bool encode_rows(CUtensorMap *m, const void *base, const Strides &s, int b, int 
     cuuint32_t one[5] = {1, 1, 1, 1, 1};
     return g_encode(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 5, const_cast<void *>(base), dims, strides, box,
                     one, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
-                    CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+                    promotion, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
 // The kernel's shared memory, allowed once per device (slot: one per kernel).
