@@ -526,84 +526,111 @@ paged_attn_kernel(const __grid_constant__ CUtensorMap tQ, const __grid_constant_
 }
 
 // Joins the parts of the rows whose run of blocks was cut: lse = log sum_s exp(lse_s), O = sum_s
-// exp(lse_s - lse) O_s, in the parts' order.  blockIdx.x: the CTA that did the last part (any other's
-// blocks leave at once).  kEach warps a row: more than one where units are few and their parts many
-// (4 units of 1024 blocks, 38 parts each: 20 us with one warp, 8 with four).
-constexpr int kJoinWarps = 4, kJoinBlocks = 32;
+// exp(lse_s - lse) O_s, in the parts' order.  Bound by latency: each block lists the cut units, the rows of
+// all of them are dealt out evenly, and a row's parts come kAtOnce at a time, weights and values together
+// (a block a unit and 32nd of its rows, weights before values: 884 tokens of 8 heads of 40, window 5470, 45 us
+// in all and 38 so; 16 x 5 tokens over 6001 rows, window 4095, 26.3 and 24.9; trees of 64 97.3 and 95.0.  Eight
+// at a time: 37, 24.5, 99; 2 blocks an SM of eight at a time: trees 106).
+// DP / 4 lanes a row; kEach warps a row where units are few and their parts many (4 units of 1024 blocks,
+// 38 parts each).
+constexpr int kJoinWarps = 8, kJoinThreads = kJoinWarps * 32, kJoinBlocks = 8;  // blocks an SM
 template <int DP, int kEach>
-__global__ void __launch_bounds__(kJoinWarps * 32) join_kernel(const __grid_constant__ AttnParams p) {
-    constexpr int E = DP / 32;
-    __shared__ float shared[kEach > 1 ? kJoinWarps : 1][E + 1][32];
+__global__ void __launch_bounds__(kJoinThreads, 4) join_kernel(const __grid_constant__ AttnParams p) {
+    constexpr int kLanes = DP / 4, kRows = 32 / kLanes * kJoinWarps / kEach, kAtOnce = 4;
+    __shared__ int4 units[kJoinThreads];
+    __shared__ int last[kJoinThreads], counts[kJoinWarps];
+    __shared__ float shared[kEach > 1 ? kJoinWarps : 1][6][32];
     launch_dependents();
     wait_prerequisites();
-    const int rows = p.qbox * p.hbox, lane = threadIdx.x & 31, warp = threadIdx.x >> 5, mine = warp % kEach;
-    const int4 cut = p.cuts[blockIdx.x];
-    if (cut.x < 0) return;
-    const int seq = cut.x, kvh = cut.z, c0 = cut.w, c1 = blockIdx.x;
-    constexpr int kRows = kJoinWarps / kEach;  // of a block at a time
-#pragma unroll 1
-    for (int y = blockIdx.y * kRows + warp / kEach; y < p.per * rows; y += gridDim.y * kRows) {
-        const int t = y / rows, x = y - t * rows, tile = cut.y * p.per + t;
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, mine = warp % kEach;
+    const int4 cut = tid < p.ctas ? p.cuts[tid] : make_int4(-1, 0, 0, 0);
+    const unsigned some = __ballot_sync(0xffffffffu, cut.x >= 0);
+    if (lane == 0) counts[warp] = __popc(some);
+    __syncthreads();
+    int n = 0, before = 0;
+    for (int w = 0; w < kJoinWarps; ++w) {
+        before += w < warp ? counts[w] : 0;
+        n += counts[w];
+    }
+    if (cut.x >= 0) {
+        const int at = before + __popc(some & ((1u << lane) - 1));
+        units[at] = cut;
+        last[at] = tid;
+    }
+    __syncthreads();
+    const int rows = p.qbox * p.hbox, all = p.per * rows, total = n * all, col = lane % kLanes * 4;
+    for (int first = blockIdx.x * kRows; first < total; first += gridDim.x * kRows) {  // (a block's warps alike)
+        const int row = first + warp / kEach * (32 / kLanes) + lane / kLanes, u = min(row, total - 1) / all,
+                  y = min(row, total - 1) - u * all, t = y / rows, x = y - t * rows;
+        const int4 unit = units[u];
+        const int c0 = unit.w, c1 = last[u], tile = unit.y * p.per + t;
         const Rows r(p, tile);
         const int i = r.q0 + (x & (p.qbox - 1)), hg = r.h0 + x / p.qbox;
-        if (tile >= p.ntiles || hg >= p.group || i >= p.nq) continue;  // (all warps of a row alike)
+        const bool exists = row < total && tile < p.ntiles && hg < p.group && i < p.nq;
         // a row is cut at the end of its first CTA's run, and goes on at the start of the others'
         auto slot = [&](int c) { return ((int64_t)(2 * c + (c == c0 ? 1 : 0)) * p.per + t) * p.N + x; };
-        float m = -INFINITY;
-        bool nan = false;  // (fmaxf drops one, and a row of nothing else would pass for one without keys)
-        for (int c = c0 + lane; c <= c1; c += 32) {
-            const float part = p.part_lse[slot(c)];
-            m = fmaxf(m, part);
-            nan |= part != part;
-        }
+        const int each = (c1 + 1 - c0 + kEach - 1) / kEach, from = c0 + mine * each, to = exists ? min(c1 + 1, from + each) : 0;
+        float m = -INFINITY, sum = 0.f, acc[4] = {};
+        for (int c = from; c < to; c += kAtOnce) {
+            float ls[kAtOnce];
+            float4 v[kAtOnce];
 #pragma unroll
-        for (int o = 16; o; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
-        if (__any_sync(0xffffffffu, nan)) m = NAN;
-        float acc[E] = {}, sum = 0.f;
-        if (m != -INFINITY) {
-            // this warp's parts
-            const int per = (c1 + 1 - c0 + kEach - 1) / kEach, first = c0 + mine * per, last = min(c1 + 1, first + per);
-            for (int c = first; c < last; c += 32) {
-                const int some = min(32, last - c);
-                const float weight = lane < some ? __expf(p.part_lse[slot(c + lane)] - m) : 0.f;
-#pragma unroll 8
-                for (int k = 0; k < some; ++k) {
-                    const float w = __shfl_sync(0xffffffffu, weight, k);
-                    sum += w;
-                    float v[E];
-                    const float *from = p.part_o + slot(c + k) * DP + lane * E;
-                    if constexpr (E == 4) {
-                        const float4 y = *reinterpret_cast<const float4 *>(from);
-                        v[0] = y.x, v[1] = y.y, v[2] = y.z, v[3] = y.w;
-                    } else {
-                        const float2 y = *reinterpret_cast<const float2 *>(from);
-                        v[0] = y.x, v[1] = y.y;
-                    }
-#pragma unroll
-                    for (int e = 0; e < E; ++e) acc[e] += w == 0.f ? 0.f : w * v[e];  // (a part without keys wrote no O)
+            for (int k = 0; k < kAtOnce; ++k) {
+                if (c + k >= to) {
+                    ls[k] = -INFINITY;
+                    continue;
                 }
+                const int64_t at = slot(c + k);
+                ls[k] = p.part_lse[at];
+                v[k] = *reinterpret_cast<const float4 *>(p.part_o + at * DP + col);
+            }
+            float mn = m;
+#pragma unroll
+            for (int k = 0; k < kAtOnce; ++k) mn = fmaxf(mn, ls[k]);
+            // (fmaxf drops a NaN, its weight does not)
+            const float f = m == mn ? 1.f : __expf(m - mn);
+            m = mn;
+            sum *= f;
+#pragma unroll
+            for (int e = 0; e < 4; ++e) acc[e] *= f;
+#pragma unroll
+            for (int k = 0; k < kAtOnce; ++k) {
+                if (ls[k] == -INFINITY) continue;  // (a part without keys wrote no O)
+                const float w = __expf(ls[k] - m);
+                sum += w;
+                acc[0] += w * v[k].x, acc[1] += w * v[k].y, acc[2] += w * v[k].z, acc[3] += w * v[k].w;
             }
         }
         if constexpr (kEach > 1) {
+            shared[warp][0][lane] = m;
+            shared[warp][1][lane] = sum;
 #pragma unroll
-            for (int e = 0; e < E; ++e) shared[warp][e][lane] = acc[e];
-            shared[warp][E][lane] = sum;
+            for (int e = 0; e < 4; ++e) shared[warp][2 + e][lane] = acc[e];
             __syncthreads();
-            for (int o = 1; o < kEach && !mine; ++o) {
+            if (mine == 0) {
+                float top = m;
+                for (int o = 1; o < kEach; ++o) top = fmaxf(top, shared[warp + o][0][lane]);
+                sum = 0.f;
 #pragma unroll
-                for (int e = 0; e < E; ++e) acc[e] += shared[warp + o][e][lane];
-                sum += shared[warp + o][E][lane];
+                for (int e = 0; e < 4; ++e) acc[e] = 0.f;
+                for (int o = 0; o < kEach; ++o) {
+                    const float mo = shared[warp + o][0][lane], f = mo == top ? 1.f : __expf(mo - top);
+                    sum += f * shared[warp + o][1][lane];
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) acc[e] += f * shared[warp + o][2 + e][lane];
+                }
+                m = top;
             }
         }
-        const float inv = sum == 0.f ? 0.f : 1.f / sum;
-        const int64_t h = (int64_t)kvh * p.group + hg;
-        __nv_bfloat16 *dst = p.out + seq * p.so.b + h * p.so.h + (int64_t)i * p.so.n;
-        if (!mine && lane * E < p.d) {
-#pragma unroll
-            for (int e = 0; e < E; e += 2)
-                *reinterpret_cast<uint32_t *>(dst + lane * E + e) = pack2(acc[e] * inv, acc[e + 1] * inv);
+        if (mine == 0 && exists) {
+            const float inv = sum == 0.f ? 0.f : 1.f / sum;
+            const int64_t h = (int64_t)unit.z * p.group + hg;
+            __nv_bfloat16 *dst = p.out + unit.x * p.so.b + h * p.so.h + (int64_t)i * p.so.n;
+            if (col < p.d)
+                *reinterpret_cast<uint2 *>(dst + col) =
+                    make_uint2(pack2(acc[0] * inv, acc[1] * inv), pack2(acc[2] * inv, acc[3] * inv));
+            if (col == 0) p.lse[(unit.x * (int64_t)p.hq + h) * p.nq + i] = sum == 0.f ? -INFINITY : m + logf(sum);
         }
-        if (!mine && lane == 0) p.lse[(seq * (int64_t)p.hq + h) * p.nq + i] = m == -INFINITY ? -INFINITY : m + logf(sum);
         if (kEach > 1) __syncthreads();  // `shared` again
     }
 }
@@ -671,15 +698,15 @@ int launch_with_join(Kernel kernel, int threads, uint32_t smem, int slot, const 
     if (!st && !p.whole) {
         KernelScope scope(LINFORMER_KERNEL_PAGED, c.stream);
         // many parts where a unit's blocks, all units alike, would fill sixteen runs
-        const bool many = (int64_t)p.b * p.units * p.hk * 16 <= p.ctas;
-        const int rows = p.per * p.qbox * p.hbox, at_once = many ? 1 : kJoinWarps;
-        // (blocks of most runs leave at once, but 30000 of them, one a row, took 25 us to do so; trees of 79
-        // nodes, 6 parts a unit: 37.5 us in all with 32 blocks a run, 41.8 with 16, 38.8 with 64)
-        cfg.gridDim = dim3((unsigned)p.ctas, (unsigned)std::min(kJoinBlocks, (rows + at_once - 1) / at_once));
-        cfg.blockDim = dim3(kJoinWarps * 32);
+        const int64_t units = std::min<int64_t>((int64_t)p.b * p.units * p.hk, p.ctas);
+        const bool many = units * 16 <= p.ctas;
+        const int64_t at_once = (dp == 64 ? 2 : 1) * (many ? kJoinWarps / 4 : kJoinWarps);
+        cfg.gridDim = dim3((unsigned)std::min<int64_t>((int64_t)device_sms() * kJoinBlocks,
+                                                       (units * p.per * p.qbox * p.hbox + at_once - 1) / at_once));
+        cfg.blockDim = dim3(kJoinThreads);
         cfg.dynamicSmemBytes = 0;
-        const auto join = dp == 64 ? (many ? join_kernel<64, kJoinWarps> : join_kernel<64, 1>)
-                                   : (many ? join_kernel<128, kJoinWarps> : join_kernel<128, 1>);
+        const auto join = dp == 64 ? (many ? join_kernel<64, 4> : join_kernel<64, 1>)
+                                   : (many ? join_kernel<128, 4> : join_kernel<128, 1>);
         if (cudaLaunchKernelEx(&cfg, join, p) != cudaSuccess) {
             cudaGetLastError();
             st = LINFORMER_ERR_LAUNCH;
@@ -744,7 +771,7 @@ int attention(const AttnCall &call) {
         p.k_lengths = call.k_lengths + b0;
         p.q_lengths = call.q_lengths ? call.q_lengths + b0 : nullptr;
         p.mask = call.mask ? call.mask + (int64_t)b0 * call.nq * call.words : nullptr;
-        p.ctas = (int)(p.direct ? units * call.hk * call.b : std::min<int64_t>(device_sms(), most * c.b));
+        p.ctas = (int)(p.direct ? units * call.hk * call.b : std::min<int64_t>(std::min(device_sms(), kJoinThreads), most * c.b));
         if (wide) st = launch_wide(c, p);
         else st = call.d <= 64 ? launch_rows<64>(c, p) : launch_rows<128>(c, p);
     }
