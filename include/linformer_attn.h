@@ -401,7 +401,7 @@ LINFORMER_API int linformer_cache_keep(void *K_pages, const int64_t *K_pages_str
  * multiple of 8 up to 128, strides multiples of 8.  Rows of the pages behind the length may hold
  * anything, and with a window so may whole pages before the first query's: their table entries are not
  * read.  A page that is not there (see above) counts as rows of zeros.  Work is cut by rows of
- * keys, not by sequences: units of work whose table holds more than 1024 rows may be joined from parts
+ * keys, not by sequences: units of work whose table holds more than 768 rows may be joined from parts
  * in a stream-ordered workspace.  The result of a call does not depend on timing.  The blocks of 128
  * rows that the queries of one sequence go through, all tiles of queries and heads counted, have to be
  * fewer than 2^31 (else LINFORMER_ERR_SIZE).

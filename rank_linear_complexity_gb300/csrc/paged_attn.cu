@@ -751,11 +751,14 @@ int attention(const AttnCall &call) {
     // are huge
     const int64_t most = units * call.hk * (((int64_t)p.width * p.page + kTile - 1) / kTile);
     if (most > 0x7fffffffLL) return LINFORMER_ERR_SIZE;
-    // Units of a few blocks at most stay whole: no workspace, no second kernel (one token, 12 heads of two
-    // sequences, whole and cut, in a graph: 500 rows 8.0 and 11.1 us, 1000 rows 11.7 and 12.3, 1500 rows 15.4
-    // and 13.1; 40 tokens of four sequences, 1000 rows 21.7 and 27.8, 2000 rows 35.5 and 32.9).
-    constexpr int kWholeBlocks = 8;
-    p.whole = (int64_t)p.width * p.page <= kWholeBlocks * kTile;
+    // Units of a few blocks at most stay whole: no workspace, no second kernel, 2.7 us less on the host.  Whole
+    // and cut, in a graph, us: one token, 12 heads of 64 of two sequences, 512 rows 7.6 and 9.5, 1000 rows 11.6
+    // and 11.1, 1500 rows 15.3 and 12.0; 40 tokens of four, 1000 rows 13.1 and 16.8; 256 tokens of two, 8 groups of
+    // heads of 128, 1000 rows 22.4 and 32.8.  One token, 8 groups of heads of 128, where a block takes
+    // longer: 512 rows 9.2 and 9.6, 768 rows 12.2 and 10.2, 1000 rows 15.6 and 10.9; of eight sequences 9.5 and
+    // 11.4, 12.5 and 12.7, 16.0 and 14.7.
+    const int whole_blocks = call.d > 64 && p.qbox * p.hbox <= 32 ? 6 : 8;
+    p.whole = (int64_t)p.width * p.page <= whole_blocks * kTile;
     p.direct = p.whole && units * call.hk * call.b <= device_sms();
     const int seqs = (int)std::min<int64_t>(kMaxSeqs, 0x7fffffffLL / most);
     p.ntiles = (int)ntiles;
