@@ -7,7 +7,7 @@
 // are computed meanwhile; the chain product, softmax, product of one step hides behind the other's and
 // the other tile's (in blocks of 128 the next scores wait for the last product: a chunk of 2048 tokens
 // over 2 x 16384, 32 over 8 heads of 128, 770 us against 700 to 726, 1.42 to 1.47 PFLOP/s, at the power limit;
-// trees of 64 nodes over 16 caches of up to 8192: 101 us against 99, 98 with partial sums 32 bytes a store).  The tensor pipe's arithmetic takes
+// trees of 64 nodes over 16 caches of up to 8192: 101 us against 99; 94 with partial sums 32 bytes a store and the join as it is).  The tensor pipe's arithmetic takes
 // 2048 of the about 3300 cycles of a block of two tiles; scores of 64 columns load their query operand
 // twice as often as scores of 128.  Two threads a row instead of one: 874 us (the scores do not fit in
 // the registers of sixteen warps and are read twice).
