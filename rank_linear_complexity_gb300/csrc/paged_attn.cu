@@ -757,9 +757,17 @@ int attention(const AttnCall &call) {
     // heads of 128, 1000 rows 22.4 and 32.8.  One token, 8 groups of heads of 128, where a block takes
     // longer: 512 rows 9.2 and 9.6, 768 rows 12.2 and 10.2, 1000 rows 15.6 and 10.9; of eight sequences 9.5 and
     // 11.4, 12.5 and 12.7, 16.0 and 14.7.
-    const int whole_blocks = call.d > 64 && p.qbox * p.hbox <= 32 ? 6 : 8;
-    p.whole = (int64_t)p.width * p.page <= whole_blocks * kTile;
-    p.direct = p.whole && units * call.hk * call.b <= device_sms();
+    // Wide units take 10 to 25 us more cut than whole (ends, partial sums, join), so those that fit a CTA each
+    // also stay whole where that leaves CTAs idle for no more than eight blocks' time: 1100 tokens of 18 units a
+    // head, 8 heads of 128, over 1500 rows 29.9 and 55.6, 3000 rows 50.4 and 73.1; 16 trees of 64 over 32 over 8
+    // heads, 2000 rows 39.2 and 60.8, ragged 37.6 and 50.8, 3000 rows ragged 52.8 and 60.2; four of them, 1500 rows 29.1
+    // and 24.3.  Of several sequences, one may be long and the others short, which only cut units even out, so
+    // then up to 24 blocks.
+    const int64_t whole_blocks = call.d > 64 && !wide ? 6 : 8, all = units * call.hk * call.b, sms = device_sms();
+    const int64_t blocks = ((int64_t)p.width * p.page + kTile - 1) / kTile;  // of a unit at most
+    p.whole = blocks <= whole_blocks ||
+              (wide && all <= sms && (call.b == 1 || blocks <= 24) && blocks * (sms - all) <= 8 * sms);
+    p.direct = p.whole && all <= sms;
     const int seqs = (int)std::min<int64_t>(kMaxSeqs, 0x7fffffffLL / most);
     p.ntiles = (int)ntiles;
     p.units = (int)units;
