@@ -19,8 +19,8 @@
 //
 // The blocks of 128 keys of all rows form one long list, sequence by sequence, and each CTA takes an
 // equal run of it, so that differing lengths cost nothing; a row whose run is cut is joined from
-// its parts, in order, by a second kernel.  Where tables are short nothing is cut, and where units are
-// few each CTA has its own without a list.
+// its parts, in order, by a second kernel.  Where tables or windows are short nothing is cut, and where
+// units are few each CTA has its own without a list.
 //
 // Bound by memory: one token over 62 ragged caches of up to 8192 rows, 32 over 8 heads of 128, pages of
 // 16: 228 us, 5.9 TB/s, 6.5 while all CTAs stream (a ring of four tiles of 32 KB is as good as five, of
@@ -764,7 +764,11 @@ int attention(const AttnCall &call) {
     // and 24.3.  Of several sequences, one may be long and the others short, which only cut units even out, so
     // then up to 24 blocks.
     const int64_t whole_blocks = call.d > 64 && !wide ? 6 : 8, all = units * call.hk * call.b, sms = device_sms();
-    const int64_t blocks = ((int64_t)p.width * p.page + kTile - 1) / kTile;  // of a unit at most
+    int64_t blocks = ((int64_t)p.width * p.page + kTile - 1) / kTile;  // of a unit at most
+    // (rows of `per` tiles of positions and their window, which need not begin with a block: one token, window of
+    // 100 in tables of 16000 rows, 32 over 8 heads of 128, 8.2 us by the table and 5.4 so; four tokens of eight
+    // sequences, window of 500, 14.2 and 9.3)
+    if (p.window) blocks = std::min(blocks, ((int64_t)p.window + p.per * p.qbox + kTile - 2) / kTile + 1);
     p.whole = blocks <= whole_blocks ||
               (wide && all <= sms && (call.b == 1 || blocks <= 24) && blocks * (sms - all) <= 8 * sms);
     p.direct = p.whole && all <= sms;

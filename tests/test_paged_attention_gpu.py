@@ -333,3 +333,24 @@ def test_nan_queries_and_keys(nq):
     kc[table[1, 899 // 64].long(), 1, 899 % 64, 5] = float("nan")
     bad[1, 2:, nq - 1] = True
     check()
+
+
+@pytest.mark.parametrize("kw", [dict(nq=1, window=1500), dict(nq=9, window=2100), dict(nq=150, window=1300),
+                                dict(nq=40, hq=8, window=1111, d=128)])
+def test_wide_windows(kw):
+    """Windows of more blocks than a unit keeps whole."""
+    check_attention(k_lengths=(4000, 900, 2222), page=32, **kw)
+    check_attention(k_lengths=(4000, 0, 2222), q_lengths=(kw["nq"], 1, max(1, kw["nq"] // 2)), page=64, layout="heads", **kw)
+
+
+@pytest.mark.parametrize("kw", [dict(), dict(window=700), dict(causal=False)])
+def test_whole_units_of_many_blocks(kw):
+    """As many units as CTAs, so that each stays whole over more blocks than it otherwise would."""
+    check_attention(b=1, hq=32, hk=8, d=40, nq=1100, k_lengths=(1777,), page=64, **kw)
+
+
+def test_whole_trees_of_many_blocks():
+    tree = paged.ancestors(random_tree(15, 64, seed=2).numpy())
+    lengths = [64 + 130 * i for i in range(15)]
+    check_attention(b=15, hq=32, hk=8, nq=64, tree=tree, k_lengths=lengths, d=40, page=32)
+    check_attention(b=15, hq=32, hk=8, nq=64, tree=tree, k_lengths=lengths, q_lengths=[64, 0, 3] * 5, d=40, page=32)
