@@ -786,7 +786,7 @@ int attention(const AttnCall &call) {
         p.k_lengths = call.k_lengths + b0;
         p.q_lengths = call.q_lengths ? call.q_lengths + b0 : nullptr;
         p.mask = call.mask ? call.mask + (int64_t)b0 * call.nq * call.words : nullptr;
-        p.ctas = (int)(p.direct ? units * call.hk * call.b : std::min<int64_t>(std::min(device_sms(), kJoinThreads), most * c.b));
+        p.ctas = (int)(p.direct ? units * call.hk * c.b : std::min<int64_t>(std::min(device_sms(), kJoinThreads), most * c.b));
         if (wide) st = launch_wide(c, p);
         else st = call.d <= 64 ? launch_rows<64>(c, p) : launch_rows<128>(c, p);
     }
