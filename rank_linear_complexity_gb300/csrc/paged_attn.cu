@@ -381,6 +381,10 @@ paged_attn_kernel(const __grid_constant__ CUtensorMap tQ, const __grid_constant_
                         const int c = c0 + key0;
                         float up = sh->part[w][0][key0];
                         for (int x = 1; x < 4; ++x) up = fmaxf(up, sh->part[w][x][key0]);
+                        // A padded query gets a reference that no score outgrows: what stands there has no vote on
+                        // when references move, on which the last bits of all results depend.  (Columns that no
+                        // box fills are zeros, alike in every call.)
+                        if (it.sp.Lq < p.nq && r.q0 + (c & (p.qbox - 1)) >= it.sp.Lq) up = INFINITY;
                         const float m = j > it.lo ? sh->m[c] : -INFINITY;
                         none = m == -INFINITY && up == -INFINITY;
                         // (a reference of 0 stands for none)

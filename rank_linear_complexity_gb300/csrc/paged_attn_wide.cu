@@ -332,7 +332,7 @@ paged_wide_kernel(const __grid_constant__ CUtensorMap tQ, const __grid_constant_
             if (it.seq < 0) break;
             // [clean_lo, clean_hi): blocks that every row of the tile sees all of
             int xlo, xhi, clean_lo, clean_hi;
-            bool warp_valid;
+            bool valid, warp_valid;
             {
                 const Part x(p, it, t);
                 int qi, head;
@@ -340,12 +340,15 @@ paged_wide_kernel(const __grid_constant__ CUtensorMap tQ, const __grid_constant_
                 const int i = x.q0 + qi;
                 xlo = x.lo;
                 xhi = x.hi;
-                warp_valid = __any_sync(0xffffffffu, x.live && head < p.hbox && x.h0 + head < p.group && i < it.sp.Lq);
+                valid = x.live && head < p.hbox && x.h0 + head < p.group && i < it.sp.Lq;
+                warp_valid = __any_sync(0xffffffffu, valid);
                 const int end = min(it.sp.end(x.q0), p.mask ? it.sp.Lk - it.sp.Lq : it.sp.Lk);
                 clean_hi = max(end, 0) / kTile;
                 clean_lo = (it.sp.first(max(min(x.q0 + p.qbox, it.sp.Lq) - 1, 0)) + kTile - 1) / kTile;
             }
-            float m = -INFINITY, l = 0.f;  // reference (of the raw scores), sum of 2^((s - m) sl)
+            // reference (of the raw scores; one that no score outgrows where there is no query, so that what
+            // stands there has no vote on when the references move), sum of 2^((s - m) sl)
+            float m = valid ? -INFINITY : INFINITY, l = 0.f;
             for (int u = 2 * xlo; u < 2 * xhi; ++u, ++n) {
                 const int j = u >> 1, h = u & 1;
                 if (!warp_spin(&sh->s_full[t][h], (n >> 1) & 1, p.status, 150, abort_flag)) {
