@@ -137,7 +137,7 @@ paged_attn_kernel(const __grid_constant__ CUtensorMap tQ, const __grid_constant_
     // (addresses in it are constants then, and take no registers)
     extern __shared__ __align__(1024) uint8_t smem[];
     if (smem_u32(smem) & 1023u) {
-        if (threadIdx.x == 0 && p.status) atomicExch(p.status, 133);
+        leave(p, 133);
         return;
     }
     Shared *sh = reinterpret_cast<Shared *>(smem + L::kEnd);

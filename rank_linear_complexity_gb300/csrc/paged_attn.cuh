@@ -230,6 +230,15 @@ __device__ __forceinline__ void write_cut(const AttnParams &p, const Walk &w, co
     p.cuts[blockIdx.x] = cut;
 }
 
+// For a CTA that has to leave without its work (all its threads do): recorded, and the join, which reads
+// every CTA's cut, is told that this one ends no unit.
+__device__ __forceinline__ void leave(const AttnParams &p, int code) {
+    if (threadIdx.x != 0) return;
+    if (p.status) atomicExch(p.status, code);
+    wait_prerequisites();  // (the workspace may be an earlier kernel's until then)
+    if (!p.whole) p.cuts[blockIdx.x] = make_int4(-1, 0, 0, 0);
+}
+
 // Units without blocks: O = 0, lse = -inf.  A unit a CTA in turn, by `warps` warps of it, 16 bytes a thread;
 // own: of a unit a CTA.
 __device__ __forceinline__ void write_empty(const AttnParams &p, const Marks &marks, const Walk *own, int warp, int warps,

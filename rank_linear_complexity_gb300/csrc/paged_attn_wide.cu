@@ -82,7 +82,7 @@ paged_wide_kernel(const __grid_constant__ CUtensorMap tQ, const __grid_constant_
     // (addresses in it are constants then, and take no registers)
     extern __shared__ __align__(1024) uint8_t smem[];
     if (smem_u32(smem) & 1023u) {
-        if (threadIdx.x == 0 && p.status) atomicExch(p.status, 157);
+        leave(p, 157);
         return;
     }
     uint8_t *sQ = smem, *sKV = smem + 2 * L::kTileBytes;
