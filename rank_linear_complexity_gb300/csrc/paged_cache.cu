@@ -186,8 +186,9 @@ __global__ void __launch_bounds__(kThreads) keep_kernel(const KeepParams p) {
         for (int k = 0; k < kRows; ++k) node[k] = i + k < count ? __ldg(path + i + k) : i + k;
         auto page_at = [&](int64_t at, bool wanted) {
             const int64_t entry = at >> p.cache.shift;
-            if (!wanted) return -2;
-            return at >= 0 && entry < p.cache.width ? __ldg(table + entry) : -1;
+            const bool inside = at >= 0 && entry < p.cache.width;
+            if (wanted && !inside) bad = kBadRow;
+            return wanted && inside ? __ldg(table + entry) : -1;
         };
 #pragma unroll
         for (int k = 0; k < kRows; ++k) {
@@ -200,7 +201,7 @@ __global__ void __launch_bounds__(kThreads) keep_kernel(const KeepParams p) {
         for (int k = 0; k < kRows; ++k) {
             const bool there = (unsigned)from[k] < (unsigned)p.cache.pages && (unsigned)to[k] < (unsigned)p.cache.pages;
             if (!there) {
-                if (from[k] != -2) bad = kBadPage;
+                if (node[k] > i + k && !bad) bad = kBadPage;  // (whatever the entry: the table may hold any)
                 to[k] = -1;
                 continue;
             }
