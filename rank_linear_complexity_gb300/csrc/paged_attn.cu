@@ -56,8 +56,9 @@ struct Layout {
     // alone, 1.7e-3 against 2.3e-3; N = 64: 4 %, left at one).
     static constexpr bool kSplit = N < 64;
     static constexpr int kCols = kSplit ? 2 * N : N;  // of P and of O
-    static constexpr int kPBufs = kCols > 64 ? 1 : 2;
-    static constexpr uint32_t kPBytes = (kCols > 64 ? 2 : 1) * kTile * 128;  // (rows of 64 columns)
+    static_assert(kCols <= 64, "a row of P is 128 bytes");
+    static constexpr int kPBufs = 2;
+    static constexpr uint32_t kPBytes = kTile * 128;
     static constexpr uint32_t kQHalf = N * 128, kQBytes = kQHalf * (DP / 64);
     static constexpr uint32_t kP = kEntries * kEntryBytes, kQ = kP + kPBufs * kPBytes, kEnd = kQ + kQBytes;
     static constexpr uint32_t kS = 0, kO = 2 * N;  // tensor memory: S, S, O
@@ -441,7 +442,7 @@ paged_attn_kernel(const __grid_constant__ CUtensorMap tQ, const __grid_constant_
                         hi[e] = pack2(a, z);
                         lo[e] = pack2(a - __uint_as_float(hi[e] << 16), z - __uint_as_float(hi[e] & 0xffff0000u));
                     }
-                    auto at = [&](int col) { return row + col / 64 * 16384 + ((col % 64 / 8 ^ (key0 & 7)) * 16); };
+                    auto at = [&](int col) { return row + ((col / 8 ^ (key0 & 7)) * 16); };
                     *reinterpret_cast<uint4 *>(at(c0 + c)) = make_uint4(hi[0], hi[1], hi[2], hi[3]);
                     if (L::kSplit) *reinterpret_cast<uint4 *>(at(N + c0 + c)) = make_uint4(lo[0], lo[1], lo[2], lo[3]);
                 }
