@@ -774,8 +774,22 @@ int attention(const AttnCall &call) {
     // 100 in tables of 16000 rows, 32 over 8 heads of 128, 8.2 us by the table and 5.4 so; four tokens of eight
     // sequences, window of 500, 14.2 and 9.3)
     if (p.window) blocks = std::min(blocks, ((int64_t)p.window + p.per * p.qbox + kTile - 2) / kTile + 1);
+    // Under a causal mask the units of a prompt's first tokens have fewer blocks than its last, and a CTA idles
+    // for `less` blocks on average: cut where that is more than 32 with a head to a unit, 64 with two, whose
+    // units cost more cut.  Whole and cut, d = 128, prompts without rows before them: 6 heads of 6400 tokens 87
+    // and 85, 8 of 4608 66 and 70, 4 of 9600 129 and 113, 3 of 12800 165 and 131, one of 38000 465 and 312; two on
+    // one of 19200 243 and 231, three of 12800 165 and 190, four of 9600 126 and 167.  Windows even units out:
+    // two heads of 19200, window of 6000, 83 and 118.
+    int64_t less = 0;
+    if (call.causal) {
+        // the positions before each of which a query sees fewer rows than the last one
+        const int64_t rows = (int64_t)p.width * p.page, before = std::max<int64_t>(rows - call.nq, 0);
+        const int64_t growing = std::max<int64_t>((p.window ? std::min<int64_t>(p.window, rows) : rows) - before, 0);
+        less = growing * growing / (2LL * kTile * call.nq);
+    }
     p.whole = blocks <= whole_blocks ||
-              (wide && all <= sms && (call.b == 1 || blocks <= 24) && blocks * (sms - all) <= 8 * sms);
+              (wide && all <= sms && (call.b == 1 || blocks <= 24) && blocks * (sms - all) <= 8 * sms &&
+               less <= (p.nch > 1 ? 64 : 32));
     p.direct = p.whole && all <= sms;
     const int seqs = (int)std::min<int64_t>(kMaxSeqs, 0x7fffffffLL / most);
     p.ntiles = (int)ntiles;
