@@ -371,6 +371,7 @@ LINFORMER_API int linformer_rotary_phase(uint64_t *phase, int rot, double base, 
  * no page for is dropped (and recorded).  No two rows of a call may go to one place.  dtype of all
  * tensors LINFORMER_F32 or LINFORMER_BF16.  Pointers 16-byte aligned (phase 8; table, starts, counts and
  * positions 4); any strides (multiples of 16 bytes, d and rot / 2 multiples of 16 bytes run fastest).
+ * fp32 serves caches that a program reads by itself; the attention below takes bf16.
  */
 LINFORMER_API int linformer_cache_append(
     const void *K, const int64_t *K_strides, const void *V, const int64_t *V_strides, void *K_pages,
@@ -402,7 +403,10 @@ LINFORMER_API int linformer_cache_keep(void *K_pages, const int64_t *K_pages_str
  * anything, and with a window so may whole pages before the first query's: their table entries are not
  * read.  A page that is not there (see above) counts as rows of zeros.  Work is cut by rows of
  * keys, not by sequences: units of work whose table holds more than 768 rows may be joined from parts
- * in a stream-ordered workspace.  The result of a call does not depend on timing.  The blocks of 128
+ * in a stream-ordered workspace.  The result of a call depends neither on timing nor, in any bit, on what
+ * rows past the lengths hold.  Probabilities enter the products as two bf16 parts where a key/value head
+ * has up to 32 rows (tokens, rounded up to a power of two, times query heads), rounded to one bf16
+ * elsewhere: at most 2^-8 of each term, as in linformer_softmax_attn_fwd.  The blocks of 128
  * rows that the queries of one sequence go through, all tiles of queries and heads counted, have to be
  * fewer than 2^31 (else LINFORMER_ERR_SIZE).
  */

@@ -5,11 +5,13 @@
 //
 // A block of 128 keys is two steps of 64.  P stands over its own scores, and the other step's scores
 // are computed meanwhile; the chain product, softmax, product of one step hides behind the other's and
-// the other tile's (in blocks of 128 the next scores wait for the last product: a chunk of 2048 tokens
-// over 2 x 16384, 32 over 8 heads of 128, 770 us against 700 to 726, 1.42 to 1.47 PFLOP/s, at the power limit;
-// trees of 64 nodes over 16 caches of up to 8192: 101 us against 99; 94 with partial sums 32 bytes a store and the join as it is).  The tensor pipe's arithmetic takes
-// 2048 of the about 3300 cycles of a block of two tiles; scores of 64 columns load their query operand
-// twice as often as scores of 128.  Two threads a row instead of one: 874 us (the scores do not fit in
+// the other tile's.  A chunk of 2048 tokens over 2 x 16384, 32 over 8 heads of 128: 697 to 757 us in a graph, 1.36
+// to 1.48 PFLOP/s, at the power limit, and 780 by the call; trees of 64 nodes over 16 caches of up to 8192, 94 to
+// 95 in a graph.  (In blocks of 128 the next scores wait for the last product: by the call, in earlier states,
+// 770 us against 726 so, trees 101 and 99.)  The tensor pipe's arithmetic takes 2048 of the about 3300 cycles
+// of a block of two tiles; scores of 64 columns load their query operand twice as often as scores of 128.
+// P goes to the tensor cores as one bf16, rounded by at most 2^-8 of each term (error of O 2.3e-3, 1.7e-3 of it
+// the result's own rounding): two parts would double the products from P, which bound chunks.  Two threads a row instead of one: 874 us (the scores do not fit in
 // the registers of sixteen warps and are read twice).
 //   warps 0-3, 4-7  softmax of tile 0 and tile 1: S out of tensor memory, P back
 //   warp 8          loads: goes through the CTA's run, tells the others each item, looks the pages up

@@ -64,3 +64,21 @@ def test_what_an_earlier_call_left_changes_no_bit(group, nq, d):
     assert lf.linformer_debug_read_device_status() == 0
     for x in got[1:]:
         assert same(x, got[0])
+
+
+@pytest.mark.parametrize("window", [0, 700])
+@pytest.mark.parametrize("d", [64, 128])
+@pytest.mark.parametrize("group,nq", SHAPES)
+def test_rows_past_the_lengths_change_no_bit(group, nq, d, window):
+    hk = 8
+    lengths = tuple(x - 37 for x in LENGTHS)  # that end inside a page and a block
+    kc, vc, table = cache(len(LENGTHS), hk, d, 16, lengths, device=DEV, seed=nq)
+    Q = queries(group * hk, nq, d, 1)
+    got = []
+    for x in (0.0, -30.0, 1e30, float("inf"), float("nan")):
+        k, v = (torch.where(c.isnan(), torch.full_like(c, x), c) for c in (kc, vc))
+        got.append(lf.paged_attention(Q, k, v, table, ints(lengths, DEV), window=window))
+    torch.cuda.synchronize()
+    assert lf.linformer_debug_read_device_status() == 0
+    for x in got[1:]:
+        assert same(x, got[0])
